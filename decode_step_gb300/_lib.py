@@ -32,6 +32,12 @@ class KVCacheDesc(ctypes.Structure):
                 ("head_dim", _i32), ("dtype", _i32), ("k_pool", _vp), ("v_pool", _vp)]
 
 
+class LatentCacheDesc(ctypes.Structure):
+    """tts_latent_cache."""
+    _fields_ = [("num_blocks", _i32), ("block_size", _i32), ("latent_dim", _i32), ("rope_dim", _i32),
+                ("dtype", _i32), ("pool", _vp)]
+
+
 class StepGraphDesc(ctypes.Structure):
     """tts_step_graph_desc."""
     _fields_ = [("cache", ctypes.POINTER(KVCacheDesc)), ("d_block_table", _vp), ("max_blocks_per_seq", _i32),
@@ -70,6 +76,16 @@ _SIGNATURES = {
                                        _i32, _i32, _f32, _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "tts_decode_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32,
                                                _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp]),
+    "tts_latent_append": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _i32, _vp, _i32, _vp, _i32, _i32,
+                                         _f32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "tts_latent_decode_attn_workspace_size": (_sz, [_i32] * 7),
+    "tts_latent_decode_attn": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _i32, _vp, _i32, _i32, _i32,
+                                              _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                              _vp, _vp]),
+    "tts_latent_prefill_attn_workspace_size": (_sz, [_i32] * 7),
+    "tts_latent_prefill_attn": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _i32, _vp, _i32, _i32, _vp,
+                                               _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                               _vp, _vp]),
     "tts_head_workspace_size": (_sz, [_i32, _i32]),
     "tts_codebook_head_select": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32,
                                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),

@@ -197,6 +197,110 @@ def tts_decode_attn_noalloc(cache: KVCache, block_table, ctx_lens, max_ctx_len, 
     check("tts_decode_attn_noalloc", lib().tts_decode_attn_noalloc(*args))
 
 
+class LatentCache:
+    """Paged latent KV pool: bf16 [num_blocks][16][latent_dim + 64] (a token's
+    latent, then its rotated key part)."""
+
+    ROPE_DIM = 64
+
+    def __init__(self, pool: torch.Tensor, latent_dim: int):
+        if pool.dtype != torch.bfloat16 or pool.dim() != 3 or pool.shape[1] != 16:
+            raise ValueError("a latent pool is bfloat16 [num_blocks][16][latent_dim + 64]")
+        if pool.shape[2] != latent_dim + self.ROPE_DIM:
+            raise ValueError(f"the pool's rows hold {pool.shape[2]} values, latent_dim + 64 = {latent_dim + 64}")
+        self.pool, self.latent_dim = pool, latent_dim
+        self.desc = _lib.LatentCacheDesc(pool.shape[0], 16, latent_dim, self.ROPE_DIM, TTS_BF16, _dev(pool, "pool"))
+
+    @property
+    def num_blocks(self) -> int:
+        return self.desc.num_blocks
+
+
+def _one_device(**tensors):
+    """Every tensor on the current device (whose stream the call is queued on)."""
+    cur = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+
+def tts_latent_append(cache: LatentCache, block_table, ctx_before, c_new, kr_new, q_rope=None, q_rope_out=None,
+                      rope_base=10000.0, row_start=None, err=None, stream=None):
+    """Appends rows c_new [T][latent_dim], kr_new [T][64] (rotated on the way)
+    and rotates q_rope [T][Hq][64] into q_rope_out (default: in place).  T is
+    B * q_len, or packed ragged rows with row_start int32 [B + 1]."""
+    B, max_blocks = block_table.shape
+    T = c_new.shape[0]
+    if q_rope is None and q_rope_out is not None:
+        raise ValueError("q_rope_out without q_rope")
+    Hq = 0 if q_rope is None else q_rope.shape[1]
+    q_rope_out = q_rope if q_rope_out is None else q_rope_out
+    bf = torch.bfloat16
+    args = (ctypes.byref(cache.desc), _dev(block_table, "block_table", torch.int32), max_blocks,
+            _dev(ctx_before, "ctx_before", torch.int32, (B,)), B,
+            None if row_start is None else _dev(row_start, "row_start", torch.int32, (B + 1,)), T, Hq,
+            float(rope_base), _dev(c_new, "c_new", bf, (T, cache.latent_dim)),
+            _dev(kr_new, "kr_new", bf, (T, cache.ROPE_DIM)),
+            None if q_rope is None else _dev(q_rope, "q_rope", bf, (T, Hq, cache.ROPE_DIM)),
+            None if q_rope is None else _dev(q_rope_out, "q_rope_out", bf, (T, Hq, cache.ROPE_DIM)),
+            None if err is None else _dev(err, "err", torch.int32), _stream(stream))
+    _one_device(pool=cache.pool, block_table=block_table, ctx_before=ctx_before, row_start=row_start, c_new=c_new,
+                kr_new=kr_new, q_rope=q_rope, q_rope_out=q_rope_out, err=err)
+    check("tts_latent_append", lib().tts_latent_append(*args))
+
+
+def tts_latent_decode_attn_workspace_size(B, q_len, num_q_heads, latent_dim, nope_dim, v_dim, max_ctx_len) -> int:
+    return int(lib().tts_latent_decode_attn_workspace_size(B, q_len, num_q_heads, latent_dim, nope_dim, v_dim,
+                                                           max_ctx_len))
+
+
+def tts_latent_decode_attn(cache: LatentCache, block_table, ctx_lens, max_ctx_len, q_nope, q_rope, w_uk, w_uv, out,
+                           ws, scale, causal=False, err=None, stream=None):
+    """q_nope [B][q_len][Hq][nope_dim], q_rope [B][q_len][Hq][64] (rotated),
+    w_uk [Hq][nope_dim][latent_dim], w_uv [Hq][v_dim][latent_dim] ->
+    out [B][q_len][Hq][v_dim], all bf16."""
+    B, max_blocks = block_table.shape
+    _, q_len, Hq, nope = q_nope.shape
+    v = out.shape[-1]
+    bf, L = torch.bfloat16, cache.latent_dim
+    args = (ctypes.byref(cache.desc), _dev(block_table, "block_table", torch.int32), max_blocks,
+            _dev(ctx_lens, "ctx_lens", torch.int32, (B,)), int(max_ctx_len), B, q_len, Hq, nope, v, float(scale),
+            int(bool(causal)), _dev(q_nope, "q_nope", bf, (B, q_len, Hq, nope)),
+            _dev(q_rope, "q_rope", bf, (B, q_len, Hq, cache.ROPE_DIM)), _dev(w_uk, "w_uk", bf, (Hq, nope, L)),
+            _dev(w_uv, "w_uv", bf, (Hq, v, L)), _dev(out, "out", bf, (B, q_len, Hq, v)), _dev(ws, "ws"),
+            ws.numel() * ws.element_size(), None if err is None else _dev(err, "err", torch.int32), _stream(stream))
+    _one_device(pool=cache.pool, block_table=block_table, ctx_lens=ctx_lens, q_nope=q_nope, q_rope=q_rope, w_uk=w_uk,
+                w_uv=w_uv, out=out, ws=ws, err=err)
+    check("tts_latent_decode_attn", lib().tts_latent_decode_attn(*args))
+
+
+def tts_latent_prefill_attn_workspace_size(B, num_rows, num_q_heads, latent_dim, nope_dim, v_dim,
+                                           max_total_ctx) -> int:
+    return int(lib().tts_latent_prefill_attn_workspace_size(B, num_rows, num_q_heads, latent_dim, nope_dim, v_dim,
+                                                            max_total_ctx))
+
+
+def tts_latent_prefill_attn(cache: LatentCache, block_table, ctx_lens, max_total_ctx, row_start, q_nope, q_rope, w_uk,
+                            w_uv, out, ws, scale, err=None, stream=None):
+    """Causal attention of packed prompt rows: q_nope [T][Hq][nope_dim], q_rope
+    [T][Hq][64] (rotated) -> out [T][Hq][v_dim]; row_start int32 [B + 1];
+    max_total_ctx bounds the sum of ctx_lens."""
+    B, max_blocks = block_table.shape
+    T, Hq, nope = q_nope.shape
+    v = out.shape[-1]
+    bf, L = torch.bfloat16, cache.latent_dim
+    args = (ctypes.byref(cache.desc), _dev(block_table, "block_table", torch.int32), max_blocks,
+            _dev(ctx_lens, "ctx_lens", torch.int32, (B,)), int(max_total_ctx), B,
+            _dev(row_start, "row_start", torch.int32, (B + 1,)), T, Hq, nope, v, float(scale),
+            _dev(q_nope, "q_nope", bf, (T, Hq, nope)), _dev(q_rope, "q_rope", bf, (T, Hq, cache.ROPE_DIM)),
+            _dev(w_uk, "w_uk", bf, (Hq, nope, L)), _dev(w_uv, "w_uv", bf, (Hq, v, L)),
+            _dev(out, "out", bf, (T, Hq, v)), _dev(ws, "ws"), ws.numel() * ws.element_size(),
+            None if err is None else _dev(err, "err", torch.int32), _stream(stream))
+    _one_device(pool=cache.pool, block_table=block_table, ctx_lens=ctx_lens, row_start=row_start, q_nope=q_nope,
+                q_rope=q_rope, w_uk=w_uk, w_uv=w_uv, out=out, ws=ws, err=err)
+    check("tts_latent_prefill_attn", lib().tts_latent_prefill_attn(*args))
+
+
 def tts_head_workspace_size(R, V) -> int:
     return int(lib().tts_head_workspace_size(R, V))
 

@@ -1,0 +1,77 @@
+// Shared by the latent-cache kernels: limits, argument checks, launching, and
+// the search for a packed row's stream (sm_103a).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "tts_decode.h"
+#include "tts_internal.h"
+
+namespace tts {
+
+constexpr int kLatentRope = 64;        // rotary values of a query or key
+constexpr int kLatentMaxDim = 512;
+constexpr int kLatentMaxHeads = 1024;
+
+inline int check_latent_cache(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks) {
+    if (!cache || !cache->pool || !d_block_table) return TTS_ERR_INVALID;
+    if (cache->num_blocks < 1 || max_blocks < 1 || max_blocks > (1 << 20)) return TTS_ERR_INVALID;
+    if (cache->num_blocks > 0x7FFFFFFF / TTS_BLOCK_TOKENS) return TTS_ERR_UNSUPPORTED;  // token rows are 32-bit
+    if (cache->block_size != TTS_BLOCK_TOKENS || cache->dtype != TTS_BF16 || cache->rope_dim != kLatentRope ||
+        cache->latent_dim < 64 || cache->latent_dim > kLatentMaxDim || cache->latent_dim % 64 != 0)
+        return TTS_ERR_UNSUPPORTED;
+    return aligned16(cache->pool) ? TTS_OK : TTS_ERR_INVALID;
+}
+
+inline bool latent_head_dim_ok(int d) { return d == 64 || d == 128; }
+
+// Launches a kernel, as a programmatic dependent of the one before it if o.pdl.
+template <typename... P, typename... A>
+inline int launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, LaunchOpts o, A &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = o.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = o.pdl ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return TTS_ERR_CUDA;
+    }
+    return TTS_OK;
+}
+
+// Number of a warp's first lanes with a true predicate.
+__device__ __forceinline__ int leading_true(bool pred) {
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, pred);
+    return m == 0xFFFFFFFFu ? 32 : __ffs(~m) - 1;
+}
+
+// Stream of packed row `row`: the b with row_start[b] <= row < row_start[b + 1],
+// or -1.  A whole warp calls it; each round probes 32 entries of the
+// non-decreasing array.  Any other array content gives -1 or a b that
+// satisfies the condition, never an access outside row_start[0..B].
+__device__ __forceinline__ int stream_of_row(const int32_t *row_start, int B, int row, int lane) {
+    int lo = 0, hi = B;  // streams 0..lo-1 end at or before `row`; the answer is in [lo, hi]
+    while (hi - lo > 32) {
+        const int step = (hi - lo + 31) / 32;
+        const int idx = lo + lane * step;
+        const int c = leading_true(idx < hi && row_start[idx + 1] <= row);
+        if (c == 0) {
+            hi = lo;
+        } else {
+            hi = min(hi, lo + c * step);
+            lo += (c - 1) * step + 1;
+        }
+    }
+    lo += leading_true(lo + lane < hi && row_start[lo + lane + 1] <= row);
+    if (lo >= B || row_start[lo] > row || row_start[lo + 1] <= row) return -1;
+    return lo;
+}
+
+}  // namespace tts

@@ -237,6 +237,111 @@ int tts_decode_attn_noalloc(const tts_kv_cache *cache, const int32_t *d_block_ta
                             float scale, int32_t causal, const void *d_q, void *d_out,
                             int32_t *d_err, void *stream);
 
+/* ---------------------------------------------------------- latent cache */
+
+/* Paged latent KV cache.  No counterpart on the pages: a compressed form of
+ * the cache above for models whose keys and values all come from one latent
+ * vector a token.  A token's row holds a latent c (latent_dim values) and one
+ * rotated key part kr (rope_dim values), shared by every head.  With the
+ * per-head weights w_uk [Hq][nope_dim][latent_dim] and w_uv
+ * [Hq][v_dim][latent_dim], head h's key is (w_uk[h] c, kr) and its value is
+ * w_uv[h] c.  A row of 512 + 64 bf16 values takes 1152 bytes where 8 KV heads
+ * of 128 take 4096.
+ * `pool` is [num_blocks][16][latent_dim + rope_dim], c before kr, 16-byte
+ * aligned; block ids and tables are those of the block pool above.
+ * Supported: TTS_BF16, latent_dim a multiple of 64 up to 512, rope_dim 64. */
+typedef struct tts_latent_cache {
+    int32_t num_blocks;
+    int32_t block_size;     /* must be 16 */
+    int32_t latent_dim;
+    int32_t rope_dim;       /* must be 64 */
+    int32_t dtype;          /* TTS_BF16 */
+    void *pool;
+} tts_latent_cache;
+
+/* Writes new tokens' rows into the latent pool, with the rotary embedding of
+ * their key parts, and rotates the same tokens' query parts.
+ * Rows are packed: row r of stream b is its token j, at position
+ * s = d_ctx_before[b] + j, and goes to block d_block_table[b][s / 16], slot
+ * s % 16.  With d_row_start NULL every stream has num_rows / B rows (r =
+ * b * (num_rows / B) + j).  Otherwise stream b has the rows
+ * d_row_start[b] <= r < d_row_start[b + 1] (int32 [B + 1], non-decreasing;
+ * prompts of different lengths in one call); rows of no stream are left alone.
+ *  d_c_new   bf16 [num_rows][latent_dim], copied as it is
+ *  d_kr_new  bf16 [num_rows][64]: with i < 32 and a = s * rope_base^(-2i/64),
+ *            x[i] cos a - x[i + 32] sin a and x[i + 32] cos a + x[i] sin a are
+ *            stored (cos a and sin a from double precision, the rotation in
+ *            fp32, rounded once to bf16)
+ *  d_q_rope, d_q_rope_out  bf16 [num_rows][num_q_heads][64], rotated likewise;
+ *            the same buffer (in place) or disjoint ones; num_q_heads 0: none
+ *            (both may then be NULL)
+ * Requires rope_base > 1.  A slot outside the table (TTS_ERRBIT_CTX_LEN) or a
+ * block id outside the pool (TTS_ERRBIT_BLOCK_ID) is skipped: neither the
+ * pool nor d_q_rope_out is written for that row. */
+int tts_latent_append(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                      const int32_t *d_ctx_before, int32_t B, const int32_t *d_row_start, int32_t num_rows,
+                      int32_t num_q_heads, float rope_base, const void *d_c_new, const void *d_kr_new,
+                      const void *d_q_rope, void *d_q_rope_out, int32_t *d_err, void *stream);
+
+/* Bytes of device workspace tts_latent_decode_attn needs for these sizes (0
+ * on bad arguments).  Needs no particular contents; calls that overlap on the
+ * GPU need separate workspaces. */
+size_t tts_latent_decode_attn_workspace_size(int32_t B, int32_t q_len, int32_t num_q_heads, int32_t latent_dim,
+                                             int32_t nope_dim, int32_t v_dim, int32_t max_ctx_len);
+
+/* Decode attention over the latent cache: for stream b, query row j < q_len
+ * and head h, with the key and value of the cache's description,
+ *   out[b][j][h] = sum_t softmax_t(scale * (q_nope . w_uk[h] c_t + q_rope . kr_t)) w_uv[h] c_t
+ * over the tokens t < limit of tts_decode_attn (d_ctx_lens counts the tokens
+ * after this step's append; causal as there).  Computed in the absorbed form:
+ * q_nope w_uk[h] first (rounded to bf16), attention over the latents
+ * themselves, then w_uv[h] on the attended latent (rounded to bf16).
+ *  d_q_nope  bf16 [B][q_len][Hq][nope_dim]
+ *  d_q_rope  bf16 [B][q_len][Hq][64], rotated (tts_latent_append)
+ *  d_w_uk    bf16 [Hq][nope_dim][latent_dim];  d_w_uv  bf16 [Hq][v_dim][latent_dim]
+ *  d_out     bf16 [B][q_len][Hq][v_dim]
+ *  max_ctx_len  host upper bound of d_ctx_lens (sizes the workspace)
+ * nope_dim and v_dim are 64 or 128; num_q_heads * q_len <= 1024; all base
+ * addresses 16-byte aligned.  A stream whose context length is outside
+ * [q_len, min(max_ctx_len, 16 * max_blocks_per_seq)] gets zeros
+ * (TTS_ERRBIT_CTX_LEN); tokens in blocks with an invalid id are left out
+ * (TTS_ERRBIT_BLOCK_ID), and a row left without tokens gets zeros. */
+int tts_latent_decode_attn(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                           const int32_t *d_ctx_lens, int32_t max_ctx_len, int32_t B, int32_t q_len,
+                           int32_t num_q_heads, int32_t nope_dim, int32_t v_dim, float scale, int32_t causal,
+                           const void *d_q_nope, const void *d_q_rope, const void *d_w_uk, const void *d_w_uv,
+                           void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream);
+
+/* Bytes of device workspace tts_latent_prefill_attn needs (0 on bad
+ * arguments): the expanded keys and values of up to max_total_ctx tokens.
+ * Needs no particular contents; overlapping calls need separate workspaces. */
+size_t tts_latent_prefill_attn_workspace_size(int32_t B, int32_t num_rows, int32_t num_q_heads, int32_t latent_dim,
+                                              int32_t nope_dim, int32_t v_dim, int32_t max_total_ctx);
+
+/* Attention of whole prompts over the latent cache, causal: the rows of
+ * stream b are d_row_start[b] <= r < d_row_start[b + 1] (int32 [B + 1],
+ * non-decreasing, at most num_rows), the last tokens of its d_ctx_lens[b]
+ * cached ones, so row r sees the tokens
+ *   t < d_ctx_lens[b] - (d_row_start[b + 1] - r) + 1.
+ * The sum is tts_latent_decode_attn's, in the expanded form: keys and values
+ * of every head are multiplied out once (rounded to bf16).
+ *  d_q_nope bf16 [num_rows][Hq][nope_dim];  d_q_rope bf16 [num_rows][Hq][64]
+ *  d_out    bf16 [num_rows][Hq][v_dim]
+ *  max_total_ctx  host upper bound of the sum of d_ctx_lens over the streams
+ *                 that have rows
+ * Rows of no stream are left alone.  A stream whose rows do not lie in
+ * [0, num_rows], or whose context length is outside [its rows,
+ * 16 * max_blocks_per_seq] or takes the sum past max_total_ctx, gets zeros in
+ * its rows that lie in [0, num_rows) (TTS_ERRBIT_CTX_LEN); tokens in blocks
+ * with an invalid id are left out (TTS_ERRBIT_BLOCK_ID), and a row left
+ * without tokens gets zeros.  num_q_heads <= 1024; other limits as
+ * tts_latent_decode_attn. */
+int tts_latent_prefill_attn(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                            const int32_t *d_ctx_lens, int32_t max_total_ctx, int32_t B, const int32_t *d_row_start,
+                            int32_t num_rows, int32_t num_q_heads, int32_t nope_dim, int32_t v_dim, float scale,
+                            const void *d_q_nope, const void *d_q_rope, const void *d_w_uk, const void *d_w_uv,
+                            void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream);
+
 /* ------------------------------------------------------------------ head */
 
 /* Bytes of device workspace tts_codebook_head_select needs (0 on bad
