@@ -238,26 +238,6 @@ struct Segments {
 
 // ------------------------------------------------------------- attention
 
-// MN-major operand, 128-byte swizzle: 64 values of the M (or N) side a row,
-// 8-row groups of the contraction side 1024 bytes apart, the next 64 values of
-// the M side `stride` bytes on.
-__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t addr, uint32_t stride) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(stride >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
-constexpr uint32_t kTransposeA = 1u << 15;  // instruction descriptor: A is MN-major
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
-        " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // Barrier of the four softmax warps with an OR over their threads.
 __device__ __forceinline__ bool softmax_any(bool pred) {
     uint32_t r;
