@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "tts_common.cuh"
 #include "tts_decode.h"
 #include "tts_internal.h"
 
@@ -45,6 +46,46 @@ inline int launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
     }
     return TTS_OK;
 }
+
+// Lane 0's value, which the compiler then knows to be the same in every lane:
+// code that depends on nothing else is compiled for the uniform registers that
+// tcgen05 and TMA instructions take their operands from.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// Bounded mbarrier wait by a whole converged warp, with one answer.
+__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) {
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(bar), parity));
+    __syncwarp();
+    return ok;
+}
+// The same for several barriers at once.  A wait that succeeds at once still
+// takes about 0.1 us, in which a warp that issues MMAs leaves the tensor core
+// idle: every barrier is polled before the first answer is used.
+template <int kMax>
+struct WarpWaits {
+    uint32_t bar[kMax], parity[kMax];  // bar 0: none
+    __device__ __forceinline__ void set(int i, const uint64_t *b, uint32_t par) {
+        bar[i] = smem_addr(b);
+        parity[i] = par;
+    }
+    __device__ __forceinline__ void none(int i) { bar[i] = 0; }
+    __device__ __forceinline__ bool wait() const {
+        bool ok[kMax];
+#pragma unroll
+        for (int i = 0; i < kMax; ++i) ok[i] = bar[i] == 0 || mbar_try_wait(bar[i], parity[i]);
+        bool all = true;
+#pragma unroll
+        for (int i = 0; i < kMax; ++i) all = all && ok[i];
+        if (!__all_sync(0xFFFFFFFFu, all)) {
+            all = true;
+#pragma unroll
+            for (int i = 0; i < kMax; ++i) all = all && (bar[i] == 0 || mbar_wait(bar[i], parity[i]));
+            all = __all_sync(0xFFFFFFFFu, all);
+        }
+        __syncwarp();
+        return all;
+    }
+};
 
 // Number of a warp's first lanes with a true predicate.
 __device__ __forceinline__ int leading_true(bool pred) {

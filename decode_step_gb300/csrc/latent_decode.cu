@@ -61,99 +61,96 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// A 16-byte read-only load that stays where it is written, before a wait that
+// does not concern it (the compiler sinks a plain one to its use).
+__device__ __forceinline__ uint4 load_now(const __nv_bfloat16 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+
 // ------------------------------------------------------------------ absorb
 
 // q~[r][h][l] = sum_d q_nope[r][h][d] w_uk[h][d][l], rounded to bf16 (the MMA
-// that follows takes bf16), then q_rope[r][h] behind it.  A CTA holds the
-// [nope][64] slice of one head's weights in registers (each of its 4 warps a
-// quarter of d) and runs over 16-row chunks; the warps' sums meet in shared
-// memory.  The contraction's and the columns' order inside an MMA is free, so
-// a lane's weights are 16-byte loads: its 4 contraction rows are 4 adjacent d,
-// its 8 column blocks 8 adjacent l.
-// Latency-bound (2 MB of weights at 16 heads): the weights are in flight
-// before the wait for the previous kernel.
-constexpr int kAbsorbChunks = 4;  // 16-row chunks per CTA
+// that follows takes bf16), then q_rope[r][h] behind it.  A warp holds a
+// head's [nope][64] slice of the weights in registers and multiplies 16 query
+// rows at a time.  The contraction's and the columns' order inside an MMA is
+// free, so a lane's weights are 16-byte loads: its 4 contraction rows are 4
+// adjacent d, its 8 column blocks 8 adjacent l, and it ends with 16 adjacent l
+// of either row.  Latency-bound (2 MB of weights at 16 heads): the weights are
+// in flight before the wait for the previous kernel.
+constexpr int kAbsorbWarps = 4;
 
-template <int kSteps>  // 16-deep MMA steps per warp: nope / 64
-__global__ void __launch_bounds__(128)
+template <int kNope>
+__global__ void __launch_bounds__(kAbsorbWarps * 32)
 latent_absorb_kernel(const __nv_bfloat16 *__restrict__ q_nope, const __nv_bfloat16 *__restrict__ q_rope,
                      const __nv_bfloat16 *__restrict__ w_uk, __nv_bfloat16 *__restrict__ qt, int R, int Hq, int L) {
-    constexpr int kNope = 64 * kSteps;
-    __shared__ float red[4][16][68];
+    constexpr int kSteps = kNope / 16;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
     const int l0 = blockIdx.x * 64, h = blockIdx.y;
-    uint32_t b[kSteps][8][2];
+    uint4 w[kSteps][4];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int d = (warp * kSteps + s) * 16 + 4 * c;
-        uint4 w[4];
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = __ldg(reinterpret_cast<const uint4 *>(w_uk + (static_cast<size_t>(h) * kNope + d + i) * L + l0 + 8 * g));
-        const uint32_t *w0 = &w[0].x, *w1 = &w[1].x, *w2 = &w[2].x, *w3 = &w[3].x;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-            b[s][j][0] = __byte_perm(w0[j / 2], w1[j / 2], sel);
-            b[s][j][1] = __byte_perm(w2[j / 2], w3[j / 2], sel);
-        }
-    }
+            w[s][i] = load_now(w_uk + (static_cast<size_t>(h) * kNope + s * 16 + 4 * c + i) * L + l0 + 8 * g);
     pdl_wait_prerequisites();
     pdl_allow_dependents();  // only now: the attention reads the pool as soon as it starts
     const int W = L + kLatentRope;
-    const int r_end = min(R, (static_cast<int>(blockIdx.z) + 1) * kAbsorbChunks * 16);
-    for (int r0 = blockIdx.z * kAbsorbChunks * 16; r0 < r_end; r0 += 16) {
+    const int stride = gridDim.z * (blockDim.x / 32) * 16;
+    for (int r0 = (blockIdx.z * (blockDim.x / 32) + warp) * 16; r0 < R; r0 += stride) {
+        uint2 lo[kSteps], hi[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            lo[s] = hi[s] = make_uint2(0, 0);
+            const __nv_bfloat16 *x = q_nope + (static_cast<size_t>(r0 + g) * Hq + h) * kNope + s * 16 + 4 * c;
+            if (r0 + g < R) lo[s] = *reinterpret_cast<const uint2 *>(x);
+            if (r0 + g + 8 < R) hi[s] = *reinterpret_cast<const uint2 *>(x + static_cast<size_t>(8) * Hq * kNope);
+        }
         float acc[8][4] = {};
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int d = (warp * kSteps + s) * 16 + 4 * c;
-            uint2 lo = make_uint2(0, 0), hi = make_uint2(0, 0);
-            if (r0 + g < R)
-                lo = *reinterpret_cast<const uint2 *>(q_nope + (static_cast<size_t>(r0 + g) * Hq + h) * kNope + d);
-            if (r0 + g + 8 < R)
-                hi = *reinterpret_cast<const uint2 *>(q_nope + (static_cast<size_t>(r0 + g + 8) * Hq + h) * kNope + d);
-            const uint32_t a[4] = {lo.x, hi.x, lo.y, hi.y};
+            const uint32_t a[4] = {lo[s].x, hi[s].x, lo[s].y, hi[s].y};
+            const uint32_t *w0 = &w[s][0].x, *w1 = &w[s][1].x, *w2 = &w[s][2].x, *w3 = &w[s][3].x;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) mma16816(acc[j], a, b[s][j][0], b[s][j][1]);
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+                mma16816(acc[j], a, __byte_perm(w0[j / 2], w1[j / 2], sel), __byte_perm(w2[j / 2], w3[j / 2], sel));
+            }
         }
-        // column 2c (+1) of block j is l0 + 16 c (+ 8) + j
+        // column 2c (+ 1) of block j is l0 + 16 c (+ 8) + j
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            red[warp][g][16 * c + j] = acc[j][0];
-            red[warp][g][16 * c + 8 + j] = acc[j][1];
-            red[warp][g + 8][16 * c + j] = acc[j][2];
-            red[warp][g + 8][16 * c + 8 + j] = acc[j][3];
-        }
-        __syncthreads();
-        const int row = threadIdx.x / 8, col = threadIdx.x % 8 * 8;
-        if (r0 + row < R) {
-            float x[8];
+        for (int half = 0; half < 2; ++half) {
+            const int r = r0 + g + 8 * half;
+            if (r >= R) continue;
+            __nv_bfloat16 *dst = qt + (static_cast<size_t>(r) * Hq + h) * W;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = (red[0][row][col + i] + red[1][row][col + i]) + (red[2][row][col + i] + red[3][row][col + i]);
-            __nv_bfloat16 *dst = qt + (static_cast<size_t>(r0 + row) * Hq + h) * W;
-            *reinterpret_cast<uint4 *>(dst + l0 + col) =
-                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-            if (blockIdx.x == 0)
-                *reinterpret_cast<uint4 *>(dst + L + col) = *reinterpret_cast<const uint4 *>(
-                    q_rope + (static_cast<size_t>(r0 + row) * Hq + h) * kLatentRope + col);
+            for (int e = 0; e < 2; ++e) {
+                const int i = 2 * half + e;
+                *reinterpret_cast<uint4 *>(dst + l0 + 16 * c + 8 * e) =
+                    make_uint4(pack_bf16(acc[0][i], acc[1][i]), pack_bf16(acc[2][i], acc[3][i]),
+                               pack_bf16(acc[4][i], acc[5][i]), pack_bf16(acc[6][i], acc[7][i]));
+                if (blockIdx.x == 0)
+                    *reinterpret_cast<uint4 *>(dst + L + 16 * c + 8 * e) = *reinterpret_cast<const uint4 *>(
+                        q_rope + (static_cast<size_t>(r) * Hq + h) * kLatentRope + 16 * c + 8 * e);
+            }
         }
-        __syncthreads();
     }
 }
 
 // -------------------------------------------------------------- work split
 
 // The work units are the 64-token tiles of every (stream, row group), group
-// bg = b * G + g, in order; CTA c of P takes units [U c / P, U (c + 1) / P).
-// The part of a group that a CTA takes is a segment; its partial result goes
-// to slot c + bg (unique: going on to the next segment raises one of the two).
+// bg = b * G + g, in order, cut evenly over the CTAs.  The part of a group
+// that a CTA takes is a segment; its partial result goes to slot c + bg
+// (unique: going on to the next segment raises one of the two).
 struct LatentPlan {
     int G, N;       // row groups a stream, rows per group (a multiple of 16)
     int P;          // CTAs
+    long units;     // at most
     size_t slots;   // P + B * G
-    size_t qt_bytes, part_bytes, ml_bytes, starts_bytes;
-    size_t total() const { return qt_bytes + part_bytes + ml_bytes + starts_bytes; }
+    size_t qt_bytes, part_bytes, ml_bytes, owner_bytes;
+    size_t total() const { return qt_bytes + part_bytes + ml_bytes + owner_bytes; }
 };
 
 LatentPlan latent_plan(int B, int q_len, int Hq, int L, int max_ctx) {
@@ -161,25 +158,30 @@ LatentPlan latent_plan(int B, int q_len, int Hq, int L, int max_ctx) {
     const int rows = q_len * Hq;
     p.G = (rows + kMaxGroup - 1) / kMaxGroup;
     p.N = ((rows + p.G - 1) / p.G + 15) / 16 * 16;
-    const long units = static_cast<long>(B) * p.G * ((static_cast<long>(max_ctx) + kTile - 1) / kTile);
-    p.P = units < kCtas ? static_cast<int>(units < 1 ? 1 : units) : kCtas;
+    p.units = static_cast<long>(B) * p.G * ((static_cast<long>(max_ctx) + kTile - 1) / kTile);
+    p.P = p.units < kCtas ? static_cast<int>(p.units < 1 ? 1 : p.units) : kCtas;
     p.slots = static_cast<size_t>(p.P) + static_cast<size_t>(B) * p.G;
     p.qt_bytes = align_up(static_cast<size_t>(B) * rows * (L + kLatentRope) * 2, 256);
     p.part_bytes = align_up(p.slots * p.N * L * 4, 256);
     p.ml_bytes = align_up(p.slots * p.N * 8, 256);
-    p.starts_bytes = align_up((static_cast<size_t>(B) + 1) * 8, 256);
+    p.owner_bytes = align_up(static_cast<size_t>(B) * p.G * 8, 256);
     return p;
 }
 
-// (of the CTAs launched, as many as there are units take part, so that every
-// one of them has a unit and a group's CTAs are consecutive)
-__device__ __forceinline__ int active_ctas(long long U, int launched) {
-    return U < launched ? static_cast<int>(U) : launched;
-}
-__device__ __forceinline__ long long unit_begin(long long U, int c, int P) { return U * c / P; }
-__device__ __forceinline__ int unit_owner(long long U, long long u, int P) {
-    return static_cast<int>(((u + 1) * P - 1) / U);
-}
+// U units over the launched CTAs: the first U % P get one more than the rest.
+// With fewer units than CTAs only the first U take part, so that a group's
+// CTAs are consecutive and every one of them has a unit.
+struct UnitCut {
+    int each, rem, wide;  // units per CTA, CTAs with one more, units in those
+    __device__ __forceinline__ UnitCut(int U, int launched) {
+        const int P = max(1, min(U, launched));
+        each = U / P;
+        rem = U - each * P;
+        wide = rem * (each + 1);
+    }
+    __device__ __forceinline__ int begin(int c) const { return c * each + min(c, rem); }
+    __device__ __forceinline__ int owner(int u) const { return u < wide ? u / (each + 1) : rem + (u - wide) / each; }
+};
 
 struct LatentAttnArgs {
     const int32_t *table;
@@ -191,35 +193,36 @@ struct LatentAttnArgs {
     int causal;
     float *part;       // [slots][N][L] unnormalised o~
     float2 *ml;        // [slots][N] running maximum (log2 units), sum
-    long long *starts; // [B + 1] first unit of each stream, U last
+    int2 *owner;       // [B * G] first and last CTA of each group (1, 0: no unit)
     int32_t *err;
     int pairs, ropes;  // ring slots
 };
 
 // Tiles of stream b (0: its length is out of range).
 __device__ __forceinline__ int stream_tiles(const LatentAttnArgs &a, int b, int *ctx_out = nullptr) {
-    const int ctx = a.ctx_lens[b];
+    const int ctx = __ldg(a.ctx_lens + b);
     if (ctx_out) *ctx_out = ctx;
     if (ctx < a.q_len || ctx > a.max_ctx || ctx > a.max_blocks * TTS_BLOCK_TOKENS) return 0;
     return (ctx + kTile - 1) / kTile;
 }
 
-// Walks a CTA's segments; every role keeps its own copy.
+// Walks a CTA's segments; every warp keeps its own copy.
 struct Segments {
     int b, g, tile;        // next segment's start
-    long long left;        // units left
+    int left;              // units left
     // current segment
     int ctx, first, count; // first tile, tiles
     int bg;
     __device__ __forceinline__ bool next(const LatentAttnArgs &a) {
         while (left > 0) {
-            const int n = stream_tiles(a, b, &ctx);
+            const int n = uniform(stream_tiles(a, b, &ctx));
+            ctx = uniform(ctx);
             if (n == 0) {  // (never the CTA's first stream)
                 ++b;
                 continue;
             }
             first = tile;
-            count = static_cast<int>(min(static_cast<long long>(n - tile), left));
+            count = min(n - tile, left);
             bg = b * a.G + g;
             left -= count;
             cur_b = b;
@@ -253,15 +256,35 @@ __device__ __forceinline__ bool softmax_any(bool pred) {
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
+// Position in a ring of shared-memory slots; phase is the parity of the
+// slot's current filling.
+struct Ring {
+    uint32_t n, slot = 0, phase = 0;
+    __device__ __forceinline__ explicit Ring(uint32_t slots) : n(slots) {}
+    __device__ __forceinline__ void next() {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    __device__ __forceinline__ void back() {
+        if (slot == 0) {
+            slot = n;
+            phase ^= 1;
+        }
+        --slot;
+    }
+};
+
 constexpr int kMaxPairs = 16, kMaxRopes = 4;
 
 struct AttnShared {
     uint64_t full_l[kMaxPairs], empty_l[kMaxPairs], full_r[kMaxRopes], empty_r[kMaxRopes];
-    uint64_t s_full[2], s_empty[2], p_full, p_empty, o_empty, q_full, q_empty, done;
-    long long U;
+    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], o_empty, q_full[2], q_empty[2], done;
     int start_b, start_g, start_tile;
     uint32_t tmem;
-    long long sums[8];
+    int sums[8];
+    int failed;
     float mref[kMaxGroup], fac[kMaxGroup];
     int limit[kMaxGroup];
     union {
@@ -270,10 +293,11 @@ struct AttnShared {
     };
 };
 
-// mbar_wait by a whole warp, with one answer.
-__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) {
-    return __all_sync(kFull, mbar_wait(smem_addr(bar), parity));
-}
+// Buffers for the weights P: with one, the softmax waits for the O^T of the
+// tile before; wide groups need the space for the ring.
+__host__ __device__ constexpr int p_buffers(int N) { return N <= 48 ? 2 : 1; }
+// Buffers for q~: with two, a segment's rows are there when the one before ends.
+__host__ __device__ constexpr int q_buffers(int N) { return N <= 32 ? 2 : 1; }
 
 template <int N>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -281,13 +305,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                    const LatentAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = smem_addr(raw);
+    constexpr int kPBufs = p_buffers(N), kQBufs = q_buffers(N);
     const int chunks = a.L / 64, nb = (a.L + 127) / 128;
-    const uint32_t q_base = base;                                       // [chunks + 1][N][128 B]
-    const uint32_t p_base = q_base + (chunks + 1) * N * 128;            // [N][128 B]
-    const uint32_t r_base = p_base + N * 128;                           // rope ring
+    const uint32_t q_base = base, q_bytes = (chunks + 1) * N * 128;     // [kQBufs][chunks + 1][N][128 B]
+    const uint32_t p_base = q_base + kQBufs * q_bytes;                  // [kPBufs][N][128 B]
+    const uint32_t r_base = p_base + kPBufs * N * 128;                         // rope ring
     const uint32_t l_base = r_base + a.ropes * kChunkBytes;             // latent ring
     AttnShared &sh = *reinterpret_cast<AttnShared *>(raw + (l_base - base) + a.pairs * kPairBytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
 
     if (warp == 5 && lane == 0) {
         for (int i = 0; i < a.pairs; ++i) {
@@ -301,13 +326,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.s_full[i]), 1);
             mbar_init(smem_addr(&sh.s_empty[i]), 4);
+            mbar_init(smem_addr(&sh.p_full[i]), 4);
+            mbar_init(smem_addr(&sh.p_empty[i]), 1);
+            mbar_init(smem_addr(&sh.q_full[i]), 1);
+            mbar_init(smem_addr(&sh.q_empty[i]), 1);
         }
-        mbar_init(smem_addr(&sh.p_full), 4);
-        mbar_init(smem_addr(&sh.p_empty), 1);
         mbar_init(smem_addr(&sh.o_empty), 4);
-        mbar_init(smem_addr(&sh.q_full), 1);
-        mbar_init(smem_addr(&sh.q_empty), 1);
         mbar_init(smem_addr(&sh.done), 1);
+        sh.failed = 0;
         fence_mbar_init();
         prefetch_tensormap(&map_kv);
         prefetch_tensormap(&map_q);
@@ -323,234 +349,255 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
     // ---- this CTA's units: a scan of the streams' tile counts
     const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
-    long long mine = 0;
+    int mine = 0;
     for (int b = b0; b < b1; ++b) {
         const int n = stream_tiles(a, b);
         mine += n;
         if (n == 0 && blockIdx.x == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
     }
-    long long incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-        const long long x = __shfl_up_sync(kFull, incl, o);
+        const int x = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += x;
     }
     if (lane == 31) sh.sums[warp] = incl;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    long long before = incl - mine, total = 0;
+    int before = incl - mine, total = 0;
+#pragma unroll
     for (int w = 0; w < kAttnThreads / 32; ++w) {
         if (w < warp) before += sh.sums[w];
         total += sh.sums[w];
     }
-    const long long U = total * a.G;
-    const int P = active_ctas(U, gridDim.x), me = blockIdx.x;
-    const long long u0 = me < P ? unit_begin(U, me, P) : U, u1 = me < P ? unit_begin(U, me + 1, P) : U;
-    {
-        long long at = before * a.G;
+    const int U = total * a.G;
+    const UnitCut cut(U, gridDim.x);
+    const int u0 = min(U, cut.begin(blockIdx.x)), u1 = min(U, cut.begin(blockIdx.x + 1));
+    if (u0 < u1 || blockIdx.x == 0) {
+        int at = before * a.G;
         for (int b = b0; b < b1; ++b) {
-            const long long n = stream_tiles(a, b);
-            if (blockIdx.x == 0) a.starts[b] = at;
+            const int n = stream_tiles(a, b);
             if (u0 < u1 && u0 >= at && u0 < at + n * a.G) {
                 sh.start_b = b;
-                sh.start_g = static_cast<int>((u0 - at) / n);
-                sh.start_tile = static_cast<int>((u0 - at) % n);
+                sh.start_g = (u0 - at) / n;
+                sh.start_tile = (u0 - at) % n;
             }
+            if (blockIdx.x == 0)
+                for (int g = 0; g < a.G; ++g)
+                    a.owner[b * a.G + g] =
+                        n ? make_int2(cut.owner(at + g * n), cut.owner(at + (g + 1) * n - 1)) : make_int2(1, 0);
             at += n * a.G;
         }
-        if (blockIdx.x == 0 && threadIdx.x == 0) a.starts[a.B] = U;
     }
     __syncthreads();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = uniform(sh.tmem);
     Segments seg;
-    seg.left = u1 - u0;
-    seg.b = sh.start_b;
-    seg.g = sh.start_g;
-    seg.tile = sh.start_tile;
+    seg.left = uniform(u1 - u0);
+    seg.b = uniform(sh.start_b);
+    seg.g = uniform(sh.start_g);
+    seg.tile = uniform(sh.start_tile);
     pdl_allow_dependents();
     bool ok = true;
 
     if (warp == 4) {
-        // ---- KV producer: per tile the rope chunk, then the latent pairs;
-        // lanes 0-3 each fetch one block's 16 rows.  A block outside the pool
-        // (or past the context) is read out of range, which fills zeros.
+        // ---- KV producer: per tile the rope chunk, then the latent pairs,
+        // one copy per block of 16 rows and 64 values.  A block outside the
+        // pool (or past the context) is read out of range, which fills zeros.
+        const uint32_t leader = elect_leader();
         const int oob = a.num_blocks * TTS_BLOCK_TOKENS;
+        Ring rope(a.ropes), lat(a.pairs);
         uint32_t it = 0, lpos = 0;
-        const uint32_t ropes = a.ropes, pairs = a.pairs;
         while (ok && seg.next(a)) {
             const int32_t *row = a.table + static_cast<size_t>(seg.cur_b) * a.max_blocks;
             const int blocks = (seg.ctx + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS;
             auto fetch = [&](int tile) {
-                const int i = tile * 4 + lane;
-                return lane < 4 && i < blocks ? row[i] : -1;
+                const int i = tile * 4 + (lane & 3);
+                return i < blocks ? row[i] : -1;
             };
             int id = fetch(seg.first);
-            for (int k = 0; ok && k < seg.count; ++k, ++it) {
+            for (int k = 0; ok && k < seg.count; ++k) {
                 const int tile = seg.first + k;
                 int y = oob;
-                if (lane < 4 && tile * 4 + lane < blocks) {
+                if (tile * 4 + (lane & 3) < blocks) {
                     if (id >= 0 && id < a.num_blocks) y = id * TTS_BLOCK_TOKENS;
                     else flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
                 }
                 if (k + 1 < seg.count) id = fetch(tile + 1);
-                const uint32_t rs = it % ropes;
-                const uint32_t fr = smem_addr(&sh.full_r[rs]);
-                if (it >= ropes && !warp_wait(&sh.empty_r[rs], (it / ropes - 1) & 1)) {
+                int ys[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ys[i] = __shfl_sync(kFull, y, i);
+                if (it >= rope.n && !warp_wait(&sh.empty_r[rope.slot], rope.phase ^ 1)) {
                     ok = false;
                     break;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(fr, kChunkBytes);
-                __syncwarp();
-                if (lane < 4) tma_load_2d(r_base + rs * kChunkBytes + lane * 2048, &map_kv, a.L, y, fr);
-                for (int p = 0; p < nb; ++p, ++lpos) {
-                    const uint32_t ls = lpos % pairs;
-                    const uint32_t fl = smem_addr(&sh.full_l[ls]);
-                    if (lpos >= pairs && !warp_wait(&sh.empty_l[ls], (lpos / pairs - 1) & 1)) {
+                const uint32_t fr = smem_addr(&sh.full_r[rope.slot]), at = r_base + rope.slot * kChunkBytes;
+                mbar_expect_tx_by(leader, fr, kChunkBytes);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tma_load_2d_by(leader, at + i * 2048, &map_kv, a.L, ys[i], fr);
+                rope.next();
+                ++it;
+                for (int p = 0; p < nb; ++p) {
+                    if (lpos >= lat.n && !warp_wait(&sh.empty_l[lat.slot], lat.phase ^ 1)) {
                         ok = false;
                         break;
                     }
-                    const int halves = min(2, chunks - 2 * p);
-                    if (lane == 0) mbar_arrive_expect_tx(fl, halves * kChunkBytes);
-                    __syncwarp();
-                    if (lane < 4)
-                        for (int i = 0; i < halves; ++i)
-                            tma_load_2d(l_base + ls * kPairBytes + i * kChunkBytes + lane * 2048, &map_kv,
-                                        (2 * p + i) * 64, y, fl);
+                    const uint32_t fl = smem_addr(&sh.full_l[lat.slot]), to = l_base + lat.slot * kPairBytes;
+                    const bool both = 2 * p + 1 < chunks;
+                    mbar_expect_tx_by(leader, fl, both ? kPairBytes : kChunkBytes);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tma_load_2d_by(leader, to + i * 2048, &map_kv, p * 128, ys[i], fl);
+                    if (both)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            tma_load_2d_by(leader, to + kChunkBytes + i * 2048, &map_kv, p * 128 + 64, ys[i], fl);
+                    lat.next();
+                    ++lpos;
                 }
             }
         }
         // every copy lands before the CTA ends
-        if (lane == 0) {
-            for (uint32_t i = it > ropes ? it - ropes : 0; i < it; ++i)
-                mbar_wait(smem_addr(&sh.full_r[i % ropes]), (i / ropes) & 1);
-            for (uint32_t i = lpos > pairs ? lpos - pairs : 0; i < lpos; ++i)
-                mbar_wait(smem_addr(&sh.full_l[i % pairs]), (i / pairs) & 1);
+        for (uint32_t i = min(it, rope.n); i > 0; --i) {
+            rope.back();
+            warp_wait(&sh.full_r[rope.slot], rope.phase);
+        }
+        for (uint32_t i = min(lpos, lat.n); i > 0; --i) {
+            lat.back();
+            warp_wait(&sh.full_l[lat.slot], lat.phase);
         }
     } else if (warp == 6) {
         // ---- Q loader: a segment's q~ rows, once the S MMAs of the one before are done
         pdl_wait_prerequisites();
-        if (lane == 0) {
-            uint32_t s = 0;
-            for (; seg.next(a); ++s) {
-                if (s > 0 && !mbar_wait(smem_addr(&sh.q_empty), (s - 1) & 1)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t bar = smem_addr(&sh.q_full);
-                mbar_arrive_expect_tx(bar, (chunks + 1) * N * 128);
-                const int y = seg.cur_b * a.q_len * a.Hq + seg.cur_g * N;
-                for (int c = 0; c <= chunks; ++c) tma_load_2d(q_base + c * N * 128, &map_q, c * 64, y, bar);
-            }
-            if (s > 0) mbar_wait(smem_addr(&sh.q_full), (s - 1) & 1);
-        }
-    } else if (warp == 5) {
-        // ---- MMA issuer (one lane issues; the warp clears stale rows).  S^T of
-        // tile i + 1 goes before O^T of tile i, so the tensor core works on it
-        // while the softmax warps turn S^T of tile i into weights.
-        constexpr uint32_t idesc_s = mma_idesc(64, N);
-        constexpr uint32_t idesc_o = mma_idesc(128, N) | kTransposeA;
-        uint32_t it = 0, lpos = 0, segs = 0;
-        const uint32_t ropes = a.ropes, pairs = a.pairs;
-        // the tile whose O^T is outstanding
-        bool pending = false, pend_first = false;
-        uint32_t pend_lpos = 0, pend_seg = 0;
-        auto issue_o = [&]() -> bool {
-            // the outstanding tile is it - 1, before and after the loop
-            if (!warp_wait(&sh.p_full, (it - 1) & 1)) return false;
-            if (pend_first && pend_seg > 0 && !warp_wait(&sh.o_empty, (pend_seg - 1) & 1)) return false;
-            tc_fence_after();
-            if (lane == 0) {
-                for (int p = 0; p < nb; ++p) {
-                    const uint32_t ls = (pend_lpos + p) % pairs;
-                    const uint32_t sa = l_base + ls * kPairBytes;
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_bf16(tmem + (2 + p) * N, sw128_mn_desc(sa + k * 2048, kChunkBytes),
-                                 sw128_desc(p_base + k * 32), idesc_o, !(pend_first && k == 0));
-                    mma_commit(smem_addr(&sh.empty_l[ls]));
-                }
-                mma_commit(smem_addr(&sh.p_empty));
-            }
-            __syncwarp();
-            return true;
-        };
-        while (ok && seg.next(a)) {
-            if (!warp_wait(&sh.q_full, segs & 1)) {
+        const uint32_t leader = elect_leader();
+        uint32_t s = 0;
+        for (; seg.next(a); ++s) {
+            const uint32_t qb = s % kQBufs, use = s / kQBufs;
+            if (use > 0 && !warp_wait(&sh.q_empty[qb], (use - 1) & 1)) {
                 ok = false;
                 break;
             }
-            for (int k = 0; ok && k < seg.count; ++k) {
+            const uint32_t bar = smem_addr(&sh.q_full[qb]), at = q_base + qb * q_bytes;
+            mbar_expect_tx_by(leader, bar, q_bytes);
+            const int y = seg.cur_b * a.q_len * a.Hq + seg.cur_g * N;
+            for (int c = 0; c <= chunks; ++c) tma_load_2d_by(leader, at + c * N * 128, &map_q, c * 64, y, bar);
+        }
+        for (uint32_t i = s > kQBufs ? s - kQBufs : 0; i < s; ++i)
+            warp_wait(&sh.q_full[i % kQBufs], (i / kQBufs) & 1);
+    } else if (warp == 5) {
+        // ---- MMA issuer (the warp runs converged; it also clears stale rows).
+        // S^T of tile i + 1 goes before O^T of tile i, so the tensor core works
+        // on it while the softmax warps turn S^T of tile i into weights (the
+        // ring holds both tiles' pairs).
+        const uint32_t leader = elect_leader();
+        constexpr uint32_t idesc_s = mma_idesc(64, N);
+        constexpr uint32_t idesc_o = mma_idesc(128, N) | kTransposeA;
+        Ring rope(a.ropes), lat(a.pairs);
+        uint32_t it = 0, segs = 0;
+        // the tile whose O^T is outstanding: the one before `it`
+        bool pending = false, pend_first = false;
+        Ring pend(a.pairs);
+        uint32_t pend_seg = 0;
+        auto issue_o = [&](uint32_t tile) -> bool {
+            const uint32_t pb = tile % kPBufs;
+            WarpWaits<2> w;
+            w.set(0, &sh.p_full[pb], (tile / kPBufs) & 1);
+            w.none(1);
+            if (pend_first && pend_seg > 0) w.set(1, &sh.o_empty, (pend_seg - 1) & 1);
+            if (!w.wait()) return false;
+            tc_fence_after();
+            const uint32_t sb = p_base + pb * (N * 128);
+            for (int p = 0; p < nb; ++p) {
+                const uint32_t sa = l_base + pend.slot * kPairBytes;
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                    mma_bf16_by(leader, tmem + (2 + p) * N, sw128_mn_desc(sa + k * 2048, kChunkBytes),
+                                sw128_desc(sb + k * 32), idesc_o, !(pend_first && k == 0));
+                mma_commit_by(leader, smem_addr(&sh.empty_l[pend.slot]));
+                pend.next();
+            }
+            mma_commit_by(leader, smem_addr(&sh.p_empty[pb]));
+            return true;
+        };
+        while (ok && seg.next(a)) {
+            const int count = seg.count, left = seg.ctx - seg.first * kTile;  // tokens from the first tile on
+            const uint32_t qs = q_base + segs % kQBufs * q_bytes;
+            for (int k = 0; k < count; ++k) {
                 const uint32_t buf = it & 1;
-                if (it >= 2 && !warp_wait(&sh.s_empty[buf], (it / 2 - 1) & 1)) {
-                    ok = false;
-                    break;
+                // the rope chunk, S's buffer, the queries and the tile's pairs
+                WarpWaits<7> w;
+                w.set(0, &sh.full_r[rope.slot], rope.phase);
+                w.none(1);
+                if (it >= 2) w.set(1, &sh.s_empty[buf], (it / 2 - 1) & 1);
+                w.none(2);
+                if (k == 0) w.set(2, &sh.q_full[segs % kQBufs], (segs / kQBufs) & 1);
+                const Ring first = lat;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    w.none(3 + p);
+                    if (p < nb) {
+                        w.set(3 + p, &sh.full_l[lat.slot], lat.phase);
+                        lat.next();
+                    }
                 }
-                const uint32_t rs = it % ropes;
-                if (!warp_wait(&sh.full_r[rs], (it / ropes) & 1)) {
+                lat = first;
+                if (!w.wait()) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t sa = r_base + rs * kChunkBytes, sb = q_base + chunks * N * 128;
+                const uint32_t sr = r_base + rope.slot * kChunkBytes;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_by(leader, tmem + buf * N, sw128_desc(sr + kk * 32),
+                                sw128_desc(qs + chunks * N * 128 + kk * 32), idesc_s, kk != 0);
+                mma_commit_by(leader, smem_addr(&sh.empty_r[rope.slot]));
+                rope.next();
+                for (int p = 0; p < nb; ++p) {
+                    const uint32_t sa = l_base + lat.slot * kPairBytes, sb = qs + 2 * p * N * 128;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16(tmem + buf * N, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32), idesc_s, kk != 0);
-                    mma_commit(smem_addr(&sh.empty_r[rs]));
-                }
-                // rows behind the context in its last block hold anything (NaN
-                // times a zero weight would spread): clear them
-                const int end = seg.ctx - (seg.first + k) * kTile;  // tokens of the context in this tile
-                const int stale = end < kTile ? (TTS_BLOCK_TOKENS - end % TTS_BLOCK_TOKENS) % TTS_BLOCK_TOKENS : 0;
-                for (int p = 0; p < nb; ++p) {
-                    const uint32_t ls = (lpos + p) % pairs;
-                    if (!warp_wait(&sh.full_l[ls], ((lpos + p) / pairs) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = l_base + ls * kPairBytes;
-                    const int halves = min(2, chunks - 2 * p);
-                    if (stale) {
-                        for (int i = lane; i < halves * stale * 8; i += 32) {
-                            const uint32_t at = sa + (i / (stale * 8)) * kChunkBytes + end * 128 + i % (stale * 8) * 16;
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
-                    if (lane == 0)
-                        for (int i = 0; i < halves; ++i)
+                        mma_bf16_by(leader, tmem + buf * N, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32), idesc_s, 1);
+                    if (2 * p + 1 < chunks)
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16(tmem + buf * N, sw128_desc(sa + i * kChunkBytes + kk * 32),
-                                         sw128_desc(q_base + (2 * p + i) * N * 128 + kk * 32), idesc_s, 1);
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16_by(leader, tmem + buf * N, sw128_desc(sa + kChunkBytes + kk * 32),
+                                        sw128_desc(sb + N * 128 + kk * 32), idesc_s, 1);
+                    lat.next();
                 }
-                if (!ok) break;
-                if (lane == 0) {
-                    mma_commit(smem_addr(&sh.s_full[buf]));
-                    if (k + 1 == seg.count) mma_commit(smem_addr(&sh.q_empty));
-                }
-                __syncwarp();
-                if (pending && !issue_o()) {
+                mma_commit_by(leader, smem_addr(&sh.s_full[buf]));
+                if (k + 1 == count) mma_commit_by(leader, smem_addr(&sh.q_empty[segs % kQBufs]));
+                if (pending && !issue_o(it - 1)) {
                     ok = false;
                     break;
                 }
+                // rows behind the context in its last block hold anything (in
+                // O^T, NaN times a zero weight would spread): clear them.  S^T
+                // may read them before or after; its rows there are masked.
+                const int end = left - k * kTile;  // tokens of the context in this tile
+                const int stop = (end + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS * TTS_BLOCK_TOKENS;
+                if (end < kTile && end < stop) {
+                    Ring r = first;
+                    for (int p = 0; p < nb; ++p, r.next())
+                        for (int t = end + lane / 8; t < stop; t += 4) {
+                            const uint32_t at = l_base + r.slot * kPairBytes + t * 128 + lane % 8 * 16;
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + kChunkBytes), "r"(0)
+                                         : "memory");
+                        }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                }
                 pending = true;
                 pend_first = k == 0;
-                pend_lpos = lpos;
+                pend = first;
                 pend_seg = segs;
-                lpos += nb;
                 ++it;
             }
             ++segs;
         }
-        if (ok && pending && !issue_o()) ok = false;
-        if (lane == 0) {
-            mma_commit(smem_addr(&sh.done));
-            if (!mbar_wait(smem_addr(&sh.done), 0)) ok = false;
-        }
+        if (ok && pending && !issue_o(it - 1)) ok = false;
+        mma_commit_by(leader, smem_addr(&sh.done));
+        if (!warp_wait(&sh.done, 0)) ok = false;
     } else {
         // ---- softmax warps: lane l < 16 of warp w has token 16 w + l of the
         // tile (a 64-row accumulator's rows 16 w.. sit in lanes 32 w..), so a
@@ -559,6 +606,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         const int tok = warp * 16 + lane;
         const bool live = lane < 16;
+        auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1); };
         const int tid = threadIdx.x;
         while (ok && seg.next(a)) {
             const int32_t *row = a.table + static_cast<size_t>(seg.cur_b) * a.max_blocks;
@@ -605,9 +653,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 float top = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < N; ++n) top = fmaxf(top, fmaf(__uint_as_float(sr[n]), a.scale_log2, -sh.mref[n]));
+                if (!ok) sh.failed = 1;
                 if (softmax_any(top > kSlack || !ok)) {
                     // rare: raise the running maxima to this tile's, rescale sums and O
-                    if (softmax_any(!ok)) {
+                    if (*static_cast<volatile int *>(&sh.failed)) {  // (all four warps leave together)
                         ok = false;
                         break;
                     }
@@ -627,7 +676,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 #pragma unroll
                     for (int n = 0; n < N; ++n) l[n] *= sh.fac[n];
                     if (k > 0) {
-                        if (!warp_wait(&sh.p_empty, (it - 1) & 1)) ok = false;
+                        if (!o_added(it - 1)) ok = false;
                         tc_fence_after();
                         for (int p = 0; p < nb; ++p)
                             for (int c = 0; c < N; c += 16) {
@@ -641,31 +690,26 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                         tmem_wait_st();
                     }
                 }
-                float x[N];
+                // the tile that last used this P buffer has had its O^T added
+                if (it >= kPBufs && !o_added(it - kPBufs)) ok = false;
+                const uint32_t pb = p_base + it % kPBufs * (N * 128) + (tok & 7) * 2;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    x[n] = hw_ex2(fmaf(__uint_as_float(sr[n]), a.scale_log2, -sh.mref[n]));
-                    l[n] += x[n];  // fp32; only the weights that enter the MMA are rounded
-                }
-                // P of the tile before has been read (and its O^T added)
-                if (it > 0 && !warp_wait(&sh.p_empty, (it - 1) & 1)) ok = false;
-                if (live) {
-#pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        const uint32_t at = p_base + n * 128 + (((tok >> 3) ^ (n & 7)) << 4) + (tok & 7) * 2;
-                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at),
-                                     "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x[n])))
+                    const float x = hw_ex2(fmaf(__uint_as_float(sr[n]), a.scale_log2, -sh.mref[n]));
+                    l[n] += x;  // fp32; only the weights that enter the MMA are rounded
+                    if (live)
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(pb + n * 128 + (((tok >> 3) ^ (n & 7)) << 4)),
+                                     "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x)))
                                      : "memory");
-                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full));
+                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[it % kPBufs]));
                 valid = next_valid;
             }
             // ---- the segment's partial result
-            if (!warp_wait(&sh.p_empty, (it - 1) & 1)) ok = false;
+            if (!o_added(it - 1)) ok = false;
             if (softmax_any(!ok)) {  // (all four warps leave together)
                 ok = false;
                 break;
@@ -713,119 +757,154 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 // ------------------------------------------------------------------ output
 
 // out[r][h] = w_uv[h] o~[r][h], o~ the join of the row's splits (weights
-// 2^(m_s - max m)), rounded to bf16 for the MMA.  A CTA takes one head and 16
-// query rows; each of its v / 8 warps holds 8 of w_uv's rows in registers
-// (loaded before the wait for the attention).  The contraction's order inside
-// an MMA is free: a lane takes 8 adjacent l per 32, one 16-byte load.
+// 2^(m_s - max m)), rounded to bf16 for the MMA.  A CTA takes one head and
+// runs over chunks of 16 query rows; each of its v / 8 warps holds 8 of w_uv's
+// rows in registers (loaded before the wait for the attention).  The
+// contraction's order inside an MMA is free: a lane takes 8 adjacent l per 32,
+// one 16-byte load.  Latency-bound: a row's splits are read as soon as their
+// slots are known, with their maxima and sums; few rows share the warps.
+constexpr int kAtOnce = 2;  // splits of a row read together
+
 template <int kV>
 __global__ void __launch_bounds__(kV * 4)
-latent_out_kernel(const LatentAttnArgs a, int N, int launched, const __nv_bfloat16 *__restrict__ w_uv,
-                  __nv_bfloat16 *__restrict__ out) {
+latent_out_kernel(const LatentAttnArgs a, int N, const __nv_bfloat16 *__restrict__ w_uv, __nv_bfloat16 *__restrict__ out) {
     constexpr int kWarps = kV / 8;
-    constexpr int kMaxK = kLatentMaxDim / 32;
+    constexpr int kMaxK = kLatentMaxDim / 32, kMaxQ = kLatentMaxDim / 128;
     extern __shared__ float4 raw4[];
+    __shared__ float2 ms[kWarps];
     const int L = a.L, R = a.B * a.q_len;
     float *sums = reinterpret_cast<float *>(raw4);                 // [kWarps][L]
     uint8_t *at = reinterpret_cast<uint8_t *>(sums + kWarps * L);  // [16] rows of L bf16 + 64 bytes
     const int row_bytes = 2 * L + 64;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
-    const int r0 = blockIdx.x * 16, h = blockIdx.y;
+    const int h = blockIdx.y;
     uint4 w[kMaxK];
 #pragma unroll
     for (int k = 0; k < kMaxK; ++k)
         if (32 * k < L)
-            w[k] = __ldg(reinterpret_cast<const uint4 *>(w_uv + (static_cast<size_t>(h) * kV + warp * 8 + g) * L + 32 * k + 8 * c));
+            w[k] = load_now(w_uv + (static_cast<size_t>(h) * kV + warp * 8 + g) * L + 32 * k + 8 * c);
     pdl_wait_prerequisites();
     pdl_allow_dependents();
 
-    // ---- join: rows in turn to groups of `share` warps, which split the row's slots
-    const int rows = min(16, R - r0);
-    int share = kWarps;
-    while (share > 1 && kWarps / share < rows) share /= 2;
-    const long long U = a.starts[a.B];
-    const int P = active_ctas(U, launched);
-    for (int rr = 0; rr < 16; rr += kWarps / share) {
-        const int i = rr + warp / share, sub = warp % share;
-        if (i < rows) {
-            const int r = r0 + i, b = r / a.q_len, idx = (r % a.q_len) * a.Hq + h;
-            const int grp = idx / N, n = idx % N, bg = b * a.G + grp;
-            float o[kLatentMaxDim / 32] = {};
-            float inv = 0.0f;
-            const long long s0 = a.starts[b], len = (a.starts[b + 1] - s0) / a.G;
-            if (len > 0) {
-                const int c0 = unit_owner(U, s0 + grp * len, P), c1 = unit_owner(U, s0 + (grp + 1) * len - 1, P);
+    for (int r0 = blockIdx.x * 16; r0 < R; r0 += gridDim.x * 16) {
+        // ---- join: a row's splits are shared by `share` warps
+        const int rows = min(16, R - r0);
+        int share = kWarps;
+        while (share > 1 && kWarps / share < rows) share /= 2;
+        const int step = kWarps / share;
+        for (int rr = 0; rr < rows; rr += step) {
+            const int i = rr + warp / share, sub = warp % share;
+            if (i < rows) {
+                const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
+                const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
+                const int2 own = a.owner[bg];
+                const float2 *ml = a.ml + (static_cast<size_t>(own.x) + bg) * N + n;  // split s: ml[s * N]
+                const float *part = a.part + ((static_cast<size_t>(own.x) + bg) * N + n) * L + 4 * lane;
+                const size_t next = static_cast<size_t>(N) * L;
+                const int splits = own.y - own.x + 1;
+                float4 o[kMaxQ] = {};
                 float M = kNoScore, S = 0.0f;
-                for (int s = c0 + lane; s <= c1; s += 32) M = fmaxf(M, a.ml[(static_cast<size_t>(s) + bg) * N + n].x);
+                for (int s0 = sub; s0 < splits; s0 += kAtOnce * share) {
+                    float4 x[kAtOnce][kMaxQ];
+                    float2 v[kAtOnce];
 #pragma unroll
-                for (int k = 16; k > 0; k >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, k));
-                for (int s = c0 + lane; s <= c1; s += 32) {
-                    const float2 v = a.ml[(static_cast<size_t>(s) + bg) * N + n];
-                    S += v.y * hw_ex2(v.x - M);
-                }
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        const int s = s0 + u * share;
+                        v[u] = make_float2(kNoScore, 0.0f);
+                        if (s < splits) {
+                            v[u] = ml[static_cast<size_t>(s) * N];
 #pragma unroll
-                for (int k = 16; k > 0; k >>= 1) S += __shfl_xor_sync(kFull, S, k);
-                inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
-#pragma unroll 4
-                for (int s = c0 + sub; s <= c1; s += share) {
-                    const size_t at_row = (static_cast<size_t>(s) + bg) * N + n;
-                    const float f = hw_ex2(a.ml[at_row].x - M);
-                    const float2 *src = reinterpret_cast<const float2 *>(a.part + at_row * L);
+                            for (int k = 0; k < kMaxQ; ++k)
+                                if (128 * k + 4 * lane < L)
+                                    x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * next + 128 * k));
+                        }
+                    }
+                    float top = M;
 #pragma unroll
-                    for (int k = 0; k < kLatentMaxDim / 64; ++k)
-                        if (64 * k < L) {
-                            const float2 v = src[32 * k + lane];
-                            o[2 * k] = fmaf(f, v.x, o[2 * k]);
-                            o[2 * k + 1] = fmaf(f, v.y, o[2 * k + 1]);
+                    for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, v[u].x);
+                    const float f0 = hw_ex2(M - top);
+                    M = top;
+                    S *= f0;
+#pragma unroll
+                    for (int k = 0; k < kMaxQ; ++k) {
+                        o[k].x *= f0;
+                        o[k].y *= f0;
+                        o[k].z *= f0;
+                        o[k].w *= f0;
+                    }
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (s0 + u * share < splits) {
+                            const float f = hw_ex2(v[u].x - top);
+                            S = fmaf(f, v[u].y, S);
+#pragma unroll
+                            for (int k = 0; k < kMaxQ; ++k)
+                                if (128 * k + 4 * lane < L) {
+                                    o[k].x = fmaf(f, x[u][k].x, o[k].x);
+                                    o[k].y = fmaf(f, x[u][k].y, o[k].y);
+                                    o[k].z = fmaf(f, x[u][k].z, o[k].z);
+                                    o[k].w = fmaf(f, x[u][k].w, o[k].w);
+                                }
                         }
                 }
-            }
+                if (share == 1) {
+                    const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
 #pragma unroll
-            for (int k = 0; k < kLatentMaxDim / 64; ++k)
-                if (64 * k < L) {
-                    if (share == 1)
-                        *reinterpret_cast<uint32_t *>(at + i * row_bytes + 128 * k + 4 * lane) =
-                            pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-                    else
-                        reinterpret_cast<float2 *>(sums + warp * L)[32 * k + lane] =
-                            make_float2(o[2 * k] * inv, o[2 * k + 1] * inv);
+                    for (int k = 0; k < kMaxQ; ++k)
+                        if (128 * k + 4 * lane < L)
+                            *reinterpret_cast<uint2 *>(at + i * row_bytes + 256 * k + 8 * lane) =
+                                make_uint2(pack_bf16(o[k].x * inv, o[k].y * inv), pack_bf16(o[k].z * inv, o[k].w * inv));
+                } else {
+                    if (lane == 0) ms[warp] = make_float2(M, S);
+#pragma unroll
+                    for (int k = 0; k < kMaxQ; ++k)
+                        if (128 * k + 4 * lane < L) reinterpret_cast<float4 *>(sums + warp * L)[32 * k + lane] = o[k];
                 }
-        }
-        if (share > 1) {
-            __syncthreads();
-            for (int e = threadIdx.x; e < kWarps / share * (L / 2); e += blockDim.x) {
-                const int which = e / (L / 2), l2 = e % (L / 2), i2 = rr + which;
-                if (i2 < rows) {
-                    float x = 0.0f, y = 0.0f;
-                    for (int s = 0; s < share; ++s) {
-                        const float2 v = reinterpret_cast<const float2 *>(sums + (which * share + s) * L)[l2];
-                        x += v.x;
-                        y += v.y;
+            }
+            if (share > 1) {
+                __syncthreads();
+                for (int e = threadIdx.x; e < step * (L / 2); e += blockDim.x) {
+                    const int which = e / (L / 2), l2 = e - which * (L / 2), i2 = rr + which;
+                    if (i2 < rows) {
+                        float M = kNoScore, S = 0.0f, x = 0.0f, y = 0.0f;
+                        for (int s = 0; s < share; ++s) M = fmaxf(M, ms[which * share + s].x);
+                        for (int s = 0; s < share; ++s) {
+                            const float2 v = reinterpret_cast<const float2 *>(sums + (which * share + s) * L)[l2];
+                            const float f = hw_ex2(ms[which * share + s].x - M);
+                            S = fmaf(f, ms[which * share + s].y, S);
+                            x = fmaf(f, v.x, x);
+                            y = fmaf(f, v.y, y);
+                        }
+                        const float inv = S == 0.0f ? 0.0f : 1.0f / S;
+                        *reinterpret_cast<uint32_t *>(at + i2 * row_bytes + 4 * l2) = pack_bf16(x * inv, y * inv);
                     }
-                    *reinterpret_cast<uint32_t *>(at + i2 * row_bytes + 4 * l2) = pack_bf16(x, y);
                 }
+                if (rr + step < rows) __syncthreads();
             }
-            __syncthreads();
         }
-        if (rr + kWarps / share >= rows) break;
-    }
-    __syncthreads();
-    float acc[4] = {};
+        __syncthreads();
+        float acc[4][4] = {};
 #pragma unroll
-    for (int k = 0; k < kMaxK; ++k)
-        if (32 * k < L) {
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            if (g < rows) lo = *reinterpret_cast<const uint4 *>(at + g * row_bytes + 64 * k + 16 * c);
-            if (g + 8 < rows) hi = *reinterpret_cast<const uint4 *>(at + (g + 8) * row_bytes + 64 * k + 16 * c);
-            const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-            mma16816(acc, a0, w[k].x, w[k].y);
-            mma16816(acc, a1, w[k].z, w[k].w);
-        }
-    const int col = warp * 8 + 2 * c;
-    if (g < rows)
-        *reinterpret_cast<uint32_t *>(out + (static_cast<size_t>(r0 + g) * a.Hq + h) * kV + col) = pack_bf16(acc[0], acc[1]);
-    if (g + 8 < rows)
-        *reinterpret_cast<uint32_t *>(out + (static_cast<size_t>(r0 + g + 8) * a.Hq + h) * kV + col) =
-            pack_bf16(acc[2], acc[3]);
+        for (int k = 0; k < kMaxK; ++k)
+            if (32 * k < L) {
+                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                if (g < rows) lo = *reinterpret_cast<const uint4 *>(at + g * row_bytes + 64 * k + 16 * c);
+                if (g + 8 < rows) hi = *reinterpret_cast<const uint4 *>(at + (g + 8) * row_bytes + 64 * k + 16 * c);
+                const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
+                mma16816(acc[k % 2 * 2], a0, w[k].x, w[k].y);
+                mma16816(acc[k % 2 * 2 + 1], a1, w[k].z, w[k].w);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[0][i] = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
+        const int col = warp * 8 + 2 * c;
+        if (g < rows)
+            *reinterpret_cast<uint32_t *>(out + (static_cast<size_t>(r0 + g) * a.Hq + h) * kV + col) =
+                pack_bf16(acc[0][0], acc[0][1]);
+        if (g + 8 < rows)
+            *reinterpret_cast<uint32_t *>(out + (static_cast<size_t>(r0 + g + 8) * a.Hq + h) * kV + col) =
+                pack_bf16(acc[0][2], acc[0][3]);
+        __syncthreads();
+    }
 }
 
 // -------------------------------------------------------------------- host
@@ -843,12 +922,11 @@ int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, LatentAttnArgs
     // shared memory: q~, P, the rope slots, and latent pairs to the brim
     const int chunks = a.L / 64;
     a.ropes = N <= 32 ? 3 : 2;
-    const int fixed = (chunks + 2) * N * 128 + a.ropes * kChunkBytes + static_cast<int>(sizeof(AttnShared));
+    const int fixed = (q_buffers(N) * (chunks + 1) + p_buffers(N)) * N * 128 + a.ropes * kChunkBytes + static_cast<int>(sizeof(AttnShared));
     a.pairs = (kSmemLimit - fixed) / kPairBytes;
     if (a.pairs > kMaxPairs) a.pairs = kMaxPairs;
+    if (a.pairs < 2 * ((a.L + 127) / 128)) return TTS_ERR_UNSUPPORTED;  // (S^T goes one tile ahead of O^T)
     const int smem = fixed + a.pairs * kPairBytes;
-    // S^T of one tile is issued while the tile before still holds its pairs
-    if (a.pairs < 2 * ((a.L + 127) / 128)) return TTS_ERR_UNSUPPORTED;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_attn_kernel<N>), smem)) return TTS_ERR_CUDA;
     return launch_kernel(latent_attn_kernel<N>, dim3(P), dim3(kAttnThreads), smem, {stream, true}, kv, q, a);
 }
@@ -881,6 +959,7 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
         return TTS_ERR_INVALID;
     if (B == 0) return TTS_OK;
     const LatentPlan pl = latent_plan(B, q_len, num_q_heads, L, max_ctx_len);
+    if (pl.units > 0x40000000L) return TTS_ERR_UNSUPPORTED;  // units are 32-bit
     if (!d_ws || !aligned16(d_ws) || ws_bytes < pl.total()) return TTS_ERR_WORKSPACE;
 
     using bf = const __nv_bfloat16 *;
@@ -901,7 +980,7 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     a.causal = causal != 0;
     a.part = reinterpret_cast<float *>(ws + pl.qt_bytes);
     a.ml = reinterpret_cast<float2 *>(ws + pl.qt_bytes + pl.part_bytes);
-    a.starts = reinterpret_cast<long long *>(ws + pl.qt_bytes + pl.part_bytes + pl.ml_bytes);
+    a.owner = reinterpret_cast<int2 *>(ws + pl.qt_bytes + pl.part_bytes + pl.ml_bytes);
     a.err = d_err;
     const int R = B * q_len, W = L + kLatentRope;
     CUtensorMap map_kv, map_q;
@@ -911,10 +990,14 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
         return TTS_ERR_CUDA;
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const dim3 agrid(L / 64, num_q_heads, (R + 16 * kAbsorbChunks - 1) / (16 * kAbsorbChunks));
-    int rc = launch_kernel(nope_dim == 128 ? latent_absorb_kernel<2> : latent_absorb_kernel<1>, agrid, dim3(128), 0,
-                           {cs, thread_pdl()}, static_cast<bf>(d_q_nope), static_cast<bf>(d_q_rope),
-                           static_cast<bf>(d_w_uk), qt, R, num_q_heads, L);
+    // a warp per 16 query rows, up to 4 a CTA; more rows repeat over the
+    // weights in registers once every SM has two CTAs
+    const int chunks16 = (R + 15) / 16, aw = chunks16 < kAbsorbWarps ? chunks16 : kAbsorbWarps;
+    const int slices = L / 64 * num_q_heads, az = (2 * kCtas + slices - 1) / slices, am = (chunks16 + aw - 1) / aw;
+    int rc = launch_kernel(nope_dim == 128 ? latent_absorb_kernel<128> : latent_absorb_kernel<64>,
+                           dim3(L / 64, num_q_heads, am < az ? am : az), dim3(32 * aw), 0, {cs, thread_pdl()},
+                           static_cast<bf>(d_q_nope), static_cast<bf>(d_q_rope), static_cast<bf>(d_w_uk), qt, R,
+                           num_q_heads, L);
     if (rc != TTS_OK) return rc;
     switch (pl.N) {
         case 16: rc = launch_attention<16>(map_kv, map_q, a, pl.P, cs); break;
@@ -926,6 +1009,8 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     const int smem = (v_dim / 8) * L * 4 + 16 * (2 * L + 64);
     auto out_kernel = v_dim == 128 ? latent_out_kernel<128> : latent_out_kernel<64>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(out_kernel), smem)) return TTS_ERR_CUDA;
-    return launch_kernel(out_kernel, dim3((R + 15) / 16, num_q_heads), dim3(v_dim * 4), smem, {cs, true}, a, pl.N, pl.P,
-                         static_cast<bf>(d_w_uv), static_cast<__nv_bfloat16 *>(d_out));
+    // one CTA fits an SM: rows beyond one wave repeat over the weights in registers
+    const int wave = (kCtas + num_q_heads - 1) / num_q_heads;
+    return launch_kernel(out_kernel, dim3(chunks16 < wave ? chunks16 : wave, num_q_heads), dim3(v_dim * 4), smem,
+                         {cs, true}, a, pl.N, static_cast<bf>(d_w_uv), static_cast<__nv_bfloat16 *>(d_out));
 }

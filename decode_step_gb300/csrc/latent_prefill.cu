@@ -41,11 +41,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// mbar_wait by a whole warp, with one answer.
-__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) {
-    return __all_sync(kFull, mbar_wait(smem_addr(bar), parity));
-}
-
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -181,7 +176,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
     extern __shared__ uint8_t raw[];
     __shared__ ExpandShared sh;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int chunks = a.L / 64;
     if (warp == 5 && lane == 0) {
         for (int i = 0; i < kExpandStages; ++i) {
@@ -199,18 +194,18 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
+    const uint32_t tmem = uniform(sh.tmem);
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const bool is_k = static_cast<int>(blockIdx.x) < k_tiles;
     const int f0 = (is_k ? blockIdx.x : blockIdx.x - k_tiles) * kTile;
     const int features = a.Hq * (is_k ? a.nope : a.v);
     const int tile = blockIdx.y;
-    const int b = stream_of_row(a.tile_start, a.B, tile, lane);  // (every warp)
+    const int b = uniform(stream_of_row(a.tile_start, a.B, tile, lane));  // (every warp)
     bool ok = true;
     if (b >= 0) {
-        const int ctx = a.ctx_lens[b];
-        const int t0 = (tile - a.tile_start[b]) * kTile;
+        const int ctx = uniform(a.ctx_lens[b]);
+        const int t0 = uniform((tile - a.tile_start[b]) * kTile);
         const int end = min(kTile, ctx - t0);  // tokens of the context in this tile
         const int32_t *row = a.table + static_cast<size_t>(b) * a.max_blocks;
         if (warp == 4) {
@@ -245,6 +240,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
             // ---- MMA issuer; rows behind the context in its last block hold
             // anything and are cleared: their keys and values become zero
             const int stale = (TTS_BLOCK_TOKENS - end % TTS_BLOCK_TOKENS) % TTS_BLOCK_TOKENS;
+            const uint32_t leader = elect_leader();
             for (int c = 0; c < chunks; ++c) {
                 const int s = c % kExpandStages;
                 if (!warp_wait(&sh.full[s], (c / kExpandStages) & 1)) {
@@ -260,19 +256,14 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16(tmem, sw128_desc(at + kk * 32), sw128_desc(at + kChunkBytes + kk * 32),
-                                 mma_idesc(kTile, kTile), (c | kk) != 0);
-                    mma_commit(smem_addr(&sh.empty[s]));
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_by(leader, tmem, sw128_desc(at + kk * 32), sw128_desc(at + kChunkBytes + kk * 32),
+                                mma_idesc(kTile, kTile), (c | kk) != 0);
+                mma_commit_by(leader, smem_addr(&sh.empty[s]));
             }
-            if (lane == 0) {
-                mma_commit(smem_addr(&sh.acc));
-                if (!mbar_wait(smem_addr(&sh.acc), 0)) ok = false;
-            }
-            ok = __all_sync(kFull, ok);
+            mma_commit_by(leader, smem_addr(&sh.acc));
+            if (!warp_wait(&sh.acc, 0)) ok = false;
         } else {
             // ---- rotated key parts, then the accumulator
             if (blockIdx.x == 0) {
@@ -352,7 +343,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
     const uint32_t q_base = smem_addr(raw);                       // [2][kQc] chunks
     const uint32_t ring = q_base + 2 * kQc * kChunkBytes;
     PrefillShared &sh = *reinterpret_cast<PrefillShared *>(raw + (2 * kQc + kSlots) * kChunkBytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     if (warp == 9 && lane == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_addr(&sh.full[i]), 1);
@@ -375,17 +366,17 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;   // S0, S1, O0, O1: 128 columns each
+    const uint32_t tmem = uniform(sh.tmem);   // S0, S1, O0, O1: 128 columns each
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int h = blockIdx.x % a.Hq, qt = blockIdx.x / a.Hq;
-    const int b = stream_of_row(a.qtile_start, a.B, qt, lane);
+    const int b = uniform(stream_of_row(a.qtile_start, a.B, qt, lane));
     bool ok = true;
     if (b >= 0) {
-        const int first = a.row_start[b], n = a.row_start[b + 1] - first, ctx = a.ctx_lens[b];
+        const int first = uniform(a.row_start[b]), n = uniform(a.row_start[b + 1]) - first, ctx = uniform(a.ctx_lens[b]);
         // a stream's last tiles, which see the most tokens, come first
-        const int q = a.qtile_start[b + 1] - 1 - qt;
-        const int tile0 = a.tile_start[b];
+        const int q = uniform(a.qtile_start[b + 1]) - 1 - qt;
+        const int tile0 = uniform(a.tile_start[b]);
         const int r0 = q * kRows;                          // first row in the stream
         const bool two = r0 + kTile < n;
         // tokens either half sees, in tiles
@@ -423,66 +414,72 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                 for (int s = 0; s < (two ? 2 : 1); ++s) mbar_wait(smem_addr(&sh.q_full[s]), 0);
             }
         } else if (warp == 9) {
-            // ---- MMA issuer (one lane): S0(0) S1(0) | O0(j) S0(j+1) O1(j) S1(j+1) ...
+            // ---- MMA issuer: S0(0) S1(0) | O0(j) S0(j+1) O1(j) S1(j+1) ...
             // S of a half is overwritten right after the O product that reads
             // the weights kept in it; the tensor core runs them in order.
-            if (lane == 0) {
-                auto k_pos = [&](int j) { return static_cast<uint32_t>(j) * (kQc + kVc); };
-                auto wait_slot = [&](uint32_t pos) {
-                    if (!mbar_wait(smem_addr(&sh.full[pos % kSlots]), (pos / kSlots) & 1)) ok = false;
-                };
-                auto scores = [&](int s, int j, bool last_use) {
-                    for (int c = 0; ok && c < kQc; ++c) {
-                        const uint32_t pos = k_pos(j) + c;
-                        wait_slot(pos);
-                        if (!ok) return;
-                        tc_fence_after();
-                        const uint32_t sa = q_base + (s * kQc + c) * kChunkBytes, sb = ring + pos % kSlots * kChunkBytes;
+            const uint32_t leader = elect_leader();
+            bool go = true;
+            auto scores = [&](int s, int j, bool last_use) {
+                const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc);
+                WarpWaits<kQc + 1> w;
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16(tmem + s * kTile, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
-                                     mma_idesc(kTile, kTile), (c | kk) != 0);
-                        if (last_use) mma_commit(smem_addr(&sh.empty[pos % kSlots]));
-                    }
-                    mma_commit(smem_addr(&sh.s_full[s]));
-                };
-                auto output = [&](int s, int j, bool last_use) {
-                    if (!mbar_wait(smem_addr(&sh.p_full[s]), j & 1)) ok = false;
-                    for (int c = 0; ok && c < kVc; ++c) {
-                        const uint32_t pos = k_pos(j) + kQc + c;
-                        wait_slot(pos);
-                        if (!ok) return;
-                        tc_fence_after();
-                        const uint32_t sb = ring + pos % kSlots * kChunkBytes;
+                for (int c = 0; c < kQc; ++c) w.set(c, &sh.full[(pos + c) % kSlots], ((pos + c) / kSlots) & 1);
+                w.set(kQc, &sh.q_full[s], 0);
+                if (!w.wait()) {
+                    go = false;
+                    return;
+                }
+                tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_bf16_ts(tmem + (2 + s) * kTile + c * 64, tmem + s * kTile + kk * 8,
-                                        sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc(kTile, 64) | kTransposeB,
-                                        (j | kk) != 0);
-                        if (last_use) mma_commit(smem_addr(&sh.empty[pos % kSlots]));
-                    }
-                };
-                ok = mbar_wait(smem_addr(&sh.q_full[0]), 0);
-                if (ok) scores(0, 0, !two);
-                if (ok && two) {
-                    ok = mbar_wait(smem_addr(&sh.q_full[1]), 0);
-                    if (ok) scores(1, 0, true);
+                for (int c = 0; c < kQc; ++c) {
+                    const uint32_t slot = (pos + c) % kSlots;
+                    const uint32_t sa = q_base + (s * kQc + c) * kChunkBytes, sb = ring + slot * kChunkBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_by(leader, tmem + s * kTile, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
+                                    mma_idesc(kTile, kTile), (c | kk) != 0);
+                    if (last_use) mma_commit_by(leader, smem_addr(&sh.empty[slot]));
                 }
-                for (int j = 0; ok && j < nt; ++j) {
-                    if (j < nt0) {
-                        output(0, j, !two);
-                        if (ok && j + 1 < nt0) scores(0, j + 1, !two);
-                        if (ok && j + 1 == nt0) mma_commit(smem_addr(&sh.o_done[0]));
-                    }
-                    if (ok && two) {
-                        output(1, j, true);
-                        if (ok && j + 1 < nt1) scores(1, j + 1, true);
-                        if (ok && j + 1 == nt1) mma_commit(smem_addr(&sh.o_done[1]));
-                    }
+                mma_commit_by(leader, smem_addr(&sh.s_full[s]));
+            };
+            auto output = [&](int s, int j, bool last_use) {
+                const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc) + kQc;
+                WarpWaits<kVc + 1> w;
+#pragma unroll
+                for (int c = 0; c < kVc; ++c) w.set(c, &sh.full[(pos + c) % kSlots], ((pos + c) / kSlots) & 1);
+                w.set(kVc, &sh.p_full[s], j & 1);
+                if (!w.wait()) {
+                    go = false;
+                    return;
                 }
-                mma_commit(smem_addr(&sh.done));
-                if (!mbar_wait(smem_addr(&sh.done), 0)) ok = false;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kVc; ++c) {
+                    const uint32_t slot = (pos + c) % kSlots, sb = ring + slot * kChunkBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_bf16_ts_by(leader, tmem + (2 + s) * kTile + c * 64, tmem + s * kTile + kk * 8,
+                                       sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc(kTile, 64) | kTransposeB,
+                                       (j | kk) != 0);
+                    if (last_use) mma_commit_by(leader, smem_addr(&sh.empty[slot]));
+                }
+            };
+            scores(0, 0, !two);
+            if (go && two) scores(1, 0, true);
+            for (int j = 0; go && j < nt; ++j) {
+                if (j < nt0) {
+                    output(0, j, !two);
+                    if (go && j + 1 < nt0) scores(0, j + 1, !two);
+                    if (go && j + 1 == nt0) mma_commit_by(leader, smem_addr(&sh.o_done[0]));
+                }
+                if (go && two) {
+                    output(1, j, true);
+                    if (go && j + 1 < nt1) scores(1, j + 1, true);
+                    if (go && j + 1 == nt1) mma_commit_by(leader, smem_addr(&sh.o_done[1]));
+                }
             }
+            mma_commit_by(leader, smem_addr(&sh.done));
+            ok = warp_wait(&sh.done, 0) && go;
         } else if (warp < 4 || two) {
             // ---- softmax warpgroups: thread = query row
             const int s = warp / 4, w = warp % 4;
