@@ -58,6 +58,19 @@ __device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) 
     __syncwarp();
     return ok;
 }
+// Whether the phase has completed, without waiting (try_wait may suspend the
+// thread for a while).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // The same for several barriers at once.  A wait that succeeds at once still
 // takes about 0.1 us, in which a warp that issues MMAs leaves the tensor core
 // idle: every barrier is polled before the first answer is used.
@@ -69,19 +82,23 @@ struct WarpWaits {
         parity[i] = par;
     }
     __device__ __forceinline__ void none(int i) { bar[i] = 0; }
-    __device__ __forceinline__ bool wait() const {
+    __device__ __forceinline__ bool poll() const {
         bool ok[kMax];
 #pragma unroll
-        for (int i = 0; i < kMax; ++i) ok[i] = bar[i] == 0 || mbar_try_wait(bar[i], parity[i]);
+        for (int i = 0; i < kMax; ++i) ok[i] = bar[i] == 0 || mbar_test(bar[i], parity[i]);
         bool all = true;
 #pragma unroll
         for (int i = 0; i < kMax; ++i) all = all && ok[i];
-        if (!__all_sync(0xFFFFFFFFu, all)) {
-            all = true;
+        all = __all_sync(0xFFFFFFFFu, all);
+        __syncwarp();
+        return all;
+    }
+    __device__ __forceinline__ bool wait() const {
+        if (poll()) return true;
+        bool all = true;
 #pragma unroll
-            for (int i = 0; i < kMax; ++i) all = all && (bar[i] == 0 || mbar_wait(bar[i], parity[i]));
-            all = __all_sync(0xFFFFFFFFu, all);
-        }
+        for (int i = 0; i < kMax; ++i) all = all && (bar[i] == 0 || mbar_wait(bar[i], parity[i]));
+        all = __all_sync(0xFFFFFFFFu, all);
         __syncwarp();
         return all;
     }

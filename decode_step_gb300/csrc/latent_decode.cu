@@ -285,7 +285,8 @@ struct AttnShared {
     uint32_t tmem;
     int sums[8];
     int failed;
-    float mref[kMaxGroup], fac[kMaxGroup];
+    alignas(16) float mref[kMaxGroup];
+    float fac[kMaxGroup];
     int limit[kMaxGroup];
     union {
         uint32_t wmax[4][kMaxGroup];  // within a tile
@@ -497,13 +498,15 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         bool pending = false, pend_first = false;
         Ring pend(a.pairs);
         uint32_t pend_seg = 0;
-        auto issue_o = [&](uint32_t tile) -> bool {
-            const uint32_t pb = tile % kPBufs;
+        auto weights = [&](uint32_t tile) {  // what O^T of `tile` waits for
             WarpWaits<2> w;
-            w.set(0, &sh.p_full[pb], (tile / kPBufs) & 1);
+            w.set(0, &sh.p_full[tile % kPBufs], (tile / kPBufs) & 1);
             w.none(1);
             if (pend_first && pend_seg > 0) w.set(1, &sh.o_empty, (pend_seg - 1) & 1);
-            if (!w.wait()) return false;
+            return w;
+        };
+        auto issue_o = [&](uint32_t tile) {
+            const uint32_t pb = tile % kPBufs;
             tc_fence_after();
             const uint32_t sb = p_base + pb * (N * 128);
             for (int p = 0; p < nb; ++p) {
@@ -516,7 +519,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 pend.next();
             }
             mma_commit_by(leader, smem_addr(&sh.p_empty[pb]));
-            return true;
+            pending = false;
         };
         while (ok && seg.next(a)) {
             const int count = seg.count, left = seg.ctx - seg.first * kTile;  // tokens from the first tile on
@@ -540,7 +543,19 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     }
                 }
                 lat = first;
-                if (!w.wait()) {
+                // a tile that is still landing lets O^T of the one before go
+                // first, if its weights are there: that frees ring slots
+                bool ready = w.poll();
+                if (!ready && pending) {
+                    const WarpWaits<2> wo = weights(it - 1);
+                    const long long t0 = clock64();
+                    while (!ready && pending && ok) {
+                        if (wo.poll()) issue_o(it - 1);
+                        ready = w.poll();
+                        ok = uniform(clock64() - t0 < kWaitLimitCycles);
+                    }
+                }
+                if (!ok || (!ready && !w.wait())) {
                     ok = false;
                     break;
                 }
@@ -566,9 +581,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 }
                 mma_commit_by(leader, smem_addr(&sh.s_full[buf]));
                 if (k + 1 == count) mma_commit_by(leader, smem_addr(&sh.q_empty[segs % kQBufs]));
-                if (pending && !issue_o(it - 1)) {
-                    ok = false;
-                    break;
+                if (pending) {
+                    if (!weights(it - 1).wait()) {
+                        ok = false;
+                        break;
+                    }
+                    issue_o(it - 1);
                 }
                 // rows behind the context in its last block hold anything (in
                 // O^T, NaN times a zero weight would spread): clear them.  S^T
@@ -595,7 +613,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             }
             ++segs;
         }
-        if (ok && pending && !issue_o(it - 1)) ok = false;
+        if (ok && pending) {
+            ok = weights(it - 1).wait();
+            if (ok) issue_o(it - 1);
+        }
         mma_commit_by(leader, smem_addr(&sh.done));
         if (!warp_wait(&sh.done, 0)) ok = false;
     } else {
@@ -633,6 +654,17 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 const int tile = seg.first + k;
                 const uint32_t buf = it & 1;
                 const bool next_valid = k + 1 < seg.count && block_ok(tile + 1);
+                // (the tile that last used this P buffer has had its O^T added)
+                if (it >= kPBufs && kPBufs > 1 && !o_added(it - kPBufs)) ok = false;
+                float mr[N];
+#pragma unroll
+                for (int n = 0; n < N; n += 4) {
+                    const float4 m4 = *reinterpret_cast<const float4 *>(sh.mref + n);
+                    mr[n] = m4.x;
+                    mr[n + 1] = m4.y;
+                    mr[n + 2] = m4.z;
+                    mr[n + 3] = m4.w;
+                }
                 if (!warp_wait(&sh.s_full[buf], (it / 2) & 1)) ok = false;
                 tc_fence_after();
                 uint32_t sr[N];
@@ -650,9 +682,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     for (int n = 0; n < N; ++n)
                         if (t >= sh.limit[n]) sr[n] = 0xFF800000u;
                 }
-                float top = -INFINITY;
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int n = 0; n < N; ++n) top = fmaxf(top, fmaf(__uint_as_float(sr[n]), a.scale_log2, -sh.mref[n]));
+                for (int n = 0; n < N; ++n)
+                    tops[n % 4] = fmaxf(tops[n % 4], fmaf(__uint_as_float(sr[n]), a.scale_log2, -mr[n]));
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if (!ok) sh.failed = 1;
                 if (softmax_any(top > kSlack || !ok)) {
                     // rare: raise the running maxima to this tile's, rescale sums and O
@@ -674,7 +708,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     }
                     softmax_sync();
 #pragma unroll
-                    for (int n = 0; n < N; ++n) l[n] *= sh.fac[n];
+                    for (int n = 0; n < N; ++n) {
+                        l[n] *= sh.fac[n];
+                        mr[n] = sh.mref[n];
+                    }
                     if (k > 0) {
                         if (!o_added(it - 1)) ok = false;
                         tc_fence_after();
@@ -690,17 +727,16 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                         tmem_wait_st();
                     }
                 }
-                // the tile that last used this P buffer has had its O^T added
-                if (it >= kPBufs && !o_added(it - kPBufs)) ok = false;
-                const uint32_t pb = p_base + it % kPBufs * (N * 128) + (tok & 7) * 2;
+                if (it > 0 && kPBufs == 1 && !o_added(it - 1)) ok = false;
+                const uint32_t pb = p_base + it % kPBufs * (N * 128) + (tok & 7) * 2, px = (tok >> 3) << 4;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
-                    const float x = hw_ex2(fmaf(__uint_as_float(sr[n]), a.scale_log2, -sh.mref[n]));
+                    const float x = hw_ex2(fmaf(__uint_as_float(sr[n]), a.scale_log2, -mr[n]));
                     l[n] += x;  // fp32; only the weights that enter the MMA are rounded
+                    // (no memory clobber: the columns' chains overlap; the fence below orders the stores)
                     if (live)
-                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(pb + n * 128 + (((tok >> 3) ^ (n & 7)) << 4)),
-                                     "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x)))
-                                     : "memory");
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(pb + n * 128 + (px ^ ((n & 7) << 4))),
+                                     "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
@@ -729,15 +765,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             tc_fence_after();
             for (int p = 0; p < nb; ++p) {
                 const int d = p * 128 + warp * 32 + lane;
-                for (int c = 0; c < N; c += 16) {
-                    uint32_t o[16];
-                    tmem_ld16_nowait(tl + (2 + p) * N + c, o);
-                    tmem_wait_ld();
-                    if (d < a.L) {
-                        float *dst = a.part + (slot * N + c) * a.L + d;
+                uint32_t o[N];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) dst[static_cast<size_t>(i) * a.L] = __uint_as_float(o[i]);
-                    }
+                for (int c = 0; c < N; c += 16) tmem_ld16_nowait(tl + (2 + p) * N + c, o + c);
+                tmem_wait_ld();
+                if (d < a.L) {
+                    float *dst = a.part + slot * N * a.L + d;
+#pragma unroll
+                    for (int n = 0; n < N; ++n) dst[n * a.L] = __uint_as_float(o[n]);
                 }
             }
             tc_fence_before();
