@@ -46,94 +46,96 @@ constexpr float kNoScore = -1e30f;     // running maximum before any token (log2
 // well as 1, and O in tensor memory is rarely rescaled.
 constexpr float kSlack = 8.0f;
 
-// ---------------------------------------------------------------- mma.sync
-
-__device__ __forceinline__ void mma16816(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
-        " {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// A 16-byte read-only load that stays where it is written, before a wait that
-// does not concern it (the compiler sinks a plain one to its use).
-__device__ __forceinline__ uint4 load_now(const __nv_bfloat16 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-
 // ------------------------------------------------------------------ absorb
 
 // q~[r][h][l] = sum_d q_nope[r][h][d] w_uk[h][d][l], rounded to bf16 (the MMA
-// that follows takes bf16), then q_rope[r][h] behind it.  A warp holds a
-// head's [nope][64] slice of the weights in registers and multiplies 16 query
-// rows at a time.  The contraction's and the columns' order inside an MMA is
-// free, so a lane's weights are 16-byte loads: its 4 contraction rows are 4
-// adjacent d, its 8 column blocks 8 adjacent l, and it ends with 16 adjacent l
-// of either row.  Latency-bound (2 MB of weights at 16 heads): the weights are
-// in flight before the wait for the previous kernel.
-constexpr int kAbsorbWarps = 4;
+// that follows takes bf16).  A CTA takes one head, 128 of l and 128 query rows:
+// one tcgen05 product of nope / 16 steps (q K-major, the weights MN-major as
+// they lie), its result staged in shared memory and stored by TMA, which clips
+// the rows past R.  Latency-bound (2 MB of weights at 16 heads): the weights
+// are in flight before the wait for the previous kernel.
+constexpr int kRowTile = 128;
 
-template <int kNope>
-__global__ void __launch_bounds__(kAbsorbWarps * 32)
-latent_absorb_kernel(const __nv_bfloat16 *__restrict__ q_nope, const __nv_bfloat16 *__restrict__ q_rope,
-                     const __nv_bfloat16 *__restrict__ w_uk, __nv_bfloat16 *__restrict__ qt, int R, int Hq, int L) {
-    constexpr int kSteps = kNope / 16;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
-    const int l0 = blockIdx.x * 64, h = blockIdx.y;
-    uint4 w[kSteps][4];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[s][i] = load_now(w_uk + (static_cast<size_t>(h) * kNope + s * 16 + 4 * c + i) * L + l0 + 8 * g);
-    pdl_wait_prerequisites();
+__global__ void __launch_bounds__(128)
+latent_absorb_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_constant__ CUtensorMap map_uk,
+                     const __grid_constant__ CUtensorMap map_qt, int nope, int L, int R, int32_t *err) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ uint64_t full, acc;
+    __shared__ uint32_t tslot;
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+    const int l0 = blockIdx.x * 128, h = blockIdx.y, r0 = blockIdx.z * kRowTile;
+    const int halves = l0 + 64 < L ? 2 : 1;
+    const uint32_t wb = smem_addr(raw), w_chunk = nope * 128;   // [2][nope][64 l]
+    const uint32_t qb = wb + 2 * w_chunk, q_chunk = kRowTile * 128;  // [nope / 64][128 rows][64 d]
+    bool ok = true;
+    if (warp == 0) {
+        const uint32_t leader = elect_leader();
+        if (leader) {
+            mbar_init(smem_addr(&full), 1);
+            mbar_init(smem_addr(&acc), 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        mbar_expect_tx_by(leader, smem_addr(&full), halves * w_chunk + nope / 64 * q_chunk);
+        for (int i = 0; i < halves; ++i)
+            tma_load_2d_by(leader, wb + i * w_chunk, &map_uk, l0 + 64 * i, h * nope, smem_addr(&full));
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tslot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        pdl_wait_prerequisites();
+        for (int i = 0; i < nope / 64; ++i)
+            tma_load_2d_by(leader, qb + i * q_chunk, &map_qn, h * nope + 64 * i, r0, smem_addr(&full));
+    }
+    if (warp != 0) pdl_wait_prerequisites();
     pdl_allow_dependents();  // only now: the attention reads the pool as soon as it starts
-    const int W = L + kLatentRope;
-    const int stride = gridDim.z * (blockDim.x / 32) * 16;
-    for (int r0 = (blockIdx.z * (blockDim.x / 32) + warp) * 16; r0 < R; r0 += stride) {
-        uint2 lo[kSteps], hi[kSteps];
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uniform(tslot);
+    if (warp == 0) {
+        const uint32_t leader = elect_leader();
+        ok = warp_wait(&full, 0);
+        tc_fence_after();
+        const uint32_t idesc = (halves == 2 ? mma_idesc(kRowTile, 128) : mma_idesc(kRowTile, 64)) | kTransposeB;
+        for (int k = 0; k < nope / 16; ++k)
+            mma_bf16_by(leader, tmem, sw128_desc(qb + k / 4 * q_chunk + k % 4 * 32), sw128_mn_desc(wb + k * 2048, w_chunk),
+                        idesc, k != 0);
+        mma_commit_by(leader, smem_addr(&acc));
+    }
+    if (!warp_wait(&acc, 0)) ok = false;
+    tc_fence_after();
+    // the products have read the shared memory: stage the rows there, 64
+    // values of a row 128-byte swizzled
+    const int row = warp * 32 + lane;
+    if (ok && r0 + warp * 32 < R)
+        for (int c = 0; c < 2 * halves; ++c) {
+            uint32_t x[32];
+            tmem_ld32_nowait(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c * 32, x);
+            tmem_wait_ld();
+            const float *f = reinterpret_cast<const float *>(x);
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            lo[s] = hi[s] = make_uint2(0, 0);
-            const __nv_bfloat16 *x = q_nope + (static_cast<size_t>(r0 + g) * Hq + h) * kNope + s * 16 + 4 * c;
-            if (r0 + g < R) lo[s] = *reinterpret_cast<const uint2 *>(x);
-            if (r0 + g + 8 < R) hi[s] = *reinterpret_cast<const uint2 *>(x + static_cast<size_t>(8) * Hq * kNope);
-        }
-        float acc[8][4] = {};
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const uint32_t a[4] = {lo[s].x, hi[s].x, lo[s].y, hi[s].y};
-            const uint32_t *w0 = &w[s][0].x, *w1 = &w[s][1].x, *w2 = &w[s][2].x, *w3 = &w[s][3].x;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-                mma16816(acc[j], a, __byte_perm(w0[j / 2], w1[j / 2], sel), __byte_perm(w2[j / 2], w3[j / 2], sel));
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = wb + c / 2 * q_chunk + row * 128 + (((c % 2 * 4 + j) ^ (row & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack_bf16(f[8 * j], f[8 * j + 1])),
+                             "r"(pack_bf16(f[8 * j + 2], f[8 * j + 3])), "r"(pack_bf16(f[8 * j + 4], f[8 * j + 5])),
+                             "r"(pack_bf16(f[8 * j + 6], f[8 * j + 7])));
             }
         }
-        // column 2c (+ 1) of block j is l0 + 16 c (+ 8) + j
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int r = r0 + g + 8 * half;
-            if (r >= R) continue;
-            __nv_bfloat16 *dst = qt + (static_cast<size_t>(r) * Hq + h) * W;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = 2 * half + e;
-                *reinterpret_cast<uint4 *>(dst + l0 + 16 * c + 8 * e) =
-                    make_uint4(pack_bf16(acc[0][i], acc[1][i]), pack_bf16(acc[2][i], acc[3][i]),
-                               pack_bf16(acc[4][i], acc[5][i]), pack_bf16(acc[6][i], acc[7][i]));
-                if (blockIdx.x == 0)
-                    *reinterpret_cast<uint4 *>(dst + L + 16 * c + 8 * e) = *reinterpret_cast<const uint4 *>(
-                        q_rope + (static_cast<size_t>(r) * Hq + h) * kLatentRope + 16 * c + 8 * e);
-            }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (!ok) flag_error(err, TTS_ERRBIT_TIMEOUT);
+    tc_fence_before();
+    ok = !__syncthreads_or(!ok);
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
+        if (ok && lane == 0) {
+            for (int i = 0; i < halves; ++i) tma_store_2d(&map_qt, h * L + l0 + 64 * i, r0, wb + i * q_chunk);
+            asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
         }
     }
 }
@@ -161,7 +163,7 @@ LatentPlan latent_plan(int B, int q_len, int Hq, int L, int max_ctx) {
     p.units = static_cast<long>(B) * p.G * ((static_cast<long>(max_ctx) + kTile - 1) / kTile);
     p.P = p.units < kCtas ? static_cast<int>(p.units < 1 ? 1 : p.units) : kCtas;
     p.slots = static_cast<size_t>(p.P) + static_cast<size_t>(B) * p.G;
-    p.qt_bytes = align_up(static_cast<size_t>(B) * rows * (L + kLatentRope) * 2, 256);
+    p.qt_bytes = align_up(static_cast<size_t>(B) * rows * L * 2, 256);
     p.part_bytes = align_up(p.slots * p.N * L * 4, 256);
     p.ml_bytes = align_up(p.slots * p.N * 8, 256);
     p.owner_bytes = align_up(static_cast<size_t>(B) * p.G * 8, 256);
@@ -303,7 +305,7 @@ __host__ __device__ constexpr int q_buffers(int N) { return N <= 32 ? 2 : 1; }
 template <int N>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q,
-                   const LatentAttnArgs a) {
+                   const __grid_constant__ CUtensorMap map_qr, const LatentAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = smem_addr(raw);
     constexpr int kPBufs = p_buffers(N), kQBufs = q_buffers(N);
@@ -338,6 +340,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         fence_mbar_init();
         prefetch_tensormap(&map_kv);
         prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_qr);
     }
     uint32_t cols = 32;
     while (cols < static_cast<uint32_t>((nb + 2) * N)) cols *= 2;
@@ -480,7 +483,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             const uint32_t bar = smem_addr(&sh.q_full[qb]), at = q_base + qb * q_bytes;
             mbar_expect_tx_by(leader, bar, q_bytes);
             const int y = seg.cur_b * a.q_len * a.Hq + seg.cur_g * N;
-            for (int c = 0; c <= chunks; ++c) tma_load_2d_by(leader, at + c * N * 128, &map_q, c * 64, y, bar);
+            for (int c = 0; c < chunks; ++c) tma_load_2d_by(leader, at + c * N * 128, &map_q, c * 64, y, bar);
+            tma_load_2d_by(leader, at + chunks * N * 128, &map_qr, 0, y, bar);
         }
         for (uint32_t i = s > kQBufs ? s - kQBufs : 0; i < s; ++i)
             warp_wait(&sh.q_full[i % kQBufs], (i / kQBufs) & 1);
@@ -792,153 +796,190 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 // ------------------------------------------------------------------ output
 
 // out[r][h] = w_uv[h] o~[r][h], o~ the join of the row's splits (weights
-// 2^(m_s - max m)), rounded to bf16 for the MMA.  A CTA takes one head and
-// runs over chunks of 16 query rows; each of its v / 8 warps holds 8 of w_uv's
-// rows in registers (loaded before the wait for the attention).  The
-// contraction's order inside an MMA is free: a lane takes 8 adjacent l per 32,
-// one 16-byte load.  Latency-bound: a row's splits are read as soon as their
-// slots are known, with their maxima and sums; few rows share the warps.
+// 2^(m_s - max m)), rounded to bf16 for the MMA.  A CTA takes one head and up
+// to 64 query rows, as many as spread the rows over the SMs: its warps join
+// the rows' splits into the A operand (few rows share the warps), then one
+// product with the head's weights, in flight since before the wait for the
+// attention.  Latency-bound: a row's splits are read as soon as their slots are
+// known, with their maxima and sums.
+constexpr int kOutThreads = 512, kOutWarps = kOutThreads / 32;
+constexpr int kOutRows = 64;
 constexpr int kAtOnce = 2;  // splits of a row read together
 
-template <int kV>
-__global__ void __launch_bounds__(kV * 4)
-latent_out_kernel(const LatentAttnArgs a, int N, const __nv_bfloat16 *__restrict__ w_uv, __nv_bfloat16 *__restrict__ out) {
-    constexpr int kWarps = kV / 8;
-    constexpr int kMaxK = kLatentMaxDim / 32, kMaxQ = kLatentMaxDim / 128;
-    extern __shared__ float4 raw4[];
-    __shared__ float2 ms[kWarps];
-    const int L = a.L, R = a.B * a.q_len;
-    float *sums = reinterpret_cast<float *>(raw4);                 // [kWarps][L]
-    uint8_t *at = reinterpret_cast<uint8_t *>(sums + kWarps * L);  // [16] rows of L bf16 + 64 bytes
-    const int row_bytes = 2 * L + 64;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
-    const int h = blockIdx.y;
-    uint4 w[kMaxK];
-#pragma unroll
-    for (int k = 0; k < kMaxK; ++k)
-        if (32 * k < L)
-            w[k] = load_now(w_uv + (static_cast<size_t>(h) * kV + warp * 8 + g) * L + 32 * k + 8 * c);
+__global__ void __launch_bounds__(kOutThreads)
+latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnArgs a, int N, int rows_per_cta, int v_dim,
+                  __nv_bfloat16 *__restrict__ out) {
+    constexpr int kMaxQ = kLatentMaxDim / 128;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ float2 ms[kOutWarps];
+    __shared__ uint64_t full, acc;
+    __shared__ uint32_t tslot;
+    const int L = a.L, R = a.B * a.q_len, chunks = L / 64;
+    const uint32_t wb = smem_addr(raw), w_chunk = v_dim * 128;     // [chunks][v][64 l]
+    uint8_t *joined = raw + chunks * w_chunk;                      // [chunks][64 rows][64 l], 128-byte swizzle
+    float *sums = reinterpret_cast<float *>(joined + chunks * kOutRows * 128);  // [kOutWarps][L]
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+    const int h = blockIdx.y, r0 = blockIdx.x * rows_per_cta, rows = min(rows_per_cta, R - r0);
+    bool ok = true;
+    if (warp == 0) {
+        const uint32_t leader = elect_leader();
+        if (leader) {
+            mbar_init(smem_addr(&full), 1);
+            mbar_init(smem_addr(&acc), 1);
+            fence_mbar_init();
+        }
+        __syncwarp();
+        mbar_expect_tx_by(leader, smem_addr(&full), chunks * w_chunk);
+        for (int c = 0; c < chunks; ++c)
+            tma_load_2d_by(leader, wb + c * w_chunk, &map_uv, 64 * c, h * v_dim, smem_addr(&full));
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tslot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     pdl_wait_prerequisites();
     pdl_allow_dependents();
 
-    for (int r0 = blockIdx.x * 16; r0 < R; r0 += gridDim.x * 16) {
-        // ---- join: a row's splits are shared by `share` warps
-        const int rows = min(16, R - r0);
-        int share = kWarps;
-        while (share > 1 && kWarps / share < rows) share /= 2;
-        const int step = kWarps / share;
-        for (int rr = 0; rr < rows; rr += step) {
-            const int i = rr + warp / share, sub = warp % share;
-            if (i < rows) {
-                const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
-                const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
-                const int2 own = a.owner[bg];
-                const float2 *ml = a.ml + (static_cast<size_t>(own.x) + bg) * N + n;  // split s: ml[s * N]
-                const float *part = a.part + ((static_cast<size_t>(own.x) + bg) * N + n) * L + 4 * lane;
-                const size_t next = static_cast<size_t>(N) * L;
-                const int splits = own.y - own.x + 1;
-                float4 o[kMaxQ] = {};
-                float M = kNoScore, S = 0.0f;
-                for (int s0 = sub; s0 < splits; s0 += kAtOnce * share) {
-                    float4 x[kAtOnce][kMaxQ];
-                    float2 v[kAtOnce];
+    // ---- join: `share` warps split a row's splits
+    int share = kOutWarps;
+    while (share > 1 && kOutWarps / share < rows) share /= 2;
+    const int step = kOutWarps / share;
+    auto put = [&](int i, int l, uint32_t x) {  // two values of row i at dimensions l, l + 1
+        *reinterpret_cast<uint32_t *>(joined + (l / 64 * kOutRows + i) * 128 + (((l % 64 / 8) ^ (i & 7)) << 4) + l % 8 * 2) = x;
+    };
+    for (int rr = 0; rr < rows; rr += step) {
+        const int i = rr + warp / share, sub = warp % share;
+        if (i < rows) {
+            const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
+            const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
+            const int2 own = a.owner[bg];
+            const float2 *ml = a.ml + (static_cast<size_t>(own.x) + bg) * N + n;  // split s: ml[s * N]
+            const float *part = a.part + ((static_cast<size_t>(own.x) + bg) * N + n) * L + 4 * lane;
+            const size_t next = static_cast<size_t>(N) * L;
+            const int splits = own.y - own.x + 1;
+            float4 o[kMaxQ] = {};
+            float M = kNoScore, S = 0.0f;
+            for (int s0 = sub; s0 < splits; s0 += kAtOnce * share) {
+                float4 x[kAtOnce][kMaxQ];
+                float2 v[kAtOnce];
 #pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u) {
-                        const int s = s0 + u * share;
-                        v[u] = make_float2(kNoScore, 0.0f);
-                        if (s < splits) {
-                            v[u] = ml[static_cast<size_t>(s) * N];
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const int s = s0 + u * share;
+                    v[u] = make_float2(kNoScore, 0.0f);
+                    if (s < splits) {
+                        v[u] = ml[static_cast<size_t>(s) * N];
 #pragma unroll
-                            for (int k = 0; k < kMaxQ; ++k)
-                                if (128 * k + 4 * lane < L)
-                                    x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * next + 128 * k));
-                        }
+                        for (int k = 0; k < kMaxQ; ++k)
+                            if (128 * k + 4 * lane < L)
+                                x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * next + 128 * k));
                     }
-                    float top = M;
+                }
+                float top = M;
 #pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, v[u].x);
-                    const float f0 = hw_ex2(M - top);
-                    M = top;
-                    S *= f0;
+                for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, v[u].x);
+                const float f0 = hw_ex2(M - top);
+                M = top;
+                S *= f0;
 #pragma unroll
-                    for (int k = 0; k < kMaxQ; ++k) {
-                        o[k].x *= f0;
-                        o[k].y *= f0;
-                        o[k].z *= f0;
-                        o[k].w *= f0;
+                for (int k = 0; k < kMaxQ; ++k) {
+                    o[k].x *= f0;
+                    o[k].y *= f0;
+                    o[k].z *= f0;
+                    o[k].w *= f0;
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u)
+                    if (s0 + u * share < splits) {
+                        const float f = hw_ex2(v[u].x - top);
+                        S = fmaf(f, v[u].y, S);
+#pragma unroll
+                        for (int k = 0; k < kMaxQ; ++k)
+                            if (128 * k + 4 * lane < L) {
+                                o[k].x = fmaf(f, x[u][k].x, o[k].x);
+                                o[k].y = fmaf(f, x[u][k].y, o[k].y);
+                                o[k].z = fmaf(f, x[u][k].z, o[k].z);
+                                o[k].w = fmaf(f, x[u][k].w, o[k].w);
+                            }
                     }
-#pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u)
-                        if (s0 + u * share < splits) {
-                            const float f = hw_ex2(v[u].x - top);
-                            S = fmaf(f, v[u].y, S);
-#pragma unroll
-                            for (int k = 0; k < kMaxQ; ++k)
-                                if (128 * k + 4 * lane < L) {
-                                    o[k].x = fmaf(f, x[u][k].x, o[k].x);
-                                    o[k].y = fmaf(f, x[u][k].y, o[k].y);
-                                    o[k].z = fmaf(f, x[u][k].z, o[k].z);
-                                    o[k].w = fmaf(f, x[u][k].w, o[k].w);
-                                }
-                        }
-                }
-                if (share == 1) {
-                    const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
-#pragma unroll
-                    for (int k = 0; k < kMaxQ; ++k)
-                        if (128 * k + 4 * lane < L)
-                            *reinterpret_cast<uint2 *>(at + i * row_bytes + 256 * k + 8 * lane) =
-                                make_uint2(pack_bf16(o[k].x * inv, o[k].y * inv), pack_bf16(o[k].z * inv, o[k].w * inv));
-                } else {
-                    if (lane == 0) ms[warp] = make_float2(M, S);
-#pragma unroll
-                    for (int k = 0; k < kMaxQ; ++k)
-                        if (128 * k + 4 * lane < L) reinterpret_cast<float4 *>(sums + warp * L)[32 * k + lane] = o[k];
-                }
             }
-            if (share > 1) {
-                __syncthreads();
-                for (int e = threadIdx.x; e < step * (L / 2); e += blockDim.x) {
-                    const int which = e / (L / 2), l2 = e - which * (L / 2), i2 = rr + which;
-                    if (i2 < rows) {
-                        float M = kNoScore, S = 0.0f, x = 0.0f, y = 0.0f;
-                        for (int s = 0; s < share; ++s) M = fmaxf(M, ms[which * share + s].x);
-                        for (int s = 0; s < share; ++s) {
-                            const float2 v = reinterpret_cast<const float2 *>(sums + (which * share + s) * L)[l2];
-                            const float f = hw_ex2(ms[which * share + s].x - M);
-                            S = fmaf(f, ms[which * share + s].y, S);
-                            x = fmaf(f, v.x, x);
-                            y = fmaf(f, v.y, y);
-                        }
-                        const float inv = S == 0.0f ? 0.0f : 1.0f / S;
-                        *reinterpret_cast<uint32_t *>(at + i2 * row_bytes + 4 * l2) = pack_bf16(x * inv, y * inv);
+            if (share == 1) {
+                const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
+#pragma unroll
+                for (int k = 0; k < kMaxQ; ++k)
+                    if (128 * k + 4 * lane < L) {
+                        put(i, 128 * k + 4 * lane, pack_bf16(o[k].x * inv, o[k].y * inv));
+                        put(i, 128 * k + 4 * lane + 2, pack_bf16(o[k].z * inv, o[k].w * inv));
                     }
-                }
-                if (rr + step < rows) __syncthreads();
+            } else {
+                if (lane == 0) ms[warp] = make_float2(M, S);
+#pragma unroll
+                for (int k = 0; k < kMaxQ; ++k)
+                    if (128 * k + 4 * lane < L) reinterpret_cast<float4 *>(sums + warp * L)[32 * k + lane] = o[k];
             }
         }
-        __syncthreads();
-        float acc[4][4] = {};
-#pragma unroll
-        for (int k = 0; k < kMaxK; ++k)
-            if (32 * k < L) {
-                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                if (g < rows) lo = *reinterpret_cast<const uint4 *>(at + g * row_bytes + 64 * k + 16 * c);
-                if (g + 8 < rows) hi = *reinterpret_cast<const uint4 *>(at + (g + 8) * row_bytes + 64 * k + 16 * c);
-                const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-                mma16816(acc[k % 2 * 2], a0, w[k].x, w[k].y);
-                mma16816(acc[k % 2 * 2 + 1], a1, w[k].z, w[k].w);
+        if (share > 1) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < step * (L / 2); e += kOutThreads) {
+                const int which = e / (L / 2), l2 = e - which * (L / 2), i2 = rr + which;
+                if (i2 < rows) {
+                    float M = kNoScore, S = 0.0f, x = 0.0f, y = 0.0f;
+                    for (int s = 0; s < share; ++s) M = fmaxf(M, ms[which * share + s].x);
+                    for (int s = 0; s < share; ++s) {
+                        const float2 v = reinterpret_cast<const float2 *>(sums + (which * share + s) * L)[l2];
+                        const float f = hw_ex2(ms[which * share + s].x - M);
+                        S = fmaf(f, ms[which * share + s].y, S);
+                        x = fmaf(f, v.x, x);
+                        y = fmaf(f, v.y, y);
+                    }
+                    const float inv = S == 0.0f ? 0.0f : 1.0f / S;
+                    put(i2, 2 * l2, pack_bf16(x * inv, y * inv));
+                }
             }
+            if (rr + step < rows) __syncthreads();
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uniform(tslot);
+    if (warp == 0) {
+        const uint32_t leader = elect_leader();
+        ok = warp_wait(&full, 0);
+        tc_fence_after();
+        const uint32_t idesc = v_dim == 128 ? mma_idesc(kOutRows, 128) : mma_idesc(kOutRows, 64);
+        const uint32_t ab = wb + chunks * w_chunk;
+        for (int k = 0; k < L / 16; ++k)
+            mma_bf16_by(leader, tmem, sw128_desc(ab + k / 4 * (kOutRows * 128) + k % 4 * 32),
+                        sw128_desc(wb + k / 4 * w_chunk + k % 4 * 32), idesc, k != 0);
+        mma_commit_by(leader, smem_addr(&acc));
+    }
+    if (warp < 4) {
+        if (!warp_wait(&acc, 0)) ok = false;
+        tc_fence_after();
+        // a 64-row accumulator: row 16 w + i in lane 32 w + i, i < 16
+        const int i = warp * 16 + lane;
+        const bool mine = ok && lane < 16 && i < rows;
+        uint4 *dst = reinterpret_cast<uint4 *>(out + (static_cast<size_t>(r0 + i) * a.Hq + h) * v_dim);
+        if (warp * 16 < rows)
+            for (int c = 0; c < v_dim; c += 32) {
+                uint32_t x[32];
+                tmem_ld32_nowait(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, x);
+                tmem_wait_ld();
+                const float *f = reinterpret_cast<const float *>(x);
+                if (mine)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[0][i] = (acc[0][i] + acc[1][i]) + (acc[2][i] + acc[3][i]);
-        const int col = warp * 8 + 2 * c;
-        if (g < rows)
-            *reinterpret_cast<uint32_t *>(out + (static_cast<size_t>(r0 + g) * a.Hq + h) * kV + col) =
-                pack_bf16(acc[0][0], acc[0][1]);
-        if (g + 8 < rows)
-            *reinterpret_cast<uint32_t *>(out + (static_cast<size_t>(r0 + g + 8) * a.Hq + h) * kV + col) =
-                pack_bf16(acc[0][2], acc[0][3]);
-        __syncthreads();
+                    for (int j = 0; j < 4; ++j)
+                        dst[c / 8 + j] = make_uint4(pack_bf16(f[8 * j], f[8 * j + 1]), pack_bf16(f[8 * j + 2], f[8 * j + 3]),
+                                                    pack_bf16(f[8 * j + 4], f[8 * j + 5]),
+                                                    pack_bf16(f[8 * j + 6], f[8 * j + 7]));
+            }
+    }
+    if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -953,7 +994,8 @@ bool decode_shape_ok(int B, int q_len, int Hq, int L, int nope, int v, int max_c
 constexpr int kSmemLimit = 232448;
 
 template <int N>
-int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, LatentAttnArgs a, int P, cudaStream_t stream) {
+int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, const CUtensorMap &qr, LatentAttnArgs a, int P,
+                     cudaStream_t stream) {
     // shared memory: q~, P, the rope slots, and latent pairs to the brim
     const int chunks = a.L / 64;
     a.ropes = N <= 32 ? 3 : 2;
@@ -963,7 +1005,7 @@ int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, LatentAttnArgs
     if (a.pairs < 2 * ((a.L + 127) / 128)) return TTS_ERR_UNSUPPORTED;  // (S^T goes one tile ahead of O^T)
     const int smem = fixed + a.pairs * kPairBytes;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_attn_kernel<N>), smem)) return TTS_ERR_CUDA;
-    return launch_kernel(latent_attn_kernel<N>, dim3(P), dim3(kAttnThreads), smem, {stream, true}, kv, q, a);
+    return launch_kernel(latent_attn_kernel<N>, dim3(P), dim3(kAttnThreads), smem, {stream, true}, kv, q, qr, a);
 }
 
 }  // namespace
@@ -997,9 +1039,8 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     if (pl.units > 0x40000000L) return TTS_ERR_UNSUPPORTED;  // units are 32-bit
     if (!d_ws || !aligned16(d_ws) || ws_bytes < pl.total()) return TTS_ERR_WORKSPACE;
 
-    using bf = const __nv_bfloat16 *;
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
-    __nv_bfloat16 *qt = reinterpret_cast<__nv_bfloat16 *>(ws);
+    void *qt = ws;  // q~ [R][Hq][L]
     LatentAttnArgs a{};
     a.table = d_block_table;
     a.max_blocks = max_blocks_per_seq;
@@ -1017,35 +1058,38 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     a.ml = reinterpret_cast<float2 *>(ws + pl.qt_bytes + pl.part_bytes);
     a.owner = reinterpret_cast<int2 *>(ws + pl.qt_bytes + pl.part_bytes + pl.ml_bytes);
     a.err = d_err;
-    const int R = B * q_len, W = L + kLatentRope;
-    CUtensorMap map_kv, map_q;
-    if (!make_tma_2d_bf16(&map_kv, cache->pool, static_cast<uint64_t>(cache->num_blocks) * TTS_BLOCK_TOKENS, W,
-                          TTS_BLOCK_TOKENS, 64) ||
-        !make_tma_2d_bf16(&map_q, qt, static_cast<uint64_t>(R) * num_q_heads, W, pl.N, 64))
+    const int R = B * q_len, Hq = num_q_heads;
+    const uint64_t qrows = static_cast<uint64_t>(R) * Hq;
+    CUtensorMap map_kv, map_q, map_qr, map_qn, map_uk, map_qt, map_uv;
+    if (!make_tma_2d_bf16(&map_kv, cache->pool, static_cast<uint64_t>(cache->num_blocks) * TTS_BLOCK_TOKENS,
+                          L + kLatentRope, TTS_BLOCK_TOKENS, 64) ||
+        !make_tma_2d_bf16(&map_q, qt, qrows, L, pl.N, 64) ||
+        !make_tma_2d_bf16(&map_qr, d_q_rope, qrows, kLatentRope, pl.N, 64) ||
+        !make_tma_2d_bf16(&map_qn, d_q_nope, R, static_cast<uint64_t>(Hq) * nope_dim, kRowTile, 64) ||
+        !make_tma_2d_bf16(&map_uk, d_w_uk, static_cast<uint64_t>(Hq) * nope_dim, L, nope_dim, 64) ||
+        !make_tma_2d_bf16(&map_qt, qt, R, static_cast<uint64_t>(Hq) * L, kRowTile, 64) ||
+        !make_tma_2d_bf16(&map_uv, d_w_uv, static_cast<uint64_t>(Hq) * v_dim, L, v_dim, 64))
         return TTS_ERR_CUDA;
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    // a warp per 16 query rows, up to 4 a CTA; more rows repeat over the
-    // weights in registers once every SM has two CTAs
-    const int chunks16 = (R + 15) / 16, aw = chunks16 < kAbsorbWarps ? chunks16 : kAbsorbWarps;
-    const int slices = L / 64 * num_q_heads, az = (2 * kCtas + slices - 1) / slices, am = (chunks16 + aw - 1) / aw;
-    int rc = launch_kernel(nope_dim == 128 ? latent_absorb_kernel<128> : latent_absorb_kernel<64>,
-                           dim3(L / 64, num_q_heads, am < az ? am : az), dim3(32 * aw), 0, {cs, thread_pdl()},
-                           static_cast<bf>(d_q_nope), static_cast<bf>(d_q_rope), static_cast<bf>(d_w_uk), qt, R,
-                           num_q_heads, L);
+    const int absorb_smem = 2 * nope_dim * 128 + nope_dim / 64 * kRowTile * 128;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_absorb_kernel), absorb_smem)) return TTS_ERR_CUDA;
+    int rc = launch_kernel(latent_absorb_kernel, dim3((L + 127) / 128, Hq, (R + kRowTile - 1) / kRowTile), dim3(128),
+                           absorb_smem, {cs, thread_pdl()}, map_qn, map_uk, map_qt, static_cast<int>(nope_dim), L, R,
+                           d_err);
     if (rc != TTS_OK) return rc;
     switch (pl.N) {
-        case 16: rc = launch_attention<16>(map_kv, map_q, a, pl.P, cs); break;
-        case 32: rc = launch_attention<32>(map_kv, map_q, a, pl.P, cs); break;
-        case 48: rc = launch_attention<48>(map_kv, map_q, a, pl.P, cs); break;
-        default: rc = launch_attention<64>(map_kv, map_q, a, pl.P, cs); break;
+        case 16: rc = launch_attention<16>(map_kv, map_q, map_qr, a, pl.P, cs); break;
+        case 32: rc = launch_attention<32>(map_kv, map_q, map_qr, a, pl.P, cs); break;
+        case 48: rc = launch_attention<48>(map_kv, map_q, map_qr, a, pl.P, cs); break;
+        default: rc = launch_attention<64>(map_kv, map_q, map_qr, a, pl.P, cs); break;
     }
     if (rc != TTS_OK) return rc;
-    const int smem = (v_dim / 8) * L * 4 + 16 * (2 * L + 64);
-    auto out_kernel = v_dim == 128 ? latent_out_kernel<128> : latent_out_kernel<64>;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(out_kernel), smem)) return TTS_ERR_CUDA;
-    // one CTA fits an SM: rows beyond one wave repeat over the weights in registers
-    const int wave = (kCtas + num_q_heads - 1) / num_q_heads;
-    return launch_kernel(out_kernel, dim3(chunks16 < wave ? chunks16 : wave, num_q_heads), dim3(v_dim * 4), smem,
-                         {cs, true}, a, pl.N, static_cast<bf>(d_w_uv), static_cast<__nv_bfloat16 *>(d_out));
+    // rows a CTA: enough CTAs for the SMs, in eights
+    const int share = (static_cast<int>((static_cast<long>(R) * Hq + kCtas - 1) / kCtas) + 7) / 8 * 8;
+    const int per = share < kOutRows ? share : kOutRows;
+    const int out_smem = L / 64 * (v_dim + kOutRows) * 128 + kOutWarps * L * 4;
+    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_out_kernel), out_smem)) return TTS_ERR_CUDA;
+    return launch_kernel(latent_out_kernel, dim3((R + per - 1) / per, Hq), dim3(kOutThreads), out_smem, {cs, true}, map_uv,
+                         a, pl.N, per, static_cast<int>(v_dim), static_cast<__nv_bfloat16 *>(d_out));
 }
