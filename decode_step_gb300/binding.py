@@ -210,18 +210,37 @@ class LatentCache:
             raise ValueError(f"the pool's rows hold {pool.shape[2]} values, latent_dim + 64 = {latent_dim + 64}")
         self.pool, self.latent_dim = pool, latent_dim
         self.desc = _lib.LatentCacheDesc(pool.shape[0], 16, latent_dim, self.ROPE_DIM, TTS_BF16, _dev(pool, "pool"))
+        self._ref = ctypes.byref(self.desc)
 
     @property
     def num_blocks(self) -> int:
         return self.desc.num_blocks
 
+    def on(self, device: int):
+        """The descriptor for a call on `device`."""
+        if self.pool.get_device() != device:
+            raise ValueError(f"the latent pool is on {self.pool.device}, the current device is cuda:{device}")
+        return self._ref
 
-def _one_device(**tensors):
-    """Every tensor on the current device (whose stream the call is queued on)."""
-    cur = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != cur:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{cur}")
+
+def _on(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
+    """Address of a contiguous tensor on `device` (the current one, whose stream
+    the call is queued on) with this dtype and shape (None: any)."""
+    if t.get_device() != device:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def tts_latent_append(cache: LatentCache, block_table, ctx_before, c_new, kr_new, q_rope=None, q_rope_out=None,
@@ -234,19 +253,15 @@ def tts_latent_append(cache: LatentCache, block_table, ctx_before, c_new, kr_new
     if q_rope is None and q_rope_out is not None:
         raise ValueError("q_rope_out without q_rope")
     Hq = 0 if q_rope is None else q_rope.shape[1]
-    q_rope_out = q_rope if q_rope_out is None else q_rope_out
-    bf = torch.bfloat16
-    args = (ctypes.byref(cache.desc), _dev(block_table, "block_table", torch.int32), max_blocks,
-            _dev(ctx_before, "ctx_before", torch.int32, (B,)), B,
-            None if row_start is None else _dev(row_start, "row_start", torch.int32, (B + 1,)), T, Hq,
-            float(rope_base), _dev(c_new, "c_new", bf, (T, cache.latent_dim)),
-            _dev(kr_new, "kr_new", bf, (T, cache.ROPE_DIM)),
-            None if q_rope is None else _dev(q_rope, "q_rope", bf, (T, Hq, cache.ROPE_DIM)),
-            None if q_rope is None else _dev(q_rope_out, "q_rope_out", bf, (T, Hq, cache.ROPE_DIM)),
-            None if err is None else _dev(err, "err", torch.int32), _stream(stream))
-    _one_device(pool=cache.pool, block_table=block_table, ctx_before=ctx_before, row_start=row_start, c_new=c_new,
-                kr_new=kr_new, q_rope=q_rope, q_rope_out=q_rope_out, err=err)
-    check("tts_latent_append", lib().tts_latent_append(*args))
+    bf, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
+    q = None if q_rope is None else _on(q_rope, "q_rope", bf, (T, Hq, 64), dev)
+    check("tts_latent_append", lib().tts_latent_append(
+        cache.on(dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_before, "ctx_before", i32, (B,), dev), B,
+        None if row_start is None else _on(row_start, "row_start", i32, (B + 1,), dev), T, Hq, rope_base,
+        _on(c_new, "c_new", bf, (T, cache.latent_dim), dev), _on(kr_new, "kr_new", bf, (T, 64), dev), q,
+        q if q_rope_out is None else _on(q_rope_out, "q_rope_out", bf, (T, Hq, 64), dev),
+        None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
 
 
 def tts_latent_decode_attn_workspace_size(B, q_len, num_q_heads, latent_dim, nope_dim, v_dim, max_ctx_len) -> int:
@@ -261,17 +276,15 @@ def tts_latent_decode_attn(cache: LatentCache, block_table, ctx_lens, max_ctx_le
     out [B][q_len][Hq][v_dim], all bf16."""
     B, max_blocks = block_table.shape
     _, q_len, Hq, nope = q_nope.shape
-    v = out.shape[-1]
-    bf, L = torch.bfloat16, cache.latent_dim
-    args = (ctypes.byref(cache.desc), _dev(block_table, "block_table", torch.int32), max_blocks,
-            _dev(ctx_lens, "ctx_lens", torch.int32, (B,)), int(max_ctx_len), B, q_len, Hq, nope, v, float(scale),
-            int(bool(causal)), _dev(q_nope, "q_nope", bf, (B, q_len, Hq, nope)),
-            _dev(q_rope, "q_rope", bf, (B, q_len, Hq, cache.ROPE_DIM)), _dev(w_uk, "w_uk", bf, (Hq, nope, L)),
-            _dev(w_uv, "w_uv", bf, (Hq, v, L)), _dev(out, "out", bf, (B, q_len, Hq, v)), _dev(ws, "ws"),
-            ws.numel() * ws.element_size(), None if err is None else _dev(err, "err", torch.int32), _stream(stream))
-    _one_device(pool=cache.pool, block_table=block_table, ctx_lens=ctx_lens, q_nope=q_nope, q_rope=q_rope, w_uk=w_uk,
-                w_uv=w_uv, out=out, ws=ws, err=err)
-    check("tts_latent_decode_attn", lib().tts_latent_decode_attn(*args))
+    v, L = out.shape[-1], cache.latent_dim
+    bf, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
+    check("tts_latent_decode_attn", lib().tts_latent_decode_attn(
+        cache.on(dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_lens, "ctx_lens", i32, (B,), dev), max_ctx_len, B, q_len, Hq, nope, v, scale, 1 if causal else 0,
+        _on(q_nope, "q_nope", bf, (B, q_len, Hq, nope), dev), _on(q_rope, "q_rope", bf, (B, q_len, Hq, 64), dev),
+        _on(w_uk, "w_uk", bf, (Hq, nope, L), dev), _on(w_uv, "w_uv", bf, (Hq, v, L), dev),
+        _on(out, "out", bf, (B, q_len, Hq, v), dev), _on(ws, "ws", None, None, dev), ws.nbytes,
+        None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
 
 
 def tts_latent_prefill_attn_workspace_size(B, num_rows, num_q_heads, latent_dim, nope_dim, v_dim,
@@ -287,18 +300,15 @@ def tts_latent_prefill_attn(cache: LatentCache, block_table, ctx_lens, max_total
     max_total_ctx bounds the sum of ctx_lens."""
     B, max_blocks = block_table.shape
     T, Hq, nope = q_nope.shape
-    v = out.shape[-1]
-    bf, L = torch.bfloat16, cache.latent_dim
-    args = (ctypes.byref(cache.desc), _dev(block_table, "block_table", torch.int32), max_blocks,
-            _dev(ctx_lens, "ctx_lens", torch.int32, (B,)), int(max_total_ctx), B,
-            _dev(row_start, "row_start", torch.int32, (B + 1,)), T, Hq, nope, v, float(scale),
-            _dev(q_nope, "q_nope", bf, (T, Hq, nope)), _dev(q_rope, "q_rope", bf, (T, Hq, cache.ROPE_DIM)),
-            _dev(w_uk, "w_uk", bf, (Hq, nope, L)), _dev(w_uv, "w_uv", bf, (Hq, v, L)),
-            _dev(out, "out", bf, (T, Hq, v)), _dev(ws, "ws"), ws.numel() * ws.element_size(),
-            None if err is None else _dev(err, "err", torch.int32), _stream(stream))
-    _one_device(pool=cache.pool, block_table=block_table, ctx_lens=ctx_lens, row_start=row_start, q_nope=q_nope,
-                q_rope=q_rope, w_uk=w_uk, w_uv=w_uv, out=out, ws=ws, err=err)
-    check("tts_latent_prefill_attn", lib().tts_latent_prefill_attn(*args))
+    v, L = out.shape[-1], cache.latent_dim
+    bf, i32, dev = torch.bfloat16, torch.int32, torch.cuda.current_device()
+    check("tts_latent_prefill_attn", lib().tts_latent_prefill_attn(
+        cache.on(dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_lens, "ctx_lens", i32, (B,), dev), max_total_ctx, B, _on(row_start, "row_start", i32, (B + 1,), dev),
+        T, Hq, nope, v, scale, _on(q_nope, "q_nope", bf, (T, Hq, nope), dev), _on(q_rope, "q_rope", bf, (T, Hq, 64), dev),
+        _on(w_uk, "w_uk", bf, (Hq, nope, L), dev), _on(w_uv, "w_uv", bf, (Hq, v, L), dev),
+        _on(out, "out", bf, (T, Hq, v), dev), _on(ws, "ws", None, None, dev), ws.nbytes,
+        None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
 
 
 def tts_head_workspace_size(R, V) -> int:
