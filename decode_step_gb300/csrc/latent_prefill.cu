@@ -3,15 +3,14 @@
 // then ordinary causal attention.  Per (row, token, head) that costs
 // 2 (nope + 64 + v) flop where the absorbed form costs 2 (2 latent_dim + 64):
 // 640 against 2176 at 128, 128 and 512, for 2 latent_dim (nope + v) more per
-// (token, head).  Three kernels, each a programmatic dependent of the one
-// before:
+// (token, head).  Two kernels, the second a programmatic dependent of the
+// first:
 //
-//  1. latent_plan_kernel (one CTA): checks the streams, lays out their tokens
-//     in the workspace (each stream from a 128-token boundary) and their query
-//     tiles.
-//  2. latent_expand_kernel: a tcgen05 GEMM per 128 tokens x 128 features,
-//     latents fetched through the block table.
-//  3. latent_prefill_kernel: attention of 256 rows of one head per CTA (two
+//  1. latent_expand_kernel: checks the streams, lays out their tokens in the
+//     workspace (each stream from a 128-token boundary) and their query tiles,
+//     and multiplies keys and values out: a tcgen05 GEMM whose token rows are
+//     fetched through the block table.
+//  2. latent_prefill_kernel: attention of 256 rows of one head per CTA (two
 //     128-row tiles that take turns on the tensor core: while one's weights
 //     are computed, the other's products run).  S and O are in tensor memory;
 //     the weights go back into S's columns as bf16 and are the A operand of
@@ -57,262 +56,378 @@ struct PrefillArgs {
     int32_t *err;
 };
 
-// -------------------------------------------------------------------- plan
-
-constexpr int kPlanThreads = 256;
-
-__global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(const PrefillArgs a) {
-    __shared__ long long sums[3][kPlanThreads / 32];
-    pdl_wait_prerequisites();
-    pdl_allow_dependents();
-    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
-    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-    // rows and context of stream b; false: its rows or its length are out of range
-    auto stream = [&](int b, int *n, int *ctx) {
-        const int first = a.row_start[b], end = a.row_start[b + 1];
-        *ctx = a.ctx_lens[b];
-        *n = 0;
-        if (first == end) return true;
-        if (first < 0 || end < first || end > a.num_rows) return false;
-        *n = end - first;
-        if (*ctx < *n || *ctx > a.max_blocks * TTS_BLOCK_TOKENS) {
-            *n = 0;
-            return false;
-        }
-        return true;
-    };
-    auto zero_rows = [&](int b) {
-        const int first = max(0, a.row_start[b]), end = min(a.num_rows, a.row_start[b + 1]);
-        flag_error(a.err, TTS_ERRBIT_CTX_LEN);
-        uint4 *o = reinterpret_cast<uint4 *>(a.out);
-        const size_t w = static_cast<size_t>(a.Hq) * a.v / 8;
-        for (size_t i = first * w; first < end && i < end * w; ++i) o[i] = make_uint4(0, 0, 0, 0);
-    };
-    // exclusive scans over the streams: contexts (against max_total), then tiles
-    auto scan = [&](long long mine, int which) {
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
-            const long long x = __shfl_up_sync(kFull, incl, o);
-            if (lane >= o) incl += x;
-        }
-        if (lane == 31) sums[which][warp] = incl;
-        __syncthreads();
-        long long at = incl - mine;
-        for (int w = 0; w < warp; ++w) at += sums[which][w];
-        return at;
-    };
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        int n, ctx;
-        if (stream(b, &n, &ctx) && n) mine += ctx;
-    }
-    long long ctx_at = scan(mine, 0);
-    const long long ctx_first = ctx_at;
-    long long tiles = 0, qtiles = 0;
-    for (int b = b0; b < b1; ++b) {
-        int n, ctx;
-        if (stream(b, &n, &ctx) && n) {
-            ctx_at += ctx;
-            if (ctx_at <= a.max_total) {
-                tiles += (ctx + kTile - 1) / kTile;
-                qtiles += (n + kRows - 1) / kRows;
-            }
-        }
-    }
-    long long t_at = scan(tiles, 1), q_at = scan(qtiles, 2);
-    ctx_at = ctx_first;
-    for (int b = b0; b < b1; ++b) {
-        int n, ctx;
-        const bool good = stream(b, &n, &ctx);
-        bool taken = good;
-        a.tile_start[b] = static_cast<int>(t_at);
-        a.qtile_start[b] = static_cast<int>(q_at);
-        if (good && n) {
-            ctx_at += ctx;
-            taken = ctx_at <= a.max_total;
-            if (taken) {
-                t_at += (ctx + kTile - 1) / kTile;
-                q_at += (n + kRows - 1) / kRows;
-            }
-        }
-        if (!taken) zero_rows(b);
-    }
-    if (b0 < b1 && b1 == a.B) {
-        a.tile_start[a.B] = static_cast<int>(t_at);
-        a.qtile_start[a.B] = static_cast<int>(q_at);
-    }
-}
-
 // ------------------------------------------------------------------ expand
 
-// K[t][h nope + d] = w_uk[h][d] . c_t and V likewise, bf16.  One CTA per 128
-// tokens x 128 features (two fit an SM, so one's epilogue runs beside the
-// other's products): A = latents through the block table, B = weights, both
-// K-major; the accumulator leaves through shared memory as bf16 by TMA.
-// The first feature tile's CTA also copies the tokens' rotated key parts and
-// records which blocks are in the pool.
-constexpr int kExpandStages = 3;
-constexpr int kExpandThreads = 192;
-constexpr int kExpandSmem = 1024 + kExpandStages * 2 * kChunkBytes;
+// K[t][h nope + d] = w_uk[h][d] . c_t and V likewise, bf16: a GEMM of 128-token
+// x 256-feature units.  Persistent, one CTA per SM, in clusters of two that
+// take neighbouring token tiles and the same features: each CTA fetches half of
+// a weight chunk for both (multicast), so a unit reads 256 KB from L2 for
+// 33 Mflop; 128 x 128 units that fetched both operands for themselves were
+// bound by those reads (10 TB/s of L2 to the SMs, 56 us at 8891 tokens x 4096
+// features x 512), and weights kept in shared memory left too short a ring
+// (90 us).  The accumulator is double buffered: one unit's results leave (as
+// bf16, through shared memory, by TMA) while the next one's products run.
+// Every CTA scans the streams by itself; CTA 0 writes the plan that the
+// attention reads.  The first feature unit of a token tile also copies the
+// tokens' rotated key parts and records which blocks are in the pool.
+constexpr int kExpandThreads = 224;        // 4 epilogue warps, producer, MMA issuer, spare (tensor memory)
+constexpr int kExpandSlots = 4;
+constexpr int kExpandCtas = 152;
+constexpr int kFeatures = 256;
+constexpr int kSlotBytes = 3 * kChunkBytes;    // 128 token rows, 256 feature rows of 64 values
+constexpr int kExpandSmem = kExpandSlots * kSlotBytes + 2 * kChunkBytes;
 
 struct ExpandShared {
-    uint64_t full[kExpandStages], empty[kExpandStages], acc;
+    uint64_t full[kExpandSlots], empty[kExpandSlots], acc_full[2], acc_empty[2], fin;
     uint32_t tmem;
+    long long sums[kExpandThreads / 32];
+    int tiles[kExpandThreads / 32], qtiles[kExpandThreads / 32];
+    int limit;             // streams from here on exceed max_total
+    int start_b, start_i;  // stream and tile of the first unit
 };
 
-__global__ void __launch_bounds__(kExpandThreads)
+// Rows and context of stream b; false: out of range.
+__device__ __forceinline__ bool prefill_stream(const PrefillArgs &a, int b, int *n, int *ctx) {
+    const int first = __ldg(a.row_start + b), end = __ldg(a.row_start + b + 1);
+    *ctx = __ldg(a.ctx_lens + b);
+    *n = 0;
+    if (first == end) return true;
+    if (first < 0 || end < first || end > a.num_rows) return false;
+    if (*ctx < end - first || *ctx > a.max_blocks * TTS_BLOCK_TOKENS) return false;
+    *n = end - first;
+    return true;
+}
+__device__ __forceinline__ int token_tiles(int ctx) { return (ctx + kTile - 1) / kTile; }
+
+// Walks the units of a CTA (every feature tile of a token tile, then the token
+// tile two on); every warp keeps its own copy.
+struct ExpandWalk {
+    int left, f, t;               // units left; feature tile, token tile
+    int feature_tiles, tiles;
+    int b, i, n, limit;           // stream of the token tile, its tile in the stream, the stream's tiles
+    int ctx;
+    __device__ __forceinline__ bool exists() const { return t < tiles; }  // (the last pair may lack its second)
+    __device__ __forceinline__ void seek(const PrefillArgs &a) {          // b: the next stream that has tiles
+        for (; b < limit; ++b) {
+            int rows, c;
+            const bool good = prefill_stream(a, b, &rows, &c);
+            n = uniform(good && rows ? token_tiles(c) : 0);
+            ctx = uniform(c);
+            if (n) return;
+        }
+    }
+    __device__ __forceinline__ void advance(const PrefillArgs &a) {
+        --left;
+        if (++f < feature_tiles) return;
+        f = 0;
+        for (int k = 0; k < 2; ++k)
+            if (++t < tiles && ++i == n) {
+                i = 0;
+                ++b;
+                seek(a);
+            }
+    }
+};
+
+__global__ void __launch_bounds__(kExpandThreads, 1)
 latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_constant__ CUtensorMap map_uk,
                      const __grid_constant__ CUtensorMap map_uv, const __grid_constant__ CUtensorMap map_k,
-                     const __grid_constant__ CUtensorMap map_v, const PrefillArgs a, int k_tiles) {
-    extern __shared__ uint8_t raw[];
+                     const __grid_constant__ CUtensorMap map_v, const PrefillArgs a, int k_tiles, int v_tiles) {
+    extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ ExpandShared sh;
-    const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+    const uint32_t ring = smem_addr(raw), stage = ring + kExpandSlots * kSlotBytes;
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int chunks = a.L / 64;
+    const uint32_t rank = blockIdx.x & 1;
     if (warp == 5 && lane == 0) {
-        for (int i = 0; i < kExpandStages; ++i) {
+        for (int i = 0; i < kExpandSlots; ++i) {
             mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), 2);  // the MMAs of both CTAs
         }
-        mbar_init(smem_addr(&sh.acc), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.acc_full[i]), 1);
+            mbar_init(smem_addr(&sh.acc_empty[i]), 4);
+        }
+        mbar_init(smem_addr(&sh.fin), 1);
+        sh.limit = a.B;
         fence_mbar_init();
     }
-    if (warp == 4) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&sh.tmem))
+    if (warp == 6) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait_prerequisites();
+    pdl_allow_dependents();
+    // ---- the streams' token and query tiles
+    const int per = (a.B + kExpandThreads - 1) / kExpandThreads;
+    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    int n, ctx;
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b)
+        if (prefill_stream(a, b, &n, &ctx) && n) mine += ctx;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) sh.sums[warp] = incl;
+    __syncthreads();
+    long long at = incl - mine;
+    for (int w = 0; w < warp; ++w) at += sh.sums[w];
+    for (int b = b0; b < b1 && at <= a.max_total; ++b)
+        if (prefill_stream(a, b, &n, &ctx) && n) {
+            at += ctx;
+            if (at > a.max_total) atomicMin(&sh.limit, b);
+        }
+    __syncthreads();
+    const int limit = sh.limit;
+    int t_mine = 0, q_mine = 0;
+    for (int b = b0; b < min(b1, limit); ++b)
+        if (prefill_stream(a, b, &n, &ctx) && n) {
+            t_mine += token_tiles(ctx);
+            q_mine += (n + kRows - 1) / kRows;
+        }
+    int t_incl = t_mine, q_incl = q_mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(kFull, t_incl, o), y = __shfl_up_sync(kFull, q_incl, o);
+        if (lane >= o) {
+            t_incl += x;
+            q_incl += y;
+        }
+    }
+    if (lane == 31) {
+        sh.tiles[warp] = t_incl;
+        sh.qtiles[warp] = q_incl;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = uniform(sh.tmem);
-    pdl_wait_prerequisites();
-    pdl_allow_dependents();
-    const bool is_k = static_cast<int>(blockIdx.x) < k_tiles;
-    const int f0 = (is_k ? blockIdx.x : blockIdx.x - k_tiles) * kTile;
-    const int features = a.Hq * (is_k ? a.nope : a.v);
-    const int tile = blockIdx.y;
-    const int b = uniform(stream_of_row(a.tile_start, a.B, tile, lane));  // (every warp)
-    bool ok = true;
-    if (b >= 0) {
-        const int ctx = uniform(a.ctx_lens[b]);
-        const int t0 = uniform((tile - a.tile_start[b]) * kTile);
-        const int end = min(kTile, ctx - t0);  // tokens of the context in this tile
-        const int32_t *row = a.table + static_cast<size_t>(b) * a.max_blocks;
-        if (warp == 4) {
-            // ---- producer: lanes 0-7 fetch a block each, lane 8 the weights
-            int y = a.num_blocks * TTS_BLOCK_TOKENS;  // out of range: zeros
-            bool in_pool = false;
-            if (lane < 8 && lane * TTS_BLOCK_TOKENS < end) {
-                const int id = row[t0 / TTS_BLOCK_TOKENS + lane];
-                in_pool = id >= 0 && id < a.num_blocks;
-                if (in_pool) y = id * TTS_BLOCK_TOKENS;
-                else if (blockIdx.x == 0) flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
+    int t_at = t_incl - t_mine, q_at = q_incl - q_mine, tiles = 0;
+#pragma unroll
+    for (int w = 0; w < kExpandThreads / 32; ++w) {
+        if (w < warp) {
+            t_at += sh.tiles[w];
+            q_at += sh.qtiles[w];
+        }
+        tiles += sh.tiles[w];
+    }
+    const int feature_tiles = k_tiles + v_tiles, clusters = gridDim.x / 2, me = blockIdx.x / 2;
+    const int units = (tiles + 1) / 2 * feature_tiles;
+    const int u0 = static_cast<int>(static_cast<long long>(units) * me / clusters);
+    const int u1 = static_cast<int>(static_cast<long long>(units) * (me + 1) / clusters);
+    const int first_t = u0 / feature_tiles * 2 + static_cast<int>(rank);
+    for (int b = b0; b < b1; ++b) {
+        const bool good = prefill_stream(a, b, &n, &ctx);
+        const int nt = good && n && b < limit ? token_tiles(ctx) : 0;
+        if (first_t >= t_at && first_t < t_at + nt) {
+            sh.start_b = b;
+            sh.start_i = first_t - t_at;
+        }
+        if (blockIdx.x == 0) {
+            a.tile_start[b] = t_at;
+            a.qtile_start[b] = q_at;
+            if (nt) q_at += (n + kRows - 1) / kRows;
+            if (!good || (n && b >= limit)) {  // refused: its rows get zeros
+                flag_error(a.err, TTS_ERRBIT_CTX_LEN);
+                const int r0 = max(0, a.row_start[b]), r1 = min(a.num_rows, a.row_start[b + 1]);
+                const size_t w = static_cast<size_t>(a.Hq) * a.v / 8;
+                for (size_t i = r0 * w; r0 < r1 && i < r1 * w; ++i) reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
             }
-            const uint32_t mask = __ballot_sync(kFull, in_pool);
-            if (blockIdx.x == 0 && lane == 0) a.blocks_ok[tile] = mask;
-            int c = 0;
-            for (; c < chunks; ++c) {
-                const int s = c % kExpandStages;
-                if (c >= kExpandStages && !warp_wait(&sh.empty[s], (c / kExpandStages - 1) & 1)) {
+            if (b == a.B - 1) {
+                a.tile_start[a.B] = t_at + nt;
+                a.qtile_start[a.B] = q_at;
+            }
+        }
+        t_at += nt;
+    }
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are initialised
+    const uint32_t tmem = uniform(sh.tmem);
+    ExpandWalk walk;
+    walk.left = uniform(u1 - u0);
+    walk.feature_tiles = feature_tiles;
+    walk.tiles = uniform(tiles);
+    walk.f = uniform(u0 % feature_tiles);
+    walk.t = uniform(first_t);
+    walk.b = uniform(sh.start_b);
+    walk.i = uniform(sh.start_i);
+    walk.limit = uniform(limit);
+    if (walk.left > 0 && walk.exists()) walk.seek(a);
+    bool ok = true;
+
+    if (warp == 4) {
+        // ---- producer: the token tile's eight blocks for this CTA, its half
+        // of the weight chunk for both.  A block outside the pool (or past the
+        // context) is read out of range, which fills zeros.
+        const uint32_t leader = elect_leader();
+        uint32_t slot = 0, phase = 0, count = 0;
+        int have = -1, ys[8] = {};
+        for (; ok && walk.left > 0; walk.advance(a)) {
+            if (walk.t != have && walk.exists()) {
+                const int block = walk.i * (kTile / TTS_BLOCK_TOKENS) + (lane & 7);
+                int y = a.num_blocks * TTS_BLOCK_TOKENS;
+                bool in_pool = false;
+                if (block * TTS_BLOCK_TOKENS < walk.ctx) {
+                    const int id = a.table[static_cast<size_t>(walk.b) * a.max_blocks + block];
+                    in_pool = id >= 0 && id < a.num_blocks;
+                    if (in_pool) y = id * TTS_BLOCK_TOKENS;
+                    else if (walk.f == 0) flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
+                }
+                const uint32_t mask = __ballot_sync(kFull, in_pool) & 0xFFu;
+                if (walk.f == 0 && lane == 0) a.blocks_ok[walk.t] = mask;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ys[i] = __shfl_sync(kFull, y, i);
+            }
+            have = walk.t;
+            const bool is_k = walk.f < k_tiles;
+            const int row = (is_k ? walk.f : walk.f - k_tiles) * kFeatures + static_cast<int>(rank) * kTile;
+            for (int c = 0; c < chunks; ++c) {
+                if (count >= kExpandSlots && !warp_wait(&sh.empty[slot], phase ^ 1)) {
                     ok = false;
                     break;
                 }
-                const uint32_t bar = smem_addr(&sh.full[s]), at = base + s * 2 * kChunkBytes;
-                if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kChunkBytes);
-                __syncwarp();
-                if (lane < 8) tma_load_2d(at + lane * 2048, &map_pool, c * 64, y, bar);
-                if (lane == 8) tma_load_2d(at + kChunkBytes, is_k ? &map_uk : &map_uv, c * 64, f0, bar);
+                const uint32_t bar = smem_addr(&sh.full[slot]), to = ring + slot * kSlotBytes;
+                mbar_expect_tx_by(leader, bar, walk.exists() ? kSlotBytes : 2 * kChunkBytes);
+                tma_multicast_2d_by(leader, to + (1 + rank) * kChunkBytes, is_k ? &map_uk : &map_uv, c * 64, row, bar, 3);
+                if (walk.exists())
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) tma_load_2d_by(leader, to + i * 2048, &map_pool, c * 64, ys[i], bar);
+                ++count;
+                if (++slot == kExpandSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-            if (lane == 0)
-                for (int i = c > kExpandStages ? c - kExpandStages : 0; i < c; ++i)
-                    mbar_wait(smem_addr(&sh.full[i % kExpandStages]), (i / kExpandStages) & 1);
-        } else if (warp == 5) {
-            // ---- MMA issuer; rows behind the context in its last block hold
-            // anything and are cleared: their keys and values become zero
-            const int stale = (TTS_BLOCK_TOKENS - end % TTS_BLOCK_TOKENS) % TTS_BLOCK_TOKENS;
-            const uint32_t leader = elect_leader();
+        }
+        // every copy lands before the CTA ends
+        for (uint32_t i = min(count, static_cast<uint32_t>(kExpandSlots)); i > 0; --i) {
+            if (slot == 0) {
+                slot = kExpandSlots;
+                phase ^= 1;
+            }
+            --slot;
+            warp_wait(&sh.full[slot], phase);
+        }
+    } else if (warp == 5) {
+        // ---- MMA issuer; rows behind the context in its last block hold
+        // anything and are cleared: their keys and values become zero
+        const uint32_t leader = elect_leader();
+        uint32_t slot = 0, phase = 0, done = 0;
+        for (; ok && walk.left > 0; walk.advance(a), ++done) {
+            const uint32_t buf = done & 1;
+            const int end = walk.ctx - walk.i * kTile;  // tokens of the context from this tile on
+            const int stop = (end + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS * TTS_BLOCK_TOKENS;
             for (int c = 0; c < chunks; ++c) {
-                const int s = c % kExpandStages;
-                if (!warp_wait(&sh.full[s], (c / kExpandStages) & 1)) {
+                WarpWaits<2> w;
+                w.set(0, &sh.full[slot], phase);
+                w.none(1);
+                if (c == 0 && done >= 2) w.set(1, &sh.acc_empty[buf], (done / 2 - 1) & 1);
+                if (!w.wait()) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = base + s * 2 * kChunkBytes;
-                if (stale) {
-                    for (int i = lane; i < stale * 8; i += 32)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + end * 128 + i * 16), "r"(0)
+                const uint32_t sa = ring + slot * kSlotBytes, sb = sa + kChunkBytes;
+                if (walk.exists() && end < kTile && end < stop) {
+                    for (int t = end + lane / 8; t < stop; t += 4)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sa + t * 128 + lane % 8 * 16), "r"(0)
                                      : "memory");
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_by(leader, tmem, sw128_desc(at + kk * 32), sw128_desc(at + kChunkBytes + kk * 32),
-                                mma_idesc(kTile, kTile), (c | kk) != 0);
-                mma_commit_by(leader, smem_addr(&sh.empty[s]));
+                    mma_bf16_by(leader, tmem + buf * kFeatures, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
+                                mma_idesc(kTile, kFeatures), (c | kk) != 0);
+                mma_commit_multicast_by(leader, smem_addr(&sh.empty[slot]), 3);
+                if (++slot == kExpandSlots) {
+                    slot = 0;
+                    phase ^= 1;
+                }
             }
-            mma_commit_by(leader, smem_addr(&sh.acc));
-            if (!warp_wait(&sh.acc, 0)) ok = false;
-        } else {
-            // ---- rotated key parts, then the accumulator
-            if (blockIdx.x == 0) {
+            if (!ok) break;
+            mma_commit_by(leader, smem_addr(&sh.acc_full[buf]));
+        }
+        mma_commit_by(leader, smem_addr(&sh.fin));
+        if (!warp_wait(&sh.fin, 0)) ok = false;
+    } else if (warp < 4) {
+        // ---- rotated key parts, then the accumulators, 64 features at a time
+        const int r = warp * 32 + lane;
+        const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        uint32_t done = 0;
+        for (; walk.left > 0; walk.advance(a), ++done) {
+            if (walk.f == 0 && walk.exists()) {
                 for (int i = threadIdx.x; i < kTile * 8; i += 128) {
-                    const int t = i / 8;
+                    const int t = walk.i * kTile + i / 8;
                     uint4 x = make_uint4(0, 0, 0, 0);
-                    if (t < end) {
-                        const int id = row[(t0 + t) / TTS_BLOCK_TOKENS];
+                    if (t < walk.ctx) {
+                        const int id = a.table[static_cast<size_t>(walk.b) * a.max_blocks + t / TTS_BLOCK_TOKENS];
                         if (id >= 0 && id < a.num_blocks)
                             x = *(reinterpret_cast<const uint4 *>(
                                       a.pool + (static_cast<size_t>(id) * TTS_BLOCK_TOKENS + t % TTS_BLOCK_TOKENS) *
                                                    (a.L + kLatentRope) + a.L) + i % 8);
                     }
-                    reinterpret_cast<uint4 *>(a.kr)[static_cast<size_t>(tile) * kTile * 8 + i] = x;
+                    reinterpret_cast<uint4 *>(a.kr)[static_cast<size_t>(walk.t) * kTile * 8 + i] = x;
                 }
             }
-            ok = warp_wait(&sh.acc, 0);
-            if (ok) {
-                tc_fence_after();
-                // every MMA has read the ring: stage the tile there, in the
-                // stores' swizzle (row r: 16-byte chunk j at j ^ (r % 8))
-                const int r = warp * 32 + lane;
-                const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+            const uint32_t buf = done & 1;
+            const bool is_k = walk.f < k_tiles;
+            const int f0 = (is_k ? walk.f : walk.f - k_tiles) * kFeatures, features = a.Hq * (is_k ? a.nope : a.v);
+            ok = warp_wait(&sh.acc_full[buf], (done / 2) & 1);
+            tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tmem_ld32_nowait(tl + c * 32, x);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int k = (c % 2) * 4 + j;
-                        const uint32_t at = base + (c / 2) * kChunkBytes + r * 128 + ((k ^ (r & 7)) << 4);
-                        const float *f = reinterpret_cast<const float *>(x) + 8 * j;
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(pack_bf16(f[0], f[1])),
-                                     "r"(pack_bf16(f[2], f[3])), "r"(pack_bf16(f[4], f[5])), "r"(pack_bf16(f[6], f[7]))
-                                     : "memory");
-                    }
+            for (int q = 0; q < kFeatures / 64; ++q) {
+                // the staging half is free once the stores before the last have read it
+                if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                int fail;
+                asm volatile(
+                    "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+                    "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                    : "=r"(fail)
+                    : "r"(ok ? 0 : 1)
+                    : "memory");
+                if (fail) {  // (all four warps leave together)
+                    ok = false;
+                    break;
                 }
+                uint32_t x[64];
+                tmem_ld32_nowait(tl + buf * kFeatures + q * 64, x);
+                tmem_ld32_nowait(tl + buf * kFeatures + q * 64 + 32, x + 32);
+                tmem_wait_ld();
+                const float *v = reinterpret_cast<const float *>(x);
+                const uint32_t to = stage + (q & 1) * kChunkBytes + r * 128;
+                // 16-byte chunk j of row r at j ^ (r % 8), the stores' swizzle
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((j ^ (r & 7)) << 4)),
+                                 "r"(pack_bf16(v[8 * j], v[8 * j + 1])), "r"(pack_bf16(v[8 * j + 2], v[8 * j + 3])),
+                                 "r"(pack_bf16(v[8 * j + 4], v[8 * j + 5])), "r"(pack_bf16(v[8 * j + 6], v[8 * j + 7])));
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+                if (threadIdx.x == 0) {
+                    if (walk.exists() && f0 + q * 64 < features)
+                        tma_store_2d(is_k ? &map_k : &map_v, f0 + q * 64, walk.t * kTile, stage + (q & 1) * kChunkBytes);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
             }
-            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-            if (threadIdx.x == 0 && ok) {
-                const CUtensorMap *m = is_k ? &map_k : &map_v;
-                tma_store_2d(m, f0, tile * kTile, base);
-                if (f0 + 64 < features) tma_store_2d(m, f0 + 64, tile * kTile, base + kChunkBytes);
-                asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
-            }
+            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&sh.acc_empty[buf]));
         }
-        if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
+        if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == 6) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+    cluster_sync();  // the peer's copies and commits into this CTA are over
 }
 
 // --------------------------------------------------------------- attention
@@ -637,8 +752,9 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
     if (B == 0 || num_rows == 0) return TTS_OK;
     const PrefillPlan pl = prefill_plan(B, num_rows, Hq, nope_dim, v_dim, max_total_ctx);
     if (!d_ws || !aligned16(d_ws) || ws_bytes < pl.total()) return TTS_ERR_WORKSPACE;
-    // grids, and token rows in the maps' 32-bit coordinates
-    if (pl.tiles > 65535 || pl.qtiles * Hq > 0x7FFFFFFF) return TTS_ERR_UNSUPPORTED;
+    // the grid, GEMM units and token rows are 32-bit
+    const int64_t unit_tiles = static_cast<int64_t>(Hq) * (nope_dim + v_dim) / kFeatures + 2;
+    if (pl.tiles * unit_tiles > 0x40000000 || pl.qtiles * Hq > 0x7FFFFFFF) return TTS_ERR_UNSUPPORTED;
 
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
     PrefillArgs a{};
@@ -678,12 +794,11 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
         return TTS_ERR_CUDA;
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    int rc = launch_kernel(latent_plan_kernel, dim3(1), dim3(kPlanThreads), 0, {cs, thread_pdl()}, a);
-    if (rc != TTS_OK) return rc;
-    const int k_tiles = static_cast<int>((fk + kTile - 1) / kTile), v_tiles = static_cast<int>((fv + kTile - 1) / kTile);
+    const int k_tiles = static_cast<int>((fk + kFeatures - 1) / kFeatures);
+    const int v_tiles = static_cast<int>((fv + kFeatures - 1) / kFeatures);
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_expand_kernel), kExpandSmem)) return TTS_ERR_CUDA;
-    rc = launch_kernel(latent_expand_kernel, dim3(k_tiles + v_tiles, static_cast<unsigned>(pl.tiles)),
-                       dim3(kExpandThreads), kExpandSmem, {cs, true}, pool, uk, uv, qkv[2], qkv[4], a, k_tiles);
+    const int rc = launch_cluster(2, latent_expand_kernel, dim3(kExpandCtas), dim3(kExpandThreads), kExpandSmem,
+                                  {cs, thread_pdl()}, pool, uk, uv, qkv[2], qkv[4], a, k_tiles, v_tiles);
     if (rc != TTS_OK) return rc;
     const unsigned grid = static_cast<unsigned>(pl.qtiles * Hq);
     if (nope_dim == 128)
