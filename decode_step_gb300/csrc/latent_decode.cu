@@ -22,6 +22,7 @@
 // in about 3100.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "latent_common.cuh"
@@ -298,9 +299,17 @@ struct AttnShared {
 
 // Buffers for the weights P: with one, the softmax waits for the O^T of the
 // tile before; wide groups need the space for the ring.
-__host__ __device__ constexpr int p_buffers(int N) { return N <= 48 ? 2 : 1; }
+__host__ __device__ constexpr int p_buffers(int N) { return N == 16 || N == 48 ? 2 : 1; }
 // Buffers for q~: with two, a segment's rows are there when the one before ends.
 __host__ __device__ constexpr int q_buffers(int N) { return N <= 32 ? 2 : 1; }
+
+// Whether P enters the product as two bf16 numbers, its rounding and the
+// remainder, in 2 N columns: the weights are then held to 2^-17.  Up to 48 rows
+// that is nearly free (a 128-row MMA of 16 to 64 columns takes 48 to 52 cycles,
+// most of them reading A); 64 rows would need more than tensor memory's 512
+// columns.
+__host__ __device__ constexpr bool p_split(int N) { return N <= 48; }
+__host__ __device__ constexpr int p_rows(int N) { return p_split(N) ? 2 * N : N; }
 
 template <int N>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -309,10 +318,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = smem_addr(raw);
     constexpr int kPBufs = p_buffers(N), kQBufs = q_buffers(N);
+    constexpr int kO = p_rows(N), kPBytes = kO * 128;  // columns of O^T (rows of P), bytes of a P buffer
     const int chunks = a.L / 64, nb = (a.L + 127) / 128;
     const uint32_t q_base = base, q_bytes = (chunks + 1) * N * 128;     // [kQBufs][chunks + 1][N][128 B]
-    const uint32_t p_base = q_base + kQBufs * q_bytes;                  // [kPBufs][N][128 B]
-    const uint32_t r_base = p_base + kPBufs * N * 128;                         // rope ring
+    const uint32_t p_base = q_base + kQBufs * q_bytes;                  // [kPBufs][kO][128 B]
+    const uint32_t r_base = p_base + kPBufs * kPBytes;                         // rope ring
     const uint32_t l_base = r_base + a.ropes * kChunkBytes;             // latent ring
     AttnShared &sh = *reinterpret_cast<AttnShared *>(raw + (l_base - base) + a.pairs * kPairBytes);
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
@@ -343,7 +353,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         prefetch_tensormap(&map_qr);
     }
     uint32_t cols = 32;
-    while (cols < static_cast<uint32_t>((nb + 2) * N)) cols *= 2;
+    while (cols < static_cast<uint32_t>(2 * N + nb * kO)) cols *= 2;
     if (warp == 6) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
                      "r"(cols)
@@ -495,7 +505,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         // ring holds both tiles' pairs).
         const uint32_t leader = elect_leader();
         constexpr uint32_t idesc_s = mma_idesc(64, N);
-        constexpr uint32_t idesc_o = mma_idesc(128, N) | kTransposeA;
+        constexpr uint32_t idesc_o = mma_idesc(128, kO) | kTransposeA;
         Ring rope(a.ropes), lat(a.pairs);
         uint32_t it = 0, segs = 0;
         // the tile whose O^T is outstanding: the one before `it`
@@ -512,12 +522,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         auto issue_o = [&](uint32_t tile) {
             const uint32_t pb = tile % kPBufs;
             tc_fence_after();
-            const uint32_t sb = p_base + pb * (N * 128);
+            const uint32_t sb = p_base + pb * kPBytes;
             for (int p = 0; p < nb; ++p) {
                 const uint32_t sa = l_base + pend.slot * kPairBytes;
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k)
-                    mma_bf16_by(leader, tmem + (2 + p) * N, sw128_mn_desc(sa + k * 2048, kChunkBytes),
+                    mma_bf16_by(leader, tmem + 2 * N + p * kO, sw128_mn_desc(sa + k * 2048, kChunkBytes),
                                 sw128_desc(sb + k * 32), idesc_o, !(pend_first && k == 0));
                 mma_commit_by(leader, smem_addr(&sh.empty_l[pend.slot]));
                 pend.next();
@@ -720,27 +730,37 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                         if (!o_added(it - 1)) ok = false;
                         tc_fence_after();
                         for (int p = 0; p < nb; ++p)
-                            for (int c = 0; c < N; c += 16) {
+                            for (int c = 0; c < kO; c += 16) {
                                 uint32_t o[16];
-                                tmem_ld16_nowait(tl + (2 + p) * N + c, o);
+                                tmem_ld16_nowait(tl + 2 * N + p * kO + c, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.fac[c + i]);
-                                tmem_st16(tl + (2 + p) * N + c, o);
+                                for (int i = 0; i < 16; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * sh.fac[(c < N ? c : c - N) + i]);
+                                tmem_st16(tl + 2 * N + p * kO + c, o);
                             }
                         tmem_wait_st();
                     }
                 }
                 if (it > 0 && kPBufs == 1 && !o_added(it - 1)) ok = false;
-                const uint32_t pb = p_base + it % kPBufs * (N * 128) + (tok & 7) * 2, px = (tok >> 3) << 4;
+                const uint32_t pb = p_base + it % kPBufs * kPBytes + (tok & 7) * 2, px = (tok >> 3) << 4;
+                // (no memory clobber: the columns' chains overlap; the fence below orders the stores)
+                auto store = [&](int n, __nv_bfloat16 x) {
+                    if (live)
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(pb + n * 128 + (px ^ ((n & 7) << 4))),
+                                     "h"(__bfloat16_as_ushort(x)));
+                };
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     const float x = hw_ex2(fmaf(__uint_as_float(sr[n]), a.scale_log2, -mr[n]));
-                    l[n] += x;  // fp32; only the weights that enter the MMA are rounded
-                    // (no memory clobber: the columns' chains overlap; the fence below orders the stores)
-                    if (live)
-                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(pb + n * 128 + (px ^ ((n & 7) << 4))),
-                                     "h"(__bfloat16_as_ushort(__float2bfloat16_rn(x))));
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+                    store(n, hi);
+                    if constexpr (p_split(N)) {
+                        store(N + n, __float2bfloat16_rn(x - __bfloat162float(hi)));
+                        l[n] += x;
+                    } else {
+                        l[n] += __bfloat162float(hi);  // as the MMA takes it: the weights then add up to one
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
@@ -769,10 +789,16 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             tc_fence_after();
             for (int p = 0; p < nb; ++p) {
                 const int d = p * 128 + warp * 32 + lane;
-                uint32_t o[N];
+                uint32_t o[N], rest[N];
 #pragma unroll
-                for (int c = 0; c < N; c += 16) tmem_ld16_nowait(tl + (2 + p) * N + c, o + c);
+                for (int c = 0; c < N; c += 16) tmem_ld16_nowait(tl + 2 * N + p * kO + c, o + c);
+                if constexpr (p_split(N))
+#pragma unroll
+                    for (int c = 0; c < N; c += 16) tmem_ld16_nowait(tl + 2 * N + p * kO + N + c, rest + c);
                 tmem_wait_ld();
+                if constexpr (p_split(N))
+#pragma unroll
+                    for (int n = 0; n < N; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) + __uint_as_float(rest[n]));
                 if (d < a.L) {
                     float *dst = a.part + slot * N * a.L + d;
 #pragma unroll
@@ -796,14 +822,17 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 // ------------------------------------------------------------------ output
 
 // out[r][h] = w_uv[h] o~[r][h], o~ the join of the row's splits (weights
-// 2^(m_s - max m)), rounded to bf16 for the MMA.  A CTA takes one head and up
-// to 64 query rows, as many as spread the rows over the SMs: its warps join
-// the rows' splits into the A operand (few rows share the warps), then one
-// product with the head's weights, in flight since before the wait for the
-// attention.  Latency-bound: a row's splits are read as soon as their slots are
-// known, with their maxima and sums.
+// 2^(m_s - max m)).  A CTA takes one head and up to 32 query rows, as many as
+// spread the rows over the SMs: its warps join the rows' splits into the A
+// operand (few rows share the warps), then one product with the head's
+// weights, in flight since before the wait for the attention.  The MMA has 64
+// rows: o~ enters as two bf16 numbers, its rounding in the first 32 rows and
+// the remainder in the others, so that it is held to 2^-17 at no cost.
+// Latency-bound: a row's splits are read as soon as their slots are known,
+// with their maxima and sums.
 constexpr int kOutThreads = 512, kOutWarps = kOutThreads / 32;
-constexpr int kOutRows = 64;
+constexpr int kOutRows = 32;
+constexpr int kOutTile = 2 * kOutRows;
 constexpr int kAtOnce = 2;  // splits of a row read together
 
 __global__ void __launch_bounds__(kOutThreads)
@@ -817,9 +846,9 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
     const int L = a.L, R = a.B * a.q_len, chunks = L / 64;
     const uint32_t wb = smem_addr(raw), w_chunk = v_dim * 128;     // [chunks][v][64 l]
     uint8_t *joined = raw + chunks * w_chunk;                      // [chunks][64 rows][64 l], 128-byte swizzle
-    float *sums = reinterpret_cast<float *>(joined + chunks * kOutRows * 128);  // [kOutWarps][L]
+    float *sums = reinterpret_cast<float *>(joined + chunks * kOutTile * 128);  // [kOutWarps][L]
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    const int h = blockIdx.y, r0 = blockIdx.x * rows_per_cta, rows = min(rows_per_cta, R - r0);
+    const int h = blockIdx.y;
     bool ok = true;
     if (warp == 0) {
         const uint32_t leader = elect_leader();
@@ -839,140 +868,170 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
     pdl_wait_prerequisites();
     pdl_allow_dependents();
 
-    // ---- join: `share` warps split a row's splits
-    int share = kOutWarps;
-    while (share > 1 && kOutWarps / share < rows) share /= 2;
-    const int step = kOutWarps / share;
-    auto put = [&](int i, int l, uint32_t x) {  // two values of row i at dimensions l, l + 1
-        *reinterpret_cast<uint32_t *>(joined + (l / 64 * kOutRows + i) * 128 + (((l % 64 / 8) ^ (i & 7)) << 4) + l % 8 * 2) = x;
-    };
-    for (int rr = 0; rr < rows; rr += step) {
-        const int i = rr + warp / share, sub = warp % share;
-        if (i < rows) {
-            const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
-            const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
-            const int2 own = a.owner[bg];
-            const float2 *ml = a.ml + (static_cast<size_t>(own.x) + bg) * N + n;  // split s: ml[s * N]
-            const float *part = a.part + ((static_cast<size_t>(own.x) + bg) * N + n) * L + 4 * lane;
-            const size_t next = static_cast<size_t>(N) * L;
-            const int splits = own.y - own.x + 1;
-            float4 o[kMaxQ] = {};
-            float M = kNoScore, S = 0.0f;
-            for (int s0 = sub; s0 < splits; s0 += kAtOnce * share) {
-                float4 x[kAtOnce][kMaxQ];
-                float2 v[kAtOnce];
-#pragma unroll
-                for (int u = 0; u < kAtOnce; ++u) {
-                    const int s = s0 + u * share;
-                    v[u] = make_float2(kNoScore, 0.0f);
-                    if (s < splits) {
-                        v[u] = ml[static_cast<size_t>(s) * N];
-#pragma unroll
-                        for (int k = 0; k < kMaxQ; ++k)
-                            if (128 * k + 4 * lane < L)
-                                x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * next + 128 * k));
-                    }
-                }
-                float top = M;
-#pragma unroll
-                for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, v[u].x);
-                const float f0 = hw_ex2(M - top);
-                M = top;
-                S *= f0;
-#pragma unroll
-                for (int k = 0; k < kMaxQ; ++k) {
-                    o[k].x *= f0;
-                    o[k].y *= f0;
-                    o[k].z *= f0;
-                    o[k].w *= f0;
-                }
-#pragma unroll
-                for (int u = 0; u < kAtOnce; ++u)
-                    if (s0 + u * share < splits) {
-                        const float f = hw_ex2(v[u].x - top);
-                        S = fmaf(f, v[u].y, S);
-#pragma unroll
-                        for (int k = 0; k < kMaxQ; ++k)
-                            if (128 * k + 4 * lane < L) {
-                                o[k].x = fmaf(f, x[u][k].x, o[k].x);
-                                o[k].y = fmaf(f, x[u][k].y, o[k].y);
-                                o[k].z = fmaf(f, x[u][k].z, o[k].z);
-                                o[k].w = fmaf(f, x[u][k].w, o[k].w);
-                            }
-                    }
-            }
-            if (share == 1) {
-                const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
-#pragma unroll
-                for (int k = 0; k < kMaxQ; ++k)
-                    if (128 * k + 4 * lane < L) {
-                        put(i, 128 * k + 4 * lane, pack_bf16(o[k].x * inv, o[k].y * inv));
-                        put(i, 128 * k + 4 * lane + 2, pack_bf16(o[k].z * inv, o[k].w * inv));
-                    }
-            } else {
-                if (lane == 0) ms[warp] = make_float2(M, S);
-#pragma unroll
-                for (int k = 0; k < kMaxQ; ++k)
-                    if (128 * k + 4 * lane < L) reinterpret_cast<float4 *>(sums + warp * L)[32 * k + lane] = o[k];
-            }
-        }
-        if (share > 1) {
-            __syncthreads();
-            for (int e = threadIdx.x; e < step * (L / 2); e += kOutThreads) {
-                const int which = e / (L / 2), l2 = e - which * (L / 2), i2 = rr + which;
-                if (i2 < rows) {
-                    float M = kNoScore, S = 0.0f, x = 0.0f, y = 0.0f;
-                    for (int s = 0; s < share; ++s) M = fmaxf(M, ms[which * share + s].x);
-                    for (int s = 0; s < share; ++s) {
-                        const float2 v = reinterpret_cast<const float2 *>(sums + (which * share + s) * L)[l2];
-                        const float f = hw_ex2(ms[which * share + s].x - M);
-                        S = fmaf(f, ms[which * share + s].y, S);
-                        x = fmaf(f, v.x, x);
-                        y = fmaf(f, v.y, y);
-                    }
-                    const float inv = S == 0.0f ? 0.0f : 1.0f / S;
-                    put(i2, 2 * l2, pack_bf16(x * inv, y * inv));
-                }
-            }
-            if (rr + step < rows) __syncthreads();
-        }
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(tslot);
-    if (warp == 0) {
-        const uint32_t leader = elect_leader();
-        ok = warp_wait(&full, 0);
-        tc_fence_after();
-        const uint32_t idesc = v_dim == 128 ? mma_idesc(kOutRows, 128) : mma_idesc(kOutRows, 64);
-        const uint32_t ab = wb + chunks * w_chunk;
-        for (int k = 0; k < L / 16; ++k)
-            mma_bf16_by(leader, tmem, sw128_desc(ab + k / 4 * (kOutRows * 128) + k % 4 * 32),
-                        sw128_desc(wb + k / 4 * w_chunk + k % 4 * 32), idesc, k != 0);
-        mma_commit_by(leader, smem_addr(&acc));
-    }
-    if (warp < 4) {
-        if (!warp_wait(&acc, 0)) ok = false;
-        tc_fence_after();
-        // a 64-row accumulator: row 16 w + i in lane 32 w + i, i < 16
-        const int i = warp * 16 + lane;
-        const bool mine = ok && lane < 16 && i < rows;
-        uint4 *dst = reinterpret_cast<uint4 *>(out + (static_cast<size_t>(r0 + i) * a.Hq + h) * v_dim);
-        if (warp * 16 < rows)
-            for (int c = 0; c < v_dim; c += 32) {
-                uint32_t x[32];
-                tmem_ld32_nowait(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, x);
-                tmem_wait_ld();
-                const float *f = reinterpret_cast<const float *>(x);
-                if (mine)
+    for (uint32_t round = 0;; ++round) {
+        const int r0 = (blockIdx.x + round * gridDim.x) * rows_per_cta, rows = min(rows_per_cta, R - r0);
+        if (rows <= 0) break;
+        // ---- join: `share` warps split a row's splits
+        int share = kOutWarps;
+        while (share > 1 && kOutWarps / share < rows) share /= 2;
+        const int step = kOutWarps / share;
+        auto put = [&](int i, int l, float x, float y) {  // two values of row i at dimensions l, l + 1
+            uint8_t *to = joined + (l / 64 * kOutTile + i) * 128 + (((l % 64 / 8) ^ (i & 7)) << 4) + l % 8 * 2;
+            const uint32_t hi = pack_bf16(x, y);
+            *reinterpret_cast<uint32_t *>(to) = hi;
+            *reinterpret_cast<uint32_t *>(to + kOutRows * 128) = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+        };
+        for (int rr = 0; rr < rows; rr += step) {
+            const int i = rr + warp / share, sub = warp % share;
+            if (i < rows) {
+                const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
+                const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
+                const int2 own = a.owner[bg];
+                const float2 *ml = a.ml + (static_cast<size_t>(own.x) + bg) * N + n;  // split s: ml[s * N]
+                const float *part = a.part + ((static_cast<size_t>(own.x) + bg) * N + n) * L + 4 * lane;
+                const size_t next = static_cast<size_t>(N) * L;
+                const int splits = own.y - own.x + 1;
+                float4 o[kMaxQ] = {};
+                float M = kNoScore, S = 0.0f;
+                for (int s0 = sub; s0 < splits; s0 += kAtOnce * share) {
+                    float4 x[kAtOnce][kMaxQ];
+                    float2 v[kAtOnce];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        dst[c / 8 + j] = make_uint4(pack_bf16(f[8 * j], f[8 * j + 1]), pack_bf16(f[8 * j + 2], f[8 * j + 3]),
-                                                    pack_bf16(f[8 * j + 4], f[8 * j + 5]),
-                                                    pack_bf16(f[8 * j + 6], f[8 * j + 7]));
+                    for (int u = 0; u < kAtOnce; ++u) {
+                        const int s = s0 + u * share;
+                        v[u] = make_float2(kNoScore, 0.0f);
+                        if (s < splits) {
+                            v[u] = ml[static_cast<size_t>(s) * N];
+#pragma unroll
+                            for (int k = 0; k < kMaxQ; ++k)
+                                if (128 * k + 4 * lane < L)
+                                    x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * next + 128 * k));
+                        }
+                    }
+                    float top = M;
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, v[u].x);
+                    const float f0 = hw_ex2(M - top);
+                    M = top;
+                    S *= f0;
+#pragma unroll
+                    for (int k = 0; k < kMaxQ; ++k) {
+                        o[k].x *= f0;
+                        o[k].y *= f0;
+                        o[k].z *= f0;
+                        o[k].w *= f0;
+                    }
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+                        if (s0 + u * share < splits) {
+                            const float f = hw_ex2(v[u].x - top);
+                            S = fmaf(f, v[u].y, S);
+#pragma unroll
+                            for (int k = 0; k < kMaxQ; ++k)
+                                if (128 * k + 4 * lane < L) {
+                                    o[k].x = fmaf(f, x[u][k].x, o[k].x);
+                                    o[k].y = fmaf(f, x[u][k].y, o[k].y);
+                                    o[k].z = fmaf(f, x[u][k].z, o[k].z);
+                                    o[k].w = fmaf(f, x[u][k].w, o[k].w);
+                                }
+                        }
+                }
+                if (share == 1) {
+                    const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
+#pragma unroll
+                    for (int k = 0; k < kMaxQ; ++k)
+                        if (128 * k + 4 * lane < L) {
+                            put(i, 128 * k + 4 * lane, o[k].x * inv, o[k].y * inv);
+                            put(i, 128 * k + 4 * lane + 2, o[k].z * inv, o[k].w * inv);
+                        }
+                } else {
+                    if (lane == 0) ms[warp] = make_float2(M, S);
+#pragma unroll
+                    for (int k = 0; k < kMaxQ; ++k)
+                        if (128 * k + 4 * lane < L) reinterpret_cast<float4 *>(sums + warp * L)[32 * k + lane] = o[k];
+                }
             }
+            if (share > 1) {
+                __syncthreads();
+                for (int e = threadIdx.x; e < step * (L / 2); e += kOutThreads) {
+                    const int which = e / (L / 2), l2 = e - which * (L / 2), i2 = rr + which;
+                    if (i2 < rows) {
+                        float M = kNoScore, S = 0.0f, x = 0.0f, y = 0.0f;
+                        for (int s = 0; s < share; ++s) M = fmaxf(M, ms[which * share + s].x);
+                        for (int s = 0; s < share; ++s) {
+                            const float2 v = reinterpret_cast<const float2 *>(sums + (which * share + s) * L)[l2];
+                            const float f = hw_ex2(ms[which * share + s].x - M);
+                            S = fmaf(f, ms[which * share + s].y, S);
+                            x = fmaf(f, v.x, x);
+                            y = fmaf(f, v.y, y);
+                        }
+                        const float inv = S == 0.0f ? 0.0f : 1.0f / S;
+                        put(i2, 2 * l2, x * inv, y * inv);
+                    }
+                }
+                if (rr + step < rows) __syncthreads();
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 0) {
+            const uint32_t leader = elect_leader();
+            if (!warp_wait(&full, 0)) ok = false;
+            tc_fence_after();
+            const uint32_t idesc = v_dim == 128 ? mma_idesc(kOutTile, 128) : mma_idesc(kOutTile, 64);
+            const uint32_t ab = wb + chunks * w_chunk;
+            for (int k = 0; k < L / 16; ++k)
+                mma_bf16_by(leader, tmem, sw128_desc(ab + k / 4 * (kOutTile * 128) + k % 4 * 32),
+                            sw128_desc(wb + k / 4 * w_chunk + k % 4 * 32), idesc, k != 0);
+            mma_commit_by(leader, smem_addr(&acc));
+        }
+        if (warp < 4) {
+            if (!warp_wait(&acc, round & 1)) ok = false;
+            tc_fence_after();
+            // a 64-row accumulator: row 16 w + i in lane 32 w + i, i < 16; the
+            // remainders' rows (warps 2 and 3) go to the others through `sums`
+            const int i = (warp % 2) * 16 + lane, pitch = v_dim + 4;
+            const bool mine = ok && lane < 16 && i < rows;
+            uint4 *dst = reinterpret_cast<uint4 *>(out + (static_cast<size_t>(r0 + i) * a.Hq + h) * v_dim);
+            const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+            if (warp >= 2)
+                for (int c = 0; c < v_dim; c += 32) {
+                    uint32_t x[32];
+                    tmem_ld32_nowait(tl + c, x);
+                    tmem_wait_ld();
+                    if (mine)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<uint4 *>(sums + i * pitch + c + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+                }
+            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+            if (warp < 2)
+                for (int c = 0; c < v_dim; c += 32) {
+                    uint32_t x[32];
+                    tmem_ld32_nowait(tl + c, x);
+                    tmem_wait_ld();
+                    const float *f = reinterpret_cast<const float *>(x);
+                    if (mine)
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8) {
+                            const float4 u = *reinterpret_cast<const float4 *>(sums + i * pitch + c + j);
+                            const float4 w = *reinterpret_cast<const float4 *>(sums + i * pitch + c + j + 4);
+                            dst[(c + j) / 8] = make_uint4(pack_bf16(f[j] + u.x, f[j + 1] + u.y), pack_bf16(f[j + 2] + u.z, f[j + 3] + u.w),
+                                                          pack_bf16(f[j + 4] + w.x, f[j + 5] + w.y),
+                                                          pack_bf16(f[j + 6] + w.z, f[j + 7] + w.w));
+                        }
+                }
+        }
+        // the next rows' A operand and accumulator take the places of these
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
     }
     if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
     tc_fence_before();
@@ -998,8 +1057,8 @@ int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, const CUtensor
                      cudaStream_t stream) {
     // shared memory: q~, P, the rope slots, and latent pairs to the brim
     const int chunks = a.L / 64;
-    a.ropes = N <= 32 ? 3 : 2;
-    const int fixed = (q_buffers(N) * (chunks + 1) + p_buffers(N)) * N * 128 + a.ropes * kChunkBytes + static_cast<int>(sizeof(AttnShared));
+    a.ropes = 2;
+    const int fixed = (q_buffers(N) * (chunks + 1) * N + p_buffers(N) * p_rows(N)) * 128 + a.ropes * kChunkBytes + static_cast<int>(sizeof(AttnShared));
     a.pairs = (kSmemLimit - fixed) / kPairBytes;
     if (a.pairs > kMaxPairs) a.pairs = kMaxPairs;
     if (a.pairs < 2 * ((a.L + 127) / 128)) return TTS_ERR_UNSUPPORTED;  // (S^T goes one tile ahead of O^T)
@@ -1085,11 +1144,14 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
         default: rc = launch_attention<64>(map_kv, map_q, map_qr, a, pl.P, cs); break;
     }
     if (rc != TTS_OK) return rc;
-    // rows a CTA: enough CTAs for the SMs, in eights
-    const int share = (static_cast<int>((static_cast<long>(R) * Hq + kCtas - 1) / kCtas) + 7) / 8 * 8;
-    const int per = share < kOutRows ? share : kOutRows;
-    const int out_smem = L / 64 * (v_dim + kOutRows) * 128 + kOutWarps * L * 4;
+    // one CTA fits an SM: as many as there are SMs share the rows evenly, in
+    // rounds of up to 32 that keep the weights
+    const int most = std::max(1, kCtas / Hq), rounds = (R + most * kOutRows - 1) / (most * kOutRows);
+    const int per = (R + most * rounds - 1) / (most * rounds), gx = std::min(most, (R + per - 1) / per);
+    // (the sums' region also passes 32 rows of remainders on)
+    const int sums_bytes = std::max(kOutWarps * L * 4, kOutRows * (v_dim + 4) * 4);
+    const int out_smem = L / 64 * (v_dim + kOutTile) * 128 + sums_bytes;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_out_kernel), out_smem)) return TTS_ERR_CUDA;
-    return launch_kernel(latent_out_kernel, dim3((R + per - 1) / per, Hq), dim3(kOutThreads), out_smem, {cs, true}, map_uv,
+    return launch_kernel(latent_out_kernel, dim3(gx, Hq), dim3(kOutThreads), out_smem, {cs, true}, map_uv,
                          a, pl.N, per, static_cast<int>(v_dim), static_cast<__nv_bfloat16 *>(d_out));
 }

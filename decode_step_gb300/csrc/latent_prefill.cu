@@ -13,9 +13,10 @@
 //  2. latent_prefill_kernel: attention of 256 rows of one head per CTA (two
 //     128-row tiles that take turns on the tensor core: while one's weights
 //     are computed, the other's products run).  S and O are in tensor memory;
-//     the weights go back into S's columns as bf16 and are the A operand of
+//     the weights go back into S's columns (as f16) and are the A operand of
 //     the second product.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <cmath>
 
@@ -40,6 +41,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// Values and softmax weights are f16: it holds them to 2^-11 where bf16 holds
+// them to 2^-8, at the same rate (weights lie in [0, 2^8]).
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
 struct PrefillArgs {
     const int32_t *table;
     int max_blocks, num_blocks;
@@ -58,15 +66,15 @@ struct PrefillArgs {
 
 // ------------------------------------------------------------------ expand
 
-// K[t][h nope + d] = w_uk[h][d] . c_t and V likewise, bf16: a GEMM of 128-token
+// K[t][h nope + d] = w_uk[h][d] . c_t (bf16) and V likewise (f16): a GEMM of 128-token
 // x 256-feature units.  Persistent, one CTA per SM, in clusters of two that
 // take neighbouring token tiles and the same features: each CTA fetches half of
 // a weight chunk for both (multicast), so a unit reads 256 KB from L2 for
 // 33 Mflop; 128 x 128 units that fetched both operands for themselves were
 // bound by those reads (10 TB/s of L2 to the SMs, 56 us at 8891 tokens x 4096
 // features x 512), and weights kept in shared memory left too short a ring
-// (90 us).  The accumulator is double buffered: one unit's results leave (as
-// bf16, through shared memory, by TMA) while the next one's products run.
+// (90 us).  The accumulator is double buffered: one unit's results leave (through
+// shared memory, by TMA) while the next one's products run.
 // Every CTA scans the streams by itself; CTA 0 writes the plan that the
 // attention reads.  The first feature unit of a token tile also copies the
 // tokens' rotated key parts and records which blocks are in the pool.
@@ -401,10 +409,15 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 const uint32_t to = stage + (q & 1) * kChunkBytes + r * 128;
                 // 16-byte chunk j of row r at j ^ (r % 8), the stores' swizzle
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((j ^ (r & 7)) << 4)),
-                                 "r"(pack_bf16(v[8 * j], v[8 * j + 1])), "r"(pack_bf16(v[8 * j + 2], v[8 * j + 3])),
-                                 "r"(pack_bf16(v[8 * j + 4], v[8 * j + 5])), "r"(pack_bf16(v[8 * j + 6], v[8 * j + 7])));
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        p[i] = is_k ? pack_bf16(v[8 * j + 2 * i], v[8 * j + 2 * i + 1])
+                                    : pack_f16(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((j ^ (r & 7)) << 4)), "r"(p[0]),
+                                 "r"(p[1]), "r"(p[2]), "r"(p[3]));
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
                 if (threadIdx.x == 0) {
@@ -566,8 +579,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                     const uint32_t slot = (pos + c) % kSlots, sb = ring + slot * kChunkBytes;
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_bf16_ts_by(leader, tmem + (2 + s) * kTile + c * 64, tmem + s * kTile + kk * 8,
-                                       sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc(kTile, 64) | kTransposeB,
+                        mma_ts_by(leader, tmem + (2 + s) * kTile + c * 64, tmem + s * kTile + kk * 8,
+                                       sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc_f16(kTile, 64) | kTransposeB,
                                        (j | kk) != 0);
                     if (last_use) mma_commit_by(leader, smem_addr(&sh.empty[slot]));
                 }
@@ -644,9 +657,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                     for (int i = 0; i < 32; ++i) {
                         const float p0 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i]), a.scale_log2, -m));
                         const float p1 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i + 1]), a.scale_log2, -m));
-                        sum[0] += p0;  // fp32; only the weights that enter the MMA are rounded
+                        sum[0] += p0;
                         sum[1] += p1;
-                        p[i] = pack_bf16(p0, p1);
+                        p[i] = pack_f16(p0, p1);
                     }
                     tmem_st32(ts + c / 2, p);
                 }

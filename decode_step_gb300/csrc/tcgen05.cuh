@@ -58,6 +58,11 @@ __host__ __device__ constexpr uint32_t mma_idesc(int M, int N) {
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same with f16 A and B.
+__host__ __device__ constexpr uint32_t mma_idesc_f16(int M, int N) {
+    return mma_idesc(M, N) & ~((1u << 7) | (1u << 10));
+}
+
 __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -218,9 +223,9 @@ __device__ __forceinline__ void mma_commit_multicast_by(uint32_t leader, uint32_
         : "memory");
 }
 
-// D[M][N] (+)= A . B with A (bf16) in tensor memory: row i in lane i, two
-// values of the contraction side a column.
-__device__ __forceinline__ void mma_bf16_ts_by(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+// D[M][N] (+)= A . B with A (16-bit, of the descriptor's type) in tensor
+// memory: row i in lane i, two values of the contraction side a column.
+__device__ __forceinline__ void mma_ts_by(uint32_t leader, uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
                                                uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"

@@ -295,7 +295,7 @@ size_t tts_latent_decode_attn_workspace_size(int32_t B, int32_t q_len, int32_t n
  * over the tokens t < limit of tts_decode_attn (d_ctx_lens counts the tokens
  * after this step's append; causal as there).  Computed in the absorbed form:
  * q_nope w_uk[h] first (rounded to bf16), attention over the latents
- * themselves, then w_uv[h] on the attended latent (rounded to bf16).
+ * themselves (weights rounded to bf16), then w_uv[h] on the attended latent.
  *  d_q_nope  bf16 [B][q_len][Hq][nope_dim]
  *  d_q_rope  bf16 [B][q_len][Hq][64], rotated (tts_latent_append)
  *  d_w_uk    bf16 [Hq][nope_dim][latent_dim];  d_w_uv  bf16 [Hq][v_dim][latent_dim]
@@ -323,8 +323,10 @@ size_t tts_latent_prefill_attn_workspace_size(int32_t B, int32_t num_rows, int32
  * non-decreasing, at most num_rows), the last tokens of its d_ctx_lens[b]
  * cached ones, so row r sees the tokens
  *   t < d_ctx_lens[b] - (d_row_start[b + 1] - r) + 1.
- * The sum is tts_latent_decode_attn's, in the expanded form: keys and values
- * of every head are multiplied out once (rounded to bf16).
+ * The sum is tts_latent_decode_attn's, in the expanded form: keys (rounded to
+ * bf16) and values (rounded to f16, as the softmax weights are) of every head
+ * are multiplied out once.  Values w_uv[h] c beyond f16's range (65504) make
+ * the outputs that they enter not finite.
  *  d_q_nope bf16 [num_rows][Hq][nope_dim];  d_q_rope bf16 [num_rows][Hq][64]
  *  d_out    bf16 [num_rows][Hq][v_dim]
  *  max_total_ctx  host upper bound of the sum of d_ctx_lens over the streams
