@@ -292,7 +292,7 @@ struct AttnShared {
     float fac[kMaxGroup];
     int limit[kMaxGroup];
     union {
-        uint32_t wmax[4][kMaxGroup];  // within a tile
+        float wmax[4][kMaxGroup];  // within a tile
         float lsum[4][kMaxGroup];     // at a segment's end
     };
 };
@@ -634,13 +634,20 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         mma_commit_by(leader, smem_addr(&sh.done));
         if (!warp_wait(&sh.done, 0)) ok = false;
     } else {
-        // ---- softmax warps: lane l < 16 of warp w has token 16 w + l of the
-        // tile (a 64-row accumulator's rows 16 w.. sit in lanes 32 w..), so a
-        // warp's tokens are one block
+        // ---- softmax warps: warp w has the tokens 16 w.. of the tile, one
+        // block (a 64-row accumulator's rows 16 w.. sit in lanes 32 w..); lane
+        // (g, c) has tokens g and g + 8 and of every 8 columns 2 c and 2 c + 1.
+        // Value i of a lane: token g + 8 (i / 2 % 2), column col(i).
         uint32_t it = 0;
         const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const int tok = warp * 16 + lane;
-        const bool live = lane < 16;
+        constexpr int kVals = N / 2;
+        const int g = lane / 4, c2 = lane % 4 * 2;
+        auto col = [&](int i) { return i / 4 * 8 + c2 + i % 2; };
+        // P's rows c2 and c2 + 1 at tokens g and g + 8 (16-byte chunk t / 8 of row n at (t / 8) ^ (n % 8))
+        uint32_t pat[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            pat[i] = p_base + (c2 + i % 2) * 128 + (((2 * warp + i / 2) ^ (c2 + i % 2)) << 4) + g * 2;
         auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1); };
         const int tid = threadIdx.x;
         while (ok && seg.next(a)) {
@@ -660,9 +667,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 sh.limit[tid] = j >= a.q_len ? 0 : a.causal ? seg.ctx - a.q_len + j + 1 : seg.ctx;
             }
             softmax_sync();
-            float l[N];
+            float l[N / 4];  // of columns col(4 j) and col(4 j + 1)
 #pragma unroll
-            for (int n = 0; n < N; ++n) l[n] = 0.0f;
+            for (int n = 0; n < N / 4; ++n) l[n] = 0.0f;
             bool valid = block_ok(seg.first);
             for (int k = 0; k < seg.count; ++k, ++it) {
                 const int tile = seg.first + k;
@@ -670,36 +677,36 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 const bool next_valid = k + 1 < seg.count && block_ok(tile + 1);
                 // (the tile that last used this P buffer has had its O^T added)
                 if (it >= kPBufs && kPBufs > 1 && !o_added(it - kPBufs)) ok = false;
-                float mr[N];
+                float mr[N / 4];
 #pragma unroll
-                for (int n = 0; n < N; n += 4) {
-                    const float4 m4 = *reinterpret_cast<const float4 *>(sh.mref + n);
-                    mr[n] = m4.x;
-                    mr[n + 1] = m4.y;
-                    mr[n + 2] = m4.z;
-                    mr[n + 3] = m4.w;
+                for (int j = 0; j < N / 8; ++j) {
+                    const float2 m2 = *reinterpret_cast<const float2 *>(sh.mref + 8 * j + c2);
+                    mr[2 * j] = m2.x;
+                    mr[2 * j + 1] = m2.y;
                 }
                 if (!warp_wait(&sh.s_full[buf], (it / 2) & 1)) ok = false;
                 tc_fence_after();
-                uint32_t sr[N];
+                uint32_t sr[kVals];
 #pragma unroll
-                for (int c = 0; c < N; c += 16) tmem_ld16_nowait(tl + buf * N + c, sr + c);
+                for (int c = 0; c < N; c += 16) tmem_ld_half16_nowait(tl + buf * N + c, sr + c / 2);
                 tmem_wait_ld();
                 tc_fence_before();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.s_empty[buf]));
-                const int t = tile * kTile + tok;
-                if (!valid || !live) {
+                const int t = tile * kTile + warp * 16 + g;
+                if (!valid) {
 #pragma unroll
-                    for (int n = 0; n < N; ++n) sr[n] = 0xFF800000u;  // -inf
+                    for (int i = 0; i < kVals; ++i) sr[i] = 0xFF800000u;  // -inf
                 } else if ((tile + 1) * kTile > low) {
 #pragma unroll
-                    for (int n = 0; n < N; ++n)
-                        if (t >= sh.limit[n]) sr[n] = 0xFF800000u;
+                    for (int i = 0; i < kVals; ++i)
+                        if (t + (i & 2) * 4 >= sh.limit[col(i)]) sr[i] = 0xFF800000u;
                 }
+                auto score = [&](int i) {  // log2 units, over the running maximum
+                    return fmaf(__uint_as_float(sr[i]), a.scale_log2, -mr[i / 4 * 2 + i % 2]);
+                };
                 float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int n = 0; n < N; ++n)
-                    tops[n % 4] = fmaxf(tops[n % 4], fmaf(__uint_as_float(sr[n]), a.scale_log2, -mr[n]));
+                for (int i = 0; i < kVals; ++i) tops[i % 4] = fmaxf(tops[i % 4], score(i));
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 if (!ok) sh.failed = 1;
                 if (softmax_any(top > kSlack || !ok)) {
@@ -709,22 +716,26 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                         break;
                     }
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        const uint32_t m = __reduce_max_sync(kFull, float_order_key(__uint_as_float(sr[n]) * a.scale_log2));
-                        if (lane == 0) sh.wmax[warp][n] = m;
+                    for (int j = 0; j < N / 4; ++j) {
+                        const int i = j / 2 * 4 + j % 2;
+                        float m = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 2])) * a.scale_log2;
+#pragma unroll
+                        for (int o = 4; o < 32; o *= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+                        if (g == 0) sh.wmax[warp][col(i)] = m;
                     }
                     softmax_sync();
                     if (tid < N) {
-                        const uint32_t m = max(max(sh.wmax[0][tid], sh.wmax[1][tid]), max(sh.wmax[2][tid], sh.wmax[3][tid]));
-                        const float old = sh.mref[tid], now = fmaxf(old, order_key_float(m));
+                        const float m = fmaxf(fmaxf(sh.wmax[0][tid], sh.wmax[1][tid]), fmaxf(sh.wmax[2][tid], sh.wmax[3][tid]));
+                        const float old = sh.mref[tid], now = fmaxf(old, m);
                         sh.mref[tid] = now;
                         sh.fac[tid] = hw_ex2(old - now);
                     }
                     softmax_sync();
 #pragma unroll
-                    for (int n = 0; n < N; ++n) {
-                        l[n] *= sh.fac[n];
-                        mr[n] = sh.mref[n];
+                    for (int j = 0; j < N / 4; ++j) {
+                        const int n = col(j / 2 * 4 + j % 2);
+                        l[j] *= sh.fac[n];
+                        mr[j] = sh.mref[n];
                     }
                     if (k > 0) {
                         if (!o_added(it - 1)) ok = false;
@@ -743,23 +754,22 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     }
                 }
                 if (it > 0 && kPBufs == 1 && !o_added(it - 1)) ok = false;
-                const uint32_t pb = p_base + it % kPBufs * kPBytes + (tok & 7) * 2, px = (tok >> 3) << 4;
-                // (no memory clobber: the columns' chains overlap; the fence below orders the stores)
-                auto store = [&](int n, __nv_bfloat16 x) {
-                    if (live)
-                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(pb + n * 128 + (px ^ ((n & 7) << 4))),
-                                     "h"(__bfloat16_as_ushort(x)));
+                const uint32_t pb = it % kPBufs * kPBytes;
+                // (no memory clobber: the values' chains overlap; the fence below orders the stores)
+                auto store = [&](uint32_t at, __nv_bfloat16 x) {
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(__bfloat16_as_ushort(x)));
                 };
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const float x = hw_ex2(fmaf(__uint_as_float(sr[n]), a.scale_log2, -mr[n]));
+                for (int i = 0; i < kVals; ++i) {
+                    const float x = hw_ex2(score(i));
                     const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-                    store(n, hi);
+                    const uint32_t at = pat[i % 4] + pb + i / 4 * 1024;
+                    store(at, hi);
                     if constexpr (p_split(N)) {
-                        store(N + n, __float2bfloat16_rn(x - __bfloat162float(hi)));
-                        l[n] += x;
+                        store(at + N * 128, __float2bfloat16_rn(x - __bfloat162float(hi)));
+                        l[i / 4 * 2 + i % 2] += x;
                     } else {
-                        l[n] += __bfloat162float(hi);  // as the MMA takes it: the weights then add up to one
+                        l[i / 4 * 2 + i % 2] += __bfloat162float(hi);  // as the MMA takes it: the weights then add up to one
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -775,11 +785,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 break;
             }
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
-                float s = l[n];
+            for (int j = 0; j < N / 4; ++j) {
+                float s = l[j];
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-                if (lane == 0) sh.lsum[warp][n] = s;
+                for (int o = 4; o < 32; o *= 2) s += __shfl_xor_sync(kFull, s, o);
+                if (g == 0) sh.lsum[warp][col(j / 2 * 4 + j % 2)] = s;
             }
             const size_t slot = static_cast<size_t>(blockIdx.x) + seg.bg;
             softmax_sync();
