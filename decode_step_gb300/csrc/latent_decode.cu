@@ -144,7 +144,9 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_co
 // -------------------------------------------------------------- work split
 
 // The work units are the 64-token tiles of every (stream, row group), group
-// bg = b * G + g, in order, cut evenly over the CTAs.  The part of a group
+// bg = b * G + g, in order, cut evenly over the CTAs; each group has one unit
+// before its tiles, which stands for what starting and ending a group costs (a
+// tile's time, about).  The part of a group
 // that a CTA takes is a segment; its partial result goes to slot c + bg
 // (unique: going on to the next segment raises one of the two).
 struct LatentPlan {
@@ -161,7 +163,7 @@ LatentPlan latent_plan(int B, int q_len, int Hq, int L, int max_ctx) {
     const int rows = q_len * Hq;
     p.G = (rows + kMaxGroup - 1) / kMaxGroup;
     p.N = ((rows + p.G - 1) / p.G + 15) / 16 * 16;
-    p.units = static_cast<long>(B) * p.G * ((static_cast<long>(max_ctx) + kTile - 1) / kTile);
+    p.units = static_cast<long>(B) * p.G * ((static_cast<long>(max_ctx) + kTile - 1) / kTile + 1);
     p.P = p.units < kCtas ? static_cast<int>(p.units < 1 ? 1 : p.units) : kCtas;
     p.slots = static_cast<size_t>(p.P) + static_cast<size_t>(B) * p.G;
     p.qt_bytes = align_up(static_cast<size_t>(B) * rows * L * 2, 256);
@@ -211,11 +213,11 @@ __device__ __forceinline__ int stream_tiles(const LatentAttnArgs &a, int b, int 
 
 // Walks a CTA's segments; every warp keeps its own copy.
 struct Segments {
-    int b, g, tile;        // next segment's start
+    int b, g, unit;        // next unit (0: the group's first, then its tiles)
     int left;              // units left
     // current segment
+    int cur_b, cur_g, bg;
     int ctx, first, count; // first tile, tiles
-    int bg;
     __device__ __forceinline__ bool next(const LatentAttnArgs &a) {
         while (left > 0) {
             const int n = uniform(stream_tiles(a, b, &ctx));
@@ -224,22 +226,22 @@ struct Segments {
                 ++b;
                 continue;
             }
-            first = tile;
-            count = min(n - tile, left);
-            bg = b * a.G + g;
-            left -= count;
+            const int units = min(n + 1 - unit, left);
+            first = max(unit - 1, 0);
+            count = unit + units - 1 - first;
             cur_b = b;
             cur_g = g;
-            tile = 0;
+            bg = b * a.G + g;
+            left -= units;
+            unit = 0;
             if (++g == a.G) {
                 g = 0;
                 ++b;
             }
-            return true;
+            if (count > 0) return true;
         }
         return false;
     }
-    int cur_b, cur_g;
 };
 
 // ------------------------------------------------------------- attention
@@ -279,12 +281,12 @@ struct Ring {
     }
 };
 
-constexpr int kMaxPairs = 16, kMaxRopes = 4;
+constexpr int kMaxPairs = 16, kMaxRopes = 8;
 
 struct AttnShared {
-    uint64_t full_l[kMaxPairs], empty_l[kMaxPairs], full_r[kMaxRopes], empty_r[kMaxRopes];
-    uint64_t s_full[2], s_empty[2], p_full[2], p_empty[2], o_empty, q_full[2], q_empty[2], done;
-    int start_b, start_g, start_tile;
+    uint64_t full[kMaxRopes], empty_l[kMaxPairs], empty_r[kMaxRopes];
+    uint64_t s_full[2], p_full[2], p_empty[2], o_empty, q_full[2], q_empty[2], done;
+    int start_b, start_g, start_unit;
     uint32_t tmem;
     int sums[8];
     int failed;
@@ -328,17 +330,13 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
 
     if (warp == 5 && lane == 0) {
-        for (int i = 0; i < a.pairs; ++i) {
-            mbar_init(smem_addr(&sh.full_l[i]), 1);
-            mbar_init(smem_addr(&sh.empty_l[i]), 1);
-        }
+        for (int i = 0; i < a.pairs; ++i) mbar_init(smem_addr(&sh.empty_l[i]), 1);
         for (int i = 0; i < a.ropes; ++i) {
-            mbar_init(smem_addr(&sh.full_r[i]), 1);
+            mbar_init(smem_addr(&sh.full[i]), 1);
             mbar_init(smem_addr(&sh.empty_r[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.s_empty[i]), 4);
             mbar_init(smem_addr(&sh.p_full[i]), 4);
             mbar_init(smem_addr(&sh.p_empty[i]), 1);
             mbar_init(smem_addr(&sh.q_full[i]), 1);
@@ -366,7 +364,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
     int mine = 0;
     for (int b = b0; b < b1; ++b) {
         const int n = stream_tiles(a, b);
-        mine += n;
+        mine += n ? n + 1 : 0;
         if (n == 0 && blockIdx.x == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
     }
     int incl = mine;
@@ -391,17 +389,17 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
     if (u0 < u1 || blockIdx.x == 0) {
         int at = before * a.G;
         for (int b = b0; b < b1; ++b) {
-            const int n = stream_tiles(a, b);
-            if (u0 < u1 && u0 >= at && u0 < at + n * a.G) {
+            const int n = stream_tiles(a, b), w = n ? n + 1 : 0;  // units of a group
+            if (u0 < u1 && u0 >= at && u0 < at + w * a.G) {
                 sh.start_b = b;
-                sh.start_g = (u0 - at) / n;
-                sh.start_tile = (u0 - at) % n;
+                sh.start_g = (u0 - at) / w;
+                sh.start_unit = (u0 - at) % w;
             }
             if (blockIdx.x == 0)
                 for (int g = 0; g < a.G; ++g)
                     a.owner[b * a.G + g] =
-                        n ? make_int2(cut.owner(at + g * n), cut.owner(at + (g + 1) * n - 1)) : make_int2(1, 0);
-            at += n * a.G;
+                        n ? make_int2(cut.owner(at + g * w + 1), cut.owner(at + (g + 1) * w - 1)) : make_int2(1, 0);
+            at += w * a.G;
         }
     }
     __syncthreads();
@@ -410,7 +408,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
     seg.left = uniform(u1 - u0);
     seg.b = uniform(sh.start_b);
     seg.g = uniform(sh.start_g);
-    seg.tile = uniform(sh.start_tile);
+    seg.unit = uniform(sh.start_unit);
     pdl_allow_dependents();
     bool ok = true;
 
@@ -445,10 +443,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     ok = false;
                     break;
                 }
-                const uint32_t fr = smem_addr(&sh.full_r[rope.slot]), at = r_base + rope.slot * kChunkBytes;
-                mbar_expect_tx_by(leader, fr, kChunkBytes);
+                // (the tile's one barrier: the MMAs of S^T take the whole tile)
+                const uint32_t bar = smem_addr(&sh.full[rope.slot]), at = r_base + rope.slot * kChunkBytes;
+                mbar_expect_tx_by(leader, bar, (chunks + 1) * kChunkBytes);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tma_load_2d_by(leader, at + i * 2048, &map_kv, a.L, ys[i], fr);
+                for (int i = 0; i < 4; ++i) tma_load_2d_by(leader, at + i * 2048, &map_kv, a.L, ys[i], bar);
                 rope.next();
                 ++it;
                 for (int p = 0; p < nb; ++p) {
@@ -456,15 +455,13 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                         ok = false;
                         break;
                     }
-                    const uint32_t fl = smem_addr(&sh.full_l[lat.slot]), to = l_base + lat.slot * kPairBytes;
-                    const bool both = 2 * p + 1 < chunks;
-                    mbar_expect_tx_by(leader, fl, both ? kPairBytes : kChunkBytes);
+                    const uint32_t to = l_base + lat.slot * kPairBytes;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tma_load_2d_by(leader, to + i * 2048, &map_kv, p * 128, ys[i], fl);
-                    if (both)
+                    for (int i = 0; i < 4; ++i) tma_load_2d_by(leader, to + i * 2048, &map_kv, p * 128, ys[i], bar);
+                    if (2 * p + 1 < chunks)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            tma_load_2d_by(leader, to + kChunkBytes + i * 2048, &map_kv, p * 128 + 64, ys[i], fl);
+                            tma_load_2d_by(leader, to + kChunkBytes + i * 2048, &map_kv, p * 128 + 64, ys[i], bar);
                     lat.next();
                     ++lpos;
                 }
@@ -473,11 +470,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         // every copy lands before the CTA ends
         for (uint32_t i = min(it, rope.n); i > 0; --i) {
             rope.back();
-            warp_wait(&sh.full_r[rope.slot], rope.phase);
-        }
-        for (uint32_t i = min(lpos, lat.n); i > 0; --i) {
-            lat.back();
-            warp_wait(&sh.full_l[lat.slot], lat.phase);
+            warp_wait(&sh.full[rope.slot], rope.phase);
         }
     } else if (warp == 6) {
         // ---- Q loader: a segment's q~ rows, once the S MMAs of the one before are done
@@ -540,23 +533,13 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             const uint32_t qs = q_base + segs % kQBufs * q_bytes;
             for (int k = 0; k < count; ++k) {
                 const uint32_t buf = it & 1;
-                // the rope chunk, S's buffer, the queries and the tile's pairs
-                WarpWaits<7> w;
-                w.set(0, &sh.full_r[rope.slot], rope.phase);
+                // the tile and the queries (S's buffer is free: the weights
+                // of the tile before the last, which came from it, are in)
+                WarpWaits<2> w;
+                w.set(0, &sh.full[rope.slot], rope.phase);
                 w.none(1);
-                if (it >= 2) w.set(1, &sh.s_empty[buf], (it / 2 - 1) & 1);
-                w.none(2);
-                if (k == 0) w.set(2, &sh.q_full[segs % kQBufs], (segs / kQBufs) & 1);
+                if (k == 0) w.set(1, &sh.q_full[segs % kQBufs], (segs / kQBufs) & 1);
                 const Ring first = lat;
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    w.none(3 + p);
-                    if (p < nb) {
-                        w.set(3 + p, &sh.full_l[lat.slot], lat.phase);
-                        lat.next();
-                    }
-                }
-                lat = first;
                 // a tile that is still landing lets O^T of the one before go
                 // first, if its weights are there: that frees ring slots
                 bool ready = w.poll();
@@ -690,8 +673,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 #pragma unroll
                 for (int c = 0; c < N; c += 16) tmem_ld_half16_nowait(tl + buf * N + c, sr + c / 2);
                 tmem_wait_ld();
-                tc_fence_before();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.s_empty[buf]));
                 const int t = tile * kTile + warp * 16 + g;
                 if (!valid) {
 #pragma unroll
@@ -1067,12 +1048,12 @@ int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, const CUtensor
                      cudaStream_t stream) {
     // shared memory: q~, P, the rope slots, and latent pairs to the brim
     const int chunks = a.L / 64;
-    a.ropes = 2;
-    const int fixed = (q_buffers(N) * (chunks + 1) * N + p_buffers(N) * p_rows(N)) * 128 + a.ropes * kChunkBytes + static_cast<int>(sizeof(AttnShared));
-    a.pairs = (kSmemLimit - fixed) / kPairBytes;
-    if (a.pairs > kMaxPairs) a.pairs = kMaxPairs;
-    if (a.pairs < 2 * ((a.L + 127) / 128)) return TTS_ERR_UNSUPPORTED;  // (S^T goes one tile ahead of O^T)
-    const int smem = fixed + a.pairs * kPairBytes;
+    const int fixed = (q_buffers(N) * (chunks + 1) * N + p_buffers(N) * p_rows(N)) * 128 + static_cast<int>(sizeof(AttnShared));
+    const int nb = (a.L + 127) / 128, tiles = (kSmemLimit - fixed) / (kChunkBytes + nb * kPairBytes);
+    a.ropes = std::min(std::max(tiles, 2), kMaxRopes);  // a rope slot for every tile on its way
+    a.pairs = std::min((kSmemLimit - fixed - a.ropes * kChunkBytes) / kPairBytes, kMaxPairs);
+    if (a.pairs < 2 * nb) return TTS_ERR_UNSUPPORTED;  // (S^T goes one tile ahead of O^T)
+    const int smem = fixed + a.ropes * kChunkBytes + a.pairs * kPairBytes;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_attn_kernel<N>), smem)) return TTS_ERR_CUDA;
     return launch_kernel(latent_attn_kernel<N>, dim3(P), dim3(kAttnThreads), smem, {stream, true}, kv, q, qr, a);
 }
