@@ -198,7 +198,7 @@ struct LatentAttnArgs {
     int causal;
     float *part;       // [slots][N][L] unnormalised o~
     float2 *ml;        // [slots][N] running maximum (log2 units), sum
-    int2 *owner;       // [B * G] first and last CTA of each group (1, 0: no unit)
+    int2 *owner;       // [B * G] first CTA and number of splits of each group
     int32_t *err;
     int pairs, ropes;  // ring slots
 };
@@ -209,6 +209,46 @@ __device__ __forceinline__ int stream_tiles(const LatentAttnArgs &a, int b, int 
     if (ctx_out) *ctx_out = ctx;
     if (ctx < a.q_len || ctx > a.max_ctx || ctx > a.max_blocks * TTS_BLOCK_TOKENS) return 0;
     return (ctx + kTile - 1) / kTile;
+}
+
+// Units of one of stream b's groups (0: its length is out of range).
+__device__ __forceinline__ int group_units(const LatentAttnArgs &a, int b) {
+    const int n = stream_tiles(a, b);
+    return n ? n + 1 : 0;
+}
+
+// A block's scan of the streams: thread t has the streams b0..b1 - 1, the first
+// of which starts at unit `at`; U units in all.  `sums` holds an entry per warp.
+struct StreamScan {
+    int b0, b1, at, U;
+};
+template <int kThreads>
+__device__ __forceinline__ StreamScan scan_streams(const LatentAttnArgs &a, int *sums) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int per = (a.B + kThreads - 1) / kThreads;
+    StreamScan s;
+    s.b0 = min(a.B, static_cast<int>(threadIdx.x) * per);
+    s.b1 = min(a.B, s.b0 + per);
+    int mine = 0;
+    for (int b = s.b0; b < s.b1; ++b) mine += group_units(a, b);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    s.at = incl - mine;
+    s.U = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) s.at += sums[w];
+        s.U += sums[w];
+    }
+    s.at *= a.G;
+    s.U *= a.G;
+    return s;
 }
 
 // Walks a CTA's segments; every warp keeps its own copy.
@@ -358,47 +398,28 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // ---- this CTA's units: a scan of the streams' tile counts
-    const int per = (a.B + kAttnThreads - 1) / kAttnThreads;
-    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const int n = stream_tiles(a, b);
-        mine += n ? n + 1 : 0;
-        if (n == 0 && blockIdx.x == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += x;
-    }
-    if (lane == 31) sh.sums[warp] = incl;
+    // ---- this CTA's units
     tc_fence_before();
-    __syncthreads();
+    const StreamScan scan = scan_streams<kAttnThreads>(a, sh.sums);
     tc_fence_after();
-    int before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnThreads / 32; ++w) {
-        if (w < warp) before += sh.sums[w];
-        total += sh.sums[w];
-    }
-    const int U = total * a.G;
-    const UnitCut cut(U, gridDim.x);
-    const int u0 = min(U, cut.begin(blockIdx.x)), u1 = min(U, cut.begin(blockIdx.x + 1));
+    const UnitCut cut(scan.U, gridDim.x);
+    const int u0 = min(scan.U, cut.begin(blockIdx.x)), u1 = min(scan.U, cut.begin(blockIdx.x + 1));
     if (u0 < u1 || blockIdx.x == 0) {
-        int at = before * a.G;
-        for (int b = b0; b < b1; ++b) {
-            const int n = stream_tiles(a, b), w = n ? n + 1 : 0;  // units of a group
+        int at = scan.at;
+        for (int b = scan.b0; b < scan.b1; ++b) {
+            const int w = group_units(a, b);
             if (u0 < u1 && u0 >= at && u0 < at + w * a.G) {
                 sh.start_b = b;
                 sh.start_g = (u0 - at) / w;
                 sh.start_unit = (u0 - at) % w;
             }
-            if (blockIdx.x == 0)
-                for (int g = 0; g < a.G; ++g)
-                    a.owner[b * a.G + g] =
-                        n ? make_int2(cut.owner(at + g * w + 1), cut.owner(at + (g + 1) * w - 1)) : make_int2(1, 0);
+            if (blockIdx.x == 0) {
+                if (w == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
+                for (int g = 0; g < a.G; ++g) {
+                    const int first = w ? cut.owner(at + g * w + 1) : 0;
+                    a.owner[b * a.G + g] = make_int2(first, w ? cut.owner(at + (g + 1) * w - 1) - first + 1 : 0);
+                }
+            }
             at += w * a.G;
         }
     }
@@ -813,31 +834,78 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 // ------------------------------------------------------------------ output
 
 // out[r][h] = w_uv[h] o~[r][h], o~ the join of the row's splits (weights
-// 2^(m_s - max m)).  A CTA takes one head and up to 32 query rows, as many as
-// spread the rows over the SMs: its warps join the rows' splits into the A
-// operand (few rows share the warps), then one product with the head's
-// weights, in flight since before the wait for the attention.  The MMA has 64
-// rows: o~ enters as two bf16 numbers, its rounding in the first 32 rows and
-// the remainder in the others, so that it is held to 2^-17 at no cost.
-// Latency-bound: a row's splits are read as soon as their slots are known,
-// with their maxima and sums.
+// 2^(m_s - max m)).  A CTA takes one head and shares the rows evenly with the
+// head's others, in rounds of up to 32; its warps join the rows' splits into
+// the B operand (few rows share the warps), then one product D[v][rows] with
+// the head's weights.  o~ enters as two bf16 numbers, its rounding in the first
+// half of the columns and the remainder in the other, so that it is held to
+// 2^-17 (the MMA's time is that of reading the weights).
+// Latency-bound: the weights are in flight before the wait for the attention,
+// and a row's partial results are read together with their maxima and sums.
 constexpr int kOutThreads = 512, kOutWarps = kOutThreads / 32;
 constexpr int kOutRows = 32;
-constexpr int kOutTile = 2 * kOutRows;
-constexpr int kAtOnce = 2;  // splits of a row read together
+
+// Sums kQ x 128 dimensions of one row over the splits s = first, first +
+// stride, .. (`count` in all), kAtOnce of them read together: o is scaled by
+// 2^-M, M the largest of the splits' maxima, and S is the sum of their sums
+// alike.  Every load is issued, past the last split or dimension from the last
+// one (with weight zero, or to no use): a condition would put them in turn.
+template <int kQ, int kAtOnce>
+__device__ __forceinline__ void join_splits(const float *part, size_t part_step, const float2 *ml, size_t ml_step, int first,
+                                            int stride, int count, const int *dims, float4 *o, float &M, float &S) {
+    for (int s0 = first; s0 < count; s0 += kAtOnce * stride) {
+        float4 x[kAtOnce][kQ];
+        float2 v[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const int s = min(s0 + u * stride, count - 1);
+            v[u] = __ldcg(ml + s * ml_step);
+#pragma unroll
+            for (int k = 0; k < kQ; ++k) x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * part_step + dims[k]));
+        }
+        float top = M;
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (s0 + u * stride >= count) v[u] = make_float2(-INFINITY, 0.0f);
+            top = fmaxf(top, v[u].x);
+        }
+        const float f0 = hw_ex2(M - top);
+        M = top;
+        S *= f0;
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) {
+            o[k].x *= f0;
+            o[k].y *= f0;
+            o[k].z *= f0;
+            o[k].w *= f0;
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+            const float f = hw_ex2(v[u].x - top);
+            S = fmaf(f, v[u].y, S);
+#pragma unroll
+            for (int k = 0; k < kQ; ++k) {
+                o[k].x = fmaf(f, x[u][k].x, o[k].x);
+                o[k].y = fmaf(f, x[u][k].y, o[k].y);
+                o[k].z = fmaf(f, x[u][k].z, o[k].z);
+                o[k].w = fmaf(f, x[u][k].w, o[k].w);
+            }
+        }
+    }
+}
 
 __global__ void __launch_bounds__(kOutThreads)
-latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnArgs a, int N, int rows_per_cta, int v_dim,
-                  __nv_bfloat16 *__restrict__ out) {
-    constexpr int kMaxQ = kLatentMaxDim / 128;
+latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnArgs a, int N,
+                  int rows_per_round, int v_dim, __nv_bfloat16 *__restrict__ out) {
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ float2 ms[kOutWarps];
     __shared__ uint64_t full, acc;
     __shared__ uint32_t tslot;
     const int L = a.L, R = a.B * a.q_len, chunks = L / 64;
+    const int cols = (rows_per_round + 7) / 8 * 16;                // columns: roundings, remainders
     const uint32_t wb = smem_addr(raw), w_chunk = v_dim * 128;     // [chunks][v][64 l]
-    uint8_t *joined = raw + chunks * w_chunk;                      // [chunks][64 rows][64 l], 128-byte swizzle
-    float *sums = reinterpret_cast<float *>(joined + chunks * kOutTile * 128);  // [kOutWarps][L]
+    uint8_t *joined = raw + chunks * w_chunk;                      // [chunks][cols][64 l], 128-byte swizzle
+    float *sums = reinterpret_cast<float *>(joined + chunks * cols * 128);  // [kOutWarps][128]
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int h = blockIdx.y;
     bool ok = true;
@@ -852,119 +920,83 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
         mbar_expect_tx_by(leader, smem_addr(&full), chunks * w_chunk);
         for (int c = 0; c < chunks; ++c)
             tma_load_2d_by(leader, wb + c * w_chunk, &map_uv, 64 * c, h * v_dim, smem_addr(&full));
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tslot))
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 64;" ::"r"(smem_addr(&tslot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait_prerequisites();
-    pdl_allow_dependents();
-
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(tslot);
+    auto put = [&](int i, int l, float x, float y) {  // two values of row i at dimensions l, l + 1
+        uint8_t *to = joined + (l / 64 * cols + i) * 128 + (((l % 64 / 8) ^ (i & 7)) << 4) + l % 8 * 2;
+        const uint32_t hi = pack_bf16(x, y);
+        *reinterpret_cast<uint32_t *>(to) = hi;
+        *reinterpret_cast<uint32_t *>(to + cols * 64) = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+    };
     for (uint32_t round = 0;; ++round) {
-        const int r0 = (blockIdx.x + round * gridDim.x) * rows_per_cta, rows = min(rows_per_cta, R - r0);
+        const int r0 = (blockIdx.x + round * gridDim.x) * rows_per_round, rows = min(rows_per_round, R - r0);
         if (rows <= 0) break;
-        // ---- join: `share` warps split a row's splits
-        int share = kOutWarps;
-        while (share > 1 && kOutWarps / share < rows) share /= 2;
-        const int step = kOutWarps / share;
-        auto put = [&](int i, int l, float x, float y) {  // two values of row i at dimensions l, l + 1
-            uint8_t *to = joined + (l / 64 * kOutTile + i) * 128 + (((l % 64 / 8) ^ (i & 7)) << 4) + l % 8 * 2;
-            const uint32_t hi = pack_bf16(x, y);
-            *reinterpret_cast<uint32_t *>(to) = hi;
-            *reinterpret_cast<uint32_t *>(to + kOutRows * 128) = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
-        };
-        for (int rr = 0; rr < rows; rr += step) {
-            const int i = rr + warp / share, sub = warp % share;
+        // ---- join: a warp a row; up to 4 rows a warp for every 128 of their
+        // dimensions, the warps left over sharing the splits
+        const int quarters = (L + 127) / 128, lq = quarters > 2 ? 2 : quarters - 1;  // log2, rounded up
+        const int lshare = rows > 4 ? 0 : rows > 2 ? 2 : rows > 1 ? 3 : 4;           // log2 of a row's warps
+        const int ldims = lshare ? lq : 0, lss = lshare - ldims, ss = 1 << lss;
+        for (int rr = 0; rr < rows; rr += kOutWarps >> lshare) {
+            const int i = rr + (warp >> lshare), sub = warp & ((1 << lshare) - 1);
+            const int first = sub >> ldims, d0 = (sub & ((1 << ldims) - 1)) * 128 + 4 * lane;
+            const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
+            const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
+            if (round == 0 && rr == 0) {
+                pdl_wait_prerequisites();
+                pdl_allow_dependents();
+            }
             if (i < rows) {
-                const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
-                const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
                 const int2 own = a.owner[bg];
-                const float2 *ml = a.ml + (static_cast<size_t>(own.x) + bg) * N + n;  // split s: ml[s * N]
-                const float *part = a.part + ((static_cast<size_t>(own.x) + bg) * N + n) * L + 4 * lane;
-                const size_t next = static_cast<size_t>(N) * L;
-                const int splits = own.y - own.x + 1;
-                float4 o[kMaxQ] = {};
+                const size_t row = (static_cast<size_t>(own.x) + bg) * N + n;
+                const float2 *ml = a.ml + row;  // split s: ml[s * N]
+                const float *part = a.part + row * L;
+                int dims[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dims[k] = min(d0 + 128 * k, L - 4);
+                const size_t step = static_cast<size_t>(N) * L;
+                float4 o[4] = {};
                 float M = kNoScore, S = 0.0f;
-                for (int s0 = sub; s0 < splits; s0 += kAtOnce * share) {
-                    float4 x[kAtOnce][kMaxQ];
-                    float2 v[kAtOnce];
-#pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u) {
-                        const int s = s0 + u * share;
-                        v[u] = make_float2(kNoScore, 0.0f);
-                        if (s < splits) {
-                            v[u] = ml[static_cast<size_t>(s) * N];
-#pragma unroll
-                            for (int k = 0; k < kMaxQ; ++k)
-                                if (128 * k + 4 * lane < L)
-                                    x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * next + 128 * k));
-                        }
-                    }
-                    float top = M;
-#pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, v[u].x);
-                    const float f0 = hw_ex2(M - top);
-                    M = top;
-                    S *= f0;
-#pragma unroll
-                    for (int k = 0; k < kMaxQ; ++k) {
-                        o[k].x *= f0;
-                        o[k].y *= f0;
-                        o[k].z *= f0;
-                        o[k].w *= f0;
-                    }
-#pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u)
-                        if (s0 + u * share < splits) {
-                            const float f = hw_ex2(v[u].x - top);
-                            S = fmaf(f, v[u].y, S);
-#pragma unroll
-                            for (int k = 0; k < kMaxQ; ++k)
-                                if (128 * k + 4 * lane < L) {
-                                    o[k].x = fmaf(f, x[u][k].x, o[k].x);
-                                    o[k].y = fmaf(f, x[u][k].y, o[k].y);
-                                    o[k].z = fmaf(f, x[u][k].z, o[k].z);
-                                    o[k].w = fmaf(f, x[u][k].w, o[k].w);
-                                }
-                        }
-                }
-                if (share == 1) {
+                if (lshare) join_splits<1, 8>(part, step, ml, N, first, ss, own.y, dims, o, M, S);
+                else join_splits<4, 2>(part, step, ml, N, 0, 1, own.y, dims, o, M, S);
+                if (lss == 0) {
                     const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
 #pragma unroll
-                    for (int k = 0; k < kMaxQ; ++k)
-                        if (128 * k + 4 * lane < L) {
-                            put(i, 128 * k + 4 * lane, o[k].x * inv, o[k].y * inv);
-                            put(i, 128 * k + 4 * lane + 2, o[k].z * inv, o[k].w * inv);
+                    for (int k = 0; k < 4; ++k)
+                        if (d0 + 128 * k < L && (k == 0 || !lshare)) {
+                            put(i, d0 + 128 * k, o[k].x * inv, o[k].y * inv);
+                            put(i, d0 + 128 * k + 2, o[k].z * inv, o[k].w * inv);
                         }
                 } else {
                     if (lane == 0) ms[warp] = make_float2(M, S);
-#pragma unroll
-                    for (int k = 0; k < kMaxQ; ++k)
-                        if (128 * k + 4 * lane < L) reinterpret_cast<float4 *>(sums + warp * L)[32 * k + lane] = o[k];
+                    if (d0 < L) *reinterpret_cast<float4 *>(sums + warp * 128 + 4 * lane) = o[0];
                 }
             }
-            if (share > 1) {
+            if (lss > 0) {  // (one pass: every row has its warps)
                 __syncthreads();
-                for (int e = threadIdx.x; e < step * (L / 2); e += kOutThreads) {
-                    const int which = e / (L / 2), l2 = e - which * (L / 2), i2 = rr + which;
-                    if (i2 < rows) {
-                        float M = kNoScore, S = 0.0f, x = 0.0f, y = 0.0f;
-                        for (int s = 0; s < share; ++s) M = fmaxf(M, ms[which * share + s].x);
-                        for (int s = 0; s < share; ++s) {
-                            const float2 v = reinterpret_cast<const float2 *>(sums + (which * share + s) * L)[l2];
-                            const float f = hw_ex2(ms[which * share + s].x - M);
-                            S = fmaf(f, ms[which * share + s].y, S);
-                            x = fmaf(f, v.x, x);
-                            y = fmaf(f, v.y, y);
-                        }
-                        const float inv = S == 0.0f ? 0.0f : 1.0f / S;
-                        put(i2, 2 * l2, x * inv, y * inv);
+                if (i < rows && first == 0 && d0 < L) {
+                    float M = kNoScore, S = 0.0f;
+                    float4 x = {};
+                    for (int s = 0; s < ss; ++s) M = fmaxf(M, ms[warp + (s << ldims)].x);
+                    for (int s = 0; s < ss; ++s) {
+                        const float2 v = ms[warp + (s << ldims)];
+                        const float4 y = *reinterpret_cast<const float4 *>(sums + (warp + (s << ldims)) * 128 + 4 * lane);
+                        const float f = hw_ex2(v.x - M);
+                        S = fmaf(f, v.y, S);
+                        x.x = fmaf(f, y.x, x.x);
+                        x.y = fmaf(f, y.y, x.y);
+                        x.z = fmaf(f, y.z, x.z);
+                        x.w = fmaf(f, y.w, x.w);
                     }
+                    const float inv = S == 0.0f ? 0.0f : 1.0f / S;
+                    put(i, d0, x.x * inv, x.y * inv);
+                    put(i, d0 + 2, x.z * inv, x.w * inv);
                 }
-                if (rr + step < rows) __syncthreads();
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -975,61 +1007,42 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
             const uint32_t leader = elect_leader();
             if (!warp_wait(&full, 0)) ok = false;
             tc_fence_after();
-            const uint32_t idesc = v_dim == 128 ? mma_idesc(kOutTile, 128) : mma_idesc(kOutTile, 64);
-            const uint32_t ab = wb + chunks * w_chunk;
-            for (int k = 0; k < L / 16; ++k)
-                mma_bf16_by(leader, tmem, sw128_desc(ab + k / 4 * (kOutTile * 128) + k % 4 * 32),
-                            sw128_desc(wb + k / 4 * w_chunk + k % 4 * 32), idesc, k != 0);
+            const uint32_t idesc = mma_idesc(v_dim, cols), ob = wb + chunks * w_chunk;
+            for (int c = 0; c < chunks; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16_by(leader, tmem, sw128_desc(wb + c * w_chunk + kk * 32), sw128_desc(ob + c * cols * 128 + kk * 32),
+                                idesc, (c | kk) != 0);
             mma_commit_by(leader, smem_addr(&acc));
         }
         if (warp < 4) {
             if (!warp_wait(&acc, round & 1)) ok = false;
             tc_fence_after();
-            // a 64-row accumulator: row 16 w + i in lane 32 w + i, i < 16; the
-            // remainders' rows (warps 2 and 3) go to the others through `sums`
-            const int i = (warp % 2) * 16 + lane, pitch = v_dim + 4;
-            const bool mine = ok && lane < 16 && i < rows;
-            uint4 *dst = reinterpret_cast<uint4 *>(out + (static_cast<size_t>(r0 + i) * a.Hq + h) * v_dim);
+            // lane = output dimension: 32 w + lane of a 128-row accumulator, 16
+            // w + lane (lane < 16) of a 64-row one; 2-byte stores, 64 bytes a warp
+            const int d = v_dim == 128 ? warp * 32 + lane : warp * 16 + lane;
             const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-            if (warp >= 2)
-                for (int c = 0; c < v_dim; c += 32) {
-                    uint32_t x[32];
-                    tmem_ld32_nowait(tl + c, x);
-                    tmem_wait_ld();
-                    if (mine)
+            for (int i = 0; i < rows; i += 8) {
+                uint32_t x[8], y[8];
+                tmem_ld8_nowait(tl + i, x);
+                tmem_ld8_nowait(tl + cols / 2 + i, y);
+                tmem_wait_ld();
+                if (ok && (v_dim == 128 || lane < 16))
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<uint4 *>(sums + i * pitch + c + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-                }
-            asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-            if (warp < 2)
-                for (int c = 0; c < v_dim; c += 32) {
-                    uint32_t x[32];
-                    tmem_ld32_nowait(tl + c, x);
-                    tmem_wait_ld();
-                    const float *f = reinterpret_cast<const float *>(x);
-                    if (mine)
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            const float4 u = *reinterpret_cast<const float4 *>(sums + i * pitch + c + j);
-                            const float4 w = *reinterpret_cast<const float4 *>(sums + i * pitch + c + j + 4);
-                            dst[(c + j) / 8] = make_uint4(pack_bf16(f[j] + u.x, f[j + 1] + u.y), pack_bf16(f[j + 2] + u.z, f[j + 3] + u.w),
-                                                          pack_bf16(f[j + 4] + w.x, f[j + 5] + w.y),
-                                                          pack_bf16(f[j + 6] + w.z, f[j + 7] + w.w));
-                        }
-                }
+                    for (int k = 0; k < 8; ++k)
+                        if (i + k < rows)
+                            out[(static_cast<size_t>(r0 + i + k) * a.Hq + h) * v_dim + d] =
+                                __float2bfloat16_rn(__uint_as_float(x[k]) + __uint_as_float(y[k]));
+            }
         }
-        // the next rows' A operand and accumulator take the places of these
+        // the next rows' operand and accumulator take the places of these
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
     }
     if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
-    tc_fence_before();
-    __syncthreads();
     if (warp == 0) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 64;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -1139,9 +1152,7 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     // rounds of up to 32 that keep the weights
     const int most = std::max(1, kCtas / Hq), rounds = (R + most * kOutRows - 1) / (most * kOutRows);
     const int per = (R + most * rounds - 1) / (most * rounds), gx = std::min(most, (R + per - 1) / per);
-    // (the sums' region also passes 32 rows of remainders on)
-    const int sums_bytes = std::max(kOutWarps * L * 4, kOutRows * (v_dim + 4) * 4);
-    const int out_smem = L / 64 * (v_dim + kOutTile) * 128 + sums_bytes;
+    const int out_smem = L / 64 * (v_dim + (per + 7) / 8 * 16) * 128 + kOutWarps * 512;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_out_kernel), out_smem)) return TTS_ERR_CUDA;
     return launch_kernel(latent_out_kernel, dim3(gx, Hq), dim3(kOutThreads), out_smem, {cs, true}, map_uv,
                          a, pl.N, per, static_cast<int>(v_dim), static_cast<__nv_bfloat16 *>(d_out));
