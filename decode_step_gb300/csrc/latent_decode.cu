@@ -845,28 +845,28 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 constexpr int kOutThreads = 512, kOutWarps = kOutThreads / 32;
 constexpr int kOutRows = 32;
 
-// Sums kQ x 128 dimensions of one row over the splits s = first, first +
-// stride, .. (`count` in all), kAtOnce of them read together: o is scaled by
-// 2^-M, M the largest of the splits' maxima, and S is the sum of their sums
-// alike.  Every load is issued, past the last split or dimension from the last
-// one (with weight zero, or to no use): a condition would put them in turn.
-template <int kQ, int kAtOnce>
-__device__ __forceinline__ void join_splits(const float *part, size_t part_step, const float2 *ml, size_t ml_step, int first,
-                                            int stride, int count, const int *dims, float4 *o, float &M, float &S) {
-    for (int s0 = first; s0 < count; s0 += kAtOnce * stride) {
+// Joins `count` splits of one row by a warp, two read together: o (4 x 128
+// dimensions) is scaled by 2^-M, M the largest of the splits' maxima, and S is
+// the sum of their sums alike.  Every load is issued, past the last split or
+// dimension from the last one (with weight zero, or to no use): under a
+// condition each would wait for the one before.
+__device__ __forceinline__ void join_row(const float *part, size_t part_step, const float2 *ml, size_t ml_step, int count,
+                                         const int *dims, float4 *o, float &M, float &S) {
+    constexpr int kQ = 4, kAtOnce = 2;
+    for (int s0 = 0; s0 < count; s0 += kAtOnce) {
         float4 x[kAtOnce][kQ];
         float2 v[kAtOnce];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-            const int s = min(s0 + u * stride, count - 1);
-            v[u] = __ldcg(ml + s * ml_step);
+            const int s = min(s0 + u, count - 1);
+            v[u] = __ldcg(ml + static_cast<size_t>(s) * ml_step);
 #pragma unroll
-            for (int k = 0; k < kQ; ++k) x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + s * part_step + dims[k]));
+            for (int k = 0; k < kQ; ++k) x[u][k] = __ldcg(reinterpret_cast<const float4 *>(part + static_cast<size_t>(s) * part_step + dims[k]));
         }
         float top = M;
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-            if (s0 + u * stride >= count) v[u] = make_float2(-INFINITY, 0.0f);
+            if (s0 + u >= count) v[u] = make_float2(-INFINITY, 0.0f);
             top = fmaxf(top, v[u].x);
         }
         const float f0 = hw_ex2(M - top);
@@ -890,6 +890,53 @@ __device__ __forceinline__ void join_splits(const float *part, size_t part_step,
                 o[k].z = fmaf(f, x[u][k].z, o[k].z);
                 o[k].w = fmaf(f, x[u][k].w, o[k].w);
             }
+        }
+    }
+}
+
+// The same for 128 dimensions (`part` is this lane's four) of the splits first,
+// first + stride, .. below `count`, which may be many: 32 at a time, each lane
+// with one split's maximum and sum, sixteen splits' parts in flight.
+__device__ __forceinline__ void join_part(const float *part, size_t part_step, const float2 *ml, size_t ml_step, int first,
+                                          int stride, int count, float4 &o, float &M, float &S) {
+    constexpr int kAtOnce = 16;
+    const int lane = threadIdx.x % 32, mine = first < count ? (count - first + stride - 1) / stride : 0;
+    for (int c0 = 0; c0 < mine; c0 += 32) {
+        const int m = min(32, mine - c0);
+        float4 x[kAtOnce];
+        auto load = [&](int u0) {
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const size_t s = first + (c0 + min(u0 + u, m - 1)) * stride;
+                x[u] = __ldcg(reinterpret_cast<const float4 *>(part + s * part_step));
+            }
+        };
+        float2 v = __ldcg(ml + static_cast<size_t>(first + (c0 + min(lane, m - 1)) * stride) * ml_step);
+        load(0);
+        if (lane >= m) v = make_float2(-INFINITY, 0.0f);
+        float top = fmaxf(M, v.x);
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+        const float f0 = hw_ex2(M - top), f = hw_ex2(v.x - top);
+        float sum = f * v.y;
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(kFull, sum, i);
+        M = top;
+        S = fmaf(S, f0, sum);
+        o.x *= f0;
+        o.y *= f0;
+        o.z *= f0;
+        o.w *= f0;
+        for (int u0 = 0; u0 < m; u0 += kAtOnce) {
+#pragma unroll
+            for (int u = 0; u < kAtOnce; ++u) {
+                const float w = __shfl_sync(kFull, f, u0 + u);
+                o.x = fmaf(w, x[u].x, o.x);
+                o.y = fmaf(w, x[u].y, o.y);
+                o.z = fmaf(w, x[u].z, o.z);
+                o.w = fmaf(w, x[u].w, o.w);
+            }
+            if (u0 + kAtOnce < m) load(u0 + kAtOnce);
         }
     }
 }
@@ -962,8 +1009,8 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
                 const size_t step = static_cast<size_t>(N) * L;
                 float4 o[4] = {};
                 float M = kNoScore, S = 0.0f;
-                if (lshare) join_splits<1, 8>(part, step, ml, N, first, ss, own.y, dims, o, M, S);
-                else join_splits<4, 2>(part, step, ml, N, 0, 1, own.y, dims, o, M, S);
+                if (lshare) join_part(part + dims[0], step, ml, N, first, ss, own.y, o[0], M, S);
+                else join_row(part, step, ml, N, own.y, dims, o, M, S);
                 if (lss == 0) {
                     const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
 #pragma unroll
