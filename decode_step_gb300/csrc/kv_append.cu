@@ -21,7 +21,6 @@
 
 #include <cmath>
 
-#include "rope.cuh"
 #include "tts_common.cuh"
 #include "tts_internal.h"
 
@@ -101,7 +100,28 @@ constexpr int kFp8Tile = 4224;  // bytes of one (block, head) record
 // TensorRT-LLM", folds the KV-cache write and the rotary embedding into the
 // same kernel; so does this one.  For the token at position s, lane l of a
 // warp owns the pairs (i, i + 64) for i = 2l, 2l + 1, whose angles are
-// a = s * theta_i (rope_cos_sin).  The rotation itself is fp32.
+// a = s * theta_i.  The angle is formed in double (the same product the
+// definition takes) and reduced modulo 2 pi in double (Cody and Waite's
+// reduction with 2 pi split into two doubles); the reduced angle r,
+// |r| <= pi, is split into floats r_hi + r_lo, and cos/sin come from
+// sincosf(r_hi) with the first-order correction for r_lo: an error of a few
+// 2^-24 for a handful of double operations per angle (double throughput is
+// low on this part).  The rotation itself is fp32.
+constexpr double kTwoPiHi = 6.283185307179586;       // 2 pi rounded to double
+constexpr double kTwoPiLo = 2.4492935982947064e-16;  // 2 pi - kTwoPiHi
+constexpr double kInvTwoPi = 0.15915494309189535;    // 1 / (2 pi)
+
+__device__ __forceinline__ float2 rope_cos_sin(int s, double theta) {
+    const double a = static_cast<double>(s) * theta;
+    const double k = rint(a * kInvTwoPi);
+    const double r = fma(-k, kTwoPiLo, fma(-k, kTwoPiHi, a));
+    const float rh = static_cast<float>(r);
+    const float rl = static_cast<float>(r - static_cast<double>(rh));
+    float sh, ch;
+    sincosf(rh, &sh, &ch);
+    return make_float2(fmaf(-sh, rl, ch), fmaf(ch, rl, sh));
+}
+
 constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowsAhead = 4;  // rows per warp loaded before the token's position is known

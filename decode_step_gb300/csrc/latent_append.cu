@@ -2,19 +2,20 @@
 // a row being a latent c (copied) and a rotated key part kr, and the same
 // tokens' query parts are rotated at the same positions.
 //
-// One CTA per row.  Its work is a list of 16-byte items: (Hq + 1) x 4 rotary
-// items (8 pairs (i, i + 32) each: 16 bytes of either half; the last head is
-// the key part) and latent_dim / 8 copies.  Pure data movement: the bytes are
-// each row's 2 (latent_dim + 64) + 2 x 64 Hq, read once and written once.
-// A row's first items are loaded before its position is known (they do not
-// depend on it); meanwhile warp 0 finds the stream and the block and computes
-// the 32 angles, shared through shared memory.
+// A row's work is a list of 16-byte items: (Hq + 1) x 4 rotary items (8 pairs
+// (i, i + 32) each: 16 bytes of either half; the last head is the key part) and
+// latent_dim / 8 copies.  Pure data movement: the bytes are each row's 2
+// (latent_dim + 64) + 2 x 64 Hq, read once and written once.
+// A CTA takes one row, or four where there are more rows than CTAs fit at once
+// (a CTA's time is latency: 8409 rows of 16 heads took 14.6 us one by one).
+// The rows' first items are loaded before their positions are known (they do
+// not depend on them); meanwhile a warp per row finds the stream and the block
+// and computes the 32 angles, shared through shared memory.
 #include <cuda_bf16.h>
 
 #include <cmath>
 
 #include "latent_common.cuh"
-#include "rope.cuh"
 #include "tts_common.cuh"
 #include "tts_internal.h"
 
@@ -22,18 +23,36 @@ namespace tts {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 2;  // items per thread loaded before the position is known
+constexpr int kAhead = 2;  // items per thread and row loaded before the position is known
+constexpr int kAtOnce = 152 * 16;  // CTAs of 128 threads that run at once
 constexpr int kHalf = kLatentRope / 2;
 
+// Rotary frequencies base^(-2i/64) in turns a token, scaled by 2^64: a
+// position's angle modulo one turn is then the low half of a 64-bit product,
+// exact but for the frequency's own rounding (2^-53: 2^-32 turns at position
+// 2^20).  Double arithmetic would bound the kernel: this part does two double
+// operations a cycle and SM, and 32 reduced angles a row take some 400.
 struct HalfFreqs {
-    double theta[kHalf];  // base^(-2i/64)
+    uint64_t turns[kHalf];
 };
+
+// cos and sin of s * turns 2 pi: the leading 24 bits by sincospif, the rest to
+// first order (an error of a few 2^-24).
+__device__ __forceinline__ float2 turn_cos_sin(int s, uint64_t turns) {
+    const int64_t a = static_cast<int64_t>(static_cast<uint64_t>(s) * turns);  // [-1/2, 1/2) turn
+    const float hi = __ll2float_rn(a);
+    const float lo = __ll2float_rn(a - __float2ll_rn(hi));
+    float sn, cs;
+    sincospif(hi * 0x1.0p-63f, &sn, &cs);  // (2^-64 turns are 2^-63 half turns)
+    const float d = lo * (6.2831853f * 0x1.0p-64f);
+    return make_float2(fmaf(-sn, d, cs), fmaf(cs, d, sn));
+}
 
 struct LatentAppendArgs {
     const int32_t *table;
     int max_blocks;
     const int32_t *ctx_before;
-    int B;
+    int B, num_rows;
     const int32_t *row_start;  // null: rows_per_stream rows each
     int rows_per_stream;
     int Hq, L, num_blocks;
@@ -44,43 +63,45 @@ struct LatentAppendArgs {
     int32_t *err;
 };
 
+template <int kRows>
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentAppendArgs a, const HalfFreqs freqs) {
-    __shared__ float2 cs[kHalf];
-    __shared__ int where[2];  // block (-1: skip the row), slot
+    __shared__ float2 cs[kRows][kHalf];
+    __shared__ int where[kRows][2];  // block (-1: skip the row), slot
     pdl_wait_prerequisites();
     pdl_allow_dependents();
-    const int row = blockIdx.x;
+    const int row0 = blockIdx.x * kRows;
     const int rope_items = 4 * (a.Hq + 1), items = rope_items + a.L / 8;
-    auto rope_src = [&](int it) -> const uint4 * {
-        const int h = it >> 2;
-        const __nv_bfloat16 *x = h < a.Hq ? a.q + (static_cast<size_t>(row) * a.Hq + h) * kLatentRope
-                                          : a.kr_new + static_cast<size_t>(row) * kLatentRope;
-        return reinterpret_cast<const uint4 *>(x) + (it & 3);
-    };
-    const uint4 *c_src = reinterpret_cast<const uint4 *>(a.c_new + static_cast<size_t>(row) * a.L);
-    auto load = [&](int it, uint4 &lo, uint4 &hi) {
+    auto load = [&](int row, int it, uint4 &lo, uint4 &hi) {
         if (it < rope_items) {
-            const uint4 *x = rope_src(it);
-            lo = x[0];
-            hi = x[4];
+            const int h = it >> 2;
+            const __nv_bfloat16 *x = h < a.Hq ? a.q + (static_cast<size_t>(row) * a.Hq + h) * kLatentRope
+                                              : a.kr_new + static_cast<size_t>(row) * kLatentRope;
+            lo = reinterpret_cast<const uint4 *>(x)[it & 3];
+            hi = reinterpret_cast<const uint4 *>(x)[(it & 3) + 4];
         } else {
-            lo = __ldg(c_src + it - rope_items);
+            lo = __ldg(reinterpret_cast<const uint4 *>(a.c_new + static_cast<size_t>(row) * a.L) + it - rope_items);
         }
     };
-    uint4 lo[kAhead], hi[kAhead];
+    uint4 lo[kRows][kAhead], hi[kRows][kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        if (threadIdx.x + u * kThreads < items) load(threadIdx.x + u * kThreads, lo[u], hi[u]);
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int it = threadIdx.x + u * kThreads;
+            if (it < items && row0 + i < a.num_rows) load(row0 + i, it, lo[i][u], hi[i][u]);
+        }
 
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int b, j;
-        if (a.row_start) {
-            b = stream_of_row(a.row_start, a.B, row, lane);
-            j = b < 0 ? 0 : row - a.row_start[b];
-        } else {
-            b = row / a.rows_per_stream;
-            j = row - b * a.rows_per_stream;
+    if (threadIdx.x < 32 * kRows) {
+        const int i = threadIdx.x / 32, lane = threadIdx.x % 32, row = row0 + i;
+        int b = -1, j = 0;
+        if (row < a.num_rows) {
+            if (a.row_start) {
+                b = stream_of_row(a.row_start, a.B, row, lane);
+                j = b < 0 ? 0 : row - a.row_start[b];
+            } else {
+                b = row / a.rows_per_stream;
+                j = row - b * a.rows_per_stream;
+            }
         }
         int blk = -1, s = 0;
         if (b >= 0) {
@@ -98,49 +119,54 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
             }
         }
         if (lane == 0) {
-            where[0] = blk;
-            where[1] = s % TTS_BLOCK_TOKENS;
+            where[i][0] = blk;
+            where[i][1] = s % TTS_BLOCK_TOKENS;
         }
-        cs[lane] = rope_cos_sin(s, freqs.theta[lane]);
+        cs[i][lane] = turn_cos_sin(s, freqs.turns[lane]);
     }
     __syncthreads();
-    const int blk = where[0];
-    if (blk < 0) return;
-    uint4 *dst = reinterpret_cast<uint4 *>(
-        a.pool + (static_cast<size_t>(blk) * TTS_BLOCK_TOKENS + where[1]) * (a.L + kLatentRope));
 
-    auto emit = [&](int it, const uint4 &vlo, const uint4 &vhi) {
-        if (it >= rope_items) {
-            dst[it - rope_items] = vlo;
-            return;
-        }
-        float x1[8], x2[8];
-        Chunk<__nv_bfloat16>::unpack(vlo, x1);
-        Chunk<__nv_bfloat16>::unpack(vhi, x2);
-        const int p = it & 3;
-        uint32_t o1[4], o2[4];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const float2 c0 = cs[8 * p + e], c1 = cs[8 * p + e + 1];
-            const __nv_bfloat162 r1 = __floats2bfloat162_rn(fmaf(-x2[e], c0.y, x1[e] * c0.x),
-                                                            fmaf(-x2[e + 1], c1.y, x1[e + 1] * c1.x));
-            const __nv_bfloat162 r2 = __floats2bfloat162_rn(fmaf(x1[e], c0.y, x2[e] * c0.x),
-                                                            fmaf(x1[e + 1], c1.y, x2[e + 1] * c1.x));
-            o1[e / 2] = *reinterpret_cast<const uint32_t *>(&r1);
-            o2[e / 2] = *reinterpret_cast<const uint32_t *>(&r2);
-        }
-        const int h = it >> 2;
-        uint4 *o = h < a.Hq ? reinterpret_cast<uint4 *>(a.q_out + (static_cast<size_t>(row) * a.Hq + h) * kLatentRope)
-                            : dst + a.L / 8;
-        o[p] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-        o[p + 4] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-    };
+    for (int i = 0; i < kRows; ++i) {
+        const int blk = where[i][0], row = row0 + i;
+        if (blk < 0) continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(
+            a.pool + (static_cast<size_t>(blk) * TTS_BLOCK_TOKENS + where[i][1]) * (a.L + kLatentRope));
+        auto emit = [&](int it, const uint4 &vlo, const uint4 &vhi) {
+            if (it >= rope_items) {
+                dst[it - rope_items] = vlo;
+                return;
+            }
+            float x1[8], x2[8];
+            Chunk<__nv_bfloat16>::unpack(vlo, x1);
+            Chunk<__nv_bfloat16>::unpack(vhi, x2);
+            const int p = it & 3;
+            uint32_t o1[4], o2[4];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-        if (threadIdx.x + u * kThreads < items) emit(threadIdx.x + u * kThreads, lo[u], hi[u]);
-    for (int it = threadIdx.x + kAhead * kThreads; it < items; it += kThreads) {
-        load(it, lo[0], hi[0]);
-        emit(it, lo[0], hi[0]);
+            for (int e = 0; e < 8; e += 2) {
+                const float2 c0 = cs[i][8 * p + e], c1 = cs[i][8 * p + e + 1];
+                const __nv_bfloat162 r1 = __floats2bfloat162_rn(fmaf(-x2[e], c0.y, x1[e] * c0.x),
+                                                                fmaf(-x2[e + 1], c1.y, x1[e + 1] * c1.x));
+                const __nv_bfloat162 r2 = __floats2bfloat162_rn(fmaf(x1[e], c0.y, x2[e] * c0.x),
+                                                                fmaf(x1[e + 1], c1.y, x2[e + 1] * c1.x));
+                o1[e / 2] = *reinterpret_cast<const uint32_t *>(&r1);
+                o2[e / 2] = *reinterpret_cast<const uint32_t *>(&r2);
+            }
+            const int h = it >> 2;
+            uint4 *o = h < a.Hq
+                           ? reinterpret_cast<uint4 *>(a.q_out + (static_cast<size_t>(row) * a.Hq + h) * kLatentRope)
+                           : dst + a.L / 8;
+            o[p] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            o[p + 4] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+        };
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (threadIdx.x + u * kThreads < items) emit(threadIdx.x + u * kThreads, lo[i][u], hi[i][u]);
+        for (int it = threadIdx.x + kAhead * kThreads; it < items; it += kThreads) {
+            uint4 vlo, vhi;
+            load(row, it, vlo, vhi);
+            emit(it, vlo, vhi);
+        }
     }
 }
 
@@ -169,6 +195,7 @@ extern "C" int tts_latent_append(const tts_latent_cache *cache, const int32_t *d
     a.max_blocks = max_blocks_per_seq;
     a.ctx_before = d_ctx_before;
     a.B = B;
+    a.num_rows = num_rows;
     a.row_start = d_row_start;
     a.rows_per_stream = num_rows / B;
     a.Hq = num_q_heads;
@@ -181,7 +208,12 @@ extern "C" int tts_latent_append(const tts_latent_cache *cache, const int32_t *d
     a.pool = static_cast<__nv_bfloat16 *>(cache->pool);
     a.err = d_err;
     HalfFreqs f;
-    for (int i = 0; i < kHalf; ++i) f.theta[i] = pow(static_cast<double>(rope_base), -2.0 * i / kLatentRope);
-    return launch_kernel(latent_append_kernel, dim3(num_rows), dim3(kThreads), 0,
-                         {static_cast<cudaStream_t>(stream), thread_pdl()}, a, f);
+    for (int i = 0; i < kHalf; ++i) {
+        const double turns = pow(static_cast<double>(rope_base), -2.0 * i / kLatentRope) * 0.15915494309189535;  // 1 / (2 pi)
+        f.turns[i] = static_cast<uint64_t>(turns * 0x1.0p64);
+    }
+    const LaunchOpts o{static_cast<cudaStream_t>(stream), thread_pdl()};
+    if (num_rows > kAtOnce)
+        return launch_kernel(latent_append_kernel<4>, dim3((num_rows + 3) / 4), dim3(kThreads), 0, o, a, f);
+    return launch_kernel(latent_append_kernel<1>, dim3(num_rows), dim3(kThreads), 0, o, a, f);
 }

@@ -27,6 +27,14 @@ inline int check_latent_cache(const tts_latent_cache *cache, const int32_t *d_bl
 
 inline bool latent_head_dim_ok(int d) { return d == 64 || d == 128; }
 
+// Dynamic shared memory of a kernel that has static shared memory too: the two
+// together pass the 48 KB that need no leave before the dynamic part does.
+template <typename... P>
+inline bool allow_smem(void (*kernel)(P...), int bytes) {
+    constexpr int kNoLeave = 48 * 1024;
+    return ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes > kNoLeave ? bytes : kNoLeave + 16);
+}
+
 // Launches a kernel, as a programmatic dependent of the one before it if
 // o.pdl, in clusters of `cluster` CTAs.
 template <typename... P, typename... A>

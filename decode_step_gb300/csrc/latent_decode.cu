@@ -203,17 +203,15 @@ struct LatentAttnArgs {
     int pairs, ropes;  // ring slots
 };
 
-// Tiles of stream b (0: its length is out of range).
-__device__ __forceinline__ int stream_tiles(const LatentAttnArgs &a, int b, int *ctx_out = nullptr) {
-    const int ctx = __ldg(a.ctx_lens + b);
-    if (ctx_out) *ctx_out = ctx;
+// Tiles of a stream of `ctx` tokens (0: out of range).
+__device__ __forceinline__ int stream_tiles(const LatentAttnArgs &a, int ctx) {
     if (ctx < a.q_len || ctx > a.max_ctx || ctx > a.max_blocks * TTS_BLOCK_TOKENS) return 0;
     return (ctx + kTile - 1) / kTile;
 }
 
 // Units of one of stream b's groups (0: its length is out of range).
 __device__ __forceinline__ int group_units(const LatentAttnArgs &a, int b) {
-    const int n = stream_tiles(a, b);
+    const int n = stream_tiles(a, __ldg(a.ctx_lens + b));
     return n ? n + 1 : 0;
 }
 
@@ -251,19 +249,23 @@ __device__ __forceinline__ StreamScan scan_streams(const LatentAttnArgs &a, int 
     return s;
 }
 
-// Walks a CTA's segments; every warp keeps its own copy.
+// Walks a CTA's segments; every warp keeps its own copy.  The length of the
+// next stream is read a segment ahead (a read takes as long as half a tile).
 struct Segments {
     int b, g, unit;        // next unit (0: the group's first, then its tiles)
     int left;              // units left
+    int ahead;             // ctx_lens[b]
     // current segment
     int cur_b, cur_g, bg;
     int ctx, first, count; // first tile, tiles
+    __device__ __forceinline__ void look(const LatentAttnArgs &a) { ahead = b < a.B ? __ldg(a.ctx_lens + b) : 0; }
     __device__ __forceinline__ bool next(const LatentAttnArgs &a) {
         while (left > 0) {
-            const int n = uniform(stream_tiles(a, b, &ctx));
-            ctx = uniform(ctx);
+            ctx = uniform(ahead);
+            const int n = stream_tiles(a, ctx);
             if (n == 0) {  // (never the CTA's first stream)
                 ++b;
+                look(a);
                 continue;
             }
             const int units = min(n + 1 - unit, left);
@@ -277,6 +279,7 @@ struct Segments {
             if (++g == a.G) {
                 g = 0;
                 ++b;
+                look(a);
             }
             if (count > 0) return true;
         }
@@ -430,6 +433,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
     seg.b = uniform(sh.start_b);
     seg.g = uniform(sh.start_g);
     seg.unit = uniform(sh.start_unit);
+    if (seg.left > 0) seg.look(a);
     pdl_allow_dependents();
     bool ok = true;
 
@@ -441,22 +445,27 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         const int oob = a.num_blocks * TTS_BLOCK_TOKENS;
         Ring rope(a.ropes), lat(a.pairs);
         uint32_t it = 0, lpos = 0;
-        while (ok && seg.next(a)) {
-            const int32_t *row = a.table + static_cast<size_t>(seg.cur_b) * a.max_blocks;
-            const int blocks = (seg.ctx + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS;
-            auto fetch = [&](int tile) {
-                const int i = tile * 4 + (lane & 3);
-                return i < blocks ? row[i] : -1;
-            };
-            int id = fetch(seg.first);
-            for (int k = 0; ok && k < seg.count; ++k) {
-                const int tile = seg.first + k;
+        auto fetch = [&](const Segments &s, int tile) {  // lanes 0-3 (and so on): the tile's block ids
+            const int i = tile * 4 + (lane & 3);
+            return i * TTS_BLOCK_TOKENS < s.ctx ? a.table[static_cast<size_t>(s.cur_b) * a.max_blocks + i] : -1;
+        };
+        bool more = seg.next(a);
+        int id = more ? fetch(seg, seg.first) : 0;
+        while (ok && more) {
+            const Segments cur = seg;
+            for (int k = 0; ok && k < cur.count; ++k) {
+                const int tile = cur.first + k;
                 int y = oob;
-                if (tile * 4 + (lane & 3) < blocks) {
+                if ((tile * 4 + (lane & 3)) * TTS_BLOCK_TOKENS < cur.ctx) {
                     if (id >= 0 && id < a.num_blocks) y = id * TTS_BLOCK_TOKENS;
                     else flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
                 }
-                if (k + 1 < seg.count) id = fetch(tile + 1);
+                if (k + 1 < cur.count) {
+                    id = fetch(cur, tile + 1);
+                } else {
+                    more = seg.next(a);
+                    if (more) id = fetch(seg, seg.first);
+                }
                 int ys[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ys[i] = __shfl_sync(kFull, y, i);
@@ -654,15 +663,14 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             pat[i] = p_base + (c2 + i % 2) * 128 + (((2 * warp + i / 2) ^ (c2 + i % 2)) << 4) + g * 2;
         auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1); };
         const int tid = threadIdx.x;
-        while (ok && seg.next(a)) {
-            const int32_t *row = a.table + static_cast<size_t>(seg.cur_b) * a.max_blocks;
-            const int blocks = (seg.ctx + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS;
-            auto block_ok = [&](int tile) {
-                const int i = tile * 4 + warp;
-                if (i >= blocks) return false;
-                const int id = row[i];
-                return id >= 0 && id < a.num_blocks;
-            };
+        auto block_ok = [&](const Segments &s, int tile) {
+            const int i = tile * 4 + warp;
+            if (i * TTS_BLOCK_TOKENS >= s.ctx) return false;
+            const int id = a.table[static_cast<size_t>(s.cur_b) * a.max_blocks + i];
+            return id >= 0 && id < a.num_blocks;
+        };
+        bool more = seg.next(a), valid = more && block_ok(seg, seg.first);
+        while (ok && more) {
             const int low = a.causal ? seg.ctx - a.q_len + 1 : seg.ctx;  // tokens every row sees
             softmax_sync();  // the last segment's reads of these are over
             if (tid < N) {
@@ -674,11 +682,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             float l[N / 4];  // of columns col(4 j) and col(4 j + 1)
 #pragma unroll
             for (int n = 0; n < N / 4; ++n) l[n] = 0.0f;
-            bool valid = block_ok(seg.first);
             for (int k = 0; k < seg.count; ++k, ++it) {
                 const int tile = seg.first + k;
                 const uint32_t buf = it & 1;
-                const bool next_valid = k + 1 < seg.count && block_ok(tile + 1);
+                const bool next_valid = k + 1 < seg.count && block_ok(seg, tile + 1);
                 // (the tile that last used this P buffer has had its O^T added)
                 if (it >= kPBufs && kPBufs > 1 && !o_added(it - kPBufs)) ok = false;
                 float mr[N / 4];
@@ -780,7 +787,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[it % kPBufs]));
                 valid = next_valid;
             }
-            // ---- the segment's partial result
+            // ---- the segment's partial result; the next one is looked up meanwhile
+            const int bg = seg.bg;
+            more = seg.next(a);
+            valid = more && block_ok(seg, seg.first);
             if (!o_added(it - 1)) ok = false;
             if (softmax_any(!ok)) {  // (all four warps leave together)
                 ok = false;
@@ -793,7 +803,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 for (int o = 4; o < 32; o *= 2) s += __shfl_xor_sync(kFull, s, o);
                 if (g == 0) sh.lsum[warp][col(j / 2 * 4 + j % 2)] = s;
             }
-            const size_t slot = static_cast<size_t>(blockIdx.x) + seg.bg;
+            const size_t slot = static_cast<size_t>(blockIdx.x) + bg;
             softmax_sync();
             if (tid < N)
                 a.ml[slot * N + tid] = make_float2(
@@ -1114,7 +1124,7 @@ int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, const CUtensor
     a.pairs = std::min((kSmemLimit - fixed - a.ropes * kChunkBytes) / kPairBytes, kMaxPairs);
     if (a.pairs < 2 * nb) return TTS_ERR_UNSUPPORTED;  // (S^T goes one tile ahead of O^T)
     const int smem = fixed + a.ropes * kChunkBytes + a.pairs * kPairBytes;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_attn_kernel<N>), smem)) return TTS_ERR_CUDA;
+    if (!allow_smem(latent_attn_kernel<N>, smem)) return TTS_ERR_CUDA;
     return launch_kernel(latent_attn_kernel<N>, dim3(P), dim3(kAttnThreads), smem, {stream, true}, kv, q, qr, a);
 }
 
@@ -1183,7 +1193,7 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int absorb_smem = 2 * nope_dim * 128 + nope_dim / 64 * kRowTile * 128;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_absorb_kernel), absorb_smem)) return TTS_ERR_CUDA;
+    if (!allow_smem(latent_absorb_kernel, absorb_smem)) return TTS_ERR_CUDA;
     int rc = launch_kernel(latent_absorb_kernel, dim3((L + 127) / 128, Hq, (R + kRowTile - 1) / kRowTile), dim3(128),
                            absorb_smem, {cs, thread_pdl()}, map_qn, map_uk, map_qt, static_cast<int>(nope_dim), L, R,
                            d_err);
@@ -1200,7 +1210,7 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     const int most = std::max(1, kCtas / Hq), rounds = (R + most * kOutRows - 1) / (most * kOutRows);
     const int per = (R + most * rounds - 1) / (most * rounds), gx = std::min(most, (R + per - 1) / per);
     const int out_smem = L / 64 * (v_dim + (per + 7) / 8 * 16) * 128 + kOutWarps * 512;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_out_kernel), out_smem)) return TTS_ERR_CUDA;
+    if (!allow_smem(latent_out_kernel, out_smem)) return TTS_ERR_CUDA;
     return launch_kernel(latent_out_kernel, dim3(gx, Hq), dim3(kOutThreads), out_smem, {cs, true}, map_uv,
                          a, pl.N, per, static_cast<int>(v_dim), static_cast<__nv_bfloat16 *>(d_out));
 }

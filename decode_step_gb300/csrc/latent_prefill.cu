@@ -731,7 +731,7 @@ template <int kNope, int kV>
 int launch_prefill(const CUtensorMap *m, const PrefillArgs &a, unsigned grid, cudaStream_t stream) {
     constexpr int kSmem = (2 * (kNope / 64 + 1) + kSlots) * kChunkBytes + static_cast<int>(sizeof(PrefillShared));
     auto kernel = latent_prefill_kernel<kNope, kV>;
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), kSmem)) return TTS_ERR_CUDA;
+    if (!allow_smem(kernel, kSmem)) return TTS_ERR_CUDA;
     return launch_kernel(kernel, dim3(grid), dim3(kAttnThreads), kSmem, {stream, true}, m[0], m[1], m[2], m[3], m[4], a);
 }
 
@@ -809,7 +809,7 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int k_tiles = static_cast<int>((fk + kFeatures - 1) / kFeatures);
     const int v_tiles = static_cast<int>((fv + kFeatures - 1) / kFeatures);
-    if (!ensure_dynamic_smem(reinterpret_cast<const void *>(latent_expand_kernel), kExpandSmem)) return TTS_ERR_CUDA;
+    if (!allow_smem(latent_expand_kernel, kExpandSmem)) return TTS_ERR_CUDA;
     const int rc = launch_cluster(2, latent_expand_kernel, dim3(kExpandCtas), dim3(kExpandThreads), kExpandSmem,
                                   {cs, thread_pdl()}, pool, uk, uv, qkv[2], qkv[4], a, k_tiles, v_tiles);
     if (rc != TTS_OK) return rc;

@@ -4,6 +4,9 @@ can go wrong.  Tolerances are those derived in latent_ref."""
 from __future__ import annotations
 
 import math
+import subprocess
+import sys
+from pathlib import Path
 
 import pytest
 import torch
@@ -12,6 +15,7 @@ import latent_ref as ref
 
 pytestmark = pytest.mark.gpu
 
+ROOT = Path(__file__).resolve().parents[1]
 NAN = float("nan")
 CTX_LEN, BLOCK_ID = 2, 1        # error bits
 
@@ -599,6 +603,22 @@ def test_a_stream_from_prompt_to_tokens(bd):
         want, tol = ref.attend_all(t, True, step != 0)
         check(out, want, tol, f"step {step}")
         lens = t["ctx"]
+
+
+@pytest.mark.parametrize("op", ["decode", "prefill"])
+@pytest.mark.parametrize("L,nope,v", [(64, 64, 64), (128, 64, 128), (256, 64, 64), (512, 128, 128)])
+def test_first_call_of_a_process(op, L, nope, v):
+    """A shape's launch does not rest on what another shape's set up before."""
+    code = f"""
+import sys; sys.path[:0] = {[str(ROOT), str(ROOT / "tests")]!r}
+import torch, latent_ref as ref, test_gpu_latent as t
+from decode_step_gb300 import binding as bd
+s = ref.make([5], [20], 4, {L}, {nope}, {v}, 5)
+out = t.run_decode(bd, s, t.up(s), 5, True) if {op == "decode"} else t.run_prefill(bd, s, t.up(s))
+want, tol = ref.attend_all(s, True, {op == "decode"})
+t.check(out.view(5, 4, {v}), want, tol)
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
 
 
 def test_tensor_checks(bd):
