@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "latent_common.cuh"
 #include "tcgen05.cuh"
@@ -445,11 +446,12 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
 
 // --------------------------------------------------------------- attention
 
-constexpr int kSlots = 8;           // ring slots of [128 tokens][64 values]
+constexpr int kSlots = 8;           // ring slots of [128 tokens][64 values]: 1.6 tiles of keys and values
+constexpr int kTiles = 4;           // barriers for the keys, and the values, of as many tiles
 constexpr int kAttnThreads = 320;   // two softmax warpgroups, producer, MMA issuer
 
 struct PrefillShared {
-    uint64_t full[kSlots], empty[kSlots], q_full[2], s_full[2], p_full[2], o_done[2], done;
+    uint64_t k_full[kTiles], k_done[kTiles], v_full[kTiles], v_done[kTiles], q_full[2], s_full[2], p_full[2], o_done[2], done;
     uint32_t tmem;
 };
 
@@ -466,9 +468,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
     PrefillShared &sh = *reinterpret_cast<PrefillShared *>(raw + (2 * kQc + kSlots) * kChunkBytes);
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     if (warp == 9 && lane == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), 1);
+        for (int i = 0; i < kTiles; ++i) {
+            mbar_init(smem_addr(&sh.k_full[i]), 1);
+            mbar_init(smem_addr(&sh.k_done[i]), 1);
+            mbar_init(smem_addr(&sh.v_full[i]), 1);
+            mbar_init(smem_addr(&sh.v_done[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.q_full[i]), 1);
@@ -514,90 +518,108 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                         tma_load_2d(at + c * kChunkBytes, &map_qn, h * kNope + c * 64, first + r0 + s * kTile, bar);
                     tma_load_2d(at + (kQc - 1) * kChunkBytes, &map_qr, h * kLatentRope, first + r0 + s * kTile, bar);
                 }
+                // a slot is free once the keys or values that it held are done with
                 uint32_t pos = 0;
-                for (int j = 0; ok && j < nt; ++j) {
+                auto slot_free = [&]() {
+                    if (pos < kSlots) return true;
+                    const uint32_t j = (pos - kSlots) / (kQc + kVc), c = (pos - kSlots) % (kQc + kVc);
+                    return mbar_wait(smem_addr((c < kQc ? sh.k_done : sh.v_done) + j % kTiles), (j / kTiles) & 1);
+                };
+                int j = 0;
+                for (; ok && j < nt; ++j) {
                     const int y = (tile0 + j) * kTile;
-                    for (int c = 0; c < kQc + kVc; ++c, ++pos) {
-                        const uint32_t s = pos % kSlots;
-                        if (pos >= kSlots && !mbar_wait(smem_addr(&sh.empty[s]), (pos / kSlots - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t bar = smem_addr(&sh.full[s]), at = ring + s * kChunkBytes;
-                        mbar_arrive_expect_tx(bar, kChunkBytes);
+                    for (int c = 0; ok && c < kQc + kVc; ++c, ++pos) {
+                        const uint32_t bar = smem_addr((c < kQc ? sh.k_full : sh.v_full) + j % kTiles);
+                        if (c == 0 || c == kQc) mbar_arrive_expect_tx(bar, (c ? kVc : kQc) * kChunkBytes);
+                        ok = slot_free();
+                        const uint32_t at = ring + pos % kSlots * kChunkBytes;
+                        if (!ok) break;
                         if (c < kQc - 1) tma_load_2d(at, &map_k, h * kNope + c * 64, y, bar);
                         else if (c == kQc - 1) tma_load_2d(at, &map_kr, 0, y, bar);
                         else tma_load_2d(at, &map_v, h * kV + (c - kQc) * 64, y, bar);
                     }
                 }
-                for (uint32_t i = pos > kSlots ? pos - kSlots : 0; i < pos; ++i)
-                    mbar_wait(smem_addr(&sh.full[i % kSlots]), (i / kSlots) & 1);
+                for (int i = max(0, j - 2); i < j; ++i) {
+                    mbar_wait(smem_addr(&sh.k_full[i % kTiles]), (i / kTiles) & 1);
+                    mbar_wait(smem_addr(&sh.v_full[i % kTiles]), (i / kTiles) & 1);
+                }
                 for (int s = 0; s < (two ? 2 : 1); ++s) mbar_wait(smem_addr(&sh.q_full[s]), 0);
             }
         } else if (warp == 9) {
-            // ---- MMA issuer: S0(0) S1(0) | O0(j) S0(j+1) O1(j) S1(j+1) ...
+            // ---- MMA issuer: S0(0) S1(0) | O0(j) S0(j+1) | O1(j) S1(j+1) ...
             // S of a half is overwritten right after the O product that reads
             // the weights kept in it; the tensor core runs them in order.
+            // Barriers are by tile: a wait or commit takes the issuing warp about
+            // 0.1 us.
             const uint32_t leader = elect_leader();
             bool go = true;
-            auto scores = [&](int s, int j, bool last_use) {
+            auto scores = [&](auto half, int j) {
+                constexpr int s = decltype(half)::value;
                 const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc);
-                WarpWaits<kQc + 1> w;
-#pragma unroll
-                for (int c = 0; c < kQc; ++c) w.set(c, &sh.full[(pos + c) % kSlots], ((pos + c) / kSlots) & 1);
-                w.set(kQc, &sh.q_full[s], 0);
-                if (!w.wait()) {
-                    go = false;
-                    return;
-                }
-                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kQc; ++c) {
-                    const uint32_t slot = (pos + c) % kSlots;
-                    const uint32_t sa = q_base + (s * kQc + c) * kChunkBytes, sb = ring + slot * kChunkBytes;
+                    const uint32_t sa = q_base + (s * kQc + c) * kChunkBytes, sb = ring + (pos + c) % kSlots * kChunkBytes;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_bf16_by(leader, tmem + s * kTile, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
                                     mma_idesc(kTile, kTile), (c | kk) != 0);
-                    if (last_use) mma_commit_by(leader, smem_addr(&sh.empty[slot]));
                 }
                 mma_commit_by(leader, smem_addr(&sh.s_full[s]));
             };
-            auto output = [&](int s, int j, bool last_use) {
+            auto output = [&](auto half, int j) {
+                constexpr int s = decltype(half)::value;
                 const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc) + kQc;
-                WarpWaits<kVc + 1> w;
-#pragma unroll
-                for (int c = 0; c < kVc; ++c) w.set(c, &sh.full[(pos + c) % kSlots], ((pos + c) / kSlots) & 1);
-                w.set(kVc, &sh.p_full[s], j & 1);
-                if (!w.wait()) {
-                    go = false;
-                    return;
-                }
-                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < kVc; ++c) {
-                    const uint32_t slot = (pos + c) % kSlots, sb = ring + slot * kChunkBytes;
+                    const uint32_t sb = ring + (pos + c) % kSlots * kChunkBytes;
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         mma_ts_by(leader, tmem + (2 + s) * kTile + c * 64, tmem + s * kTile + kk * 8,
-                                       sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc_f16(kTile, 64) | kTransposeB,
-                                       (j | kk) != 0);
-                    if (last_use) mma_commit_by(leader, smem_addr(&sh.empty[slot]));
+                                  sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc_f16(kTile, 64) | kTransposeB,
+                                  (j | kk) != 0);
                 }
             };
-            scores(0, 0, !two);
-            if (go && two) scores(1, 0, true);
+            constexpr std::integral_constant<int, 0> h0{};
+            constexpr std::integral_constant<int, 1> h1{};
+            {
+                WarpWaits<3> w;
+                w.set(0, &sh.k_full[0], 0);
+                w.set(1, &sh.q_full[0], 0);
+                w.none(2);
+                if (two) w.set(2, &sh.q_full[1], 0);
+                go = w.wait();
+                tc_fence_after();
+                if (go) {
+                    scores(h0, 0);
+                    if (two) scores(h1, 0);
+                    mma_commit_by(leader, smem_addr(&sh.k_done[0]));
+                }
+            }
             for (int j = 0; go && j < nt; ++j) {
-                if (j < nt0) {
-                    output(0, j, !two);
-                    if (go && j + 1 < nt0) scores(0, j + 1, !two);
-                    if (go && j + 1 == nt0) mma_commit_by(leader, smem_addr(&sh.o_done[0]));
-                }
-                if (go && two) {
-                    output(1, j, true);
-                    if (go && j + 1 < nt1) scores(1, j + 1, true);
-                    if (go && j + 1 == nt1) mma_commit_by(leader, smem_addr(&sh.o_done[1]));
-                }
+                // (a half beyond its last tile is passed over; the first half ends first)
+                auto turn = [&](auto half, int mine) {
+                    constexpr int s = decltype(half)::value;
+                    const bool last = s == 1 || !two;  // to use this tile's values and the next one's keys
+                    WarpWaits<2> w;
+                    w.set(0, &sh.p_full[s], j & 1);
+                    w.set(1, &sh.v_full[j % kTiles], (j / kTiles) & 1);
+                    go = w.wait();
+                    if (!go) return;
+                    tc_fence_after();
+                    output(half, j);
+                    if (last) mma_commit_by(leader, smem_addr(&sh.v_done[j % kTiles]));
+                    if (j + 1 < mine) {
+                        go = warp_wait(&sh.k_full[(j + 1) % kTiles], ((j + 1) / kTiles) & 1);
+                        if (!go) return;
+                        tc_fence_after();
+                        scores(half, j + 1);
+                        if (last) mma_commit_by(leader, smem_addr(&sh.k_done[(j + 1) % kTiles]));
+                    } else {
+                        mma_commit_by(leader, smem_addr(&sh.o_done[s]));
+                    }
+                };
+                if (j < nt0) turn(h0, nt0);
+                if (go && two) turn(h1, nt1);
             }
             mma_commit_by(leader, smem_addr(&sh.done));
             ok = warp_wait(&sh.done, 0) && go;
