@@ -1156,7 +1156,9 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
         return TTS_ERR_INVALID;
     if (B == 0) return TTS_OK;
     const LatentPlan pl = latent_plan(B, q_len, num_q_heads, L, max_ctx_len);
-    if (pl.units > 0x40000000L) return TTS_ERR_UNSUPPORTED;  // units are 32-bit
+    // units are 32-bit (contexts end at the table's last block)
+    const int most_ctx = std::min(max_ctx_len, max_blocks_per_seq * TTS_BLOCK_TOKENS);
+    if (latent_plan(B, q_len, num_q_heads, L, most_ctx).units > 0x40000000L) return TTS_ERR_UNSUPPORTED;
     if (!d_ws || !aligned16(d_ws) || ws_bytes < pl.total()) return TTS_ERR_WORKSPACE;
 
     uint8_t *ws = static_cast<uint8_t *>(d_ws);

@@ -6,6 +6,10 @@ launched as programmatic dependents) on one stream.  The attention output
 [B][q_len][Hq][D] is read by the head as h [B * q_len][Hq * D], so Hq * D must
 equal the head's hidden width.
 
+`LatentStep` does the same over a latent cache (tts_latent_append,
+tts_latent_decode_attn, tts_codebook_head_select), and appends and attends over
+whole prompts.
+
 `GraphedStep` wraps tts_step_graph: a whole serving step captured once by the
 library for fixed buffers (the copy of the step's inputs from pinned host
 memory, the decode step, the chosen ids and a boundary-token count back to
@@ -18,6 +22,7 @@ import math
 
 import torch
 
+from . import _lib
 from . import binding as bd
 
 
@@ -56,6 +61,84 @@ class DecodeStep:
                            causal=self.causal, mode=self.mode, temperature=self.temperature,
                            seed=seed, step=step, eos_allowed=eos_allowed, best=best,
                            logits_out=logits_out, err=self.err, stream=stream, rope_base=self.rope_base)
+        return self.ids
+
+
+class LatentStep:
+    """A batch's steps over a latent cache, for fixed shapes: `prompt` appends
+    whole prompts and attends over them, calling the object appends q_len
+    tokens a stream, attends (absorbed form) and picks codec tokens.
+
+    w_uk [Hq][nope_dim][latent_dim], w_uv [Hq][v_dim][latent_dim] and the head's
+    W [V][Hq * v_dim] are bf16; the object owns the workspaces and outputs
+    (`out` [B][q_len][Hq][v_dim], `ids` [B * q_len]).  Key and query rotary
+    parts are passed unrotated.  prompt_rows and prompt_ctx bound a prompt
+    call's rows and the sum of its streams' context lengths (0: no prompts).
+    """
+
+    def __init__(self, cache: bd.LatentCache, w_uk: torch.Tensor, w_uv: torch.Tensor, W: torch.Tensor, B: int,
+                 max_ctx_len: int, q_len: int = 1, causal: bool = False, mode: int = bd.TTS_ARGMAX,
+                 temperature: float = 0.0, scale: float | None = None, rope_base: float = 10000.0,
+                 prompt_rows: int = 0, prompt_ctx: int = 0):
+        dev = cache.pool.device
+        Hq, nope, L = w_uk.shape
+        v = w_uv.shape[1]
+        if L != cache.latent_dim:
+            raise ValueError(f"w_uk's latent width {L} != the cache's {cache.latent_dim}")
+        if W.shape[1] != Hq * v:
+            raise ValueError(f"head width {W.shape[1]} != num_q_heads * v_dim = {Hq * v}")
+        self.cache, self.w_uk, self.w_uv, self.W = cache, w_uk, w_uv, W
+        self.B, self.q_len, self.Hq, self.max_ctx_len, self.causal = B, q_len, Hq, max_ctx_len, causal
+        self.mode, self.temperature, self.rope_base = mode, temperature, rope_base
+        self.scale = 1.0 / math.sqrt(nope + cache.ROPE_DIM) if scale is None else scale
+        self.R, self.V, self.v = B * q_len, W.shape[0], v
+        ws = bd.tts_latent_decode_attn_workspace_size(B, q_len, Hq, L, nope, v, max_ctx_len)
+        head_ws = bd.tts_head_workspace_size(self.R, self.V)
+        prompt_ws = bd.tts_latent_prefill_attn_workspace_size(B, prompt_rows, Hq, L, nope, v, prompt_ctx)
+        if ws == 0 or head_ws == 0 or prompt_ws == 0:
+            raise ValueError("unsupported latent-step shape")
+        self.ws = torch.empty(max(ws, prompt_ws if prompt_rows else 0), dtype=torch.uint8, device=dev)
+        self.head_ws = torch.zeros(head_ws, dtype=torch.uint8, device=dev)
+        self.q = torch.empty((max(self.R, prompt_rows), Hq, cache.ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        self.out = torch.empty((B, q_len, Hq, v), dtype=torch.bfloat16, device=dev)
+        self.ids = torch.empty(self.R, dtype=torch.int32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.prompt_rows, self.prompt_ctx = prompt_rows, prompt_ctx
+
+    def prompt(self, block_table, ctx_before, ctx_lens, row_start, q_nope, q_rope, c_new, kr_new, out=None,
+               stream=None) -> torch.Tensor:
+        """Appends the packed rows of up to B streams (stream b: rows
+        row_start[b]..row_start[b + 1] - 1 at positions ctx_before[b]..) and
+        attends causally; returns the attention output [rows][Hq][v_dim]."""
+        T = c_new.shape[0]
+        if T > self.prompt_rows:
+            raise ValueError(f"{T} prompt rows exceed prompt_rows = {self.prompt_rows}")
+        out = torch.empty((T, self.Hq, self.v), dtype=torch.bfloat16, device=self.out.device) if out is None else out
+        q = self.q[:T]
+        bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope, q, self.rope_base,
+                             row_start=row_start, err=self.err, stream=stream)
+        bd.tts_latent_prefill_attn(self.cache, block_table, ctx_lens, self.prompt_ctx, row_start, q_nope, q, self.w_uk,
+                                   self.w_uv, out, self.ws, self.scale, err=self.err, stream=stream)
+        return out
+
+    def __call__(self, block_table, ctx_before, ctx_lens, q_nope, q_rope, c_new, kr_new, seed=None, step=None,
+                 eos_allowed=None, logits_out=None, best=None, stream=None) -> torch.Tensor:
+        """One step: q_nope [B][q_len][Hq][nope_dim], q_rope [B][q_len][Hq][64],
+        c_new [B * q_len][latent_dim], kr_new [B * q_len][64]; returns the
+        device tensor of chosen ids [B * q_len]."""
+        q = self.q[:self.R]
+        bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope.view(self.R, self.Hq, -1), q,
+                             self.rope_base, err=self.err, stream=stream)
+        # the later kernels start while the ones before them finish
+        flags = bd.tts_set_launch_flags(_lib.LAUNCH_PROGRAMMATIC)
+        try:
+            bd.tts_latent_decode_attn(self.cache, block_table, ctx_lens, self.max_ctx_len, q_nope,
+                                      q.view(self.B, self.q_len, self.Hq, -1), self.w_uk, self.w_uv, self.out, self.ws,
+                                      self.scale, causal=self.causal, err=self.err, stream=stream)
+            bd.tts_codebook_head_select(self.out.view(self.R, -1), self.W, self.ids, self.head_ws, self.mode,
+                                        self.temperature, seed, step, eos_allowed, best, logits_out, stream)
+        finally:
+            bd.tts_set_launch_flags(flags)
         return self.ids
 
 

@@ -305,7 +305,10 @@ size_t tts_latent_decode_attn_workspace_size(int32_t B, int32_t q_len, int32_t n
  * addresses 16-byte aligned.  A stream whose context length is outside
  * [q_len, min(max_ctx_len, 16 * max_blocks_per_seq)] gets zeros
  * (TTS_ERRBIT_CTX_LEN); tokens in blocks with an invalid id are left out
- * (TTS_ERRBIT_BLOCK_ID), and a row left without tokens gets zeros. */
+ * (TTS_ERRBIT_BLOCK_ID), and a row left without tokens gets zeros.
+ * TTS_ERRBIT_TIMEOUT: a bounded wait ran out, the outputs are undefined.
+ * B * ceil(q_len * Hq / 64) streams' worth of row groups times their 64-token
+ * tiles must stay below 2^30 (TTS_ERR_UNSUPPORTED). */
 int tts_latent_decode_attn(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                            const int32_t *d_ctx_lens, int32_t max_ctx_len, int32_t B, int32_t q_len,
                            int32_t num_q_heads, int32_t nope_dim, int32_t v_dim, float scale, int32_t causal,
@@ -668,12 +671,14 @@ void tts_code_predictor_graph_destroy(tts_code_predictor_graph *graph);
 /* No counterpart on the pages: kernel-launch plumbing.  With
  * TTS_LAUNCH_PROGRAMMATIC set, the single-kernel calls this thread makes
  * afterwards (tts_kv_append, tts_kv_append_rope, tts_decode_attn,
- * tts_codebook_head_select) launch their kernel as a
+ * tts_codebook_head_select, and the first kernel of tts_latent_append,
+ * tts_latent_decode_attn and tts_latent_prefill_attn) launch their kernel as a
  * programmatic dependent of the previous kernel in the stream: it may start
  * while that kernel finishes (hiding the launch latency, as the kernels of
  * tts_decode_step do) and waits for its completion before touching anything
  * that kernel may write, except: tts_decode_attn reads d_ctx_lens and
- * d_block_table, and tts_codebook_head_select reads d_W, before that wait,
+ * d_block_table, tts_codebook_head_select reads d_W, and
+ * tts_latent_decode_attn reads d_w_uk, before that wait,
  * so the previous kernel must not write those.  The setting is per calling
  * thread.  Returns the previous flags. */
 enum { TTS_LAUNCH_PROGRAMMATIC = 1 };

@@ -605,6 +605,185 @@ def test_a_stream_from_prompt_to_tokens(bd):
         lens = t["ctx"]
 
 
+def test_append_far_positions(bd):
+    """Angles of positions past a million tokens."""
+    s = ref.make([2, 1], [0, 0], 4, 128, 64, 64, 7, garbage=1.0)
+    s["before"] = [1_000_003, 7_654_321]
+    s["ctx_before"] = torch.tensor(s["before"], dtype=torch.int32)
+    s["table"] = torch.full((2, 500_000), -1, dtype=torch.int32)
+    s["table"][0, 1_000_003 // 16], s["table"][1, 7_654_321 // 16] = 0, 1
+    d = up(s)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = run_append(bd, s, d, True, err=err)
+    assert int(err) == 0
+    _check_append(s, d, q_out)
+
+
+def test_append_many_rows(bd):
+    """More rows than CTAs run at once: four rows a CTA, the last CTA partly filled."""
+    new = [701, 0, 1200, 1, 600]
+    s = ref.make(new, [3, 0, 90, 15, 1], 2, 64, 64, 64, 8, garbage=1.0)
+    d = up(s)
+    _check_append(s, d, run_append(bd, s, d, True))
+    s = ref.make([2447], [5], 2, 64, 64, 64, 9, garbage=1.0)
+    d = up(s)
+    _check_append(s, d, run_append(bd, s, d, False))
+
+
+def test_shared_prefix_blocks(bd):
+    """Streams whose tables name the same blocks (a shared voice prompt)."""
+    s = ref.make([3, 3, 3], [61, 61, 61], 8, 128, 64, 64, 81)
+    s["table"][1, :2] = s["table"][0, :2]
+    s["table"][2, 1] = s["table"][0, 1]
+    d = up(s)
+    want, tol = ref.attend_all(s, True, True)
+    check(run_decode(bd, s, d, 3, True).view(9, 8, 64), want, tol, "decode")
+    want, tol = ref.attend_all(s, True, False)
+    check(run_prefill(bd, s, d), want, tol, "prefill")
+
+
+def test_two_streams_at_once(bd):
+    """Calls that overlap, each with its own workspace."""
+    cases, outs = [], []
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for i in range(3):
+        s = ref.make([2] * 20, [50 * i + 7 * k for k in range(20)], 16, 256, 64, 64, 90 + i)
+        d = up(s)
+        ws = [poisoned(bd.tts_latent_decode_attn_workspace_size(20, 2, 16, 256, 64, 64, max(s["ctx"]))),
+              poisoned(bd.tts_latent_prefill_attn_workspace_size(20, s["T"], 16, 256, 64, 64, sum(s["ctx"])))]
+        out = [torch.full((20, 2, 16, 64), NAN, dtype=torch.bfloat16, device="cuda"),
+               torch.full((40, 16, 64), NAN, dtype=torch.bfloat16, device="cuda")]
+        cases.append((s, d, ws, out))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st, (s, d, ws, out) in zip(streams, cases):
+            with torch.cuda.stream(st):
+                run_decode(bd, s, d, 2, True, ws=ws[0], out=out[0])
+                run_prefill(bd, s, d, ws=ws[1], out=out[1])
+    torch.cuda.synchronize()
+    for s, d, ws, out in cases:
+        want, tol = ref.attend_all(s, True, True)
+        check(out[0].view(40, 16, 64), want, tol, "decode")
+        want, tol = ref.attend_all(s, True, False)
+        check(out[1], want, tol, "prefill")
+
+
+def test_two_graphs_share_a_workspace(bd):
+    """A decode and a prompt call captured with one workspace, replayed in turn."""
+    s = ref.make([1] * 6, [40 * k + 3 for k in range(6)], 16, 256, 64, 64, 95)
+    t = ref.make([50, 7, 130], [0, 20, 3], 16, 256, 64, 64, 96)
+    d, e = up(s), up(t)
+    ws = poisoned(max(bd.tts_latent_decode_attn_workspace_size(6, 1, 16, 256, 64, 64, max(s["ctx"])),
+                      bd.tts_latent_prefill_attn_workspace_size(3, t["T"], 16, 256, 64, 64, sum(t["ctx"]))))
+    out = [torch.full((6, 1, 16, 64), NAN, dtype=torch.bfloat16, device="cuda"),
+           torch.full((t["T"], 16, 64), NAN, dtype=torch.bfloat16, device="cuda")]
+    graphs = []
+    for run in (lambda: run_decode(bd, s, d, 1, False, ws=ws, out=out[0]), lambda: run_prefill(bd, t, e, ws=ws, out=out[1])):
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    for o in out:
+        o.fill_(NAN)
+    for _ in range(2):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    want, tol = ref.attend_all(s, False, True)
+    check(out[0].view(6, 16, 64), want, tol, "decode")
+    want, tol = ref.attend_all(t, True, False)
+    check(out[1], want, tol, "prefill")
+
+
+def test_programmatic_launches(bd):
+    """Append, attention, append, attention, .. with programmatic launches: each
+    call sees what the one before wrote."""
+    from decode_step_gb300 import _lib
+    Hq, L = 16, 512
+    s = ref.make([1] * 30, [20 + 9 * i for i in range(30)], Hq, L, 128, 128, 97)
+    d = up(s)
+    cache = bd.LatentCache(d["pool"], L)
+    ws = poisoned(bd.tts_latent_decode_attn_workspace_size(30, 1, Hq, L, 128, 128, 400))
+    prev = bd.tts_set_launch_flags(_lib.LAUNCH_PROGRAMMATIC)
+    try:
+        outs, qs, steps = [], [], []
+        for i in range(4):
+            t = ref.make([1] * 30, s["before"], Hq, L, 128, 128, 100 + i)
+            e = up(t)
+            q = torch.empty_like(e["q_rope"])
+            out = torch.empty((30, 1, Hq, 128), dtype=torch.bfloat16, device="cuda")
+            steps.append((t, e))
+            qs.append(q)
+            outs.append(out)
+        torch.cuda.synchronize()
+        for (t, e), q, out in zip(steps, qs, outs):     # the same slots again and again
+            bd.tts_latent_append(cache, d["table"], d["ctx_before"], e["c_new"], e["kr_new"], e["q_rope"], q, BASE)
+            bd.tts_latent_decode_attn(cache, d["table"], d["ctx_lens"], 400, e["q_nope"].view(30, 1, Hq, 128),
+                                      q.view(30, 1, Hq, 64), d["w_uk"], d["w_uv"], out, ws, s["scale"])
+    finally:
+        bd.tts_set_launch_flags(prev)
+    torch.cuda.synchronize()
+    pool = s["pool"]
+    for (t, e), q, out in zip(steps, qs, outs):
+        for b in range(30):
+            p = s["before"][b]
+            pool[int(s["table"][b, p // 16]), p % 16] = torch.cat(
+                (t["c_new"][b], ref.rotate(t["kr_new"][b], torch.tensor(p), BASE).to(torch.bfloat16)))
+        u = dict(s, pool=pool, q_nope=t["q_nope"], q_rope=q.cpu())
+        want, tol = ref.attend_all(u, False, True)
+        # a value of the new token's stored key part may be rounded the other way than here: a step (2^-7) of
+        # a value near 1, times a query value near 1 and the scale 0.072, times its weight, at most 1 / 20
+        check(out.view(30, Hq, 128), want, tol + 2.0 ** -7 * 0.072 * 4 / 20, "step")
+
+
+def test_latent_step(bd):
+    """LatentStep: prompts, then steps that pick tokens, eagerly and captured."""
+    from decode_step_gb300.step import LatentStep
+    Hq, L, nope, v, V = 8, 128, 64, 64, 600
+    s = ref.make([40, 1, 77], [0, 0, 0], Hq, L, nope, v, 98, max_blocks=10, spare=40)
+    s["table"] = torch.randperm(s["pool"].shape[0], generator=torch.Generator().manual_seed(5))[:30].to(torch.int32).view(3, 10).contiguous()
+    s["pool"].fill_(NAN)
+    d = up(s)
+    W = (torch.randn(V, Hq * v, generator=torch.Generator().manual_seed(6)) * 0.2).to(torch.bfloat16).cuda()
+    cache = bd.LatentCache(d["pool"], L)
+    step = LatentStep(cache, d["w_uk"], d["w_uv"], W, 3, 160, prompt_rows=128, prompt_ctx=200)
+    out = step.prompt(d["table"], d["ctx_before"], d["ctx_lens"], d["row_start"], d["q_nope"], d["q_rope"], d["c_new"], d["kr_new"])
+    torch.cuda.synchronize()
+    t = dict(s, pool=d["pool"].cpu(), q_rope=step.q[:118].cpu())
+    want, tol = ref.attend_all(t, True, False)
+    check(out, want, tol, "prompt")
+    with pytest.raises(ValueError, match="prompt rows"):
+        step.prompt(d["table"], d["ctx_before"], d["ctx_lens"], d["row_start"], d["q_nope"], d["q_rope"],
+                    torch.zeros(129, L, dtype=torch.bfloat16, device="cuda"), d["kr_new"])
+    e = up(ref.make([1] * 3, s["ctx"], Hq, L, nope, v, 99))
+    args = (d["table"], e["ctx_before"], e["ctx_lens"], e["q_nope"].view(3, 1, Hq, nope), e["q_rope"].view(3, 1, Hq, 64),
+            e["c_new"], e["kr_new"])
+
+    def check_step():
+        torch.cuda.synchronize()
+        u = dict(s, new=[1] * 3, ctx=[c + 1 for c in s["ctx"]], T=3, row_start=torch.arange(4), pool=d["pool"].cpu(),
+                 q_nope=e["q_nope"].cpu(), q_rope=step.q[:3].cpu())
+        want, tol = ref.attend_all(u, False, True)
+        check(step.out.view(3, Hq, v), want, tol, "step")
+        logits = step.out.view(3, -1).double() @ W.double().t()
+        top = logits.topk(2, 1)
+        clear = (top.values[:, 0] - top.values[:, 1] > 1e-3).cpu()
+        assert clear.any() and torch.equal(step.ids.cpu()[clear], top.indices[:, 0].int().cpu()[clear])
+        assert int(step.err) == 0
+
+    step(*args)
+    check_step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(*args)
+    step.out.fill_(NAN)
+    step.ids.fill_(-1)
+    g.replay()
+    check_step()
+
+
 @pytest.mark.parametrize("op", ["decode", "prefill"])
 @pytest.mark.parametrize("L,nope,v", [(64, 64, 64), (128, 64, 128), (256, 64, 64), (512, 128, 128)])
 def test_first_call_of_a_process(op, L, nope, v):
