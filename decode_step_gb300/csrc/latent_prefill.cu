@@ -49,6 +49,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// kRows rows of one stream, what they see and where its keys and values are
+struct __align__(16) QueryTile {
+    int first, rows, ctx, tile0;  // of the stream: first row, rows, tokens, first token tile
+    int b, q, unused[2];          // stream; which of its tiles
+};
+
 struct PrefillArgs {
     const int32_t *table;
     int max_blocks, num_blocks;
@@ -56,8 +62,10 @@ struct PrefillArgs {
     const int32_t *row_start;
     int max_total, B, num_rows, Hq, L, nope, v;
     float scale_log2;
-    int32_t *tile_start;   // [B + 1] first token tile of each stream
-    int32_t *qtile_start;  // [B + 1] first query tile
+    int32_t *tile_start;   // [B] first token tile of each stream
+    int32_t *num_qtiles;   // query tiles in all
+    QueryTile *qtiles;     // [max_qtiles] those that see the most tokens first
+    int max_qtiles;
     uint32_t *blocks_ok;   // [token tiles] bit i: block i of the tile is in the pool
     const __nv_bfloat16 *pool;
     __nv_bfloat16 *kr;     // [token tiles * 128][64]
@@ -90,7 +98,8 @@ struct ExpandShared {
     uint64_t full[kExpandSlots], empty[kExpandSlots], acc_full[2], acc_empty[2], fin;
     uint32_t tmem;
     long long sums[kExpandThreads / 32];
-    int tiles[kExpandThreads / 32], qtiles[kExpandThreads / 32];
+    int tiles[kExpandThreads / 32], most[kExpandThreads / 32];
+    int bucket[64];
     int limit;             // streams from here on exceed max_total
     int start_b, start_i;  // stream and tile of the first unit
 };
@@ -168,65 +177,76 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
     }
     pdl_wait_prerequisites();
     pdl_allow_dependents();
-    // ---- the streams' token and query tiles
+    // ---- the streams' token tiles
     const int per = (a.B + kExpandThreads - 1) / kExpandThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
-    int n, ctx;
+    int n, ctx, limit = a.B;
     long long mine = 0;
+    int t_mine = 0, most = 0;
     for (int b = b0; b < b1; ++b)
-        if (prefill_stream(a, b, &n, &ctx) && n) mine += ctx;
+        if (prefill_stream(a, b, &n, &ctx) && n) {
+            mine += ctx;
+            t_mine += token_tiles(ctx);
+            most = max(most, ctx);
+        }
     long long incl = mine;
+    int t_incl = t_mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const long long x = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += x;
-    }
-    if (lane == 31) sh.sums[warp] = incl;
-    __syncthreads();
-    long long at = incl - mine;
-    for (int w = 0; w < warp; ++w) at += sh.sums[w];
-    for (int b = b0; b < b1 && at <= a.max_total; ++b)
-        if (prefill_stream(a, b, &n, &ctx) && n) {
-            at += ctx;
-            if (at > a.max_total) atomicMin(&sh.limit, b);
-        }
-    __syncthreads();
-    const int limit = sh.limit;
-    int t_mine = 0, q_mine = 0;
-    for (int b = b0; b < min(b1, limit); ++b)
-        if (prefill_stream(a, b, &n, &ctx) && n) {
-            t_mine += token_tiles(ctx);
-            q_mine += (n + kRows - 1) / kRows;
-        }
-    int t_incl = t_mine, q_incl = q_mine;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(kFull, t_incl, o), y = __shfl_up_sync(kFull, q_incl, o);
+        const int y = __shfl_up_sync(kFull, t_incl, o);
         if (lane >= o) {
-            t_incl += x;
-            q_incl += y;
+            incl += x;
+            t_incl += y;
         }
     }
+    most = __reduce_max_sync(kFull, most);
     if (lane == 31) {
+        sh.sums[warp] = incl;
         sh.tiles[warp] = t_incl;
-        sh.qtiles[warp] = q_incl;
+        sh.most[warp] = most;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int t_at = t_incl - t_mine, q_at = q_incl - q_mine, tiles = 0;
+    long long at = incl - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < kExpandThreads / 32; ++w) {
-        if (w < warp) {
-            t_at += sh.tiles[w];
-            q_at += sh.qtiles[w];
+        if (w < warp) at += sh.sums[w];
+        total += sh.sums[w];
+        most = max(most, sh.most[w]);
+    }
+    if (total > a.max_total) {  // rare: which streams fit, and their tiles
+        for (int b = b0; b < b1 && at <= a.max_total; ++b)
+            if (prefill_stream(a, b, &n, &ctx) && n) {
+                at += ctx;
+                if (at > a.max_total) atomicMin(&sh.limit, b);
+            }
+        __syncthreads();
+        limit = sh.limit;
+        t_mine = 0;
+        for (int b = b0; b < min(b1, limit); ++b)
+            if (prefill_stream(a, b, &n, &ctx) && n) t_mine += token_tiles(ctx);
+        t_incl = t_mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(kFull, t_incl, o);
+            if (lane >= o) t_incl += y;
         }
+        if (lane == 31) sh.tiles[warp] = t_incl;
+        __syncthreads();
+    }
+    int t_at = t_incl - t_mine, tiles = 0;
+#pragma unroll
+    for (int w = 0; w < kExpandThreads / 32; ++w) {
+        if (w < warp) t_at += sh.tiles[w];
         tiles += sh.tiles[w];
     }
     const int feature_tiles = k_tiles + v_tiles, clusters = gridDim.x / 2, me = blockIdx.x / 2;
     const int units = (tiles + 1) / 2 * feature_tiles;
-    const int u0 = static_cast<int>(static_cast<long long>(units) * me / clusters);
-    const int u1 = static_cast<int>(static_cast<long long>(units) * (me + 1) / clusters);
+    const int each = units / clusters;
+    const int fewer = clusters - (units - each * clusters);  // the clusters behind these take one more
+    const int u0 = me * each + max(0, me - fewer), u1 = u0 + each + (me >= fewer);
     const int first_t = u0 / feature_tiles * 2 + static_cast<int>(rank);
     for (int b = b0; b < b1; ++b) {
         const bool good = prefill_stream(a, b, &n, &ctx);
@@ -237,17 +257,11 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         }
         if (blockIdx.x == 0) {
             a.tile_start[b] = t_at;
-            a.qtile_start[b] = q_at;
-            if (nt) q_at += (n + kRows - 1) / kRows;
             if (!good || (n && b >= limit)) {  // refused: its rows get zeros
                 flag_error(a.err, TTS_ERRBIT_CTX_LEN);
                 const int r0 = max(0, a.row_start[b]), r1 = min(a.num_rows, a.row_start[b + 1]);
                 const size_t w = static_cast<size_t>(a.Hq) * a.v / 8;
                 for (size_t i = r0 * w; r0 < r1 && i < r1 * w; ++i) reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
-            }
-            if (b == a.B - 1) {
-                a.tile_start[a.B] = t_at + nt;
-                a.qtile_start[a.B] = q_at;
             }
         }
         t_at += nt;
@@ -434,6 +448,42 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         }
         if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    else if (warp == 6 && blockIdx.x == 0) {
+        // ---- the query tiles by the tokens that they see, most first (64
+        // buckets): the attention's CTAs start in this order, so that the last
+        // ones to run are short
+        const int shift = max(0, 26 - __clz(max(1, token_tiles(most))));
+        auto each_tile = [&](auto &&f) {
+            for (int b = lane; b < limit; b += 32) {
+                int rows, c;
+                if (!prefill_stream(a, b, &rows, &c)) continue;
+                for (int q = 0; q * kRows < rows; ++q)
+                    f(b, q, 63 - min(63, token_tiles(c - rows + min(rows, (q + 1) * kRows)) >> shift));
+            }
+            __syncwarp();
+        };
+        sh.bucket[lane] = sh.bucket[lane + 32] = 0;
+        __syncwarp();
+        each_tile([&](int, int, int k) { atomicAdd(&sh.bucket[k], 1); });
+        const int lo = sh.bucket[2 * lane], hi = sh.bucket[2 * lane + 1];
+        int upto = lo + hi;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const int x = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += x;
+        }
+        if (lane == 31) *a.num_qtiles = upto;
+        sh.bucket[2 * lane] = upto - lo - hi;
+        sh.bucket[2 * lane + 1] = upto - hi;
+        __syncwarp();
+        each_tile([&](int b, int q, int k) {
+            const int to = atomicAdd(&sh.bucket[k], 1);
+            if (to >= a.max_qtiles) return;  // (streams whose rows overlap)
+            const int first = a.row_start[b];
+            reinterpret_cast<int4 *>(a.qtiles + to)[0] = make_int4(first, a.row_start[b + 1] - first, a.ctx_lens[b], a.tile_start[b]);
+            reinterpret_cast<int4 *>(a.qtiles + to)[1] = make_int4(b, q, 0, 0);
+        });
+    }
     if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
     tc_fence_before();
     __syncthreads();
@@ -495,13 +545,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int h = blockIdx.x % a.Hq, qt = blockIdx.x / a.Hq;
-    const int b = uniform(stream_of_row(a.qtile_start, a.B, qt, lane));
+    const bool mine = qt < __ldg(a.num_qtiles);
+    const int4 of = __ldg(reinterpret_cast<const int4 *>(a.qtiles + qt));  // (the list has room for every CTA)
+    const int4 which = __ldg(reinterpret_cast<const int4 *>(a.qtiles + qt) + 1);
     bool ok = true;
-    if (b >= 0) {
-        const int first = uniform(a.row_start[b]), n = uniform(a.row_start[b + 1]) - first, ctx = uniform(a.ctx_lens[b]);
-        // a stream's last tiles, which see the most tokens, come first
-        const int q = uniform(a.qtile_start[b + 1]) - 1 - qt;
-        const int tile0 = uniform(a.tile_start[b]);
+    if (uniform(mine)) {
+        const int first = uniform(of.x), n = uniform(of.y), ctx = uniform(of.z), tile0 = uniform(of.w);
+        const int q = uniform(which.y);
         const int r0 = q * kRows;                          // first row in the stream
         const bool two = r0 + kTile < n;
         // tokens either half sees, in tiles
@@ -732,8 +782,8 @@ bool prefill_shape_ok(int B, int T, int Hq, int L, int nope, int v, int max_tota
 // the plan's arrays.
 struct PrefillPlan {
     int64_t tiles, qtiles;   // at most
-    size_t k_bytes, v_bytes, kr_bytes, start_bytes, ok_bytes;
-    size_t total() const { return k_bytes + v_bytes + kr_bytes + 2 * start_bytes + ok_bytes; }
+    size_t k_bytes, v_bytes, kr_bytes, start_bytes, qtile_bytes, ok_bytes;
+    size_t total() const { return k_bytes + v_bytes + kr_bytes + start_bytes + qtile_bytes + ok_bytes + 256; }
 };
 
 PrefillPlan prefill_plan(int B, int T, int Hq, int nope, int v, int max_total) {
@@ -745,6 +795,7 @@ PrefillPlan prefill_plan(int B, int T, int Hq, int nope, int v, int max_total) {
     p.v_bytes = rows * Hq * v * 2;
     p.kr_bytes = rows * kLatentRope * 2;
     p.start_bytes = align_up((static_cast<size_t>(B) + 1) * 4, 256);
+    p.qtile_bytes = align_up(static_cast<size_t>(p.qtiles) * sizeof(QueryTile), 256);
     p.ok_bytes = align_up(static_cast<size_t>(p.tiles) * 4, 256);
     return p;
 }
@@ -810,8 +861,10 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
     a.kr = reinterpret_cast<__nv_bfloat16 *>(ws + pl.k_bytes + pl.v_bytes);
     uint8_t *at = ws + pl.k_bytes + pl.v_bytes + pl.kr_bytes;
     a.tile_start = reinterpret_cast<int32_t *>(at);
-    a.qtile_start = reinterpret_cast<int32_t *>(at + pl.start_bytes);
-    a.blocks_ok = reinterpret_cast<uint32_t *>(at + 2 * pl.start_bytes);
+    a.qtiles = reinterpret_cast<QueryTile *>(at + pl.start_bytes);
+    a.max_qtiles = static_cast<int>(pl.qtiles);
+    a.blocks_ok = reinterpret_cast<uint32_t *>(at + pl.start_bytes + pl.qtile_bytes);
+    a.num_qtiles = reinterpret_cast<int32_t *>(at + pl.start_bytes + pl.qtile_bytes + pl.ok_bytes);
     a.pool = static_cast<const __nv_bfloat16 *>(cache->pool);
     a.out = static_cast<__nv_bfloat16 *>(d_out);
     a.err = d_err;
