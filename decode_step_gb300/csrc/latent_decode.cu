@@ -656,11 +656,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         constexpr int kVals = N / 2;
         const int g = lane / 4, c2 = lane % 4 * 2;
         auto col = [&](int i) { return i / 4 * 8 + c2 + i % 2; };
-        // P's rows c2 and c2 + 1 at tokens g and g + 8 (16-byte chunk t / 8 of row n at (t / 8) ^ (n % 8))
-        uint32_t pat[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            pat[i] = p_base + (c2 + i % 2) * 128 + (((2 * warp + i / 2) ^ (c2 + i % 2)) << 4) + g * 2;
+        // Eight tokens of a row n of P are the 16-byte chunk (t / 8) ^ (n % 8),
+        // a row of a transposed 8 x 8 matrix: the lane's of a store of four,
+        // rows 0-7 at tokens 0-7 and 8-15, then rows 8-15
+        const uint32_t pat = p_base + (lane / 16 * 8 + lane % 8) * 128 + (((2 * warp + lane / 8 % 2) ^ (lane % 8)) << 4);
         auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1); };
         const int tid = threadIdx.x;
         auto block_ok = [&](const Segments &s, int tile) {
@@ -765,21 +764,30 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 if (it > 0 && kPBufs == 1 && !o_added(it - 1)) ok = false;
                 const uint32_t pb = it % kPBufs * kPBytes;
                 // (no memory clobber: the values' chains overlap; the fence below orders the stores)
-                auto store = [&](uint32_t at, __nv_bfloat16 x) {
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(__bfloat16_as_ushort(x)));
+                auto store = [&](uint32_t at, const uint32_t *m) {
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                                 "r"(m[0]), "r"(m[1]), "r"(m[2]), "r"(m[3]));
                 };
 #pragma unroll
-                for (int i = 0; i < kVals; ++i) {
-                    const float x = hw_ex2(score(i));
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-                    const uint32_t at = pat[i % 4] + pb + i / 4 * 1024;
-                    store(at, hi);
-                    if constexpr (p_split(N)) {
-                        store(at + N * 128, __float2bfloat16_rn(x - __bfloat162float(hi)));
-                        l[i / 4 * 2 + i % 2] += x;
-                    } else {
-                        l[i / 4 * 2 + i % 2] += __bfloat162float(hi);  // as the MMA takes it: the weights then add up to one
+                for (int i = 0; i < kVals; i += 8) {  // two times eight columns
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const float x = hw_ex2(score(i + 2 * m)), y = hw_ex2(score(i + 2 * m + 1));
+                        hi[m] = pack_bf16(x, y);
+                        const float hx = __uint_as_float(hi[m] << 16), hy = __uint_as_float(hi[m] & 0xFFFF0000u);
+                        float *sum = l + (i / 4 + m / 2) * 2;
+                        if constexpr (p_split(N)) {
+                            lo[m] = pack_bf16(x - hx, y - hy);
+                            sum[0] += x;
+                            sum[1] += y;
+                        } else {  // as the MMA takes them: the weights then add up to one
+                            sum[0] += hx;
+                            sum[1] += hy;
+                        }
                     }
+                    store(pat + pb + i * 256, hi);
+                    if constexpr (p_split(N)) store(pat + pb + i * 256 + N * 128, lo);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
