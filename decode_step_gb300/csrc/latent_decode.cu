@@ -304,6 +304,22 @@ __device__ __forceinline__ bool softmax_any(bool pred) {
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
+// Sets the bf16 values in 16 bytes of shared memory that are not finite to zero.
+__device__ __forceinline__ void keep_finite(uint32_t at) {
+    uint32_t x[4];
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool low = (x[i] & 0x7F80u) == 0x7F80u, high = (x[i] & 0x7F800000u) == 0x7F800000u;
+        if (low) x[i] &= 0xFFFF0000u;
+        if (high) x[i] &= 0xFFFFu;
+        found = found || low || high;
+    }
+    if (found)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+}
+
 // Position in a ring of shared-memory slots; phase is the parity of the
 // slot's current filling.
 struct Ring {
@@ -662,6 +678,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         const uint32_t pat = p_base + (lane / 16 * 8 + lane % 8) * 128 + (((2 * warp + lane / 8 % 2) ^ (lane % 8)) << 4);
         auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1); };
         const int tid = threadIdx.x;
+        int lslot = 0;  // latent ring slot of the tile's first pair
         auto block_ok = [&](const Segments &s, int tile) {
             const int i = tile * 4 + warp;
             if (i * TTS_BLOCK_TOKENS >= s.ctx) return false;
@@ -789,6 +806,18 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     store(pat + pb + i * 256, hi);
                     if constexpr (p_split(N)) store(pat + pb + i * 256 + N * 128, lo);
                 }
+                // A later row's token that is not finite would spread to the
+                // rows that do not see it (NaN times a zero weight).  The scores
+                // have it already: the rows that see it have NaN weights, the
+                // product can do without it.
+                const int hi = min(seg.ctx - tile * kTile, kTile), lo = max(low - tile * kTile, 0);
+                if (lo < hi)
+                    for (int p = 0; p < nb; ++p) {
+                        const int slot = lslot + p < a.pairs ? lslot + p : lslot + p - a.pairs;
+                        for (int i = tid; i < (hi - lo) * 16; i += 128)
+                            keep_finite(l_base + slot * kPairBytes + i / 8 % 2 * kChunkBytes + (lo + i / 16) * 128 + i % 8 * 16);
+                    }
+                lslot = lslot + nb < a.pairs ? lslot + nb : lslot + nb - a.pairs;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();

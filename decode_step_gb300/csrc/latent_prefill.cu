@@ -420,7 +420,13 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 tmem_ld32_nowait(tl + buf * kFeatures + q * 64, x);
                 tmem_ld32_nowait(tl + buf * kFeatures + q * 64 + 32, x + 32);
                 tmem_wait_ld();
-                const float *v = reinterpret_cast<const float *>(x);
+                float *v = reinterpret_cast<float *>(x);
+                // A token's value that is not finite would spread to rows that
+                // do not see it (NaN times a zero weight); those that do have
+                // it from the keys, which come from the same latent.
+                if (!is_k)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.0f;
                 const uint32_t to = stage + (q & 1) * kChunkBytes + r * 128;
                 // 16-byte chunk j of row r at j ^ (r % 8), the stores' swizzle
 #pragma unroll

@@ -270,7 +270,7 @@ typedef struct tts_latent_cache {
  *  d_c_new   bf16 [num_rows][latent_dim], copied as it is
  *  d_kr_new  bf16 [num_rows][64]: with i < 32 and a = s * rope_base^(-2i/64),
  *            x[i] cos a - x[i + 32] sin a and x[i + 32] cos a + x[i] sin a are
- *            stored (cos a and sin a from double precision, the rotation in
+ *            stored (a reduced exactly from a frequency in 64 bits, the rest in
  *            fp32, rounded once to bf16)
  *  d_q_rope, d_q_rope_out  bf16 [num_rows][num_q_heads][64], rotated likewise;
  *            the same buffer (in place) or disjoint ones; num_q_heads 0: none
@@ -295,7 +295,9 @@ size_t tts_latent_decode_attn_workspace_size(int32_t B, int32_t q_len, int32_t n
  * over the tokens t < limit of tts_decode_attn (d_ctx_lens counts the tokens
  * after this step's append; causal as there).  Computed in the absorbed form:
  * q_nope w_uk[h] first (rounded to bf16), attention over the latents
- * themselves (weights rounded to bf16), then w_uv[h] on the attended latent.
+ * themselves (weights as two bf16 numbers, or rounded to one with more than 48
+ * of a stream's query rows together), then w_uv[h] on the attended latent.  A
+ * token that is not finite makes the rows that see it so, and no others.
  *  d_q_nope  bf16 [B][q_len][Hq][nope_dim]
  *  d_q_rope  bf16 [B][q_len][Hq][64], rotated (tts_latent_append)
  *  d_w_uk    bf16 [Hq][nope_dim][latent_dim];  d_w_uv  bf16 [Hq][v_dim][latent_dim]
@@ -328,8 +330,8 @@ size_t tts_latent_prefill_attn_workspace_size(int32_t B, int32_t num_rows, int32
  *   t < d_ctx_lens[b] - (d_row_start[b + 1] - r) + 1.
  * The sum is tts_latent_decode_attn's, in the expanded form: keys (rounded to
  * bf16) and values (rounded to f16, as the softmax weights are) of every head
- * are multiplied out once.  Values w_uv[h] c beyond f16's range (65504) make
- * the outputs that they enter not finite.
+ * are multiplied out once.  A value w_uv[h] c beyond f16's range (65504) makes
+ * outputs of its stream not finite, from up to 127 tokens before it on.
  *  d_q_nope bf16 [num_rows][Hq][nope_dim];  d_q_rope bf16 [num_rows][Hq][64]
  *  d_out    bf16 [num_rows][Hq][v_dim]
  *  max_total_ctx  host upper bound of the sum of d_ctx_lens over the streams

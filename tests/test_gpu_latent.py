@@ -225,6 +225,24 @@ def test_decode_query_rows(bd, q_len, causal, Hq):
     decode_case(bd, [q_len, q_len + 1, 64, 65, 67, 200], q_len, Hq, 256, 128, 128, causal)
 
 
+@pytest.mark.parametrize("what", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("q_len,ctx,Hq", [(5, 71, 16), (5, 66, 4), (3, 64, 16), (70, 200, 2)])
+def test_decode_later_tokens_not_finite(bd, what, q_len, ctx, Hq):
+    """A row's own token (and what follows) does not reach the rows before it."""
+    s = ref.make([q_len] * 2, [ctx - q_len] * 2, Hq, 192, 128, 64, 12)
+    want, tol = ref.attend_all(s, True, True)
+    first = q_len // 2                        # the row whose token is spoilt
+    t = ctx - q_len + first
+    s["pool"][s["table"][0, t // 16].long(), t % 16, 5:40] = what
+    s["pool"][s["table"][0, t // 16].long(), t % 16, 192 + 7] = what
+    out = run_decode(bd, s, up(s), q_len, True).view(2, q_len, Hq, 64)
+    want, tol = want.view(out.shape), tol.view(out.shape)
+    check(out[1], want[1], tol[1], "the other stream")
+    check(out[0, :first], want[0, :first], tol[0, :first], "rows before")
+    if what != what:
+        assert torch.isnan(out[0, first:].float()).all()
+
+
 def test_decode_many_rows(bd):
     decode_case(bd, [300, 128], 8, 128, 128, 64, 64, True)       # 1024 query rows a stream
 
@@ -418,6 +436,21 @@ def test_prefill_ragged(bd, new):
 
 def test_prefill_longer(bd):
     prefill_case(bd, [1500, 700], [77, 0], 2, 256, 128, 128)
+
+
+@pytest.mark.parametrize("what", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("n,before,spoilt", [(140, 20, 100), (300, 3, 200), (7, 0, 1), (20, 125, 4)])
+def test_prefill_later_tokens_not_finite(bd, what, n, before, spoilt):
+    s = ref.make([n, 9], [before, 2], 2, 128, 64, 128, 33)
+    want, tol = ref.attend_all(s, True, False)
+    t = before + spoilt
+    s["pool"][s["table"][0, t // 16].long(), t % 16, 5:40] = what
+    s["pool"][s["table"][0, t // 16].long(), t % 16, 128 + 7] = what
+    out = run_prefill(bd, s, up(s))
+    check(out[n:], want[n:], tol[n:], "the other stream")
+    check(out[:spoilt], want[:spoilt], tol[:spoilt], "rows before")
+    if what != what:
+        assert torch.isnan(out[spoilt:n].float()).all()
 
 
 @pytest.mark.parametrize("gain", [8.0])
