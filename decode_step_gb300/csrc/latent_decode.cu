@@ -364,13 +364,15 @@ __host__ __device__ constexpr int p_buffers(int N) { return N == 16 || N == 48 ?
 // Buffers for q~: with two, a segment's rows are there when the one before ends.
 __host__ __device__ constexpr int q_buffers(int N) { return N <= 32 ? 2 : 1; }
 
-// Whether P enters the product as two bf16 numbers, its rounding and the
-// remainder, in 2 N columns: the weights are then held to 2^-17.  Up to 48 rows
-// that is nearly free (a 128-row MMA of 16 to 64 columns takes 48 to 52 cycles,
-// most of them reading A); 64 rows would need more than tensor memory's 512
-// columns.
-__host__ __device__ constexpr bool p_split(int N) { return N <= 48; }
-__host__ __device__ constexpr int p_rows(int N) { return p_split(N) ? 2 * N : N; }
+// P enters the product as two bf16 numbers, its rounding and the remainder:
+// the weights are then held to 2^-17.  Up to 48 rows the remainders are N more
+// columns of the same MMAs, which is nearly free (a 128-row MMA of 16 to 64
+// columns takes 48 to 52 cycles, most of them reading A).  64 rows would need
+// more than tensor memory's 512 columns: the remainders are then a second
+// operand for the same accumulator, kept in the tile's rope slot, whose keys
+// S^T is done with.
+__host__ __device__ constexpr bool p_beside(int N) { return N <= 48; }
+__host__ __device__ constexpr int p_rows(int N) { return p_beside(N) ? 2 * N : N; }
 
 template <int N>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -550,7 +552,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         // the tile whose O^T is outstanding: the one before `it`
         bool pending = false, pend_first = false;
         Ring pend(a.pairs);
-        uint32_t pend_seg = 0;
+        uint32_t pend_seg = 0, pend_rope = 0;
         auto weights = [&](uint32_t tile) {  // what O^T of `tile` waits for
             WarpWaits<2> w;
             w.set(0, &sh.p_full[tile % kPBufs], (tile / kPBufs) & 1);
@@ -568,10 +570,16 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 for (int k = 0; k < kTile / 16; ++k)
                     mma_bf16_by(leader, tmem + 2 * N + p * kO, sw128_mn_desc(sa + k * 2048, kChunkBytes),
                                 sw128_desc(sb + k * 32), idesc_o, !(pend_first && k == 0));
+                if constexpr (!p_beside(N))
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_bf16_by(leader, tmem + 2 * N + p * kO, sw128_mn_desc(sa + k * 2048, kChunkBytes),
+                                    sw128_desc(r_base + pend_rope * kChunkBytes + k * 32), idesc_o, 1);
                 mma_commit_by(leader, smem_addr(&sh.empty_l[pend.slot]));
                 pend.next();
             }
             mma_commit_by(leader, smem_addr(&sh.p_empty[pb]));
+            if constexpr (!p_beside(N)) mma_commit_by(leader, smem_addr(&sh.empty_r[pend_rope]));
             pending = false;
         };
         while (ok && seg.next(a)) {
@@ -608,7 +616,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 for (int kk = 0; kk < 4; ++kk)
                     mma_bf16_by(leader, tmem + buf * N, sw128_desc(sr + kk * 32),
                                 sw128_desc(qs + chunks * N * 128 + kk * 32), idesc_s, kk != 0);
-                mma_commit_by(leader, smem_addr(&sh.empty_r[rope.slot]));
+                const uint32_t rope_slot = rope.slot;
+                if constexpr (p_beside(N)) mma_commit_by(leader, smem_addr(&sh.empty_r[rope_slot]));
                 rope.next();
                 for (int p = 0; p < nb; ++p) {
                     const uint32_t sa = l_base + lat.slot * kPairBytes, sb = qs + 2 * p * N * 128;
@@ -652,6 +661,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 pend_first = k == 0;
                 pend = first;
                 pend_seg = segs;
+                pend_rope = rope_slot;
                 ++it;
             }
             ++segs;
@@ -678,7 +688,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         const uint32_t pat = p_base + (lane / 16 * 8 + lane % 8) * 128 + (((2 * warp + lane / 8 % 2) ^ (lane % 8)) << 4);
         auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1); };
         const int tid = threadIdx.x;
-        int lslot = 0;  // latent ring slot of the tile's first pair
+        int lslot = 0, rslot = 0;  // the tile's ring slots: its first latent pair, its rope chunk
         auto block_ok = [&](const Segments &s, int tile) {
             const int i = tile * 4 + warp;
             if (i * TTS_BLOCK_TOKENS >= s.ctx) return false;
@@ -779,7 +789,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     }
                 }
                 if (it > 0 && kPBufs == 1 && !o_added(it - 1)) ok = false;
-                const uint32_t pb = it % kPBufs * kPBytes;
+                const uint32_t at_hi = pat + it % kPBufs * kPBytes;
+                const uint32_t at_lo = p_beside(N) ? at_hi + N * 128 : pat - p_base + r_base + rslot * kChunkBytes;
+                rslot = rslot + 1 < a.ropes ? rslot + 1 : 0;
                 // (no memory clobber: the values' chains overlap; the fence below orders the stores)
                 auto store = [&](uint32_t at, const uint32_t *m) {
                     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at),
@@ -792,19 +804,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     for (int m = 0; m < 4; ++m) {
                         const float x = hw_ex2(score(i + 2 * m)), y = hw_ex2(score(i + 2 * m + 1));
                         hi[m] = pack_bf16(x, y);
-                        const float hx = __uint_as_float(hi[m] << 16), hy = __uint_as_float(hi[m] & 0xFFFF0000u);
-                        float *sum = l + (i / 4 + m / 2) * 2;
-                        if constexpr (p_split(N)) {
-                            lo[m] = pack_bf16(x - hx, y - hy);
-                            sum[0] += x;
-                            sum[1] += y;
-                        } else {  // as the MMA takes them: the weights then add up to one
-                            sum[0] += hx;
-                            sum[1] += hy;
-                        }
+                        lo[m] = pack_bf16(x - __uint_as_float(hi[m] << 16), y - __uint_as_float(hi[m] & 0xFFFF0000u));
+                        l[(i / 4 + m / 2) * 2] += x;
+                        l[(i / 4 + m / 2) * 2 + 1] += y;
                     }
-                    store(pat + pb + i * 256, hi);
-                    if constexpr (p_split(N)) store(pat + pb + i * 256 + N * 128, lo);
+                    store(at_hi + i * 256, hi);
+                    store(at_lo + i * 256, lo);
                 }
                 // A later row's token that is not finite would spread to the
                 // rows that do not see it (NaN times a zero weight).  The scores
@@ -851,11 +856,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 uint32_t o[N], rest[N];
 #pragma unroll
                 for (int c = 0; c < N; c += 16) tmem_ld16_nowait(tl + 2 * N + p * kO + c, o + c);
-                if constexpr (p_split(N))
+                if constexpr (p_beside(N))
 #pragma unroll
                     for (int c = 0; c < N; c += 16) tmem_ld16_nowait(tl + 2 * N + p * kO + N + c, rest + c);
                 tmem_wait_ld();
-                if constexpr (p_split(N))
+                if constexpr (p_beside(N))
 #pragma unroll
                     for (int n = 0; n < N; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) + __uint_as_float(rest[n]));
                 if (d < a.L) {

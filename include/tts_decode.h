@@ -295,9 +295,9 @@ size_t tts_latent_decode_attn_workspace_size(int32_t B, int32_t q_len, int32_t n
  * over the tokens t < limit of tts_decode_attn (d_ctx_lens counts the tokens
  * after this step's append; causal as there).  Computed in the absorbed form:
  * q_nope w_uk[h] first (rounded to bf16), attention over the latents
- * themselves (weights as two bf16 numbers, or rounded to one with more than 48
- * of a stream's query rows together), then w_uv[h] on the attended latent.  A
- * token that is not finite makes the rows that see it so, and no others.
+ * themselves (weights as two bf16 numbers), then w_uv[h] on the attended
+ * latent.  A token that is not finite makes the rows that see it so, and no
+ * others.
  *  d_q_nope  bf16 [B][q_len][Hq][nope_dim]
  *  d_q_rope  bf16 [B][q_len][Hq][64], rotated (tts_latent_append)
  *  d_w_uk    bf16 [Hq][nope_dim][latent_dim];  d_w_uv  bf16 [Hq][v_dim][latent_dim]
