@@ -7,7 +7,8 @@
 // latent_dim / 8 copies.  Pure data movement: the bytes are each row's 2
 // (latent_dim + 64) + 2 x 64 Hq, read once and written once.
 // A CTA takes one row, or four where there are more rows than CTAs fit at once
-// (a CTA's time is latency: 8409 rows of 16 heads took 14.6 us one by one).
+// (a CTA's time is latency): 8409 rows of 16 heads take 11.5 us, 4.7 TB/s (one
+// by one 14.6 us), 64 rows 3.4 us.
 // The rows' first items are loaded before their positions are known (they do
 // not depend on them); meanwhile a warp per row finds the stream and the block
 // and computes the 32 angles, shared through shared memory.

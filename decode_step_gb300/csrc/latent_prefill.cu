@@ -9,12 +9,15 @@
 //  1. latent_expand_kernel: checks the streams, lays out their tokens in the
 //     workspace (each stream from a 128-token boundary) and their query tiles,
 //     and multiplies keys and values out: a tcgen05 GEMM whose token rows are
-//     fetched through the block table.
+//     fetched through the block table.  36 us for 8891 tokens (16 heads, 512 ->
+//     128 + 128: 1.0 PFLOP/s, 73 MB written), 10 us for 333, latency.
 //  2. latent_prefill_kernel: attention of 256 rows of one head per CTA (two
 //     128-row tiles that take turns on the tensor core: while one's weights
 //     are computed, the other's products run).  S and O are in tensor memory;
 //     the weights go back into S's columns (as f16) and are the A operand of
-//     the second product.
+//     the second product.  Bound: the tensor core (640 flop a row, token and
+//     head); 247 us for 8191 rows after 700 tokens, 1.63 PFLOP/s, 86% of the
+//     rate that a large bf16 matrix product reaches.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -52,7 +55,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // kRows rows of one stream, what they see and where its keys and values are
 struct __align__(16) QueryTile {
     int first, rows, ctx, tile0;  // of the stream: first row, rows, tokens, first token tile
-    int b, q, unused[2];          // stream; which of its tiles
+    int q, unused[3];             // which of its tiles
 };
 
 struct PrefillArgs {
@@ -457,7 +460,8 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
     else if (warp == 6 && blockIdx.x == 0) {
         // ---- the query tiles by the tokens that they see, most first (64
         // buckets): the attention's CTAs start in this order, so that the last
-        // ones to run are short
+        // ones to run are short (16 prompts of 61 to 700 rows, 8 heads: 18.4 us
+        // against 24 us in the streams' order)
         const int shift = max(0, 26 - __clz(max(1, token_tiles(most))));
         auto each_tile = [&](auto &&f) {
             for (int b = lane; b < limit; b += 32) {
@@ -486,8 +490,9 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
             const int to = atomicAdd(&sh.bucket[k], 1);
             if (to >= a.max_qtiles) return;  // (streams whose rows overlap)
             const int first = a.row_start[b];
-            reinterpret_cast<int4 *>(a.qtiles + to)[0] = make_int4(first, a.row_start[b + 1] - first, a.ctx_lens[b], a.tile_start[b]);
-            reinterpret_cast<int4 *>(a.qtiles + to)[1] = make_int4(b, q, 0, 0);
+            reinterpret_cast<int4 *>(a.qtiles + to)[0] =
+                make_int4(first, a.row_start[b + 1] - first, a.ctx_lens[b], a.tile_start[b]);
+            reinterpret_cast<int4 *>(a.qtiles + to)[1] = make_int4(q, 0, 0, 0);
         });
     }
     if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
@@ -557,7 +562,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
     bool ok = true;
     if (uniform(mine)) {
         const int first = uniform(of.x), n = uniform(of.y), ctx = uniform(of.z), tile0 = uniform(of.w);
-        const int q = uniform(which.y);
+        const int q = uniform(which.x);
         const int r0 = q * kRows;                          // first row in the stream
         const bool two = r0 + kTile < n;
         // tokens either half sees, in tiles
