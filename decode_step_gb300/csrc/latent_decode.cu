@@ -895,7 +895,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 
 // out[r][h] = w_uv[h] o~[r][h], o~ the join of the row's splits (weights
 // 2^(m_s - max m)).  A CTA takes one head and shares the rows evenly with the
-// head's others, in rounds of up to 32; its warps join the rows' splits into
+// head's others, in rounds of up to 40; its warps join the rows' splits into
 // the B operand (few rows share the warps), then one product D[v][rows] with
 // the head's weights.  o~ enters as two bf16 numbers, its rounding in the first
 // half of the columns and the remainder in the other, so that it is held to
@@ -905,7 +905,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 // 6.3 us for one row of one split, 10 us for 256 rows, 9.4 us for one row of
 // 152 splits, 14 us for 320 rows (27 MB of partial sums, from L2).
 constexpr int kOutThreads = 512, kOutWarps = kOutThreads / 32;
-constexpr int kOutRows = 32;
+constexpr int kOutRows = 40;
 
 // Joins `count` splits of one row by a warp, two read together: o (4 x 128
 // dimensions) is scaled by 2^-M, M the largest of the splits' maxima, and S is
@@ -1029,7 +1029,7 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
         mbar_expect_tx_by(leader, smem_addr(&full), chunks * w_chunk);
         for (int c = 0; c < chunks; ++c)
             tma_load_2d_by(leader, wb + c * w_chunk, &map_uv, 64 * c, h * v_dim, smem_addr(&full));
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 64;" ::"r"(smem_addr(&tslot))
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tslot))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -1051,17 +1051,26 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
         const int quarters = (L + 127) / 128, lq = quarters > 2 ? 2 : quarters - 1;  // log2, rounded up
         const int lshare = rows > 4 ? 0 : rows > 2 ? 2 : rows > 1 ? 3 : 4;           // log2 of a row's warps
         const int ldims = lshare ? lq : 0, lss = lshare - ldims, ss = 1 << lss;
+        const int sub = warp & ((1 << lshare) - 1), i0 = warp >> lshare;
+        const int first = sub >> ldims, d0 = (sub & ((1 << ldims) - 1)) * 128 + 4 * lane;
+        auto group = [&](int i, int &n) {  // of this round's row i, and the row in it
+            const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h, grp = idx / N;
+            n = idx - grp * N;
+            return b * a.G + grp;
+        };
+        if (round == 0) {
+            pdl_wait_prerequisites();
+            pdl_allow_dependents();
+        }
+        int n, bg = group(min(i0, rows - 1), n);
+        int2 own = __ldcg(a.owner + bg);
         for (int rr = 0; rr < rows; rr += kOutWarps >> lshare) {
-            const int i = rr + (warp >> lshare), sub = warp & ((1 << lshare) - 1);
-            const int first = sub >> ldims, d0 = (sub & ((1 << ldims) - 1)) * 128 + 4 * lane;
-            const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h;
-            const int grp = idx / N, n = idx - grp * N, bg = b * a.G + grp;
-            if (round == 0 && rr == 0) {
-                pdl_wait_prerequisites();
-                pdl_allow_dependents();
-            }
+            const int i = rr + i0;
+            // the next row's owner is read a row ahead
+            int n_next;
+            const int bg_next = group(min(i + (kOutWarps >> lshare), rows - 1), n_next);
+            const int2 own_next = __ldcg(a.owner + bg_next);
             if (i < rows) {
-                const int2 own = a.owner[bg];
                 const size_t row = (static_cast<size_t>(own.x) + bg) * N + n;
                 const float2 *ml = a.ml + row;  // split s: ml[s * N]
                 const float *part = a.part + row * L;
@@ -1107,6 +1116,9 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
                     put(i, d0 + 2, x.z * inv, x.w * inv);
                 }
             }
+            own = own_next;
+            n = n_next;
+            bg = bg_next;
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
@@ -1151,7 +1163,7 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
     }
     if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
     if (warp == 0) {
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 64;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
     }
 }
 
@@ -1260,7 +1272,7 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     }
     if (rc != TTS_OK) return rc;
     // one CTA fits an SM: as many as there are SMs share the rows evenly, in
-    // rounds of up to 32 that keep the weights
+    // rounds of up to 40 that keep the weights
     const int most = std::max(1, kCtas / Hq), rounds = (R + most * kOutRows - 1) / (most * kOutRows);
     const int per = (R + most * rounds - 1) / (most * rounds), gx = std::min(most, (R + per - 1) / per);
     const int out_smem = L / 64 * (v_dim + (per + 7) / 8 * 16) * 128 + kOutWarps * 512;
