@@ -520,6 +520,26 @@ def test_prefill_bad_rows(bd):
     assert (out[20:] == 0).all()
 
 
+def test_prefill_overlapping_rows_stay_in_the_workspace(bd):
+    """Streams that claim the same rows have more query tiles than the
+    workspace is sized for; those past its end are left out."""
+    Hq, L, T, B = 2, 64, 700, 9
+    s = ref.make([T], [0], Hq, L, 64, 64, 63)
+    d = up(s)
+    d["table"] = s["table"].expand(B, -1).contiguous().cuda()
+    d["ctx_lens"] = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    rows = torch.tensor([0, T] * 5, dtype=torch.int32, device="cuda")      # streams 0, 2, 4, ...: all the rows
+    n = bd.tts_latent_prefill_attn_workspace_size(B, T, Hq, L, 64, 64, 5 * T)
+    ws = poisoned(n + 4096)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.empty((T, Hq, 64), dtype=torch.bfloat16, device="cuda")
+    bd.tts_latent_prefill_attn(bd.LatentCache(d["pool"], L), d["table"], d["ctx_lens"], 5 * T, rows, d["q_nope"],
+                               d["q_rope"], d["w_uk"], d["w_uv"], out, ws[:n], s["scale"], err=err)
+    torch.cuda.synchronize()
+    assert (ws[n:] == 0xFF).all()
+    assert int(err) == CTX_LEN
+
+
 def test_prefill_bad_blocks(bd):
     s = ref.make([150, 20, 40], [30, 0, 0], 4, 128, 64, 64, 37)
     nb = s["pool"].shape[0]
@@ -650,6 +670,37 @@ def test_append_far_positions(bd):
     q_out = run_append(bd, s, d, True, err=err)
     assert int(err) == 0
     _check_append(s, d, q_out)
+
+
+def test_blocks_beyond_32_bits(bd):
+    """Blocks whose values lie past 2^31 elements and 2^32 bytes of the pool."""
+    L, Hq, nblocks = 512, 4, 240_000                      # 2.2e9 elements, 4.4 GB
+    s = ref.make([9, 33], [70, 0], Hq, L, 128, 128, 61)
+    pool = torch.empty((nblocks, 16, L + 64), dtype=torch.bfloat16, device="cuda")
+    used = s["pool"].shape[0]
+    ids = torch.where(torch.arange(used) % 3 == 0, torch.arange(used), nblocks - 1 - torch.arange(used))
+    pool[ids.cuda()] = s["pool"].cuda()
+    d = up(s)
+    d["table"] = torch.where(s["table"] >= 0, ids[s["table"].clamp(min=0).long()].int(), s["table"]).cuda()
+    d["pool"] = pool
+    q = run_append(bd, s, d, ragged=True)
+    t = dict(s, pool=pool[ids.cuda()].cpu(), q_rope=q.cpu())
+    at = 0
+    for b, (n, before) in enumerate(zip(s["new"], s["before"])):
+        for j in range(n):
+            got = t["pool"][s["table"][b, (before + j) // 16].long(), (before + j) % 16]
+            assert torch.equal(got[:L], s["c_new"][at + j])
+            check_rotated(got[None, L:], s["kr_new"][at + j][None], torch.tensor([before + j]))
+        at += n
+    d["q_rope"] = q
+    want, tol = ref.attend_all(t, True, False)
+    check(run_prefill(bd, s, d), want, tol, "prompt")
+    u = ref.make([1, 1], [78, 32], Hq, L, 128, 128, 62)
+    t.update(new=[1, 1], T=2, row_start=u["row_start"], q_nope=u["q_nope"], q_rope=u["q_rope"])
+    e = dict(d, q_nope=u["q_nope"].cuda(), q_rope=u["q_rope"].cuda())
+    want, tol = ref.attend_all(t, False, True)
+    out = run_decode(bd, t, e, 1, False)
+    check(out.view(2, Hq, 128), want, tol, "step")
 
 
 def test_append_many_rows(bd):
