@@ -78,22 +78,23 @@ struct PrefillArgs {
 
 // ------------------------------------------------------------------ expand
 
-// K[t][h nope + d] = w_uk[h][d] . c_t (bf16) and V likewise (f16): a GEMM of 128-token
-// x 256-feature units.  Persistent, one CTA per SM, in clusters of two that
-// take neighbouring token tiles and the same features: each CTA fetches half of
-// a weight chunk for both (multicast), so a unit reads 256 KB from L2 for
-// 33 Mflop; 128 x 128 units that fetched both operands for themselves were
-// bound by those reads (10 TB/s of L2 to the SMs, 56 us at 8891 tokens x 4096
-// features x 512), and weights kept in shared memory left too short a ring
-// (90 us).  The accumulator is double buffered: one unit's results leave (through
-// shared memory, by TMA) while the next one's products run.
+// K[t][h nope + d] = w_uk[h][d] . c_t (bf16) and V likewise (f16): a GEMM of
+// 128-token x 256-feature units (128-feature ones for few tokens).  Persistent,
+// one CTA per SM, in clusters of two that take neighbouring token tiles and the
+// same features: each CTA fetches half of a weight chunk for both (multicast),
+// so a unit reads 256 KB from L2 for 33 Mflop; 128 x 128 units that fetched
+// both operands for themselves were bound by those reads (10 TB/s of L2 to the
+// SMs, 56 us at 8891 tokens x 4096 features x 512), and weights kept in shared
+// memory left too short a ring (90 us).  The accumulator is double buffered:
+// one unit's results leave (through shared memory, by TMA) while the next one's
+// products run.
 // Every CTA scans the streams by itself; CTA 0 writes the plan that the
 // attention reads.  The first feature unit of a token tile also copies the
 // tokens' rotated key parts and records which blocks are in the pool.
 constexpr int kExpandThreads = 224;        // 4 epilogue warps, producer, MMA issuer, spare (tensor memory)
 constexpr int kExpandSlots = 4;
 constexpr int kExpandCtas = 152;
-constexpr int kFeatures = 256;
+constexpr int kFeatures = 256, kWeightRows = 64;  // features per unit at most; weight rows per copy
 constexpr int kSlotBytes = 3 * kChunkBytes;    // 128 token rows, 256 feature rows of 64 values
 constexpr int kExpandSmem = kExpandSlots * kSlotBytes + 2 * kChunkBytes;
 
@@ -153,7 +154,7 @@ struct ExpandWalk {
 __global__ void __launch_bounds__(kExpandThreads, 1)
 latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_constant__ CUtensorMap map_uk,
                      const __grid_constant__ CUtensorMap map_uv, const __grid_constant__ CUtensorMap map_k,
-                     const __grid_constant__ CUtensorMap map_v, const PrefillArgs a, int k_tiles, int v_tiles) {
+                     const __grid_constant__ CUtensorMap map_v, const PrefillArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
     __shared__ ExpandShared sh;
     const uint32_t ring = smem_addr(raw), stage = ring + kExpandSlots * kSlotBytes;
@@ -172,6 +173,17 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         mbar_init(smem_addr(&sh.fin), 1);
         sh.limit = a.B;
         fence_mbar_init();
+    }
+    __syncwarp();
+    cluster_arrive();
+    if (warp == 4 && lane == 0) {
+        prefetch_tensormap(&map_pool);
+        prefetch_tensormap(&map_uk);
+        prefetch_tensormap(&map_uv);
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
     }
     if (warp == 6) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
@@ -245,8 +257,16 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         if (w < warp) t_at += sh.tiles[w];
         tiles += sh.tiles[w];
     }
-    const int feature_tiles = k_tiles + v_tiles, clusters = gridDim.x / 2, me = blockIdx.x / 2;
-    const int units = (tiles + 1) / 2 * feature_tiles;
+    // Units of 256 features, or of 128 where those still make one round of the
+    // clusters (one prompt of 333 rows, the whole call: 17.4 against 18.2 us; 16
+    // prompts whose 96 units of 256 make two rounds and 192 of 128 three: 30.8
+    // against 30.1)
+    const int clusters = gridDim.x / 2, me = blockIdx.x / 2, pairs = (tiles + 1) / 2;
+    auto tiles_of = [](int features, int each) { return (features + each - 1) / each; };
+    auto units_of = [&](int each) { return pairs * (tiles_of(a.Hq * a.nope, each) + tiles_of(a.Hq * a.v, each)); };
+    const int features = units_of(kFeatures / 2) <= clusters ? kFeatures / 2 : kFeatures;
+    const int k_tiles = tiles_of(a.Hq * a.nope, features), feature_tiles = k_tiles + tiles_of(a.Hq * a.v, features);
+    const int units = units_of(features);
     const int each = units / clusters;
     const int fewer = clusters - (units - each * clusters);  // the clusters behind these take one more
     const int u0 = me * each + max(0, me - fewer), u1 = u0 + each + (me >= fewer);
@@ -270,7 +290,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         t_at += nt;
     }
     __syncthreads();
-    cluster_sync();  // the peer's barriers are initialised
+    cluster_wait();  // the peer's barriers are initialised
     const uint32_t tmem = uniform(sh.tmem);
     ExpandWalk walk;
     walk.left = uniform(u1 - u0);
@@ -309,15 +329,17 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
             }
             have = walk.t;
             const bool is_k = walk.f < k_tiles;
-            const int row = (is_k ? walk.f : walk.f - k_tiles) * kFeatures + static_cast<int>(rank) * kTile;
+            const int row = (is_k ? walk.f : walk.f - k_tiles) * features + static_cast<int>(rank) * (features / 2);
             for (int c = 0; c < chunks; ++c) {
                 if (count >= kExpandSlots && !warp_wait(&sh.empty[slot], phase ^ 1)) {
                     ok = false;
                     break;
                 }
                 const uint32_t bar = smem_addr(&sh.full[slot]), to = ring + slot * kSlotBytes;
-                mbar_expect_tx_by(leader, bar, walk.exists() ? kSlotBytes : 2 * kChunkBytes);
-                tma_multicast_2d_by(leader, to + (1 + rank) * kChunkBytes, is_k ? &map_uk : &map_uv, c * 64, row, bar, 3);
+                mbar_expect_tx_by(leader, bar, (walk.exists() ? kChunkBytes : 0) + features * 128);
+                for (int i = 0; i < features / 2; i += kWeightRows)
+                    tma_multicast_2d_by(leader, to + kChunkBytes + (rank * (features / 2) + i) * 128, is_k ? &map_uk : &map_uv,
+                                        c * 64, row + i, bar, 3);
                 if (walk.exists())
 #pragma unroll
                     for (int i = 0; i < 8; ++i) tma_load_2d_by(leader, to + i * 2048, &map_pool, c * 64, ys[i], bar);
@@ -341,6 +363,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         // ---- MMA issuer; rows behind the context in its last block hold
         // anything and are cleared: their keys and values become zero
         const uint32_t leader = elect_leader();
+        const uint32_t idesc = uniform(features == kFeatures ? mma_idesc(kTile, kFeatures) : mma_idesc(kTile, kFeatures / 2));
         uint32_t slot = 0, phase = 0, done = 0;
         for (; ok && walk.left > 0; walk.advance(a), ++done) {
             const uint32_t buf = done & 1;
@@ -367,7 +390,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_bf16_by(leader, tmem + buf * kFeatures, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
-                                mma_idesc(kTile, kFeatures), (c | kk) != 0);
+                                idesc, (c | kk) != 0);
                 mma_commit_multicast_by(leader, smem_addr(&sh.empty[slot]), 3);
                 if (++slot == kExpandSlots) {
                     slot = 0;
@@ -401,11 +424,11 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
             }
             const uint32_t buf = done & 1;
             const bool is_k = walk.f < k_tiles;
-            const int f0 = (is_k ? walk.f : walk.f - k_tiles) * kFeatures, features = a.Hq * (is_k ? a.nope : a.v);
+            const int f0 = (is_k ? walk.f : walk.f - k_tiles) * features, all = a.Hq * (is_k ? a.nope : a.v);
             ok = warp_wait(&sh.acc_full[buf], (done / 2) & 1);
             tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < kFeatures / 64; ++q) {
+#pragma unroll 2
+            for (int q = 0; q < features / 64; ++q) {
                 // the staging half is free once the stores before the last have read it
                 if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 int fail;
@@ -445,7 +468,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
                 if (threadIdx.x == 0) {
-                    if (walk.exists() && f0 + q * 64 < features)
+                    if (walk.exists() && f0 + q * 64 < all)
                         tma_store_2d(is_k ? &map_k : &map_v, f0 + q * 64, walk.t * kTile, stage + (q & 1) * kChunkBytes);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
@@ -543,6 +566,11 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
         }
         mbar_init(smem_addr(&sh.done), 1);
         fence_mbar_init();
+        prefetch_tensormap(&map_qn);
+        prefetch_tensormap(&map_qr);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_kr);
+        prefetch_tensormap(&map_v);
     }
     if (warp == 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
@@ -884,7 +912,7 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
     CUtensorMap pool, uk, uv, qkv[5];
     if (!make_tma_2d_bf16(&pool, cache->pool, static_cast<uint64_t>(cache->num_blocks) * TTS_BLOCK_TOKENS,
                           L + kLatentRope, TTS_BLOCK_TOKENS, 64) ||
-        !make_tma_2d_bf16(&uk, d_w_uk, fk, L, kTile, 64) || !make_tma_2d_bf16(&uv, d_w_uv, fv, L, kTile, 64) ||
+        !make_tma_2d_bf16(&uk, d_w_uk, fk, L, kWeightRows, 64) || !make_tma_2d_bf16(&uv, d_w_uv, fv, L, kWeightRows, 64) ||
         !make_tma_2d_bf16(&qkv[0], d_q_nope, T, fk, kTile, 64) ||
         !make_tma_2d_bf16(&qkv[1], d_q_rope, T, static_cast<uint64_t>(Hq) * kLatentRope, kTile, 64) ||
         !make_tma_2d_bf16(&qkv[2], k, kv_rows, fk, kTile, 64) ||
@@ -893,11 +921,9 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
         return TTS_ERR_CUDA;
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const int k_tiles = static_cast<int>((fk + kFeatures - 1) / kFeatures);
-    const int v_tiles = static_cast<int>((fv + kFeatures - 1) / kFeatures);
     if (!allow_smem(latent_expand_kernel, kExpandSmem)) return TTS_ERR_CUDA;
     const int rc = launch_cluster(2, latent_expand_kernel, dim3(kExpandCtas), dim3(kExpandThreads), kExpandSmem,
-                                  {cs, thread_pdl()}, pool, uk, uv, qkv[2], qkv[4], a, k_tiles, v_tiles);
+                                  {cs, thread_pdl()}, pool, uk, uv, qkv[2], qkv[4], a);
     if (rc != TTS_OK) return rc;
     const unsigned grid = static_cast<unsigned>(pl.qtiles * Hq);
     if (nope_dim == 128)
