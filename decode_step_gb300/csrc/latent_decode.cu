@@ -153,10 +153,13 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_co
 
 // The work units are the 64-token tiles of every (stream, row group), group
 // bg = b * G + g, in order, cut evenly over the CTAs; each group has one unit
-// before its tiles, which stands for what starting and ending a group costs (a
-// tile's time, about).  The part of a group
-// that a CTA takes is a segment; its partial result goes to slot c + bg
-// (unique: going on to the next segment raises one of the two).
+// before its tiles (two with 48 rows or more), which stands for what starting
+// and ending a group costs (a tile's time, about; 80 verify rows a stream: 53.1
+// us the call with two, 53.6 with one).  The part of a group that a CTA takes is
+// a segment; its partial result goes to slot c + bg (unique: going on to the
+// next segment raises one of the two).
+__host__ __device__ constexpr int start_units(int N) { return N >= 48 ? 2 : 1; }
+
 struct LatentPlan {
     int G, N;       // row groups a stream, rows per group (a multiple of 16)
     int P;          // CTAs
@@ -171,7 +174,7 @@ LatentPlan latent_plan(int B, int q_len, int Hq, int L, int max_ctx) {
     const int rows = q_len * Hq;
     p.G = (rows + kMaxGroup - 1) / kMaxGroup;
     p.N = ((rows + p.G - 1) / p.G + 15) / 16 * 16;
-    p.units = static_cast<long>(B) * p.G * ((static_cast<long>(max_ctx) + kTile - 1) / kTile + 1);
+    p.units = static_cast<long>(B) * p.G * ((static_cast<long>(max_ctx) + kTile - 1) / kTile + start_units(p.N));
     p.P = p.units < kCtas ? static_cast<int>(p.units < 1 ? 1 : p.units) : kCtas;
     p.slots = static_cast<size_t>(p.P) + static_cast<size_t>(B) * p.G;
     p.qt_bytes = align_up(static_cast<size_t>(B) * rows * L * 2, 256);
@@ -201,7 +204,7 @@ struct LatentAttnArgs {
     int max_blocks, num_blocks;
     const int32_t *ctx_lens;
     int max_ctx, B, q_len, Hq, L;
-    int G;
+    int G, start;      // row groups a stream, units before a group's tiles
     float scale_log2;  // scale * log2(e)
     int causal;
     float *part;       // [slots][N][L] unnormalised o~
@@ -220,7 +223,7 @@ __device__ __forceinline__ int stream_tiles(const LatentAttnArgs &a, int ctx) {
 // Units of one of stream b's groups (0: its length is out of range).
 __device__ __forceinline__ int group_units(const LatentAttnArgs &a, int b) {
     const int n = stream_tiles(a, __ldg(a.ctx_lens + b));
-    return n ? n + 1 : 0;
+    return n ? n + a.start : 0;
 }
 
 // A block's scan of the streams: thread t has the streams b0..b1 - 1, the first
@@ -276,9 +279,9 @@ struct Segments {
                 look(a);
                 continue;
             }
-            const int units = min(n + 1 - unit, left);
-            first = max(unit - 1, 0);
-            count = unit + units - 1 - first;
+            const int units = min(n + a.start - unit, left);
+            first = max(unit - a.start, 0);
+            count = unit + units - a.start - first;
             cur_b = b;
             cur_g = g;
             bg = b * a.G + g;
@@ -352,7 +355,7 @@ constexpr int kMaxPairs = 16, kMaxRopes = 8;
 
 struct AttnShared {
     uint64_t full[kMaxRopes], empty_l[kMaxPairs], empty_r[kMaxRopes];
-    uint64_t s_full[2], p_full[2], p_empty[2], o_empty, q_full[2], q_empty[2], done;
+    uint64_t s_full[2], p_full[2], p_empty[2], o_empty, q_full, q_empty, done;
     int start_b, start_g, start_unit;
     uint32_t tmem;
     int sums[8];
@@ -369,8 +372,6 @@ struct AttnShared {
 // Buffers for the weights P: with one, the softmax waits for the O^T of the
 // tile before; wide groups need the space for the ring.
 __host__ __device__ constexpr int p_buffers(int N) { return N == 16 || N == 48 ? 2 : 1; }
-// Buffers for q~: with two, a segment's rows are there when the one before ends.
-__host__ __device__ constexpr int q_buffers(int N) { return N <= 32 ? 2 : 1; }
 
 // P enters the product as two bf16 numbers, its rounding and the remainder:
 // the weights are then held to 2^-17.  Up to 48 rows the remainders are N more
@@ -388,11 +389,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                    const __grid_constant__ CUtensorMap map_qr, const LatentAttnArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = smem_addr(raw);
-    constexpr int kPBufs = p_buffers(N), kQBufs = q_buffers(N);
+    constexpr int kPBufs = p_buffers(N);
     constexpr int kO = p_rows(N), kPBytes = kO * 128;  // columns of O^T (rows of P), bytes of a P buffer
     const int chunks = a.L / 64, nb = (a.L + 127) / 128;
-    const uint32_t q_base = base, q_bytes = (chunks + 1) * N * 128;     // [kQBufs][chunks + 1][N][128 B]
-    const uint32_t p_base = q_base + kQBufs * q_bytes;                  // [kPBufs][kO][128 B]
+    const uint32_t q_base = base, q_bytes = (chunks + 1) * N * 128;     // [chunks + 1][N][128 B]
+    const uint32_t p_base = q_base + q_bytes;                           // [kPBufs][kO][128 B]
     const uint32_t r_base = p_base + kPBufs * kPBytes;                         // rope ring
     const uint32_t l_base = r_base + a.ropes * kChunkBytes;             // latent ring
     AttnShared &sh = *reinterpret_cast<AttnShared *>(raw + (l_base - base) + a.pairs * kPairBytes);
@@ -408,9 +409,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             mbar_init(smem_addr(&sh.s_full[i]), 1);
             mbar_init(smem_addr(&sh.p_full[i]), 4);
             mbar_init(smem_addr(&sh.p_empty[i]), 1);
-            mbar_init(smem_addr(&sh.q_full[i]), 1);
-            mbar_init(smem_addr(&sh.q_empty[i]), 1);
         }
+        mbar_init(smem_addr(&sh.q_full), 1);
+        mbar_init(smem_addr(&sh.q_empty), 1);
         mbar_init(smem_addr(&sh.o_empty), 4);
         mbar_init(smem_addr(&sh.done), 1);
         sh.failed = 0;
@@ -445,7 +446,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             if (blockIdx.x == 0) {
                 if (w == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
                 for (int g = 0; g < a.G; ++g) {
-                    const int first = w ? cut.owner(at + g * w + 1) : 0;
+                    const int first = w ? cut.owner(at + g * w + a.start) : 0;
                     a.owner[b * a.G + g] = make_int2(first, w ? cut.owner(at + (g + 1) * w - 1) - first + 1 : 0);
                 }
             }
@@ -534,19 +535,17 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         const uint32_t leader = elect_leader();
         uint32_t s = 0;
         for (; seg.next(a); ++s) {
-            const uint32_t qb = s % kQBufs, use = s / kQBufs;
-            if (use > 0 && !warp_wait(&sh.q_empty[qb], (use - 1) & 1)) {
+            if (s > 0 && !warp_wait(&sh.q_empty, (s - 1) & 1)) {
                 ok = false;
                 break;
             }
-            const uint32_t bar = smem_addr(&sh.q_full[qb]), at = q_base + qb * q_bytes;
+            const uint32_t bar = smem_addr(&sh.q_full);
             mbar_expect_tx_by(leader, bar, q_bytes);
             const int y = seg.cur_b * a.q_len * a.Hq + seg.cur_g * N;
-            for (int c = 0; c < chunks; ++c) tma_load_2d_by(leader, at + c * N * 128, &map_q, c * 64, y, bar);
-            tma_load_2d_by(leader, at + chunks * N * 128, &map_qr, 0, y, bar);
+            for (int c = 0; c < chunks; ++c) tma_load_2d_by(leader, q_base + c * N * 128, &map_q, c * 64, y, bar);
+            tma_load_2d_by(leader, q_base + chunks * N * 128, &map_qr, 0, y, bar);
         }
-        for (uint32_t i = s > kQBufs ? s - kQBufs : 0; i < s; ++i)
-            warp_wait(&sh.q_full[i % kQBufs], (i / kQBufs) & 1);
+        if (s > 0) warp_wait(&sh.q_full, (s - 1) & 1);
     } else if (warp == 5) {
         // ---- MMA issuer (the warp runs converged; it also clears stale rows).
         // S^T of tile i + 1 goes before O^T of tile i, so the tensor core works
@@ -592,7 +591,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         };
         while (ok && seg.next(a)) {
             const int count = seg.count, left = seg.ctx - seg.first * kTile;  // tokens from the first tile on
-            const uint32_t qs = q_base + segs % kQBufs * q_bytes;
             for (int k = 0; k < count; ++k) {
                 const uint32_t buf = it & 1;
                 // the tile and the queries (S's buffer is free: the weights
@@ -600,7 +598,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 WarpWaits<2> w;
                 w.set(0, &sh.full[rope.slot], rope.phase);
                 w.none(1);
-                if (k == 0) w.set(1, &sh.q_full[segs % kQBufs], (segs / kQBufs) & 1);
+                if (k == 0) w.set(1, &sh.q_full, segs & 1);
                 const Ring first = lat;
                 // a tile that is still landing lets O^T of the one before go
                 // first, if its weights are there: that frees ring slots
@@ -623,12 +621,12 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     mma_bf16_by(leader, tmem + buf * N, sw128_desc(sr + kk * 32),
-                                sw128_desc(qs + chunks * N * 128 + kk * 32), idesc_s, kk != 0);
+                                sw128_desc(q_base + chunks * N * 128 + kk * 32), idesc_s, kk != 0);
                 const uint32_t rope_slot = rope.slot;
                 if constexpr (p_beside(N)) mma_commit_by(leader, smem_addr(&sh.empty_r[rope_slot]));
                 rope.next();
                 for (int p = 0; p < nb; ++p) {
-                    const uint32_t sa = l_base + lat.slot * kPairBytes, sb = qs + 2 * p * N * 128;
+                    const uint32_t sa = l_base + lat.slot * kPairBytes, sb = q_base + 2 * p * N * 128;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_bf16_by(leader, tmem + buf * N, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32), idesc_s, 1);
@@ -640,7 +638,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     lat.next();
                 }
                 mma_commit_by(leader, smem_addr(&sh.s_full[buf]));
-                if (k + 1 == count) mma_commit_by(leader, smem_addr(&sh.q_empty[segs % kQBufs]));
+                if (k + 1 == count) mma_commit_by(leader, smem_addr(&sh.q_empty));
                 if (pending) {
                     if (!weights(it - 1).wait()) {
                         ok = false;
@@ -1182,7 +1180,7 @@ int launch_attention(const CUtensorMap &kv, const CUtensorMap &q, const CUtensor
                      cudaStream_t stream) {
     // shared memory: q~, P, the rope slots, and latent pairs to the brim
     const int chunks = a.L / 64;
-    const int fixed = (q_buffers(N) * (chunks + 1) * N + p_buffers(N) * p_rows(N)) * 128 + static_cast<int>(sizeof(AttnShared));
+    const int fixed = ((chunks + 1) * N + p_buffers(N) * p_rows(N)) * 128 + static_cast<int>(sizeof(AttnShared));
     const int nb = (a.L + 127) / 128, tiles = (kSmemLimit - fixed) / (kChunkBytes + nb * kPairBytes);
     a.ropes = std::min(std::max(tiles, 2), kMaxRopes);  // a rope slot for every tile on its way
     a.pairs = std::min((kSmemLimit - fixed - a.ropes * kChunkBytes) / kPairBytes, kMaxPairs);
@@ -1238,6 +1236,7 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     a.Hq = num_q_heads;
     a.L = L;
     a.G = pl.G;
+    a.start = start_units(pl.N);
     a.scale_log2 = scale * kLog2e;
     a.causal = causal != 0;
     a.part = reinterpret_cast<float *>(ws + pl.qt_bytes);
