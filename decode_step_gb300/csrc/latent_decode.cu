@@ -893,17 +893,73 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
 
 // out[r][h] = w_uv[h] o~[r][h], o~ the join of the row's splits (weights
 // 2^(m_s - max m)).  A CTA takes one head and shares the rows evenly with the
-// head's others, in rounds of up to 40; its warps join the rows' splits into
-// the B operand (few rows share the warps), then one product D[v][rows] with
-// the head's weights.  o~ enters as two bf16 numbers, its rounding in the first
-// half of the columns and the remainder in the other, so that it is held to
-// 2^-17 (the MMA's time is that of reading the weights).
+// head's others; its warps join the rows' splits into the B operand, then one
+// product D[v][rows] with the head's weights.  o~ enters as two bf16 numbers,
+// its rounding in the first half of the columns and the remainder in the other,
+// so that it is held to 2^-17 (the MMA's time is that of reading the weights).
 // Latency-bound: the weights are in flight before the wait for the attention,
 // and a row's partial results are read together with their maxima and sums.
-// 6.3 us for one row of one split, 10 us for 256 rows, 9.4 us for one row of
-// 152 splits, 11.5 us for 320 rows (27 MB of partial sums, from L2).
+// 6.3 us for one row of one split, 7 us for 64 rows, 9.4 us for one row of 152
+// splits, 11.5 us for 320 rows (27 MB of partial sums, from L2).
+// Up to 80 rows a CTA go through in one or two rounds, one after the other
+// (latent_out_kernel; few rows share the warps).  More go through in rounds of
+// 24 whose joins, products and stores overlap (latent_out_rounds_kernel).  The
+// whole call, without and with: 512 rows of 16 heads (57 a CTA) 51.5 and 53.4
+// us, 768 rows (86) 61.8 and 59.6 us, 1185 rows of 20 heads 112 and 106 us, 1128
+// rows of short contexts 55.5 and 47.1 us.
 constexpr int kOutThreads = 512, kOutWarps = kOutThreads / 32;
-constexpr int kOutRows = 40;
+constexpr int kOutRows = 40;               // rows a round of latent_out_kernel, at most
+constexpr int kJoinWarps = 12, kRoundRows = 24;
+constexpr int kRoundThreads = (4 + kJoinWarps + 1) * 32;  // stores, joins, weights and MMAs
+constexpr int kRoundCols = 2 * kRoundRows;
+
+// Group of query row r's head h, and the row in it.
+__device__ __forceinline__ int group_of(const LatentAttnArgs &a, int N, int r, int h, int &n) {
+    const int b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h, grp = idx / N;
+    n = idx - grp * N;
+    return b * a.G + grp;
+}
+
+// Two values of row i at dimensions l and l + 1 into the operand [L / 64][cols][64],
+// 128-byte swizzled: roundings, remainders cols / 2 rows on.
+__device__ __forceinline__ void put_joined(uint8_t *joined, int cols, int i, int l, float x, float y) {
+    uint8_t *to = joined + (l / 64 * cols + i) * 128 + (((l % 64 / 8) ^ (i & 7)) << 4) + l % 8 * 2;
+    const uint32_t hi = pack_bf16(x, y);
+    *reinterpret_cast<uint32_t *>(to) = hi;
+    *reinterpret_cast<uint32_t *>(to + cols * 64) = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+}
+
+// D[v][cols] = the head's weights . the joined rows, by one warp.
+__device__ __forceinline__ void out_product(uint32_t leader, uint32_t d, uint32_t weights, uint32_t joined, int chunks,
+                                            int v_dim, int cols) {
+    const uint32_t idesc = mma_idesc(v_dim, cols);
+    for (int c = 0; c < chunks; ++c)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_by(leader, d, sw128_desc(weights + c * v_dim * 128 + kk * 32), sw128_desc(joined + c * cols * 128 + kk * 32),
+                        idesc, (c | kk) != 0);
+}
+
+// Stores `rows` rows from r0 on by four warps (`warp` 0-3), lane = output
+// dimension: 32 w + lane of a 128-row accumulator, 16 w + lane (lane < 16) of a
+// 64-row one; 2-byte stores, 64 bytes a warp.
+__device__ __forceinline__ void store_rows(const LatentAttnArgs &a, int warp, uint32_t tmem, int cols, int v_dim, int h,
+                                           int r0, int rows, __nv_bfloat16 *out) {
+    const int lane = threadIdx.x % 32, d = v_dim == 128 ? warp * 32 + lane : warp * 16 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    for (int i = 0; i < rows; i += 8) {
+        uint32_t x[8], y[8];
+        tmem_ld8_nowait(tl + i, x);
+        tmem_ld8_nowait(tl + cols / 2 + i, y);
+        tmem_wait_ld();
+        if (v_dim == 128 || lane < 16)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k < rows)
+                    out[(static_cast<size_t>(r0 + i + k) * a.Hq + h) * v_dim + d] =
+                        __float2bfloat16_rn(__uint_as_float(x[k]) + __uint_as_float(y[k]));
+    }
+}
 
 // Joins `count` splits of one row by a warp, two read together: o (4 x 128
 // dimensions) is scaled by 2^-M, M the largest of the splits' maxima, and S is
@@ -1035,12 +1091,6 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(tslot);
-    auto put = [&](int i, int l, float x, float y) {  // two values of row i at dimensions l, l + 1
-        uint8_t *to = joined + (l / 64 * cols + i) * 128 + (((l % 64 / 8) ^ (i & 7)) << 4) + l % 8 * 2;
-        const uint32_t hi = pack_bf16(x, y);
-        *reinterpret_cast<uint32_t *>(to) = hi;
-        *reinterpret_cast<uint32_t *>(to + cols * 64) = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
-    };
     for (uint32_t round = 0;; ++round) {
         const int r0 = (blockIdx.x + round * gridDim.x) * rows_per_round, rows = min(rows_per_round, R - r0);
         if (rows <= 0) break;
@@ -1051,22 +1101,17 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
         const int ldims = lshare ? lq : 0, lss = lshare - ldims, ss = 1 << lss;
         const int sub = warp & ((1 << lshare) - 1), i0 = warp >> lshare;
         const int first = sub >> ldims, d0 = (sub & ((1 << ldims) - 1)) * 128 + 4 * lane;
-        auto group = [&](int i, int &n) {  // of this round's row i, and the row in it
-            const int r = r0 + i, b = r / a.q_len, idx = (r - b * a.q_len) * a.Hq + h, grp = idx / N;
-            n = idx - grp * N;
-            return b * a.G + grp;
-        };
         if (round == 0) {
             pdl_wait_prerequisites();
             pdl_allow_dependents();
         }
-        int n, bg = group(min(i0, rows - 1), n);
+        int n, bg = group_of(a, N, r0 + min(i0, rows - 1), h, n);
         int2 own = __ldcg(a.owner + bg);
         for (int rr = 0; rr < rows; rr += kOutWarps >> lshare) {
             const int i = rr + i0;
             // the next row's owner is read a row ahead
             int n_next;
-            const int bg_next = group(min(i + (kOutWarps >> lshare), rows - 1), n_next);
+            const int bg_next = group_of(a, N, r0 + min(i + (kOutWarps >> lshare), rows - 1), h, n_next);
             const int2 own_next = __ldcg(a.owner + bg_next);
             if (i < rows) {
                 const size_t row = (static_cast<size_t>(own.x) + bg) * N + n;
@@ -1085,8 +1130,8 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (d0 + 128 * k < L && (k == 0 || !lshare)) {
-                            put(i, d0 + 128 * k, o[k].x * inv, o[k].y * inv);
-                            put(i, d0 + 128 * k + 2, o[k].z * inv, o[k].w * inv);
+                            put_joined(joined, cols, i, d0 + 128 * k, o[k].x * inv, o[k].y * inv);
+                            put_joined(joined, cols, i, d0 + 128 * k + 2, o[k].z * inv, o[k].w * inv);
                         }
                 } else {
                     if (lane == 0) ms[warp] = make_float2(M, S);
@@ -1110,8 +1155,8 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
                         x.w = fmaf(f, y.w, x.w);
                     }
                     const float inv = S == 0.0f ? 0.0f : 1.0f / S;
-                    put(i, d0, x.x * inv, x.y * inv);
-                    put(i, d0 + 2, x.z * inv, x.w * inv);
+                    put_joined(joined, cols, i, d0, x.x * inv, x.y * inv);
+                    put_joined(joined, cols, i, d0 + 2, x.z * inv, x.w * inv);
                 }
             }
             own = own_next;
@@ -1126,33 +1171,13 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
             const uint32_t leader = elect_leader();
             if (!warp_wait(&full, 0)) ok = false;
             tc_fence_after();
-            const uint32_t idesc = mma_idesc(v_dim, cols), ob = wb + chunks * w_chunk;
-            for (int c = 0; c < chunks; ++c)
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16_by(leader, tmem, sw128_desc(wb + c * w_chunk + kk * 32), sw128_desc(ob + c * cols * 128 + kk * 32),
-                                idesc, (c | kk) != 0);
+            out_product(leader, tmem, wb, smem_addr(joined), chunks, v_dim, cols);
             mma_commit_by(leader, smem_addr(&acc));
         }
         if (warp < 4) {
             if (!warp_wait(&acc, round & 1)) ok = false;
             tc_fence_after();
-            // lane = output dimension: 32 w + lane of a 128-row accumulator, 16
-            // w + lane (lane < 16) of a 64-row one; 2-byte stores, 64 bytes a warp
-            const int d = v_dim == 128 ? warp * 32 + lane : warp * 16 + lane;
-            const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-            for (int i = 0; i < rows; i += 8) {
-                uint32_t x[8], y[8];
-                tmem_ld8_nowait(tl + i, x);
-                tmem_ld8_nowait(tl + cols / 2 + i, y);
-                tmem_wait_ld();
-                if (ok && (v_dim == 128 || lane < 16))
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (i + k < rows)
-                            out[(static_cast<size_t>(r0 + i + k) * a.Hq + h) * v_dim + d] =
-                                __float2bfloat16_rn(__uint_as_float(x[k]) + __uint_as_float(y[k]));
-            }
+            if (ok) store_rows(a, warp, tmem, cols, v_dim, h, r0, rows, out);
         }
         // the next rows' operand and accumulator take the places of these
         tc_fence_before();
@@ -1161,6 +1186,135 @@ latent_out_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnAr
     }
     if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
     if (warp == 0) {
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
+    }
+}
+
+// The same for more rows a CTA (`per` of them, from per x blockIdx.x on), `each`
+// (up to 24) a round: twelve warps join two rows each into one of two operands,
+// one warp issues the products, four store.
+__global__ void __launch_bounds__(kRoundThreads)
+latent_out_rounds_kernel(const __grid_constant__ CUtensorMap map_uv, const LatentAttnArgs a, int N, int per, int each,
+                         int v_dim, __nv_bfloat16 *__restrict__ out) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    __shared__ uint64_t full, joined_full[2], joined_empty[2], acc_full[2], acc_empty[2], fin;
+    __shared__ uint32_t tslot;
+    const int L = a.L, chunks = L / 64;
+    const uint32_t w_chunk = v_dim * 128, j_bytes = chunks * kRoundCols * 128;
+    uint8_t *joined = raw + chunks * w_chunk;                      // [2][chunks][48][64 l], after [chunks][v][64 l]
+    const uint32_t wb = smem_addr(raw), jb = smem_addr(joined);
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+    const int h = blockIdx.y, begin = blockIdx.x * per, end = min(begin + per, a.B * a.q_len);
+    const int rounds = (end - begin + each - 1) / each;
+    constexpr int kIssuer = 4 + kJoinWarps;
+    bool ok = true;
+    if (warp == kIssuer) {
+        const uint32_t leader = elect_leader();
+        if (leader) {
+            mbar_init(smem_addr(&full), 1);
+            mbar_init(smem_addr(&fin), 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_addr(&joined_full[i]), kJoinWarps);
+                mbar_init(smem_addr(&joined_empty[i]), 1);
+                mbar_init(smem_addr(&acc_full[i]), 1);
+                mbar_init(smem_addr(&acc_empty[i]), 4);
+            }
+            fence_mbar_init();
+        }
+        __syncwarp();
+        mbar_expect_tx_by(leader, smem_addr(&full), chunks * w_chunk);
+        for (int c = 0; c < chunks; ++c)
+            tma_load_2d_by(leader, wb + c * w_chunk, &map_uv, 64 * c, h * v_dim, smem_addr(&full));
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tslot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uniform(tslot);
+    if (warp == kIssuer) {
+        const uint32_t leader = elect_leader();
+        ok = warp_wait(&full, 0);
+        for (int k = 0; ok && k < rounds; ++k) {
+            const int buf = k & 1;
+            WarpWaits<2> w;
+            w.set(0, &joined_full[buf], (k / 2) & 1);
+            w.none(1);
+            if (k >= 2) w.set(1, &acc_empty[buf], (k / 2 - 1) & 1);
+            ok = w.wait();
+            if (!ok) break;
+            tc_fence_after();
+            out_product(leader, tmem + buf * kRoundCols, wb, jb + buf * j_bytes, chunks, v_dim, kRoundCols);
+            mma_commit_by(leader, smem_addr(&joined_empty[buf]));
+            mma_commit_by(leader, smem_addr(&acc_full[buf]));
+        }
+        mma_commit_by(leader, smem_addr(&fin));
+        if (!warp_wait(&fin, 0)) ok = false;
+    } else if (warp >= 4) {
+        const int i = warp - 4;
+        int dims[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dims[k] = min(4 * lane + 128 * k, L - 4);
+        const size_t step = static_cast<size_t>(N) * L;
+        pdl_wait_prerequisites();
+        pdl_allow_dependents();
+        int n, bg = group_of(a, N, min(begin + i, end - 1), h, n);
+        int2 own = __ldcg(a.owner + bg);
+        for (int k = 0; ok && k < rounds; ++k) {
+            const int buf = k & 1, r0 = begin + k * each, rows = min(each, end - r0);
+            for (int j = i; j < each; j += kJoinWarps) {
+                // (the next row's owner is read a row ahead)
+                int n_next;
+                const int r_next = j + kJoinWarps < each ? r0 + j + kJoinWarps : r0 + each + i;
+                const int bg_next = group_of(a, N, min(r_next, end - 1), h, n_next);
+                const int2 own_next = __ldcg(a.owner + bg_next);
+                const size_t row = (static_cast<size_t>(own.x) + bg) * N + n;
+                float4 o[4] = {};
+                float M = kNoScore, S = 0.0f;
+                if (j < rows) join_row(a.part + row * L, step, a.ml + row, N, own.y, dims, o, M, S);
+                if (j == i && k >= 2 && !warp_wait(&joined_empty[buf], (k / 2 - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (j < rows) {
+                    const float inv = S == 0.0f ? 0.0f : 1.0f / S;  // no token left: zeros
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int d = 4 * lane + 128 * q;
+                        if (d < L) {
+                            put_joined(joined + buf * j_bytes, kRoundCols, j, d, o[q].x * inv, o[q].y * inv);
+                            put_joined(joined + buf * j_bytes, kRoundCols, j, d + 2, o[q].z * inv, o[q].w * inv);
+                        }
+                    }
+                }
+                own = own_next;
+                n = n_next;
+                bg = bg_next;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(smem_addr(&joined_full[buf]));
+        }
+    } else {
+        for (int k = 0; k < rounds; ++k) {
+            const int buf = k & 1, r0 = begin + k * each;
+            if (!warp_wait(&acc_full[buf], (k / 2) & 1)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            store_rows(a, warp, tmem + buf * kRoundCols, kRoundCols, v_dim, h, r0, min(each, end - r0), out);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&acc_empty[buf]));
+        }
+    }
+    if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kIssuer) {
+        tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem) : "memory");
     }
 }
@@ -1270,12 +1424,20 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
         default: rc = launch_attention<64>(map_kv, map_q, map_qr, a, pl.P, cs); break;
     }
     if (rc != TTS_OK) return rc;
-    // one CTA fits an SM: as many as there are SMs share the rows evenly, in
-    // rounds of up to 40 that keep the weights
-    const int most = std::max(1, kCtas / Hq), rounds = (R + most * kOutRows - 1) / (most * kOutRows);
-    const int per = (R + most * rounds - 1) / (most * rounds), gx = std::min(most, (R + per - 1) / per);
-    const int out_smem = L / 64 * (v_dim + (per + 7) / 8 * 16) * 128 + kOutWarps * 512;
-    if (!allow_smem(latent_out_kernel, out_smem)) return TTS_ERR_CUDA;
-    return launch_kernel(latent_out_kernel, dim3(gx, Hq), dim3(kOutThreads), out_smem, {cs, true}, map_uv,
-                         a, pl.N, per, static_cast<int>(v_dim), static_cast<__nv_bfloat16 *>(d_out));
+    // one CTA fits an SM: as many as there are SMs share the rows evenly
+    const int most = std::max(1, kCtas / Hq), cta_rows = (R + most - 1) / most;
+    auto *o = static_cast<__nv_bfloat16 *>(d_out);
+    const int v = v_dim;
+    if (cta_rows <= 2 * kOutRows) {
+        const int rounds = cta_rows > kOutRows ? 2 : 1;
+        const int per = (R + most * rounds - 1) / (most * rounds), gx = std::min(most, (R + per - 1) / per);
+        const int smem = L / 64 * (v + (per + 7) / 8 * 16) * 128 + kOutWarps * 512;
+        if (!allow_smem(latent_out_kernel, smem)) return TTS_ERR_CUDA;
+        return launch_kernel(latent_out_kernel, dim3(gx, Hq), dim3(kOutThreads), smem, {cs, true}, map_uv, a, pl.N, per, v, o);
+    }
+    const int rounds = (cta_rows + kRoundRows - 1) / kRoundRows, each = (cta_rows + rounds - 1) / rounds;
+    const int smem = L / 64 * (v + 2 * kRoundCols) * 128;
+    if (!allow_smem(latent_out_rounds_kernel, smem)) return TTS_ERR_CUDA;
+    return launch_kernel(latent_out_rounds_kernel, dim3((R + cta_rows - 1) / cta_rows, Hq), dim3(kRoundThreads), smem,
+                         {cs, true}, map_uv, a, pl.N, cta_rows, each, v, o);
 }

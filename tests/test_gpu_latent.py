@@ -247,6 +247,12 @@ def test_decode_many_rows(bd):
     decode_case(bd, [300, 128], 8, 128, 128, 64, 64, True)       # 1024 query rows a stream
 
 
+@pytest.mark.parametrize("B,q_len,Hq,L,nope,v", [(42, 2, 152, 512, 64, 128), (85, 8, 20, 192, 128, 64), (30, 2, 152, 64, 64, 64)])
+def test_decode_many_rows_per_head(bd, B, q_len, Hq, L, nope, v):
+    """So many rows a head that the output product takes them in rounds."""
+    decode_case(bd, [q_len + (5 * i) % 23 for i in range(B)], q_len, Hq, L, nope, v, True)
+
+
 def test_decode_ragged_batch(bd):
     ctx = [1 + (37 * i * i) % 700 for i in range(70)]
     decode_case(bd, ctx, 1, 8, 256, 64, 64, False)
