@@ -19,8 +19,8 @@
 // Bound: HBM at one query row a stream (16 heads: 30 flop a byte).  HBM
 // delivers a 64-token tile's 73.7 KB to an SM in 1.65 us; its 36 + 16 MMAs take
 // 1.1 us at N <= 32 (an M = 64 MMA of 16 to 64 columns 38 to 42 cycles, an M =
-// 128 one 48 to 52), and the ring holds two and a half tiles, so that a tile
-// takes 2.0 us.  With 48 rows (a verify step's 80 in two groups) the second
+// 128 one 48 to 52), and the ring holds 2.75 tiles, so that a tile takes
+// 2.0 us.  With 48 rows (a verify step's 80 in two groups) the second
 // group's reads come from L2, and the two tiles that fit beside the queries
 // turn loads and MMAs into a chain of 1.6 us a tile; ending a segment costs
 // another 2 to 3 us (98 KB of partial sums).  Measured, 16 heads, latent 512:
