@@ -93,18 +93,19 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_co
         mbar_expect_tx_by(leader, smem_addr(&full), halves * w_chunk + nope / 64 * q_chunk);
         for (int i = 0; i < halves; ++i)
             tma_load_2d_by(leader, wb + i * w_chunk, &map_uk, l0 + 64 * i, h * nope, smem_addr(&full));
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tslot))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         pdl_wait_prerequisites();
         for (int i = 0; i < nope / 64; ++i)
             tma_load_2d_by(leader, qb + i * q_chunk, &map_qn, h * nope + 64 * i, r0, smem_addr(&full));
+        // (tensor memory only after the wait: the kernel before may be one that
+        // still has to allocate its own)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(smem_addr(&tslot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp != 0) pdl_wait_prerequisites();
-    pdl_allow_dependents();  // only now: the attention reads the pool as soon as it starts
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_allow_dependents();  // only now: the attention allocates tensor memory and reads the pool as soon as it starts
     const uint32_t tmem = uniform(tslot);
     if (warp == 0) {
         const uint32_t leader = elect_leader();

@@ -185,13 +185,14 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
+    pdl_wait_prerequisites();
+    // (tensor memory only after the wait: the kernel before may be one that
+    // still has to allocate its own)
     if (warp == 6) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    pdl_wait_prerequisites();
-    pdl_allow_dependents();
     // ---- the streams' token tiles
     const int per = (a.B + kExpandThreads - 1) / kExpandThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
@@ -224,6 +225,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_allow_dependents();
     long long at = incl - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < kExpandThreads / 32; ++w) {
