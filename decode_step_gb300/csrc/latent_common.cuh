@@ -35,33 +35,24 @@ inline bool allow_smem(void (*kernel)(P...), int bytes) {
     return ensure_dynamic_smem(reinterpret_cast<const void *>(kernel), bytes > kNoLeave ? bytes : kNoLeave + 16);
 }
 
-// Launches a kernel, as a programmatic dependent of the one before it if
-// o.pdl, in clusters of `cluster` CTAs.
+// Launches a kernel, as a programmatic dependent of the one before it if o.pdl.
 template <typename... P, typename... A>
-inline int launch_cluster(unsigned cluster, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, LaunchOpts o,
-                          A &&...args) {
+inline int launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, LaunchOpts o, A &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = o.stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {cluster, 1, 1};
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = o.pdl ? 2 : 1;
+    cfg.numAttrs = o.pdl ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...) != cudaSuccess) {
         cudaGetLastError();
         return TTS_ERR_CUDA;
     }
     return TTS_OK;
-}
-
-template <typename... P, typename... A>
-inline int launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, LaunchOpts o, A &&...args) {
-    return launch_cluster(1, kernel, grid, block, smem, o, static_cast<A &&>(args)...);
 }
 
 // Lane 0's value, which the compiler then knows to be the same in every lane:

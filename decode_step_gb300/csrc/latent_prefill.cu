@@ -80,21 +80,19 @@ struct PrefillArgs {
 
 // K[t][h nope + d] = w_uk[h][d] . c_t (bf16) and V likewise (f16): a GEMM of
 // 128-token x 256-feature units (128-feature ones for few tokens).  Persistent,
-// one CTA per SM, in clusters of two that take neighbouring token tiles and the
-// same features: each CTA fetches half of a weight chunk for both (multicast),
-// so a unit reads 256 KB from L2 for 33 Mflop; 128 x 128 units that fetched
-// both operands for themselves were bound by those reads (10 TB/s of L2 to the
-// SMs, 56 us at 8891 tokens x 4096 features x 512), and weights kept in shared
-// memory left too short a ring (90 us).  The accumulator is double buffered:
-// one unit's results leave (through shared memory, by TMA) while the next one's
-// products run.
+// one CTA per SM.  A unit reads 384 KB from L2 for 33 Mflop; 128 x 128 units
+// were bound by those reads (10 TB/s of L2 to the SMs, 56 us at 8891 tokens x
+// 4096 features x 512), and weights kept in shared memory left too short a ring
+// (90 us).  (The weights are not multicast to pairs of CTAs: such copies are only
+// for programs on one GPU, and replicas on several use this library too.)  The accumulator is double buffered: one unit's results
+// leave (through shared memory, by TMA) while the next one's products run.
 // Every CTA scans the streams by itself; CTA 0 writes the plan that the
 // attention reads.  The first feature unit of a token tile also copies the
 // tokens' rotated key parts and records which blocks are in the pool.
 constexpr int kExpandThreads = 224;        // 4 epilogue warps, producer, MMA issuer, spare (tensor memory)
 constexpr int kExpandSlots = 4;
 constexpr int kExpandCtas = 152;
-constexpr int kFeatures = 256, kWeightRows = 64;  // features per unit at most; weight rows per copy
+constexpr int kFeatures = 256, kWeightRows = 128;  // features per unit at most; weight rows per copy
 constexpr int kSlotBytes = 3 * kChunkBytes;    // 128 token rows, 256 feature rows of 64 values
 constexpr int kExpandSmem = kExpandSlots * kSlotBytes + 2 * kChunkBytes;
 
@@ -121,14 +119,13 @@ __device__ __forceinline__ bool prefill_stream(const PrefillArgs &a, int b, int 
 }
 __device__ __forceinline__ int token_tiles(int ctx) { return (ctx + kTile - 1) / kTile; }
 
-// Walks the units of a CTA (every feature tile of a token tile, then the token
-// tile two on); every warp keeps its own copy.
+// Walks the units of a CTA (every feature tile of a token tile, then the next
+// token tile); every warp keeps its own copy.
 struct ExpandWalk {
     int left, f, t;               // units left; feature tile, token tile
-    int feature_tiles, tiles;
+    int feature_tiles;
     int b, i, n, limit;           // stream of the token tile, its tile in the stream, the stream's tiles
     int ctx;
-    __device__ __forceinline__ bool exists() const { return t < tiles; }  // (the last pair may lack its second)
     __device__ __forceinline__ void seek(const PrefillArgs &a) {          // b: the next stream that has tiles
         for (; b < limit; ++b) {
             int rows, c;
@@ -142,12 +139,12 @@ struct ExpandWalk {
         --left;
         if (++f < feature_tiles) return;
         f = 0;
-        for (int k = 0; k < 2; ++k)
-            if (++t < tiles && ++i == n) {
-                i = 0;
-                ++b;
-                seek(a);
-            }
+        ++t;
+        if (++i == n) {
+            i = 0;
+            ++b;
+            seek(a);
+        }
     }
 };
 
@@ -160,11 +157,10 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
     const uint32_t ring = smem_addr(raw), stage = ring + kExpandSlots * kSlotBytes;
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int chunks = a.L / 64;
-    const uint32_t rank = blockIdx.x & 1;
     if (warp == 5 && lane == 0) {
         for (int i = 0; i < kExpandSlots; ++i) {
             mbar_init(smem_addr(&sh.full[i]), 1);
-            mbar_init(smem_addr(&sh.empty[i]), 2);  // the MMAs of both CTAs
+            mbar_init(smem_addr(&sh.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.acc_full[i]), 1);
@@ -174,8 +170,6 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         sh.limit = a.B;
         fence_mbar_init();
     }
-    __syncwarp();
-    cluster_arrive();
     if (warp == 4 && lane == 0) {
         prefetch_tensormap(&map_pool);
         prefetch_tensormap(&map_uk);
@@ -260,19 +254,19 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         tiles += sh.tiles[w];
     }
     // Units of 256 features, or of 128 where those still make one round of the
-    // clusters (one prompt of 333 rows, the whole call: 17.4 against 18.2 us; 16
+    // CTAs (one prompt of 333 rows, the whole call: 17.4 against 18.2 us; 16
     // prompts whose 96 units of 256 make two rounds and 192 of 128 three: 30.8
     // against 30.1)
-    const int clusters = gridDim.x / 2, me = blockIdx.x / 2, pairs = (tiles + 1) / 2;
+    const int ctas = gridDim.x, me = blockIdx.x;
     auto tiles_of = [](int features, int each) { return (features + each - 1) / each; };
-    auto units_of = [&](int each) { return pairs * (tiles_of(a.Hq * a.nope, each) + tiles_of(a.Hq * a.v, each)); };
-    const int features = units_of(kFeatures / 2) <= clusters ? kFeatures / 2 : kFeatures;
+    auto units_of = [&](int each) { return tiles * (tiles_of(a.Hq * a.nope, each) + tiles_of(a.Hq * a.v, each)); };
+    const int features = units_of(kFeatures / 2) <= ctas ? kFeatures / 2 : kFeatures;
     const int k_tiles = tiles_of(a.Hq * a.nope, features), feature_tiles = k_tiles + tiles_of(a.Hq * a.v, features);
     const int units = units_of(features);
-    const int each = units / clusters;
-    const int fewer = clusters - (units - each * clusters);  // the clusters behind these take one more
+    const int each = units / ctas;
+    const int fewer = ctas - (units - each * ctas);  // the CTAs behind these take one more
     const int u0 = me * each + max(0, me - fewer), u1 = u0 + each + (me >= fewer);
-    const int first_t = u0 / feature_tiles * 2 + static_cast<int>(rank);
+    const int first_t = u0 / feature_tiles;
     for (int b = b0; b < b1; ++b) {
         const bool good = prefill_stream(a, b, &n, &ctx);
         const int nt = good && n && b < limit ? token_tiles(ctx) : 0;
@@ -292,29 +286,27 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         t_at += nt;
     }
     __syncthreads();
-    cluster_wait();  // the peer's barriers are initialised
     const uint32_t tmem = uniform(sh.tmem);
     ExpandWalk walk;
     walk.left = uniform(u1 - u0);
     walk.feature_tiles = feature_tiles;
-    walk.tiles = uniform(tiles);
     walk.f = uniform(u0 % feature_tiles);
     walk.t = uniform(first_t);
     walk.b = uniform(sh.start_b);
     walk.i = uniform(sh.start_i);
     walk.limit = uniform(limit);
-    if (walk.left > 0 && walk.exists()) walk.seek(a);
+    if (walk.left > 0) walk.seek(a);
     bool ok = true;
 
     if (warp == 4) {
-        // ---- producer: the token tile's eight blocks for this CTA, its half
-        // of the weight chunk for both.  A block outside the pool (or past the
-        // context) is read out of range, which fills zeros.
+        // ---- producer: the token tile's eight blocks and the weight chunk.  A
+        // block outside the pool (or past the context) is read out of range,
+        // which fills zeros.
         const uint32_t leader = elect_leader();
         uint32_t slot = 0, phase = 0, count = 0;
         int have = -1, ys[8] = {};
         for (; ok && walk.left > 0; walk.advance(a)) {
-            if (walk.t != have && walk.exists()) {
+            if (walk.t != have) {
                 const int block = walk.i * (kTile / TTS_BLOCK_TOKENS) + (lane & 7);
                 int y = a.num_blocks * TTS_BLOCK_TOKENS;
                 bool in_pool = false;
@@ -331,20 +323,18 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
             }
             have = walk.t;
             const bool is_k = walk.f < k_tiles;
-            const int row = (is_k ? walk.f : walk.f - k_tiles) * features + static_cast<int>(rank) * (features / 2);
+            const int row = (is_k ? walk.f : walk.f - k_tiles) * features;
             for (int c = 0; c < chunks; ++c) {
                 if (count >= kExpandSlots && !warp_wait(&sh.empty[slot], phase ^ 1)) {
                     ok = false;
                     break;
                 }
                 const uint32_t bar = smem_addr(&sh.full[slot]), to = ring + slot * kSlotBytes;
-                mbar_expect_tx_by(leader, bar, (walk.exists() ? kChunkBytes : 0) + features * 128);
-                for (int i = 0; i < features / 2; i += kWeightRows)
-                    tma_multicast_2d_by(leader, to + kChunkBytes + (rank * (features / 2) + i) * 128, is_k ? &map_uk : &map_uv,
-                                        c * 64, row + i, bar, 3);
-                if (walk.exists())
+                mbar_expect_tx_by(leader, bar, kChunkBytes + features * 128);
+                for (int i = 0; i < features; i += kWeightRows)
+                    tma_load_2d_by(leader, to + kChunkBytes + i * 128, is_k ? &map_uk : &map_uv, c * 64, row + i, bar);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) tma_load_2d_by(leader, to + i * 2048, &map_pool, c * 64, ys[i], bar);
+                for (int i = 0; i < 8; ++i) tma_load_2d_by(leader, to + i * 2048, &map_pool, c * 64, ys[i], bar);
                 ++count;
                 if (++slot == kExpandSlots) {
                     slot = 0;
@@ -382,7 +372,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 }
                 tc_fence_after();
                 const uint32_t sa = ring + slot * kSlotBytes, sb = sa + kChunkBytes;
-                if (walk.exists() && end < kTile && end < stop) {
+                if (end < kTile && end < stop) {
                     for (int t = end + lane / 8; t < stop; t += 4)
                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(sa + t * 128 + lane % 8 * 16), "r"(0)
                                      : "memory");
@@ -393,7 +383,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 for (int kk = 0; kk < 4; ++kk)
                     mma_bf16_by(leader, tmem + buf * kFeatures, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
                                 idesc, (c | kk) != 0);
-                mma_commit_multicast_by(leader, smem_addr(&sh.empty[slot]), 3);
+                mma_commit_by(leader, smem_addr(&sh.empty[slot]));
                 if (++slot == kExpandSlots) {
                     slot = 0;
                     phase ^= 1;
@@ -410,7 +400,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         uint32_t done = 0;
         for (; walk.left > 0; walk.advance(a), ++done) {
-            if (walk.f == 0 && walk.exists()) {
+            if (walk.f == 0) {
                 for (int i = threadIdx.x; i < kTile * 8; i += 128) {
                     const int t = walk.i * kTile + i / 8;
                     uint4 x = make_uint4(0, 0, 0, 0);
@@ -470,7 +460,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
                 if (threadIdx.x == 0) {
-                    if (walk.exists() && f0 + q * 64 < all)
+                    if (f0 + q * 64 < all)
                         tma_store_2d(is_k ? &map_k : &map_v, f0 + q * 64, walk.t * kTile, stage + (q & 1) * kChunkBytes);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
@@ -527,7 +517,6 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    cluster_sync();  // the peer's copies and commits into this CTA are over
 }
 
 // --------------------------------------------------------------- attention
@@ -881,7 +870,7 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
     if (!d_ws || !aligned16(d_ws) || ws_bytes < pl.total()) return TTS_ERR_WORKSPACE;
     // the grid, GEMM units and token rows are 32-bit
     const int64_t unit_tiles = static_cast<int64_t>(Hq) * (nope_dim + v_dim) / kFeatures + 2;
-    if (pl.tiles * unit_tiles > 0x40000000 || pl.qtiles * Hq > 0x7FFFFFFF) return TTS_ERR_UNSUPPORTED;
+    if (pl.tiles * unit_tiles > 0x20000000 || pl.qtiles * Hq > 0x7FFFFFFF) return TTS_ERR_UNSUPPORTED;
 
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
     PrefillArgs a{};
@@ -924,8 +913,8 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
 
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (!allow_smem(latent_expand_kernel, kExpandSmem)) return TTS_ERR_CUDA;
-    const int rc = launch_cluster(2, latent_expand_kernel, dim3(kExpandCtas), dim3(kExpandThreads), kExpandSmem,
-                                  {cs, thread_pdl()}, pool, uk, uv, qkv[2], qkv[4], a);
+    const int rc = launch_kernel(latent_expand_kernel, dim3(kExpandCtas), dim3(kExpandThreads), kExpandSmem,
+                                 {cs, thread_pdl()}, pool, uk, uv, qkv[2], qkv[4], a);
     if (rc != TTS_OK) return rc;
     const unsigned grid = static_cast<unsigned>(pl.qtiles * Hq);
     if (nope_dim == 128)

@@ -9,13 +9,8 @@
 
 namespace tts {
 
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    cluster_arrive();
-    cluster_wait();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -202,18 +197,6 @@ __device__ __forceinline__ void tma_load_2d_by(uint32_t leader, uint32_t dst, co
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(leader)
         : "memory");
 }
-// The same into the CTAs of the cluster whose bits are set in `mask`, at the
-// same shared-memory offsets, each copy signalling its own CTA's barrier.
-__device__ __forceinline__ void tma_multicast_2d_by(uint32_t leader, uint32_t dst, const CUtensorMap *map, int x, int y,
-                                                    uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster"
-        " [%0], [%1, {%2, %3}], [%4], %6;\n\t}" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(leader), "h"(mask)
-        : "memory");
-}
 __device__ __forceinline__ void mbar_expect_tx_by(uint32_t leader, uint32_t bar, uint32_t bytes) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
@@ -228,17 +211,6 @@ __device__ __forceinline__ void mma_commit_by(uint32_t leader, uint32_t bar) {
         "setp.ne.b32 q, %1, 0;\n\t"
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
         "r"(leader)
-        : "memory");
-}
-
-// A commit that arrives on the barrier at this offset in every CTA of `mask`.
-__device__ __forceinline__ void mma_commit_multicast_by(uint32_t leader, uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(
-            bar),
-        "r"(leader), "h"(mask)
         : "memory");
 }
 
