@@ -119,6 +119,30 @@ __device__ __forceinline__ bool prefill_stream(const PrefillArgs &a, int b, int 
 }
 __device__ __forceinline__ int token_tiles(int ctx) { return (ctx + kTile - 1) / kTile; }
 
+// Zeros in the rows of the refused streams (rare), by every thread of the grid:
+// each warp of the CTA looks at 32 streams and finds the same ones.
+__device__ __noinline__ void zero_refused(const PrefillArgs &a, int limit) {
+    const int lane = threadIdx.x % 32;
+    const size_t width = static_cast<size_t>(a.Hq) * a.v / 8;  // 16-byte pieces a row
+    const size_t me = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x, all = static_cast<size_t>(gridDim.x) * blockDim.x;
+    for (int base = 0; base < a.B; base += 32) {
+        bool bad = false;
+        int n, ctx, r0 = 0, r1 = 0;
+        if (base + lane < a.B) {
+            const int b = base + lane;
+            bad = !prefill_stream(a, b, &n, &ctx) || (n && b >= limit);
+            r0 = max(0, a.row_start[b]);
+            r1 = min(a.num_rows, a.row_start[b + 1]);
+        }
+        for (unsigned m = __ballot_sync(kFull, bad); m; m &= m - 1) {
+            const int from = __shfl_sync(kFull, r0, __ffs(m) - 1), to = __shfl_sync(kFull, r1, __ffs(m) - 1);
+            if (me == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
+            if (from >= to) continue;
+            for (size_t i = from * width + me; i < to * width; i += all) reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
 // Walks the units of a CTA (every feature tile of a token tile, then the next
 // token tile); every warp keeps its own copy.
 struct ExpandWalk {
@@ -267,6 +291,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
     const int fewer = ctas - (units - each * ctas);  // the CTAs behind these take one more
     const int u0 = me * each + max(0, me - fewer), u1 = u0 + each + (me >= fewer);
     const int first_t = u0 / feature_tiles;
+    bool refused = false;  // any of this thread's streams
     for (int b = b0; b < b1; ++b) {
         const bool good = prefill_stream(a, b, &n, &ctx);
         const int nt = good && n && b < limit ? token_tiles(ctx) : 0;
@@ -274,18 +299,11 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
             sh.start_b = b;
             sh.start_i = first_t - t_at;
         }
-        if (blockIdx.x == 0) {
-            a.tile_start[b] = t_at;
-            if (!good || (n && b >= limit)) {  // refused: its rows get zeros
-                flag_error(a.err, TTS_ERRBIT_CTX_LEN);
-                const int r0 = max(0, a.row_start[b]), r1 = min(a.num_rows, a.row_start[b + 1]);
-                const size_t w = static_cast<size_t>(a.Hq) * a.v / 8;
-                for (size_t i = r0 * w; r0 < r1 && i < r1 * w; ++i) reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
-            }
-        }
+        if (blockIdx.x == 0) a.tile_start[b] = t_at;
+        refused = refused || !good || (n && b >= limit);
         t_at += nt;
     }
-    __syncthreads();
+    if (__syncthreads_or(refused)) zero_refused(a, limit);
     const uint32_t tmem = uniform(sh.tmem);
     ExpandWalk walk;
     walk.left = uniform(u1 - u0);
