@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
             lo = reinterpret_cast<const uint4 *>(x)[it & 3];
             hi = reinterpret_cast<const uint4 *>(x)[(it & 3) + 4];
         } else {
-            lo = __ldg(reinterpret_cast<const uint4 *>(a.c_new + static_cast<size_t>(row) * a.L) + it - rope_items);
+            lo = reinterpret_cast<const uint4 *>(a.c_new + static_cast<size_t>(row) * a.L)[it - rope_items];
         }
     };
     uint4 lo[kRows][kAhead], hi[kRows][kAhead];

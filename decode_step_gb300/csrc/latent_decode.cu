@@ -221,7 +221,10 @@ __device__ __forceinline__ int stream_tiles(const LatentAttnArgs &a, int ctx) {
     return (ctx + kTile - 1) / kTile;
 }
 
-// Units of one of stream b's groups (0: its length is out of range).
+// Units of one of stream b's groups (0: its length is out of range).  The
+// lengths may be read through the read-only path: this kernel starts when every
+// CTA of the absorb kernel is past its wait, so nothing writes them any more.
+// (Plain loads: 64 streams 26.7 -> 27.1 us the call, verify 56.6 -> 57.1.)
 __device__ __forceinline__ int group_units(const LatentAttnArgs &a, int b) {
     const int n = stream_tiles(a, __ldg(a.ctx_lens + b));
     return n ? n + a.start : 0;

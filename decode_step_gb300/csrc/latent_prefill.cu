@@ -108,8 +108,8 @@ struct ExpandShared {
 
 // Rows and context of stream b; false: out of range.
 __device__ __forceinline__ bool prefill_stream(const PrefillArgs &a, int b, int *n, int *ctx) {
-    const int first = __ldg(a.row_start + b), end = __ldg(a.row_start + b + 1);
-    *ctx = __ldg(a.ctx_lens + b);
+    const int first = __ldcg(a.row_start + b), end = __ldcg(a.row_start + b + 1);
+    *ctx = __ldcg(a.ctx_lens + b);
     *n = 0;
     if (first == end) return true;
     if (first < 0 || end < first || end > a.num_rows) return false;
@@ -593,9 +593,9 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int h = blockIdx.x % a.Hq, qt = blockIdx.x / a.Hq;
-    const bool mine = qt < __ldg(a.num_qtiles);
-    const int4 of = __ldg(reinterpret_cast<const int4 *>(a.qtiles + qt));  // (the list has room for every CTA)
-    const int4 which = __ldg(reinterpret_cast<const int4 *>(a.qtiles + qt) + 1);
+    const bool mine = qt < __ldcg(a.num_qtiles);
+    const int4 of = __ldcg(reinterpret_cast<const int4 *>(a.qtiles + qt));  // (the list has room for every CTA)
+    const int4 which = __ldcg(reinterpret_cast<const int4 *>(a.qtiles + qt) + 1);
     bool ok = true;
     if (uniform(mine)) {
         const int first = uniform(of.x), n = uniform(of.y), ctx = uniform(of.z), tile0 = uniform(of.w);
