@@ -119,6 +119,35 @@ __device__ __forceinline__ bool prefill_stream(const PrefillArgs &a, int b, int 
 }
 __device__ __forceinline__ int token_tiles(int ctx) { return (ctx + kTile - 1) / kTile; }
 
+// Largest magnitude of 64 values, NaN if one of them is.
+__device__ __forceinline__ float largest64(const uint32_t *x) {
+    auto larger = [](float a, float b) {
+        float m;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+        return m;
+    };
+    float m[4] = {};
+#pragma unroll
+    for (int i = 0; i < 64; ++i) m[i % 4] = larger(m[i % 4], fabsf(__uint_as_float(x[i])));
+    return larger(larger(m[0], m[1]), larger(m[2], m[3]));
+}
+
+// Whether a token's latent is finite (rare: asked when a product of it is not).
+__device__ __noinline__ bool latent_finite(const PrefillArgs &a, int b, int t, int ctx) {
+    if (t >= ctx) return true;
+    const int id = a.table[static_cast<size_t>(b) * a.max_blocks + t / TTS_BLOCK_TOKENS];
+    if (id < 0 || id >= a.num_blocks) return true;
+    const uint4 *c = reinterpret_cast<const uint4 *>(
+        a.pool + (static_cast<size_t>(id) * TTS_BLOCK_TOKENS + t % TTS_BLOCK_TOKENS) * (a.L + kLatentRope));
+    bool finite = true;
+    for (int i = 0; i < a.L / 8; ++i) {
+        const uint4 x = c[i];
+        for (const uint32_t w : {x.x, x.y, x.z, x.w})
+            finite = finite && (w & 0x7F80u) != 0x7F80u && (w & 0x7F800000u) != 0x7F800000u;
+    }
+    return finite;
+}
+
 // Zeros in the rows of the refused streams (rare), by every thread of the grid:
 // each warp of the CTA looks at 32 streams and finds the same ones.
 __device__ __noinline__ void zero_refused(const PrefillArgs &a, int limit) {
@@ -456,13 +485,16 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 tmem_ld32_nowait(tl + buf * kFeatures + q * 64, x);
                 tmem_ld32_nowait(tl + buf * kFeatures + q * 64 + 32, x + 32);
                 tmem_wait_ld();
-                float *v = reinterpret_cast<float *>(x);
-                // A token's value that is not finite would spread to rows that
-                // do not see it (NaN times a zero weight); those that do have
-                // it from the keys, which come from the same latent.
-                if (!is_k)
+                // A latent that is not finite makes every key and value of its
+                // token so.  In the values it would spread to rows that do not
+                // see the token (NaN times a zero weight): the values become
+                // zero and the keys NaN, and the rows that see it are NaN from
+                // their scores.  Values that are not finite by their weights
+                // are so for every token: they stay.
+                if (!(largest64(x) < INFINITY) && !latent_finite(a, walk.b, walk.i * kTile + r, walk.ctx))
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) v[i] = fabsf(v[i]) < INFINITY ? v[i] : 0.0f;
+                    for (int i = 0; i < 64; ++i) x[i] = is_k ? 0x7FFFFFFFu : 0u;
+                const float *v = reinterpret_cast<const float *>(x);
                 const uint32_t to = stage + (q & 1) * kChunkBytes + r * 128;
                 // 16-byte chunk j of row r at j ^ (r % 8), the stores' swizzle
 #pragma unroll
