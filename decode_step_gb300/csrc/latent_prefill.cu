@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -46,10 +47,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // Values and softmax weights are f16: it holds them to 2^-11 where bf16 holds
-// them to 2^-8, at the same rate (weights lie in [0, 2^8]).
+// them to 2^-8, at the same rate.
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
+}
+// Where f16 does not hold the values of a head's 128 tokens (of some token the
+// largest is not in [2^-10, 65504]), each token's are kept divided by 2^e, e the
+// exponent of its largest, and e is added to its scores (in log2 units): the
+// weights are then w_t 2^e, held as precisely against the largest of them, and
+// the sum of the weights w_t themselves is computed beside.  So a value is held to
+// 2^-11 of itself or 2^-15 of its token's largest, and no finite one spreads to
+// rows that do not see it.  e's limits keep the sum, relative to the largest
+// w_t 2^e, between 2^-121 and 2^122 (2^24 tokens).
+constexpr uint32_t kScaled = 0x100;
+constexpr int kMinExp = -90, kMaxExp = 113;
+__device__ __forceinline__ bool f16_holds(float largest) { return largest >= 0x1.0p-10f && largest <= 65504.0f; }
+__device__ __forceinline__ int value_exp(float largest) {  // of a token's largest value
+    return min(max(static_cast<int>(__float_as_uint(largest) >> 23) - 127, kMinExp), kMaxExp);
 }
 
 // kRows rows of one stream, what they see and where its keys and values are
@@ -69,7 +84,9 @@ struct PrefillArgs {
     int32_t *num_qtiles;   // query tiles in all
     QueryTile *qtiles;     // [max_qtiles] those that see the most tokens first
     int max_qtiles;
-    uint32_t *blocks_ok;   // [token tiles] bit i: block i of the tile is in the pool
+    uint32_t *info;        // [Hq][max_tiles] bit i: block i of the tile is in the pool; kScaled: the head's values there are scaled
+    int max_tiles;
+    int8_t *exps;          // [Hq][max_tiles][128] the tokens' e, where scaled
     const __nv_bfloat16 *pool;
     __nv_bfloat16 *kr;     // [token tiles * 128][64]
     __nv_bfloat16 *out;
@@ -119,17 +136,30 @@ __device__ __forceinline__ bool prefill_stream(const PrefillArgs &a, int b, int 
 }
 __device__ __forceinline__ int token_tiles(int ctx) { return (ctx + kTile - 1) / kTile; }
 
+// Barrier of the four epilogue warps with an OR over their threads.
+__device__ __forceinline__ bool epilogue_any(bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred))
+        : "memory");
+    return r != 0;
+}
+
 // Largest magnitude of 64 values, NaN if one of them is.
 __device__ __forceinline__ float largest64(const uint32_t *x) {
-    auto larger = [](float a, float b) {
+    auto larger = [](float a, float b, float c) {
         float m;
-        asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
         return m;
     };
     float m[4] = {};
 #pragma unroll
-    for (int i = 0; i < 64; ++i) m[i % 4] = larger(m[i % 4], fabsf(__uint_as_float(x[i])));
-    return larger(larger(m[0], m[1]), larger(m[2], m[3]));
+    for (int i = 0; i < 64; i += 2)
+        m[i / 2 % 4] = larger(m[i / 2 % 4], fabsf(__uint_as_float(x[i])), fabsf(__uint_as_float(x[i + 1])));
+    return larger(larger(m[0], m[1], m[2]), m[3], m[3]);
 }
 
 // Whether a token's latent is finite (rare: asked when a product of it is not).
@@ -363,8 +393,6 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                     if (in_pool) y = id * TTS_BLOCK_TOKENS;
                     else if (walk.f == 0) flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
                 }
-                const uint32_t mask = __ballot_sync(kFull, in_pool) & 0xFFu;
-                if (walk.f == 0 && lane == 0) a.blocks_ok[walk.t] = mask;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ys[i] = __shfl_sync(kFull, y, i);
             }
@@ -445,8 +473,15 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         // ---- rotated key parts, then the accumulators, 64 features at a time
         const int r = warp * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        uint32_t done = 0;
+        uint32_t done = 0, in_pool = 0, half = 0;
+        int have = -1;
         for (; walk.left > 0; walk.advance(a), ++done) {
+            if (warp == 0 && walk.f >= k_tiles && walk.t != have) {
+                have = walk.t;
+                const int block = walk.i * (kTile / TTS_BLOCK_TOKENS) + (lane & 7);
+                const int id = block * TTS_BLOCK_TOKENS < walk.ctx ? a.table[static_cast<size_t>(walk.b) * a.max_blocks + block] : -1;
+                in_pool = __ballot_sync(kFull, id >= 0 && id < a.num_blocks) & 0xFFu;
+            }
             if (walk.f == 0) {
                 for (int i = threadIdx.x; i < kTile * 8; i += 128) {
                     const int t = walk.i * kTile + i / 8;
@@ -466,18 +501,16 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
             const int f0 = (is_k ? walk.f : walk.f - k_tiles) * features, all = a.Hq * (is_k ? a.nope : a.v);
             ok = warp_wait(&sh.acc_full[buf], (done / 2) & 1);
             tc_fence_after();
-#pragma unroll 2
-            for (int q = 0; q < features / 64; ++q) {
+            // a head's values are written as they are, and again scaled if f16
+            // does not hold them (rare; known with the barrier that the stores
+            // wait for)
+            const int token = walk.i * kTile + r;
+            bool scaled = false;
+            float largest = 0.0f;  // of this token's finite values of the head
+            for (int q = 0; q < features / 64;) {
                 // the staging half is free once the stores before the last have read it
                 if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                int fail;
-                asm volatile(
-                    "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-                    "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                    : "=r"(fail)
-                    : "r"(ok ? 0 : 1)
-                    : "memory");
-                if (fail) {  // (all four warps leave together)
+                if (epilogue_any(!ok)) {  // (all four warps leave together)
                     ok = false;
                     break;
                 }
@@ -485,17 +518,31 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                 tmem_ld32_nowait(tl + buf * kFeatures + q * 64, x);
                 tmem_ld32_nowait(tl + buf * kFeatures + q * 64 + 32, x + 32);
                 tmem_wait_ld();
+                float here = largest64(x);
                 // A latent that is not finite makes every key and value of its
                 // token so.  In the values it would spread to rows that do not
                 // see the token (NaN times a zero weight): the values become
                 // zero and the keys NaN, and the rows that see it are NaN from
                 // their scores.  Values that are not finite by their weights
                 // are so for every token: they stay.
-                if (!(largest64(x) < INFINITY) && !latent_finite(a, walk.b, walk.i * kTile + r, walk.ctx))
+                if (!(here < INFINITY)) {
+                    const bool weights = latent_finite(a, walk.b, token, walk.ctx);
+                    here = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) x[i] = is_k ? 0x7FFFFFFFu : 0u;
+                    for (int i = 0; i < 64; ++i) {
+                        if (!weights) x[i] = is_k ? 0x7FFFFFFFu : 0u;
+                        const float size = fabsf(__uint_as_float(x[i]));
+                        if (size < INFINITY) here = fmaxf(here, size);
+                    }
+                }
+                if (!scaled) largest = fmaxf(largest, here);
+                if (scaled) {
+                    const float by = __uint_as_float(static_cast<uint32_t>(127 - value_exp(largest)) << 23);  // 2^-e
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * by);
+                }
                 const float *v = reinterpret_cast<const float *>(x);
-                const uint32_t to = stage + (q & 1) * kChunkBytes + r * 128;
+                const uint32_t to = stage + half * kChunkBytes + r * 128;
                 // 16-byte chunk j of row r at j ^ (r % 8), the stores' swizzle
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -508,11 +555,28 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
                                  "r"(p[1]), "r"(p[2]), "r"(p[3]));
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
+                const bool ends = !is_k && (a.v == 64 || q % 2);  // a head's values end
+                const bool again = epilogue_any(ends && !scaled && f0 + q * 64 < all && token < walk.ctx && !f16_holds(largest));
                 if (threadIdx.x == 0) {
                     if (f0 + q * 64 < all)
-                        tma_store_2d(is_k ? &map_k : &map_v, f0 + q * 64, walk.t * kTile, stage + (q & 1) * kChunkBytes);
+                        tma_store_2d(is_k ? &map_k : &map_v, f0 + q * 64, walk.t * kTile, stage + half * kChunkBytes);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+                half ^= 1;
+                ++q;
+                if (!ends) continue;
+                const size_t head = (f0 + q * 64) / a.v - 1;
+                if (again) {
+                    scaled = true;
+                    q -= a.v / 64;
+                    a.exps[(head * a.max_tiles + walk.t) * kTile + r] = static_cast<int8_t>(value_exp(largest));
+                    // (the same places are written once more)
+                    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                } else {
+                    if (threadIdx.x == 0 && f0 + q * 64 <= all)
+                        a.info[head * a.max_tiles + walk.t] = in_pool | (scaled ? kScaled : 0u);
+                    scaled = false;
+                    largest = 0.0f;
                 }
             }
             if (!ok) break;
@@ -573,12 +637,42 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
 
 constexpr int kSlots = 8;           // ring slots of [128 tokens][64 values]: 1.6 tiles of keys and values
 constexpr int kTiles = 4;           // barriers for the keys, and the values, of as many tiles
-constexpr int kAttnThreads = 320;   // two softmax warpgroups, producer, MMA issuer
+constexpr int kAttnThreads = 384;   // two softmax warpgroups; producer, MMA issuer and two spare warps
+// A softmax thread holds a row's 128 scores: the registers that the others do not
+// need go to it (8191 rows after 700 tokens: 262 us without, 255 with).  The
+// block has to start with kStartRegs a thread; launch_prefill looks.
+constexpr int kSoftmaxRegs = 224, kOtherRegs = 56, kStartRegs = 168;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kAttnThreads * kStartRegs);
 
 struct PrefillShared {
     uint64_t k_full[kTiles], k_done[kTiles], v_full[kTiles], v_done[kTiles], q_full[2], s_full[2], p_full[2], o_done[2], done;
     uint32_t tmem;
 };
+
+// A tile of scaled values (rare): the scores in log2 units with the tokens' e.
+__device__ __forceinline__ void add_exps(uint32_t *x, float unit, const int8_t *exps) {
+#pragma unroll
+    for (int i = 0; i < kTile; i += 16) {
+        const int4 e = reinterpret_cast<const int4 *>(exps)[i / 16];
+        const int w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            x[i + k] = __float_as_uint(fmaf(static_cast<float>(static_cast<int8_t>(w[k / 4] >> (8 * (k % 4)))), unit, __uint_as_float(x[i + k])));
+    }
+}
+// The sum of the weights without them.
+__device__ __forceinline__ float sum_unscaled(const uint32_t *x, float scale_log2, float m, const int8_t *exps) {
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kTile; i += 16) {
+        const int4 e = reinterpret_cast<const int4 *>(exps)[i / 16];
+        const int w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            sum[k % 2] += hw_ex2(fmaf(__uint_as_float(x[i + k]), scale_log2, -m) - static_cast<float>(static_cast<int8_t>(w[k / 4] >> (8 * (k % 4)))));
+    }
+    return sum[0] + sum[1];
+}
 
 template <int kNope, int kV>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -638,206 +732,221 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
         const int seen0 = ctx - n + min(n, r0 + kTile), seen1 = ctx - n + min(n, r0 + kRows);
         const int nt0 = (seen0 + kTile - 1) / kTile, nt1 = two ? (seen1 + kTile - 1) / kTile : 0;
         const int nt = max(nt0, nt1);
-        if (warp == 8) {
-            // ---- producer (one lane): the queries, then K and V of every tile
-            if (lane == 0) {
-                for (int s = 0; s < (two ? 2 : 1); ++s) {
-                    const uint32_t bar = smem_addr(&sh.q_full[s]), at = q_base + s * kQc * kChunkBytes;
-                    mbar_arrive_expect_tx(bar, kQc * kChunkBytes);
-                    for (int c = 0; c < kQc - 1; ++c)
-                        tma_load_2d(at + c * kChunkBytes, &map_qn, h * kNope + c * 64, first + r0 + s * kTile, bar);
-                    tma_load_2d(at + (kQc - 1) * kChunkBytes, &map_qr, h * kLatentRope, first + r0 + s * kTile, bar);
+        if (warp >= 8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+            if (warp == 8) {
+                // ---- producer (one lane): the queries, then K and V of every tile
+                if (lane == 0) {
+                    for (int s = 0; s < (two ? 2 : 1); ++s) {
+                        const uint32_t bar = smem_addr(&sh.q_full[s]), at = q_base + s * kQc * kChunkBytes;
+                        mbar_arrive_expect_tx(bar, kQc * kChunkBytes);
+                        for (int c = 0; c < kQc - 1; ++c)
+                            tma_load_2d(at + c * kChunkBytes, &map_qn, h * kNope + c * 64, first + r0 + s * kTile, bar);
+                        tma_load_2d(at + (kQc - 1) * kChunkBytes, &map_qr, h * kLatentRope, first + r0 + s * kTile, bar);
+                    }
+                    // a slot is free once the keys or values that it held are done with
+                    uint32_t pos = 0;
+                    auto slot_free = [&]() {
+                        if (pos < kSlots) return true;
+                        const uint32_t j = (pos - kSlots) / (kQc + kVc), c = (pos - kSlots) % (kQc + kVc);
+                        return mbar_wait(smem_addr((c < kQc ? sh.k_done : sh.v_done) + j % kTiles), (j / kTiles) & 1);
+                    };
+                    int j = 0;
+                    for (; ok && j < nt; ++j) {
+                        const int y = (tile0 + j) * kTile;
+                        for (int c = 0; ok && c < kQc + kVc; ++c, ++pos) {
+                            const uint32_t bar = smem_addr((c < kQc ? sh.k_full : sh.v_full) + j % kTiles);
+                            if (c == 0 || c == kQc) mbar_arrive_expect_tx(bar, (c ? kVc : kQc) * kChunkBytes);
+                            ok = slot_free();
+                            const uint32_t at = ring + pos % kSlots * kChunkBytes;
+                            if (!ok) break;
+                            if (c < kQc - 1) tma_load_2d(at, &map_k, h * kNope + c * 64, y, bar);
+                            else if (c == kQc - 1) tma_load_2d(at, &map_kr, 0, y, bar);
+                            else tma_load_2d(at, &map_v, h * kV + (c - kQc) * 64, y, bar);
+                        }
+                    }
+                    for (int i = max(0, j - 2); i < j; ++i) {
+                        mbar_wait(smem_addr(&sh.k_full[i % kTiles]), (i / kTiles) & 1);
+                        mbar_wait(smem_addr(&sh.v_full[i % kTiles]), (i / kTiles) & 1);
+                    }
+                    for (int s = 0; s < (two ? 2 : 1); ++s) mbar_wait(smem_addr(&sh.q_full[s]), 0);
                 }
-                // a slot is free once the keys or values that it held are done with
-                uint32_t pos = 0;
-                auto slot_free = [&]() {
-                    if (pos < kSlots) return true;
-                    const uint32_t j = (pos - kSlots) / (kQc + kVc), c = (pos - kSlots) % (kQc + kVc);
-                    return mbar_wait(smem_addr((c < kQc ? sh.k_done : sh.v_done) + j % kTiles), (j / kTiles) & 1);
+            } else if (warp == 9) {
+                // ---- MMA issuer: S0(0) S1(0) | O0(j) S0(j+1) | O1(j) S1(j+1) ...
+                // S of a half is overwritten right after the O product that reads
+                // the weights kept in it; the tensor core runs them in order.
+                // Barriers are by tile: a wait or commit takes the issuing warp about
+                // 0.1 us.
+                const uint32_t leader = elect_leader();
+                bool go = true;
+                auto scores = [&](auto half, int j) {
+                    constexpr int s = decltype(half)::value;
+                    const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc);
+#pragma unroll
+                    for (int c = 0; c < kQc; ++c) {
+                        const uint32_t sa = q_base + (s * kQc + c) * kChunkBytes, sb = ring + (pos + c) % kSlots * kChunkBytes;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_bf16_by(leader, tmem + s * kTile, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
+                                        mma_idesc(kTile, kTile), (c | kk) != 0);
+                    }
+                    mma_commit_by(leader, smem_addr(&sh.s_full[s]));
                 };
-                int j = 0;
-                for (; ok && j < nt; ++j) {
-                    const int y = (tile0 + j) * kTile;
-                    for (int c = 0; ok && c < kQc + kVc; ++c, ++pos) {
-                        const uint32_t bar = smem_addr((c < kQc ? sh.k_full : sh.v_full) + j % kTiles);
-                        if (c == 0 || c == kQc) mbar_arrive_expect_tx(bar, (c ? kVc : kQc) * kChunkBytes);
-                        ok = slot_free();
-                        const uint32_t at = ring + pos % kSlots * kChunkBytes;
-                        if (!ok) break;
-                        if (c < kQc - 1) tma_load_2d(at, &map_k, h * kNope + c * 64, y, bar);
-                        else if (c == kQc - 1) tma_load_2d(at, &map_kr, 0, y, bar);
-                        else tma_load_2d(at, &map_v, h * kV + (c - kQc) * 64, y, bar);
+                auto output = [&](auto half, int j) {
+                    constexpr int s = decltype(half)::value;
+                    const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc) + kQc;
+#pragma unroll
+                    for (int c = 0; c < kVc; ++c) {
+                        const uint32_t sb = ring + (pos + c) % kSlots * kChunkBytes;
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma_ts_by(leader, tmem + (2 + s) * kTile + c * 64, tmem + s * kTile + kk * 8,
+                                      sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc_f16(kTile, 64) | kTransposeB,
+                                      (j | kk) != 0);
+                    }
+                };
+                constexpr std::integral_constant<int, 0> h0{};
+                constexpr std::integral_constant<int, 1> h1{};
+                {
+                    WarpWaits<3> w;
+                    w.set(0, &sh.k_full[0], 0);
+                    w.set(1, &sh.q_full[0], 0);
+                    w.none(2);
+                    if (two) w.set(2, &sh.q_full[1], 0);
+                    go = w.wait();
+                    tc_fence_after();
+                    if (go) {
+                        scores(h0, 0);
+                        if (two) scores(h1, 0);
+                        mma_commit_by(leader, smem_addr(&sh.k_done[0]));
                     }
                 }
-                for (int i = max(0, j - 2); i < j; ++i) {
-                    mbar_wait(smem_addr(&sh.k_full[i % kTiles]), (i / kTiles) & 1);
-                    mbar_wait(smem_addr(&sh.v_full[i % kTiles]), (i / kTiles) & 1);
-                }
-                for (int s = 0; s < (two ? 2 : 1); ++s) mbar_wait(smem_addr(&sh.q_full[s]), 0);
-            }
-        } else if (warp == 9) {
-            // ---- MMA issuer: S0(0) S1(0) | O0(j) S0(j+1) | O1(j) S1(j+1) ...
-            // S of a half is overwritten right after the O product that reads
-            // the weights kept in it; the tensor core runs them in order.
-            // Barriers are by tile: a wait or commit takes the issuing warp about
-            // 0.1 us.
-            const uint32_t leader = elect_leader();
-            bool go = true;
-            auto scores = [&](auto half, int j) {
-                constexpr int s = decltype(half)::value;
-                const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc);
-#pragma unroll
-                for (int c = 0; c < kQc; ++c) {
-                    const uint32_t sa = q_base + (s * kQc + c) * kChunkBytes, sb = ring + (pos + c) % kSlots * kChunkBytes;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_by(leader, tmem + s * kTile, sw128_desc(sa + kk * 32), sw128_desc(sb + kk * 32),
-                                    mma_idesc(kTile, kTile), (c | kk) != 0);
-                }
-                mma_commit_by(leader, smem_addr(&sh.s_full[s]));
-            };
-            auto output = [&](auto half, int j) {
-                constexpr int s = decltype(half)::value;
-                const uint32_t pos = static_cast<uint32_t>(j) * (kQc + kVc) + kQc;
-#pragma unroll
-                for (int c = 0; c < kVc; ++c) {
-                    const uint32_t sb = ring + (pos + c) % kSlots * kChunkBytes;
-#pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_ts_by(leader, tmem + (2 + s) * kTile + c * 64, tmem + s * kTile + kk * 8,
-                                  sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc_f16(kTile, 64) | kTransposeB,
-                                  (j | kk) != 0);
-                }
-            };
-            constexpr std::integral_constant<int, 0> h0{};
-            constexpr std::integral_constant<int, 1> h1{};
-            {
-                WarpWaits<3> w;
-                w.set(0, &sh.k_full[0], 0);
-                w.set(1, &sh.q_full[0], 0);
-                w.none(2);
-                if (two) w.set(2, &sh.q_full[1], 0);
-                go = w.wait();
-                tc_fence_after();
-                if (go) {
-                    scores(h0, 0);
-                    if (two) scores(h1, 0);
-                    mma_commit_by(leader, smem_addr(&sh.k_done[0]));
-                }
-            }
-            for (int j = 0; go && j < nt; ++j) {
-                // (a half beyond its last tile is passed over; the first half ends first)
-                auto turn = [&](auto half, int mine) {
-                    constexpr int s = decltype(half)::value;
-                    const bool last = s == 1 || !two;  // to use this tile's values and the next one's keys
-                    WarpWaits<2> w;
-                    w.set(0, &sh.p_full[s], j & 1);
-                    w.set(1, &sh.v_full[j % kTiles], (j / kTiles) & 1);
-                    go = w.wait();
-                    if (!go) return;
-                    tc_fence_after();
-                    output(half, j);
-                    if (last) mma_commit_by(leader, smem_addr(&sh.v_done[j % kTiles]));
-                    if (j + 1 < mine) {
-                        go = warp_wait(&sh.k_full[(j + 1) % kTiles], ((j + 1) / kTiles) & 1);
+                for (int j = 0; go && j < nt; ++j) {
+                    // (a half beyond its last tile is passed over; the first half ends first)
+                    auto turn = [&](auto half, int mine) {
+                        constexpr int s = decltype(half)::value;
+                        const bool last = s == 1 || !two;  // to use this tile's values and the next one's keys
+                        WarpWaits<2> w;
+                        w.set(0, &sh.p_full[s], j & 1);
+                        w.set(1, &sh.v_full[j % kTiles], (j / kTiles) & 1);
+                        go = w.wait();
                         if (!go) return;
                         tc_fence_after();
-                        scores(half, j + 1);
-                        if (last) mma_commit_by(leader, smem_addr(&sh.k_done[(j + 1) % kTiles]));
-                    } else {
-                        mma_commit_by(leader, smem_addr(&sh.o_done[s]));
-                    }
-                };
-                if (j < nt0) turn(h0, nt0);
-                if (go && two) turn(h1, nt1);
-            }
-            mma_commit_by(leader, smem_addr(&sh.done));
-            ok = warp_wait(&sh.done, 0) && go;
-        } else if (warp < 4 || two) {
-            // ---- softmax warpgroups: thread = query row
-            const int s = warp / 4, w = warp % 4;
-            const int r = r0 + s * kTile + w * 32 + lane;          // row in the stream
-            const int limit = ctx - n + min(n - 1, r) + 1;         // tokens it sees
-            const int low = ctx - n + r0 + s * kTile + 1;          // tokens every row of the half sees
-            const int tiles = s ? nt1 : nt0;
-            const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-            const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + (2 + s) * kTile;
-            float m = kNoScore, l = 0.0f;
-            uint32_t mask = a.blocks_ok[tile0];
-            for (int j = 0; j < tiles; ++j) {
-                const uint32_t next_mask = j + 1 < tiles ? a.blocks_ok[tile0 + j + 1] : 0;
-                if (!warp_wait(&sh.s_full[s], j & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                uint32_t x[kTile];
-#pragma unroll
-                for (int c = 0; c < kTile; c += 32) tmem_ld32_nowait(ts + c, x + c);
-                tmem_wait_ld();
-                if ((j + 1) * kTile > low || mask != 0xFFu) {
-                    const int left = limit - j * kTile;
-#pragma unroll
-                    for (int i = 0; i < kTile; ++i)
-                        if (i >= left || !((mask >> (i / TTS_BLOCK_TOKENS)) & 1)) x[i] = 0xFF800000u;  // -inf
-                }
-                mask = next_mask;
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
-                const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                if (__any_sync(kFull, t > m + kSlack)) {
-                    // (S(j) complete means that O(j - 1) is too)
-                    const float now = fmaxf(m, t), f = hw_ex2(m - now);
-                    m = now;
-                    l *= f;
-                    if (j > 0)
-                        for (int c = 0; c < kV; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_nowait(to + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tmem_st16(to + c, o);
+                        output(half, j);
+                        if (last) mma_commit_by(leader, smem_addr(&sh.v_done[j % kTiles]));
+                        if (j + 1 < mine) {
+                            go = warp_wait(&sh.k_full[(j + 1) % kTiles], ((j + 1) / kTiles) & 1);
+                            if (!go) return;
+                            tc_fence_after();
+                            scores(half, j + 1);
+                            if (last) mma_commit_by(leader, smem_addr(&sh.k_done[(j + 1) % kTiles]));
+                        } else {
+                            mma_commit_by(leader, smem_addr(&sh.o_done[s]));
                         }
+                    };
+                    if (j < nt0) turn(h0, nt0);
+                    if (go && two) turn(h1, nt1);
                 }
-                float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int c = 0; c < kTile; c += 64) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float p0 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i]), a.scale_log2, -m));
-                        const float p1 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i + 1]), a.scale_log2, -m));
-                        sum[0] += p0;
-                        sum[1] += p1;
-                        p[i] = pack_f16(p0, p1);
-                    }
-                    tmem_st32(ts + c / 2, p);
-                }
-                l += sum[0] + sum[1];
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
+                mma_commit_by(leader, smem_addr(&sh.done));
+                ok = warp_wait(&sh.done, 0) && go;
             }
-            if (ok) ok = warp_wait(&sh.o_done[s], 0);
-            if (ok) {
-                tc_fence_after();
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token left: zeros
-                uint4 *dst = reinterpret_cast<uint4 *>(a.out + (static_cast<size_t>(first + r) * a.Hq + h) * kV);
-                for (int c = 0; c < kV; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32_nowait(to + c, o);
-                    tmem_wait_ld();
-                    const float *f = reinterpret_cast<const float *>(o);
-                    if (r < n)
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+            if (warp < 4 || two) {
+                // ---- softmax warpgroups: thread = query row
+                const int s = warp / 4, w = warp % 4;
+                const int r = r0 + s * kTile + w * 32 + lane;          // row in the stream
+                const int limit = ctx - n + min(n - 1, r) + 1;         // tokens it sees
+                const int low = ctx - n + r0 + s * kTile + 1;          // tokens every row of the half sees
+                const int tiles = s ? nt1 : nt0;
+                const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+                const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + (2 + s) * kTile;
+                float m = kNoScore, l = 0.0f;
+                const uint32_t *info = a.info + static_cast<size_t>(h) * a.max_tiles + tile0;
+                const int8_t *exps = a.exps + (static_cast<size_t>(h) * a.max_tiles + tile0) * kTile;
+                uint32_t mask = info[0];
+                for (int j = 0; j < tiles; ++j) {
+                    const uint32_t next_mask = j + 1 < tiles ? info[j + 1] : 0;
+                    if (!warp_wait(&sh.s_full[s], j & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    uint32_t x[kTile];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[c / 8 + i] = make_uint4(pack_bf16(f[8 * i] * inv, f[8 * i + 1] * inv),
-                                                        pack_bf16(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
-                                                        pack_bf16(f[8 * i + 4] * inv, f[8 * i + 5] * inv),
-                                                        pack_bf16(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+                    for (int c = 0; c < kTile; c += 32) tmem_ld32_nowait(ts + c, x + c);
+                    tmem_wait_ld();
+                    const bool scaled = mask & kScaled;
+                    if ((j + 1) * kTile > low || mask != 0xFFu) {
+                        const int left = limit - j * kTile;
+#pragma unroll
+                        for (int i = 0; i < kTile; ++i)
+                            if (i >= left || !((mask >> (i / TTS_BLOCK_TOKENS)) & 1)) x[i] = 0xFF800000u;  // -inf
+                        if (scaled) {
+                            add_exps(x, 1.0f / a.scale_log2, exps + j * kTile);
+                        }
+                    }
+                    mask = next_mask;
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
+                    const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                    if (__any_sync(kFull, t > m + kSlack)) {
+                        // (S(j) complete means that O(j - 1) is too)
+                        // (the sum may be far larger than 2^m's own weight, where
+                        // values are scaled: the factor in two steps)
+                        const float now = fmaxf(m, t), root = hw_ex2(0.5f * (m - now)), f = root * root;
+                        m = now;
+                        l = l * root * root;
+                        if (j > 0)
+                            for (int c = 0; c < kV; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_nowait(to + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st16(to + c, o);
+                            }
+                    }
+                    if (scaled) l += sum_unscaled(x, a.scale_log2, m, exps + j * kTile);
+                    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 64) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float p0 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i]), a.scale_log2, -m));
+                            const float p1 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i + 1]), a.scale_log2, -m));
+                            sum[0] += p0;
+                            sum[1] += p1;
+                            p[i] = pack_f16(p0, p1);
+                        }
+                        tmem_st32(ts + c / 2, p);
+                    }
+                    if (!scaled) l += sum[0] + sum[1];
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
+                }
+                if (ok) ok = warp_wait(&sh.o_done[s], 0);
+                if (ok) {
+                    tc_fence_after();
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token left: zeros
+                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + (static_cast<size_t>(first + r) * a.Hq + h) * kV);
+                    for (int c = 0; c < kV; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_nowait(to + c, o);
+                        tmem_wait_ld();
+                        const float *f = reinterpret_cast<const float *>(o);
+                        if (r < n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[c / 8 + i] = make_uint4(pack_bf16(f[8 * i] * inv, f[8 * i + 1] * inv),
+                                                            pack_bf16(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
+                                                            pack_bf16(f[8 * i + 4] * inv, f[8 * i + 5] * inv),
+                                                            pack_bf16(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+                    }
                 }
             }
         }
@@ -862,8 +971,8 @@ bool prefill_shape_ok(int B, int T, int Hq, int L, int nope, int v, int max_tota
 // the plan's arrays.
 struct PrefillPlan {
     int64_t tiles, qtiles;   // at most
-    size_t k_bytes, v_bytes, kr_bytes, start_bytes, qtile_bytes, ok_bytes;
-    size_t total() const { return k_bytes + v_bytes + kr_bytes + start_bytes + qtile_bytes + ok_bytes + 256; }
+    size_t k_bytes, v_bytes, kr_bytes, start_bytes, qtile_bytes, info_bytes, exp_bytes;
+    size_t total() const { return k_bytes + v_bytes + kr_bytes + start_bytes + qtile_bytes + info_bytes + exp_bytes + 256; }
 };
 
 PrefillPlan prefill_plan(int B, int T, int Hq, int nope, int v, int max_total) {
@@ -876,7 +985,8 @@ PrefillPlan prefill_plan(int B, int T, int Hq, int nope, int v, int max_total) {
     p.kr_bytes = rows * kLatentRope * 2;
     p.start_bytes = align_up((static_cast<size_t>(B) + 1) * 4, 256);
     p.qtile_bytes = align_up(static_cast<size_t>(p.qtiles) * sizeof(QueryTile), 256);
-    p.ok_bytes = align_up(static_cast<size_t>(p.tiles) * 4, 256);
+    p.info_bytes = align_up(static_cast<size_t>(p.tiles) * Hq * 4, 256);
+    p.exp_bytes = rows * Hq;
     return p;
 }
 
@@ -885,6 +995,16 @@ int launch_prefill(const CUtensorMap *m, const PrefillArgs &a, unsigned grid, cu
     constexpr int kSmem = (2 * (kNope / 64 + 1) + kSlots) * kChunkBytes + static_cast<int>(sizeof(PrefillShared));
     auto kernel = latent_prefill_kernel<kNope, kV>;
     if (!allow_smem(kernel, kSmem)) return TTS_ERR_CUDA;
+    static std::atomic<int> regs{0};  // (a compiler's choice, the same on every device)
+    if (regs.load(std::memory_order_relaxed) == 0) {
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, reinterpret_cast<const void *>(kernel)) != cudaSuccess) {
+            cudaGetLastError();
+            return TTS_ERR_CUDA;
+        }
+        regs.store(attr.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < kStartRegs) return TTS_ERR_UNSUPPORTED;
     return launch_kernel(kernel, dim3(grid), dim3(kAttnThreads), kSmem, {stream, true}, m[0], m[1], m[2], m[3], m[4], a);
 }
 
@@ -943,8 +1063,10 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
     a.tile_start = reinterpret_cast<int32_t *>(at);
     a.qtiles = reinterpret_cast<QueryTile *>(at + pl.start_bytes);
     a.max_qtiles = static_cast<int>(pl.qtiles);
-    a.blocks_ok = reinterpret_cast<uint32_t *>(at + pl.start_bytes + pl.qtile_bytes);
-    a.num_qtiles = reinterpret_cast<int32_t *>(at + pl.start_bytes + pl.qtile_bytes + pl.ok_bytes);
+    a.info = reinterpret_cast<uint32_t *>(at + pl.start_bytes + pl.qtile_bytes);
+    a.max_tiles = static_cast<int>(pl.tiles);
+    a.exps = reinterpret_cast<int8_t *>(at + pl.start_bytes + pl.qtile_bytes + pl.info_bytes);
+    a.num_qtiles = reinterpret_cast<int32_t *>(at + pl.start_bytes + pl.qtile_bytes + pl.info_bytes + pl.exp_bytes);
     a.pool = static_cast<const __nv_bfloat16 *>(cache->pool);
     a.out = static_cast<__nv_bfloat16 *>(d_out);
     a.err = d_err;

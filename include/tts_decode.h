@@ -330,10 +330,12 @@ size_t tts_latent_prefill_attn_workspace_size(int32_t B, int32_t num_rows, int32
  *   t < d_ctx_lens[b] - (d_row_start[b + 1] - r) + 1.
  * The sum is tts_latent_decode_attn's, in the expanded form: keys (rounded to
  * bf16) and values (rounded to f16, as the softmax weights are) of every head
- * are multiplied out once.  A latent that is not finite makes the rows that see
- * its token so, and no others; weights that are not finite act as in the sum.
- * A value w_uv[h] c beyond f16's range (65504) makes outputs of its stream not
- * finite, from up to 127 tokens before it on.
+ * are multiplied out once.  Where a token's values of a head do not fit f16 they
+ * are kept divided by a power of two of their size, so that values are held to
+ * 2^-11 of themselves or 2^-15 of their token's largest of the head (or 2^-115).
+ * Keys and values have to lie in fp32's range.  A latent that is not finite makes the
+ * rows that see its token so, and no others; weights that are not finite act as
+ * in the sum.
  *  d_q_nope bf16 [num_rows][Hq][nope_dim];  d_q_rope bf16 [num_rows][Hq][64]
  *  d_out    bf16 [num_rows][Hq][v_dim]
  *  max_total_ctx  host upper bound of the sum of d_ctx_lens over the streams

@@ -80,3 +80,62 @@ def test_a_head_whose_weights_are_nan(bd, form, which):
     assert torch.isnan(out[:, 1].float()).all()
     for h in (0, 2):
         check(out[:, h], want[:, h], tol[:, h], f"head {h}")
+
+
+# --------------------------------------------------------- values far from one
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("v", [64, 128])
+@pytest.mark.parametrize("exps", [(-22, -22, -22), (-40, -40, -40), (20, 20, 20), (90, 90, 90), (0, -22, 24), (-60, 0, 17)])
+def test_values_of_any_size(bd, form, v, exps):
+    """Value weights times powers of two, head by head: the outputs scale
+    exactly, so each is within the same relative tolerance."""
+    n = 4 if form == "decode" else 150
+    s = ref.make([n, n], [40, 3], 3, 128, 64, v, 37)
+    want, tol = ref.attend_all(s, True, form == "decode")
+    size = torch.tensor([2.0 ** e for e in exps], dtype=torch.float64).view(1, 3, 1)
+    s["w_uv"] = (s["w_uv"].double() * size.view(3, 1, 1)).to(torch.bfloat16)
+    d = up(s)
+    out = (run_decode(bd, s, d, n, True) if form == "decode" else run_prefill(bd, s, d)).view(2 * n, 3, v)
+    check(out.double().cpu() / size, want, tol, f"{form} {exps}")
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("small,large", [(1.0, 2.0 ** 20), (1.0, 2.0 ** 60), (2.0 ** -30, 1.0), (2.0 ** -24, 2.0 ** 30)])
+def test_a_later_token_of_another_size(bd, form, small, large):
+    """The first tokens' latents times `small`, a later one's times `large`:
+    rows before it have outputs of the small size, rows that see it are right
+    too.  (The keys are kept apart: q_nope is zero, the scores are the rotated
+    parts'.)"""
+    n, before = (8, 50) if form == "decode" else (200, 10)
+    s = ref.make([n, 5 if form == "prefill" else n], [before, 2], 2, 128, 64, 64, 38)
+    s["q_nope"].zero_()
+    ids, spoilt = s["table"][0, :-(-s["ctx"][0] // 16)].long(), n // 2
+    rows = s["pool"][ids].view(-1, 192)
+    rows[:s["ctx"][0], :128] = (rows[:s["ctx"][0], :128].double() * small).to(torch.bfloat16)
+    t = before + spoilt
+    rows[t, :128] = (rows[t, :128].double() / small * large).to(torch.bfloat16)
+    s["pool"][ids] = rows.view(-1, 16, 192)
+    want, tol = ref.attend_all(s, True, form == "decode")
+    d = up(s)
+    out = run_decode(bd, s, d, n, True).view(2 * n, 2, 64) if form == "decode" else run_prefill(bd, s, d)
+    check(out[n:], want[n:], tol[n:], "the other stream")
+    check(out[:spoilt], want[:spoilt], tol[:spoilt], "rows before")
+    check(out[spoilt:n], want[spoilt:n], tol[spoilt:n], "rows that see it")
+
+
+@pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** -12, 1.0, 2.0 ** 40])
+def test_prompt_tokens_without_values(bd, size):
+    """The first 130 tokens' latents are zero, the others of one size: the
+    zeros have their weights and add nothing."""
+    s = ref.make([170], [60], 2, 128, 64, 64, 41)
+    s["q_nope"].zero_()
+    ids = s["table"][0, :-(-s["ctx"][0] // 16)].long()
+    rows = s["pool"][ids].view(-1, 192)
+    rows[:130, :128] = 0
+    rows[130:230, :128] = (rows[130:230, :128].double() * size).to(torch.bfloat16)
+    s["pool"][ids] = rows.view(-1, 16, 192)
+    want, tol = ref.attend_all(s, True, False)
+    out = run_prefill(bd, s, up(s))
+    check(out, want, tol)
+    assert (out[:70] == 0).all() and (out[70:] != 0).any()
