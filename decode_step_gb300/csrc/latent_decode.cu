@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "latent_common.cuh"
@@ -319,8 +320,9 @@ __device__ __forceinline__ bool softmax_any(bool pred) {
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
-// Sets the bf16 values in 16 bytes of shared memory that are not finite to zero.
-__device__ __forceinline__ void keep_finite(uint32_t at) {
+// Sets the bf16 values in 16 bytes of shared memory that are not finite to zero;
+// whether there were any.
+__device__ __forceinline__ bool keep_finite(uint32_t at) {
     uint32_t x[4];
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
     bool found = false;
@@ -333,6 +335,7 @@ __device__ __forceinline__ void keep_finite(uint32_t at) {
     }
     if (found)
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+    return found;
 }
 
 // Position in a ring of shared-memory slots; phase is the parity of the
@@ -364,6 +367,7 @@ struct AttnShared {
     uint32_t tmem;
     int sums[8];
     int failed;
+    int spoilt;       // of the tokens that not every row sees, the first whose latent is not finite
     alignas(16) float mref[kMaxGroup];
     float fac[kMaxGroup];
     int limit[kMaxGroup];
@@ -709,6 +713,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         while (ok && more) {
             const int low = a.causal ? seg.ctx - a.q_len + 1 : seg.ctx;  // tokens every row sees
             softmax_sync();  // the last segment's reads of these are over
+            if (tid == 0) sh.spoilt = INT_MAX;
             if (tid < N) {
                 sh.mref[tid] = kNoScore;
                 const int j = (seg.cur_g * N + tid) / a.Hq;
@@ -821,16 +826,19 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     store(at_hi + i * 256, hi);
                     store(at_lo + i * 256, lo);
                 }
-                // A later row's token that is not finite would spread to the
-                // rows that do not see it (NaN times a zero weight).  The scores
-                // have it already: the rows that see it have NaN weights, the
-                // product can do without it.
+                // A later row's latent that is not finite would spread to the
+                // rows that do not see it (NaN times a zero weight): the product
+                // does without it, and the rows that do see it get a NaN sum
+                // (their scores of it may be minus infinity, a weight of zero).
                 const int hi = min(seg.ctx - tile * kTile, kTile), lo = max(low - tile * kTile, 0);
                 if (lo < hi)
                     for (int p = 0; p < nb; ++p) {
                         const int slot = lslot + p < a.pairs ? lslot + p : lslot + p - a.pairs;
-                        for (int i = tid; i < (hi - lo) * 16; i += 128)
-                            keep_finite(l_base + slot * kPairBytes + i / 8 % 2 * kChunkBytes + (lo + i / 16) * 128 + i % 8 * 16);
+                        for (int i = tid; i < (hi - lo) * 16; i += 128) {
+                            if (2 * p + i / 8 % 2 == chunks) continue;  // (an odd last chunk's other half is not loaded)
+                            if (keep_finite(l_base + slot * kPairBytes + i / 8 % 2 * kChunkBytes + (lo + i / 16) * 128 + i % 8 * 16))
+                                atomicMin(&sh.spoilt, tile * kTile + lo + i / 16);
+                        }
                     }
                 lslot = lslot + nb < a.pairs ? lslot + nb : lslot + nb - a.pairs;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -857,9 +865,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             }
             const size_t slot = static_cast<size_t>(blockIdx.x) + bg;
             softmax_sync();
-            if (tid < N)
-                a.ml[slot * N + tid] = make_float2(
-                    sh.mref[tid], (sh.lsum[0][tid] + sh.lsum[1][tid]) + (sh.lsum[2][tid] + sh.lsum[3][tid]));
+            if (tid < N) {
+                const float sum = (sh.lsum[0][tid] + sh.lsum[1][tid]) + (sh.lsum[2][tid] + sh.lsum[3][tid]);
+                a.ml[slot * N + tid] = make_float2(sh.mref[tid], sh.limit[tid] > sh.spoilt ? NAN : sum);
+            }
             tc_fence_after();
             for (int p = 0; p < nb; ++p) {
                 const int d = p * 128 + warp * 32 + lane;

@@ -296,8 +296,8 @@ size_t tts_latent_decode_attn_workspace_size(int32_t B, int32_t q_len, int32_t n
  * after this step's append; causal as there).  Computed in the absorbed form:
  * q_nope w_uk[h] first (rounded to bf16), attention over the latents
  * themselves (weights as two bf16 numbers), then w_uv[h] on the attended
- * latent.  A token that is not finite makes the rows that see it so, and no
- * others.
+ * latent.  A latent that is not finite makes the rows that see its token so, and
+ * no others; a key part that is not finite acts through its scores.
  *  d_q_nope  bf16 [B][q_len][Hq][nope_dim]
  *  d_q_rope  bf16 [B][q_len][Hq][64], rotated (tts_latent_append)
  *  d_w_uk    bf16 [Hq][nope_dim][latent_dim];  d_w_uv  bf16 [Hq][v_dim][latent_dim]

@@ -32,6 +32,34 @@ def not_finite(x):
 # ------------------------------------------------- latents that are not finite
 
 @pytest.mark.parametrize("what", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("q_len,ctx,Hq,first", [(5, 71, 16, 2), (5, 66, 4, 1), (3, 64, 16, 0), (8, 130, 20, 7), (70, 200, 2, 30)])
+def test_decode_rows_that_see_an_infinite_latent(bd, what, q_len, ctx, Hq, first):
+    """One element of a late token's latent: its score is minus infinity for
+    the heads whose q~ has the other sign there, so that its weight is zero;
+    in the definition the value times that zero is still not a number.  Rows
+    before the token do not see it."""
+    s = ref.make([q_len] * 2, [ctx - q_len] * 2, Hq, 192, 128, 64, 12)
+    want, tol = ref.attend_all(s, True, True)
+    spoil(s, 0, ctx - q_len + first, 11, what)
+    out = run_decode(bd, s, up(s), q_len, True).view(2, q_len, Hq, 64)
+    want, tol = want.view(out.shape), tol.view(out.shape)
+    check(out[1], want[1], tol[1], "the other stream")
+    if first:
+        check(out[0, :first], want[0, :first], tol[0, :first], "rows before")
+    assert not_finite(out[0, first:]).all()
+
+
+@pytest.mark.parametrize("what", [NAN, math.inf, -math.inf])
+def test_decode_an_infinite_latent_that_all_rows_see(bd, what):
+    s = ref.make([5] * 2, [100, 60], 16, 192, 128, 64, 13)
+    want, tol = ref.attend_all(s, True, True)
+    spoil(s, 0, 17, 191, what)
+    out = run_decode(bd, s, up(s), 5, True).view(10, 16, 64)
+    check(out[5:], want[5:], tol[5:], "the other stream")
+    assert not_finite(out[:5]).all()
+
+
+@pytest.mark.parametrize("what", [NAN, math.inf, -math.inf])
 @pytest.mark.parametrize("n,before,spoilt", [(140, 20, 100), (300, 3, 200), (7, 0, 1), (20, 125, 3)])
 def test_prefill_rows_that_see_an_infinite_latent(bd, what, n, before, spoilt):
     """Queries and key weights of one sign, so that every head's score of the
