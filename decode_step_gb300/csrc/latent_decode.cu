@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 
@@ -49,7 +50,9 @@ constexpr int kMaxGroup = 64;          // query rows per work unit
 constexpr int kCtas = 152;             // one per SM
 constexpr int kAttnThreads = 224;      // 4 softmax warps, KV producer, MMA issuer, Q loader
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoScore = -1e30f;     // running maximum before any token (log2 units)
+// Running maximum before any token (log2 units): no finite score is below it, so
+// that a row whose scores are all far below zero still has weights.
+constexpr float kNoScore = -FLT_MAX;
 // The running maximum is moved only when a score passes it by this much (log2
 // units): weights then reach 2^8, which fp32 sums and bf16 weights hold as
 // well as 1, and O in tensor memory is rarely rescaled.

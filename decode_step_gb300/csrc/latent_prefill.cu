@@ -22,6 +22,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -38,7 +39,9 @@ constexpr int kTile = 128;                 // tokens per tile, rows per query ha
 constexpr int kRows = 256;                 // query rows per work item
 constexpr int kChunkBytes = kTile * 128;   // [128 rows][64 values] bf16, 128-byte swizzle
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoScore = -1e30f;         // running maximum before any token (log2 units)
+// Running maximum before any token (log2 units): no finite score is below it, so
+// that a row whose scores are all far below zero still has weights.
+constexpr float kNoScore = -FLT_MAX;
 constexpr float kSlack = 8.0f;             // scores may pass it by this much before it moves (log2 units)
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {

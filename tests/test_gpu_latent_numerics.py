@@ -167,3 +167,25 @@ def test_prompt_tokens_without_values(bd, size):
     out = run_prefill(bd, s, up(s))
     check(out, want, tol)
     assert (out[:70] == 0).all() and (out[70:] != 0).any()
+
+
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+def test_scores_far_below_zero(bd, form):
+    """Every score of a row at -1.2e32 or (the first tokens') twice that: the
+    softmax is over the others, evenly."""
+    n = 2 if form == "decode" else 140
+    s = ref.make([n], [90], 2, 128, 64, 64, 39)
+    s["q_nope"].zero_()
+    s["q_rope"].zero_()
+    s["q_rope"][..., 3] = -2.0 ** 55
+    ids = s["table"][0, :-(-s["ctx"][0] // 16)].long()
+    rows = s["pool"][ids].view(-1, 192)
+    rows[:, 128:] = 0
+    rows[:, 128 + 3] = 2.0 ** 55
+    rows[:70, 128 + 3] = 2.0 ** 56
+    s["pool"][ids] = rows.view(-1, 16, 192)
+    want, tol = ref.attend_all(s, True, form == "decode")
+    assert (want != 0).all()
+    d = up(s)
+    out = run_decode(bd, s, d, n, True).view(n, 2, 64) if form == "decode" else run_prefill(bd, s, d)
+    check(out, want, tol, form)
