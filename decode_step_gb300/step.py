@@ -109,11 +109,15 @@ class LatentStep:
                stream=None) -> torch.Tensor:
         """Appends the packed rows of up to B streams (stream b: rows
         row_start[b]..row_start[b + 1] - 1 at positions ctx_before[b]..) and
-        attends causally; returns the attention output [rows][Hq][v_dim]."""
+        attends causally; returns the attention output [rows][Hq][v_dim] (a new
+        tensor of `stream`, unless `out` is given)."""
         T = c_new.shape[0]
         if T > self.prompt_rows:
             raise ValueError(f"{T} prompt rows exceed prompt_rows = {self.prompt_rows}")
-        out = torch.empty((T, self.Hq, self.v), dtype=torch.bfloat16, device=self.out.device) if out is None else out
+        if out is None:
+            # allocated on the stream that writes it: memory freed on the current one may still be in use there
+            with torch.cuda.stream(stream):
+                out = torch.empty((T, self.Hq, self.v), dtype=torch.bfloat16, device=self.out.device)
         q = self.q[:T]
         bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope, q, self.rope_base,
                              row_start=row_start, err=self.err, stream=stream)
