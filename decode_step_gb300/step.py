@@ -64,6 +64,11 @@ class DecodeStep:
         return self.ids
 
 
+def _capturing(stream: torch.cuda.Stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class LatentStep:
     """A batch's steps over a latent cache, for fixed shapes: `prompt` appends
     whole prompts and attends over them, calling the object appends q_len
@@ -74,6 +79,13 @@ class LatentStep:
     (`out` [B][q_len][Hq][v_dim], `ids` [B * q_len]).  Key and query rotary
     parts are passed unrotated.  prompt_rows and prompt_ctx bound a prompt
     call's rows and the sum of its streams' context lengths (0: no prompts).
+
+    Prompts may run on one CUDA stream while steps of other streams' blocks run
+    on another: the two have workspaces and query buffers of their own (`q` is
+    the latest call's rotated queries).  Calls of one kind share theirs, and a
+    call on another stream than the last one of its kind waits for what that
+    stream holds.  Not while a graph is being captured, and not for replays:
+    there the caller keeps calls of one kind apart.
     """
 
     def __init__(self, cache: bd.LatentCache, w_uk: torch.Tensor, w_uv: torch.Tensor, W: torch.Tensor, B: int,
@@ -97,13 +109,25 @@ class LatentStep:
         prompt_ws = bd.tts_latent_prefill_attn_workspace_size(B, prompt_rows, Hq, L, nope, v, prompt_ctx)
         if ws == 0 or head_ws == 0 or prompt_ws == 0:
             raise ValueError("unsupported latent-step shape")
-        self.ws = torch.empty(max(ws, prompt_ws if prompt_rows else 0), dtype=torch.uint8, device=dev)
+        self.ws = torch.empty(ws, dtype=torch.uint8, device=dev)
+        self.prompt_ws = torch.empty(prompt_ws if prompt_rows else 0, dtype=torch.uint8, device=dev)
         self.head_ws = torch.zeros(head_ws, dtype=torch.uint8, device=dev)
-        self.q = torch.empty((max(self.R, prompt_rows), Hq, cache.ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        self.step_q = torch.empty((self.R, Hq, cache.ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        self.prompt_q = torch.empty((prompt_rows, Hq, cache.ROPE_DIM), dtype=torch.bfloat16, device=dev)
+        self.q = self.step_q
+        self._streams: dict[str, torch.cuda.Stream] = {}  # of the latest call of each kind
         self.out = torch.empty((B, q_len, Hq, v), dtype=torch.bfloat16, device=dev)
         self.ids = torch.empty(self.R, dtype=torch.int32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.prompt_rows, self.prompt_ctx = prompt_rows, prompt_ctx
+
+    def _follow(self, kind: str, stream) -> None:
+        """Orders a call behind the latest one of its kind."""
+        now = torch.cuda.current_stream(self.out.device) if stream is None else stream
+        last = self._streams.get(kind, now)
+        if last != now and not (_capturing(last) or _capturing(now)):
+            now.wait_stream(last)
+        self._streams[kind] = now
 
     def prompt(self, block_table, ctx_before, ctx_lens, row_start, q_nope, q_rope, c_new, kr_new, out=None,
                stream=None) -> torch.Tensor:
@@ -118,11 +142,12 @@ class LatentStep:
             # allocated on the stream that writes it: memory freed on the current one may still be in use there
             with torch.cuda.stream(stream):
                 out = torch.empty((T, self.Hq, self.v), dtype=torch.bfloat16, device=self.out.device)
-        q = self.q[:T]
+        self._follow("prompt", stream)
+        q = self.q = self.prompt_q[:T]
         bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope, q, self.rope_base,
                              row_start=row_start, err=self.err, stream=stream)
         bd.tts_latent_prefill_attn(self.cache, block_table, ctx_lens, self.prompt_ctx, row_start, q_nope, q, self.w_uk,
-                                   self.w_uv, out, self.ws, self.scale, err=self.err, stream=stream)
+                                   self.w_uv, out, self.prompt_ws, self.scale, err=self.err, stream=stream)
         return out
 
     def __call__(self, block_table, ctx_before, ctx_lens, q_nope, q_rope, c_new, kr_new, seed=None, step=None,
@@ -130,7 +155,8 @@ class LatentStep:
         """One step: q_nope [B][q_len][Hq][nope_dim], q_rope [B][q_len][Hq][64],
         c_new [B * q_len][latent_dim], kr_new [B * q_len][64]; returns the
         device tensor of chosen ids [B * q_len]."""
-        q = self.q[:self.R]
+        self._follow("step", stream)
+        q = self.q = self.step_q
         bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope.view(self.R, self.Hq, -1), q,
                              self.rope_base, err=self.err, stream=stream)
         # the later kernels start while the ones before them finish
