@@ -189,3 +189,81 @@ def test_scores_far_below_zero(bd, form):
     d = up(s)
     out = run_decode(bd, s, d, n, True).view(n, 2, 64) if form == "decode" else run_prefill(bd, s, d)
     check(out, want, tol, form)
+
+
+# --------------------------------------------------------- the inner roundings
+#
+# q_nope is zero, so q~ and the expanded keys do not matter and the scores are
+# the rotated parts' (fp32).  A head's w_uv takes two latent dimensions in the
+# proportion in which its row's attended latent cancels, so that the output is
+# some 2^-9 of its terms and its own rounding some 2^-17 of them: what is left
+# is the roundings inside.  In units of the terms, with half steps h (bf16 2^-8,
+# f16 2^-11) and softmax weights p_t:
+#   decode  weights and attended latents each as a rounding and the rounding of
+#           its remainder: off by at most h^2 = 2^-16 each
+#   prompt  weights and values to f16: independent, each of variance at most
+#           h^2 / 3 = 2^-22 / 3 of its square
+# plus 2^-18 of the terms for fp32 (scores up to 16 to 2^-23 of themselves, the
+# hardware exponential, sums of some hundred terms) and half a step of the output.
+
+def cancelling(s):
+    """w_uv so that the last row's outputs cancel; returns, per head and output
+    dimension, the definition's output, the sum of the terms' sizes over tokens
+    and over latent dimensions, and the root of the sum of their squares."""
+    Hq, L, v = s["Hq"], s["L"], s["v"]
+    s["q_nope"].zero_()
+    rows, _ = ref.cached_rows(s, 0)
+    c, kr = rows[:, :L], rows[:, L:]
+    sc = s["scale"] * (s["q_rope"][s["new"][0] - 1].double() @ kr.t())
+    assert float(sc.abs().max()) < 16
+    p = torch.softmax(sc, 1)                                   # [Hq][ctx]
+    lat = p @ c
+    s["w_uv"].zero_()
+    for h in range(Hq):
+        for d in range(v):
+            i, j = d, v + (5 * d + 3 * h) % (L - v)
+            k = math.frexp(max(abs(float(lat[h, i])), abs(float(lat[h, j]))))[1]
+            s["w_uv"][h, d, i] = math.ldexp(float(lat[h, j]), -k)
+            s["w_uv"][h, d, j] = -math.ldexp(float(lat[h, i]), -k)
+    w = s["w_uv"].double()
+    val = torch.einsum("hdl,tl->htd", w, c)
+    out = torch.einsum("ht,htd->hd", p, val)
+    assert (ref.attend(s, 0, True, False)[0][-1] - out).abs().max() < 1e-12
+    return dict(p=p, c=c, w=w, val=val, out=out,
+                tokens=torch.einsum("ht,hdl,tl->hd", p, w.abs(), c.abs()), latents=torch.einsum("hl,hdl->hd", lat.abs(), w.abs()),
+                squares=torch.einsum("ht,htd->hd", p * p, val * val).sqrt(),
+                values=torch.einsum("ht,htd->hd", p, val.abs()))
+
+
+def decode_tol(x):
+    return 2.0 ** -8 * x["out"].abs() + 2.0 ** -16 * (x["tokens"] + x["latents"]) + 2.0 ** -18 * x["tokens"]
+
+
+def prefill_tol(x):
+    # eight standard deviations of 2 squares' worth of roundings
+    return 2.0 ** -8 * x["out"].abs() + 8 * 2.0 ** -11 * x["squares"] * (2 / 3) ** 0.5 + 2.0 ** -18 * x["tokens"]
+
+
+def decode_inputs(Hq, ctx):
+    return ref.make([1], [ctx - 1], Hq, 192, 64, 64, 40 + Hq, q_gain=3.0)
+
+
+def prefill_inputs(v):
+    return ref.make([150], [60], 16, 256, 64, v, 50 + v, q_gain=3.0)
+
+
+@pytest.mark.parametrize("Hq", [16, 32, 48, 64, 128])
+@pytest.mark.parametrize("ctx", [60, 500])
+def test_decode_inner_roundings(bd, Hq, ctx):
+    s = decode_inputs(Hq, ctx)
+    x = cancelling(s)
+    out = run_decode(bd, s, up(s), 1, False)
+    check(out.view(Hq, 64), x["out"], decode_tol(x), "decode")
+
+
+@pytest.mark.parametrize("v", [64, 128])
+def test_prefill_inner_roundings(bd, v):
+    s = prefill_inputs(v)
+    x = cancelling(s)
+    out = run_prefill(bd, s, up(s))
+    check(out[-1], x["out"], prefill_tol(x), "prefill")
