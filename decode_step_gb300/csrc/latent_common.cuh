@@ -60,9 +60,11 @@ inline int launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
 // tcgen05 and TMA instructions take their operands from.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
 
-// Bounded mbarrier wait by a whole converged warp, with one answer.
-__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity) {
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(bar), parity));
+// Bounded mbarrier wait by a whole converged warp, with one answer.  Waits for
+// copies and products that are on their way when a kernel gives up take the
+// default limit.
+__device__ __forceinline__ bool warp_wait(const uint64_t *bar, uint32_t parity, long long limit = kWaitLimitCycles) {
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_addr(bar), parity, limit));
     __syncwarp();
     return ok;
 }
@@ -101,11 +103,11 @@ struct WarpWaits {
         __syncwarp();
         return all;
     }
-    __device__ __forceinline__ bool wait() const {
+    __device__ __forceinline__ bool wait(long long limit = kWaitLimitCycles) const {
         if (poll()) return true;
         bool all = true;
 #pragma unroll
-        for (int i = 0; i < kMax; ++i) all = all && (bar[i] == 0 || mbar_wait(bar[i], parity[i]));
+        for (int i = 0; i < kMax; ++i) all = all && (bar[i] == 0 || mbar_wait(bar[i], parity[i], limit));
         all = __all_sync(0xFFFFFFFFu, all);
         __syncwarp();
         return all;

@@ -217,6 +217,8 @@ struct LatentAttnArgs {
     int2 *owner;       // [B * G] first CTA and number of splits of each group
     int32_t *err;
     int pairs, ropes;  // ring slots
+    long long wait_limit;  // SM clock cycles per bounded wait
+    int stall;         // test support: a CTA's first tile expects 16 bytes that never come
 };
 
 // Tiles of a stream of `ctx` tokens (0: out of range).
@@ -507,19 +509,19 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 int ys[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) ys[i] = __shfl_sync(kFull, y, i);
-                if (it >= rope.n && !warp_wait(&sh.empty_r[rope.slot], rope.phase ^ 1)) {
+                if (it >= rope.n && !warp_wait(&sh.empty_r[rope.slot], rope.phase ^ 1, a.wait_limit)) {
                     ok = false;
                     break;
                 }
                 // (the tile's one barrier: the MMAs of S^T take the whole tile)
                 const uint32_t bar = smem_addr(&sh.full[rope.slot]), at = r_base + rope.slot * kChunkBytes;
-                mbar_expect_tx_by(leader, bar, (chunks + 1) * kChunkBytes);
+                mbar_expect_tx_by(leader, bar, (chunks + 1) * kChunkBytes + (a.stall && it == 0 ? 16 : 0));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tma_load_2d_by(leader, at + i * 2048, &map_kv, a.L, ys[i], bar);
                 rope.next();
                 ++it;
                 for (int p = 0; p < nb; ++p) {
-                    if (lpos >= lat.n && !warp_wait(&sh.empty_l[lat.slot], lat.phase ^ 1)) {
+                    if (lpos >= lat.n && !warp_wait(&sh.empty_l[lat.slot], lat.phase ^ 1, a.wait_limit)) {
                         ok = false;
                         break;
                     }
@@ -546,7 +548,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         const uint32_t leader = elect_leader();
         uint32_t s = 0;
         for (; seg.next(a); ++s) {
-            if (s > 0 && !warp_wait(&sh.q_empty, (s - 1) & 1)) {
+            if (s > 0 && !warp_wait(&sh.q_empty, (s - 1) & 1, a.wait_limit)) {
                 ok = false;
                 break;
             }
@@ -620,10 +622,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     while (!ready && pending && ok) {
                         if (wo.poll()) issue_o(it - 1);
                         ready = w.poll();
-                        ok = uniform(clock64() - t0 < kWaitLimitCycles);
+                        ok = uniform(clock64() - t0 < a.wait_limit);
                     }
                 }
-                if (!ok || (!ready && !w.wait())) {
+                if (!ok || (!ready && !w.wait(a.wait_limit))) {
                     ok = false;
                     break;
                 }
@@ -651,7 +653,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                 mma_commit_by(leader, smem_addr(&sh.s_full[buf]));
                 if (k + 1 == count) mma_commit_by(leader, smem_addr(&sh.q_empty));
                 if (pending) {
-                    if (!weights(it - 1).wait()) {
+                    if (!weights(it - 1).wait(a.wait_limit)) {
                         ok = false;
                         break;
                     }
@@ -684,7 +686,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
             ++segs;
         }
         if (ok && pending) {
-            ok = weights(it - 1).wait();
+            ok = weights(it - 1).wait(a.wait_limit);
             if (ok) issue_o(it - 1);
         }
         mma_commit_by(leader, smem_addr(&sh.done));
@@ -703,7 +705,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
         // a row of a transposed 8 x 8 matrix: the lane's of a store of four,
         // rows 0-7 at tokens 0-7 and 8-15, then rows 8-15
         const uint32_t pat = p_base + (lane / 16 * 8 + lane % 8) * 128 + (((2 * warp + lane / 8 % 2) ^ (lane % 8)) << 4);
-        auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1); };
+        auto o_added = [&](uint32_t tile) { return warp_wait(&sh.p_empty[tile % kPBufs], (tile / kPBufs) & 1, a.wait_limit); };
         const int tid = threadIdx.x;
         int lslot = 0, rslot = 0;  // the tile's ring slots: its first latent pair, its rope chunk
         auto block_ok = [&](const Segments &s, int tile) {
@@ -739,7 +741,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_cons
                     mr[2 * j] = m2.x;
                     mr[2 * j + 1] = m2.y;
                 }
-                if (!warp_wait(&sh.s_full[buf], (it / 2) & 1)) ok = false;
+                if (!warp_wait(&sh.s_full[buf], (it / 2) & 1, a.wait_limit)) ok = false;
                 tc_fence_after();
                 uint32_t sr[kVals];
 #pragma unroll
@@ -1413,6 +1415,8 @@ extern "C" int tts_latent_decode_attn(const tts_latent_cache *cache, const int32
     a.ml = reinterpret_cast<float2 *>(ws + pl.qt_bytes + pl.part_bytes);
     a.owner = reinterpret_cast<int2 *>(ws + pl.qt_bytes + pl.part_bytes + pl.ml_bytes);
     a.err = d_err;
+    a.wait_limit = thread_opts().wait_limit;
+    a.stall = thread_opts().stall == TTS_TEST_STALL_LATENT_DECODE;
     const int R = B * q_len, Hq = num_q_heads;
     const uint64_t qrows = static_cast<uint64_t>(R) * Hq;
     CUtensorMap map_kv, map_q, map_qr, map_qn, map_uk, map_qt, map_uv;

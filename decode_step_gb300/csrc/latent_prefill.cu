@@ -94,6 +94,8 @@ struct PrefillArgs {
     __nv_bfloat16 *kr;     // [token tiles * 128][64]
     __nv_bfloat16 *out;
     int32_t *err;
+    long long wait_limit;  // SM clock cycles per bounded wait of the attention
+    int stall;             // test support: the first tile's keys expect 16 bytes that never come
 };
 
 // ------------------------------------------------------------------ expand
@@ -752,14 +754,14 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                     auto slot_free = [&]() {
                         if (pos < kSlots) return true;
                         const uint32_t j = (pos - kSlots) / (kQc + kVc), c = (pos - kSlots) % (kQc + kVc);
-                        return mbar_wait(smem_addr((c < kQc ? sh.k_done : sh.v_done) + j % kTiles), (j / kTiles) & 1);
+                        return mbar_wait(smem_addr((c < kQc ? sh.k_done : sh.v_done) + j % kTiles), (j / kTiles) & 1, a.wait_limit);
                     };
                     int j = 0;
                     for (; ok && j < nt; ++j) {
                         const int y = (tile0 + j) * kTile;
                         for (int c = 0; ok && c < kQc + kVc; ++c, ++pos) {
                             const uint32_t bar = smem_addr((c < kQc ? sh.k_full : sh.v_full) + j % kTiles);
-                            if (c == 0 || c == kQc) mbar_arrive_expect_tx(bar, (c ? kVc : kQc) * kChunkBytes);
+                            if (c == 0 || c == kQc) mbar_arrive_expect_tx(bar, (c ? kVc : kQc) * kChunkBytes + (a.stall && j == 0 && c == 0 ? 16 : 0));
                             ok = slot_free();
                             const uint32_t at = ring + pos % kSlots * kChunkBytes;
                             if (!ok) break;
@@ -768,7 +770,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                             else tma_load_2d(at, &map_v, h * kV + (c - kQc) * 64, y, bar);
                         }
                     }
-                    for (int i = max(0, j - 2); i < j; ++i) {
+                    for (int i = max(0, j - kTiles); i < j; ++i) {  // (the ring holds parts of at most kTiles tiles)
                         mbar_wait(smem_addr(&sh.k_full[i % kTiles]), (i / kTiles) & 1);
                         mbar_wait(smem_addr(&sh.v_full[i % kTiles]), (i / kTiles) & 1);
                     }
@@ -816,7 +818,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                     w.set(1, &sh.q_full[0], 0);
                     w.none(2);
                     if (two) w.set(2, &sh.q_full[1], 0);
-                    go = w.wait();
+                    go = w.wait(a.wait_limit);
                     tc_fence_after();
                     if (go) {
                         scores(h0, 0);
@@ -832,13 +834,13 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                         WarpWaits<2> w;
                         w.set(0, &sh.p_full[s], j & 1);
                         w.set(1, &sh.v_full[j % kTiles], (j / kTiles) & 1);
-                        go = w.wait();
+                        go = w.wait(a.wait_limit);
                         if (!go) return;
                         tc_fence_after();
                         output(half, j);
                         if (last) mma_commit_by(leader, smem_addr(&sh.v_done[j % kTiles]));
                         if (j + 1 < mine) {
-                            go = warp_wait(&sh.k_full[(j + 1) % kTiles], ((j + 1) / kTiles) & 1);
+                            go = warp_wait(&sh.k_full[(j + 1) % kTiles], ((j + 1) / kTiles) & 1, a.wait_limit);
                             if (!go) return;
                             tc_fence_after();
                             scores(half, j + 1);
@@ -870,7 +872,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                 uint32_t mask = info[0];
                 for (int j = 0; j < tiles; ++j) {
                     const uint32_t next_mask = j + 1 < tiles ? info[j + 1] : 0;
-                    if (!warp_wait(&sh.s_full[s], j & 1)) {
+                    if (!warp_wait(&sh.s_full[s], j & 1, a.wait_limit)) {
                         ok = false;
                         break;
                     }
@@ -932,7 +934,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
                 }
-                if (ok) ok = warp_wait(&sh.o_done[s], 0);
+                if (ok) ok = warp_wait(&sh.o_done[s], 0, a.wait_limit);
                 if (ok) {
                     tc_fence_after();
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token left: zeros
@@ -1073,6 +1075,8 @@ extern "C" int tts_latent_prefill_attn(const tts_latent_cache *cache, const int3
     a.pool = static_cast<const __nv_bfloat16 *>(cache->pool);
     a.out = static_cast<__nv_bfloat16 *>(d_out);
     a.err = d_err;
+    a.wait_limit = thread_opts().wait_limit;
+    a.stall = thread_opts().stall == TTS_TEST_STALL_LATENT_PREFILL;
     const uint64_t kv_rows = static_cast<uint64_t>(pl.tiles) * kTile, T = num_rows;
     const uint64_t fk = static_cast<uint64_t>(Hq) * nope_dim, fv = static_cast<uint64_t>(Hq) * v_dim;
     CUtensorMap pool, uk, uv, qkv[5];

@@ -345,8 +345,8 @@ size_t tts_latent_prefill_attn_workspace_size(int32_t B, int32_t num_rows, int32
  * 16 * max_blocks_per_seq] or takes the sum past max_total_ctx, gets zeros in
  * its rows that lie in [0, num_rows) (TTS_ERRBIT_CTX_LEN); tokens in blocks
  * with an invalid id are left out (TTS_ERRBIT_BLOCK_ID), and a row left
- * without tokens gets zeros.  num_q_heads <= 1024; other limits as
- * tts_latent_decode_attn. */
+ * without tokens gets zeros.  TTS_ERRBIT_TIMEOUT as tts_latent_decode_attn.
+ * num_q_heads <= 1024; other limits as tts_latent_decode_attn. */
 int tts_latent_prefill_attn(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                             const int32_t *d_ctx_lens, int32_t max_total_ctx, int32_t B, const int32_t *d_row_start,
                             int32_t num_rows, int32_t num_q_heads, int32_t nope_dim, int32_t v_dim, float scale,
@@ -699,12 +699,22 @@ int32_t tts_set_launch_flags(int32_t flags);
  *     kernel expects 16 more bytes on its first ring stage than its copies
  *     deliver, so its first wait runs out;
  *   TTS_TEST_STALL_PREDICTOR_GRID: the persistent code-predictor kernel's
- *     first grid barrier waits for one CTA more than the grid has.
+ *     first grid barrier waits for one CTA more than the grid has;
+ *   TTS_TEST_STALL_LATENT_DECODE, TTS_TEST_STALL_LATENT_PREFILL: the first tile
+ *     of every CTA of tts_latent_decode_attn's (tts_latent_prefill_attn's)
+ *     attention kernel expects 16 more bytes than its copies deliver (these
+ *     kernels wait for what is on its way with the default limit).
  * The kernel then ORs TTS_ERRBIT_TIMEOUT into *d_err, stops issuing work,
  * waits (bounded) for the copies it issued, and returns; its outputs are
  * undefined.  TTS_TEST_STALL_NONE restores normal operation.
  * TTS_ERR_INVALID for an unknown mode or a limit outside [1e3, 4e9]. */
-enum { TTS_TEST_STALL_NONE = 0, TTS_TEST_STALL_ATTN_RING = 1, TTS_TEST_STALL_PREDICTOR_GRID = 2 };
+enum {
+    TTS_TEST_STALL_NONE = 0,
+    TTS_TEST_STALL_ATTN_RING = 1,
+    TTS_TEST_STALL_PREDICTOR_GRID = 2,
+    TTS_TEST_STALL_LATENT_DECODE = 4, /* (3 is no mode) */
+    TTS_TEST_STALL_LATENT_PREFILL = 5
+};
 int tts_test_set_stall(int32_t what, int64_t wait_limit_cycles);
 
 /* Test support (no counterpart on the pages): the Gumbel noise every Gumbel
