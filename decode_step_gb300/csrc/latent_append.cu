@@ -7,8 +7,8 @@
 // latent_dim / 8 copies.  Pure data movement: the bytes are each row's 2
 // (latent_dim + 64) + 2 x 64 Hq, read once and written once.
 // A CTA takes one row, or four where there are more rows than CTAs fit at once
-// (a CTA's time is latency): 8409 rows of 16 heads take 11.5 us, 4.7 TB/s (one
-// by one 14.6 us), 64 rows 3.4 us.
+// (a CTA's time is latency): 8409 rows of 16 heads take 10.9 us, 4.9 TB/s (one
+// by one 14.6 us), 64 rows 2.6 us.
 // The rows' first items are loaded before their positions are known (they do
 // not depend on them); meanwhile a warp per row finds the stream and the block
 // and computes the 32 angles, shared through shared memory.
@@ -25,7 +25,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kAhead = 2;  // items per thread and row loaded before the position is known
-constexpr int kAtOnce = 152 * 16;  // CTAs of 128 threads that run at once
+// One-row CTAs that run at once (38 registers a thread: twelve an SM).  Up to so
+// many rows the one-row kernel is ahead (1520 rows 3.85 us against 4.2), beyond
+// them its second wave is not (2000 rows 5.15 against 4.45, 2432 rows 5.35 against
+// 4.5; 16 heads, latent 512).
+constexpr int kAtOnce = 152 * 12;
 constexpr int kHalf = kLatentRope / 2;
 
 // Rotary frequencies base^(-2i/64) in turns a token, scaled by 2^64: a
