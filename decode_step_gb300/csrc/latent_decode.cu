@@ -159,8 +159,9 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_co
 // The work units are the 64-token tiles of every (stream, row group), group
 // bg = b * G + g, in order, cut evenly over the CTAs; each group has one unit
 // before its tiles (two with 48 rows or more), which stands for what starting
-// and ending a group costs (a tile's time, about; 80 verify rows a stream: 53.1
-// us the call with two, 53.6 with one).  The part of a group that a CTA takes is
+// and ending a group costs, a tile's time or two (16 rows, 64 streams: 23.8 us
+// the call with one, 24.3 with two; 48 rows 32.6 and 31.8, at latent 256 23.5 and
+// 22.4; 64 rows 36.3 and 35.9).  The part of a group that a CTA takes is
 // a segment; its partial result goes to slot c + bg (unique: going on to the
 // next segment raises one of the two).
 __host__ __device__ constexpr int start_units(int N) { return N >= 48 ? 2 : 1; }
@@ -383,8 +384,11 @@ struct AttnShared {
 };
 
 // Buffers for the weights P: with one, the softmax waits for the O^T of the
-// tile before; wide groups need the space for the ring.
-__host__ __device__ constexpr int p_buffers(int N) { return N == 16 || N == 48 ? 2 : 1; }
+// tile before.  A second one pays at 48 rows (64 streams x 5 causal rows of 16
+// heads 54.0 us the call against 54.5); with 16 it makes no difference (64 streams
+// 23.8), with 32 its space is worth more to the ring (28.1 against 28.4), with 64
+// it does not fit.
+__host__ __device__ constexpr int p_buffers(int N) { return N == 48 ? 2 : 1; }
 
 // P enters the product as two bf16 numbers, its rounding and the remainder:
 // the weights are then held to 2^-17.  Up to 48 rows the remainders are N more
