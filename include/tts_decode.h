@@ -309,8 +309,9 @@ size_t tts_latent_decode_attn_workspace_size(int32_t B, int32_t q_len, int32_t n
  * (TTS_ERRBIT_CTX_LEN); tokens in blocks with an invalid id are left out
  * (TTS_ERRBIT_BLOCK_ID), and a row left without tokens gets zeros.
  * TTS_ERRBIT_TIMEOUT: a bounded wait ran out, the outputs are undefined.
- * B * ceil(q_len * Hq / 64) streams' worth of row groups times their 64-token
- * tiles must stay below 2^30 (TTS_ERR_UNSUPPORTED). */
+ * B * q_len must not exceed 2^20, and B * ceil(q_len * Hq / 64) streams' worth
+ * of row groups times their 64-token tiles must stay below 2^30
+ * (TTS_ERR_UNSUPPORTED; the workspace query gives 0 for the former). */
 int tts_latent_decode_attn(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                            const int32_t *d_ctx_lens, int32_t max_ctx_len, int32_t B, int32_t q_len,
                            int32_t num_q_heads, int32_t nope_dim, int32_t v_dim, float scale, int32_t causal,
@@ -346,7 +347,7 @@ size_t tts_latent_prefill_attn_workspace_size(int32_t B, int32_t num_rows, int32
  * its rows that lie in [0, num_rows) (TTS_ERRBIT_CTX_LEN); tokens in blocks
  * with an invalid id are left out (TTS_ERRBIT_BLOCK_ID), and a row left
  * without tokens gets zeros.  TTS_ERRBIT_TIMEOUT as tts_latent_decode_attn.
- * num_q_heads <= 1024; other limits as tts_latent_decode_attn. */
+ * num_q_heads <= 1024, B <= 2^20; other limits as tts_latent_decode_attn. */
 int tts_latent_prefill_attn(const tts_latent_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                             const int32_t *d_ctx_lens, int32_t max_total_ctx, int32_t B, const int32_t *d_row_start,
                             int32_t num_rows, int32_t num_q_heads, int32_t nope_dim, int32_t v_dim, float scale,

@@ -110,6 +110,22 @@ def test_a_head_whose_weights_are_nan(bd, form, which):
         check(out[:, h], want[:, h], tol[:, h], f"head {h}")
 
 
+@pytest.mark.parametrize("what", [NAN, math.inf])
+@pytest.mark.parametrize("form", ["decode", "prefill"])
+@pytest.mark.parametrize("which", ["q_nope", "q_rope"])
+def test_queries_that_are_not_finite(bd, what, form, which):
+    """A query of one row and head reaches that row's output of that head."""
+    n = 5 if form == "decode" else 150
+    s = ref.make([n, n], [40, 3], 3, 128, 64, 64, 42)
+    want, tol = ref.attend_all(s, True, form == "decode")
+    s[which][n + 2, 1, 9] = what
+    d = up(s)
+    out = (run_decode(bd, s, d, n, True) if form == "decode" else run_prefill(bd, s, d)).view(2 * n, 3, 64).cpu()
+    assert not_finite(out[n + 2, 1]).all()
+    out[n + 2, 1] = want[n + 2, 1].to(torch.bfloat16)
+    check(out, want, tol, form)
+
+
 # --------------------------------------------------------- values far from one
 
 @pytest.mark.parametrize("form", ["decode", "prefill"])
