@@ -887,19 +887,17 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
 #pragma unroll
                         for (int i = 0; i < kTile; ++i)
                             if (i >= left || !((mask >> (i / TTS_BLOCK_TOKENS)) & 1)) x[i] = 0xFF800000u;  // -inf
-                        if (scaled) {
-                            add_exps(x, 1.0f / a.scale_log2, exps + j * kTile);
-                        }
+                        if (scaled) add_exps(x, 1.0f / a.scale_log2, exps + j * kTile);
                     }
                     mask = next_mask;
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
                     const float t = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                    if (__any_sync(kFull, t > m + kSlack)) {
-                        // (S(j) complete means that O(j - 1) is too)
-                        // (the sum may be far larger than 2^m's own weight, where
-                        // values are scaled: the factor in two steps)
+                    if (__any_sync(kFull, t > m + kSlack || scaled)) {
+                        // (S(j) complete means that O(j - 1) is too; where values
+                        // are scaled the sum may be far larger than 2^m's own weight:
+                        // the factor in two steps)
                         const float now = fmaxf(m, t), root = hw_ex2(0.5f * (m - now)), f = root * root;
                         m = now;
                         l = l * root * root;
@@ -912,8 +910,8 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
                                 tmem_st16(to + c, o);
                             }
+                        if (scaled) l += sum_unscaled(x, a.scale_log2, m, exps + j * kTile);
                     }
-                    if (scaled) l += sum_unscaled(x, a.scale_log2, m, exps + j * kTile);
                     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                     for (int c = 0; c < kTile; c += 64) {
@@ -928,7 +926,7 @@ latent_prefill_kernel(const __grid_constant__ CUtensorMap map_qn, const __grid_c
                         }
                         tmem_st32(ts + c / 2, p);
                     }
-                    if (!scaled) l += sum[0] + sum[1];
+                    l += scaled ? 0.0f : sum[0] + sum[1];
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
