@@ -7,8 +7,8 @@
 // latent_dim / 8 copies.  Pure data movement: the bytes are each row's 2
 // (latent_dim + 64) + 2 x 64 Hq, read once and written once.
 // A CTA takes one row, or four where there are more rows than CTAs fit at once
-// (a CTA's time is latency): 8409 rows of 16 heads take 10.9 us, 4.9 TB/s (one
-// by one 14.6 us), 64 rows 2.6 us.
+// (a CTA's time is latency): 12 prompts of 8409 rows in all, 16 heads, take 11.9
+// us, 4.5 TB/s, 64 rows 2.5 us.
 // The rows' first items are loaded before their positions are known (they do
 // not depend on them); meanwhile a warp per row finds the stream and the block
 // and computes the 32 angles, shared through shared memory.
@@ -25,11 +25,11 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kAhead = 2;  // items per thread and row loaded before the position is known
-// One-row CTAs that run at once (38 registers a thread: twelve an SM).  Up to so
-// many rows the one-row kernel is ahead (1520 rows 3.85 us against 4.2), beyond
-// them its second wave is not (2000 rows 5.15 against 4.45, 2432 rows 5.35 against
-// 4.5; 16 heads, latent 512).
-constexpr int kAtOnce = 152 * 12;
+// One-row CTAs that run at once (42 registers a thread: ten an SM).  Up to so
+// many rows the one-row kernel is ahead (1520 rows 3.7 us against 4.2), beyond
+// them its second wave is not (1600 rows 4.6 against 4.2, 2432 rows 5.2 against
+// 4.55; 16 heads, latent 512).
+constexpr int kAtOnce = 152 * 10;
 constexpr int kHalf = kLatentRope / 2;
 
 // Rotary frequencies base^(-2i/64) in turns a token, scaled by 2^64: a
@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
             lo = reinterpret_cast<const uint4 *>(x)[it & 3];
             hi = reinterpret_cast<const uint4 *>(x)[(it & 3) + 4];
         } else {
-            lo = reinterpret_cast<const uint4 *>(a.c_new + static_cast<size_t>(row) * a.L)[it - rope_items];
+            lo = __ldcs(reinterpret_cast<const uint4 *>(a.c_new + static_cast<size_t>(row) * a.L) + it - rope_items);
         }
     };
     uint4 lo[kRows][kAhead], hi[kRows][kAhead];
