@@ -25,7 +25,7 @@
 // turn loads and MMAs into a chain of 1.6 us a tile; ending a segment costs
 // another 2 to 3 us (98 KB of partial sums).  Measured, 16 heads, latent 512:
 // 256 streams of 32 to 4096 tokens 52 us (4.8 TB/s), 64 streams of 50 to 1500
-// 15 us, 64 x 5 causal rows over 256 to 2048 tokens 40 us, one stream of 65533
+// 15 us, 64 x 5 causal rows over 256 to 2048 tokens 41 us, one stream of 65533
 // tokens 16 us, one of 17 tokens 6.7 us.
 #include <cuda_bf16.h>
 

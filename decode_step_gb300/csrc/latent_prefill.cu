@@ -9,15 +9,15 @@
 //  1. latent_expand_kernel: checks the streams, lays out their tokens in the
 //     workspace (each stream from a 128-token boundary) and their query tiles,
 //     and multiplies keys and values out: a tcgen05 GEMM whose token rows are
-//     fetched through the block table.  36 us for 8891 tokens (16 heads, 512 ->
-//     128 + 128: 1.0 PFLOP/s, 73 MB written), 10 us for 333, latency.
+//     fetched through the block table.  37 us for 8891 tokens (16 heads, 512 ->
+//     128 + 128: 1.0 PFLOP/s, 73 MB written), 9 us for 333, latency.
 //  2. latent_prefill_kernel: attention of 256 rows of one head per CTA (two
 //     128-row tiles that take turns on the tensor core: while one's weights
 //     are computed, the other's products run).  S and O are in tensor memory;
 //     the weights go back into S's columns (as f16) and are the A operand of
 //     the second product.  Bound: the tensor core (640 flop a row, token and
-//     head); 247 us for 8191 rows after 700 tokens, 1.63 PFLOP/s, 86% of the
-//     rate that a large bf16 matrix product reaches.
+//     head); 251 us for 8191 rows after 700 tokens, 1.60 PFLOP/s, 85% of the
+//     measured rate of a large bf16 matrix product.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -342,9 +342,8 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap map_pool, const __grid_
         tiles += sh.tiles[w];
     }
     // Units of 256 features, or of 128 where those still make one round of the
-    // CTAs (one prompt of 333 rows, the whole call: 17.4 against 18.2 us; 16
-    // prompts whose 96 units of 256 make two rounds and 192 of 128 three: 30.8
-    // against 30.1)
+    // CTAs (one prompt of 333 rows, the whole call: 17.6 against 19.4 us; in
+    // three rounds of 128 or two of 256, 16 prompts take 30.9 and 30.8)
     const int ctas = gridDim.x, me = blockIdx.x;
     auto tiles_of = [](int features, int each) { return (features + each - 1) / each; };
     auto units_of = [&](int each) { return tiles * (tiles_of(a.Hq * a.nope, each) + tiles_of(a.Hq * a.v, each)); };
@@ -644,8 +643,9 @@ constexpr int kSlots = 8;           // ring slots of [128 tokens][64 values]: 1.
 constexpr int kTiles = 4;           // barriers for the keys, and the values, of as many tiles
 constexpr int kAttnThreads = 384;   // two softmax warpgroups; producer, MMA issuer and two spare warps
 // A softmax thread holds a row's 128 scores: the registers that the others do not
-// need go to it (8191 rows after 700 tokens: 262 us without, 255 with).  The
-// block has to start with kStartRegs a thread; launch_prefill looks.
+// need go to it (8191 rows after 700 tokens: 260 us without, 253 with; 16 prompts,
+// the whole call, 32.2 and 30.9).  The block has to start with kStartRegs a
+// thread; launch_prefill looks.
 constexpr int kSoftmaxRegs = 224, kOtherRegs = 56, kStartRegs = 168;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kAttnThreads * kStartRegs);
 
