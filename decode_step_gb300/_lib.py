@@ -15,7 +15,7 @@ TTS_OK = 0
 TTS_F32, TTS_BF16, TTS_FP8_E4M3 = 0, 1, 2
 TTS_ARGMAX, TTS_GUMBEL = 0, 1
 TTS_VERIFY_BONUS = 1
-ERRBIT_BLOCK_ID, ERRBIT_CTX_LEN, ERRBIT_TOKEN, ERRBIT_TIMEOUT = 1, 2, 4, 8
+ERRBIT_BLOCK_ID, ERRBIT_CTX_LEN, ERRBIT_TOKEN, ERRBIT_TIMEOUT, ERRBIT_STREAM = 1, 2, 4, 8, 16
 LAUNCH_PROGRAMMATIC = 1
 TEST_STALL_NONE, TEST_STALL_ATTN_RING, TEST_STALL_PREDICTOR_GRID = 0, 1, 2
 TEST_STALL_LATENT_DECODE, TEST_STALL_LATENT_PREFILL = 4, 5
@@ -66,17 +66,31 @@ _SIGNATURES = {
     "tts_block_pool_create": (ctypes.c_int, [_i32, ctypes.POINTER(_vp)]),
     "tts_block_pool_alloc": (ctypes.c_int, [_vp, _i32, _vp]),
     "tts_block_pool_free": (ctypes.c_int, [_vp, _vp, _i32]),
+    "tts_block_pool_share": (ctypes.c_int, [_vp, _vp, _i32]),
+    "tts_block_pool_owners": (_i32, [_vp, _i32]),
+    "tts_block_pool_compact": (_i32, [_vp, _vp]),
     "tts_block_pool_num_free": (_i32, [_vp]),
     "tts_block_pool_destroy": (None, [_vp]),
     "tts_kv_append": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _i32,
                                      _vp, _vp, _vp, _vp]),
     "tts_kv_append_rope": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _i32, _i32,
                                           _f32, _vp, _vp, _vp, _vp, _vp]),
+    "tts_kv_append_packed": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _vp, _i32, _i32, _f32,
+                                            _vp, _vp, _vp, _vp, _vp, _vp]),
+    "tts_kv_copy_blocks": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _vp, _i32, _vp, _vp]),
+    "tts_kv_fork": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "tts_kv_compact": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _vp, _i32, _i32, _vp, _vp]),
     "tts_decode_attn_workspace_size": (_sz, [_i32] * 6),
     "tts_decode_attn": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _i32,
                                        _i32, _i32, _f32, _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "tts_decode_attn_noalloc": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32,
                                                _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp]),
+    "tts_window_decode_attn": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _i32, _i32, _i32, _f32,
+                                              _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "tts_latent_copy_blocks": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _vp, _i32, _vp, _vp]),
+    "tts_latent_fork": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp,
+                                       _vp]),
+    "tts_latent_compact": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _vp, _i32, _i32, _vp, _vp]),
     "tts_latent_append": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _i32, _vp, _i32, _vp, _i32, _i32,
                                          _f32, _vp, _vp, _vp, _vp, _vp, _vp]),
     "tts_latent_decode_attn_workspace_size": (_sz, [_i32] * 7),

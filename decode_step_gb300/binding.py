@@ -101,9 +101,12 @@ class KVCache:
 
 
 class BlockPool:
-    """Host free list of KV block ids (tts_block_pool_*)."""
+    """Host free list of KV block ids (tts_block_pool_*); a block that streams
+    share has several owners."""
 
     def __init__(self, num_blocks: int):
+        self._h = None
+        self.num_blocks = num_blocks
         h = ctypes.c_void_p()
         check("tts_block_pool_create", lib().tts_block_pool_create(num_blocks, ctypes.byref(h)))
         self._h = h
@@ -116,6 +119,26 @@ class BlockPool:
     def free(self, ids) -> None:
         arr = (ctypes.c_int32 * max(len(ids), 1))(*ids)
         check("tts_block_pool_free", lib().tts_block_pool_free(self._h, arr, len(ids)))
+
+    def share(self, ids) -> None:
+        """One owner more for each block."""
+        arr = (ctypes.c_int32 * max(len(ids), 1))(*ids)
+        check("tts_block_pool_share", lib().tts_block_pool_share(self._h, arr, len(ids)))
+
+    def owners(self, block: int) -> int:
+        n = lib().tts_block_pool_owners(self._h, block)
+        if n < 0:
+            check("tts_block_pool_owners", n)
+        return n
+
+    def compact(self) -> list[int]:
+        """Moves the blocks in use to the lowest ids; every block's new id (the
+        map of tts_kv_compact)."""
+        arr = (ctypes.c_int32 * self.num_blocks)()
+        n = lib().tts_block_pool_compact(self._h, arr)
+        if n < 0:
+            check("tts_block_pool_compact", n)
+        return list(arr)
 
     @property
     def num_free(self) -> int:
@@ -162,6 +185,77 @@ def tts_kv_append_rope(cache: KVCache, block_table, ctx_before, q, k_new, v_new,
     check("tts_kv_append_rope", lib().tts_kv_append_rope(*args))
 
 
+def _cache_on(cache, device: int):
+    """The descriptor of a KV cache for a call on `device`, the current one."""
+    if isinstance(cache, LatentCache):
+        return cache.on(device)
+    for pool in (cache.k_pool, cache.v_pool):
+        if pool is not None and pool.get_device() != device:
+            raise ValueError(f"the cache is on {pool.device}, the current device is cuda:{device}")
+    return ctypes.byref(cache.desc)
+
+
+def tts_kv_append_packed(cache: KVCache, block_table, ctx_before, row_start, k_new, v_new, q=None, q_out=None,
+                         rope_base=0.0, err=None, stream=None):
+    """Appends the packed rows k_new, v_new [T][Hkv][head_dim] of streams of
+    different lengths (row_start int32 [B + 1]); with rope_base != 0, k_new is
+    rotated on the way and q [T][Hq][head_dim] into q_out (default: in place)."""
+    B, max_blocks = block_table.shape
+    T = k_new.shape[0]
+    if (q is None) != (rope_base == 0.0):
+        raise ValueError("q goes with rope_base != 0 (nothing else is done with it)")
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    i32, dev = torch.int32, torch.cuda.current_device()
+    Hq = 0 if q is None else q.shape[1]
+    shape = (T, cache.num_kv_heads, cache.head_dim)
+    qp = None if q is None else _on(q, "q", cache.dtype, (T, Hq, cache.head_dim), dev)
+    check("tts_kv_append_packed", lib().tts_kv_append_packed(
+        _cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_before, "ctx_before", i32, (B,), dev), B, _on(row_start, "row_start", i32, (B + 1,), dev), T, Hq,
+        float(rope_base), qp, qp if q_out is None else _on(q_out, "q_out", cache.dtype, (T, Hq, cache.head_dim), dev),
+        _on(k_new, "k_new", cache.dtype, shape, dev), _on(v_new, "v_new", cache.dtype, shape, dev),
+        None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
+
+
+def _pages(cache, call: str):
+    """The library's function of a page move for this kind of cache, and its name."""
+    name = ("tts_latent_" if isinstance(cache, LatentCache) else "tts_kv_") + call
+    return getattr(lib(), name), name
+
+
+def tts_kv_copy_blocks(cache, src, dst, err=None, stream=None):
+    """Block dst[i] of a KVCache or LatentCache becomes block src[i] (int32 [n])."""
+    n, i32, dev = src.shape[0], torch.int32, torch.cuda.current_device()
+    fn, name = _pages(cache, "copy_blocks")
+    check(name, fn(_cache_on(cache, dev), _on(src, "src", i32, (n,), dev), _on(dst, "dst", i32, (n,), dev), n,
+                   None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
+
+
+def tts_kv_fork(cache, block_table, ctx_lens, parent, child, new_block, err=None, stream=None):
+    """Streams child[i] (rows of block_table and ctx_lens, which are updated)
+    become continuations of parent[i]: full blocks shared, the last one copied
+    to new_block[i] where it is partly filled.  A KVCache or LatentCache."""
+    B, max_blocks = block_table.shape
+    n, i32, dev = parent.shape[0], torch.int32, torch.cuda.current_device()
+    fn, name = _pages(cache, "fork")
+    check(name, fn(_cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+                   _on(ctx_lens, "ctx_lens", i32, (B,), dev), B, _on(parent, "parent", i32, (n,), dev),
+                   _on(child, "child", i32, (n,), dev), _on(new_block, "new_block", i32, (n,), dev), n,
+                   None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
+
+
+def tts_kv_compact(cache, block_map, block_table, err=None, stream=None):
+    """Moves block i of a KVCache or LatentCache to block_map[i] (int32
+    [num_blocks]; BlockPool.compact gives one) and block_table's entries with it."""
+    B, max_blocks = block_table.shape
+    i32, dev = torch.int32, torch.cuda.current_device()
+    fn, name = _pages(cache, "compact")
+    check(name, fn(_cache_on(cache, dev), _on(block_map, "block_map", i32, (cache.num_blocks,), dev),
+                   _on(block_table, "block_table", i32, None, dev), max_blocks, B,
+                   None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
+
+
 def tts_decode_attn_workspace_size(B, q_len, num_q_heads, num_kv_heads, head_dim, max_ctx_len) -> int:
     return int(lib().tts_decode_attn_workspace_size(B, q_len, num_q_heads, num_kv_heads, head_dim,
                                                    max_ctx_len))
@@ -178,6 +272,22 @@ def tts_decode_attn(cache: KVCache, block_table, ctx_lens, max_ctx_len, q, out, 
             ws.numel() * ws.element_size(), None if err is None else _dev(err, "err", torch.int32),
             _stream(stream))
     check("tts_decode_attn", lib().tts_decode_attn(*args))
+
+
+def tts_window_decode_attn(cache: KVCache, block_table, ctx_lens, max_ctx_len, q, out, ws, scale, window, sinks=0,
+                           causal=False, err=None, stream=None):
+    """tts_decode_attn over the last `window` tokens of each row's and the first
+    `sinks`; the workspace is tts_decode_attn's."""
+    B, max_blocks = block_table.shape
+    _, q_len, Hq, D = q.shape
+    i32, dev = torch.int32, torch.cuda.current_device()
+    shape = (B, q_len, Hq, cache.head_dim)
+    check("tts_window_decode_attn", lib().tts_window_decode_attn(
+        _cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_lens, "ctx_lens", i32, (B,), dev), int(max_ctx_len), B, q_len, Hq, float(scale), int(bool(causal)),
+        int(window), int(sinks), _on(q, "q", cache.dtype, shape, dev), _on(out, "out", cache.dtype, shape, dev),
+        _on(ws, "ws", None, None, dev), ws.nbytes, None if err is None else _on(err, "err", i32, None, dev),
+        _raw_stream(stream, dev)))
 
 
 def tts_decode_attn_noalloc(cache: KVCache, block_table, ctx_lens, max_ctx_len, q, out, scale,

@@ -34,6 +34,12 @@
 // p, p + 2, ...; dot products are reduced across the 16 chunk lanes by
 // recursive halving, leaving every lane the full scores of one token for half
 // of the query rows.
+//
+// Sliding window (kWindow; tts_window_decode_attn): rows see the last `window`
+// tokens and the first `sinks` ones, and a stream's tiles are the blocks that
+// hold a token that some row sees, so that the work follows the window, not the
+// context.  Nothing else of the schedule changes; without a window the kernels
+// are compiled as they were.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -79,7 +85,24 @@ struct AttnArgs {
     int32_t *err;
     long long wait_limit;  // SM clock cycles per bounded wait
     int stall;             // test support: first ring stage expects 16 bytes that never come
+    int window, sinks;     // kWindow only
 };
+
+// The blocks of a stream of L tokens that some row sees (kWindow): the first
+// `head` and, where `skip` more are passed over, those behind them.
+struct Seen {
+    int blocks, skip;
+};
+__device__ __forceinline__ int head_blocks(const AttnArgs &a) { return (a.sinks + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS; }
+template <bool kWindow>
+__device__ __forceinline__ Seen seen_blocks(const AttnArgs &a, int L) {
+    const int all = (L + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS;
+    if constexpr (!kWindow) return {all, 0};
+    // the first token of the first row's window
+    const int low = max(0, (a.causal ? L - a.q_len + 1 : L) - a.window);
+    const int skip = max(0, low / TTS_BLOCK_TOKENS - head_blocks(a));
+    return {all - skip, skip};
+}
 
 // The work partition: Wtot warps share the flat list of T tiles in order,
 // the first rem = T mod Wtot warps taking q + 1 tiles and the others q = T /
@@ -102,7 +125,7 @@ __device__ __forceinline__ int warp_of_tile(const Part &p, int t) {
 // Context lengths -> per-stream tile prefix (x Hkv, stream-major) in shared
 // memory; invalid streams get no tiles, zero outputs (CTA 0) and an error bit.
 // Called by every thread of the CTA.
-template <typename T, int D, int WARPS>
+template <typename T, int D, int WARPS, bool kWindow>
 __device__ void scan_streams(const AttnArgs &a, int *prefix, int *ctxs, int *scan) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cap = min(a.max_ctx, a.max_blocks * TTS_BLOCK_TOKENS);
@@ -113,7 +136,7 @@ __device__ void scan_streams(const AttnArgs &a, int *prefix, int *ctxs, int *sca
         const int L = __ldg(a.ctx_lens + i);
         const bool ok = L >= a.q_len && L <= cap;
         ctxs[i] = ok ? L : 0;
-        local += ok ? (L + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS : 0;
+        local += ok ? seen_blocks<kWindow>(a, L).blocks : 0;
         if (!ok && blockIdx.x == 0) {
             flag_error(a.err, TTS_ERRBIT_CTX_LEN);
             T *o = static_cast<T *>(a.out) + static_cast<size_t>(i) * a.q_len * a.Hq * D;
@@ -135,16 +158,17 @@ __device__ void scan_streams(const AttnArgs &a, int *prefix, int *ctxs, int *sca
     }
     for (int i = i0; i < i1; ++i) {
         prefix[i] = run * a.Hkv;
-        run += ctxs[i] ? (ctxs[i] + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS : 0;
+        run += ctxs[i] ? seen_blocks<kWindow>(a, ctxs[i]).blocks : 0;
     }
     if (threadIdx.x == 0) prefix[a.B] = total * a.Hkv;
     __syncthreads();
 }
 
 // Tile t of the flat list -> (raw block id, segment = stream * Hkv + head,
-// block index in the stream); t must be < prefix[B].  The block id load is
-// left in flight (validated where it is used).
-__device__ __forceinline__ void tile_meta(const AttnArgs &a, const int *prefix, int t, int &id,
+// index among the segment's blocks); t must be < prefix[B].  The block id load
+// is left in flight (validated where it is used).
+template <bool kWindow>
+__device__ __forceinline__ void tile_meta(const AttnArgs &a, const int *prefix, const int *ctxs, int t, int &id,
                                           int &seg, int &blk) {
     int lo = 0, hi = a.B;  // prefix[lo] <= t < prefix[hi]
     while (hi - lo > 1) {
@@ -156,7 +180,10 @@ __device__ __forceinline__ void tile_meta(const AttnArgs &a, const int *prefix, 
     const int g = r / nb;
     blk = r - g * nb;
     seg = lo * a.Hkv + g;
-    id = __ldg(a.table + static_cast<size_t>(lo) * a.max_blocks + blk);
+    int at = blk;
+    if constexpr (kWindow)
+        if (blk >= head_blocks(a)) at += (ctxs[lo] + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS - nb;
+    id = __ldg(a.table + static_cast<size_t>(lo) * a.max_blocks + at);
 }
 
 // Output pointer of query row r (= j * group + hh) of segment (b, g).
@@ -301,7 +328,7 @@ struct SimtSmem {
     static size_t total(int B) { return prefix + 4 * (2 * size_t(B) + 1 + kWarps); }
 };
 
-template <int NR>
+template <int NR, bool kWindow>
 __global__ void __launch_bounds__(kWarps * 32, NR <= 4 ? 3 : 1)
 decode_attn_simt_kernel(const AttnArgs a) {
     using T = float;
@@ -318,7 +345,7 @@ decode_attn_simt_kernel(const AttnArgs a) {
     const int n_rows = a.group * a.q_len;
 
     pdl_allow_dependents();
-    scan_streams<T, D, kWarps>(a, prefix, ctxs, scan);
+    scan_streams<T, D, kWarps, kWindow>(a, prefix, ctxs, scan);
     const long long Ttot = prefix[a.B];
     const long long Wtot = active_workers(a.workers, Ttot, static_cast<long long>(a.B) * a.Hkv);
     const int wid = blockIdx.x * kWarps + warp;
@@ -344,7 +371,7 @@ decode_attn_simt_kernel(const AttnArgs a) {
         id = -1;
         seg = -1;
         blk = 0;
-        if (t < t1) tile_meta(a, prefix, t, id, seg, blk);
+        if (t < t1) tile_meta<kWindow>(a, prefix, ctxs, t, id, seg, blk);
     };
     load_meta(0, cur_id, cur_seg, cur_blk);
     if (n > 32) load_meta(1, nxt_id, nxt_seg, nxt_blk);
@@ -394,7 +421,7 @@ decode_attn_simt_kernel(const AttnArgs a) {
 
     const int p = lane >> 4, c = lane & 15;
     const int my_tok = p + 2 * ((lane >> 1) & 7);
-    int seg_id = -1, seg_b = 0, seg_g = 0, seg_L = 0, s0 = 0, s1 = 0;
+    int seg_id = -1, seg_b = 0, seg_g = 0, seg_L = 0, seg_skip = 0, s0 = 0, s1 = 0;
     int lim[HALF];
     float q[NR][EPC], m_run[HALF], l_run[HALF], o[NR][EPC];
 
@@ -446,6 +473,16 @@ decode_attn_simt_kernel(const AttnArgs a) {
         finish_split_segment<T, D>(a, seg_id, s0, s1, n_rows, pt, lane);
     };
 
+    // block of the stream that holds the segment's tile `blk`
+    auto block_at = [&](int blk) {
+        if constexpr (kWindow) return blk >= head_blocks(a) ? blk + seg_skip : blk;
+        return blk;
+    };
+    // whether a row whose tokens end at `limit` sees token t
+    auto sees = [&](int t, int limit) {
+        if constexpr (kWindow) return t < limit && (t < a.sinks || t >= limit - a.window);
+        return t < limit;
+    };
     bool timed_out = false;
     int waited = 0;
     for (int i = 0; i < n; ++i) {
@@ -475,7 +512,9 @@ decode_attn_simt_kernel(const AttnArgs a) {
             seg_b = t_seg / a.Hkv;
             seg_g = t_seg % a.Hkv;
             seg_L = ctxs[seg_b];
-            const int nb = (seg_L + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS;
+            const Seen seen = seen_blocks<kWindow>(a, seg_L);
+            const int nb = seen.blocks;
+            seg_skip = seen.skip;
             s0 = prefix[seg_b] + seg_g * nb;
             s1 = s0 + nb;
 #pragma unroll
@@ -501,7 +540,7 @@ decode_attn_simt_kernel(const AttnArgs a) {
             }
         }
         if (!timed_out && t_id >= 0 && t_id < a.num_blocks) {
-            const int base = t_blk * TTS_BLOCK_TOKENS;
+            const int base = block_at(t_blk) * TTS_BLOCK_TOKENS;
             float acc[8 * NR];
 #pragma unroll
             for (int jt = 0; jt < 8; ++jt) {
@@ -531,7 +570,7 @@ decode_attn_simt_kernel(const AttnArgs a) {
             float alpha[HALF], other[HALF];
 #pragma unroll
             for (int k = 0; k < HALF; ++k) {
-                const float s = tpos < lim[k] ? acc[k] : -INFINITY;
+                const float s = sees(tpos, lim[k]) ? acc[k] : -INFINITY;
                 float mx = s;
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
@@ -564,8 +603,14 @@ decode_attn_simt_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     const float w = pr[r];
+                    if constexpr (kWindow) {
+                        // (a token that the row does not see may hold anything)
 #pragma unroll
-                    for (int e = 0; e < EPC; ++e) o[r][e] = fmaf(w, vf[e], o[r][e]);
+                        for (int e = 0; e < EPC; ++e) o[r][e] = w == 0.0f ? o[r][e] : fmaf(w, vf[e], o[r][e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < EPC; ++e) o[r][e] = fmaf(w, vf[e], o[r][e]);
+                    }
                 }
             }
         }
@@ -716,7 +761,79 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
     return r;
 }
 
-template <bool kFp8, int kRing, int kCtas>
+// ---- a window's edges in a tile of values (kWindow)
+
+// Bit t: token base + t is seen by every row (of any, with `every` false).
+// `first`, `last`: the limits of the first and the last row.
+__device__ __forceinline__ uint32_t seen_mask(const AttnArgs &a, int base, int first, int last, bool every) {
+    auto below = [&](int t) {  // bits of the tokens before t
+        const int n = min(max(t - base, 0), TTS_BLOCK_TOKENS);
+        return (1u << n) - 1u;
+    };
+    const uint32_t limit = below(every ? first : last);
+    return limit & (below(a.sinks) | ~below((every ? last : first) - a.window));
+}
+
+// Address of value (token t, dimension d) in a tile: bf16 in swizzled boxes, or
+// an FP8 code.
+template <bool kFp8>
+__device__ __forceinline__ uint32_t value_at(int t, int d) {
+    if constexpr (kFp8) return 16 * d + 4 * ((t & 7) >> 1) + (t & 1) + 2 * (t >> 3);
+    return swz(0, t, d >> 3) + 2 * (d & 7);
+}
+// The value if it is not finite, else 0.
+template <bool kFp8>
+__device__ __forceinline__ float odd_value(const uint8_t *v, int t, int d) {
+    const uint8_t *p = v + value_at<kFp8>(t, d);
+    if constexpr (kFp8) return (*p & 0x7F) == 0x7F ? __uint_as_float(0x7FC00000u) : 0.0f;
+    const uint32_t w = *reinterpret_cast<const uint16_t *>(p);
+    return (w & 0x7F80u) == 0x7F80u ? __uint_as_float(w << 16) : 0.0f;
+}
+// Clears the tokens outside `any`; returns those of `any` outside `every` that
+// hold a value that is not finite.  A whole warp calls these.
+template <bool kFp8>
+__device__ __forceinline__ uint32_t clear_hidden(uint8_t *v, uint32_t any, uint32_t every, int lane) {
+    uint32_t bad = 0;
+    if constexpr (kFp8) {
+        for (int d = lane; d < 128; d += 32) {
+            for (int t = 0; t < TTS_BLOCK_TOKENS; ++t) {
+                uint8_t *p = v + value_at<true>(t, d);
+                if (!((any >> t) & 1)) *p = 0;
+                else if (!((every >> t) & 1) && (*p & 0x7F) == 0x7F) bad |= 1u << t;
+            }
+        }
+    } else {
+        for (int i = lane; i < TTS_BLOCK_TOKENS * 16; i += 32) {
+            const int t = i / 16;
+            if ((every >> t) & 1) continue;
+            uint4 *p = reinterpret_cast<uint4 *>(v + value_at<false>(t, i % 16 * 8));
+            if (!((any >> t) & 1)) {
+                *p = make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            const uint4 x = *p;
+            for (const uint32_t w : {x.x, x.y, x.z, x.w})
+                if ((w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u) bad |= 1u << t;
+        }
+    }
+    __syncwarp();
+    return __reduce_or_sync(kFull, bad);
+}
+// Clears the values that are not finite of the tokens in `bad`.
+template <bool kFp8>
+__device__ __noinline__ void clear_odd(uint8_t *v, uint32_t bad, int lane) {
+    for (uint32_t m = bad; m; m &= m - 1) {
+        const int t = __ffs(m) - 1;
+        for (int d = lane; d < 128; d += 32) {
+            if (odd_value<kFp8>(v, t, d) == 0.0f) continue;
+            uint8_t *p = v + value_at<kFp8>(t, d);
+            if constexpr (kFp8) *p = 0;
+            else *reinterpret_cast<uint16_t *>(p) = 0;
+        }
+    }
+}
+
+template <bool kFp8, int kRing, int kCtas, bool kWindow>
 __global__ void __launch_bounds__(kTcWarps * 32, kCtas)
 decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const AttnArgs a) {
@@ -737,7 +854,7 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     pdl_allow_dependents();
-    scan_streams<T, D, kTcWarps>(a, prefix, ctxs, scan);
+    scan_streams<T, D, kTcWarps, kWindow>(a, prefix, ctxs, scan);
     const long long Ttot = prefix[a.B];
     const long long Wtot = active_workers(a.workers, Ttot, static_cast<long long>(a.B) * a.Hkv);
     const int wid = blockIdx.x * kTcWarps + warp;
@@ -762,7 +879,7 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         id = -1;
         seg = -1;
         blk = 0;
-        if (t < t1) tile_meta(a, prefix, t, id, seg, blk);
+        if (t < t1) tile_meta<kWindow>(a, prefix, ctxs, t, id, seg, blk);
     };
     load_meta(0, cur_id, cur_seg, cur_blk);
     if (n > 32) load_meta(1, nxt_id, nxt_seg, nxt_blk);
@@ -822,7 +939,7 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     // ldmatrix row-address roles: matrix mi = lane / 8, row mr = lane % 8.
     const int mi = lane >> 3, mr = lane & 7;
 
-    int seg_id = -1, seg_b = 0, seg_g = 0, seg_L = 0, s0 = 0, s1 = 0;
+    int seg_id = -1, seg_b = 0, seg_g = 0, seg_L = 0, seg_skip = 0, s0 = 0, s1 = 0;
     int limA = 0, limB = 0;                 // visible-token limits of rows fg and fg + 8
     uint32_t qa[8][4];                      // Q A-fragments, 8 k-steps of 16 dims
     float mA = kNegBig, mB = kNegBig, lA = 0.0f, lB = 0.0f;
@@ -872,6 +989,16 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         finish_split_segment<T, D>(a, seg_id, s0, s1, n_rows, pt, lane);
     };
 
+    // block of the stream that holds the segment's tile `blk`
+    auto block_at = [&](int blk) {
+        if constexpr (kWindow) return blk >= head_blocks(a) ? blk + seg_skip : blk;
+        return blk;
+    };
+    // whether a row whose tokens end at `limit` sees token t
+    auto sees = [&](int t, int limit) {
+        if constexpr (kWindow) return t < limit && (t < a.sinks || t >= limit - a.window);
+        return t < limit;
+    };
     bool timed_out = false;
     int waited = 0;
     for (int i = 0; i < n; ++i) {
@@ -903,7 +1030,9 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             seg_b = t_seg / a.Hkv;
             seg_g = t_seg % a.Hkv;
             seg_L = ctxs[seg_b];
-            const int nb = (seg_L + TTS_BLOCK_TOKENS - 1) / TTS_BLOCK_TOKENS;
+            const Seen seen = seen_blocks<kWindow>(a, seg_L);
+            const int nb = seen.blocks;
+            seg_skip = seen.skip;
             s0 = prefix[seg_b] + seg_g * nb;
             s1 = s0 + nb;
             const int rA = fg, rB = fg + 8;
@@ -936,7 +1065,7 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 for (int e = 0; e < 4; ++e) o[nt][e] = 0.0f;
         }
         if (!timed_out && t_id >= 0 && t_id < a.num_blocks) {
-            const int base_tok = t_blk * TTS_BLOCK_TOKENS;
+            const int base_tok = block_at(t_blk) * TTS_BLOCK_TOKENS;
             // ---- S = Q K^T: 2 n-tiles of 8 tokens x 8 k-steps of 16 dims
             float s[2][4];
             // FP8: this lane's key and value scales (tokens 2t, 2t+1 | 2t+8, 2t+9)
@@ -991,8 +1120,8 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                     const int tok = base_tok + 8 * nt + 2 * ft + e;
                     float f = a.qscale;
                     if constexpr (kFp8) f *= (e == 0 ? ksc[nt].x : ksc[nt].y);
-                    xa[2 * nt + e] = tok < limA ? s[nt][e] * f : -INFINITY;
-                    xb[2 * nt + e] = tok < limB ? s[nt][2 + e] * f : -INFINITY;
+                    xa[2 * nt + e] = sees(tok, limA) ? s[nt][e] * f : -INFINITY;
+                    xb[2 * nt + e] = sees(tok, limB) ? s[nt][2 + e] * f : -INFINITY;
                 }
             }
             float ma = fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]));
@@ -1030,8 +1159,8 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 for (int e = 0; e < 4; ++e) {
                     const int tok = base_tok + 8 * (e >> 1) + 2 * ft + (e & 1);
                     const float vs = ((e & 1) ? vsc[e >> 1].y : vsc[e >> 1].x) * kFp8PFix;
-                    qa_[e] = tok < limA ? pa[e] * vs : 0.0f;
-                    qb_[e] = tok < limB ? pb[e] * vs : 0.0f;
+                    qa_[e] = sees(tok, limA) ? pa[e] * vs : 0.0f;
+                    qb_[e] = sees(tok, limB) ? pb[e] * vs : 0.0f;
                 }
                 pf[0] = pack_f16x2(qa_[0], qa_[1]);
                 pf[1] = pack_f16x2(qb_[0], qb_[1]);
@@ -1073,6 +1202,36 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
+            }
+            if constexpr (kWindow) {
+                // Tokens that not every row sees (the edges of the sinks and of
+                // the windows, and causal rows' last tokens): where none does
+                // the values are cleared, else those that are not finite go to
+                // the rows that see them here and are cleared for the product.
+                const int first = a.causal ? seg_L - a.q_len + 1 : seg_L;  // the first row's limit
+                const uint32_t any = seen_mask(a, base_tok, first, seg_L, false);
+                const uint32_t every = seen_mask(a, base_tok, first, seg_L, true);
+                if (every != 0xFFFFu) {
+                    const uint32_t bad = clear_hidden<kFp8>(smem + (vt - base), any, every, lane);
+                    for (uint32_t m = bad; m; m &= m - 1) {
+                        const int t = __ffs(m) - 1;
+                        const bool ina = sees(base_tok + t, limA), inb = sees(base_tok + t, limB);
+#pragma unroll
+                        for (int nt = 0; nt < 16; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float v = odd_value<kFp8>(smem + (vt - base), t, nt * 8 + 2 * ft + e);
+                                if (ina) o[nt][e] += v;
+                                if (inb) o[nt][2 + e] += v;
+                            }
+                    }
+                    if (bad) {
+                        __syncwarp();
+                        clear_odd<kFp8>(smem + (vt - base), bad, lane);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
             }
             // ---- O += P V: 8 pairs of n-tiles (16 dims each), k = 16 tokens
             if constexpr (kFp8) {
@@ -1139,10 +1298,10 @@ cudaLaunchAttribute pdl_attr() {
     return at;
 }
 
-template <int NR>
+template <int NR, bool kWindow>
 int launch_simt_nr(const AttnArgs &a, int ctas, LaunchOpts o) {
     const size_t smem = SimtSmem<NR>::total(a.B);
-    auto kern = decode_attn_simt_kernel<NR>;
+    auto kern = decode_attn_simt_kernel<NR, kWindow>;
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(smem))) return TTS_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, 1, 1);
@@ -1159,30 +1318,31 @@ int launch_simt_nr(const AttnArgs &a, int ctas, LaunchOpts o) {
     return TTS_OK;
 }
 
+template <bool kWindow>
 int launch_simt(const AttnArgs &a, int nr, int ctas, LaunchOpts o) {
     switch (nr) {
-        case 2: return launch_simt_nr<2>(a, ctas, o);
-        case 4: return launch_simt_nr<4>(a, ctas, o);
-        case 8: return launch_simt_nr<8>(a, ctas, o);
-        case 10: return launch_simt_nr<10>(a, ctas, o);
-        case 16: return launch_simt_nr<16>(a, ctas, o);
+        case 2: return launch_simt_nr<2, kWindow>(a, ctas, o);
+        case 4: return launch_simt_nr<4, kWindow>(a, ctas, o);
+        case 8: return launch_simt_nr<8, kWindow>(a, ctas, o);
+        case 10: return launch_simt_nr<10, kWindow>(a, ctas, o);
+        case 16: return launch_simt_nr<16, kWindow>(a, ctas, o);
         default: return TTS_ERR_UNSUPPORTED;
     }
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kWindow>
 int launch_tc(const AttnArgs &a, const CUtensorMap &kmap, const CUtensorMap &vmap, int ctas, LaunchOpts o) {
     static_assert(tc_max_stages(3) == 2 && tc_max_stages(2) == 3,
                   "instantiated: 3 CTAs x 1-2 stages (1-3 with FP8), 2 x 1-3");
     const int rows = a.group * a.q_len;
     const size_t smem = tc_smem(rows, a.B, a.stages, kFp8).total;
     const auto kern = tc_ctas_per_sm(rows) == 2
-                          ? (a.stages == 3   ? decode_attn_tc_kernel<kFp8, 3, 2>
-                             : a.stages == 2 ? decode_attn_tc_kernel<kFp8, 2, 2>
-                                             : decode_attn_tc_kernel<kFp8, 1, 2>)
-                          : (kFp8 && a.stages == 3 ? decode_attn_tc_kernel<kFp8, 3, 3>
-                             : a.stages == 2       ? decode_attn_tc_kernel<kFp8, 2, 3>
-                                                   : decode_attn_tc_kernel<kFp8, 1, 3>);
+                          ? (a.stages == 3   ? decode_attn_tc_kernel<kFp8, 3, 2, kWindow>
+                             : a.stages == 2 ? decode_attn_tc_kernel<kFp8, 2, 2, kWindow>
+                                             : decode_attn_tc_kernel<kFp8, 1, 2, kWindow>)
+                          : (kFp8 && a.stages == 3 ? decode_attn_tc_kernel<kFp8, 3, 3, kWindow>
+                             : a.stages == 2       ? decode_attn_tc_kernel<kFp8, 2, 3, kWindow>
+                                                   : decode_attn_tc_kernel<kFp8, 1, 3, kWindow>);
     if (!ensure_dynamic_smem(reinterpret_cast<const void *>(kern), static_cast<int>(smem)))
         return TTS_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -1252,7 +1412,7 @@ static_assert(sizeof(AttnLaunchState) <= sizeof(AttnLaunch::storage), "AttnLaunc
 int prepare_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                  const int32_t *d_ctx_lens, int32_t max_ctx_len, int32_t B, int32_t q_len,
                  int32_t num_q_heads, float scale, int32_t causal, const void *d_q, void *d_out,
-                 void *d_ws, size_t ws_bytes, int32_t *d_err, AttnLaunch *out) {
+                 void *d_ws, size_t ws_bytes, int32_t *d_err, AttnLaunch *out, int32_t window, int32_t sinks) {
     if (!cache || !d_block_table || !d_ctx_lens || !d_q || !d_out) return TTS_ERR_INVALID;
     if (!cache->k_pool || (!cache->v_pool && cache->dtype != TTS_FP8_E4M3) || cache->num_blocks < 1)
         return TTS_ERR_INVALID;
@@ -1310,6 +1470,9 @@ int prepare_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_
     if (a.stages < 1) return TTS_ERR_UNSUPPORTED;
     a.err = d_err;
     a.wait_limit = thread_opts().wait_limit;
+    // (no context passes 2^24 tokens)
+    a.window = window < (1 << 25) ? window : 1 << 25;
+    a.sinks = sinks < (1 << 24) ? sinks : 1 << 24;
     a.stall = thread_opts().stall == TTS_TEST_STALL_ATTN_RING && cache->dtype != TTS_F32;
     st->dtype = cache->dtype;
     st->rows = pl.rows;
@@ -1326,9 +1489,14 @@ int prepare_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_
 int launch_attn(const AttnLaunch &L, LaunchOpts o) {
     const AttnLaunchState *st = reinterpret_cast<const AttnLaunchState *>(L.storage);
     if (st->ctas == 0) return TTS_OK;  // empty batch
-    if (st->dtype == TTS_BF16) return launch_tc<false>(st->a, st->kmap, st->vmap, st->ctas, o);
-    if (st->dtype == TTS_FP8_E4M3) return launch_tc<true>(st->a, st->kmap, st->vmap, st->ctas, o);
-    return launch_simt(st->a, st->rows, st->ctas, o);
+    const bool w = st->a.window > 0;
+    if (st->dtype == TTS_BF16)
+        return w ? launch_tc<false, true>(st->a, st->kmap, st->vmap, st->ctas, o)
+                 : launch_tc<false, false>(st->a, st->kmap, st->vmap, st->ctas, o);
+    if (st->dtype == TTS_FP8_E4M3)
+        return w ? launch_tc<true, true>(st->a, st->kmap, st->vmap, st->ctas, o)
+                 : launch_tc<true, false>(st->a, st->kmap, st->vmap, st->ctas, o);
+    return w ? launch_simt<true>(st->a, st->rows, st->ctas, o) : launch_simt<false>(st->a, st->rows, st->ctas, o);
 }
 
 }  // namespace tts
@@ -1341,6 +1509,19 @@ extern "C" int tts_decode_attn(const tts_kv_cache *cache, const int32_t *d_block
     tts::AttnLaunch L;
     const int st = tts::prepare_attn(cache, d_block_table, max_blocks_per_seq, d_ctx_lens, max_ctx_len, B,
                                      q_len, num_q_heads, scale, causal, d_q, d_out, d_ws, ws_bytes, d_err, &L);
+    if (st != TTS_OK) return st;
+    return tts::launch_attn(L, {static_cast<cudaStream_t>(stream), tts::thread_pdl()});
+}
+
+extern "C" int tts_window_decode_attn(const tts_kv_cache *cache, const int32_t *d_block_table,
+                                      int32_t max_blocks_per_seq, const int32_t *d_ctx_lens, int32_t max_ctx_len,
+                                      int32_t B, int32_t q_len, int32_t num_q_heads, float scale, int32_t causal,
+                                      int32_t window, int32_t sinks, const void *d_q, void *d_out, void *d_ws,
+                                      size_t ws_bytes, int32_t *d_err, void *stream) {
+    if (window < 1 || sinks < 0) return TTS_ERR_INVALID;
+    tts::AttnLaunch L;
+    const int st = tts::prepare_attn(cache, d_block_table, max_blocks_per_seq, d_ctx_lens, max_ctx_len, B, q_len,
+                                     num_q_heads, scale, causal, d_q, d_out, d_ws, ws_bytes, d_err, &L, window, sinks);
     if (st != TTS_OK) return st;
     return tts::launch_attn(L, {static_cast<cudaStream_t>(stream), tts::thread_pdl()});
 }

@@ -17,6 +17,9 @@
 // chunks swizzled, values dimension-major in the layout's slot order, then
 // the scales.  The rotary append rotates the new token's query and key rows
 // by its position before these writes.
+//
+// Packed rows (kPacked): prompts of different lengths, one row a new token;
+// the CTA looks its row's stream up while its first words are on their way.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -29,9 +32,32 @@ namespace {
 
 constexpr int kVecsAhead = 4;  // 16-byte words per thread loaded before the position is known
 
+// The packed rows' streams (kPacked; else NULL and 0).
+struct PackedRows {
+    const int32_t *row_start;
+    int B;
+};
+
+// Stream and index among the stream's new tokens of the CTA's row; false: the
+// row is no stream's.  A whole warp calls it.
+template <bool kPacked>
+__device__ __forceinline__ bool locate(const PackedRows &packed, int q_len, int &b, int &j) {
+    if constexpr (!kPacked) {
+        b = blockIdx.x / q_len;
+        j = blockIdx.x % q_len;
+        return true;
+    } else {
+        b = stream_of_row(packed.row_start, packed.B, blockIdx.x, threadIdx.x & 31);
+        if (b < 0) return false;
+        j = blockIdx.x - packed.row_start[b];
+        return true;
+    }
+}
+
+template <bool kPacked>
 __global__ void __launch_bounds__(128)
 kv_append_kernel(const int32_t *__restrict__ table, int max_blocks,
-                 const int32_t *__restrict__ ctx_before, int q_len, int Hkv, int num_blocks,
+                 const int32_t *__restrict__ ctx_before, const PackedRows packed, int q_len, int Hkv, int num_blocks,
                  int row_vecs, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
                  uint4 *__restrict__ k_pool, uint4 *__restrict__ v_pool, int32_t *err, int wait_last) {
     // wait_last: the inputs are not written by the kernel before (they come
@@ -50,8 +76,8 @@ kv_append_kernel(const int32_t *__restrict__ table, int max_blocks,
         const int i = threadIdx.x + u * blockDim.x;
         if (i < 2 * per_tensor) ahead[u] = load(i);
     }
-    const int b = blockIdx.x / q_len;
-    const int j = blockIdx.x % q_len;
+    int b, j;
+    if (!locate<kPacked>(packed, q_len, b, j)) return;
     const int before = ctx_before[b];
     const int cap = max_blocks * TTS_BLOCK_TOKENS;
     if (before < 0 || before >= cap || j >= cap - before) {
@@ -127,8 +153,8 @@ constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kRowsAhead = 4;  // rows per warp loaded before the token's position is known
 
 // One CTA per (stream, new token) of bf16 rows with head_dim 128; one warp per
-// row.  Rows: with kRope the Hq query rows first (rotated, written back in
-// place as bf16), then the Hkv key rows (rotated with kRope), then the Hkv
+// row.  Rows: with kRope the Hq query rows first (rotated, written to q_out,
+// which may be q itself, as bf16), then the Hkv key rows (rotated with kRope), then the Hkv
 // value rows.  Key and value rows go to the cache: bf16 rows, or with kFp8
 // one quantisation block per row (scale = max|x| / 448, codes = E4M3(x /
 // scale), IEEE fp32 division, round to nearest even, saturating; an all-zero
@@ -138,10 +164,11 @@ constexpr int kRowsAhead = 4;  // rows per warp loaded before the token's positi
 // read (they do not depend on it); meanwhile threads 0..63 read the position
 // and the block, and with kRope each computes one angle's cos/sin, shared
 // through shared memory.
-template <bool kFp8, bool kRope>
+template <bool kFp8, bool kRope, bool kPacked>
 __global__ void __launch_bounds__(kRowThreads)
 kv_append_rows_kernel(const int32_t *__restrict__ table, int max_blocks, const int32_t *__restrict__ ctx_before,
-                      int q_len, int Hq, int Hkv, int num_blocks, const RopeFreqs freqs, __nv_bfloat16 *q,
+                      const PackedRows packed, int q_len, int Hq, int Hkv, int num_blocks, const RopeFreqs freqs,
+                      const __nv_bfloat16 *q, __nv_bfloat16 *q_out,
                       const __nv_bfloat16 *__restrict__ k_new, const __nv_bfloat16 *__restrict__ v_new,
                       uint8_t *__restrict__ k_pool, uint8_t *__restrict__ v_pool, int32_t *err) {
     __shared__ float2 cs[kFp8D / 2];
@@ -169,12 +196,14 @@ kv_append_rows_kernel(const int32_t *__restrict__ table, int max_blocks, const i
         }
     }
     if (threadIdx.x < kFp8D / 2) {
-        const int b = blockIdx.x / q_len;
-        const int j = blockIdx.x % q_len;
-        const int before = ctx_before[b];
+        int b = 0, j = 0;
+        const bool mine = locate<kPacked>(packed, q_len, b, j);
+        const int before = mine ? ctx_before[b] : 0;
         const int cap = max_blocks * TTS_BLOCK_TOKENS;
         int blk = -1, s = 0;
-        if (before < 0 || before >= cap || j >= cap - before) {
+        if (!mine) {
+            // the row is no stream's
+        } else if (before < 0 || before >= cap || j >= cap - before) {
             if (threadIdx.x == 0) flag_error(err, TTS_ERRBIT_CTX_LEN);
         } else {
             s = before + j;
@@ -213,7 +242,7 @@ kv_append_rows_kernel(const int32_t *__restrict__ table, int max_blocks, const i
         }
         const __nv_bfloat162 plo = __floats2bfloat162_rn(x[0], x[1]), phi = __floats2bfloat162_rn(x[2], x[3]);
         if (is_q) {
-            uint32_t *dst = reinterpret_cast<uint32_t *>(q + (static_cast<size_t>(blockIdx.x) * Hq + row) * kFp8D);
+            uint32_t *dst = reinterpret_cast<uint32_t *>(q_out + (static_cast<size_t>(blockIdx.x) * Hq + row) * kFp8D);
             dst[lane] = *reinterpret_cast<const uint32_t *>(&plo);
             dst[32 + lane] = *reinterpret_cast<const uint32_t *>(&phi);
             return;
@@ -285,7 +314,7 @@ int prepare_append(const tts_kv_cache *cache, const int32_t *d_block_table, int3
         if (!aligned16(cache->k_pool) || !aligned16(d_k_new) || !aligned16(d_v_new)) return TTS_ERR_INVALID;
         if (static_cast<long>(B) * q_len > 0x7FFFFFFFL) return TTS_ERR_INVALID;
         *out = AppendLaunch{cache, d_block_table, max_blocks_per_seq, d_ctx_before, B, q_len, d_k_new, d_v_new,
-                            d_err, false, 0, nullptr, {}, false};
+                            d_err, false, 0, nullptr, {}, false, nullptr, nullptr};
         return TTS_OK;
     }
     if (cache->dtype != TTS_F32 && cache->dtype != TTS_BF16) return TTS_ERR_UNSUPPORTED;
@@ -297,7 +326,7 @@ int prepare_append(const tts_kv_cache *cache, const int32_t *d_block_table, int3
         return TTS_ERR_INVALID;
     if (static_cast<long>(B) * q_len > 0x7FFFFFFFL) return TTS_ERR_INVALID;
     *out = AppendLaunch{cache, d_block_table, max_blocks_per_seq, d_ctx_before, B, q_len, d_k_new, d_v_new, d_err,
-                        false, 0, nullptr, {}, false};
+                        false, 0, nullptr, {}, false, nullptr, nullptr};
     return TTS_OK;
 }
 
@@ -318,7 +347,7 @@ int prepare_append_rope(const tts_kv_cache *cache, const int32_t *d_block_table,
     if (!aligned16(d_q)) return TTS_ERR_INVALID;
     out->rope = true;
     out->Hq = num_q_heads;
-    out->q = d_q;
+    out->q = out->q_out = d_q;
     for (int i = 0; i < kFp8D / 2; ++i) out->freqs.theta[i] = pow(static_cast<double>(rope_base), -2.0 * i / kFp8D);
     return TTS_OK;
 }
@@ -326,7 +355,9 @@ int prepare_append_rope(const tts_kv_cache *cache, const int32_t *d_block_table,
 int launch_append(const AppendLaunch &L, LaunchOpts o) {
     if (L.B == 0) return TTS_OK;
     cudaLaunchConfig_t cfg = {};
+    // (packed rows: B is their number, q_len 1, and the streams are apart)
     cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long>(L.B) * L.q_len), 1, 1);
+    const PackedRows packed{L.row_start, L.streams};
     cfg.blockDim = dim3(128, 1, 1);
     cfg.stream = o.stream;
     cudaLaunchAttribute attr[1];
@@ -338,11 +369,15 @@ int launch_append(const AppendLaunch &L, LaunchOpts o) {
         // bf16 rows of head_dim 128 (checked by the prepare functions)
         cfg.blockDim = dim3(kRowThreads, 1, 1);
         const bool fp8 = L.cache->dtype == TTS_FP8_E4M3;
-        auto kernel = L.rope ? (fp8 ? kv_append_rows_kernel<true, true> : kv_append_rows_kernel<false, true>)
-                             : kv_append_rows_kernel<true, false>;
-        if (cudaLaunchKernelEx(&cfg, kernel, L.table, L.max_blocks, L.ctx_before, L.q_len, L.Hq,
+        auto kernel = L.rope ? (fp8 ? kv_append_rows_kernel<true, true, false> : kv_append_rows_kernel<false, true, false>)
+                             : kv_append_rows_kernel<true, false, false>;
+        if (L.row_start)
+            kernel = L.rope ? (fp8 ? kv_append_rows_kernel<true, true, true> : kv_append_rows_kernel<false, true, true>)
+                            : kv_append_rows_kernel<true, false, true>;
+        if (cudaLaunchKernelEx(&cfg, kernel, L.table, L.max_blocks, L.ctx_before, packed, L.q_len, L.Hq,
                                static_cast<int>(L.cache->num_kv_heads), static_cast<int>(L.cache->num_blocks), L.freqs,
-                               static_cast<__nv_bfloat16 *>(L.q), static_cast<const __nv_bfloat16 *>(L.k_new),
+                               static_cast<const __nv_bfloat16 *>(L.q), static_cast<__nv_bfloat16 *>(L.q_out),
+                               static_cast<const __nv_bfloat16 *>(L.k_new),
                                static_cast<const __nv_bfloat16 *>(L.v_new), static_cast<uint8_t *>(L.cache->k_pool),
                                fp8 ? nullptr : static_cast<uint8_t *>(L.cache->v_pool), L.err) != cudaSuccess) {
             cudaGetLastError();
@@ -352,7 +387,8 @@ int launch_append(const AppendLaunch &L, LaunchOpts o) {
     }
     const int elem = L.cache->dtype == TTS_F32 ? 4 : 2;
     const int row_vecs = L.cache->head_dim * elem / 16;
-    if (cudaLaunchKernelEx(&cfg, kv_append_kernel, L.table, L.max_blocks, L.ctx_before, L.q_len,
+    if (cudaLaunchKernelEx(&cfg, L.row_start ? kv_append_kernel<true> : kv_append_kernel<false>, L.table, L.max_blocks,
+                           L.ctx_before, packed, L.q_len,
                            static_cast<int>(L.cache->num_kv_heads), static_cast<int>(L.cache->num_blocks),
                            row_vecs, static_cast<const uint4 *>(L.k_new), static_cast<const uint4 *>(L.v_new),
                            static_cast<uint4 *>(L.cache->k_pool), static_cast<uint4 *>(L.cache->v_pool),
@@ -385,5 +421,24 @@ extern "C" int tts_kv_append_rope(const tts_kv_cache *cache, const int32_t *d_bl
     const int st = tts::prepare_append_rope(cache, d_block_table, max_blocks_per_seq, d_ctx_before, B, q_len,
                                             num_q_heads, rope_base, d_q, d_k_new, d_v_new, d_err, &L);
     if (st != TTS_OK) return st;
+    return tts::launch_append(L, {static_cast<cudaStream_t>(stream), tts::thread_pdl()});
+}
+
+extern "C" int tts_kv_append_packed(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                                    const int32_t *d_ctx_before, int32_t B, const int32_t *d_row_start,
+                                    int32_t num_rows, int32_t num_q_heads, float rope_base, const void *d_q,
+                                    void *d_q_out, const void *d_k_new, const void *d_v_new, int32_t *d_err,
+                                    void *stream) {
+    if (!d_row_start || B < 0 || B > (1 << 20) || num_rows < 0) return TTS_ERR_INVALID;
+    const bool rope = rope_base != 0.0f;
+    if (rope && (!d_q_out || !tts::aligned16(d_q_out))) return TTS_ERR_INVALID;
+    tts::AppendLaunch L;
+    const int st = tts::prepare_append_rope(cache, d_block_table, max_blocks_per_seq, d_ctx_before, num_rows, 1,
+                                            num_q_heads, rope_base, const_cast<void *>(d_q), d_k_new, d_v_new, d_err, &L);
+    if (st != TTS_OK) return st;
+    if (B == 0) return TTS_OK;
+    L.q_out = d_q_out;
+    L.row_start = d_row_start;
+    L.streams = B;
     return tts::launch_append(L, {static_cast<cudaStream_t>(stream), tts::thread_pdl()});
 }

@@ -138,6 +138,36 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
+// ------------------------------------------------------------- packed rows
+
+// Number of a warp's first lanes with a true predicate.
+__device__ __forceinline__ int leading_true(bool pred) {
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, pred);
+    return m == 0xFFFFFFFFu ? 32 : __ffs(~m) - 1;
+}
+
+// Stream of packed row `row`: the b with row_start[b] <= row < row_start[b + 1],
+// or -1.  A whole warp calls it; each round probes 32 entries of the
+// non-decreasing array.  Any other array content gives -1 or a b that
+// satisfies the condition, never an access outside row_start[0..B].
+__device__ __forceinline__ int stream_of_row(const int32_t *row_start, int B, int row, int lane) {
+    int lo = 0, hi = B;  // streams 0..lo-1 end at or before `row`; the answer is in [lo, hi]
+    while (hi - lo > 32) {
+        const int step = (hi - lo + 31) / 32;
+        const int idx = lo + lane * step;
+        const int c = leading_true(idx < hi && row_start[idx + 1] <= row);
+        if (c == 0) {
+            hi = lo;
+        } else {
+            hi = min(hi, lo + c * step);
+            lo += (c - 1) * step + 1;
+        }
+    }
+    lo += leading_true(lo + lane < hi && row_start[lo + lane + 1] <= row);
+    if (lo >= B || row_start[lo] > row || row_start[lo + 1] <= row) return -1;
+    return lo;
+}
+
 // ------------------------------------------------------------------ Philox
 
 // Philox4x64-10 (Salmon et al., "Parallel Random Numbers: As Easy as 1, 2, 3",

@@ -18,14 +18,31 @@
 // gives them back when it finishes or is aborted ("Optimizing Streaming
 // Text-to-Speech Models for Sub-50 Millisecond Latency", section "Dynamic
 // Token-Level Batching"; "TTS Serving, in depth", section "Barge-in and
-// cancellation").  A LIFO stack of free ids plus an allocation bitmap that
+// cancellation").  A LIFO stack of free ids plus every block's number of
+// owners (streams that share a forked prompt own its blocks together), which
 // catches double frees and foreign ids.
 
 struct tts_block_pool {
     std::mutex mu;
-    std::vector<int32_t> free_ids;   // stack; back() is handed out next
-    std::vector<uint8_t> allocated;  // 1 while a block is out
+    std::vector<int32_t> free_ids;  // stack; back() is handed out next
+    std::vector<int32_t> owners;    // 0: free; negative only inside a call, to catch repeats
 };
+
+namespace {
+// Whether every id is allocated and none is repeated (pool locked).  Leaves
+// the owners of the ids negated if so, else as they were.
+bool mark_ids(tts_block_pool *pool, const int32_t *ids, int32_t n) {
+    const int32_t nb = static_cast<int32_t>(pool->owners.size());
+    for (int32_t i = 0; i < n; ++i) {
+        if (ids[i] < 0 || ids[i] >= nb || pool->owners[ids[i]] < 1) {
+            while (i-- > 0) pool->owners[ids[i]] = -pool->owners[ids[i]];
+            return false;
+        }
+        pool->owners[ids[i]] = -pool->owners[ids[i]];
+    }
+    return true;
+}
+}  // namespace
 
 extern "C" int tts_block_pool_create(int32_t num_blocks, tts_block_pool **out) {
     if (!out || num_blocks < 1) return TTS_ERR_INVALID;
@@ -35,7 +52,7 @@ extern "C" int tts_block_pool_create(int32_t num_blocks, tts_block_pool **out) {
     p->free_ids.resize(num_blocks);
     // Lowest ids on top of the stack, so a fresh pool hands out 0, 1, 2, ...
     for (int32_t i = 0; i < num_blocks; ++i) p->free_ids[i] = num_blocks - 1 - i;
-    p->allocated.assign(num_blocks, 0);
+    p->owners.assign(num_blocks, 0);
     *out = p;
     return TTS_OK;
 }
@@ -47,7 +64,7 @@ extern "C" int tts_block_pool_alloc(tts_block_pool *pool, int32_t n, int32_t *ho
     for (int32_t i = 0; i < n; ++i) {
         const int32_t id = pool->free_ids.back();
         pool->free_ids.pop_back();
-        pool->allocated[id] = 1;
+        pool->owners[id] = 1;
         host_ids_out[i] = id;
     }
     return TTS_OK;
@@ -56,23 +73,56 @@ extern "C" int tts_block_pool_alloc(tts_block_pool *pool, int32_t n, int32_t *ho
 extern "C" int tts_block_pool_free(tts_block_pool *pool, const int32_t *host_ids, int32_t n) {
     if (!pool || n < 0 || (n > 0 && !host_ids)) return TTS_ERR_INVALID;
     std::lock_guard<std::mutex> lock(pool->mu);
-    const int32_t nb = static_cast<int32_t>(pool->allocated.size());
-    // Validate everything first (all or nothing), marking with 2 to catch repeats.
-    int32_t bad = -1;
+    if (!mark_ids(pool, host_ids, n)) return TTS_ERR_INVALID;
     for (int32_t i = 0; i < n; ++i) {
-        const int32_t id = host_ids[i];
-        if (id < 0 || id >= nb || pool->allocated[id] != 1) { bad = i; break; }
-        pool->allocated[id] = 2;
-    }
-    if (bad >= 0) {
-        for (int32_t i = 0; i < bad; ++i) pool->allocated[host_ids[i]] = 1;
-        return TTS_ERR_INVALID;
-    }
-    for (int32_t i = 0; i < n; ++i) {
-        pool->allocated[host_ids[i]] = 0;
-        pool->free_ids.push_back(host_ids[i]);
+        int32_t &owners = pool->owners[host_ids[i]];
+        owners = -owners - 1;
+        // (free_ids was as large as the pool when it was made: no allocation)
+        if (owners == 0) pool->free_ids.push_back(host_ids[i]);
     }
     return TTS_OK;
+}
+
+extern "C" int tts_block_pool_share(tts_block_pool *pool, const int32_t *host_ids, int32_t n) {
+    if (!pool || n < 0 || (n > 0 && !host_ids)) return TTS_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(pool->mu);
+    if (!mark_ids(pool, host_ids, n)) return TTS_ERR_INVALID;
+    bool full = false;
+    for (int32_t i = 0; i < n; ++i) {
+        int32_t &owners = pool->owners[host_ids[i]];
+        owners = -owners;
+        full = full || owners == INT32_MAX;
+    }
+    if (full) return TTS_ERR_INVALID;
+    for (int32_t i = 0; i < n; ++i) ++pool->owners[host_ids[i]];
+    return TTS_OK;
+}
+
+extern "C" int32_t tts_block_pool_owners(const tts_block_pool *pool, int32_t id) {
+    if (!pool) return TTS_ERR_INVALID;
+    auto *p = const_cast<tts_block_pool *>(pool);
+    std::lock_guard<std::mutex> lock(p->mu);
+    if (id < 0 || static_cast<size_t>(id) >= p->owners.size()) return TTS_ERR_INVALID;
+    return p->owners[id];
+}
+
+extern "C" int32_t tts_block_pool_compact(tts_block_pool *pool, int32_t *host_map_out) {
+    if (!pool || !host_map_out) return TTS_ERR_INVALID;
+    std::lock_guard<std::mutex> lock(pool->mu);
+    const int32_t nb = static_cast<int32_t>(pool->owners.size());
+    const int32_t live = nb - static_cast<int32_t>(pool->free_ids.size());
+    int32_t to = 0, moves = 0;
+    for (int32_t id = 0; id < nb; ++id) {
+        host_map_out[id] = id;
+        if (id < live || pool->owners[id] == 0) continue;
+        while (pool->owners[to] != 0) ++to;  // (as many are free before `live` as are in use behind it)
+        host_map_out[id] = to;
+        pool->owners[to] = pool->owners[id];
+        pool->owners[id] = 0;
+        ++moves;
+    }
+    for (int32_t i = 0; i < nb - live; ++i) pool->free_ids[i] = nb - 1 - i;
+    return moves;
 }
 
 extern "C" int32_t tts_block_pool_num_free(const tts_block_pool *pool) {

@@ -98,7 +98,8 @@ struct AppendLaunch {
     int B, q_len;
     const void *k_new, *v_new;
     int32_t *err;
-    // rotary embedding (rope == false: none): q [B][q_len][Hq][128] rotated in place
+    // rotary embedding (rope == false: none): q [B][q_len][Hq][128], rotated in
+    // place or (packed rows) to q_out
     bool rope;
     int Hq;
     void *q;
@@ -107,6 +108,11 @@ struct AppendLaunch {
     // kernel before (they are read from pinned host memory), so the append
     // runs at once and waits for that kernel just before it ends
     bool wait_last;
+    void *q_out;
+    // packed rows (NULL: none): B is the number of rows and q_len 1 where
+    // `streams` streams have them
+    const int32_t *row_start;
+    int streams;
 };
 int prepare_append(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                    const int32_t *d_ctx_before, int32_t B, int32_t q_len, const void *d_k_new,
@@ -125,7 +131,8 @@ struct AttnLaunch {
 int prepare_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                  const int32_t *d_ctx_lens, int32_t max_ctx_len, int32_t B, int32_t q_len,
                  int32_t num_q_heads, float scale, int32_t causal, const void *d_q, void *d_out,
-                 void *d_ws, size_t ws_bytes, int32_t *d_err, AttnLaunch *out);
+                 void *d_ws, size_t ws_bytes, int32_t *d_err, AttnLaunch *out, int32_t window = 0,
+                 int32_t sinks = 0);  // window 0: none
 int launch_attn(const AttnLaunch &L, LaunchOpts o);
 
 struct HeadLaunch {

@@ -68,7 +68,8 @@ enum {
     TTS_ERRBIT_BLOCK_ID = 1,   /* block table entry outside [0, num_blocks) */
     TTS_ERRBIT_CTX_LEN = 2,    /* context length outside its valid range */
     TTS_ERRBIT_TOKEN = 4,      /* draft token outside [0, V) */
-    TTS_ERRBIT_TIMEOUT = 8     /* a bounded on-device wait ran out */
+    TTS_ERRBIT_TIMEOUT = 8,    /* a bounded on-device wait ran out */
+    TTS_ERRBIT_STREAM = 16     /* stream index outside [0, B) */
 };
 
 #define TTS_BLOCK_TOKENS 16
@@ -125,9 +126,29 @@ int tts_block_pool_create(int32_t num_blocks, tts_block_pool **out);
  * TTS_ERR_POOL_EXHAUSTED (and no change) when fewer than n are free. */
 int tts_block_pool_alloc(tts_block_pool *pool, int32_t n, int32_t *host_ids_out);
 
-/* Returns n blocks.  All or nothing: TTS_ERR_INVALID (and no change) if any id
- * is outside the pool, not currently allocated, or repeated. */
+/* Returns n blocks: each loses one owner (a block has one when it is handed
+ * out, and one more with every tts_block_pool_share) and is free once it has
+ * none.  All or nothing: TTS_ERR_INVALID (and no change) if any id is outside
+ * the pool, not currently allocated, or repeated. */
 int tts_block_pool_free(tts_block_pool *pool, const int32_t *host_ids, int32_t n);
+
+/* Gives n allocated blocks one owner more each: a stream that is forked from
+ * another (tts_kv_fork) shares its full blocks, and each stream frees them when
+ * it ends.  All or nothing, refused as tts_block_pool_free. */
+int tts_block_pool_share(tts_block_pool *pool, const int32_t *host_ids, int32_t n);
+
+/* Owners of a block: 0 if it is free, TTS_ERR_INVALID for a null pool or an id
+ * outside it.  A stream that is about to write into a block with more than one
+ * takes a copy first (tts_kv_copy_blocks). */
+int32_t tts_block_pool_owners(const tts_block_pool *pool, int32_t id);
+
+/* Closes the gaps of the pool: with n blocks in use, those with ids from n on
+ * take, in order, the lowest free ids, with their owners.  host_map_out
+ * [num_blocks] gets every block's new id (its own where it stays, and for free
+ * blocks): the map of tts_kv_compact, which moves their contents.  Afterwards
+ * the pool hands out n, n + 1, ... first.  Returns the number of blocks that
+ * move, or TTS_ERR_INVALID for a null argument. */
+int32_t tts_block_pool_compact(tts_block_pool *pool, int32_t *host_map_out);
 
 /* Number of free blocks, or TTS_ERR_INVALID for a null pool. */
 int32_t tts_block_pool_num_free(const tts_block_pool *pool);
@@ -174,6 +195,62 @@ int tts_kv_append_rope(const tts_kv_cache *cache, const int32_t *d_block_table, 
                        float rope_base, void *d_q, const void *d_k_new, const void *d_v_new, int32_t *d_err,
                        void *stream);
 
+/* Append of prompts, or pieces of them, of different lengths: rows are packed,
+ * and row r of stream b, d_row_start[b] <= r < d_row_start[b + 1] (int32
+ * [B + 1], non-decreasing, at most num_rows), is its new token j = r -
+ * d_row_start[b], at position d_ctx_before[b] + j.  Rows of no stream are left
+ * alone.  Otherwise as tts_kv_append (rope_base 0) or tts_kv_append_rope:
+ *  d_k_new, d_v_new  [num_rows][num_kv_heads][head_dim]
+ *  d_q, d_q_out      bf16 [num_rows][num_q_heads][128], the same buffer (in
+ *                    place) or disjoint ones; only read and written with
+ *                    rope_base != 0 (else num_q_heads is not looked at and both
+ *                    may be NULL)
+ * B <= 2^20. */
+int tts_kv_append_packed(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                         const int32_t *d_ctx_before, int32_t B, const int32_t *d_row_start, int32_t num_rows,
+                         int32_t num_q_heads, float rope_base, const void *d_q, void *d_q_out, const void *d_k_new,
+                         const void *d_v_new, int32_t *d_err, void *stream);
+
+/* ------------------------------------------------------------ page moves */
+
+/* Copies whole blocks, keys and values of every head: block d_dst[i] becomes
+ * block d_src[i], i < n (int32, device).  A stream that is about to write into
+ * a block that it shares copies it to one of its own first.  Blocks of d_dst
+ * are distinct and none is in d_src, else the blocks concerned have undefined
+ * contents.  A pair with an id outside the pool is skipped
+ * (TTS_ERRBIT_BLOCK_ID).  Any cache type. */
+int tts_kv_copy_blocks(const tts_kv_cache *cache, const int32_t *d_src, const int32_t *d_dst, int32_t n, int32_t *d_err,
+                       void *stream);
+
+/* Makes streams continuations of others: for i < n, with p = d_parent[i], c =
+ * d_child[i] and L = d_ctx_lens[p], row c of the table takes the first L / 16
+ * entries of row p (as they are, with -1 for blocks behind a window), and where
+ * L is no multiple of 16 the block with the last L % 16 tokens is copied to
+ * d_new_block[i], which becomes the next entry.  d_ctx_lens[c] becomes L.  The
+ * other entries of row c are left alone.
+ *  d_block_table  int32 [B][max_blocks_per_seq], in/out;  d_ctx_lens int32 [B], in/out
+ *  d_parent, d_child, d_new_block  int32 [n]
+ * Children are distinct, and no child is a parent in the same call.  A fork is
+ * skipped if p or c lies outside [0, B) or p = c (TTS_ERRBIT_STREAM), if L lies
+ * outside [0, 16 * max_blocks_per_seq] (TTS_ERRBIT_CTX_LEN), or if a block that
+ * is to be copied, or to be written, lies outside the pool
+ * (TTS_ERRBIT_BLOCK_ID). */
+int tts_kv_fork(const tts_kv_cache *cache, int32_t *d_block_table, int32_t max_blocks_per_seq, int32_t *d_ctx_lens,
+                int32_t B, const int32_t *d_parent, const int32_t *d_child, const int32_t *d_new_block, int32_t n,
+                int32_t *d_err, void *stream);
+
+/* Moves blocks and the table entries that name them: block i goes to
+ * d_map[i] (int32 [num_blocks]; d_map[i] = i: it stays), and every entry e of
+ * the tables within the pool becomes d_map[e].  A destination does not move
+ * itself (d_map[d_map[i]] = d_map[i]) and takes one block only (else it has
+ * undefined contents); a block whose destination is outside the pool or moves is
+ * not moved, nor are its entries changed (TTS_ERRBIT_BLOCK_ID).  The map of
+ * tts_block_pool_compact is of this form.  The contents of the old places
+ * remain.
+ *  d_block_table  int32 [B][max_blocks_per_seq], in/out (B 0: none) */
+int tts_kv_compact(const tts_kv_cache *cache, const int32_t *d_map, int32_t *d_block_table, int32_t max_blocks_per_seq,
+                   int32_t B, int32_t *d_err, void *stream);
+
 /* ------------------------------------------------------------- attention */
 
 /* Bytes of device workspace tts_decode_attn needs for these sizes (0 on bad
@@ -210,6 +287,20 @@ int tts_decode_attn(const tts_kv_cache *cache, const int32_t *d_block_table,
                     int32_t B, int32_t q_len, int32_t num_q_heads, float scale, int32_t causal,
                     const void *d_q, void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_err,
                     void *stream);
+
+/* tts_decode_attn with a sliding window and sinks: a row that tts_decode_attn
+ * gives the tokens t < limit sees of them t >= limit - window and t < sinks
+ * (the first tokens stay visible).  window >= 1, sinks >= 0; a window that no
+ * context passes gives tts_decode_attn's results.  Reads only the blocks that
+ * hold a token that some row of the stream sees: the other entries of the table
+ * may hold anything (blocks that went back to the pool).  Tokens that a row does
+ * not see do not reach it, whatever their keys and values are; a value that is
+ * not finite makes that dimension of the rows that see it so.
+ * Everything else, the workspace too, as tts_decode_attn. */
+int tts_window_decode_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                           const int32_t *d_ctx_lens, int32_t max_ctx_len, int32_t B, int32_t q_len,
+                           int32_t num_q_heads, float scale, int32_t causal, int32_t window, int32_t sinks,
+                           const void *d_q, void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream);
 
 /* Decode attention with no caller workspace and no allocation.
  * The pages have no counterpart for this entry point.  It is for callers that
@@ -258,6 +349,15 @@ typedef struct tts_latent_cache {
     int32_t dtype;          /* TTS_BF16 */
     void *pool;
 } tts_latent_cache;
+
+/* tts_kv_copy_blocks, tts_kv_fork and tts_kv_compact for a latent cache. */
+int tts_latent_copy_blocks(const tts_latent_cache *cache, const int32_t *d_src, const int32_t *d_dst, int32_t n,
+                           int32_t *d_err, void *stream);
+int tts_latent_fork(const tts_latent_cache *cache, int32_t *d_block_table, int32_t max_blocks_per_seq,
+                    int32_t *d_ctx_lens, int32_t B, const int32_t *d_parent, const int32_t *d_child,
+                    const int32_t *d_new_block, int32_t n, int32_t *d_err, void *stream);
+int tts_latent_compact(const tts_latent_cache *cache, const int32_t *d_map, int32_t *d_block_table,
+                       int32_t max_blocks_per_seq, int32_t B, int32_t *d_err, void *stream);
 
 /* Writes new tokens' rows into the latent pool, with the rotary embedding of
  * their key parts, and rotates the same tokens' query parts.
@@ -677,14 +777,15 @@ void tts_code_predictor_graph_destroy(tts_code_predictor_graph *graph);
 
 /* No counterpart on the pages: kernel-launch plumbing.  With
  * TTS_LAUNCH_PROGRAMMATIC set, the single-kernel calls this thread makes
- * afterwards (tts_kv_append, tts_kv_append_rope, tts_decode_attn,
- * tts_codebook_head_select, and the first kernel of tts_latent_append,
+ * afterwards (tts_kv_append, tts_kv_append_rope, tts_kv_append_packed,
+ * tts_decode_attn, tts_window_decode_attn, tts_codebook_head_select, the page
+ * moves, and the first kernel of tts_latent_append,
  * tts_latent_decode_attn and tts_latent_prefill_attn) launch their kernel as a
  * programmatic dependent of the previous kernel in the stream: it may start
  * while that kernel finishes (hiding the launch latency, as the kernels of
  * tts_decode_step do) and waits for its completion before touching anything
- * that kernel may write, except: tts_decode_attn reads d_ctx_lens and
- * d_block_table, tts_codebook_head_select reads d_W, and
+ * that kernel may write, except: tts_decode_attn and tts_window_decode_attn read
+ * d_ctx_lens and d_block_table, tts_codebook_head_select reads d_W, and
  * tts_latent_decode_attn reads d_w_uk, before that wait,
  * so the previous kernel must not write those.  The setting is per calling
  * thread.  Returns the previous flags. */
