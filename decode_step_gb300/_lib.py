@@ -18,7 +18,7 @@ TTS_VERIFY_BONUS = 1
 ERRBIT_BLOCK_ID, ERRBIT_CTX_LEN, ERRBIT_TOKEN, ERRBIT_TIMEOUT, ERRBIT_STREAM = 1, 2, 4, 8, 16
 LAUNCH_PROGRAMMATIC = 1
 TEST_STALL_NONE, TEST_STALL_ATTN_RING, TEST_STALL_PREDICTOR_GRID = 0, 1, 2
-TEST_STALL_LATENT_DECODE, TEST_STALL_LATENT_PREFILL = 4, 5
+TEST_STALL_LATENT_DECODE, TEST_STALL_LATENT_PREFILL, TEST_STALL_PROMPT = 4, 5, 6
 
 HEADER = Path(__file__).resolve().parents[1] / "include" / "tts_decode.h"
 
@@ -87,6 +87,9 @@ _SIGNATURES = {
                                                _i32, _i32, _i32, _f32, _i32, _vp, _vp, _vp, _vp]),
     "tts_window_decode_attn": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _i32, _i32, _i32, _f32,
                                               _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "tts_prompt_attn_workspace_size": (_sz, [_i32] * 5),
+    "tts_prompt_attn": (ctypes.c_int, [ctypes.POINTER(KVCacheDesc), _vp, _i32, _vp, _i32, _vp, _i32, _i32, _f32, _i32,
+                                       _i32, _vp, _vp, _vp, _sz, _vp, _vp]),
     "tts_latent_copy_blocks": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _vp, _i32, _vp, _vp]),
     "tts_latent_fork": (ctypes.c_int, [ctypes.POINTER(LatentCacheDesc), _vp, _i32, _vp, _i32, _vp, _vp, _vp, _i32, _vp,
                                        _vp]),

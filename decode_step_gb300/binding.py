@@ -290,6 +290,27 @@ def tts_window_decode_attn(cache: KVCache, block_table, ctx_lens, max_ctx_len, q
         _raw_stream(stream, dev)))
 
 
+def tts_prompt_attn_workspace_size(B, num_rows, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(lib().tts_prompt_attn_workspace_size(B, num_rows, num_q_heads, num_kv_heads, head_dim))
+
+
+def tts_prompt_attn(cache: KVCache, block_table, ctx_lens, row_start, q, out, ws, scale, window=0, sinks=0, err=None,
+                    stream=None):
+    """Causal attention of packed prompt rows q [T][Hq][head_dim] over their
+    streams' cached tokens (ctx_lens, the rows' own among them) -> out, alike;
+    row_start int32 [B + 1]; window 0: the whole context."""
+    B, max_blocks = block_table.shape
+    T, Hq, D = q.shape
+    i32, dev = torch.int32, torch.cuda.current_device()
+    shape = (T, Hq, cache.head_dim)
+    check("tts_prompt_attn", lib().tts_prompt_attn(
+        _cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_lens, "ctx_lens", i32, (B,), dev), B, _on(row_start, "row_start", i32, (B + 1,), dev), T, Hq, float(scale),
+        int(window), int(sinks), _on(q, "q", cache.dtype, shape, dev), _on(out, "out", cache.dtype, shape, dev),
+        _on(ws, "ws", None, None, dev), ws.nbytes, None if err is None else _on(err, "err", i32, None, dev),
+        _raw_stream(stream, dev)))
+
+
 def tts_decode_attn_noalloc(cache: KVCache, block_table, ctx_lens, max_ctx_len, q, out, scale,
                             causal=False, err=None, stream=None):
     """tts_decode_attn without a workspace, for callers that cannot allocate

@@ -21,7 +21,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 BUILD = PKG / "_build"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["kv_append.cu", "kv_pages.cu", "decode_attn.cu", "head_select.cu", "spec_verify.cu", "tts_host.cpp",
+SOURCES = ["kv_append.cu", "kv_pages.cu", "prompt_attn.cu", "decode_attn.cu", "head_select.cu", "spec_verify.cu", "tts_host.cpp",
            "tts_step.cpp", "tts_graph.cu", "code_predictor.cu", "latent_append.cu",
            "latent_decode.cu", "latent_prefill.cu"]
 

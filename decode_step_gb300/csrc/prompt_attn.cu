@@ -1,0 +1,941 @@
+// Attention of chunks of new tokens (prompts, or pieces of them) over the paged
+// KV cache, causal, with an optional sliding window and sinks:
+//   out[r][h] = sum_t softmax_t(scale * q[r][h] . k_t) v_t
+// over the tokens t <= p (p the row's position) with t < sinks or t > p - window.
+//
+// Work.  A query tile is two halves of 128 matrix rows; a half holds 128 /
+// group tokens with all `group` query heads of one KV head (so that a KV tile is
+// read once for the group).  A segment is a query tile and a KV head; its work is
+// the 128-token tiles of the context that some row sees.  The flat list of all
+// segments' tiles is split into equal contiguous ranges, one a CTA: long and
+// short segments, prompts and few rows over a long context all spread over the
+// SMs alike.  A range boundary that falls within kSnap tiles of a segment's end
+// moves there; a segment that is split all the same is published in parts (m, l,
+// o), and the last CTA to finish one (an atomic ticket, never a wait) joins them
+// in the order of the CTAs, so that results do not depend on who is last.  Every
+// CTA finds its range by itself from the streams' lengths.
+//
+// A CTA.  Two softmax warpgroups, one a half, that take turns on the tensor core;
+// a producer warp (TMA, one box of 16 tokens x 64 dimensions a block, through the
+// table); an MMA issuer; two warps that look at the values of the tiles that not
+// every row sees whole (below).  S = Q K^T and O += P V run as tcgen05 MMAs of
+// 128 x 128 x 16; S and O are in tensor memory, P (bf16, 2^-9 of a weight at
+// most; the softmax sum is of the weights before the rounding) goes back into
+// S's columns.
+//
+// Values that are not finite.  A weight of zero times NaN is NaN, so a token that
+// a row does not see must not meet it in the matrix product.  Tiles that every
+// row sees need no care.  In the others the two spare warps clear such values in
+// shared memory, and the rows that do see them get them at the end.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <cmath>
+
+#include "latent_common.cuh"
+#include "tcgen05.cuh"
+#include "tts_common.cuh"
+#include "tts_internal.h"
+
+namespace tts {
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kDim = 128;
+constexpr int kTile = 128;                  // tokens a tile, matrix rows a half
+constexpr int kChunkBytes = kTile * 128;    // [128 rows][64 values], 128-byte swizzle
+constexpr int kSlotBytes = 2 * kChunkBytes; // a tile of keys or values
+constexpr int kKeySlots = 2, kValueSlots = 3;  // (keys are done with half a tile before the values)
+constexpr int kThreads = 384;               // two softmax warpgroups; producer, issuer, two checkers
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104, kStartRegs = 168;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kStartRegs);
+constexpr int kMaxStreams = 4096;           // (their lengths are staged in shared memory)
+constexpr int kSnap = 2;                    // tiles
+constexpr int kMinTiles = 4;                // tiles a CTA at least, where there are more CTAs than segments
+constexpr float kLog2e = 1.4426950408889634f;
+// Running maximum before any token (log2 units): no finite score is below it.
+constexpr float kNoScore = -FLT_MAX;
+constexpr float kSlack = 8.0f;              // scores may pass it by this much before it moves (log2 units)
+constexpr int kPartFloats = kTile * kDim + 2 * kTile;  // o, m, l of a half
+
+struct PromptArgs {
+    const int32_t *table;
+    int max_blocks, num_blocks;
+    const int32_t *ctx_lens;
+    const int32_t *row_start;
+    int B, num_rows, Hq, Hkv, group, tokens;  // tokens: of a half
+    int window, sinks;                        // window 0: none
+    float scale_log2;
+    const uint8_t *v_pool;
+    __nv_bfloat16 *out;
+    float *part;          // [CTA][first, later part][half] partial results
+    int32_t *tickets;     // [CTA][half]
+    int ctas, max_tiles;  // query tiles at most
+    int zero_row;         // a row behind the pool: reads as zeros
+    int32_t *err;
+    long long wait_limit; // SM clock cycles per bounded wait
+    int stall;            // test support: the first keys expect 16 bytes that never come
+};
+
+// ---------------------------------------------------------------- the work
+
+// Rows and context of stream b; false: out of range.
+__device__ __forceinline__ bool prompt_stream(const PromptArgs &a, int b, int *first, int *n, int *ctx) {
+    *first = __ldcg(a.row_start + b);
+    const int end = __ldcg(a.row_start + b + 1);
+    *ctx = __ldcg(a.ctx_lens + b);
+    *n = 0;
+    if (*first == end) return true;
+    if (*first < 0 || end < *first || end > a.num_rows) return false;
+    if (*ctx < end - *first || *ctx > a.max_blocks * TTS_BLOCK_TOKENS) return false;
+    *n = end - *first;
+    return true;
+}
+__device__ __forceinline__ int query_tiles(const PromptArgs &a, int n) { return (n + 2 * a.tokens - 1) / (2 * a.tokens); }
+
+// What a query tile sees: the tokens below `high`, of which those from `low` on
+// (the first row's window) and the sinks; in 128-token tiles: the first `head`
+// ones and, `skip` further on, the others.
+struct Span {
+    int low, high, tiles, head, skip;
+};
+__device__ __forceinline__ Span span_of(const PromptArgs &a, int n, int ctx, int i) {
+    Span s;
+    const int r0 = i * 2 * a.tokens;
+    s.high = ctx - n + min(n, r0 + 2 * a.tokens);
+    s.low = a.window ? max(0, ctx - n + r0 + 1 - a.window) : 0;
+    s.head = (min(a.sinks, s.high) + kTile - 1) / kTile;
+    s.skip = max(0, s.low / kTile - s.head);
+    s.tiles = (s.high + kTile - 1) / kTile - s.skip;
+    return s;
+}
+
+// Equal ranges of the flat list (T tiles, W CTAs, T >= W).
+struct Ranges {
+    int q, rem;
+    __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
+    __device__ __forceinline__ int of(int t) const {
+        const int big = rem * (q + 1);
+        return t < big ? t / (q + 1) : rem + (t - big) / q;
+    }
+};
+
+// Walks a CTA's range: part after part of a segment, tile after tile.
+struct Walk {
+    int left;                  // tiles of the range left, this one among them
+    int b, i, g, k;            // stream, query tile, KV head, tile of the segment
+    int s0;                    // the segment's first tile in the flat list
+    int first, n, ctx;         // of the stream
+    Span span;
+    bool fresh;                // first tile of a part
+    __device__ __forceinline__ int r0(const PromptArgs &a) const { return i * 2 * a.tokens; }
+    __device__ __forceinline__ bool two(const PromptArgs &a) const { return r0(a) + a.tokens < n; }
+    __device__ __forceinline__ int tile() const { return k < span.head ? k : k + span.skip; }
+    __device__ __forceinline__ bool ends() const { return k + 1 == span.tiles || left == 1; }  // the part
+    __device__ __forceinline__ void seek(const PromptArgs &a) {  // b: the next stream that has rows
+        for (; b < a.B; ++b) {
+            const bool good = prompt_stream(a, b, &first, &n, &ctx);
+            n = uniform(good ? n : 0);
+            ctx = uniform(ctx);
+            first = uniform(first);
+            if (n) return;
+        }
+    }
+    __device__ __forceinline__ void settle(const PromptArgs &a) {  // k may be behind the segment's last tile
+        fresh = true;
+        if (k < span.tiles) return;
+        k = 0;
+        s0 += span.tiles;
+        if (++g < a.Hkv) return;
+        g = 0;
+        if (++i == query_tiles(a, n)) {
+            i = 0;
+            ++b;
+            seek(a);
+        }
+        span = span_of(a, n, ctx, i);
+    }
+    __device__ __forceinline__ void advance(const PromptArgs &a) {
+        fresh = false;
+        ++k;
+        if (--left > 0 && k == span.tiles) settle(a);
+    }
+    // whether some row of the query tile does not see some token of the tile
+    __device__ __forceinline__ bool edge(const PromptArgs &a) const {
+        const int t0 = tile() * kTile, first_limit = ctx - n + r0(a) + 1;
+        return !(t0 + kTile <= first_limit && (!a.window || t0 + kTile <= a.sinks || t0 >= span.high - a.window));
+    }
+};
+
+// A place in a ring of slots and its barriers' parity.
+template <int kSlots>
+struct Place {
+    uint32_t slot = 0, phase = 0;
+    bool again = false;  // the ring has been through once
+    __device__ __forceinline__ void next() {
+        if (++slot == kSlots) {
+            slot = 0;
+            phase ^= 1;
+            again = true;
+        }
+    }
+    // Waits for what the slots were last filled with.
+    __device__ __forceinline__ void drain(const uint64_t *full) {
+        for (int i = again ? kSlots : slot; i > 0; --i) {
+            if (slot == 0) {
+                slot = kSlots;
+                phase ^= 1;
+            }
+            --slot;
+            warp_wait(&full[slot], phase);
+        }
+    }
+};
+
+struct PromptShared {
+    uint64_t k_full[kKeySlots], k_empty[kKeySlots], v_full[kValueSlots], v_empty[kValueSlots], checked[kValueSlots];
+    uint64_t q_full[2], q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], stored[2], told[2], done;
+    uint32_t tmem;
+    uint32_t valid[8];     // blocks of a tile that are in the pool, by tile % 8
+    int odd[4];            // number (from 1) of the part whose tiles held values that are not finite, by number % 4
+    int last[2];           // whether the half's part was the last one
+    long long scan[2][kThreads / 32];
+    int b, i, g, k, s0, from, to, workers, q, rem;
+};
+constexpr int kSmem = (2 + kKeySlots + kValueSlots) * kSlotBytes + static_cast<int>(sizeof(PromptShared));
+static_assert(kSmem <= 227 * 1024);
+static_assert(kMaxStreams * 16 <= (kKeySlots + kValueSlots) * kSlotBytes);
+
+// Zeros in the rows of the refused streams (rare), by every thread of the grid.
+__device__ __noinline__ void zero_refused(const PromptArgs &a) {
+    const size_t width = static_cast<size_t>(a.Hq) * kDim / 8;  // 16-byte pieces a row
+    const size_t me = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x, all = static_cast<size_t>(gridDim.x) * blockDim.x;
+    for (int b = 0; b < a.B; ++b) {
+        int first, n, ctx;
+        if (prompt_stream(a, b, &first, &n, &ctx)) continue;
+        if (me == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
+        const int from = max(0, first), to = min(a.num_rows, __ldcg(a.row_start + b + 1));
+        if (from >= to) continue;
+        for (size_t i = from * width + me; i < to * width; i += all) reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Sum over the threads before this one, and over all.
+__device__ __forceinline__ long long scan_before(long long mine, long long *warps, long long *all) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) warps[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warps[w];
+        total += warps[w];
+    }
+    *all = total;
+    return before;
+}
+
+// Finds the CTA's range: sh.b, i, g, k, s0 (its first tile) and sh.from, to.
+// `streams`: room for kMaxStreams + 1.  Every thread calls it.
+__device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh, int4 *streams) {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    long long mine = 0;
+    bool refused = false;
+    for (int b = b0; b < b1; ++b) {
+        int first, n, ctx;
+        refused = !prompt_stream(a, b, &first, &n, &ctx) || refused;
+        mine += query_tiles(a, n);
+        streams[b] = make_int4(first, n, ctx, 0);
+    }
+    long long all_tiles;
+    long long at = scan_before(mine, sh.scan[0], &all_tiles);
+    // (more than these only if the streams' rows overlap)
+    const bool apart = all_tiles <= a.max_tiles;
+    const int tiles = apart ? static_cast<int>(all_tiles) : 0;
+    if (!apart && blockIdx.x == 0 && threadIdx.x == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
+    for (int b = b0; b < b1; ++b) {
+        streams[b].w = static_cast<int>(at);
+        at += query_tiles(a, streams[b].y);
+    }
+    if (__syncthreads_or(refused)) zero_refused(a);
+    // the tiles of this thread's share of the query tiles
+    const int each = (tiles + kThreads - 1) / kThreads;
+    const int t0 = min(tiles, static_cast<int>(threadIdx.x) * each), t1 = min(tiles, t0 + each);
+    int start_b = 0;
+    if (t0 < t1) {
+        int hi = a.B;  // streams[start_b].w <= t0 < streams[hi].w
+        while (hi - start_b > 1) {
+            const int mid = (start_b + hi) / 2;
+            if (streams[mid].w <= t0) start_b = mid;
+            else hi = mid;
+        }
+    }
+    auto each_tile = [&](auto &&f) {
+        int b = start_b;
+        int4 s = t0 < t1 ? streams[b] : make_int4(0, 0, 0, 0);
+        for (int t = t0; t < t1; ++t) {
+            while (b + 1 < a.B && streams[b + 1].w <= t) s = streams[++b];
+            f(b, t - s.w, span_of(a, s.y, s.z, t - s.w).tiles);
+        }
+    };
+    long long sum = 0, total;
+    each_tile([&](int, int, int n) { sum += n; });
+    const long long before = scan_before(sum, sh.scan[1], &total) * a.Hkv;
+    const int T = static_cast<int>(total) * a.Hkv;  // (below 2^30, as the host has seen to)
+    const int segments = tiles * a.Hkv;
+    const int W = min(min(a.ctas, T), max((T + kMinTiles - 1) / kMinTiles, segments));
+    const int c = blockIdx.x;
+    Ranges ranges{W ? T / W : 0, W ? T % W : 0};
+    if (threadIdx.x == 0) {
+        sh.workers = W;
+        sh.q = ranges.q;
+        sh.rem = ranges.rem;
+        if (c >= W) sh.from = sh.to = 0;
+        else if (c + 1 == W) sh.to = T;
+    }
+    if (c < W) {
+        const int x0 = ranges.start(c), x1 = ranges.start(c + 1);
+        int at_tile = static_cast<int>(before);
+        each_tile([&](int b, int i, int n) {
+            const int end = at_tile + n * a.Hkv;
+            for (int which = 0; which < 2; ++which) {
+                const int x = which ? x1 : x0;
+                if (x < at_tile || x >= end) continue;
+                const int g = (x - at_tile) / n, s0 = at_tile + g * n;
+                int k = x - s0;
+                if (k <= kSnap) k = 0;
+                else if (n - k <= kSnap) k = n;
+                if (which) {
+                    sh.to = s0 + k;
+                } else {
+                    sh.from = s0 + k;
+                    sh.b = b;
+                    sh.i = i;
+                    sh.g = g;
+                    sh.k = k;
+                    sh.s0 = s0;
+                }
+            }
+            at_tile = end;
+        });
+    }
+    __syncthreads();
+}
+
+// CTAs that share a segment: its first part's and how many follow.
+struct Shares {
+    int first, more;
+};
+__device__ __forceinline__ Shares shares_of(const Ranges &r, int s0, int tiles) {
+    if (tiles <= 2 * kSnap) return {0, 0};
+    const int lo = r.of(s0 + kSnap) + 1, hi = r.of(s0 + tiles - kSnap - 1);  // boundaries inside that stay
+    return {lo - 1, max(0, hi - lo + 1)};
+}
+
+// ------------------------------------------------------------- the softmax
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+// Bits of the tokens of word w (32 tokens from `base` on) before token t.
+__device__ __forceinline__ uint32_t bits_before(int t, int base) {
+    const int n = t - base;
+    return n <= 0 ? 0u : n >= 32 ? kFull : (1u << n) - 1u;
+}
+
+// Values of this row's tokens that are not finite, of 32 dimensions from d on,
+// added up in o (rare): those of the tiles that the checkers cleared.
+__device__ __noinline__ void find_odd(const PromptArgs &a, Walk part, int tiles, int limit, int d, float *o) {
+    for (int j = 0; j < tiles; ++j, ++part.k) {
+        if (!part.edge(a)) continue;
+        for (int t = part.tile() * kTile; t < part.tile() * kTile + kTile && t < limit; ++t) {
+            if (a.window && t >= a.sinks && t < limit - a.window) continue;
+            const int id = __ldcg(a.table + static_cast<size_t>(part.b) * a.max_blocks + t / TTS_BLOCK_TOKENS);
+            if (id < 0 || id >= a.num_blocks) continue;
+            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v_pool) +
+                                ((static_cast<size_t>(id) * a.Hkv + part.g) * TTS_BLOCK_TOKENS + t % TTS_BLOCK_TOKENS) * kDim + d;
+            for (int e = 0; e < 32; ++e) {
+                const uint32_t w = v[e];
+                if ((w & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float(w << 16);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void add_odd(const PromptArgs &a, const Walk &part, int tiles, int limit, int d, float *f) {
+    float o[32];
+    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+    find_odd(a, part, tiles, limit, d, o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) f[i] += o[i];
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    const uint32_t q_base = smem_addr(raw), k_base = q_base + 2 * kSlotBytes, v_base = k_base + kKeySlots * kSlotBytes;
+    PromptShared &sh = *reinterpret_cast<PromptShared *>(raw + (2 + kKeySlots + kValueSlots) * kSlotBytes);
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+    if (warp == 9 && lane == 0) {
+        for (int i = 0; i < kKeySlots; ++i) {
+            mbar_init(smem_addr(&sh.k_full[i]), 1);
+            mbar_init(smem_addr(&sh.k_empty[i]), 1);
+        }
+        for (int i = 0; i < kValueSlots; ++i) {
+            mbar_init(smem_addr(&sh.v_full[i]), 1);
+            mbar_init(smem_addr(&sh.v_empty[i]), 1);
+            mbar_init(smem_addr(&sh.checked[i]), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.q_full[i]), 1);
+            mbar_init(smem_addr(&sh.s_full[i]), 1);
+            mbar_init(smem_addr(&sh.p_full[i]), 4);
+            mbar_init(smem_addr(&sh.o_full[i]), 1);
+            mbar_init(smem_addr(&sh.o_empty[i]), 4);
+            mbar_init(smem_addr(&sh.stored[i]), 4);
+            mbar_init(smem_addr(&sh.told[i]), 1);
+        }
+        mbar_init(smem_addr(&sh.q_empty), 1);
+        mbar_init(smem_addr(&sh.done), 1);
+        for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8 && lane == 0) {
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    pdl_wait_prerequisites();
+    // (tensor memory only after the wait: the kernel before may be one that
+    // still has to allocate its own)
+    if (warp == 10) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    find_range(a, sh, reinterpret_cast<int4 *>(raw + 2 * kSlotBytes));
+    // (the staged lengths make way for copies)
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_allow_dependents();
+    const uint32_t tmem = uniform(sh.tmem);  // S0, S1, O0, O1: 128 columns each
+    const Ranges ranges{uniform(sh.q), uniform(sh.rem)};
+    Walk walk;
+    walk.left = uniform(sh.to - sh.from);
+    bool ok = true;
+    if (walk.left > 0) {
+        walk.b = uniform(sh.b);
+        walk.i = uniform(sh.i);
+        walk.g = uniform(sh.g);
+        walk.k = uniform(sh.k);
+        walk.s0 = uniform(sh.s0);
+        walk.seek(a);
+        walk.span = span_of(a, walk.n, walk.ctx, walk.i);
+        walk.settle(a);
+        if (warp >= 8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+            if (warp == 8) {
+                // ---- producer: lanes 0-7 look after a block each
+                uint32_t part = 0, q_count[2] = {0, 0};
+                Place<kKeySlots> keys;
+                Place<kValueSlots> values;
+                auto lookup = [&](const Walk &w, int &id) {
+                    const int t = (w.tile() * 8 + lane % 8) * TTS_BLOCK_TOKENS;
+                    // blocks without a token that some row sees may hold anything
+                    const bool seen = t < w.span.high && (t < a.sinks || t + TTS_BLOCK_TOKENS > w.span.low);
+                    id = seen ? __ldcg(a.table + static_cast<size_t>(w.b) * a.max_blocks + t / TTS_BLOCK_TOKENS) : -1;
+                    return seen;
+                };
+                int id, id_next = -1;
+                bool seen = lookup(walk, id), seen_next = false;
+                auto load = [&](const CUtensorMap *map, int y, uint64_t *full, uint64_t *empty, uint32_t base, auto &at,
+                                uint32_t more) {
+                    if (at.again && !warp_wait(&empty[at.slot], at.phase ^ 1, a.wait_limit)) return false;
+                    const uint32_t bar = smem_addr(&full[at.slot]), to = base + at.slot * kSlotBytes;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, kSlotBytes + more);
+                    __syncwarp();
+                    if (lane < 16) tma_load_2d(to + lane / 8 * kChunkBytes + lane % 8 * 2048, map, lane / 8 * 64, y, bar);
+                    at.next();
+                    return true;
+                };
+                for (uint32_t t = 0; ok && walk.left > 0; ++t) {
+                    const bool good = id >= 0 && id < a.num_blocks;
+                    if (seen && !good && lane < 8) flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
+                    const int y = good ? (id * a.Hkv + walk.g) * TTS_BLOCK_TOKENS : a.zero_row;
+                    const uint32_t mask = __ballot_sync(kFull, good) & 0xFFu;
+                    Walk next = walk;
+                    next.advance(a);
+                    if (next.left > 0) seen_next = lookup(next, id_next);
+                    if (lane == 0) sh.valid[t % 8] = mask;
+                    ok = load(&map_k, y, sh.k_full, sh.k_empty, k_base, keys, a.stall && t == 0 ? 16 : 0);
+                    if (!ok) break;
+                    if (walk.fresh) {
+                        ok = part == 0 || warp_wait(&sh.q_empty, (part - 1) & 1, a.wait_limit);
+                        if (!ok) break;
+                        const uint32_t halves = walk.two(a) ? 2 : 1;
+                        ++q_count[0];
+                        q_count[1] += halves - 1;
+                        if (lane == 0)
+                            for (uint32_t s = 0; s < halves; ++s) {
+                                const uint32_t bar = smem_addr(&sh.q_full[s]);
+                                mbar_arrive_expect_tx(bar, 2 * a.tokens * a.group * 128);
+                                for (int c = 0; c < 2; ++c)
+                                    asm volatile(
+                                        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                                        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_base + s * kSlotBytes + c * kChunkBytes),
+                                        "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(c * 64), "r"(walk.g * a.group),
+                                        "r"(walk.first + walk.r0(a) + static_cast<int>(s) * a.tokens), "r"(bar)
+                                        : "memory");
+                            }
+                        __syncwarp();
+                        ++part;
+                    }
+                    ok = load(&map_v, y, sh.v_full, sh.v_empty, v_base, values, 0);
+                    walk = next;
+                    id = id_next;
+                    seen = seen_next;
+                }
+                // every copy lands before the CTA ends
+                keys.drain(sh.k_full);
+                values.drain(sh.v_full);
+                for (uint32_t s = 0; s < 2; ++s)
+                    if (q_count[s]) warp_wait(&sh.q_full[s], (q_count[s] - 1) & 1);
+            } else if (warp == 9) {
+                // ---- MMA issuer: S0 S1 | O0(t) S0(t + 1) | O1(t) S1(t + 1) ...; at a
+                // part's end O0 O1 | S0 S1 of the next.  A half's S is overwritten
+                // right after the O product that reads the weights kept in it; the
+                // tensor core runs them in order.
+                const uint32_t leader = elect_leader();
+                Place<kKeySlots> keys;      // of the next scores
+                Place<kValueSlots> values;  // of this tile
+                uint32_t p_count[2] = {0, 0}, q_count[2] = {0, 0}, o_count[2] = {0, 0};
+                auto scores = [&](int s) {
+                    const uint32_t sa = q_base + s * kSlotBytes, sb = k_base + keys.slot * kSlotBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16_by(leader, tmem + s * kTile, sw128_desc(sa + kk / 4 * kChunkBytes + kk % 4 * 32),
+                                    sw128_desc(sb + kk / 4 * kChunkBytes + kk % 4 * 32), mma_idesc(kTile, kTile), kk != 0);
+                    mma_commit_by(leader, smem_addr(&sh.s_full[s]));
+                };
+                auto output = [&](int s, bool fresh) {
+                    const uint32_t sb = v_base + values.slot * kSlotBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_ts_by(leader, tmem + (2 + s) * kTile, tmem + s * kTile + kk * 8,
+                                  sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc(kTile, kTile) | kTransposeB,
+                                  !fresh || kk != 0);
+                };
+                // the keys are done with (w: their tile)
+                auto keys_done = [&](const Walk &w) {
+                    mma_commit_by(leader, smem_addr(&sh.k_empty[keys.slot]));
+                    if (w.ends()) mma_commit_by(leader, smem_addr(&sh.q_empty));
+                    keys.next();
+                };
+                // the first scores of a part
+                auto begin = [&](const Walk &w) {
+                    const bool two = w.two(a);
+                    WarpWaits<3> x;
+                    x.set(0, &sh.k_full[keys.slot], keys.phase);
+                    x.set(1, &sh.q_full[0], q_count[0]++ & 1);
+                    x.none(2);
+                    if (two) x.set(2, &sh.q_full[1], q_count[1]++ & 1);
+                    if (!x.wait(a.wait_limit)) return false;
+                    tc_fence_after();
+                    scores(0);
+                    if (two) scores(1);
+                    keys_done(w);
+                    return true;
+                };
+                bool go = begin(walk);
+                while (go && walk.left > 0) {
+                    const bool two = walk.two(a), ends = walk.ends(), fresh = walk.fresh;
+                    Walk next = walk;
+                    next.advance(a);
+                    for (int s = 0; go && s < (two ? 2 : 1); ++s) {
+                        WarpWaits<4> x;
+                        x.set(0, &sh.p_full[s], p_count[s]++ & 1);
+                        x.none(1);
+                        x.none(2);
+                        x.none(3);
+                        if (s == 0) {
+                            x.set(1, &sh.v_full[values.slot], values.phase);
+                            x.set(3, &sh.checked[values.slot], values.phase);
+                        }
+                        if (fresh) {
+                            if (o_count[s]) x.set(2, &sh.o_empty[s], (o_count[s] - 1) & 1);
+                            ++o_count[s];
+                        }
+                        go = x.wait(a.wait_limit);
+                        if (!go) break;
+                        tc_fence_after();
+                        output(s, fresh);
+                        if (ends) mma_commit_by(leader, smem_addr(&sh.o_full[s]));
+                        if (s == 1 || !two) mma_commit_by(leader, smem_addr(&sh.v_empty[values.slot]));
+                        if (!ends) {
+                            if (s == 0) {
+                                go = warp_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
+                                if (!go) break;
+                                tc_fence_after();
+                            }
+                            scores(s);
+                            if (s == 1 || !two) keys_done(next);
+                        }
+                    }
+                    values.next();
+                    if (go && ends && next.left > 0) go = begin(next);
+                    walk = next;
+                }
+                mma_commit_by(leader, smem_addr(&sh.done));
+                ok = warp_wait(&sh.done, 0) && go;
+            } else {
+                // ---- checkers: values that are not finite leave the tiles that some
+                // row does not see whole.  (They keep step with every tile: a barrier's
+                // parity tells one use of a slot from the next, not from the one after.)
+                Place<kValueSlots> values;
+                int part = 0;
+                while (ok && walk.left > 0) {
+                    part += walk.fresh;
+                    ok = warp_wait(&sh.v_full[values.slot], values.phase, a.wait_limit);
+                    if (!ok) break;
+                    if (walk.edge(a)) {
+                        const int t0 = walk.tile() * kTile, first_limit = walk.ctx - walk.n + walk.r0(a) + 1;
+                        uint8_t *v = raw + (2 + kKeySlots + values.slot) * kSlotBytes;
+                        bool odd = false;
+#pragma unroll 4
+                        for (int e = (warp - 10) * 32 + lane; e < kSlotBytes / 16; e += 64) {
+                            uint4 x = reinterpret_cast<uint4 *>(v)[e];
+                            uint32_t bad = 0;
+                            for (const uint32_t w : {x.x, x.y, x.z, x.w})
+                                bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+                            if (!bad) continue;
+                            const int t = t0 + e / 8 % kTile;
+                            odd = odd || (t < walk.span.high && (!a.window || t < a.sinks || t >= first_limit - a.window));
+                            uint16_t *h = reinterpret_cast<uint16_t *>(v + e * 16);
+                            for (int i = 0; i < 8; ++i)
+                                if ((h[i] & 0x7F80u) == 0x7F80u) h[i] = 0;
+                        }
+                        if (odd) sh.odd[part % 4] = part;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.checked[values.slot]));
+                    values.next();
+                    walk.advance(a);
+                }
+            }
+        } else {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+            // ---- softmax warpgroups: thread = matrix row
+            const int s = warp / 4, w = warp % 4;
+            const int row = w * 32 + lane, token = row / a.group, head = row % a.group;
+            const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+            const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + (2 + s) * kTile;
+            uint32_t tiles = 0, parts = 0, joins = 0;  // of this half
+            int part = 0;
+            uint32_t t = 0;
+            while (ok && walk.left > 0) {
+                // ---- a part
+                ++part;
+                const Walk begun = walk;
+                const int tiles_here = min(walk.left, walk.span.tiles - walk.k);
+                if (s == 1 && !walk.two(a)) {
+                    walk.left -= tiles_here - 1;
+                    walk.k += tiles_here - 1;
+                    t += tiles_here;
+                    walk.advance(a);
+                    continue;
+                }
+                const int half0 = walk.r0(a) + s * a.tokens, before = walk.ctx - walk.n;
+                const int high = before + min(walk.n, half0 + a.tokens);       // tokens that the last row sees
+                const int r = half0 + token;                                   // row in the stream
+                const int limit = min(before + r + 1, high);                   // tokens up to the row's own
+                float m = kNoScore, l = 0.0f;
+                for (int j = 0; j < tiles_here; ++j, ++t, ++tiles, ++walk.k) {
+                    if (!warp_wait(&sh.s_full[s], tiles & 1, a.wait_limit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t valid = *reinterpret_cast<volatile uint32_t *>(&sh.valid[t % 8]);
+                    uint32_t x[kTile];
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 32) tmem_ld32_nowait(ts + c, x + c);
+                    tmem_wait_ld();
+                    const int t0 = walk.tile() * kTile;
+                    const bool whole = t0 + kTile <= before + half0 + 1 &&
+                                       (!a.window || t0 + kTile <= a.sinks || t0 >= high - a.window);
+                    if (!whole || valid != 0xFFu) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int base = t0 + 32 * c;
+                            uint32_t see = bits_before(limit, base);
+                            if (a.window) see &= bits_before(a.sinks, base) | ~bits_before(limit - a.window, base);
+                            see &= ((valid >> (2 * c)) & 1 ? 0xFFFFu : 0u) | ((valid >> (2 * c)) & 2 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((see >> i) & 1)) x[32 * c + i] = 0xFF800000u;  // -inf
+                        }
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
+                    const float high_now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                    if (__any_sync(kFull, high_now > m + kSlack)) {
+                        // (S(t) complete means that the product before it is too)
+                        const float now = fmaxf(m, high_now), f = hw_ex2(m - now);
+                        m = now;
+                        l *= f;
+                        if (j > 0)
+                            for (int c = 0; c < kDim; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_nowait(to + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tmem_st16(to + c, o);
+                            }
+                    }
+                    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 64) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float p0 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i]), a.scale_log2, -m));
+                            const float p1 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i + 1]), a.scale_log2, -m));
+                            sum[0] += p0;
+                            sum[1] += p1;
+                            p[i] = pack_bf16(p0, p1);
+                        }
+                        tmem_st32(ts + c / 2, p);
+                    }
+                    l += sum[0] + sum[1];
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
+                }
+                if (!ok) break;
+                // ---- the part's end: the rows, or what other CTAs' parts are joined with
+                ok = warp_wait(&sh.o_full[s], parts & 1, a.wait_limit);
+                if (!ok) break;
+                ++parts;
+                tc_fence_after();
+                const Shares shares = shares_of(ranges, begun.s0, begun.span.tiles);
+                const bool odd = *reinterpret_cast<volatile int *>(&sh.odd[part % 4]) == part;
+                const bool real = token < a.tokens && r < begun.n;
+                __nv_bfloat16 *out = a.out + (static_cast<size_t>(begun.first + r) * a.Hq + begun.g * a.group + head) * kDim;
+                if (shares.more == 0) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token left: zeros
+                    for (int c = 0; c < kDim; c += 32) {
+                        float f[32];
+                        tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
+                        tmem_wait_ld();
+                        if (odd && real) add_odd(a, begun, tiles_here, limit, c, f);
+                        if (real)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                reinterpret_cast<uint4 *>(out + c)[i] =
+                                    make_uint4(pack_bf16(f[8 * i] * inv, f[8 * i + 1] * inv),
+                                               pack_bf16(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
+                                               pack_bf16(f[8 * i + 4] * inv, f[8 * i + 5] * inv),
+                                               pack_bf16(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.o_empty[s]));
+                } else {
+                    // a part's slot: [first part of a segment or a later one][half], [32][128 rows][4] and m, l
+                    auto slot = [&](int c) {
+                        return a.part + static_cast<size_t>((c * 2 + (c == shares.first ? 0 : 1)) * 2 + s) * kPartFloats;
+                    };
+                    float *mine = slot(blockIdx.x);
+                    for (int c = 0; c < kDim; c += 32) {
+                        float f[32];
+                        tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
+                        tmem_wait_ld();
+                        if (odd && real) add_odd(a, begun, tiles_here, limit, c, f);
+                        if (real)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                reinterpret_cast<float4 *>(mine)[(c / 4 + i) * kTile + row] =
+                                    make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                    }
+                    if (real) {
+                        mine[kTile * kDim + row] = m;
+                        mine[kTile * kDim + kTile + row] = l;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(smem_addr(&sh.o_empty[s]));
+                        mbar_arrive(smem_addr(&sh.stored[s]));
+                    }
+                    // (bounded waits, as everywhere: a warp may have given up)
+                    if (w == 0) ok = warp_wait(&sh.stored[s], joins & 1, a.wait_limit);
+                    if (row == 0 && ok) {
+                        int old;
+                        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                                     : "=r"(old)
+                                     : "l"(a.tickets + 2 * shares.first + s)
+                                     : "memory");
+                        sh.last[s] = old == shares.more;
+                        if (old == shares.more) a.tickets[2 * shares.first + s] = 0;
+                        mbar_arrive(smem_addr(&sh.told[s]));
+                    }
+                    __syncwarp();
+                    ok = ok && warp_wait(&sh.told[s], joins & 1, a.wait_limit);
+                    ++joins;
+                    if (!ok) break;
+                    if (*reinterpret_cast<volatile int *>(&sh.last[s]) && real) {
+                        float top = kNoScore, sum = 0.0f;
+                        for (int c = 0; c <= shares.more; ++c) top = fmaxf(top, __ldcg(slot(shares.first + c) + kTile * kDim + row));
+                        for (int c = 0; c <= shares.more; ++c) {
+                            const float *p = slot(shares.first + c) + kTile * kDim + row;
+                            sum = fmaf(hw_ex2(__ldcg(p) - top), __ldcg(p + kTile), sum);
+                        }
+                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                        for (int d = 0; d < kDim; d += 32) {
+                            float4 o[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            for (int c = 0; c <= shares.more; ++c) {
+                                const float *p = slot(shares.first + c);
+                                const float f = hw_ex2(__ldcg(p + kTile * kDim + row) - top);
+                                float4 x[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) x[i] = __ldcg(reinterpret_cast<const float4 *>(p) + (d / 4 + i) * kTile + row);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    o[i].x = fmaf(x[i].x, f, o[i].x);
+                                    o[i].y = fmaf(x[i].y, f, o[i].y);
+                                    o[i].z = fmaf(x[i].z, f, o[i].z);
+                                    o[i].w = fmaf(x[i].w, f, o[i].w);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                reinterpret_cast<uint4 *>(out + d)[i] =
+                                    make_uint4(pack_bf16(o[2 * i].x * inv, o[2 * i].y * inv),
+                                               pack_bf16(o[2 * i].z * inv, o[2 * i].w * inv),
+                                               pack_bf16(o[2 * i + 1].x * inv, o[2 * i + 1].y * inv),
+                                               pack_bf16(o[2 * i + 1].z * inv, o[2 * i + 1].w * inv));
+                        }
+                    }
+                }
+                // (the walk stands behind the part's last tile)
+                --walk.k;
+                walk.left -= tiles_here - 1;
+                walk.advance(a);
+            }
+        }
+        if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 10) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// -------------------------------------------------------------------- host
+
+int prompt_ctas() {
+    const int n = sm_count();
+    return n > 0 ? n : 160;  // no device visible (size queries on a build host)
+}
+
+bool prompt_shape_ok(int B, int T, int Hq, int Hkv) {
+    return B >= 0 && T >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0;
+}
+
+size_t prompt_part_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 4 * kPartFloats * sizeof(float), 256); }
+size_t prompt_ticket_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 2 * sizeof(int32_t), 256); }
+
+}  // namespace
+}  // namespace tts
+
+extern "C" size_t tts_prompt_attn_workspace_size(int32_t B, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                                 int32_t head_dim) {
+    using namespace tts;
+    if (!prompt_shape_ok(B, num_rows, num_q_heads, num_kv_heads) || head_dim != kDim || B > kMaxStreams ||
+        num_q_heads / num_kv_heads > kTile)
+        return 0;
+    return prompt_part_bytes() + prompt_ticket_bytes();
+}
+
+extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                               const int32_t *d_ctx_lens, int32_t B, const int32_t *d_row_start, int32_t num_rows,
+                               int32_t num_q_heads, float scale, int32_t window, int32_t sinks, const void *d_q,
+                               void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream) {
+    using namespace tts;
+    if (!cache || !d_block_table || !d_ctx_lens || !d_row_start || !d_q || !d_out) return TTS_ERR_INVALID;
+    if (!cache->k_pool || (!cache->v_pool && cache->dtype != TTS_FP8_E4M3) || cache->num_blocks < 1 ||
+        cache->num_kv_heads < 1)
+        return TTS_ERR_INVALID;
+    if (max_blocks_per_seq < 1 || max_blocks_per_seq > (1 << 20) || window < 0 || sinks < 0 || !(scale > 0.0f) ||
+        std::isinf(scale))
+        return TTS_ERR_INVALID;
+    const int Hq = num_q_heads, Hkv = cache->num_kv_heads;
+    if (!prompt_shape_ok(B, num_rows, Hq, Hkv)) return TTS_ERR_INVALID;
+    if (cache->block_size != TTS_BLOCK_TOKENS || cache->dtype != TTS_BF16 || cache->head_dim != kDim) return TTS_ERR_UNSUPPORTED;
+    if (B > kMaxStreams || Hq / Hkv > kTile) return TTS_ERR_UNSUPPORTED;
+    const uint64_t pool_rows = static_cast<uint64_t>(cache->num_blocks) * Hkv * TTS_BLOCK_TOKENS;
+    if (pool_rows >= (1ULL << 31)) return TTS_ERR_UNSUPPORTED;
+    if (!aligned16(cache->k_pool) || !aligned16(cache->v_pool) || !aligned16(d_q) || !aligned16(d_out)) return TTS_ERR_INVALID;
+    if (B == 0 || num_rows == 0) return TTS_OK;
+    if (!d_ws || ws_bytes < prompt_part_bytes() + prompt_ticket_bytes() || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0)
+        return TTS_ERR_WORKSPACE;
+
+    PromptArgs a{};
+    a.table = d_block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = cache->num_blocks;
+    a.ctx_lens = d_ctx_lens;
+    a.row_start = d_row_start;
+    a.B = B;
+    a.num_rows = num_rows;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.group = Hq / Hkv;
+    a.tokens = kTile / a.group;
+    // (no context passes 2^24 tokens)
+    a.window = window < (1 << 25) ? window : 0;
+    a.sinks = sinks < (1 << 24) ? sinks : 1 << 24;
+    if (!a.window) a.sinks = 0;
+    a.scale_log2 = scale * kLog2e;
+    a.v_pool = static_cast<const uint8_t *>(cache->v_pool);
+    a.out = static_cast<__nv_bfloat16 *>(d_out);
+    a.ctas = prompt_ctas();
+    a.part = static_cast<float *>(d_ws);
+    a.tickets = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + prompt_part_bytes());
+    a.zero_row = static_cast<int>(pool_rows);
+    a.err = d_err;
+    a.wait_limit = thread_opts().wait_limit;
+    a.stall = thread_opts().stall == TTS_TEST_STALL_PROMPT;
+    // the flat list of tiles is 32-bit
+    const int64_t query_tiles = static_cast<int64_t>(num_rows) / (2 * a.tokens) + B;
+    a.max_tiles = static_cast<int>(query_tiles);
+    if (query_tiles * Hkv * (max_blocks_per_seq / 8 + 1) >= (1LL << 30)) return TTS_ERR_UNSUPPORTED;
+    CUtensorMap map_q, map_k, map_v;
+    if (!make_tma_queries_bf16(&map_q, d_q, num_rows, Hq, a.group, a.tokens) ||
+        !make_tma_2d_bf16(&map_k, cache->k_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64) ||
+        !make_tma_2d_bf16(&map_v, cache->v_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64))
+        return TTS_ERR_CUDA;
+    if (!allow_smem(prompt_attn_kernel, kSmem)) return TTS_ERR_CUDA;
+    return launch_kernel(prompt_attn_kernel, dim3(a.ctas), dim3(kThreads), kSmem,
+                         {static_cast<cudaStream_t>(stream), thread_pdl()}, map_q, map_k, map_v, a);
+}

@@ -166,7 +166,7 @@ extern "C" int32_t tts_set_launch_flags(int32_t flags) {
 }
 
 extern "C" int tts_test_set_stall(int32_t what, int64_t wait_limit_cycles) {
-    if (what < TTS_TEST_STALL_NONE || what > TTS_TEST_STALL_LATENT_PREFILL || what == 3) return TTS_ERR_INVALID;
+    if (what < TTS_TEST_STALL_NONE || what > TTS_TEST_STALL_PROMPT || what == 3) return TTS_ERR_INVALID;
     if (wait_limit_cycles < 1000 || wait_limit_cycles > 4000000000LL) return TTS_ERR_INVALID;
     tts::ThreadOpts &o = tts::thread_opts();
     o.stall = what;
@@ -231,6 +231,19 @@ bool make_tma_rows_in_halves_bf16(CUtensorMap *map, const void *ptr, uint64_t ro
     const cuuint64_t dims[3] = {64, rows, 2};
     const cuuint64_t strides[2] = {256, 128};  // next row, next half
     const cuuint32_t box[3] = {64, box_rows, 2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tma_queries_bf16(CUtensorMap *map, const void *ptr, uint64_t tokens, uint64_t heads, uint32_t box_heads,
+                           uint32_t box_tokens) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {128, heads, tokens};
+    const cuuint64_t strides[2] = {256, 256 * static_cast<cuuint64_t>(heads)};
+    const cuuint32_t box[3] = {64, box_heads, box_tokens};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -39,6 +39,10 @@ bool cached_tma_2d(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t co
 // copy lands a tile of box_rows rows as [half][row][64] (each half 128-byte
 // swizzled), the layout two 2-D boxes of 64 columns would give.
 bool make_tma_rows_in_halves_bf16(CUtensorMap *map, const void *ptr, uint64_t rows, uint32_t box_rows);
+// 3-D descriptor of queries [tokens][heads][128] (bf16) in boxes of 64
+// dimensions x box_heads x box_tokens, 128-byte swizzle.
+bool make_tma_queries_bf16(CUtensorMap *map, const void *ptr, uint64_t tokens, uint64_t heads, uint32_t box_heads,
+                           uint32_t box_tokens);
 // bf16 forms of the two.
 bool make_tma_2d_bf16(CUtensorMap *map, const void *ptr, uint64_t rows, uint64_t cols,
                       uint32_t box_rows, uint32_t box_cols);

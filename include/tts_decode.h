@@ -302,6 +302,40 @@ int tts_window_decode_attn(const tts_kv_cache *cache, const int32_t *d_block_tab
                            int32_t num_q_heads, float scale, int32_t causal, int32_t window, int32_t sinks,
                            const void *d_q, void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream);
 
+/* Bytes of device workspace tts_prompt_attn needs (0 on bad or unsupported
+ * arguments); it does not depend on the lengths.  Zero-filled before its first
+ * use; every completed call leaves the part that has to be zero so.  Calls that
+ * overlap on the GPU need separate workspaces. */
+size_t tts_prompt_attn_workspace_size(int32_t B, int32_t num_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim);
+
+/* Attention of prompts, or chunks of them, over the paged cache, causal: the
+ * rows of stream b are d_row_start[b] <= r < d_row_start[b + 1] (int32 [B + 1],
+ * non-decreasing, at most num_rows), the last tokens of its d_ctx_lens[b] cached
+ * ones (append first: tts_kv_append_packed), so row r sees the tokens
+ *   t < limit = d_ctx_lens[b] - (d_row_start[b + 1] - r) + 1,
+ * with window > 0 of them those with t >= limit - window or t < sinks.  The sum
+ * is tts_decode_attn's, the weights rounded to bf16 before they meet the values.
+ *  d_q, d_out  bf16 [num_rows][num_q_heads][128], 16-byte aligned
+ *  window, sinks  >= 0; window 0: the whole context
+ * Supported: TTS_BF16, head_dim 128, num_q_heads / num_kv_heads <= 128, B <= 4096;
+ * query tiles (rows / (2 * (128 / group)) + B) x KV heads x 128-token tiles of
+ * max_blocks_per_seq below 2^30.
+ * Reads only the blocks that hold a token that some row sees, as
+ * tts_window_decode_attn; tokens that a row does not see do not reach it, and a
+ * value that is not finite makes that dimension of the rows that see it so.
+ * Rows of no stream are left alone.  A stream whose rows do not lie in [0,
+ * num_rows], or whose context length is outside [its rows,
+ * 16 * max_blocks_per_seq], gets zeros in its rows that lie there
+ * (TTS_ERRBIT_CTX_LEN); tokens in blocks with an invalid id are left out
+ * (TTS_ERRBIT_BLOCK_ID), and a row left without tokens gets zeros.
+ * TTS_ERRBIT_TIMEOUT: a bounded wait ran out, the outputs are undefined and the
+ * workspace has to be zero-filled again. */
+int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
+                    const int32_t *d_ctx_lens, int32_t B, const int32_t *d_row_start, int32_t num_rows,
+                    int32_t num_q_heads, float scale, int32_t window, int32_t sinks, const void *d_q, void *d_out,
+                    void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream);
+
 /* Decode attention with no caller workspace and no allocation.
  * The pages have no counterpart for this entry point.  It is for callers that
  * cannot call cudaMalloc where they run a decode step: engines that hand all
@@ -779,7 +813,7 @@ void tts_code_predictor_graph_destroy(tts_code_predictor_graph *graph);
  * TTS_LAUNCH_PROGRAMMATIC set, the single-kernel calls this thread makes
  * afterwards (tts_kv_append, tts_kv_append_rope, tts_kv_append_packed,
  * tts_decode_attn, tts_window_decode_attn, tts_codebook_head_select, the page
- * moves, and the first kernel of tts_latent_append,
+ * moves, tts_prompt_attn, and the first kernel of tts_latent_append,
  * tts_latent_decode_attn and tts_latent_prefill_attn) launch their kernel as a
  * programmatic dependent of the previous kernel in the stream: it may start
  * while that kernel finishes (hiding the launch latency, as the kernels of
@@ -802,8 +836,9 @@ int32_t tts_set_launch_flags(int32_t flags);
  *     deliver, so its first wait runs out;
  *   TTS_TEST_STALL_PREDICTOR_GRID: the persistent code-predictor kernel's
  *     first grid barrier waits for one CTA more than the grid has;
- *   TTS_TEST_STALL_LATENT_DECODE, TTS_TEST_STALL_LATENT_PREFILL: the first tile
- *     of every CTA of tts_latent_decode_attn's (tts_latent_prefill_attn's)
+ *   TTS_TEST_STALL_LATENT_DECODE, TTS_TEST_STALL_LATENT_PREFILL,
+ *   TTS_TEST_STALL_PROMPT: the first tile of every CTA of
+ *     tts_latent_decode_attn's (tts_latent_prefill_attn's, tts_prompt_attn's)
  *     attention kernel expects 16 more bytes than its copies deliver (these
  *     kernels wait for what is on its way with the default limit).
  * The kernel then ORs TTS_ERRBIT_TIMEOUT into *d_err, stops issuing work,
@@ -815,7 +850,8 @@ enum {
     TTS_TEST_STALL_ATTN_RING = 1,
     TTS_TEST_STALL_PREDICTOR_GRID = 2,
     TTS_TEST_STALL_LATENT_DECODE = 4, /* (3 is no mode) */
-    TTS_TEST_STALL_LATENT_PREFILL = 5
+    TTS_TEST_STALL_LATENT_PREFILL = 5,
+    TTS_TEST_STALL_PROMPT = 6
 };
 int tts_test_set_stall(int32_t what, int64_t wait_limit_cycles);
 

@@ -135,3 +135,28 @@ def test_window_refusals():
     assert window(c, ws=16) == -3
     assert window(kv(head_dim=64)) == -2
     assert window(c, B=0) == 0
+
+
+def prompt(cache, B=2, start=A, rows=5, Hq=4, scale=0.1, win=0, sinks=0, q=A, ws=1 << 30, ws_at=A, blocks=4):
+    return lib().tts_prompt_attn(ctypes.byref(cache), A, blocks, A, B, start, rows, Hq, scale, win, sinks, q, A, ws_at, ws,
+                                 None, None)
+
+
+def test_prompt_refusals():
+    c = kv()
+    assert prompt(c, start=None) == -1 and prompt(c, q=None) == -1 and prompt(c, q=A + 8) == -1
+    assert prompt(c, B=-1) == -1 and prompt(c, rows=-1) == -1
+    assert prompt(c, win=-1) == -1 and prompt(c, sinks=-1) == -1
+    assert prompt(c, scale=0.0) == -1 and prompt(c, scale=float("nan")) == -1 and prompt(c, scale=float("inf")) == -1
+    assert prompt(c, Hq=3) == -1 and prompt(c, Hq=0) == -1
+    assert prompt(c, blocks=0) == -1 and prompt(c, blocks=(1 << 20) + 1) == -1
+    assert prompt(kv(dtype=_lib.TTS_F32, head_dim=64)) == -2 and prompt(kv(head_dim=64)) == -2
+    assert prompt(c, Hq=258) == -2 and prompt(c, B=4097) == -2
+    assert prompt(kv(num_blocks=1 << 27)) == -2                # 2^32 rows of keys
+    assert prompt(c, ws=1000) == -3 and prompt(c, ws_at=None) == -3 and prompt(c, ws_at=A + 16) == -3
+    assert prompt(c, blocks=1 << 20, rows=1 << 24, Hq=256) == -2   # tiles past 2^30
+    assert prompt(c, B=0) == 0 and prompt(c, rows=0) == 0
+    size = lib().tts_prompt_attn_workspace_size
+    assert size(1, 1, 4, 2, 128) == size(4096, 10 ** 6, 128, 1, 128) > 0
+    assert size(1, 1, 3, 2, 128) == 0 and size(1, 1, 4, 2, 64) == 0 and size(4097, 1, 4, 2, 128) == 0
+    assert size(-1, 1, 4, 2, 128) == 0 and size(1, 1, 129, 1, 128) == 0
