@@ -48,7 +48,7 @@ constexpr int kChunkBytes = kTile * 128;    // [128 rows][64 values], 128-byte s
 constexpr int kSlotBytes = 2 * kChunkBytes; // a tile of keys or values
 constexpr int kKeySlots = 2, kValueSlots = 3;  // (keys are done with half a tile before the values)
 constexpr int kThreads = 384;               // two softmax warpgroups; producer, issuer, two checkers
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104, kStartRegs = 168;
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72, kStartRegs = 168;
 static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kStartRegs);
 constexpr int kMaxStreams = 4096;           // (their lengths are staged in shared memory)
 constexpr int kSnap = 2;                    // tiles
@@ -58,6 +58,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoScore = -FLT_MAX;
 constexpr float kSlack = 8.0f;              // scores may pass it by this much before it moves (log2 units)
 constexpr int kPartFloats = kTile * kDim + 2 * kTile;  // o, m, l of a half
+constexpr int kTakeTurns = 8;               // tiles of a segment from which on its one half's rows use both
+constexpr int kJoinHere = 4;                // parts that the last CTA joins; more are left to the second kernel
 
 struct PromptArgs {
     const int32_t *table;
@@ -71,6 +73,7 @@ struct PromptArgs {
     __nv_bfloat16 *out;
     float *part;          // [CTA][first, later part][half] partial results
     int32_t *tickets;     // [CTA][half]
+    int4 *jobs;           // [CTA][half] segments that the second kernel joins: rows (0: none), first row, KV head, parts
     int ctas, max_tiles;  // query tiles at most
     int zero_row;         // a row behind the pool: reads as zeros
     int32_t *err;
@@ -121,6 +124,12 @@ struct Ranges {
     }
 };
 
+// Whether some row does not see some token of the tile (`first`, `last`: tokens up
+// to the first and the last row's own).
+__device__ __forceinline__ bool tile_edge(const PromptArgs &a, int t0, int first, int last) {
+    return !(t0 + kTile <= first && (!a.window || t0 + kTile <= a.sinks || t0 >= last - a.window));
+}
+
 // Walks a CTA's range: part after part of a segment, tile after tile.
 struct Walk {
     int left;                  // tiles of the range left, this one among them
@@ -132,7 +141,6 @@ struct Walk {
     __device__ __forceinline__ int r0(const PromptArgs &a) const { return i * 2 * a.tokens; }
     __device__ __forceinline__ bool two(const PromptArgs &a) const { return r0(a) + a.tokens < n; }
     __device__ __forceinline__ int tile() const { return k < span.head ? k : k + span.skip; }
-    __device__ __forceinline__ bool ends() const { return k + 1 == span.tiles || left == 1; }  // the part
     __device__ __forceinline__ void seek(const PromptArgs &a) {  // b: the next stream that has rows
         for (; b < a.B; ++b) {
             const bool good = prompt_stream(a, b, &first, &n, &ctx);
@@ -161,10 +169,8 @@ struct Walk {
         ++k;
         if (--left > 0 && k == span.tiles) settle(a);
     }
-    // whether some row of the query tile does not see some token of the tile
     __device__ __forceinline__ bool edge(const PromptArgs &a) const {
-        const int t0 = tile() * kTile, first_limit = ctx - n + r0(a) + 1;
-        return !(t0 + kTile <= first_limit && (!a.window || t0 + kTile <= a.sinks || t0 >= span.high - a.window));
+        return tile_edge(a, tile() * kTile, ctx - n + r0(a) + 1, span.high);
     }
 };
 
@@ -193,12 +199,29 @@ struct Place {
     }
 };
 
+// What the producer tells the other warps: of a part (a segment's tiles in this
+// CTA), and of a tile that a half works on.
+struct PartInfo {
+    int first, n, ctx, b;         // of the stream
+    int r0, g, number, tiles;     // first row of the query tile, KV head, from 1, tiles of the part
+    int k, head, skip, low;       // first tile of the part; Span
+    int high, shares, more, mode; // first CTA of the segment, CTAs that follow
+};
+constexpr int kBoth = 1, kTurns = 2;  // mode: both halves have rows; the one half's rows use both, tile by tile
+struct __align__(8) TileInfo {
+    int flags, t0;  // bits 0-7: blocks in the pool, from kPartShift on: its part's note; first token
+};
+constexpr int kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12;
+constexpr int kInfos = 8;  // (the producer is at most four tiles ahead)
+
 struct PromptShared {
     uint64_t k_full[kKeySlots], k_empty[kKeySlots], v_full[kValueSlots], v_empty[kValueSlots], checked[kValueSlots];
     uint64_t q_full[2], q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], stored[2], told[2], done;
+    __align__(16) PartInfo parts[kInfos];
+    TileInfo tiles[2][kInfos];  // by use of the half
+    int4 jobs[2];
     uint32_t tmem;
-    uint32_t valid[8];     // blocks of a tile that are in the pool, by tile % 8
-    int odd[4];            // number (from 1) of the part whose tiles held values that are not finite, by number % 4
+    int odd[4];            // number of the part whose tiles held values that are not finite, by number % 4
     int last[2];           // whether the half's part was the last one
     long long scan[2][kThreads / 32];
     int b, i, g, k, s0, from, to, workers, q, rem;
@@ -354,10 +377,12 @@ __device__ __forceinline__ uint32_t bits_before(int t, int base) {
 
 // Values of this row's tokens that are not finite, of 32 dimensions from d on,
 // added up in o (rare): those of the tiles that the checkers cleared.
-__device__ __noinline__ void find_odd(const PromptArgs &a, Walk part, int tiles, int limit, int d, float *o) {
-    for (int j = 0; j < tiles; ++j, ++part.k) {
-        if (!part.edge(a)) continue;
-        for (int t = part.tile() * kTile; t < part.tile() * kTile + kTile && t < limit; ++t) {
+__device__ __noinline__ void find_odd(const PromptArgs &a, const PartInfo &part, int step, int j, int limit, int d, float *o) {
+    const int first_limit = part.ctx - part.n + part.r0 + 1;
+    for (; j < part.tiles; j += step) {
+        const int k = part.k + j, t0 = (k < part.head ? k : k + part.skip) * kTile;
+        if (!tile_edge(a, t0, first_limit, part.high)) continue;
+        for (int t = t0; t < t0 + kTile && t < limit; ++t) {
             if (a.window && t >= a.sinks && t < limit - a.window) continue;
             const int id = __ldcg(a.table + static_cast<size_t>(part.b) * a.max_blocks + t / TTS_BLOCK_TOKENS);
             if (id < 0 || id >= a.num_blocks) continue;
@@ -370,13 +395,34 @@ __device__ __noinline__ void find_odd(const PromptArgs &a, Walk part, int tiles,
         }
     }
 }
-
-__device__ __forceinline__ void add_odd(const PromptArgs &a, const Walk &part, int tiles, int limit, int d, float *f) {
+__device__ __forceinline__ void add_odd(const PromptArgs &a, const PartInfo &part, int step, int j, int limit, int d, float *f) {
     float o[32];
     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-    find_odd(a, part, tiles, limit, d, o);
+    find_odd(a, part, step, j, limit, d, o);
 #pragma unroll
     for (int i = 0; i < 32; ++i) f[i] += o[i];
+}
+
+// o / l as 32 bf16 values.
+__device__ __forceinline__ void store_row(__nv_bfloat16 *out, const float *f, float inv) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint4 *>(out)[i] =
+            make_uint4(pack_bf16(f[8 * i] * inv, f[8 * i + 1] * inv), pack_bf16(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
+                       pack_bf16(f[8 * i + 4] * inv, f[8 * i + 5] * inv), pack_bf16(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+}
+__device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }  // no token left: zeros
+
+// Slot of a part: CTA, whether the segment begins in it, half.  [32][128 rows][4]
+// floats o, then m and l of the rows.
+__device__ __forceinline__ float *part_slot(float *parts, int cta, bool begins, int half) {
+    return parts + static_cast<size_t>((cta * 2 + (begins ? 0 : 1)) * 2 + half) * kPartFloats;
+}
+// Part i of a segment whose first CTA is `first`: one a CTA (of half s), or with
+// both halves' in turns two.
+__device__ __forceinline__ float *segment_part(float *parts, int first, int i, bool turns, int s) {
+    const int c = turns ? i / 2 : i;
+    return part_slot(parts, first + c, c == 0, turns ? i % 2 : s);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -408,6 +454,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         mbar_init(smem_addr(&sh.q_empty), 1);
         mbar_init(smem_addr(&sh.done), 1);
         for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
+        sh.jobs[0] = sh.jobs[1] = make_int4(0, 0, 0, 0);
         fence_mbar_init();
     }
     if (warp == 8 && lane == 0) {
@@ -470,25 +517,52 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     at.next();
                     return true;
                 };
-                for (uint32_t t = 0; ok && walk.left > 0; ++t) {
+                int uses[2] = {0, 0}, j = 0, mode = 0, tiles = 0, note = 0;  // j: tile of the part
+                for (bool begun = false; ok && walk.left > 0; begun = true) {
                     const bool good = id >= 0 && id < a.num_blocks;
                     if (seen && !good && lane < 8) flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
                     const int y = good ? (id * a.Hkv + walk.g) * TTS_BLOCK_TOKENS : a.zero_row;
-                    const uint32_t mask = __ballot_sync(kFull, good) & 0xFFu;
+                    const int mask = __ballot_sync(kFull, good) & 0xFF;
+                    const int r0 = walk.r0(a);
+                    if (walk.fresh) {
+                        j = 0;
+                        note = part % kInfos;
+                        tiles = min(walk.left, walk.span.tiles - walk.k);
+                        mode = walk.two(a) ? kBoth : walk.span.tiles >= kTakeTurns ? kTurns : 0;
+                        if (lane == 0) {
+                            const Shares shares = shares_of(ranges, walk.s0, walk.span.tiles);
+                            PartInfo &p = sh.parts[note];
+                            p.first = walk.first; p.n = walk.n; p.ctx = walk.ctx; p.b = walk.b;
+                            p.r0 = r0; p.g = walk.g; p.number = part + 1; p.tiles = tiles;
+                            p.k = walk.k; p.head = walk.span.head; p.skip = walk.span.skip; p.low = walk.span.low;
+                            p.high = walk.span.high; p.shares = shares.first; p.more = shares.more; p.mode = mode;
+                        }
+                    }
+                    const int t0 = walk.tile() * kTile, before = walk.ctx - walk.n;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (mode == kTurns ? s != j % 2 : s == 1 && mode != kBoth) continue;
+                        const int from = r0 + (mode == kTurns ? 0 : s * a.tokens);
+                        const bool masked = mask != 0xFF || tile_edge(a, t0, before + from + 1, before + min(walk.n, from + a.tokens));
+                        const bool fresh = j < (mode == kTurns ? 2 : 1), last = j >= tiles - (mode == kTurns ? 2 : 1);
+                        if (lane == 0)
+                            sh.tiles[s][uses[s] % kInfos] = {mask | (masked ? kMasked : 0) | (fresh ? kFresh : 0) | (last ? kLast : 0) | note << kPartShift, t0};
+                        uses[s] += 1;
+                    }
+                    ++j;
                     Walk next = walk;
                     next.advance(a);
                     if (next.left > 0) seen_next = lookup(next, id_next);
-                    if (lane == 0) sh.valid[t % 8] = mask;
-                    ok = load(&map_k, y, sh.k_full, sh.k_empty, k_base, keys, a.stall && t == 0 ? 16 : 0);
+                    ok = load(&map_k, y, sh.k_full, sh.k_empty, k_base, keys, a.stall && !begun ? 16 : 0);
                     if (!ok) break;
                     if (walk.fresh) {
                         ok = part == 0 || warp_wait(&sh.q_empty, (part - 1) & 1, a.wait_limit);
                         if (!ok) break;
-                        const uint32_t halves = walk.two(a) ? 2 : 1;
+                        const int halves = mode == kBoth ? 2 : 1;
                         ++q_count[0];
                         q_count[1] += halves - 1;
                         if (lane == 0)
-                            for (uint32_t s = 0; s < halves; ++s) {
+                            for (int s = 0; s < halves; ++s) {
                                 const uint32_t bar = smem_addr(&sh.q_full[s]);
                                 mbar_arrive_expect_tx(bar, 2 * a.tokens * a.group * 128);
                                 for (int c = 0; c < 2; ++c)
@@ -496,7 +570,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
                                         " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_base + s * kSlotBytes + c * kChunkBytes),
                                         "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(c * 64), "r"(walk.g * a.group),
-                                        "r"(walk.first + walk.r0(a) + static_cast<int>(s) * a.tokens), "r"(bar)
+                                        "r"(walk.first + r0 + s * a.tokens), "r"(bar)
                                         : "memory");
                             }
                         __syncwarp();
@@ -513,16 +587,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 for (uint32_t s = 0; s < 2; ++s)
                     if (q_count[s]) warp_wait(&sh.q_full[s], (q_count[s] - 1) & 1);
             } else if (warp == 9) {
-                // ---- MMA issuer: S0 S1 | O0(t) S0(t + 1) | O1(t) S1(t + 1) ...; at a
-                // part's end O0 O1 | S0 S1 of the next.  A half's S is overwritten
-                // right after the O product that reads the weights kept in it; the
-                // tensor core runs them in order.
+                // ---- MMA issuer: S0 S1 | O0(j) S0(j + 1) | O1(j) S1(j + 1) ..., or, where
+                // the halves take turns, S0(0) S1(1) | O0(0) S0(2) | O1(1) S1(3) ...  A half's
+                // S is overwritten right after the O product that reads the weights kept
+                // in it; the tensor core runs them in order.
                 const uint32_t leader = elect_leader();
                 Place<kKeySlots> keys;      // of the next scores
-                Place<kValueSlots> values;  // of this tile
-                uint32_t p_count[2] = {0, 0}, q_count[2] = {0, 0}, o_count[2] = {0, 0};
-                auto scores = [&](int s) {
-                    const uint32_t sa = q_base + s * kSlotBytes, sb = k_base + keys.slot * kSlotBytes;
+                Place<kValueSlots> values;  // of the next outputs
+                // uses so far of either half's weights, queries and output
+                uint32_t p0 = 0, p1 = 0, q0 = 0, q1 = 0, o0 = 0, o1 = 0;
+                auto scores = [&](int s, uint32_t q) {
+                    const uint32_t sa = q_base + q * kSlotBytes, sb = k_base + keys.slot * kSlotBytes;
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         mma_bf16_by(leader, tmem + s * kTile, sw128_desc(sa + kk / 4 * kChunkBytes + kk % 4 * 32),
@@ -537,66 +612,108 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                   sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc(kTile, kTile) | kTransposeB,
                                   !fresh || kk != 0);
                 };
-                // the keys are done with (w: their tile)
-                auto keys_done = [&](const Walk &w) {
+                bool go = true;
+                auto keys_here = [&]() {
+                    go = warp_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
+                    tc_fence_after();
+                    return go;
+                };
+                auto keys_done = [&](bool last) {  // last: of the part, the queries are done with too
                     mma_commit_by(leader, smem_addr(&sh.k_empty[keys.slot]));
-                    if (w.ends()) mma_commit_by(leader, smem_addr(&sh.q_empty));
+                    if (last) mma_commit_by(leader, smem_addr(&sh.q_empty));
                     keys.next();
                 };
-                // the first scores of a part
-                auto begin = [&](const Walk &w) {
-                    const bool two = w.two(a);
-                    WarpWaits<3> x;
-                    x.set(0, &sh.k_full[keys.slot], keys.phase);
-                    x.set(1, &sh.q_full[0], q_count[0]++ & 1);
+                // O of half s: its weights, and the values where nobody has waited for them yet
+                auto outputs = [&](int s, bool look, bool fresh, bool last) {
+                    WarpWaits<4> x;
+                    x.set(0, &sh.p_full[s], (s ? p1 : p0) & 1);
+                    p0 += 1 - s;
+                    p1 += s;
+                    x.none(1);
                     x.none(2);
-                    if (two) x.set(2, &sh.q_full[1], q_count[1]++ & 1);
-                    if (!x.wait(a.wait_limit)) return false;
+                    x.none(3);
+                    if (look) {
+                        x.set(1, &sh.v_full[values.slot], values.phase);
+                        x.set(3, &sh.checked[values.slot], values.phase);
+                    }
+                    if (fresh) {
+                        const uint32_t o = s ? o1 : o0;
+                        if (o) x.set(2, &sh.o_empty[s], (o - 1) & 1);
+                        o0 += 1 - s;
+                        o1 += s;
+                    }
+                    go = x.wait(a.wait_limit);
+                    if (!go) return;
                     tc_fence_after();
-                    scores(0);
-                    if (two) scores(1);
-                    keys_done(w);
-                    return true;
+                    output(s, fresh);
+                    if (last) mma_commit_by(leader, smem_addr(&sh.o_full[s]));
                 };
-                bool go = begin(walk);
-                while (go && walk.left > 0) {
-                    const bool two = walk.two(a), ends = walk.ends(), fresh = walk.fresh;
-                    Walk next = walk;
-                    next.advance(a);
-                    for (int s = 0; go && s < (two ? 2 : 1); ++s) {
-                        WarpWaits<4> x;
-                        x.set(0, &sh.p_full[s], p_count[s]++ & 1);
-                        x.none(1);
-                        x.none(2);
-                        x.none(3);
-                        if (s == 0) {
-                            x.set(1, &sh.v_full[values.slot], values.phase);
-                            x.set(3, &sh.checked[values.slot], values.phase);
+                auto values_done = [&]() {
+                    mma_commit_by(leader, smem_addr(&sh.v_empty[values.slot]));
+                    values.next();
+                };
+                int left = walk.left;
+                for (int part = 0; go && left > 0; ++part) {
+                    // (the producer's notes are there once the part's first keys are)
+                    if (!keys_here()) break;
+                    const volatile PartInfo &info = sh.parts[part % kInfos];
+                    const int tiles = uniform(info.tiles), mode = uniform(info.mode);
+                    left -= tiles;
+                    const bool two = mode == kBoth;
+                    WarpWaits<2> x;
+                    x.set(0, &sh.q_full[0], q0++ & 1);
+                    x.none(1);
+                    if (two) x.set(1, &sh.q_full[1], q1++ & 1);
+                    go = x.wait(a.wait_limit);
+                    if (!go) break;
+                    tc_fence_after();
+                    scores(0, 0);
+                    if (mode == kTurns) {
+                        keys_done(tiles == 1);
+                        if (tiles > 1 && keys_here()) {
+                            scores(1, 0);
+                            keys_done(tiles == 2);
                         }
-                        if (fresh) {
-                            if (o_count[s]) x.set(2, &sh.o_empty[s], (o_count[s] - 1) & 1);
-                            ++o_count[s];
-                        }
-                        go = x.wait(a.wait_limit);
-                        if (!go) break;
-                        tc_fence_after();
-                        output(s, fresh);
-                        if (ends) mma_commit_by(leader, smem_addr(&sh.o_full[s]));
-                        if (s == 1 || !two) mma_commit_by(leader, smem_addr(&sh.v_empty[values.slot]));
-                        if (!ends) {
-                            if (s == 0) {
-                                go = warp_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
-                                if (!go) break;
-                                tc_fence_after();
+                        for (int j = 0; go && j < tiles; ++j) {
+                            const int s = j & 1;
+                            outputs(s, true, j < 2, j + 2 >= tiles);
+                            if (!go) break;
+                            values_done();
+                            if (j + 2 < tiles && keys_here()) {
+                                scores(s, 0);
+                                keys_done(j + 3 == tiles);
                             }
-                            scores(s);
-                            if (s == 1 || !two) keys_done(next);
+                        }
+                    } else {
+                        if (two) scores(1, 1);
+                        keys_done(tiles == 1);
+                        for (int j = 0; go && j < tiles; ++j) {
+                            const bool last = j + 1 == tiles;
+                            outputs(0, true, j == 0, last);
+                            if (!go) break;
+                            if (!two) values_done();
+                            if (!last) {
+                                if (!keys_here()) break;
+                                scores(0, 0);
+                            }
+                            if (two) {
+                                outputs(1, false, j == 0, last);
+                                if (!go) break;
+                                values_done();
+                                if (!last) scores(1, 1);
+                            }
+                            if (!last) keys_done(j + 2 == tiles);
                         }
                     }
-                    values.next();
-                    if (go && ends && next.left > 0) go = begin(next);
-                    walk = next;
                 }
+                // nothing more for the softmax warps (their latest scores' barriers are
+                // complete: their weights were waited for)
+                if (go && lane == 0)
+                    for (int s = 0; s < 2; ++s) {
+                        reinterpret_cast<volatile int &>(sh.tiles[s][(s ? p1 : p0) % kInfos].flags) = kEnd;
+                        mbar_arrive(smem_addr(&sh.s_full[s]));
+                    }
+                __syncwarp();
                 mma_commit_by(leader, smem_addr(&sh.done));
                 ok = warp_wait(&sh.done, 0) && go;
             } else {
@@ -639,215 +756,267 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
             // ---- softmax warpgroups: thread = matrix row
             const int s = warp / 4, w = warp % 4;
-            const int row = w * 32 + lane, token = row / a.group, head = row % a.group;
+            const int row = w * 32 + lane, token = row / a.group;
             const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
             const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + (2 + s) * kTile;
-            uint32_t tiles = 0, parts = 0, joins = 0;  // of this half
-            int part = 0;
-            uint32_t t = 0;
-            while (ok && walk.left > 0) {
-                // ---- a part
-                ++part;
-                const Walk begun = walk;
-                const int tiles_here = min(walk.left, walk.span.tiles - walk.k);
-                if (s == 1 && !walk.two(a)) {
-                    walk.left -= tiles_here - 1;
-                    walk.k += tiles_here - 1;
-                    t += tiles_here;
-                    walk.advance(a);
-                    continue;
+            uint32_t parts = 0, joins = 0;  // of this half
+            int limit = 0;                  // tokens up to the row's own
+            float m = kNoScore, l = 0.0f;
+            for (uint32_t use = 0;; ++use) {
+                if (!warp_wait(&sh.s_full[s], use & 1, a.wait_limit)) {
+                    ok = false;
+                    break;
                 }
-                const int half0 = walk.r0(a) + s * a.tokens, before = walk.ctx - walk.n;
-                const int high = before + min(walk.n, half0 + a.tokens);       // tokens that the last row sees
-                const int r = half0 + token;                                   // row in the stream
-                const int limit = min(before + r + 1, high);                   // tokens up to the row's own
-                float m = kNoScore, l = 0.0f;
-                for (int j = 0; j < tiles_here; ++j, ++t, ++tiles, ++walk.k) {
-                    if (!warp_wait(&sh.s_full[s], tiles & 1, a.wait_limit)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t valid = *reinterpret_cast<volatile uint32_t *>(&sh.valid[t % 8]);
-                    uint32_t x[kTile];
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 32) tmem_ld32_nowait(ts + c, x + c);
-                    tmem_wait_ld();
-                    const int t0 = walk.tile() * kTile;
-                    const bool whole = t0 + kTile <= before + half0 + 1 &&
-                                       (!a.window || t0 + kTile <= a.sinks || t0 >= high - a.window);
-                    if (!whole || valid != 0xFFu) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int base = t0 + 32 * c;
-                            uint32_t see = bits_before(limit, base);
-                            if (a.window) see &= bits_before(a.sinks, base) | ~bits_before(limit - a.window, base);
-                            see &= ((valid >> (2 * c)) & 1 ? 0xFFFFu : 0u) | ((valid >> (2 * c)) & 2 ? 0xFFFF0000u : 0u);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((see >> i) & 1)) x[32 * c + i] = 0xFF800000u;  // -inf
-                        }
-                    }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
-                    const float high_now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-                    if (__any_sync(kFull, high_now > m + kSlack)) {
-                        // (S(t) complete means that the product before it is too)
-                        const float now = fmaxf(m, high_now), f = hw_ex2(m - now);
-                        m = now;
-                        l *= f;
-                        if (j > 0)
-                            for (int c = 0; c < kDim; c += 16) {
-                                uint32_t o[16];
-                                tmem_ld16_nowait(to + c, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st16(to + c, o);
-                            }
-                    }
-                    float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 64) {
-                        uint32_t p[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float p0 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i]), a.scale_log2, -m));
-                            const float p1 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i + 1]), a.scale_log2, -m));
-                            sum[0] += p0;
-                            sum[1] += p1;
-                            p[i] = pack_bf16(p0, p1);
-                        }
-                        tmem_st32(ts + c / 2, p);
-                    }
-                    l += sum[0] + sum[1];
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
+                tc_fence_after();
+                const volatile TileInfo &info = sh.tiles[s][use % kInfos];
+                const int flags = info.flags;
+                if (flags & kEnd) break;
+                if (flags & kFresh) {
+                    const volatile PartInfo *p = &sh.parts[flags >> kPartShift];
+                    const int before = p->ctx - p->n, from = p->r0 + (s == 1 && p->mode == kBoth ? a.tokens : 0);
+                    limit = before + min(from + token + 1, min(p->n, from + a.tokens));
+                    m = kNoScore;
+                    l = 0.0f;
                 }
-                if (!ok) break;
-                // ---- the part's end: the rows, or what other CTAs' parts are joined with
+                uint32_t x[kTile];
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32) tmem_ld32_nowait(ts + c, x + c);
+                tmem_wait_ld();
+                if (flags & kMasked) {
+                    const int t0 = info.t0;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int base = t0 + 32 * c;
+                        uint32_t see = bits_before(limit, base);
+                        if (a.window) see &= bits_before(a.sinks, base) | ~bits_before(limit - a.window, base);
+                        see &= ((flags >> (2 * c)) & 1 ? 0xFFFFu : 0u) | ((flags >> (2 * c)) & 2 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((see >> i) & 1)) x[32 * c + i] = 0xFF800000u;  // -inf
+                    }
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
+                const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                if (__any_sync(kFull, high > m + kSlack)) {
+                    // (the scores' being complete means that the product before them is too)
+                    const float now = fmaxf(m, high), f = hw_ex2(m - now);
+                    m = now;
+                    l *= f;
+                    if (!(flags & kFresh))
+                        for (int c = 0; c < kDim; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_nowait(to + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st16(to + c, o);
+                        }
+                }
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < kTile; c += 64) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float p0 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i]), a.scale_log2, -m));
+                        const float p1 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i + 1]), a.scale_log2, -m));
+                        sum[0] += p0;
+                        sum[1] += p1;
+                        p[i] = pack_bf16(p0, p1);
+                    }
+                    tmem_st32(ts + c / 2, p);
+                }
+                l += sum[0] + sum[1];
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
+                if (!(flags & kLast)) continue;
+                // ---- the part's end: the rows, or what is joined with other parts
                 ok = warp_wait(&sh.o_full[s], parts & 1, a.wait_limit);
                 if (!ok) break;
                 ++parts;
                 tc_fence_after();
-                const Shares shares = shares_of(ranges, begun.s0, begun.span.tiles);
-                const bool odd = *reinterpret_cast<volatile int *>(&sh.odd[part % 4]) == part;
-                const bool real = token < a.tokens && r < begun.n;
-                __nv_bfloat16 *out = a.out + (static_cast<size_t>(begun.first + r) * a.Hq + begun.g * a.group + head) * kDim;
-                if (shares.more == 0) {
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // no token left: zeros
+                const PartInfo &p = sh.parts[flags >> kPartShift];
+                const bool turns = p.mode == kTurns;
+                const int r = p.r0 + (s == 1 && !turns ? a.tokens : 0) + token;  // row in the stream
+                const bool odd = *reinterpret_cast<volatile int *>(&sh.odd[p.number % 4]) == p.number;
+                const bool real = token < a.tokens && r < p.n;
+                const int first = p.shares, count = (p.more + 1) * (turns ? 2 : 1);
+                __nv_bfloat16 *out = a.out + (static_cast<size_t>(p.first + r) * a.Hq + p.g * a.group + row % a.group) * kDim;
+                // (with both halves' parts in turns: half 1's tiles are the odd ones)
+                const int step = turns ? 2 : 1, j0 = turns ? s : 0;
+                if (count == 1) {
+                    const float inv = inverse(l);
                     for (int c = 0; c < kDim; c += 32) {
                         float f[32];
                         tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
                         tmem_wait_ld();
-                        if (odd && real) add_odd(a, begun, tiles_here, limit, c, f);
-                        if (real)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                reinterpret_cast<uint4 *>(out + c)[i] =
-                                    make_uint4(pack_bf16(f[8 * i] * inv, f[8 * i + 1] * inv),
-                                               pack_bf16(f[8 * i + 2] * inv, f[8 * i + 3] * inv),
-                                               pack_bf16(f[8 * i + 4] * inv, f[8 * i + 5] * inv),
-                                               pack_bf16(f[8 * i + 6] * inv, f[8 * i + 7] * inv));
+                        if (odd && real) add_odd(a, p, step, j0, limit, c, f);
+                        if (real) store_row(out + c, f, inv);
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_addr(&sh.o_empty[s]));
-                } else {
-                    // a part's slot: [first part of a segment or a later one][half], [32][128 rows][4] and m, l
-                    auto slot = [&](int c) {
-                        return a.part + static_cast<size_t>((c * 2 + (c == shares.first ? 0 : 1)) * 2 + s) * kPartFloats;
-                    };
-                    float *mine = slot(blockIdx.x);
-                    for (int c = 0; c < kDim; c += 32) {
-                        float f[32];
-                        tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
-                        tmem_wait_ld();
-                        if (odd && real) add_odd(a, begun, tiles_here, limit, c, f);
-                        if (real)
+                    continue;
+                }
+                const bool begins = static_cast<int>(blockIdx.x) == first || p.more == 0, alone = turns && p.tiles == 1;
+                const int from = p.more == 0 ? static_cast<int>(blockIdx.x) : first;  // the segment's first CTA
+                float *mine = part_slot(a.part, blockIdx.x, begins, s);
+                for (int c = 0; c < kDim; c += 32) {
+                    float f[32];
+                    tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
+                    tmem_wait_ld();
+                    if (odd && real) add_odd(a, p, step, j0, limit, c, f);
+                    if (real)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<float4 *>(mine)[(c / 4 + i) * kTile + row] =
-                                    make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-                    }
-                    if (real) {
-                        mine[kTile * kDim + row] = m;
-                        mine[kTile * kDim + kTile + row] = l;
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(smem_addr(&sh.o_empty[s]));
-                        mbar_arrive(smem_addr(&sh.stored[s]));
-                    }
-                    // (bounded waits, as everywhere: a warp may have given up)
-                    if (w == 0) ok = warp_wait(&sh.stored[s], joins & 1, a.wait_limit);
-                    if (row == 0 && ok) {
-                        int old;
-                        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
-                                     : "=r"(old)
-                                     : "l"(a.tickets + 2 * shares.first + s)
-                                     : "memory");
-                        sh.last[s] = old == shares.more;
-                        if (old == shares.more) a.tickets[2 * shares.first + s] = 0;
-                        mbar_arrive(smem_addr(&sh.told[s]));
-                    }
-                    __syncwarp();
-                    ok = ok && warp_wait(&sh.told[s], joins & 1, a.wait_limit);
-                    ++joins;
-                    if (!ok) break;
-                    if (*reinterpret_cast<volatile int *>(&sh.last[s]) && real) {
-                        float top = kNoScore, sum = 0.0f;
-                        for (int c = 0; c <= shares.more; ++c) top = fmaxf(top, __ldcg(slot(shares.first + c) + kTile * kDim + row));
-                        for (int c = 0; c <= shares.more; ++c) {
-                            const float *p = slot(shares.first + c) + kTile * kDim + row;
-                            sum = fmaf(hw_ex2(__ldcg(p) - top), __ldcg(p + kTile), sum);
-                        }
-                        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-                        for (int d = 0; d < kDim; d += 32) {
-                            float4 o[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            for (int c = 0; c <= shares.more; ++c) {
-                                const float *p = slot(shares.first + c);
-                                const float f = hw_ex2(__ldcg(p + kTile * kDim + row) - top);
-                                float4 x[8];
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) x[i] = __ldcg(reinterpret_cast<const float4 *>(p) + (d / 4 + i) * kTile + row);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    o[i].x = fmaf(x[i].x, f, o[i].x);
-                                    o[i].y = fmaf(x[i].y, f, o[i].y);
-                                    o[i].z = fmaf(x[i].z, f, o[i].z);
-                                    o[i].w = fmaf(x[i].w, f, o[i].w);
-                                }
-                            }
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                reinterpret_cast<uint4 *>(out + d)[i] =
-                                    make_uint4(pack_bf16(o[2 * i].x * inv, o[2 * i].y * inv),
-                                               pack_bf16(o[2 * i].z * inv, o[2 * i].w * inv),
-                                               pack_bf16(o[2 * i + 1].x * inv, o[2 * i + 1].y * inv),
-                                               pack_bf16(o[2 * i + 1].z * inv, o[2 * i + 1].w * inv));
-                        }
+                        for (int i = 0; i < 8; ++i)
+                            reinterpret_cast<float4 *>(mine)[(c / 4 + i) * kTile + row] =
+                                make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                }
+                if (real) {
+                    mine[kTile * kDim + row] = m;
+                    mine[kTile * kDim + kTile + row] = l;
+                    if (alone) {  // no tile was half 1's
+                        mine[kPartFloats + kTile * kDim + row] = kNoScore;
+                        mine[kPartFloats + kTile * kDim + kTile + row] = 0.0f;
                     }
                 }
-                // (the walk stands behind the part's last tile)
-                --walk.k;
-                walk.left -= tiles_here - 1;
-                walk.advance(a);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.o_empty[s]));
+                if (count > kJoinHere) {
+                    if (begins && row == 0 && (s == 0 || !turns))
+                        sh.jobs[s] = make_int4(min(p.n - (r - token), a.tokens) * a.group, p.first + r, p.g, turns ? -count : count);
+                    continue;
+                }
+                if (lane == 0) mbar_arrive(smem_addr(&sh.stored[s]));
+                // (bounded waits, as everywhere: a warp may have given up)
+                if (w == 0) ok = warp_wait(&sh.stored[s], joins & 1, a.wait_limit);
+                if (row == 0 && ok) {
+                    int old;
+                    int32_t *ticket = a.tickets + 2 * from + (turns ? 0 : s);
+                    const int add = alone ? 2 : 1;
+                    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(ticket), "r"(add) : "memory");
+                    sh.last[s] = old + add == count;
+                    if (old + add == count) *ticket = 0;
+                    mbar_arrive(smem_addr(&sh.told[s]));
+                }
+                __syncwarp();
+                ok = ok && warp_wait(&sh.told[s], joins & 1, a.wait_limit);
+                ++joins;
+                if (!ok) break;
+                if (!*reinterpret_cast<volatile int *>(&sh.last[s]) || !real) continue;
+                float best = kNoScore, total = 0.0f;
+                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, from, i, turns, s) + kTile * kDim + row));
+                for (int i = 0; i < count; ++i) {
+                    const float *q = segment_part(a.part, from, i, turns, s) + kTile * kDim + row;
+                    total = fmaf(hw_ex2(__ldcg(q) - best), __ldcg(q + kTile), total);
+                }
+                const float inv = inverse(total);
+                for (int d = 0; d < kDim; d += 32) {
+                    float o[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+                    for (int i = 0; i < count; ++i) {
+                        const float *q = segment_part(a.part, from, i, turns, s);
+                        const float mq = __ldcg(q + kTile * kDim + row);
+                        const float f = hw_ex2(mq - best);
+                        if (turns && mq == kNoScore && __ldcg(q + kTile * kDim + kTile + row) == 0.0f) continue;  // (nothing there)
+                        float4 x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = __ldcg(reinterpret_cast<const float4 *>(q) + (d / 4 + e) * kTile + row);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            o[4 * e] = fmaf(x[e].x, f, o[4 * e]);
+                            o[4 * e + 1] = fmaf(x[e].y, f, o[4 * e + 1]);
+                            o[4 * e + 2] = fmaf(x[e].z, f, o[4 * e + 2]);
+                            o[4 * e + 3] = fmaf(x[e].w, f, o[4 * e + 3]);
+                        }
+                    }
+                    store_row(out + d, o, inv);
+                }
             }
         }
         if (!ok) flag_error(a.err, TTS_ERRBIT_TIMEOUT);
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x < 2) a.jobs[2 * blockIdx.x + threadIdx.x] = sh.jobs[threadIdx.x];
     if (warp == 10) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- the join
+
+// Segments of more than kJoinHere parts: one CTA's threads would read them at a
+// few bytes a cycle (61 rows of 8 KV heads in 19 parts of 62 KB each: 54 us), so
+// a second kernel spreads the work over every SM, 128 rows of 8 dimensions an
+// item.  It always runs, and finds that there is nothing to do by looking at one
+// word a CTA and half.
+constexpr int kJoinThreads = 256, kJoinItems = kDim / 8;
+
+__global__ void __launch_bounds__(kJoinThreads)
+prompt_join_kernel(float *parts, const int4 *jobs, int ctas, __nv_bfloat16 *out, int Hq, int group) {
+    __shared__ int found[kJoinThreads / 32 + 1];
+    pdl_wait_prerequisites();
+    pdl_allow_dependents();
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int before = 0;  // jobs of the entries seen so far
+    for (int base = 0; base < 2 * ctas; base += kJoinThreads) {
+        const int e = base + threadIdx.x;
+        const int mine = e < 2 * ctas ? __ldcg(&jobs[e].x) : 0;
+        const unsigned any = __ballot_sync(kFull, mine != 0);
+        if (lane == 0) found[warp] = __popc(any);
+        __syncthreads();
+        int total = 0;
+        for (int w = 0; w < kJoinThreads / 32; ++w) total += found[w];
+        // this CTA's items of these entries
+        const int lo = before * kJoinItems, hi = (before + total) * kJoinItems;
+        for (int item = blockIdx.x + (max(lo - static_cast<int>(blockIdx.x), 0) + gridDim.x - 1) / gridDim.x * gridDim.x; item < hi;
+             item += gridDim.x) {
+            // the entry of the job: the warp that found it, then its lane
+            __shared__ int entry;
+            int nth = item / kJoinItems - before;
+            for (int w = 0; w < warp; ++w) nth -= found[w];
+            if (mine != 0 && nth == __popc(any & ((1u << lane) - 1u))) entry = e;
+            __syncthreads();
+            const int4 job = __ldcg(jobs + entry);
+            const int s = entry % 2, first = entry / 2, row = threadIdx.x % kTile, d = item % kJoinItems * 8 + threadIdx.x / kTile * 4;
+            const bool turns = job.w < 0;
+            const int count = abs(job.w);
+            if (row < job.x) {
+                float best = kNoScore;
+#pragma unroll 8
+                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(parts, first, i, turns, s) + kTile * kDim + row));
+                float total_l = 0.0f;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                for (int i = 0; i < count; ++i) {
+                    const float *q = segment_part(parts, first, i, turns, s);
+                    const float mq = __ldcg(q + kTile * kDim + row), lq = __ldcg(q + kTile * kDim + kTile + row), f = hw_ex2(mq - best);
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + d / 4 * kTile + row);
+                    const bool none = turns && mq == kNoScore && lq == 0.0f;  // (nothing there)
+                    total_l = fmaf(f, lq, total_l);
+                    o.x = none ? o.x : fmaf(x.x, f, o.x);
+                    o.y = none ? o.y : fmaf(x.y, f, o.y);
+                    o.z = none ? o.z : fmaf(x.z, f, o.z);
+                    o.w = none ? o.w : fmaf(x.w, f, o.w);
+                }
+                const float inv = inverse(total_l);
+                uint32_t *dst = reinterpret_cast<uint32_t *>(
+                    out + (static_cast<size_t>(job.y + row / group) * Hq + job.z * group + row % group) * kDim + d);
+                dst[0] = pack_bf16(o.x * inv, o.y * inv);
+                dst[1] = pack_bf16(o.z * inv, o.w * inv);
+            }
+            __syncthreads();
+        }
+        before += total;
+        __syncthreads();
     }
 }
 
@@ -864,6 +1033,9 @@ bool prompt_shape_ok(int B, int T, int Hq, int Hkv) {
 
 size_t prompt_part_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 4 * kPartFloats * sizeof(float), 256); }
 size_t prompt_ticket_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 2 * sizeof(int32_t), 256); }
+size_t prompt_job_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 2 * sizeof(int4), 256); }
+// parts, jobs, and last the tickets
+size_t prompt_workspace_bytes() { return prompt_part_bytes() + prompt_job_bytes() + prompt_ticket_bytes(); }
 
 }  // namespace
 }  // namespace tts
@@ -874,7 +1046,7 @@ extern "C" size_t tts_prompt_attn_workspace_size(int32_t B, int32_t num_rows, in
     if (!prompt_shape_ok(B, num_rows, num_q_heads, num_kv_heads) || head_dim != kDim || B > kMaxStreams ||
         num_q_heads / num_kv_heads > kTile)
         return 0;
-    return prompt_part_bytes() + prompt_ticket_bytes();
+    return prompt_workspace_bytes();
 }
 
 extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
@@ -897,7 +1069,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     if (pool_rows >= (1ULL << 31)) return TTS_ERR_UNSUPPORTED;
     if (!aligned16(cache->k_pool) || !aligned16(cache->v_pool) || !aligned16(d_q) || !aligned16(d_out)) return TTS_ERR_INVALID;
     if (B == 0 || num_rows == 0) return TTS_OK;
-    if (!d_ws || ws_bytes < prompt_part_bytes() + prompt_ticket_bytes() || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0)
+    if (!d_ws || ws_bytes < prompt_workspace_bytes() || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0)
         return TTS_ERR_WORKSPACE;
 
     PromptArgs a{};
@@ -921,7 +1093,8 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     a.out = static_cast<__nv_bfloat16 *>(d_out);
     a.ctas = prompt_ctas();
     a.part = static_cast<float *>(d_ws);
-    a.tickets = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + prompt_part_bytes());
+    a.jobs = reinterpret_cast<int4 *>(static_cast<uint8_t *>(d_ws) + prompt_part_bytes());
+    a.tickets = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + prompt_part_bytes() + prompt_job_bytes());
     a.zero_row = static_cast<int>(pool_rows);
     a.err = d_err;
     a.wait_limit = thread_opts().wait_limit;
@@ -936,6 +1109,10 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
         !make_tma_2d_bf16(&map_v, cache->v_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64))
         return TTS_ERR_CUDA;
     if (!allow_smem(prompt_attn_kernel, kSmem)) return TTS_ERR_CUDA;
-    return launch_kernel(prompt_attn_kernel, dim3(a.ctas), dim3(kThreads), kSmem,
-                         {static_cast<cudaStream_t>(stream), thread_pdl()}, map_q, map_k, map_v, a);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const int rc = launch_kernel(prompt_attn_kernel, dim3(a.ctas), dim3(kThreads), kSmem, {cs, thread_pdl()}, map_q, map_k, map_v, a);
+    // no segment has more than 2 * kSnap tiles: none is split
+    if (rc != TTS_OK || max_blocks_per_seq <= 2 * kSnap * kTile / TTS_BLOCK_TOKENS) return rc;
+    return launch_kernel(prompt_join_kernel, dim3(a.ctas), dim3(kJoinThreads), 0, {cs, true}, a.part, a.jobs, a.ctas, a.out,
+                         a.Hq, a.group);
 }
