@@ -103,6 +103,17 @@ struct WarpWaits {
         __syncwarp();
         return all;
     }
+    // Polls until all have: where a wait stands in a chain of short steps
+    // (try_wait's wake-up takes a few hundred cycles).
+    __device__ __forceinline__ bool spin(long long limit = kWaitLimitCycles) const {
+        if (poll()) return true;
+        const long long t0 = clock64();
+        for (uint32_t n = 1;; ++n) {
+            if (poll()) return true;
+            // (one answer for the warp: the lanes' clocks may differ)
+            if ((n & 63u) == 0 && __any_sync(0xFFFFFFFFu, clock64() - t0 > limit)) return false;
+        }
+    }
     __device__ __forceinline__ bool wait(long long limit = kWaitLimitCycles) const {
         if (poll()) return true;
         bool all = true;

@@ -45,7 +45,8 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kDim = 128;
 constexpr int kTile = 128;                  // tokens a tile, matrix rows a half
 constexpr int kChunkBytes = kTile * 128;    // [128 rows][64 values], 128-byte swizzle
-constexpr int kSlotBytes = 2 * kChunkBytes; // a tile of keys or values
+constexpr int kSlotBytes = 2 * kChunkBytes; // a tile of keys, or of values block by block: [8][2][16 tokens][64 values]
+constexpr int kBlockBytes = 4096;           // a block's values of a head
 constexpr int kKeySlots = 2, kValueSlots = 3;  // (keys are done with half a tile before the values)
 constexpr int kThreads = 384;               // two softmax warpgroups; producer, issuer, two checkers
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72, kStartRegs = 168;
@@ -216,7 +217,7 @@ constexpr int kInfos = 8;  // (the producer is at most four tiles ahead)
 
 struct PromptShared {
     uint64_t k_full[kKeySlots], k_empty[kKeySlots], v_full[kValueSlots], v_empty[kValueSlots], checked[kValueSlots];
-    uint64_t q_full[2], q_empty, s_full[2], p_full[2], o_full[2], o_empty[2], stored[2], told[2], done;
+    uint64_t q_full[2], q_empty, s_full[2], p_full[2][2], o_full[2], o_empty[2], stored[2], told[2], done;
     __align__(16) PartInfo parts[kInfos];
     TileInfo tiles[2][kInfos];  // by use of the half
     int4 jobs[2];
@@ -224,7 +225,7 @@ struct PromptShared {
     int odd[4];            // number of the part whose tiles held values that are not finite, by number % 4
     int last[2];           // whether the half's part was the last one
     long long scan[2][kThreads / 32];
-    int b, i, g, k, s0, from, to, workers, q, rem;
+    int b, i, g, k, s0, first, n, ctx, from, to, q, rem;
 };
 constexpr int kSmem = (2 + kKeySlots + kValueSlots) * kSlotBytes + static_cast<int>(sizeof(PromptShared));
 static_assert(kSmem <= 227 * 1024);
@@ -318,7 +319,6 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
     const int c = blockIdx.x;
     Ranges ranges{W ? T / W : 0, W ? T % W : 0};
     if (threadIdx.x == 0) {
-        sh.workers = W;
         sh.q = ranges.q;
         sh.rem = ranges.rem;
         if (c >= W) sh.from = sh.to = 0;
@@ -345,6 +345,9 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
                     sh.g = g;
                     sh.k = k;
                     sh.s0 = s0;
+                    sh.first = streams[b].x;
+                    sh.n = streams[b].y;
+                    sh.ctx = streams[b].z;
                 }
             }
             at_tile = end;
@@ -363,11 +366,46 @@ __device__ __forceinline__ Shares shares_of(const Ranges &r, int s0, int tiles) 
     return {lo - 1, max(0, hi - lo + 1)};
 }
 
+// A block's rows, both halves (make_tma_rows_in_halves_bf16), by a converged warp's leader.
+__device__ __forceinline__ void tma_load_rows_by(uint32_t leader, uint32_t dst, const CUtensorMap *map, int y, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %2}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(bar), "r"(leader)
+        : "memory");
+}
+
 // ------------------------------------------------------------- the softmax
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
+}
+// Two fp32 operations an instruction, and the largest of three.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
 }
 // Bits of the tokens of word w (32 tokens from `base` on) before token t.
 __device__ __forceinline__ uint32_t bits_before(int t, int base) {
@@ -445,7 +483,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.q_full[i]), 1);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.p_full[i]), 4);
+            mbar_init(smem_addr(&sh.p_full[i][0]), 4);
+            mbar_init(smem_addr(&sh.p_full[i][1]), 4);
             mbar_init(smem_addr(&sh.o_full[i]), 1);
             mbar_init(smem_addr(&sh.o_empty[i]), 4);
             mbar_init(smem_addr(&sh.stored[i]), 4);
@@ -488,7 +527,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         walk.g = uniform(sh.g);
         walk.k = uniform(sh.k);
         walk.s0 = uniform(sh.s0);
-        walk.seek(a);
+        walk.first = uniform(sh.first);
+        walk.n = uniform(sh.n);
+        walk.ctx = uniform(sh.ctx);
         walk.span = span_of(a, walk.n, walk.ctx, walk.i);
         walk.settle(a);
         if (warp >= 8) {
@@ -507,14 +548,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 };
                 int id, id_next = -1;
                 bool seen = lookup(walk, id), seen_next = false;
-                auto load = [&](const CUtensorMap *map, int y, uint64_t *full, uint64_t *empty, uint32_t base, auto &at,
-                                uint32_t more) {
+                const uint32_t leader = elect_leader();
+                auto room = [&](uint64_t *full, uint64_t *empty, auto &at, uint32_t bytes) {
                     if (at.again && !warp_wait(&empty[at.slot], at.phase ^ 1, a.wait_limit)) return false;
-                    const uint32_t bar = smem_addr(&full[at.slot]), to = base + at.slot * kSlotBytes;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, kSlotBytes + more);
-                    __syncwarp();
-                    if (lane < 16) tma_load_2d(to + lane / 8 * kChunkBytes + lane % 8 * 2048, map, lane / 8 * 64, y, bar);
-                    at.next();
+                    mbar_expect_tx_by(leader, smem_addr(&full[at.slot]), bytes);
                     return true;
                 };
                 int uses[2] = {0, 0}, j = 0, mode = 0, tiles = 0, note = 0;  // j: tile of the part
@@ -553,8 +590,18 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     Walk next = walk;
                     next.advance(a);
                     if (next.left > 0) seen_next = lookup(next, id_next);
-                    ok = load(&map_k, y, sh.k_full, sh.k_empty, k_base, keys, a.stall && !begun ? 16 : 0);
+                    int ys[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ys[i] = __shfl_sync(kFull, y, i);
+                    ok = room(sh.k_full, sh.k_empty, keys, kSlotBytes + (a.stall && !begun ? 16 : 0));
                     if (!ok) break;
+                    {
+                        const uint32_t bar = smem_addr(&sh.k_full[keys.slot]), to = k_base + keys.slot * kSlotBytes;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            tma_load_2d_by(leader, to + i / 8 * kChunkBytes + i % 8 * 2048, &map_k, i / 8 * 64, ys[i % 8], bar);
+                        keys.next();
+                    }
                     if (walk.fresh) {
                         ok = part == 0 || warp_wait(&sh.q_empty, (part - 1) & 1, a.wait_limit);
                         if (!ok) break;
@@ -576,7 +623,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         __syncwarp();
                         ++part;
                     }
-                    ok = load(&map_v, y, sh.v_full, sh.v_empty, v_base, values, 0);
+                    ok = room(sh.v_full, sh.v_empty, values, kSlotBytes);
+                    if (!ok) break;
+                    {
+                        const uint32_t bar = smem_addr(&sh.v_full[values.slot]), to = v_base + values.slot * kSlotBytes;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) tma_load_rows_by(leader, to + i * kBlockBytes, &map_v, ys[i], bar);
+                        values.next();
+                    }
                     walk = next;
                     id = id_next;
                     seen = seen_next;
@@ -604,17 +658,19 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                     sw128_desc(sb + kk / 4 * kChunkBytes + kk % 4 * 32), mma_idesc(kTile, kTile), kk != 0);
                     mma_commit_by(leader, smem_addr(&sh.s_full[s]));
                 };
-                auto output = [&](int s, bool fresh) {
+                auto output = [&](int s, int half, bool fresh) {  // of 64 tokens
                     const uint32_t sb = v_base + values.slot * kSlotBytes;
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
+                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
                         mma_ts_by(leader, tmem + (2 + s) * kTile, tmem + s * kTile + kk * 8,
-                                  sw128_mn_desc(sb + kk * 2048, kChunkBytes), mma_idesc(kTile, kTile) | kTransposeB,
+                                  sw128_mn_desc(sb + kk * kBlockBytes, kBlockBytes / 2), mma_idesc(kTile, kTile) | kTransposeB,
                                   !fresh || kk != 0);
                 };
                 bool go = true;
                 auto keys_here = [&]() {
-                    go = warp_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
+                    WarpWaits<1> x;
+                    x.set(0, &sh.k_full[keys.slot], keys.phase);
+                    go = x.spin(a.wait_limit);
                     tc_fence_after();
                     return go;
                 };
@@ -626,7 +682,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 // O of half s: its weights, and the values where nobody has waited for them yet
                 auto outputs = [&](int s, bool look, bool fresh, bool last) {
                     WarpWaits<4> x;
-                    x.set(0, &sh.p_full[s], (s ? p1 : p0) & 1);
+                    const uint32_t phase = (s ? p1 : p0) & 1;
+                    x.set(0, &sh.p_full[s][0], phase);
                     p0 += 1 - s;
                     p1 += s;
                     x.none(1);
@@ -642,10 +699,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         o0 += 1 - s;
                         o1 += s;
                     }
-                    go = x.wait(a.wait_limit);
+                    go = x.spin(a.wait_limit);
                     if (!go) return;
                     tc_fence_after();
-                    output(s, fresh);
+                    output(s, 0, fresh);
+                    WarpWaits<1> y;
+                    y.set(0, &sh.p_full[s][1], phase);
+                    go = y.spin(a.wait_limit);
+                    if (!go) return;
+                    tc_fence_after();
+                    output(s, 1, false);
                     if (last) mma_commit_by(leader, smem_addr(&sh.o_full[s]));
                 };
                 auto values_done = [&]() {
@@ -737,7 +800,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             for (const uint32_t w : {x.x, x.y, x.z, x.w})
                                 bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
                             if (!bad) continue;
-                            const int t = t0 + e / 8 % kTile;
+                            const int t = t0 + e / (kBlockBytes / 16) * TTS_BLOCK_TOKENS + e / 8 % TTS_BLOCK_TOKENS;
                             odd = odd || (t < walk.span.high && (!a.window || t < a.sinks || t >= first_limit - a.window));
                             uint16_t *h = reinterpret_cast<uint16_t *>(v + e * 16);
                             for (int i = 0; i < 8; ++i)
@@ -797,8 +860,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < kTile; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(x[i]));
-                const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                for (int i = 0; i < kTile; i += 2)
+                    top[i / 2 % 4] = max3(top[i / 2 % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
                 if (__any_sync(kFull, high > m + kSlack)) {
                     // (the scores' being complete means that the product before them is too)
                     const float now = fmaxf(m, high), f = hw_ex2(m - now);
@@ -814,25 +878,30 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             tmem_st16(to + c, o);
                         }
                 }
-                float sum[2] = {0.0f, 0.0f};
+                // (the first 64 tokens' product starts while the others' weights are computed)
+                uint64_t sum[2] = {0, 0};
+                const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), minus2 = pack2(-m, -m);
 #pragma unroll
                 for (int c = 0; c < kTile; c += 64) {
                     uint32_t p[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
-                        const float p0 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i]), a.scale_log2, -m));
-                        const float p1 = hw_ex2(fmaf(__uint_as_float(x[c + 2 * i + 1]), a.scale_log2, -m));
-                        sum[0] += p0;
-                        sum[1] += p1;
+                        float p0, p1;
+                        unpack2(fma2(pack2(__uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1])), scale2, minus2), p0, p1);
+                        p0 = hw_ex2(p0);
+                        p1 = hw_ex2(p1);
+                        sum[i % 2] = add2(sum[i % 2], pack2(p0, p1));
                         p[i] = pack_bf16(p0, p1);
                     }
                     tmem_st32(ts + c / 2, p);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s][c / 64]));
                 }
-                l += sum[0] + sum[1];
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
+                float sum0, sum1;
+                unpack2(add2(sum[0], sum[1]), sum0, sum1);
+                l += sum0 + sum1;
                 if (!(flags & kLast)) continue;
                 // ---- the part's end: the rows, or what is joined with other parts
                 ok = warp_wait(&sh.o_full[s], parts & 1, a.wait_limit);
@@ -956,16 +1025,18 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 // Segments of more than kJoinHere parts: one CTA's threads would read them at a
 // few bytes a cycle (61 rows of 8 KV heads in 19 parts of 62 KB each: 54 us), so
 // a second kernel spreads the work over every SM, 128 rows of 8 dimensions an
-// item.  It always runs, and finds that there is nothing to do by looking at one
+// item, four threads a row.  It always runs, and finds that there is nothing to do by looking at one
 // word a CTA and half.
-constexpr int kJoinThreads = 256, kJoinItems = kDim / 8;
+constexpr int kJoinThreads = 512, kJoinItems = kDim / 8, kJoinGroups = kJoinThreads / kTile;
 
 __global__ void __launch_bounds__(kJoinThreads)
 prompt_join_kernel(float *parts, const int4 *jobs, int ctas, __nv_bfloat16 *out, int Hq, int group) {
-    __shared__ int found[kJoinThreads / 32 + 1];
+    __shared__ int found[kJoinThreads / 32], entry;
+    __shared__ float some[kJoinGroups][10][kTile];  // m, l and 8 dimensions of each group's parts
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int row = threadIdx.x % kTile, mine_of = threadIdx.x / kTile;
     int before = 0;  // jobs of the entries seen so far
     for (int base = 0; base < 2 * ctas; base += kJoinThreads) {
         const int e = base + threadIdx.x;
@@ -975,43 +1046,78 @@ prompt_join_kernel(float *parts, const int4 *jobs, int ctas, __nv_bfloat16 *out,
         __syncthreads();
         int total = 0;
         for (int w = 0; w < kJoinThreads / 32; ++w) total += found[w];
-        // this CTA's items of these entries
-        const int lo = before * kJoinItems, hi = (before + total) * kJoinItems;
-        for (int item = blockIdx.x + (max(lo - static_cast<int>(blockIdx.x), 0) + gridDim.x - 1) / gridDim.x * gridDim.x; item < hi;
-             item += gridDim.x) {
+        // this CTA's items (job, 8 dimensions) of these entries
+        const int lo = before * kJoinItems, hi = (before + total) * kJoinItems, grid = gridDim.x, me = blockIdx.x;
+        for (int item = me + (max(lo - me, 0) + grid - 1) / grid * grid; item < hi; item += grid) {
             // the entry of the job: the warp that found it, then its lane
-            __shared__ int entry;
             int nth = item / kJoinItems - before;
             for (int w = 0; w < warp; ++w) nth -= found[w];
             if (mine != 0 && nth == __popc(any & ((1u << lane) - 1u))) entry = e;
             __syncthreads();
             const int4 job = __ldcg(jobs + entry);
-            const int s = entry % 2, first = entry / 2, row = threadIdx.x % kTile, d = item % kJoinItems * 8 + threadIdx.x / kTile * 4;
-            const bool turns = job.w < 0;
+            const int s = entry % 2, first = entry / 2, d = item % kJoinItems * 8;
+            const bool turns = job.w < 0, real = row < job.x;
             const int count = abs(job.w);
-            if (row < job.x) {
-                float best = kNoScore;
-#pragma unroll 8
-                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(parts, first, i, turns, s) + kTile * kDim + row));
-                float total_l = 0.0f;
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-                for (int i = 0; i < count; ++i) {
+            // a thread: parts mine_of, mine_of + 4, ... of a row
+            float best = kNoScore, l = 0.0f, o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = 0.0f;
+            constexpr int kAhead = 5;
+            for (int i0 = mine_of; real && i0 < count; i0 += kAhead * kJoinGroups) {
+                float mq[kAhead], lq[kAhead];
+                float4 x[kAhead][2];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int i = i0 + u * kJoinGroups;
+                    mq[u] = kNoScore;
+                    lq[u] = 0.0f;
+                    x[u][0] = x[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i >= count) continue;
                     const float *q = segment_part(parts, first, i, turns, s);
-                    const float mq = __ldcg(q + kTile * kDim + row), lq = __ldcg(q + kTile * kDim + kTile + row), f = hw_ex2(mq - best);
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(q) + d / 4 * kTile + row);
-                    const bool none = turns && mq == kNoScore && lq == 0.0f;  // (nothing there)
-                    total_l = fmaf(f, lq, total_l);
-                    o.x = none ? o.x : fmaf(x.x, f, o.x);
-                    o.y = none ? o.y : fmaf(x.y, f, o.y);
-                    o.z = none ? o.z : fmaf(x.z, f, o.z);
-                    o.w = none ? o.w : fmaf(x.w, f, o.w);
+                    mq[u] = __ldcg(q + kTile * kDim + row);
+                    lq[u] = __ldcg(q + kTile * kDim + kTile + row);
+                    x[u][0] = __ldcg(reinterpret_cast<const float4 *>(q) + d / 4 * kTile + row);
+                    x[u][1] = __ldcg(reinterpret_cast<const float4 *>(q) + (d / 4 + 1) * kTile + row);
                 }
-                const float inv = inverse(total_l);
-                uint32_t *dst = reinterpret_cast<uint32_t *>(
-                    out + (static_cast<size_t>(job.y + row / group) * Hq + job.z * group + row % group) * kDim + d);
-                dst[0] = pack_bf16(o.x * inv, o.y * inv);
-                dst[1] = pack_bf16(o.z * inv, o.w * inv);
+                float now = best;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) now = fmaxf(now, mq[u]);
+                const float f0 = hw_ex2(best - now);
+                best = now;
+                l *= f0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] *= f0;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    // (a part without a tile of this half has no weights, and nothing in o)
+                    const float f = hw_ex2(mq[u] - now);
+                    const bool none = mq[u] == kNoScore && lq[u] == 0.0f;
+                    const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+                    l = fmaf(f, lq[u], l);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = none ? o[i] : fmaf(f, v[i], o[i]);
+                }
+            }
+            some[mine_of][0][row] = best;
+            some[mine_of][1][row] = l;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) some[mine_of][2 + i][row] = o[i];
+            __syncthreads();
+            if (mine_of == 0 && real) {
+                float top = kNoScore, sum = 0.0f, r[8];
+                for (int k = 0; k < kJoinGroups; ++k) top = fmaxf(top, some[k][0][row]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = 0.0f;
+                for (int k = 0; k < kJoinGroups; ++k) {
+                    const float f = hw_ex2(some[k][0][row] - top);
+                    sum = fmaf(f, some[k][1][row], sum);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r[i] = fmaf(f, some[k][2 + i][row], r[i]);
+                }
+                const float inv = inverse(sum);
+                *reinterpret_cast<uint4 *>(out + (static_cast<size_t>(job.y + row / group) * Hq + job.z * group + row % group) * kDim + d) =
+                    make_uint4(pack_bf16(r[0] * inv, r[1] * inv), pack_bf16(r[2] * inv, r[3] * inv),
+                               pack_bf16(r[4] * inv, r[5] * inv), pack_bf16(r[6] * inv, r[7] * inv));
             }
             __syncthreads();
         }
@@ -1106,7 +1212,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     CUtensorMap map_q, map_k, map_v;
     if (!make_tma_queries_bf16(&map_q, d_q, num_rows, Hq, a.group, a.tokens) ||
         !make_tma_2d_bf16(&map_k, cache->k_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64) ||
-        !make_tma_2d_bf16(&map_v, cache->v_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64))
+        !make_tma_rows_in_halves_bf16(&map_v, cache->v_pool, pool_rows, TTS_BLOCK_TOKENS))
         return TTS_ERR_CUDA;
     if (!allow_smem(prompt_attn_kernel, kSmem)) return TTS_ERR_CUDA;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
