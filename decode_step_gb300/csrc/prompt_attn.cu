@@ -43,23 +43,27 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kDim = 128;
-constexpr int kTile = 128;                  // tokens a tile, matrix rows a half
-constexpr int kChunkBytes = kTile * 128;    // [128 rows][64 values], 128-byte swizzle
-constexpr int kSlotBytes = 2 * kChunkBytes; // a tile of keys, or of values block by block: [8][2][16 tokens][64 values]
+constexpr int kRows = 128;                  // matrix rows of a half
+constexpr int kBlocks = 5, kTile = kBlocks * TTS_BLOCK_TOKENS;  // blocks and tokens a tile
+constexpr int kQueryBytes = kRows * 128;    // [128 rows][64 values], 128-byte swizzle; two a half
+constexpr int kChunkBytes = kTile * 128;    // [80 tokens][64 values]
+constexpr int kSlotBytes = 2 * kChunkBytes; // a tile of keys, or of values block by block: [5][2][16 tokens][64 values]
 constexpr int kBlockBytes = 4096;           // a block's values of a head
-constexpr int kKeySlots = 2, kValueSlots = 3;  // (keys are done with half a tile before the values)
-constexpr int kThreads = 384;               // two softmax warpgroups; producer, issuer, two checkers
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72, kStartRegs = 168;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kStartRegs);
+constexpr int kSlots = 4;                   // tiles of keys, and of values, in the ring
+// Tensor memory: a half's S, its P (two weights a column), and both halves' O
+constexpr int kS = 0, kP = kTile, kHalf = 128, kO = 256;
+static_assert(kP + kTile / 2 <= kHalf);
+constexpr int kThreads = 416;               // two softmax warpgroups; producer, two issuers, two checkers
 constexpr int kMaxStreams = 4096;           // (their lengths are staged in shared memory)
 constexpr int kSnap = 2;                    // tiles
-constexpr int kMinTiles = 4;                // tiles a CTA at least, where there are more CTAs than segments
+constexpr int kPartCost = 2;                // what a segment costs beside its tiles, in tiles
+constexpr int kMinTiles = 6;                // tiles a CTA at least, where there are more CTAs than segments
 constexpr float kLog2e = 1.4426950408889634f;
 // Running maximum before any token (log2 units): no finite score is below it.
 constexpr float kNoScore = -FLT_MAX;
 constexpr float kSlack = 8.0f;              // scores may pass it by this much before it moves (log2 units)
-constexpr int kPartFloats = kTile * kDim + 2 * kTile;  // o, m, l of a half
-constexpr int kTakeTurns = 8;               // tiles of a segment from which on its one half's rows use both
+constexpr int kPartFloats = kRows * kDim + 2 * kRows;  // o, m, l of a half
+constexpr int kTakeTurns = 12;              // tiles of a segment from which on its one half's rows use both
 constexpr int kJoinHere = 4;                // parts that the last CTA joins; more are left to the second kernel
 
 struct PromptArgs {
@@ -99,7 +103,7 @@ __device__ __forceinline__ bool prompt_stream(const PromptArgs &a, int b, int *f
 __device__ __forceinline__ int query_tiles(const PromptArgs &a, int n) { return (n + 2 * a.tokens - 1) / (2 * a.tokens); }
 
 // What a query tile sees: the tokens below `high`, of which those from `low` on
-// (the first row's window) and the sinks; in 128-token tiles: the first `head`
+// (the first row's window) and the sinks; in tiles: the first `head`
 // ones and, `skip` further on, the others.
 struct Span {
     int low, high, tiles, head, skip;
@@ -115,7 +119,8 @@ __device__ __forceinline__ Span span_of(const PromptArgs &a, int n, int ctx, int
     return s;
 }
 
-// Equal ranges of the flat list (T tiles, W CTAs, T >= W).
+// Equal ranges of the flat list, each segment kPartCost and then its tiles long
+// (T in all, W CTAs, T >= W).
 struct Ranges {
     int q, rem;
     __device__ __forceinline__ int start(int c) const { return c * q + min(c, rem); }
@@ -131,16 +136,22 @@ __device__ __forceinline__ bool tile_edge(const PromptArgs &a, int t0, int first
     return !(t0 + kTile <= first && (!a.window || t0 + kTile <= a.sinks || t0 >= last - a.window));
 }
 
+// How a part's tiles are worked on: by the first half, by both (both have rows), or
+// by the two halves in turns (for the first one's rows).
+constexpr int kBoth = 1, kTurns = 2;
+
 // Walks a CTA's range: part after part of a segment, tile after tile.
 struct Walk {
     int left;                  // tiles of the range left, this one among them
     int b, i, g, k;            // stream, query tile, KV head, tile of the segment
-    int s0;                    // the segment's first tile in the flat list
+    int s0;                    // the segment's place in the flat list
     int first, n, ctx;         // of the stream
     Span span;
     bool fresh;                // first tile of a part
     __device__ __forceinline__ int r0(const PromptArgs &a) const { return i * 2 * a.tokens; }
     __device__ __forceinline__ bool two(const PromptArgs &a) const { return r0(a) + a.tokens < n; }
+    __device__ __forceinline__ int tiles() const { return min(left, span.tiles - k); }  // of the part, from its first one on
+    __device__ __forceinline__ int mode(const PromptArgs &a) const { return two(a) ? kBoth : span.tiles >= kTakeTurns ? kTurns : 0; }
     __device__ __forceinline__ int tile() const { return k < span.head ? k : k + span.skip; }
     __device__ __forceinline__ void seek(const PromptArgs &a) {  // b: the next stream that has rows
         for (; b < a.B; ++b) {
@@ -155,7 +166,7 @@ struct Walk {
         fresh = true;
         if (k < span.tiles) return;
         k = 0;
-        s0 += span.tiles;
+        s0 += kPartCost + span.tiles;
         if (++g < a.Hkv) return;
         g = 0;
         if (++i == query_tiles(a, n)) {
@@ -176,7 +187,6 @@ struct Walk {
 };
 
 // A place in a ring of slots and its barriers' parity.
-template <int kSlots>
 struct Place {
     uint32_t slot = 0, phase = 0;
     bool again = false;  // the ring has been through once
@@ -208,28 +218,29 @@ struct PartInfo {
     int k, head, skip, low;       // first tile of the part; Span
     int high, shares, more, mode; // first CTA of the segment, CTAs that follow
 };
-constexpr int kBoth = 1, kTurns = 2;  // mode: both halves have rows; the one half's rows use both, tile by tile
 struct __align__(8) TileInfo {
-    int flags, t0;  // bits 0-7: blocks in the pool, from kPartShift on: its part's note; first token
+    int flags, t0;  // bits 0-4: blocks in the pool; then its part's note and its slot; first token
 };
-constexpr int kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12;
-constexpr int kInfos = 8;  // (the producer is at most four tiles ahead)
+constexpr int kAllBlocks = (1 << kBlocks) - 1, kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12, kSlotShift = 16;
+constexpr int kInfos = 16;  // (the producer is at most six tiles ahead)
+constexpr int kLookups = 6;  // tiles whose blocks a warp looks up at once
+static_assert(kLookups * kBlocks <= 32);
 
 struct PromptShared {
-    uint64_t k_full[kKeySlots], k_empty[kKeySlots], v_full[kValueSlots], v_empty[kValueSlots], checked[kValueSlots];
-    uint64_t q_full[2], q_empty, s_full[2], p_full[2][2], o_full[2], o_empty[2], stored[2], told[2], done;
+    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], checked[kSlots];
+    uint64_t q_full[2], q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_empty[2], stored[2], told[2], done[2];
     __align__(16) PartInfo parts[kInfos];
     TileInfo tiles[2][kInfos];  // by use of the half
     int4 jobs[2];
     uint32_t tmem;
-    int odd[4];            // number of the part whose tiles held values that are not finite, by number % 4
+    int odd[8];            // number of the part whose tiles held values that are not finite, by number % 8
     int last[2];           // whether the half's part was the last one
     long long scan[2][kThreads / 32];
     int b, i, g, k, s0, first, n, ctx, from, to, q, rem;
 };
-constexpr int kSmem = (2 + kKeySlots + kValueSlots) * kSlotBytes + static_cast<int>(sizeof(PromptShared));
+constexpr int kSmem = 4 * kQueryBytes + 2 * kSlots * kSlotBytes + static_cast<int>(sizeof(PromptShared));
 static_assert(kSmem <= 227 * 1024);
-static_assert(kMaxStreams * 16 <= (kKeySlots + kValueSlots) * kSlotBytes);
+static_assert(kMaxStreams * 16 <= 2 * kSlots * kSlotBytes);
 
 // Zeros in the rows of the refused streams (rare), by every thread of the grid.
 __device__ __noinline__ void zero_refused(const PromptArgs &a) {
@@ -307,11 +318,11 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
         int4 s = t0 < t1 ? streams[b] : make_int4(0, 0, 0, 0);
         for (int t = t0; t < t1; ++t) {
             while (b + 1 < a.B && streams[b + 1].w <= t) s = streams[++b];
-            f(b, t - s.w, span_of(a, s.y, s.z, t - s.w).tiles);
+            f(b, t, t - s.w, span_of(a, s.y, s.z, t - s.w).tiles);
         }
     };
     long long sum = 0, total;
-    each_tile([&](int, int, int n) { sum += n; });
+    each_tile([&](int, int, int, int n) { sum += kPartCost + n; });
     const long long before = scan_before(sum, sh.scan[1], &total) * a.Hkv;
     const int T = static_cast<int>(total) * a.Hkv;  // (below 2^30, as the host has seen to)
     const int segments = tiles * a.Hkv;
@@ -322,24 +333,25 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
         sh.q = ranges.q;
         sh.rem = ranges.rem;
         if (c >= W) sh.from = sh.to = 0;
-        else if (c + 1 == W) sh.to = T;
+        else if (c + 1 == W) sh.to = T - kPartCost * segments;
     }
     if (c < W) {
         const int x0 = ranges.start(c), x1 = ranges.start(c + 1);
         int at_tile = static_cast<int>(before);
-        each_tile([&](int b, int i, int n) {
-            const int end = at_tile + n * a.Hkv;
+        each_tile([&](int b, int t, int i, int n) {
+            const int each_g = kPartCost + n, end = at_tile + each_g * a.Hkv;
             for (int which = 0; which < 2; ++which) {
                 const int x = which ? x1 : x0;
                 if (x < at_tile || x >= end) continue;
-                const int g = (x - at_tile) / n, s0 = at_tile + g * n;
-                int k = x - s0;
+                const int g = (x - at_tile) / each_g, s0 = at_tile + g * each_g;
+                int k = x - s0 - kPartCost;
                 if (k <= kSnap) k = 0;
                 else if (n - k <= kSnap) k = n;
+                const int before_it = s0 - kPartCost * (t * a.Hkv + g) + k;  // tiles
                 if (which) {
-                    sh.to = s0 + k;
+                    sh.to = before_it;
                 } else {
-                    sh.from = s0 + k;
+                    sh.from = before_it;
                     sh.b = b;
                     sh.i = i;
                     sh.g = g;
@@ -362,6 +374,7 @@ struct Shares {
 };
 __device__ __forceinline__ Shares shares_of(const Ranges &r, int s0, int tiles) {
     if (tiles <= 2 * kSnap) return {0, 0};
+    s0 += kPartCost;
     const int lo = r.of(s0 + kSnap) + 1, hi = r.of(s0 + tiles - kSnap - 1);  // boundaries inside that stay
     return {lo - 1, max(0, hi - lo + 1)};
 }
@@ -406,6 +419,12 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
     return r;
+}
+// Bits 15 and 31: whether the halves' exponents (bf16) are all ones.
+__device__ __forceinline__ uint32_t ones(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+// warp_wait where the phase has mostly completed.
+__device__ __forceinline__ bool quick_wait(const uint64_t *bar, uint32_t parity, long long limit) {
+    return __all_sync(kFull, mbar_test(smem_addr(bar), parity)) || warp_wait(bar, parity, limit);
 }
 // Bits of the tokens of word w (32 tokens from `base` on) before token t.
 __device__ __forceinline__ uint32_t bits_before(int t, int base) {
@@ -467,32 +486,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
     extern __shared__ __align__(1024) uint8_t raw[];
-    const uint32_t q_base = smem_addr(raw), k_base = q_base + 2 * kSlotBytes, v_base = k_base + kKeySlots * kSlotBytes;
-    PromptShared &sh = *reinterpret_cast<PromptShared *>(raw + (2 + kKeySlots + kValueSlots) * kSlotBytes);
+    const uint32_t q_base = smem_addr(raw), k_base = q_base + 4 * kQueryBytes, v_base = k_base + kSlots * kSlotBytes;
+    PromptShared &sh = *reinterpret_cast<PromptShared *>(raw + 4 * kQueryBytes + 2 * kSlots * kSlotBytes);
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    if (warp == 9 && lane == 0) {
-        for (int i = 0; i < kKeySlots; ++i) {
+    if (warp == 11 && lane == 0) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(smem_addr(&sh.k_full[i]), 1);
-            mbar_init(smem_addr(&sh.k_empty[i]), 1);
-        }
-        for (int i = 0; i < kValueSlots; ++i) {
+            mbar_init(smem_addr(&sh.k_empty[i]), 2);  // (a half each, by who is done with the slot)
             mbar_init(smem_addr(&sh.v_full[i]), 1);
-            mbar_init(smem_addr(&sh.v_empty[i]), 1);
+            mbar_init(smem_addr(&sh.v_empty[i]), 2);
             mbar_init(smem_addr(&sh.checked[i]), 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.q_full[i]), 1);
             mbar_init(smem_addr(&sh.s_full[i]), 1);
-            mbar_init(smem_addr(&sh.p_full[i][0]), 4);
-            mbar_init(smem_addr(&sh.p_full[i][1]), 4);
-            mbar_init(smem_addr(&sh.o_full[i]), 1);
+            mbar_init(smem_addr(&sh.s_empty[i]), 4);
+            mbar_init(smem_addr(&sh.p_full[i]), 4);
+            mbar_init(smem_addr(&sh.o_done[i]), 1);
             mbar_init(smem_addr(&sh.o_empty[i]), 4);
             mbar_init(smem_addr(&sh.stored[i]), 4);
             mbar_init(smem_addr(&sh.told[i]), 1);
         }
-        mbar_init(smem_addr(&sh.q_empty), 1);
-        mbar_init(smem_addr(&sh.done), 1);
-        for (int i = 0; i < 4; ++i) sh.odd[i] = 0;
+        mbar_init(smem_addr(&sh.q_empty), 2);
+        mbar_init(smem_addr(&sh.done[0]), 1);
+        mbar_init(smem_addr(&sh.done[1]), 1);
+        for (int i = 0; i < 8; ++i) sh.odd[i] = 0;
         sh.jobs[0] = sh.jobs[1] = make_int4(0, 0, 0, 0);
         fence_mbar_init();
     }
@@ -504,19 +522,19 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     pdl_wait_prerequisites();
     // (tensor memory only after the wait: the kernel before may be one that
     // still has to allocate its own)
-    if (warp == 10) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    find_range(a, sh, reinterpret_cast<int4 *>(raw + 2 * kSlotBytes));
+    find_range(a, sh, reinterpret_cast<int4 *>(raw + 4 * kQueryBytes));
     // (the staged lengths make way for copies)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     pdl_allow_dependents();
-    const uint32_t tmem = uniform(sh.tmem);  // S0, S1, O0, O1: 128 columns each
+    const uint32_t tmem = uniform(sh.tmem);
     const Ranges ranges{uniform(sh.q), uniform(sh.rem)};
     Walk walk;
     walk.left = uniform(sh.to - sh.from);
@@ -533,300 +551,293 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         walk.span = span_of(a, walk.n, walk.ctx, walk.i);
         walk.settle(a);
         if (warp >= 8) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
             if (warp == 8) {
-                // ---- producer: lanes 0-7 look after a block each
-                uint32_t part = 0, q_count[2] = {0, 0};
-                Place<kKeySlots> keys;
-                Place<kValueSlots> values;
-                auto lookup = [&](const Walk &w, int &id) {
-                    const int t = (w.tile() * 8 + lane % 8) * TTS_BLOCK_TOKENS;
-                    // blocks without a token that some row sees may hold anything
-                    const bool seen = t < w.span.high && (t < a.sinks || t + TTS_BLOCK_TOKENS > w.span.low);
-                    id = seen ? __ldcg(a.table + static_cast<size_t>(w.b) * a.max_blocks + t / TTS_BLOCK_TOKENS) : -1;
-                    return seen;
-                };
-                int id, id_next = -1;
-                bool seen = lookup(walk, id), seen_next = false;
+                // ---- producer.  Lane l looks up block l % 5 of the l / 5-th of the next six tiles
                 const uint32_t leader = elect_leader();
-                auto room = [&](uint64_t *full, uint64_t *empty, auto &at, uint32_t bytes) {
+                uint32_t part = 0, q_count[2] = {0, 0};
+                Place keys, values;
+                auto room = [&](uint64_t *full, uint64_t *empty, const Place &at, uint32_t bytes) {
                     if (at.again && !warp_wait(&empty[at.slot], at.phase ^ 1, a.wait_limit)) return false;
                     mbar_expect_tx_by(leader, smem_addr(&full[at.slot]), bytes);
                     return true;
                 };
-                int uses[2] = {0, 0}, j = 0, mode = 0, tiles = 0, note = 0;  // j: tile of the part
-                for (bool begun = false; ok && walk.left > 0; begun = true) {
-                    const bool good = id >= 0 && id < a.num_blocks;
-                    if (seen && !good && lane < 8) flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
-                    const int y = good ? (id * a.Hkv + walk.g) * TTS_BLOCK_TOKENS : a.zero_row;
-                    const int mask = __ballot_sync(kFull, good) & 0xFF;
-                    const int r0 = walk.r0(a);
-                    if (walk.fresh) {
-                        j = 0;
-                        note = part % kInfos;
-                        tiles = min(walk.left, walk.span.tiles - walk.k);
-                        mode = walk.two(a) ? kBoth : walk.span.tiles >= kTakeTurns ? kTurns : 0;
-                        if (lane == 0) {
-                            const Shares shares = shares_of(ranges, walk.s0, walk.span.tiles);
-                            PartInfo &p = sh.parts[note];
-                            p.first = walk.first; p.n = walk.n; p.ctx = walk.ctx; p.b = walk.b;
-                            p.r0 = r0; p.g = walk.g; p.number = part + 1; p.tiles = tiles;
-                            p.k = walk.k; p.head = walk.span.head; p.skip = walk.span.skip; p.low = walk.span.low;
-                            p.high = walk.span.high; p.shares = shares.first; p.more = shares.more; p.mode = mode;
+                // ids of the tiles from the part's j-th on (kNoBlock: no token of it is seen)
+                constexpr int kNoBlock = -0x7FFFFFFF;
+                auto lookup = [&](const Walk &w, int tiles, int j) {
+                    j += lane / kBlocks;
+                    const int k = w.k + j, t = ((k < w.span.head ? k : k + w.span.skip) * kBlocks + lane % kBlocks) * TTS_BLOCK_TOKENS;
+                    // (blocks without a token that some row sees may hold anything)
+                    if (lane >= kLookups * kBlocks || j >= tiles || t >= w.span.high ||
+                        (t >= a.sinks && t + TTS_BLOCK_TOKENS <= w.span.low))
+                        return kNoBlock;
+                    return __ldcg(a.table + static_cast<size_t>(w.b) * a.max_blocks + t / TTS_BLOCK_TOKENS);
+                };
+                int uses[2] = {0, 0};
+                int tiles = walk.tiles(), id = lookup(walk, tiles, 0);
+                for (bool begun = false; ok && walk.left > 0;) {
+                    const int mode = walk.mode(a), note = part % kInfos, r0 = walk.r0(a), before = walk.ctx - walk.n;
+                    if (lane == 0) {
+                        const Shares shares = shares_of(ranges, walk.s0, walk.span.tiles);
+                        PartInfo &p = sh.parts[note];
+                        p.first = walk.first; p.n = walk.n; p.ctx = walk.ctx; p.b = walk.b;
+                        p.r0 = r0; p.g = walk.g; p.number = part + 1; p.tiles = tiles;
+                        p.k = walk.k; p.head = walk.span.head; p.skip = walk.span.skip; p.low = walk.span.low;
+                        p.high = walk.span.high; p.shares = shares.first; p.more = shares.more; p.mode = mode;
+                    }
+                    Walk next = walk;
+                    next.left -= tiles - 1;
+                    next.k += tiles - 1;
+                    next.advance(a);
+                    const int next_tiles = next.left > 0 ? next.tiles() : 0;
+                    int ahead = lookup(walk, tiles, kLookups), after = next.left > 0 ? lookup(next, next_tiles, 0) : kNoBlock;
+                    int y = 0, good = 0;
+                    for (int j = 0; ok && j < tiles; ++j) {
+                        const int from = j % kLookups * kBlocks;
+                        if (from == 0) {
+                            if (j) {
+                                id = ahead;
+                                ahead = lookup(walk, tiles, j + kLookups);
+                            }
+                            const bool here = id >= 0 && id < a.num_blocks;
+                            if (!here && id != kNoBlock) flag_error(a.err, TTS_ERRBIT_BLOCK_ID);
+                            y = here ? (id * a.Hkv + walk.g) * TTS_BLOCK_TOKENS : a.zero_row;
+                            good = static_cast<int>(__ballot_sync(kFull, here));
+                        }
+                        const int mask = (good >> from) & kAllBlocks;
+                        const int k = walk.k + j, t0 = (k < walk.span.head ? k : k + walk.span.skip) * kTile;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (mode == kTurns ? s != j % 2 : s == 1 && mode != kBoth) continue;
+                            const int row0 = r0 + (mode == kTurns ? 0 : s * a.tokens);
+                            const bool masked = mask != kAllBlocks ||
+                                                tile_edge(a, t0, before + row0 + 1, before + min(walk.n, row0 + a.tokens));
+                            const bool fresh = j < (mode == kTurns ? 2 : 1), last = j >= tiles - (mode == kTurns ? 2 : 1);
+                            if (lane == 0)
+                                sh.tiles[s][uses[s] % kInfos] = {mask | (masked ? kMasked : 0) | (fresh ? kFresh : 0) |
+                                                                     (last ? kLast : 0) | note << kPartShift |
+                                                                     static_cast<int>(keys.slot) << kSlotShift, t0};
+                            uses[s] += 1;
+                        }
+                        int ys[kBlocks];
+#pragma unroll
+                        for (int i = 0; i < kBlocks; ++i) ys[i] = __shfl_sync(kFull, y, from + i);
+                        ok = room(sh.k_full, sh.k_empty, keys, kSlotBytes + (a.stall && !begun ? 16 : 0));
+                        if (!ok) break;
+                        begun = true;
+                        {
+                            const uint32_t bar = smem_addr(&sh.k_full[keys.slot]), to = k_base + keys.slot * kSlotBytes;
+#pragma unroll
+                            for (int i = 0; i < 2 * kBlocks; ++i)
+                                tma_load_2d_by(leader, to + i / kBlocks * kChunkBytes + i % kBlocks * 2048, &map_k, i / kBlocks * 64,
+                                               ys[i % kBlocks], bar);
+                            keys.next();
+                        }
+                        if (j == 0) {
+                            ok = part == 0 || warp_wait(&sh.q_empty, (part - 1) & 1, a.wait_limit);
+                            if (!ok) break;
+                            const int halves = mode == kBoth ? 2 : 1;
+                            ++q_count[0];
+                            q_count[1] += halves - 1;
+                            if (lane == 0)
+                                for (int s = 0; s < halves; ++s) {
+                                    const uint32_t bar = smem_addr(&sh.q_full[s]);
+                                    mbar_arrive_expect_tx(bar, 2 * a.tokens * a.group * 128);
+                                    for (int c = 0; c < 2; ++c)
+                                        asm volatile(
+                                            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                                            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_base + (2 * s + c) * kQueryBytes),
+                                            "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(c * 64), "r"(walk.g * a.group),
+                                            "r"(walk.first + r0 + s * a.tokens), "r"(bar)
+                                            : "memory");
+                                }
+                            __syncwarp();
+                            ++part;
+                        }
+                        ok = room(sh.v_full, sh.v_empty, values, kSlotBytes);
+                        if (!ok) break;
+                        {
+                            const uint32_t bar = smem_addr(&sh.v_full[values.slot]), to = v_base + values.slot * kSlotBytes;
+#pragma unroll
+                            for (int i = 0; i < kBlocks; ++i) tma_load_rows_by(leader, to + i * kBlockBytes, &map_v, ys[i], bar);
+                            values.next();
                         }
                     }
-                    const int t0 = walk.tile() * kTile, before = walk.ctx - walk.n;
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (mode == kTurns ? s != j % 2 : s == 1 && mode != kBoth) continue;
-                        const int from = r0 + (mode == kTurns ? 0 : s * a.tokens);
-                        const bool masked = mask != 0xFF || tile_edge(a, t0, before + from + 1, before + min(walk.n, from + a.tokens));
-                        const bool fresh = j < (mode == kTurns ? 2 : 1), last = j >= tiles - (mode == kTurns ? 2 : 1);
-                        if (lane == 0)
-                            sh.tiles[s][uses[s] % kInfos] = {mask | (masked ? kMasked : 0) | (fresh ? kFresh : 0) | (last ? kLast : 0) | note << kPartShift, t0};
-                        uses[s] += 1;
-                    }
-                    ++j;
-                    Walk next = walk;
-                    next.advance(a);
-                    if (next.left > 0) seen_next = lookup(next, id_next);
-                    int ys[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) ys[i] = __shfl_sync(kFull, y, i);
-                    ok = room(sh.k_full, sh.k_empty, keys, kSlotBytes + (a.stall && !begun ? 16 : 0));
-                    if (!ok) break;
-                    {
-                        const uint32_t bar = smem_addr(&sh.k_full[keys.slot]), to = k_base + keys.slot * kSlotBytes;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            tma_load_2d_by(leader, to + i / 8 * kChunkBytes + i % 8 * 2048, &map_k, i / 8 * 64, ys[i % 8], bar);
-                        keys.next();
-                    }
-                    if (walk.fresh) {
-                        ok = part == 0 || warp_wait(&sh.q_empty, (part - 1) & 1, a.wait_limit);
-                        if (!ok) break;
-                        const int halves = mode == kBoth ? 2 : 1;
-                        ++q_count[0];
-                        q_count[1] += halves - 1;
-                        if (lane == 0)
-                            for (int s = 0; s < halves; ++s) {
-                                const uint32_t bar = smem_addr(&sh.q_full[s]);
-                                mbar_arrive_expect_tx(bar, 2 * a.tokens * a.group * 128);
-                                for (int c = 0; c < 2; ++c)
-                                    asm volatile(
-                                        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                                        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_base + s * kSlotBytes + c * kChunkBytes),
-                                        "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(c * 64), "r"(walk.g * a.group),
-                                        "r"(walk.first + r0 + s * a.tokens), "r"(bar)
-                                        : "memory");
-                            }
-                        __syncwarp();
-                        ++part;
-                    }
-                    ok = room(sh.v_full, sh.v_empty, values, kSlotBytes);
-                    if (!ok) break;
-                    {
-                        const uint32_t bar = smem_addr(&sh.v_full[values.slot]), to = v_base + values.slot * kSlotBytes;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) tma_load_rows_by(leader, to + i * kBlockBytes, &map_v, ys[i], bar);
-                        values.next();
-                    }
                     walk = next;
-                    id = id_next;
-                    seen = seen_next;
+                    tiles = next_tiles;
+                    id = after;
                 }
                 // every copy lands before the CTA ends
                 keys.drain(sh.k_full);
                 values.drain(sh.v_full);
                 for (uint32_t s = 0; s < 2; ++s)
                     if (q_count[s]) warp_wait(&sh.q_full[s], (q_count[s] - 1) & 1);
-            } else if (warp == 9) {
-                // ---- MMA issuer: S0 S1 | O0(j) S0(j + 1) | O1(j) S1(j + 1) ..., or, where
-                // the halves take turns, S0(0) S1(1) | O0(0) S0(2) | O1(1) S1(3) ...  A half's
-                // S is overwritten right after the O product that reads the weights kept
-                // in it; the tensor core runs them in order.
+            } else if (warp <= 10) {
+                // ---- MMA issuers, one a half: S(j + 1) O(j), or, where the halves take
+                // turns, S(j + 2) O(j).  The next scores need only that the last ones were
+                // read, so that the softmax warps find theirs when they come.  (A commit or
+                // a wait takes the issuing warp about 0.1 us: one warp for both halves was
+                // the bound.)  Every slot is waited for and given back by either half,
+                // worked on or not: a barrier's parity tells one use from the next, not
+                // from the one after.
+                const int s = warp - 9;
                 const uint32_t leader = elect_leader();
-                Place<kKeySlots> keys;      // of the next scores
-                Place<kValueSlots> values;  // of the next outputs
-                // uses so far of either half's weights, queries and output
-                uint32_t p0 = 0, p1 = 0, q0 = 0, q1 = 0, o0 = 0, o1 = 0;
-                auto scores = [&](int s, uint32_t q) {
-                    const uint32_t sa = q_base + q * kSlotBytes, sb = k_base + keys.slot * kSlotBytes;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_by(leader, tmem + s * kTile, sw128_desc(sa + kk / 4 * kChunkBytes + kk % 4 * 32),
-                                    sw128_desc(sb + kk / 4 * kChunkBytes + kk % 4 * 32), mma_idesc(kTile, kTile), kk != 0);
-                    mma_commit_by(leader, smem_addr(&sh.s_full[s]));
-                };
-                auto output = [&](int s, int half, bool fresh) {  // of 64 tokens
-                    const uint32_t sb = v_base + values.slot * kSlotBytes;
-#pragma unroll
-                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                        mma_ts_by(leader, tmem + (2 + s) * kTile, tmem + s * kTile + kk * 8,
-                                  sw128_mn_desc(sb + kk * kBlockBytes, kBlockBytes / 2), mma_idesc(kTile, kTile) | kTransposeB,
-                                  !fresh || kk != 0);
-                };
+                Place keys, values;  // of the next scores, and outputs
+                uint32_t uses = 0, outs = 0, parts = 0, part = 0, both = 0;
                 bool go = true;
-                auto keys_here = [&]() {
+                auto scores = [&](int q) {  // with the queries of half q
+                    go = quick_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
+                    if (!go) return;
                     WarpWaits<1> x;
-                    x.set(0, &sh.k_full[keys.slot], keys.phase);
-                    go = x.spin(a.wait_limit);
-                    tc_fence_after();
-                    return go;
-                };
-                auto keys_done = [&](bool last) {  // last: of the part, the queries are done with too
-                    mma_commit_by(leader, smem_addr(&sh.k_empty[keys.slot]));
-                    if (last) mma_commit_by(leader, smem_addr(&sh.q_empty));
-                    keys.next();
-                };
-                // O of half s: its weights, and the values where nobody has waited for them yet
-                auto outputs = [&](int s, bool look, bool fresh, bool last) {
-                    WarpWaits<4> x;
-                    const uint32_t phase = (s ? p1 : p0) & 1;
-                    x.set(0, &sh.p_full[s][0], phase);
-                    p0 += 1 - s;
-                    p1 += s;
-                    x.none(1);
-                    x.none(2);
-                    x.none(3);
-                    if (look) {
-                        x.set(1, &sh.v_full[values.slot], values.phase);
-                        x.set(3, &sh.checked[values.slot], values.phase);
-                    }
-                    if (fresh) {
-                        const uint32_t o = s ? o1 : o0;
-                        if (o) x.set(2, &sh.o_empty[s], (o - 1) & 1);
-                        o0 += 1 - s;
-                        o1 += s;
-                    }
+                    x.none(0);
+                    if (uses) x.set(0, &sh.s_empty[s], (uses - 1) & 1);
+                    ++uses;
                     go = x.spin(a.wait_limit);
                     if (!go) return;
                     tc_fence_after();
-                    output(s, 0, fresh);
+                    const uint32_t sa = q_base + 2 * q * kQueryBytes, sb = k_base + keys.slot * kSlotBytes;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16_by(leader, tmem + s * kHalf + kS, sw128_desc(sa + kk / 4 * kQueryBytes + kk % 4 * 32),
+                                    sw128_desc(sb + kk / 4 * kChunkBytes + kk % 4 * 32), mma_idesc(kRows, kTile), kk != 0);
+                    mma_commit_by(leader, smem_addr(&sh.s_full[s]));
+                    keys.next();
+                };
+                auto outputs = [&](bool fresh) {
+                    WarpWaits<3> x;
+                    x.set(0, &sh.v_full[values.slot], values.phase);
+                    x.set(1, &sh.checked[values.slot], values.phase);
+                    x.none(2);
+                    if (fresh) {
+                        if (parts) x.set(2, &sh.o_empty[s], (parts - 1) & 1);
+                        ++parts;
+                    }
+                    go = x.wait(a.wait_limit);
+                    if (!go) return;
                     WarpWaits<1> y;
-                    y.set(0, &sh.p_full[s][1], phase);
+                    y.set(0, &sh.p_full[s], outs++ & 1);
                     go = y.spin(a.wait_limit);
                     if (!go) return;
                     tc_fence_after();
-                    output(s, 1, false);
-                    if (last) mma_commit_by(leader, smem_addr(&sh.o_full[s]));
-                };
-                auto values_done = [&]() {
-                    mma_commit_by(leader, smem_addr(&sh.v_empty[values.slot]));
+                    const uint32_t sb = v_base + values.slot * kSlotBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kBlocks; ++kk)
+                        mma_ts_by(leader, tmem + kO + s * kDim, tmem + s * kHalf + kP + kk * 8,
+                                  sw128_mn_desc(sb + kk * kBlockBytes, kBlockBytes / 2), mma_idesc(kRows, kDim) | kTransposeB,
+                                  !fresh || kk != 0);
+                    mma_commit_by(leader, smem_addr(&sh.o_done[s]));
                     values.next();
                 };
-                int left = walk.left;
-                for (int part = 0; go && left > 0; ++part) {
-                    // (the producer's notes are there once the part's first keys are)
-                    if (!keys_here()) break;
-                    const volatile PartInfo &info = sh.parts[part % kInfos];
-                    const int tiles = uniform(info.tiles), mode = uniform(info.mode);
-                    left -= tiles;
-                    const bool two = mode == kBoth;
+                auto pass_keys = [&]() {
+                    go = warp_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
+                    if (go && lane == 0) mbar_arrive(smem_addr(&sh.k_empty[keys.slot]));
+                    keys.next();
+                };
+                auto pass_values = [&]() {
                     WarpWaits<2> x;
-                    x.set(0, &sh.q_full[0], q0++ & 1);
-                    x.none(1);
-                    if (two) x.set(1, &sh.q_full[1], q1++ & 1);
+                    x.set(0, &sh.v_full[values.slot], values.phase);
+                    x.set(1, &sh.checked[values.slot], values.phase);
                     go = x.wait(a.wait_limit);
-                    if (!go) break;
-                    tc_fence_after();
-                    scores(0, 0);
-                    if (mode == kTurns) {
-                        keys_done(tiles == 1);
-                        if (tiles > 1 && keys_here()) {
-                            scores(1, 0);
-                            keys_done(tiles == 2);
+                    if (go && lane == 0) mbar_arrive(smem_addr(&sh.v_empty[values.slot]));
+                    values.next();
+                };
+                while (go && walk.left > 0) {
+                    const int tiles = walk.tiles(), mode = walk.mode(a);
+                    const int step = mode == kTurns ? 2 : 1, q = mode == kTurns ? 0 : s;
+                    int j = mode == kTurns ? s : s == 1 && mode == 0 ? tiles : 0;  // this half's first tile of the part
+                    {
+                        WarpWaits<2> x;
+                        x.set(0, &sh.q_full[0], part++ & 1);
+                        x.none(1);
+                        if (s == 1 && mode == kBoth) x.set(1, &sh.q_full[1], both++ & 1);
+                        go = x.wait(a.wait_limit);
+                    }
+                    if (go && j >= tiles) {
+                        if (lane == 0) mbar_arrive(smem_addr(&sh.q_empty));
+                        for (int i = 0; go && i < tiles; ++i) {
+                            pass_keys();
+                            if (go) pass_values();
                         }
-                        for (int j = 0; go && j < tiles; ++j) {
-                            const int s = j & 1;
-                            outputs(s, true, j < 2, j + 2 >= tiles);
-                            if (!go) break;
-                            values_done();
-                            if (j + 2 < tiles && keys_here()) {
-                                scores(s, 0);
-                                keys_done(j + 3 == tiles);
-                            }
-                        }
-                    } else {
-                        if (two) scores(1, 1);
-                        keys_done(tiles == 1);
-                        for (int j = 0; go && j < tiles; ++j) {
-                            const bool last = j + 1 == tiles;
-                            outputs(0, true, j == 0, last);
-                            if (!go) break;
-                            if (!two) values_done();
-                            if (!last) {
-                                if (!keys_here()) break;
-                                scores(0, 0);
-                            }
-                            if (two) {
-                                outputs(1, false, j == 0, last);
-                                if (!go) break;
-                                values_done();
-                                if (!last) scores(1, 1);
-                            }
-                            if (!last) keys_done(j + 2 == tiles);
+                    } else if (go) {
+                        if (j) pass_keys();
+                        if (go) scores(q);
+                        if (go && j) pass_values();
+                        for (const int first = j; go && j < tiles; j += step) {
+                            if (step == 2 && j + 1 < tiles) pass_keys();
+                            if (go && j + step < tiles) scores(q);
+                            if (go) outputs(j == first);
+                            if (go && step == 2 && j + 1 < tiles) pass_values();
                         }
                     }
+                    walk.left -= tiles - 1;
+                    walk.k += tiles - 1;
+                    walk.advance(a);
                 }
-                // nothing more for the softmax warps (their latest scores' barriers are
+                // nothing more for the softmax warps (their latest scores' barrier is
                 // complete: their weights were waited for)
-                if (go && lane == 0)
-                    for (int s = 0; s < 2; ++s) {
-                        reinterpret_cast<volatile int &>(sh.tiles[s][(s ? p1 : p0) % kInfos].flags) = kEnd;
-                        mbar_arrive(smem_addr(&sh.s_full[s]));
-                    }
+                if (go && lane == 0) {
+                    reinterpret_cast<volatile int &>(sh.tiles[s][uses % kInfos].flags) = kEnd;
+                    mbar_arrive(smem_addr(&sh.s_full[s]));
+                }
                 __syncwarp();
-                mma_commit_by(leader, smem_addr(&sh.done));
-                ok = warp_wait(&sh.done, 0) && go;
+                mma_commit_by(leader, smem_addr(&sh.done[s]));
+                ok = warp_wait(&sh.done[s], 0) && go;
             } else {
                 // ---- checkers: values that are not finite leave the tiles that some
                 // row does not see whole.  (They keep step with every tile: a barrier's
                 // parity tells one use of a slot from the next, not from the one after.)
-                Place<kValueSlots> values;
-                int part = 0;
-                while (ok && walk.left > 0) {
-                    part += walk.fresh;
-                    ok = warp_wait(&sh.v_full[values.slot], values.phase, a.wait_limit);
-                    if (!ok) break;
-                    if (walk.edge(a)) {
-                        const int t0 = walk.tile() * kTile, first_limit = walk.ctx - walk.n + walk.r0(a) + 1;
-                        uint8_t *v = raw + (2 + kKeySlots + values.slot) * kSlotBytes;
-                        bool odd = false;
-#pragma unroll 4
-                        for (int e = (warp - 10) * 32 + lane; e < kSlotBytes / 16; e += 64) {
-                            uint4 x = reinterpret_cast<uint4 *>(v)[e];
-                            uint32_t bad = 0;
-                            for (const uint32_t w : {x.x, x.y, x.z, x.w})
-                                bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-                            if (!bad) continue;
-                            const int t = t0 + e / (kBlockBytes / 16) * TTS_BLOCK_TOKENS + e / 8 % TTS_BLOCK_TOKENS;
-                            odd = odd || (t < walk.span.high && (!a.window || t < a.sinks || t >= first_limit - a.window));
-                            uint16_t *h = reinterpret_cast<uint16_t *>(v + e * 16);
-                            for (int i = 0; i < 8; ++i)
-                                if ((h[i] & 0x7F80u) == 0x7F80u) h[i] = 0;
+                Place values;
+                for (int part = 1; ok && walk.left > 0; ++part) {
+                    const int tiles = walk.tiles(), first = walk.ctx - walk.n + walk.r0(a) + 1, high = walk.span.high;
+                    for (int j = 0; j < tiles; ++j) {
+                        ok = quick_wait(&sh.v_full[values.slot], values.phase, a.wait_limit);
+                        if (!ok) break;
+                        const int k = walk.k + j, t0 = (k < walk.span.head ? k : k + walk.span.skip) * kTile;
+                        if (tile_edge(a, t0, first, high)) {
+                            uint8_t *v = raw + 4 * kQueryBytes + (kSlots + values.slot) * kSlotBytes;
+                            const uint32_t from = smem_addr(v) + ((warp - 11) * 32 + lane) * 16;
+                            // bit 15 or 31 of a word: an exponent of ones in that half
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int e = 0; e < kSlotBytes / 1024; ++e) {
+                                const uint4 x = lds128(from + e * 1024);
+                                any |= ones(x.x) | ones(x.y) | ones(x.z) | ones(x.w);
+                            }
+                            if (any & 0x80008000u) {  // rare
+                                bool odd = false;
+                                for (int e = (warp - 11) * 32 + lane; e < kSlotBytes / 16; e += 64) {
+                                    uint16_t *h = reinterpret_cast<uint16_t *>(v + e * 16);
+                                    const int t = t0 + e / (kBlockBytes / 16) * TTS_BLOCK_TOKENS + e / 8 % TTS_BLOCK_TOKENS;
+                                    for (int i = 0; i < 8; ++i)
+                                        if ((h[i] & 0x7F80u) == 0x7F80u) {
+                                            h[i] = 0;
+                                            odd = odd || (t < high && (!a.window || t < a.sinks || t >= first - a.window));
+                                        }
+                                }
+                                if (odd) sh.odd[part % 8] = part;
+                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            }
+                            __syncwarp();
                         }
-                        if (odd) sh.odd[part % 4] = part;
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&sh.checked[values.slot]));
+                        values.next();
                     }
-                    if (lane == 0) mbar_arrive(smem_addr(&sh.checked[values.slot]));
-                    values.next();
+                    walk.left -= tiles - 1;
+                    walk.k += tiles - 1;
                     walk.advance(a);
                 }
             }
         } else {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
             // ---- softmax warpgroups: thread = matrix row
             const int s = warp / 4, w = warp % 4;
             const int row = w * 32 + lane, token = row / a.group;
             const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
-            const uint32_t ts = tmem + lanes + s * kTile, to = tmem + lanes + (2 + s) * kTile;
-            uint32_t parts = 0, joins = 0;  // of this half
+            const uint32_t ts = tmem + lanes + s * kHalf + kS, tp = ts - kS + kP, to = tmem + lanes + kO + s * kDim;
+            uint32_t joins = 0;  // of this half's parts with others'
             int limit = 0;                  // tokens up to the row's own
+            int held = -1;                  // slot of the values of the last use, until it is given back
             float m = kNoScore, l = 0.0f;
             for (uint32_t use = 0;; ++use) {
-                if (!warp_wait(&sh.s_full[s], use & 1, a.wait_limit)) {
+                if (!quick_wait(&sh.s_full[s], use & 1, a.wait_limit)) {
                     ok = false;
                     break;
                 }
@@ -835,26 +846,36 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int flags = info.flags;
                 if (flags & kEnd) break;
                 if (flags & kFresh) {
-                    const volatile PartInfo *p = &sh.parts[flags >> kPartShift];
+                    const volatile PartInfo *p = &sh.parts[(flags >> kPartShift) % kInfos];
                     const int before = p->ctx - p->n, from = p->r0 + (s == 1 && p->mode == kBoth ? a.tokens : 0);
                     limit = before + min(from + token + 1, min(p->n, from + a.tokens));
                     m = kNoScore;
                     l = 0.0f;
                 }
                 uint32_t x[kTile];
-#pragma unroll
-                for (int c = 0; c < kTile; c += 32) tmem_ld32_nowait(ts + c, x + c);
+                tmem_ld32_nowait(ts, x);
+                tmem_ld32_nowait(ts + 32, x + 32);
+                tmem_ld16_nowait(ts + 64, x + 64);
                 tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&sh.s_empty[s]));
+                    if (w == 0) {
+                        mbar_arrive(smem_addr(&sh.k_empty[flags >> kSlotShift]));
+                        if (flags & kLast) mbar_arrive(smem_addr(&sh.q_empty));
+                    }
+                }
                 if (flags & kMasked) {
                     const int t0 = info.t0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < (kTile + 31) / 32; ++c) {
                         const int base = t0 + 32 * c;
                         uint32_t see = bits_before(limit, base);
                         if (a.window) see &= bits_before(a.sinks, base) | ~bits_before(limit - a.window, base);
                         see &= ((flags >> (2 * c)) & 1 ? 0xFFFFu : 0u) | ((flags >> (2 * c)) & 2 ? 0xFFFF0000u : 0u);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
+                        for (int i = 0; i < 32 && 32 * c + i < kTile; ++i)
                             if (!((see >> i) & 1)) x[32 * c + i] = 0xFF800000u;  // -inf
                     }
                 }
@@ -863,8 +884,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 for (int i = 0; i < kTile; i += 2)
                     top[i / 2 % 4] = max3(top[i / 2 % 4], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                 const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
+                // (the product before this tile's has to be complete before O is scaled, and
+                // before its weights are overwritten: waited for as late as possible)
                 if (__any_sync(kFull, high > m + kSlack)) {
-                    // (the scores' being complete means that the product before them is too)
+                    if (use && !quick_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                     const float now = fmaxf(m, high), f = hw_ex2(m - now);
                     m = now;
                     l *= f;
@@ -878,40 +905,45 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             tmem_st16(to + c, o);
                         }
                 }
-                // (the first 64 tokens' product starts while the others' weights are computed)
                 uint64_t sum[2] = {0, 0};
                 const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), minus2 = pack2(-m, -m);
+                uint32_t weights[kTile / 2];
 #pragma unroll
-                for (int c = 0; c < kTile; c += 64) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float p0, p1;
-                        unpack2(fma2(pack2(__uint_as_float(x[c + 2 * i]), __uint_as_float(x[c + 2 * i + 1])), scale2, minus2), p0, p1);
-                        p0 = hw_ex2(p0);
-                        p1 = hw_ex2(p1);
-                        sum[i % 2] = add2(sum[i % 2], pack2(p0, p1));
-                        p[i] = pack_bf16(p0, p1);
-                    }
-                    tmem_st32(ts + c / 2, p);
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s][c / 64]));
+                for (int i = 0; i < kTile / 2; ++i) {
+                    float e0, e1;
+                    unpack2(fma2(pack2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, minus2), e0, e1);
+                    e0 = hw_ex2(e0);
+                    e1 = hw_ex2(e1);
+                    sum[i % 2] = add2(sum[i % 2], pack2(e0, e1));
+                    weights[i] = pack_bf16(e0, e1);
                 }
+                if (use && !quick_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (held >= 0 && threadIdx.x % 128 == 0) mbar_arrive(smem_addr(&sh.v_empty[held]));
+                held = flags >> kSlotShift;
+                tmem_st32(tp, weights);
+                tmem_st8(tp + 32, weights + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
                 float sum0, sum1;
                 unpack2(add2(sum[0], sum[1]), sum0, sum1);
                 l += sum0 + sum1;
                 if (!(flags & kLast)) continue;
                 // ---- the part's end: the rows, or what is joined with other parts
-                ok = warp_wait(&sh.o_full[s], parts & 1, a.wait_limit);
+                ok = warp_wait(&sh.o_done[s], use & 1, a.wait_limit);
                 if (!ok) break;
-                ++parts;
                 tc_fence_after();
-                const PartInfo &p = sh.parts[flags >> kPartShift];
+                if (threadIdx.x % 128 == 0) mbar_arrive(smem_addr(&sh.v_empty[held]));
+                held = -1;
+                const PartInfo &p = sh.parts[(flags >> kPartShift) % kInfos];
                 const bool turns = p.mode == kTurns;
                 const int r = p.r0 + (s == 1 && !turns ? a.tokens : 0) + token;  // row in the stream
-                const bool odd = *reinterpret_cast<volatile int *>(&sh.odd[p.number % 4]) == p.number;
+                const bool odd = *reinterpret_cast<volatile int *>(&sh.odd[p.number % 8]) == p.number;
                 const bool real = token < a.tokens && r < p.n;
                 const int first = p.shares, count = (p.more + 1) * (turns ? 2 : 1);
                 __nv_bfloat16 *out = a.out + (static_cast<size_t>(p.first + r) * a.Hq + p.g * a.group + row % a.group) * kDim;
@@ -942,15 +974,15 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     if (real)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<float4 *>(mine)[(c / 4 + i) * kTile + row] =
+                            reinterpret_cast<float4 *>(mine)[(c / 4 + i) * kRows + row] =
                                 make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                 }
                 if (real) {
-                    mine[kTile * kDim + row] = m;
-                    mine[kTile * kDim + kTile + row] = l;
+                    mine[kRows * kDim + row] = m;
+                    mine[kRows * kDim + kRows + row] = l;
                     if (alone) {  // no tile was half 1's
-                        mine[kPartFloats + kTile * kDim + row] = kNoScore;
-                        mine[kPartFloats + kTile * kDim + kTile + row] = 0.0f;
+                        mine[kPartFloats + kRows * kDim + row] = kNoScore;
+                        mine[kPartFloats + kRows * kDim + kRows + row] = 0.0f;
                     }
                 }
                 tc_fence_before();
@@ -979,10 +1011,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (!ok) break;
                 if (!*reinterpret_cast<volatile int *>(&sh.last[s]) || !real) continue;
                 float best = kNoScore, total = 0.0f;
-                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, from, i, turns, s) + kTile * kDim + row));
+                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, from, i, turns, s) + kRows * kDim + row));
                 for (int i = 0; i < count; ++i) {
-                    const float *q = segment_part(a.part, from, i, turns, s) + kTile * kDim + row;
-                    total = fmaf(hw_ex2(__ldcg(q) - best), __ldcg(q + kTile), total);
+                    const float *q = segment_part(a.part, from, i, turns, s) + kRows * kDim + row;
+                    total = fmaf(hw_ex2(__ldcg(q) - best), __ldcg(q + kRows), total);
                 }
                 const float inv = inverse(total);
                 for (int d = 0; d < kDim; d += 32) {
@@ -991,12 +1023,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
                     for (int i = 0; i < count; ++i) {
                         const float *q = segment_part(a.part, from, i, turns, s);
-                        const float mq = __ldcg(q + kTile * kDim + row);
+                        const float mq = __ldcg(q + kRows * kDim + row);
                         const float f = hw_ex2(mq - best);
-                        if (turns && mq == kNoScore && __ldcg(q + kTile * kDim + kTile + row) == 0.0f) continue;  // (nothing there)
+                        if (turns && mq == kNoScore && __ldcg(q + kRows * kDim + kRows + row) == 0.0f) continue;  // (nothing there)
                         float4 x[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = __ldcg(reinterpret_cast<const float4 *>(q) + (d / 4 + e) * kTile + row);
+                        for (int e = 0; e < 8; ++e) x[e] = __ldcg(reinterpret_cast<const float4 *>(q) + (d / 4 + e) * kRows + row);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             o[4 * e] = fmaf(x[e].x, f, o[4 * e]);
@@ -1014,7 +1046,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x < 2) a.jobs[2 * blockIdx.x + threadIdx.x] = sh.jobs[threadIdx.x];
-    if (warp == 10) {
+    if (warp == 12) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
@@ -1027,16 +1059,16 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 // a second kernel spreads the work over every SM, 128 rows of 8 dimensions an
 // item, four threads a row.  It always runs, and finds that there is nothing to do by looking at one
 // word a CTA and half.
-constexpr int kJoinThreads = 512, kJoinItems = kDim / 8, kJoinGroups = kJoinThreads / kTile;
+constexpr int kJoinThreads = 512, kJoinItems = kDim / 8, kJoinGroups = kJoinThreads / kRows;
 
 __global__ void __launch_bounds__(kJoinThreads)
 prompt_join_kernel(float *parts, const int4 *jobs, int ctas, __nv_bfloat16 *out, int Hq, int group) {
     __shared__ int found[kJoinThreads / 32], entry;
-    __shared__ float some[kJoinGroups][10][kTile];  // m, l and 8 dimensions of each group's parts
+    __shared__ float some[kJoinGroups][10][kRows];  // m, l and 8 dimensions of each group's parts
     pdl_wait_prerequisites();
     pdl_allow_dependents();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    const int row = threadIdx.x % kTile, mine_of = threadIdx.x / kTile;
+    const int row = threadIdx.x % kRows, mine_of = threadIdx.x / kRows;
     int before = 0;  // jobs of the entries seen so far
     for (int base = 0; base < 2 * ctas; base += kJoinThreads) {
         const int e = base + threadIdx.x;
@@ -1074,10 +1106,10 @@ prompt_join_kernel(float *parts, const int4 *jobs, int ctas, __nv_bfloat16 *out,
                     x[u][0] = x[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (i >= count) continue;
                     const float *q = segment_part(parts, first, i, turns, s);
-                    mq[u] = __ldcg(q + kTile * kDim + row);
-                    lq[u] = __ldcg(q + kTile * kDim + kTile + row);
-                    x[u][0] = __ldcg(reinterpret_cast<const float4 *>(q) + d / 4 * kTile + row);
-                    x[u][1] = __ldcg(reinterpret_cast<const float4 *>(q) + (d / 4 + 1) * kTile + row);
+                    mq[u] = __ldcg(q + kRows * kDim + row);
+                    lq[u] = __ldcg(q + kRows * kDim + kRows + row);
+                    x[u][0] = __ldcg(reinterpret_cast<const float4 *>(q) + d / 4 * kRows + row);
+                    x[u][1] = __ldcg(reinterpret_cast<const float4 *>(q) + (d / 4 + 1) * kRows + row);
                 }
                 float now = best;
 #pragma unroll
@@ -1150,7 +1182,7 @@ extern "C" size_t tts_prompt_attn_workspace_size(int32_t B, int32_t num_rows, in
                                                  int32_t head_dim) {
     using namespace tts;
     if (!prompt_shape_ok(B, num_rows, num_q_heads, num_kv_heads) || head_dim != kDim || B > kMaxStreams ||
-        num_q_heads / num_kv_heads > kTile)
+        num_q_heads / num_kv_heads > kRows)
         return 0;
     return prompt_workspace_bytes();
 }
@@ -1170,7 +1202,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     const int Hq = num_q_heads, Hkv = cache->num_kv_heads;
     if (!prompt_shape_ok(B, num_rows, Hq, Hkv)) return TTS_ERR_INVALID;
     if (cache->block_size != TTS_BLOCK_TOKENS || cache->dtype != TTS_BF16 || cache->head_dim != kDim) return TTS_ERR_UNSUPPORTED;
-    if (B > kMaxStreams || Hq / Hkv > kTile) return TTS_ERR_UNSUPPORTED;
+    if (B > kMaxStreams || Hq / Hkv > kRows) return TTS_ERR_UNSUPPORTED;
     const uint64_t pool_rows = static_cast<uint64_t>(cache->num_blocks) * Hkv * TTS_BLOCK_TOKENS;
     if (pool_rows >= (1ULL << 31)) return TTS_ERR_UNSUPPORTED;
     if (!aligned16(cache->k_pool) || !aligned16(cache->v_pool) || !aligned16(d_q) || !aligned16(d_out)) return TTS_ERR_INVALID;
@@ -1189,7 +1221,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     a.Hq = Hq;
     a.Hkv = Hkv;
     a.group = Hq / Hkv;
-    a.tokens = kTile / a.group;
+    a.tokens = kRows / a.group;
     // (no context passes 2^24 tokens)
     a.window = window < (1 << 25) ? window : 0;
     a.sinks = sinks < (1 << 24) ? sinks : 1 << 24;
@@ -1208,7 +1240,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     // the flat list of tiles is 32-bit
     const int64_t query_tiles = static_cast<int64_t>(num_rows) / (2 * a.tokens) + B;
     a.max_tiles = static_cast<int>(query_tiles);
-    if (query_tiles * Hkv * (max_blocks_per_seq / 8 + 1) >= (1LL << 30)) return TTS_ERR_UNSUPPORTED;
+    if (query_tiles * Hkv * (max_blocks_per_seq / kBlocks + 1 + kPartCost) >= (1LL << 30)) return TTS_ERR_UNSUPPORTED;
     CUtensorMap map_q, map_k, map_v;
     if (!make_tma_queries_bf16(&map_q, d_q, num_rows, Hq, a.group, a.tokens) ||
         !make_tma_2d_bf16(&map_k, cache->k_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64) ||
@@ -1218,7 +1250,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int rc = launch_kernel(prompt_attn_kernel, dim3(a.ctas), dim3(kThreads), kSmem, {cs, thread_pdl()}, map_q, map_k, map_v, a);
     // no segment has more than 2 * kSnap tiles: none is split
-    if (rc != TTS_OK || max_blocks_per_seq <= 2 * kSnap * kTile / TTS_BLOCK_TOKENS) return rc;
+    if (rc != TTS_OK || max_blocks_per_seq <= 2 * kSnap * kBlocks) return rc;
     return launch_kernel(prompt_join_kernel, dim3(a.ctas), dim3(kJoinThreads), 0, {cs, true}, a.part, a.jobs, a.ctas, a.out,
                          a.Hq, a.group);
 }
