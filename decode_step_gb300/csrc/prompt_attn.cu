@@ -181,9 +181,6 @@ struct Walk {
         ++k;
         if (--left > 0 && k == span.tiles) settle(a);
     }
-    __device__ __forceinline__ bool edge(const PromptArgs &a) const {
-        return tile_edge(a, tile() * kTile, ctx - n + r0(a) + 1, span.high);
-    }
 };
 
 // A place in a ring of slots and its barriers' parity.
@@ -836,8 +833,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             int limit = 0;                  // tokens up to the row's own
             int held = -1;                  // slot of the values of the last use, until it is given back
             float m = kNoScore, l = 0.0f;
+            const uint32_t first_lane = lane == 0, first_thread = threadIdx.x % 128 == 0;
+            // (a barrier takes more than a hundred cycles to answer: it is asked before
+            // other work, and waited for only where the answer was no)
+            bool there = false;
             for (uint32_t use = 0;; ++use) {
-                if (!quick_wait(&sh.s_full[s], use & 1, a.wait_limit)) {
+                if (!__all_sync(kFull, there) && !warp_wait(&sh.s_full[s], use & 1, a.wait_limit)) {
                     ok = false;
                     break;
                 }
@@ -859,13 +860,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&sh.s_empty[s]));
-                    if (w == 0) {
-                        mbar_arrive(smem_addr(&sh.k_empty[flags >> kSlotShift]));
-                        if (flags & kLast) mbar_arrive(smem_addr(&sh.q_empty));
-                    }
-                }
+                mbar_arrive_by(first_lane, smem_addr(&sh.s_empty[s]));
+                mbar_arrive_by(first_thread, smem_addr(&sh.k_empty[flags >> kSlotShift]));
+                mbar_arrive_by(first_thread && (flags & kLast), smem_addr(&sh.q_empty));
+                const bool free = use == 0 || mbar_test(smem_addr(&sh.o_done[s]), (use - 1) & 1);
                 if (flags & kMasked) {
                     const int t0 = info.t0;
 #pragma unroll
@@ -917,19 +915,20 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     sum[i % 2] = add2(sum[i % 2], pack2(e0, e1));
                     weights[i] = pack_bf16(e0, e1);
                 }
-                if (use && !quick_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
+                if (!__all_sync(kFull, free) && !warp_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
                     ok = false;
                     break;
                 }
+                there = mbar_test(smem_addr(&sh.s_full[s]), (use + 1) & 1);
                 tc_fence_after();
-                if (held >= 0 && threadIdx.x % 128 == 0) mbar_arrive(smem_addr(&sh.v_empty[held]));
+                mbar_arrive_by(first_thread && held >= 0, smem_addr(&sh.v_empty[max(held, 0)]));
                 held = flags >> kSlotShift;
                 tmem_st32(tp, weights);
                 tmem_st8(tp + 32, weights + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.p_full[s]));
+                mbar_arrive_by(first_lane, smem_addr(&sh.p_full[s]));
                 float sum0, sum1;
                 unpack2(add2(sum[0], sum[1]), sum0, sum1);
                 l += sum0 + sum1;
@@ -938,7 +937,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 ok = warp_wait(&sh.o_done[s], use & 1, a.wait_limit);
                 if (!ok) break;
                 tc_fence_after();
-                if (threadIdx.x % 128 == 0) mbar_arrive(smem_addr(&sh.v_empty[held]));
+                mbar_arrive_by(first_thread, smem_addr(&sh.v_empty[held]));
                 held = -1;
                 const PartInfo &p = sh.parts[(flags >> kPartShift) % kInfos];
                 const bool turns = p.mode == kTurns;
