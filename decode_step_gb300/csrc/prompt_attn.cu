@@ -152,7 +152,6 @@ struct Walk {
     __device__ __forceinline__ bool two(const PromptArgs &a) const { return r0(a) + a.tokens < n; }
     __device__ __forceinline__ int tiles() const { return min(left, span.tiles - k); }  // of the part, from its first one on
     __device__ __forceinline__ int mode(const PromptArgs &a) const { return two(a) ? kBoth : span.tiles >= kTakeTurns ? kTurns : 0; }
-    __device__ __forceinline__ int tile() const { return k < span.head ? k : k + span.skip; }
     __device__ __forceinline__ void seek(const PromptArgs &a) {  // b: the next stream that has rows
         for (; b < a.B; ++b) {
             const bool good = prompt_stream(a, b, &first, &n, &ctx);
@@ -313,6 +312,7 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
     auto each_tile = [&](auto &&f) {
         int b = start_b;
         int4 s = t0 < t1 ? streams[b] : make_int4(0, 0, 0, 0);
+#pragma unroll 1
         for (int t = t0; t < t1; ++t) {
             while (b + 1 < a.B && streams[b + 1].w <= t) s = streams[++b];
             f(b, t, t - s.w, span_of(a, s.y, s.z, t - s.w).tiles);
@@ -442,6 +442,7 @@ __device__ __noinline__ void find_odd(const PromptArgs &a, const PartInfo &part,
             if (id < 0 || id >= a.num_blocks) continue;
             const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v_pool) +
                                 ((static_cast<size_t>(id) * a.Hkv + part.g) * TTS_BLOCK_TOKENS + t % TTS_BLOCK_TOKENS) * kDim + d;
+#pragma unroll 1
             for (int e = 0; e < 32; ++e) {
                 const uint32_t w = v[e];
                 if ((w & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float(w << 16);
@@ -533,20 +534,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     pdl_allow_dependents();
     const uint32_t tmem = uniform(sh.tmem);
     const Ranges ranges{uniform(sh.q), uniform(sh.rem)};
-    Walk walk;
-    walk.left = uniform(sh.to - sh.from);
+    const int all_tiles = uniform(sh.to - sh.from);
     bool ok = true;
-    if (walk.left > 0) {
-        walk.b = uniform(sh.b);
-        walk.i = uniform(sh.i);
-        walk.g = uniform(sh.g);
-        walk.k = uniform(sh.k);
-        walk.s0 = uniform(sh.s0);
-        walk.first = uniform(sh.first);
-        walk.n = uniform(sh.n);
-        walk.ctx = uniform(sh.ctx);
-        walk.span = span_of(a, walk.n, walk.ctx, walk.i);
-        walk.settle(a);
+    if (all_tiles > 0) {
         if (warp >= 8) {
             if (warp == 8) {
                 // ---- producer.  Lane l looks up block l % 5 of the l / 5-th of the next six tiles
@@ -569,6 +559,18 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         return kNoBlock;
                     return __ldcg(a.table + static_cast<size_t>(w.b) * a.max_blocks + t / TTS_BLOCK_TOKENS);
                 };
+                Walk walk;
+                walk.left = all_tiles;
+                walk.b = uniform(sh.b);
+                walk.i = uniform(sh.i);
+                walk.g = uniform(sh.g);
+                walk.k = uniform(sh.k);
+                walk.s0 = uniform(sh.s0);
+                walk.first = uniform(sh.first);
+                walk.n = uniform(sh.n);
+                walk.ctx = uniform(sh.ctx);
+                walk.span = span_of(a, walk.n, walk.ctx, walk.i);
+                walk.settle(a);
                 int uses[2] = {0, 0};
                 int tiles = walk.tiles(), id = lookup(walk, tiles, 0);
                 for (bool begun = false; ok && walk.left > 0;) {
@@ -588,6 +590,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     const int next_tiles = next.left > 0 ? next.tiles() : 0;
                     int ahead = lookup(walk, tiles, kLookups), after = next.left > 0 ? lookup(next, next_tiles, 0) : kNoBlock;
                     int y = 0, good = 0;
+#pragma unroll 1
                     for (int j = 0; ok && j < tiles; ++j) {
                         const int from = j % kLookups * kBlocks;
                         if (from == 0) {
@@ -679,95 +682,83 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int s = warp - 9;
                 const uint32_t leader = elect_leader();
                 Place keys, values;  // of the next scores, and outputs
-                uint32_t uses = 0, outs = 0, parts = 0, part = 0, both = 0;
+                uint32_t uses = 0, outs = 0, parts = 0, both = 0;
                 bool go = true;
-                auto scores = [&](int q) {  // with the queries of half q
+                const uint32_t d_s = tmem + s * kHalf + kS, d_p = tmem + s * kHalf + kP, d_o = tmem + kO + s * kDim;
+                uint64_t queries = 0;
+                for (int left = all_tiles, part = 0; go && left > 0; ++part) {
+                    // (the producer's notes are there once the part's first keys are)
                     go = quick_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
-                    if (!go) return;
-                    WarpWaits<1> x;
-                    x.none(0);
-                    if (uses) x.set(0, &sh.s_empty[s], (uses - 1) & 1);
-                    ++uses;
-                    go = x.spin(a.wait_limit);
-                    if (!go) return;
-                    tc_fence_after();
-                    const uint32_t sa = q_base + 2 * q * kQueryBytes, sb = k_base + keys.slot * kSlotBytes;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_by(leader, tmem + s * kHalf + kS, sw128_desc(sa + kk / 4 * kQueryBytes + kk % 4 * 32),
-                                    sw128_desc(sb + kk / 4 * kChunkBytes + kk % 4 * 32), mma_idesc(kRows, kTile), kk != 0);
-                    mma_commit_by(leader, smem_addr(&sh.s_full[s]));
-                    keys.next();
-                };
-                auto outputs = [&](bool fresh) {
-                    WarpWaits<3> x;
-                    x.set(0, &sh.v_full[values.slot], values.phase);
-                    x.set(1, &sh.checked[values.slot], values.phase);
-                    x.none(2);
-                    if (fresh) {
-                        if (parts) x.set(2, &sh.o_empty[s], (parts - 1) & 1);
-                        ++parts;
-                    }
-                    go = x.wait(a.wait_limit);
-                    if (!go) return;
-                    WarpWaits<1> y;
-                    y.set(0, &sh.p_full[s], outs++ & 1);
-                    go = y.spin(a.wait_limit);
-                    if (!go) return;
-                    tc_fence_after();
-                    const uint32_t sb = v_base + values.slot * kSlotBytes;
-#pragma unroll
-                    for (int kk = 0; kk < kBlocks; ++kk)
-                        mma_ts_by(leader, tmem + kO + s * kDim, tmem + s * kHalf + kP + kk * 8,
-                                  sw128_mn_desc(sb + kk * kBlockBytes, kBlockBytes / 2), mma_idesc(kRows, kDim) | kTransposeB,
-                                  !fresh || kk != 0);
-                    mma_commit_by(leader, smem_addr(&sh.o_done[s]));
-                    values.next();
-                };
-                auto pass_keys = [&]() {
-                    go = warp_wait(&sh.k_full[keys.slot], keys.phase, a.wait_limit);
-                    if (go && lane == 0) mbar_arrive(smem_addr(&sh.k_empty[keys.slot]));
-                    keys.next();
-                };
-                auto pass_values = [&]() {
-                    WarpWaits<2> x;
-                    x.set(0, &sh.v_full[values.slot], values.phase);
-                    x.set(1, &sh.checked[values.slot], values.phase);
-                    go = x.wait(a.wait_limit);
-                    if (go && lane == 0) mbar_arrive(smem_addr(&sh.v_empty[values.slot]));
-                    values.next();
-                };
-                while (go && walk.left > 0) {
-                    const int tiles = walk.tiles(), mode = walk.mode(a);
-                    const int step = mode == kTurns ? 2 : 1, q = mode == kTurns ? 0 : s;
-                    int j = mode == kTurns ? s : s == 1 && mode == 0 ? tiles : 0;  // this half's first tile of the part
+                    if (!go) break;
+                    const volatile PartInfo &info = sh.parts[part % kInfos];
+                    const int tiles = uniform(info.tiles), mode = uniform(info.mode);
+                    left -= tiles;
+                    // the first half's tiles are all, the second's all or none; in turns every other one
+                    const int of = mode == kTurns ? 1 + s : s == 0 || mode == kBoth ? 3 : 0;  // bits: even, odd tiles
+                    const int lag = mode == kTurns ? 2 : 1;
+                    queries = sw128_desc(q_base + (mode == kTurns ? 0 : 2 * s * kQueryBytes));
                     {
                         WarpWaits<2> x;
-                        x.set(0, &sh.q_full[0], part++ & 1);
+                        x.set(0, &sh.q_full[0], part & 1);
                         x.none(1);
                         if (s == 1 && mode == kBoth) x.set(1, &sh.q_full[1], both++ & 1);
                         go = x.wait(a.wait_limit);
                     }
-                    if (go && j >= tiles) {
-                        if (lane == 0) mbar_arrive(smem_addr(&sh.q_empty));
-                        for (int i = 0; go && i < tiles; ++i) {
-                            pass_keys();
-                            if (go) pass_values();
+                    bool fresh = true;
+                    if (go && (of == 0 || (of == 2 && tiles == 1)) && lane == 0) mbar_arrive(smem_addr(&sh.q_empty));
+#pragma unroll 1
+                    for (int j = 0; go && j < tiles + lag; ++j) {
+                        if (j < tiles) {
+                            const bool work = (of >> (j & 1)) & 1;
+                            WarpWaits<2> x;
+                            x.set(0, &sh.k_full[keys.slot], keys.phase);
+                            x.none(1);
+                            if (work && uses) x.set(1, &sh.s_empty[s], (uses - 1) & 1);
+                            go = x.spin(a.wait_limit);
+                            if (!go) break;
+                            if (work) {
+                                ++uses;
+                                tc_fence_after();
+                                const uint64_t k0 = sw128_desc(k_base + keys.slot * kSlotBytes);
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)  // (descriptors count 16 bytes)
+                                    mma_bf16_by(leader, d_s, queries + (kk / 4 * kQueryBytes + kk % 4 * 32) / 16,
+                                                k0 + (kk / 4 * kChunkBytes + kk % 4 * 32) / 16, mma_idesc(kRows, kTile), kk != 0);
+                                mma_commit_by(leader, smem_addr(&sh.s_full[s]));
+                            } else {
+                                mbar_arrive_by(leader, smem_addr(&sh.k_empty[keys.slot]));
+                            }
+                            keys.next();
                         }
-                    } else if (go) {
-                        if (j) pass_keys();
-                        if (go) scores(q);
-                        if (go && j) pass_values();
-                        for (const int first = j; go && j < tiles; j += step) {
-                            if (step == 2 && j + 1 < tiles) pass_keys();
-                            if (go && j + step < tiles) scores(q);
-                            if (go) outputs(j == first);
-                            if (go && step == 2 && j + 1 < tiles) pass_values();
+                        if (j >= lag) {
+                            const bool work = (of >> ((j - lag) & 1)) & 1;
+                            WarpWaits<3> x;
+                            x.set(0, &sh.v_full[values.slot], values.phase);
+                            x.set(1, &sh.checked[values.slot], values.phase);
+                            x.none(2);
+                            if (work && fresh && outs) x.set(2, &sh.o_empty[s], (parts - 1) & 1);
+                            go = x.spin(a.wait_limit);
+                            if (!go) break;
+                            if (work) {
+                                WarpWaits<1> y;
+                                y.set(0, &sh.p_full[s], outs++ & 1);
+                                go = y.spin(a.wait_limit);
+                                if (!go) break;
+                                tc_fence_after();
+                                const uint64_t v0 = sw128_mn_desc(v_base + values.slot * kSlotBytes, kBlockBytes / 2);
+#pragma unroll
+                                for (int kk = 0; kk < kBlocks; ++kk)
+                                    mma_ts_by(leader, d_o, d_p + kk * 8, v0 + kk * kBlockBytes / 16,
+                                              mma_idesc(kRows, kDim) | kTransposeB, !fresh || kk != 0);
+                                mma_commit_by(leader, smem_addr(&sh.o_done[s]));
+                                if (fresh) ++parts;
+                                fresh = false;
+                            } else {
+                                mbar_arrive_by(leader, smem_addr(&sh.v_empty[values.slot]));
+                            }
+                            values.next();
                         }
                     }
-                    walk.left -= tiles - 1;
-                    walk.k += tiles - 1;
-                    walk.advance(a);
                 }
                 // nothing more for the softmax warps (their latest scores' barrier is
                 // complete: their weights were waited for)
@@ -783,12 +774,18 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 // row does not see whole.  (They keep step with every tile: a barrier's
                 // parity tells one use of a slot from the next, not from the one after.)
                 Place values;
-                for (int part = 1; ok && walk.left > 0; ++part) {
-                    const int tiles = walk.tiles(), first = walk.ctx - walk.n + walk.r0(a) + 1, high = walk.span.high;
+                for (int left = all_tiles, part = 1; ok && left > 0; ++part) {
+                    ok = quick_wait(&sh.v_full[values.slot], values.phase, a.wait_limit);
+                    if (!ok) break;
+                    const volatile PartInfo &info = sh.parts[(part - 1) % kInfos];
+                    const int tiles = uniform(info.tiles), first = uniform(info.ctx - info.n + info.r0 + 1), high = uniform(info.high);
+                    const int k0 = uniform(info.k), head = uniform(info.head), skip = uniform(info.skip);
+                    left -= tiles;
+#pragma unroll 1
                     for (int j = 0; j < tiles; ++j) {
                         ok = quick_wait(&sh.v_full[values.slot], values.phase, a.wait_limit);
                         if (!ok) break;
-                        const int k = walk.k + j, t0 = (k < walk.span.head ? k : k + walk.span.skip) * kTile;
+                        const int k = k0 + j, t0 = (k < head ? k : k + skip) * kTile;
                         if (tile_edge(a, t0, first, high)) {
                             uint8_t *v = raw + 4 * kQueryBytes + (kSlots + values.slot) * kSlotBytes;
                             const uint32_t from = smem_addr(v) + ((warp - 11) * 32 + lane) * 16;
@@ -801,9 +798,11 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             }
                             if (any & 0x80008000u) {  // rare
                                 bool odd = false;
+#pragma unroll 1
                                 for (int e = (warp - 11) * 32 + lane; e < kSlotBytes / 16; e += 64) {
                                     uint16_t *h = reinterpret_cast<uint16_t *>(v + e * 16);
                                     const int t = t0 + e / (kBlockBytes / 16) * TTS_BLOCK_TOKENS + e / 8 % TTS_BLOCK_TOKENS;
+#pragma unroll 1
                                     for (int i = 0; i < 8; ++i)
                                         if ((h[i] & 0x7F80u) == 0x7F80u) {
                                             h[i] = 0;
@@ -818,9 +817,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (lane == 0) mbar_arrive(smem_addr(&sh.checked[values.slot]));
                         values.next();
                     }
-                    walk.left -= tiles - 1;
-                    walk.k += tiles - 1;
-                    walk.advance(a);
                 }
             }
         } else {
@@ -894,6 +890,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     m = now;
                     l *= f;
                     if (!(flags & kFresh))
+#pragma unroll 1
                         for (int c = 0; c < kDim; c += 16) {
                             uint32_t o[16];
                             tmem_ld16_nowait(to + c, o);
@@ -950,6 +947,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int step = turns ? 2 : 1, j0 = turns ? s : 0;
                 if (count == 1) {
                     const float inv = inverse(l);
+#pragma unroll 1
                     for (int c = 0; c < kDim; c += 32) {
                         float f[32];
                         tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
@@ -965,6 +963,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const bool begins = static_cast<int>(blockIdx.x) == first || p.more == 0, alone = turns && p.tiles == 1;
                 const int from = p.more == 0 ? static_cast<int>(blockIdx.x) : first;  // the segment's first CTA
                 float *mine = part_slot(a.part, blockIdx.x, begins, s);
+#pragma unroll 1
                 for (int c = 0; c < kDim; c += 32) {
                     float f[32];
                     tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
@@ -1010,16 +1009,20 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (!ok) break;
                 if (!*reinterpret_cast<volatile int *>(&sh.last[s]) || !real) continue;
                 float best = kNoScore, total = 0.0f;
+#pragma unroll 1
                 for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, from, i, turns, s) + kRows * kDim + row));
+#pragma unroll 1
                 for (int i = 0; i < count; ++i) {
                     const float *q = segment_part(a.part, from, i, turns, s) + kRows * kDim + row;
                     total = fmaf(hw_ex2(__ldcg(q) - best), __ldcg(q + kRows), total);
                 }
                 const float inv = inverse(total);
+#pragma unroll 1
                 for (int d = 0; d < kDim; d += 32) {
                     float o[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+#pragma unroll 1
                     for (int i = 0; i < count; ++i) {
                         const float *q = segment_part(a.part, from, i, turns, s);
                         const float mq = __ldcg(q + kRows * kDim + row);
