@@ -53,7 +53,7 @@ constexpr int kSlots = 4;                   // tiles of keys, and of values, in 
 // Tensor memory: a half's S, its P (two weights a column), and both halves' O
 constexpr int kS = 0, kP = kTile, kHalf = 128, kO = 256;
 static_assert(kP + kTile / 2 <= kHalf);
-constexpr int kThreads = 416;               // two softmax warpgroups; producer, two issuers, two checkers
+constexpr int kThreads = 448;               // two softmax warpgroups; two issuers, two checkers, two producers
 constexpr int kMaxStreams = 4096;           // (their lengths are staged in shared memory)
 constexpr int kSnap = 2;                    // tiles
 constexpr int kPartCost = 2;                // what a segment costs beside its tiles, in tiles
@@ -217,13 +217,13 @@ struct PartInfo {
 struct __align__(8) TileInfo {
     int flags, t0;  // bits 0-4: blocks in the pool; then its part's note and its slot; first token
 };
-constexpr int kAllBlocks = (1 << kBlocks) - 1, kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12, kSlotShift = 16;
+constexpr int kAllBlocks = (1 << kBlocks) - 1, kPair = 0x80, kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12, kSlotShift = 16;
 constexpr int kInfos = 16;  // (the producer is at most six tiles ahead)
 constexpr int kLookups = 6;  // tiles whose blocks a warp looks up at once
 static_assert(kLookups * kBlocks <= 32);
 
 struct PromptShared {
-    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], checked[kSlots];
+    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], checked[kSlots], behind[kSlots];
     uint64_t q_full[2], q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_empty[2], stored[2], told[2], done[2];
     __align__(16) PartInfo parts[kInfos];
     TileInfo tiles[2][kInfos];  // by use of the half
@@ -494,6 +494,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             mbar_init(smem_addr(&sh.v_full[i]), 1);
             mbar_init(smem_addr(&sh.v_empty[i]), 2);
             mbar_init(smem_addr(&sh.checked[i]), 2);
+            mbar_init(smem_addr(&sh.behind[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sh.q_full[i]), 1);
@@ -538,16 +539,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     bool ok = true;
     if (all_tiles > 0) {
         if (warp >= 8) {
-            if (warp == 8) {
-                // ---- producer.  Lane l looks up block l % 5 of the l / 5-th of the next six tiles
+            if (warp == 8 || warp == 13) {
+                // ---- producers, of keys and of values.  Lane l looks up block l % 5 of the l / 5-th of the next six tiles
+                const bool for_keys = warp == 8;
                 const uint32_t leader = elect_leader();
                 uint32_t part = 0, q_count[2] = {0, 0};
-                Place keys, values;
-                auto room = [&](uint64_t *full, uint64_t *empty, const Place &at, uint32_t bytes) {
-                    if (at.again && !warp_wait(&empty[at.slot], at.phase ^ 1, a.wait_limit)) return false;
-                    mbar_expect_tx_by(leader, smem_addr(&full[at.slot]), bytes);
-                    return true;
-                };
+                Place at;
+                uint64_t *full = for_keys ? sh.k_full : sh.v_full;
                 // ids of the tiles from the part's j-th on (kNoBlock: no token of it is seen)
                 constexpr int kNoBlock = -0x7FFFFFFF;
                 auto lookup = [&](const Walk &w, int tiles, int j) {
@@ -575,7 +573,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 int tiles = walk.tiles(), id = lookup(walk, tiles, 0);
                 for (bool begun = false; ok && walk.left > 0;) {
                     const int mode = walk.mode(a), note = part % kInfos, r0 = walk.r0(a), before = walk.ctx - walk.n;
-                    if (lane == 0) {
+                    if (for_keys && lane == 0) {
                         const Shares shares = shares_of(ranges, walk.s0, walk.span.tiles);
                         PartInfo &p = sh.parts[note];
                         p.first = walk.first; p.n = walk.n; p.ctx = walk.ctx; p.b = walk.b;
@@ -589,11 +587,21 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     next.advance(a);
                     const int next_tiles = next.left > 0 ? next.tiles() : 0;
                     int ahead = lookup(walk, tiles, kLookups), after = next.left > 0 ? lookup(next, next_tiles, 0) : kNoBlock;
-                    int y = 0, good = 0;
+                    // the tiles that every row of a half sees whole begin in [from, to], or up to sinks
+                    int whole_from[2], whole_to[2];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const int row0 = r0 + (mode == kTurns ? 0 : s * a.tokens);
+                        whole_from[s] = a.window ? before + min(walk.n, row0 + a.tokens) - a.window : 0;
+                        whole_to[s] = before + row0 + 1 - kTile;
+                    }
+                    const int step = mode == kTurns ? 2 : 1;
+                    int y = 0, good = 0, from = kLookups * kBlocks;
 #pragma unroll 1
                     for (int j = 0; ok && j < tiles; ++j) {
-                        const int from = j % kLookups * kBlocks;
-                        if (from == 0) {
+                        from += kBlocks;
+                        if (from >= kLookups * kBlocks) {
+                            from = 0;
                             if (j) {
                                 id = ahead;
                                 ahead = lookup(walk, tiles, j + kLookups);
@@ -603,36 +611,45 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             y = here ? (id * a.Hkv + walk.g) * TTS_BLOCK_TOKENS : a.zero_row;
                             good = static_cast<int>(__ballot_sync(kFull, here));
                         }
-                        const int mask = (good >> from) & kAllBlocks;
-                        const int k = walk.k + j, t0 = (k < walk.span.head ? k : k + walk.span.skip) * kTile;
+                        if (for_keys) {
+                            const int mask = (good >> from) & kAllBlocks;
+                            const int k = walk.k + j, t0 = (k < walk.span.head ? k : k + walk.span.skip) * kTile;
+                            const int common = mask | (mode == kBoth ? kPair : 0) | (j < step ? kFresh : 0) |
+                                               (j >= tiles - step ? kLast : 0) | note << kPartShift |
+                                               static_cast<int>(at.slot) << kSlotShift;
 #pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            if (mode == kTurns ? s != j % 2 : s == 1 && mode != kBoth) continue;
-                            const int row0 = r0 + (mode == kTurns ? 0 : s * a.tokens);
-                            const bool masked = mask != kAllBlocks ||
-                                                tile_edge(a, t0, before + row0 + 1, before + min(walk.n, row0 + a.tokens));
-                            const bool fresh = j < (mode == kTurns ? 2 : 1), last = j >= tiles - (mode == kTurns ? 2 : 1);
-                            if (lane == 0)
-                                sh.tiles[s][uses[s] % kInfos] = {mask | (masked ? kMasked : 0) | (fresh ? kFresh : 0) |
-                                                                     (last ? kLast : 0) | note << kPartShift |
-                                                                     static_cast<int>(keys.slot) << kSlotShift, t0};
-                            uses[s] += 1;
+                            for (int s = 0; s < 2; ++s) {
+                                if (mode == kTurns ? s != j % 2 : s == 1 && mode != kBoth) continue;
+                                const bool whole = mask == kAllBlocks && t0 <= whole_to[s] &&
+                                                   (t0 >= whole_from[s] || t0 + kTile <= a.sinks);
+                                if (lane == 0) sh.tiles[s][uses[s] % kInfos] = {common | (whole ? 0 : kMasked), t0};
+                                uses[s] += 1;
+                            }
                         }
                         int ys[kBlocks];
 #pragma unroll
                         for (int i = 0; i < kBlocks; ++i) ys[i] = __shfl_sync(kFull, y, from + i);
-                        ok = room(sh.k_full, sh.k_empty, keys, kSlotBytes + (a.stall && !begun ? 16 : 0));
-                        if (!ok) break;
+                        if (at.again && !quick_wait(&(for_keys ? sh.k_empty : sh.v_empty)[at.slot], at.phase ^ 1, a.wait_limit)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t bar = smem_addr(&full[at.slot]);
+                        mbar_expect_tx_by(leader, bar, kSlotBytes + (a.stall && for_keys && !begun ? 16 : 0));
                         begun = true;
-                        {
-                            const uint32_t bar = smem_addr(&sh.k_full[keys.slot]), to = k_base + keys.slot * kSlotBytes;
+                        if (for_keys) {
+                            const uint32_t to = k_base + at.slot * kSlotBytes;
 #pragma unroll
                             for (int i = 0; i < 2 * kBlocks; ++i)
                                 tma_load_2d_by(leader, to + i / kBlocks * kChunkBytes + i % kBlocks * 2048, &map_k, i / kBlocks * 64,
                                                ys[i % kBlocks], bar);
-                            keys.next();
+                        } else {
+                            const uint32_t to = v_base + at.slot * kSlotBytes;
+#pragma unroll
+                            for (int i = 0; i < kBlocks; ++i) tma_load_rows_by(leader, to + i * kBlockBytes, &map_v, ys[i], bar);
                         }
-                        if (j == 0) {
+                        at.next();
+                        if (for_keys && j == 0) {
+                            // the part's queries
                             ok = part == 0 || warp_wait(&sh.q_empty, (part - 1) & 1, a.wait_limit);
                             if (!ok) break;
                             const int halves = mode == kBoth ? 2 : 1;
@@ -640,35 +657,26 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             q_count[1] += halves - 1;
                             if (lane == 0)
                                 for (int s = 0; s < halves; ++s) {
-                                    const uint32_t bar = smem_addr(&sh.q_full[s]);
-                                    mbar_arrive_expect_tx(bar, 2 * a.tokens * a.group * 128);
+                                    const uint32_t q_bar = smem_addr(&sh.q_full[s]);
+                                    mbar_arrive_expect_tx(q_bar, 2 * a.tokens * a.group * 128);
                                     for (int c = 0; c < 2; ++c)
                                         asm volatile(
                                             "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
                                             " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_base + (2 * s + c) * kQueryBytes),
                                             "l"(reinterpret_cast<uint64_t>(&map_q)), "r"(c * 64), "r"(walk.g * a.group),
-                                            "r"(walk.first + r0 + s * a.tokens), "r"(bar)
+                                            "r"(walk.first + r0 + s * a.tokens), "r"(q_bar)
                                             : "memory");
                                 }
                             __syncwarp();
-                            ++part;
-                        }
-                        ok = room(sh.v_full, sh.v_empty, values, kSlotBytes);
-                        if (!ok) break;
-                        {
-                            const uint32_t bar = smem_addr(&sh.v_full[values.slot]), to = v_base + values.slot * kSlotBytes;
-#pragma unroll
-                            for (int i = 0; i < kBlocks; ++i) tma_load_rows_by(leader, to + i * kBlockBytes, &map_v, ys[i], bar);
-                            values.next();
                         }
                     }
+                    ++part;
                     walk = next;
                     tiles = next_tiles;
                     id = after;
                 }
                 // every copy lands before the CTA ends
-                keys.drain(sh.k_full);
-                values.drain(sh.v_full);
+                at.drain(full);
                 for (uint32_t s = 0; s < 2; ++s)
                     if (q_count[s]) warp_wait(&sh.q_full[s], (q_count[s] - 1) & 1);
             } else if (warp <= 10) {
@@ -682,7 +690,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int s = warp - 9;
                 const uint32_t leader = elect_leader();
                 Place keys, values;  // of the next scores, and outputs
-                uint32_t uses = 0, outs = 0, parts = 0, both = 0;
+                uint32_t uses = 0, outs = 0, parts = 0, both = 0, behind = 0;
                 bool go = true;
                 const uint32_t d_s = tmem + s * kHalf + kS, d_p = tmem + s * kHalf + kP, d_o = tmem + kO + s * kDim;
                 uint64_t queries = 0;
@@ -715,6 +723,12 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             x.none(1);
                             if (work && uses) x.set(1, &sh.s_empty[s], (uses - 1) & 1);
                             go = x.spin(a.wait_limit);
+                            if (go && s == 1 && mode == kBoth) {
+                                // half 1 stays half a step behind (its exponentials while half
+                                // 0 waits and loads, not at the same time)
+                                go = quick_wait(&sh.behind[keys.slot], behind >> keys.slot & 1, a.wait_limit);
+                                behind ^= 1u << keys.slot;
+                            }
                             if (!go) break;
                             if (work) {
                                 ++uses;
@@ -926,6 +940,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tc_fence_before();
                 __syncwarp();
                 mbar_arrive_by(first_lane, smem_addr(&sh.p_full[s]));
+                mbar_arrive_by(threadIdx.x == 0 && (flags & kPair), smem_addr(&sh.behind[flags >> kSlotShift]));
                 float sum0, sum1;
                 unpack2(add2(sum[0], sum[1]), sum0, sum1);
                 l += sum0 + sum1;
