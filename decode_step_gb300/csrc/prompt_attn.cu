@@ -49,11 +49,18 @@ constexpr int kQueryBytes = kRows * 128;    // [128 rows][64 values], 128-byte s
 constexpr int kChunkBytes = kTile * 128;    // [80 tokens][64 values]
 constexpr int kSlotBytes = 2 * kChunkBytes; // a tile of keys, or of values block by block: [5][2][16 tokens][64 values]
 constexpr int kBlockBytes = 4096;           // a block's values of a head
-constexpr int kSlots = 4;                   // tiles of keys, and of values, in the ring
+__host__ __device__ constexpr int prompt_slots(bool fp8) { return fp8 ? 2 : 4; }  // tiles of keys, and of values, in the ring
+constexpr int kRawSlots = 3, kRawBytes = kBlocks * 2048;       // FP8: tiles of codes on their way, of keys and of values
+constexpr int kRecordBytes = 4224, kScaleStages = 8, kScaleBytes = kBlocks * 128;
+// FP8: weights times the value's scale times 2^8 in f16, as tts_decode_attn has them
+constexpr float kFp8Fix = 0x1p8f;
 // Tensor memory: a half's S, its P (two weights a column), and both halves' O
 constexpr int kS = 0, kP = kTile, kHalf = 128, kO = 256;
 static_assert(kP + kTile / 2 <= kHalf);
-constexpr int kThreads = 448;               // two softmax warpgroups; two issuers, two checkers, two producers
+// Two softmax warpgroups; two issuers, two checkers, two producers; FP8: four
+// converters instead of the checkers
+__host__ __device__ constexpr int prompt_threads(bool fp8) { return fp8 ? 512 : 448; }
+constexpr int kMostThreads = 512;
 constexpr int kMaxStreams = 4096;           // (their lengths are staged in shared memory)
 constexpr int kSnap = 2;                    // tiles
 constexpr int kPartCost = 2;                // what a segment costs beside its tiles, in tiles
@@ -61,7 +68,9 @@ constexpr int kMinTiles = 6;                // tiles a CTA at least, where there
 constexpr float kLog2e = 1.4426950408889634f;
 // Running maximum before any token (log2 units): no finite score is below it.
 constexpr float kNoScore = -FLT_MAX;
-constexpr float kSlack = 8.0f;              // scores may pass it by this much before it moves (log2 units)
+// Scores may pass it by this much before it moves (log2 units); in FP8 weights stay
+// at 1 at most, so that with a scale below 256 they are in f16's range.
+__host__ __device__ constexpr float prompt_slack(bool fp8) { return fp8 ? 0.0f : 8.0f; }
 constexpr int kPartFloats = kRows * kDim + 2 * kRows;  // o, m, l of a half
 constexpr int kTakeTurns = 12;              // tiles of a segment from which on its one half's rows use both
 constexpr int kJoinHere = 4;                // parts that the last CTA joins; more are left to the second kernel
@@ -74,7 +83,7 @@ struct PromptArgs {
     int B, num_rows, Hq, Hkv, group, tokens;  // tokens: of a half
     int window, sinks;                        // window 0: none
     float scale_log2;
-    const uint8_t *v_pool;
+    const uint8_t *k_pool, *v_pool;           // FP8: the records, and none
     __nv_bfloat16 *out;
     float *part;          // [CTA][first, later part][half] partial results
     int32_t *tickets;     // [CTA][half]
@@ -183,6 +192,7 @@ struct Walk {
 };
 
 // A place in a ring of slots and its barriers' parity.
+template <int kSlots>
 struct Place {
     uint32_t slot = 0, phase = 0;
     bool again = false;  // the ring has been through once
@@ -214,29 +224,44 @@ struct PartInfo {
     int k, head, skip, low;       // first tile of the part; Span
     int high, shares, more, mode; // first CTA of the segment, CTAs that follow
 };
-struct __align__(8) TileInfo {
-    int flags, t0;  // bits 0-4: blocks in the pool; then its part's note and its slot; first token
+// The same of a part's values, by their producer, which may be ahead of the keys'.
+struct ValueInfo {
+    int tiles, first, high, k, head, skip;  // first, high: tokens up to the first and the last row's own
 };
-constexpr int kAllBlocks = (1 << kBlocks) - 1, kPair = 0x80, kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12, kSlotShift = 16;
-constexpr int kInfos = 16;  // (the producer is at most six tiles ahead)
+struct __align__(8) TileInfo {
+    int flags, t0;  // bits 0-4: blocks in the pool; then its part's note, its slot and its scales' stage; first token
+};
+constexpr int kAllBlocks = (1 << kBlocks) - 1, kPair = 0x80, kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12, kSlotShift = 16, kStageShift = 18;
+constexpr int kInfos = 8;  // (the producers are at most six tiles ahead)
 constexpr int kLookups = 6;  // tiles whose blocks a warp looks up at once
 static_assert(kLookups * kBlocks <= 32);
 
 struct PromptShared {
-    uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots], checked[kSlots], behind[kSlots];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], checked[4], behind[4];
+    uint64_t raw_full[2][kRawSlots], raw_empty[2][kRawSlots], q_raw[2];  // FP8: of keys, values; the queries before f16
     uint64_t q_full[2], q_empty, s_full[2], s_empty[2], p_full[2], o_done[2], o_empty[2], stored[2], told[2], done[2];
     __align__(16) PartInfo parts[kInfos];
+    ValueInfo values[kInfos];
     TileInfo tiles[2][kInfos];  // by use of the half
     int4 jobs[2];
+    int v_valid[kInfos];   // FP8: blocks of a tile of values in the pool
     uint32_t tmem;
     int odd[8];            // number of the part whose tiles held values that are not finite, by number % 8
     int last[2];           // whether the half's part was the last one
-    long long scan[2][kThreads / 32];
+    long long scan[2][kMostThreads / 32];
     int b, i, g, k, s0, first, n, ctx, from, to, q, rem;
 };
-constexpr int kSmem = 4 * kQueryBytes + 2 * kSlots * kSlotBytes + static_cast<int>(sizeof(PromptShared));
-static_assert(kSmem <= 227 * 1024);
-static_assert(kMaxStreams * 16 <= 2 * kSlots * kSlotBytes);
+// Shared memory: the queries, the ring of keys, of values, in FP8 the codes of
+// either and the scales, and PromptShared.
+template <bool kFp8>
+struct PromptSmem {
+    static constexpr int keys = 4 * kQueryBytes, values = keys + prompt_slots(kFp8) * kSlotBytes;
+    static constexpr int raw = values + prompt_slots(kFp8) * kSlotBytes, scales = raw + (kFp8 ? 2 * kRawSlots * kRawBytes : 0);
+    static constexpr int shared = scales + (kFp8 ? kScaleStages * kScaleBytes : 0);
+    static constexpr int total = shared + static_cast<int>(sizeof(PromptShared));
+    static_assert(total <= 227 * 1024);
+    static_assert(kMaxStreams * 16 <= scales - keys);
+};
 
 // Zeros in the rows of the refused streams (rare), by every thread of the grid.
 __device__ __noinline__ void zero_refused(const PromptArgs &a) {
@@ -253,6 +278,7 @@ __device__ __noinline__ void zero_refused(const PromptArgs &a) {
 }
 
 // Sum over the threads before this one, and over all.
+template <int kThreads>
 __device__ __forceinline__ long long scan_before(long long mine, long long *warps, long long *all) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     long long incl = mine;
@@ -275,6 +301,7 @@ __device__ __forceinline__ long long scan_before(long long mine, long long *warp
 
 // Finds the CTA's range: sh.b, i, g, k, s0 (its first tile) and sh.from, to.
 // `streams`: room for kMaxStreams + 1.  Every thread calls it.
+template <int kThreads>
 __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh, int4 *streams) {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
@@ -287,7 +314,7 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
         streams[b] = make_int4(first, n, ctx, 0);
     }
     long long all_tiles;
-    long long at = scan_before(mine, sh.scan[0], &all_tiles);
+    long long at = scan_before<kThreads>(mine, sh.scan[0], &all_tiles);
     // (more than these only if the streams' rows overlap)
     const bool apart = all_tiles <= a.max_tiles;
     const int tiles = apart ? static_cast<int>(all_tiles) : 0;
@@ -320,7 +347,7 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
     };
     long long sum = 0, total;
     each_tile([&](int, int, int, int n) { sum += kPartCost + n; });
-    const long long before = scan_before(sum, sh.scan[1], &total) * a.Hkv;
+    const long long before = scan_before<kThreads>(sum, sh.scan[1], &total) * a.Hkv;
     const int T = static_cast<int>(total) * a.Hkv;  // (below 2^30, as the host has seen to)
     const int segments = tiles * a.Hkv;
     const int W = min(min(a.ctas, T), max((T + kMinTiles - 1) / kMinTiles, segments));
@@ -393,6 +420,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
 }
+// Four E4M3 codes as two f16 pairs: exact.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint32_t bf16_to_f16(uint32_t w) { return pack_f16(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Codes of 0x7F or 0xFF (not a number) of a word become 0.
+__device__ __forceinline__ void drop_odd(uint32_t &w) {
+    const uint32_t bad = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // 0x80 in such a byte
+    w &= ~((bad >> 7) * 0xFFu);
+}
+// Operand whose 8 x 16-byte pieces are contiguous (no swizzle), the contraction
+// side's next eight values `lead` bytes on, the other side's next eight rows `stride`.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lead >> 4) << 16) |
+           (static_cast<uint64_t>(stride >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
 // Two fp32 operations an instruction, and the largest of three.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
@@ -431,6 +486,7 @@ __device__ __forceinline__ uint32_t bits_before(int t, int base) {
 
 // Values of this row's tokens that are not finite, of 32 dimensions from d on,
 // added up in o (rare): those of the tiles that the checkers cleared.
+template <bool kFp8>
 __device__ __noinline__ void find_odd(const PromptArgs &a, const PartInfo &part, int step, int j, int limit, int d, float *o) {
     const int first_limit = part.ctx - part.n + part.r0 + 1;
     for (; j < part.tiles; j += step) {
@@ -440,20 +496,26 @@ __device__ __noinline__ void find_odd(const PromptArgs &a, const PartInfo &part,
             if (a.window && t >= a.sinks && t < limit - a.window) continue;
             const int id = __ldcg(a.table + static_cast<size_t>(part.b) * a.max_blocks + t / TTS_BLOCK_TOKENS);
             if (id < 0 || id >= a.num_blocks) continue;
-            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.v_pool) +
-                                ((static_cast<size_t>(id) * a.Hkv + part.g) * TTS_BLOCK_TOKENS + t % TTS_BLOCK_TOKENS) * kDim + d;
+            const size_t tile = static_cast<size_t>(id) * a.Hkv + part.g;
+            const int slot = t % TTS_BLOCK_TOKENS;
 #pragma unroll 1
             for (int e = 0; e < 32; ++e) {
-                const uint32_t w = v[e];
-                if ((w & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float(w << 16);
+                if constexpr (kFp8) {
+                    const uint8_t code = a.k_pool[tile * kRecordBytes + 2048 + 16 * (d + e) + 4 * (slot % 8 / 2) + slot % 2 + 2 * (slot / 8)];
+                    if ((code & 0x7F) == 0x7F) o[e] = __uint_as_float(0x7FC00000u);
+                } else {
+                    const uint32_t w = reinterpret_cast<const uint16_t *>(a.v_pool)[(tile * TTS_BLOCK_TOKENS + slot) * kDim + d + e];
+                    if ((w & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float(w << 16);
+                }
             }
         }
     }
 }
+template <bool kFp8>
 __device__ __forceinline__ void add_odd(const PromptArgs &a, const PartInfo &part, int step, int j, int limit, int d, float *f) {
     float o[32];
     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-    find_odd(a, part, step, j, limit, d, o);
+    find_odd<kFp8>(a, part, step, j, limit, d, o);
 #pragma unroll
     for (int i = 0; i < 32; ++i) f[i] += o[i];
 }
@@ -480,24 +542,32 @@ __device__ __forceinline__ float *segment_part(float *parts, int first, int i, b
     return part_slot(parts, first + c, c == 0, turns ? i % 2 : s);
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool kFp8>
+__global__ void __launch_bounds__(prompt_threads(kFp8), 1)
 prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+    constexpr int kThreads = prompt_threads(kFp8), kSlots = prompt_slots(kFp8);
+    using Smem = PromptSmem<kFp8>;
     extern __shared__ __align__(1024) uint8_t raw[];
-    const uint32_t q_base = smem_addr(raw), k_base = q_base + 4 * kQueryBytes, v_base = k_base + kSlots * kSlotBytes;
-    PromptShared &sh = *reinterpret_cast<PromptShared *>(raw + 4 * kQueryBytes + 2 * kSlots * kSlotBytes);
+    const uint32_t q_base = smem_addr(raw), k_base = q_base + Smem::keys, v_base = q_base + Smem::values;
+    PromptShared &sh = *reinterpret_cast<PromptShared *>(raw + Smem::shared);
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     if (warp == 11 && lane == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(smem_addr(&sh.k_full[i]), 1);
+            mbar_init(smem_addr(&sh.k_full[i]), kFp8 ? 2 : 1);
             mbar_init(smem_addr(&sh.k_empty[i]), 2);  // (a half each, by who is done with the slot)
-            mbar_init(smem_addr(&sh.v_full[i]), 1);
+            mbar_init(smem_addr(&sh.v_full[i]), kFp8 ? 2 : 1);
             mbar_init(smem_addr(&sh.v_empty[i]), 2);
             mbar_init(smem_addr(&sh.checked[i]), 2);
             mbar_init(smem_addr(&sh.behind[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sh.q_full[i]), 1);
+            mbar_init(smem_addr(&sh.q_full[i]), kFp8 ? 4 : 1);
+            mbar_init(smem_addr(&sh.q_raw[i]), 1);
+            for (int j = 0; j < kRawSlots; ++j) {
+                mbar_init(smem_addr(&sh.raw_full[i][j]), 1);
+                mbar_init(smem_addr(&sh.raw_empty[i][j]), 2);
+            }
             mbar_init(smem_addr(&sh.s_full[i]), 1);
             mbar_init(smem_addr(&sh.s_empty[i]), 4);
             mbar_init(smem_addr(&sh.p_full[i]), 4);
@@ -515,8 +585,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     }
     if (warp == 8 && lane == 0) {
         prefetch_tensormap(&map_q);
-        prefetch_tensormap(&map_k);
-        prefetch_tensormap(&map_v);
+        if constexpr (!kFp8) {
+            prefetch_tensormap(&map_k);
+            prefetch_tensormap(&map_v);
+        }
     }
     pdl_wait_prerequisites();
     // (tensor memory only after the wait: the kernel before may be one that
@@ -526,7 +598,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    find_range(a, sh, reinterpret_cast<int4 *>(raw + 4 * kQueryBytes));
+    find_range<kThreads>(a, sh, reinterpret_cast<int4 *>(raw + Smem::keys));
     // (the staged lengths make way for copies)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
@@ -544,8 +616,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const bool for_keys = warp == 8;
                 const uint32_t leader = elect_leader();
                 uint32_t part = 0, q_count[2] = {0, 0};
-                Place at;
-                uint64_t *full = for_keys ? sh.k_full : sh.v_full;
+                Place<kFp8 ? kRawSlots : kSlots> at;
+                uint64_t *full = kFp8 ? sh.raw_full[!for_keys] : for_keys ? sh.k_full : sh.v_full;
+                uint64_t *empty = kFp8 ? sh.raw_empty[!for_keys] : for_keys ? sh.k_empty : sh.v_empty;
+                uint32_t tile = 0;  // of the CTA
                 // ids of the tiles from the part's j-th on (kNoBlock: no token of it is seen)
                 constexpr int kNoBlock = -0x7FFFFFFF;
                 auto lookup = [&](const Walk &w, int tiles, int j) {
@@ -581,6 +655,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         p.k = walk.k; p.head = walk.span.head; p.skip = walk.span.skip; p.low = walk.span.low;
                         p.high = walk.span.high; p.shares = shares.first; p.more = shares.more; p.mode = mode;
                     }
+                    if (!for_keys && lane == 0)
+                        sh.values[note] = {tiles, before + r0 + 1, walk.span.high, walk.k, walk.span.head, walk.span.skip};
                     Walk next = walk;
                     next.left -= tiles - 1;
                     next.k += tiles - 1;
@@ -616,7 +692,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             const int k = walk.k + j, t0 = (k < walk.span.head ? k : k + walk.span.skip) * kTile;
                             const int common = mask | (mode == kBoth ? kPair : 0) | (j < step ? kFresh : 0) |
                                                (j >= tiles - step ? kLast : 0) | note << kPartShift |
-                                               static_cast<int>(at.slot) << kSlotShift;
+                                               static_cast<int>(tile % kSlots) << kSlotShift |
+                                               static_cast<int>(tile % kScaleStages) << kStageShift;
 #pragma unroll
                             for (int s = 0; s < 2; ++s) {
                                 if (mode == kTurns ? s != j % 2 : s == 1 && mode != kBoth) continue;
@@ -629,25 +706,43 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         int ys[kBlocks];
 #pragma unroll
                         for (int i = 0; i < kBlocks; ++i) ys[i] = __shfl_sync(kFull, y, from + i);
-                        if (at.again && !quick_wait(&(for_keys ? sh.k_empty : sh.v_empty)[at.slot], at.phase ^ 1, a.wait_limit)) {
+                        if (at.again && !quick_wait(&empty[at.slot], at.phase ^ 1, a.wait_limit)) {
                             ok = false;
                             break;
                         }
-                        const uint32_t bar = smem_addr(&full[at.slot]);
-                        mbar_expect_tx_by(leader, bar, kSlotBytes + (a.stall && for_keys && !begun ? 16 : 0));
+                        const uint32_t bar = smem_addr(&full[at.slot]), more = a.stall && for_keys && !begun ? 16 : 0;
                         begun = true;
-                        if (for_keys) {
+                        if constexpr (kFp8) {
+                            // codes (and with the keys' the scales) of the blocks that are in the pool
+                            const int here = (good >> from) & kAllBlocks;
+                            if (!for_keys && lane == 0) sh.v_valid[tile % kInfos] = here;
+                            __syncwarp();
+                            mbar_expect_tx_by(leader, bar, __popc(here) * (for_keys ? 2048 + 128 : 2048) + more);
+                            const uint32_t to = q_base + Smem::raw + ((for_keys ? 0 : kRawSlots) + at.slot) * kRawBytes;
+                            const uint32_t scales = q_base + Smem::scales + tile % kScaleStages * kScaleBytes;
+#pragma unroll
+                            for (int i = 0; i < kBlocks; ++i)
+                                if ((here >> i) & 1 && leader) {
+                                    const uint8_t *record = a.k_pool + static_cast<size_t>(ys[i] / TTS_BLOCK_TOKENS) * kRecordBytes;
+                                    bulk_load_nohint(to + i * 2048, record + (for_keys ? 0 : 2048), 2048, bar);
+                                    if (for_keys) bulk_load_nohint(scales + i * 128, record + 4096, 128, bar);
+                                }
+                            __syncwarp();
+                        } else if (for_keys) {
+                            mbar_expect_tx_by(leader, bar, kSlotBytes + more);
                             const uint32_t to = k_base + at.slot * kSlotBytes;
 #pragma unroll
                             for (int i = 0; i < 2 * kBlocks; ++i)
                                 tma_load_2d_by(leader, to + i / kBlocks * kChunkBytes + i % kBlocks * 2048, &map_k, i / kBlocks * 64,
                                                ys[i % kBlocks], bar);
                         } else {
+                            mbar_expect_tx_by(leader, bar, kSlotBytes);
                             const uint32_t to = v_base + at.slot * kSlotBytes;
 #pragma unroll
                             for (int i = 0; i < kBlocks; ++i) tma_load_rows_by(leader, to + i * kBlockBytes, &map_v, ys[i], bar);
                         }
                         at.next();
+                        ++tile;
                         if (for_keys && j == 0) {
                             // the part's queries
                             ok = part == 0 || warp_wait(&sh.q_empty, (part - 1) & 1, a.wait_limit);
@@ -657,7 +752,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             q_count[1] += halves - 1;
                             if (lane == 0)
                                 for (int s = 0; s < halves; ++s) {
-                                    const uint32_t q_bar = smem_addr(&sh.q_full[s]);
+                                    const uint32_t q_bar = smem_addr(kFp8 ? &sh.q_raw[s] : &sh.q_full[s]);
                                     mbar_arrive_expect_tx(q_bar, 2 * a.tokens * a.group * 128);
                                     for (int c = 0; c < 2; ++c)
                                         asm volatile(
@@ -678,8 +773,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 // every copy lands before the CTA ends
                 at.drain(full);
                 for (uint32_t s = 0; s < 2; ++s)
-                    if (q_count[s]) warp_wait(&sh.q_full[s], (q_count[s] - 1) & 1);
-            } else if (warp <= 10) {
+                    if (q_count[s]) warp_wait(kFp8 ? &sh.q_raw[s] : &sh.q_full[s], (q_count[s] - 1) & 1);
+            } else if (warp == 9 || warp == 10) {
                 // ---- MMA issuers, one a half: S(j + 1) O(j), or, where the halves take
                 // turns, S(j + 2) O(j).  The next scores need only that the last ones were
                 // read, so that the softmax warps find theirs when they come.  (A commit or
@@ -689,7 +784,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 // from the one after.
                 const int s = warp - 9;
                 const uint32_t leader = elect_leader();
-                Place keys, values;  // of the next scores, and outputs
+                Place<kSlots> keys, values;  // of the next scores, and outputs
                 uint32_t uses = 0, outs = 0, parts = 0, both = 0, behind = 0;
                 bool go = true;
                 const uint32_t d_s = tmem + s * kHalf + kS, d_p = tmem + s * kHalf + kP, d_o = tmem + kO + s * kDim;
@@ -737,7 +832,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                                 for (int kk = 0; kk < 8; ++kk)  // (descriptors count 16 bytes)
                                     mma_bf16_by(leader, d_s, queries + (kk / 4 * kQueryBytes + kk % 4 * 32) / 16,
-                                                k0 + (kk / 4 * kChunkBytes + kk % 4 * 32) / 16, mma_idesc(kRows, kTile), kk != 0);
+                                                k0 + (kk / 4 * kChunkBytes + kk % 4 * 32) / 16,
+                                                kFp8 ? mma_idesc_f16(kRows, kTile) : mma_idesc(kRows, kTile), kk != 0);
                                 mma_commit_by(leader, smem_addr(&sh.s_full[s]));
                             } else {
                                 mbar_arrive_by(leader, smem_addr(&sh.k_empty[keys.slot]));
@@ -748,8 +844,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             const bool work = (of >> ((j - lag) & 1)) & 1;
                             WarpWaits<3> x;
                             x.set(0, &sh.v_full[values.slot], values.phase);
-                            x.set(1, &sh.checked[values.slot], values.phase);
+                            x.none(1);
                             x.none(2);
+                            if constexpr (!kFp8) x.set(1, &sh.checked[values.slot], values.phase);
                             if (work && fresh && outs) x.set(2, &sh.o_empty[s], (parts - 1) & 1);
                             go = x.spin(a.wait_limit);
                             if (!go) break;
@@ -759,11 +856,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                 go = y.spin(a.wait_limit);
                                 if (!go) break;
                                 tc_fence_after();
-                                const uint64_t v0 = sw128_mn_desc(v_base + values.slot * kSlotBytes, kBlockBytes / 2);
+                                // (FP8: a block's values as [2][128 dimensions][8 tokens])
+                                const uint32_t v_at = v_base + values.slot * kSlotBytes;
+                                const uint64_t v0 = kFp8 ? plain_desc(v_at, kBlockBytes / 2, 128) : sw128_mn_desc(v_at, kBlockBytes / 2);
 #pragma unroll
                                 for (int kk = 0; kk < kBlocks; ++kk)
                                     mma_ts_by(leader, d_o, d_p + kk * 8, v0 + kk * kBlockBytes / 16,
-                                              mma_idesc(kRows, kDim) | kTransposeB, !fresh || kk != 0);
+                                              kFp8 ? mma_idesc_f16(kRows, kDim) : mma_idesc(kRows, kDim) | kTransposeB,
+                                              !fresh || kk != 0);
                                 mma_commit_by(leader, smem_addr(&sh.o_done[s]));
                                 if (fresh) ++parts;
                                 fresh = false;
@@ -783,16 +883,125 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 __syncwarp();
                 mma_commit_by(leader, smem_addr(&sh.done[s]));
                 ok = warp_wait(&sh.done[s], 0) && go;
+            } else if constexpr (kFp8) {
+                // ---- converters: warps 11 and 12 keys, 14 and 15 values; all the queries.
+                // Codes are exact in f16; the scales go to the scores and the weights.
+                const bool for_keys = warp < 13;
+                const int me = (warp & 1) ^ (for_keys ? 1 : 0);  // of two
+                Place<kRawSlots> from;
+                Place<kSlots> to;
+                uint64_t *empty = for_keys ? sh.k_empty : sh.v_empty, *full = for_keys ? sh.k_full : sh.v_full;
+                uint32_t tile = 0, both = 0;
+                auto give_up = [&](bool good) { return ok = good; };
+                for (int left = all_tiles, part = 0; ok && left > 0; ++part) {
+                    if (!give_up(quick_wait(&sh.raw_full[!for_keys][from.slot], from.phase, a.wait_limit))) break;
+                    // (the notes on the queries come with them, those on the tiles with the codes)
+                    if (!give_up(warp_wait(&sh.q_raw[0], part & 1, a.wait_limit))) break;
+                    const int mode = uniform(static_cast<const volatile PartInfo &>(sh.parts[part % kInfos]).mode);
+                    int tiles, first = 0, high = 0, k0 = 0, head = 0, skip = 0;
+                    if (for_keys) {
+                        tiles = uniform(static_cast<const volatile PartInfo &>(sh.parts[part % kInfos]).tiles);
+                    } else {
+                        const volatile ValueInfo &info = sh.values[part % kInfos];
+                        tiles = uniform(info.tiles);
+                        first = uniform(info.first);
+                        high = uniform(info.high);
+                        k0 = uniform(info.k);
+                        head = uniform(info.head);
+                        skip = uniform(info.skip);
+                    }
+                    left -= tiles;
+                    for (int s = 0; s < (mode == kBoth ? 2 : 1); ++s) {
+                        if (s == 1 && !give_up(warp_wait(&sh.q_raw[1], both++ & 1, a.wait_limit))) break;
+                        const uint32_t q = q_base + 2 * s * kQueryBytes + ((for_keys ? 0 : 2) + me) * (kQueryBytes / 2) + lane * 16;
+#pragma unroll 4
+                        for (int e = 0; e < kQueryBytes / 2; e += 512) {
+                            const uint4 x = lds128(q + e);
+                            sts128(q + e, bf16_to_f16(x.x), bf16_to_f16(x.y), bf16_to_f16(x.z), bf16_to_f16(x.w));
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        mbar_arrive_by(lane == 0, smem_addr(&sh.q_full[s]));
+                    }
+                    if (!ok) break;
+#pragma unroll 1
+                    for (int j = 0; j < tiles; ++j, ++tile) {
+                        if (!give_up(quick_wait(&sh.raw_full[!for_keys][from.slot], from.phase, a.wait_limit))) break;
+                        if (to.again && !give_up(quick_wait(&empty[to.slot], to.phase ^ 1, a.wait_limit))) break;
+                        const uint32_t codes = q_base + Smem::raw + ((for_keys ? 0 : kRawSlots) + from.slot) * kRawBytes;
+                        const uint32_t out = (for_keys ? k_base : v_base) + to.slot * kSlotBytes;
+                        if (for_keys) {
+                            // 16 codes of a token: 16-byte piece p of row r, which holds dimensions 16 (p ^ r % 8) on
+#pragma unroll 2
+                            for (int e = me * 32 + lane; e < kRawBytes / 16; e += 64) {
+                                const int r = e / 8, c = e % 8 ^ (r & 7);
+                                const uint4 x = lds128(codes + e * 16);
+                                uint32_t h[8];
+                                codes_to_f16(x.x, h[0], h[1]);
+                                codes_to_f16(x.y, h[2], h[3]);
+                                codes_to_f16(x.z, h[4], h[5]);
+                                codes_to_f16(x.w, h[6], h[7]);
+                                const uint32_t at = out + c / 4 * kChunkBytes + r * 128, q = c % 4 * 2;
+                                // (the two halves' stores on different banks)
+                                const bool second = c >= 4;
+                                sts128(at + (((q + second) ^ (r & 7)) << 4), second ? h[4] : h[0], second ? h[5] : h[1],
+                                       second ? h[6] : h[2], second ? h[7] : h[3]);
+                                sts128(at + (((q + !second) ^ (r & 7)) << 4), second ? h[0] : h[4], second ? h[1] : h[5],
+                                       second ? h[2] : h[6], second ? h[3] : h[7]);
+                            }
+                        } else {
+                            const int k = k0 + j, t0 = (k < head ? k : k + skip) * kTile;
+                            const int valid = *reinterpret_cast<volatile int *>(&sh.v_valid[tile % kInfos]);
+                            const bool clean = valid != kAllBlocks || tile_edge(a, t0, first, high);
+                            bool odd = false;
+                            // a dimension's 16 codes of a block: word i has slots 2i, 2i + 1, 2i + 8, 2i + 9
+#pragma unroll 2
+                            for (int e = me * 32 + lane; e < kBlocks * kDim; e += 64) {
+                                uint4 x = lds128(codes + e * 16);
+                                if (clean) {
+                                    const uint4 was = x;
+                                    drop_odd(x.x);
+                                    drop_odd(x.y);
+                                    drop_odd(x.z);
+                                    drop_odd(x.w);
+                                    // (stale codes of a block that is not in the pool count for nothing)
+                                    if (((was.x ^ x.x) | (was.y ^ x.y) | (was.z ^ x.z) | (was.w ^ x.w)) && ((valid >> (e / kDim)) & 1))
+#pragma unroll 1
+                                        for (int i = 0; i < 16; ++i) {
+                                            const uint32_t w = i / 4 == 0 ? was.x ^ x.x : i / 4 == 1 ? was.y ^ x.y : i / 4 == 2 ? was.z ^ x.z : was.w ^ x.w;
+                                            const int b = i % 4, t = t0 + e / kDim * TTS_BLOCK_TOKENS + i / 4 * 2 + b % 2 + b / 2 * 8;
+                                            odd = odd || ((w >> (8 * b)) & 0xFF && t < high && (!a.window || t < a.sinks || t >= first - a.window));
+                                        }
+                                }
+                                uint32_t h[8];
+                                codes_to_f16(x.x, h[0], h[4]);
+                                codes_to_f16(x.y, h[1], h[5]);
+                                codes_to_f16(x.z, h[2], h[6]);
+                                codes_to_f16(x.w, h[3], h[7]);
+                                const uint32_t at = out + e / kDim * kBlockBytes + e % kDim * 16;
+                                sts128(at, h[0], h[1], h[2], h[3]);
+                                sts128(at + kBlockBytes / 2, h[4], h[5], h[6], h[7]);
+                            }
+                            if (odd) sh.odd[(part + 1) % 8] = part + 1;
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        mbar_arrive_by(lane == 0, smem_addr(&full[to.slot]));
+                        mbar_arrive_by(lane == 0, smem_addr(&sh.raw_empty[!for_keys][from.slot]));
+                        from.next();
+                        to.next();
+                    }
+                }
             } else {
                 // ---- checkers: values that are not finite leave the tiles that some
                 // row does not see whole.  (They keep step with every tile: a barrier's
                 // parity tells one use of a slot from the next, not from the one after.)
-                Place values;
+                Place<kSlots> values;
                 for (int left = all_tiles, part = 1; ok && left > 0; ++part) {
                     ok = quick_wait(&sh.v_full[values.slot], values.phase, a.wait_limit);
                     if (!ok) break;
-                    const volatile PartInfo &info = sh.parts[(part - 1) % kInfos];
-                    const int tiles = uniform(info.tiles), first = uniform(info.ctx - info.n + info.r0 + 1), high = uniform(info.high);
+                    const volatile ValueInfo &info = sh.values[(part - 1) % kInfos];
+                    const int tiles = uniform(info.tiles), first = uniform(info.first), high = uniform(info.high);
                     const int k0 = uniform(info.k), head = uniform(info.head), skip = uniform(info.skip);
                     left -= tiles;
 #pragma unroll 1
@@ -801,7 +1010,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (!ok) break;
                         const int k = k0 + j, t0 = (k < head ? k : k + skip) * kTile;
                         if (tile_edge(a, t0, first, high)) {
-                            uint8_t *v = raw + 4 * kQueryBytes + (kSlots + values.slot) * kSlotBytes;
+                            uint8_t *v = raw + Smem::values + values.slot * kSlotBytes;
                             const uint32_t from = smem_addr(v) + ((warp - 11) * 32 + lane) * 16;
                             // bit 15 or 31 of a word: an exponent of ones in that half
                             uint32_t any = 0;
@@ -871,9 +1080,22 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tc_fence_before();
                 __syncwarp();
                 mbar_arrive_by(first_lane, smem_addr(&sh.s_empty[s]));
-                mbar_arrive_by(first_thread, smem_addr(&sh.k_empty[flags >> kSlotShift]));
+                mbar_arrive_by(first_thread, smem_addr(&sh.k_empty[(flags >> kSlotShift) % 4]));
                 mbar_arrive_by(first_thread && (flags & kLast), smem_addr(&sh.q_empty));
                 const bool free = use == 0 || mbar_test(smem_addr(&sh.o_done[s]), (use - 1) & 1);
+                // FP8: the scales of the tile's keys and values, 16 and 16 a block
+                const float *scales = nullptr;
+                if constexpr (kFp8) {
+                    scales = reinterpret_cast<const float *>(raw + Smem::scales + (flags >> kStageShift) % kScaleStages * kScaleBytes);
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 4) {
+                        const float4 k = *reinterpret_cast<const float4 *>(scales + i / 16 * 32 + i % 16);
+                        x[i] = __float_as_uint(__uint_as_float(x[i]) * k.x);
+                        x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * k.y);
+                        x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * k.z);
+                        x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * k.w);
+                    }
+                }
                 if (flags & kMasked) {
                     const int t0 = info.t0;
 #pragma unroll
@@ -894,7 +1116,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const float high = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
                 // (the product before this tile's has to be complete before O is scaled, and
                 // before its weights are overwritten: waited for as late as possible)
-                if (__any_sync(kFull, high > m + kSlack)) {
+                if (__any_sync(kFull, high > m + prompt_slack(kFp8))) {
                     if (use && !quick_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
                         ok = false;
                         break;
@@ -924,7 +1146,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     e0 = hw_ex2(e0);
                     e1 = hw_ex2(e1);
                     sum[i % 2] = add2(sum[i % 2], pack2(e0, e1));
-                    weights[i] = pack_bf16(e0, e1);
+                    if constexpr (kFp8) {
+                        // (a token without weight may have any scale)
+                        const float2 v = *reinterpret_cast<const float2 *>(scales + i / 8 * 32 + 16 + i % 8 * 2);
+                        weights[i] = pack_f16(e0 == 0.0f ? 0.0f : e0 * (v.x * kFp8Fix), e1 == 0.0f ? 0.0f : e1 * (v.y * kFp8Fix));
+                    } else {
+                        weights[i] = pack_bf16(e0, e1);
+                    }
                 }
                 if (!__all_sync(kFull, free) && !warp_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
                     ok = false;
@@ -933,14 +1161,14 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 there = mbar_test(smem_addr(&sh.s_full[s]), (use + 1) & 1);
                 tc_fence_after();
                 mbar_arrive_by(first_thread && held >= 0, smem_addr(&sh.v_empty[max(held, 0)]));
-                held = flags >> kSlotShift;
+                held = (flags >> kSlotShift) % 4;
                 tmem_st32(tp, weights);
                 tmem_st8(tp + 32, weights + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 mbar_arrive_by(first_lane, smem_addr(&sh.p_full[s]));
-                mbar_arrive_by(threadIdx.x == 0 && (flags & kPair), smem_addr(&sh.behind[flags >> kSlotShift]));
+                mbar_arrive_by(threadIdx.x == 0 && (flags & kPair), smem_addr(&sh.behind[(flags >> kSlotShift) % 4]));
                 float sum0, sum1;
                 unpack2(add2(sum[0], sum[1]), sum0, sum1);
                 l += sum0 + sum1;
@@ -949,6 +1177,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 ok = warp_wait(&sh.o_done[s], use & 1, a.wait_limit);
                 if (!ok) break;
                 tc_fence_after();
+                if constexpr (kFp8) l *= kFp8Fix;
                 mbar_arrive_by(first_thread, smem_addr(&sh.v_empty[held]));
                 held = -1;
                 const PartInfo &p = sh.parts[(flags >> kPartShift) % kInfos];
@@ -967,7 +1196,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         float f[32];
                         tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
                         tmem_wait_ld();
-                        if (odd && real) add_odd(a, p, step, j0, limit, c, f);
+                        if (odd && real) add_odd<kFp8>(a, p, step, j0, limit, c, f);
                         if (real) store_row(out + c, f, inv);
                     }
                     tc_fence_before();
@@ -983,7 +1212,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     float f[32];
                     tmem_ld32_nowait(to + c, reinterpret_cast<uint32_t *>(f));
                     tmem_wait_ld();
-                    if (odd && real) add_odd(a, p, step, j0, limit, c, f);
+                    if (odd && real) add_odd<kFp8>(a, p, step, j0, limit, c, f);
                     if (real)
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -1218,11 +1447,14 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
         return TTS_ERR_INVALID;
     const int Hq = num_q_heads, Hkv = cache->num_kv_heads;
     if (!prompt_shape_ok(B, num_rows, Hq, Hkv)) return TTS_ERR_INVALID;
-    if (cache->block_size != TTS_BLOCK_TOKENS || cache->dtype != TTS_BF16 || cache->head_dim != kDim) return TTS_ERR_UNSUPPORTED;
+    if (cache->block_size != TTS_BLOCK_TOKENS || cache->head_dim != kDim ||
+        (cache->dtype != TTS_BF16 && cache->dtype != TTS_FP8_E4M3))
+        return TTS_ERR_UNSUPPORTED;
     if (B > kMaxStreams || Hq / Hkv > kRows) return TTS_ERR_UNSUPPORTED;
     const uint64_t pool_rows = static_cast<uint64_t>(cache->num_blocks) * Hkv * TTS_BLOCK_TOKENS;
     if (pool_rows >= (1ULL << 31)) return TTS_ERR_UNSUPPORTED;
-    if (!aligned16(cache->k_pool) || !aligned16(cache->v_pool) || !aligned16(d_q) || !aligned16(d_out)) return TTS_ERR_INVALID;
+    const bool fp8 = cache->dtype == TTS_FP8_E4M3;
+    if (!aligned16(cache->k_pool) || (!fp8 && !aligned16(cache->v_pool)) || !aligned16(d_q) || !aligned16(d_out)) return TTS_ERR_INVALID;
     if (B == 0 || num_rows == 0) return TTS_OK;
     if (!d_ws || ws_bytes < prompt_workspace_bytes() || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0)
         return TTS_ERR_WORKSPACE;
@@ -1244,6 +1476,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     a.sinks = sinks < (1 << 24) ? sinks : 1 << 24;
     if (!a.window) a.sinks = 0;
     a.scale_log2 = scale * kLog2e;
+    a.k_pool = static_cast<const uint8_t *>(cache->k_pool);
     a.v_pool = static_cast<const uint8_t *>(cache->v_pool);
     a.out = static_cast<__nv_bfloat16 *>(d_out);
     a.ctas = prompt_ctas();
@@ -1258,14 +1491,16 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     const int64_t query_tiles = static_cast<int64_t>(num_rows) / (2 * a.tokens) + B;
     a.max_tiles = static_cast<int>(query_tiles);
     if (query_tiles * Hkv * (max_blocks_per_seq / kBlocks + 1 + kPartCost) >= (1LL << 30)) return TTS_ERR_UNSUPPORTED;
-    CUtensorMap map_q, map_k, map_v;
-    if (!make_tma_queries_bf16(&map_q, d_q, num_rows, Hq, a.group, a.tokens) ||
-        !make_tma_2d_bf16(&map_k, cache->k_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64) ||
-        !make_tma_rows_in_halves_bf16(&map_v, cache->v_pool, pool_rows, TTS_BLOCK_TOKENS))
+    CUtensorMap map_q, map_k{}, map_v{};
+    if (!make_tma_queries_bf16(&map_q, d_q, num_rows, Hq, a.group, a.tokens)) return TTS_ERR_CUDA;
+    if (!fp8 && (!make_tma_2d_bf16(&map_k, cache->k_pool, pool_rows, kDim, TTS_BLOCK_TOKENS, 64) ||
+        !make_tma_rows_in_halves_bf16(&map_v, cache->v_pool, pool_rows, TTS_BLOCK_TOKENS)))
         return TTS_ERR_CUDA;
-    if (!allow_smem(prompt_attn_kernel, kSmem)) return TTS_ERR_CUDA;
+    const auto kernel = fp8 ? prompt_attn_kernel<true> : prompt_attn_kernel<false>;
+    const int smem = fp8 ? PromptSmem<true>::total : PromptSmem<false>::total;
+    if (!allow_smem(kernel, smem)) return TTS_ERR_CUDA;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const int rc = launch_kernel(prompt_attn_kernel, dim3(a.ctas), dim3(kThreads), kSmem, {cs, thread_pdl()}, map_q, map_k, map_v, a);
+    const int rc = launch_kernel(kernel, dim3(a.ctas), dim3(prompt_threads(fp8)), smem, {cs, thread_pdl()}, map_q, map_k, map_v, a);
     // no segment has more than 2 * kSnap tiles: none is split
     if (rc != TTS_OK || max_blocks_per_seq <= 2 * kSnap * kBlocks) return rc;
     return launch_kernel(prompt_join_kernel, dim3(a.ctas), dim3(kJoinThreads), 0, {cs, true}, a.part, a.jobs, a.ctas, a.out,

@@ -315,10 +315,13 @@ size_t tts_prompt_attn_workspace_size(int32_t B, int32_t num_rows, int32_t num_q
  * ones (append first: tts_kv_append_packed), so row r sees the tokens
  *   t < limit = d_ctx_lens[b] - (d_row_start[b + 1] - r) + 1,
  * with window > 0 of them those with t >= limit - window or t < sinks.  The sum
- * is tts_decode_attn's, the weights rounded to bf16 before they meet the values.
+ * is tts_decode_attn's; the weights are rounded to bf16 before they meet the
+ * values, in an FP8 cache times the value's scale and 2^8 to f16 (the limits that
+ * tts_kv_cache states hold here too).
  *  d_q, d_out  bf16 [num_rows][num_q_heads][128], 16-byte aligned
  *  window, sinks  >= 0; window 0: the whole context
- * Supported: TTS_BF16, head_dim 128, num_q_heads / num_kv_heads <= 128, B <= 4096;
+ * Supported: TTS_BF16 and TTS_FP8_E4M3, head_dim 128, num_q_heads / num_kv_heads
+ * <= 128, B <= 4096;
  * query tiles (rows / (2 * (128 / group)) + B) x KV heads x 128-token tiles of
  * max_blocks_per_seq below 2^30.
  * Reads only the blocks that hold a token that some row sees, as

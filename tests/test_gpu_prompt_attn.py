@@ -3,6 +3,8 @@ head groups, windows, sinks and their edges, ragged and refused streams, values
 that are not finite, work split over CTAs, captured calls."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
@@ -14,7 +16,7 @@ if torch.cuda.is_available():
     from decode_step_gb300 import _lib
     from decode_step_gb300 import binding as bd
 
-DTYPES = ["bf16"]
+DTYPES = ["bf16", "fp8"]
 
 
 def upload(s):
@@ -123,6 +125,36 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(value):
         bad = ~torch.isfinite(ref[:, 2, d])
         assert bad.any() and not bad.all()
     pr.check(run(s), ref, tol)
+
+
+def test_fp8_values_that_are_not_numbers_reach_the_rows_that_see_them():
+    s = pr.make([90], [300], 4, 2, "fp8", 100, 4, seed=6, hide=False)
+    vis = pr.visible(s, 0)
+    for t, d in ((250, 5), (340, 127), (389, 66), (3, 64), (100, 9), (5, 11)):
+        b, slot = int(s["table"][0, t // 16]), t % 16
+        s["pools"][0][b, 1, 2048 + 16 * d + 4 * (slot % 8 // 2) + slot % 2 + 2 * (slot // 8)] = 0xFF
+        s["v_val"][b, 1, slot, d] = float("nan")
+    assert not vis[:, 100].any() and not vis[:, 5].any()
+    ref, tol = pr.attend_all(s)
+    assert torch.isfinite(ref[:, :2]).all() and torch.isfinite(ref[:, 2:, 9]).all()
+    for d in (5, 127, 66):
+        bad = ~torch.isfinite(ref[:, 2, d])
+        assert bad.any() and not bad.all()
+    pr.check(run(s), ref, tol)
+
+
+def test_fp8_scales_of_any_size():
+    """Values from 2^-20 to 50,000: scales times 2^8 from 2^-21 to 28,571.  A weight times that is a
+    subnormal of f16 below 2^-14, off by 2^-25: 2^-33 of a code of at most 448, a token."""
+    s = pr.make([70, 40], [0, 200], 4, 2, "fp8", seed=21)
+    g = torch.Generator().manual_seed(22)
+    k, v = s["k_pool"], s["v_pool"]
+    size = torch.exp(torch.rand(v.shape[:3], generator=g) * (math.log(5e4) - math.log(2.0 ** -20)) + math.log(2.0 ** -20))
+    top = v.float().abs().amax(-1)
+    s["v_pool"] = (v.float() / top[..., None] * size[..., None]).to(torch.bfloat16)
+    pr.finish(s)
+    ref, tol = pr.attend_all(s)
+    pr.check(run(s), ref, tol + 270 * 2.0 ** -33 * 448)
 
 
 def test_values_that_are_not_finite_in_split_segments():
