@@ -72,6 +72,7 @@ constexpr float kNoScore = -FLT_MAX;
 // at 1 at most, so that with a scale below 256 they are in f16's range.
 __host__ __device__ constexpr float prompt_slack(bool fp8) { return fp8 ? 0.0f : 8.0f; }
 constexpr int kPartFloats = kRows * kDim + 2 * kRows;  // o, m, l of a half
+constexpr int kPairTiles = 10;              // tiles of a part from which on half 1 stays half a step behind
 constexpr int kTakeTurns = 12;              // tiles of a segment from which on its one half's rows use both
 constexpr int kJoinHere = 4;                // parts that the last CTA joins; more are left to the second kernel
 
@@ -462,6 +463,14 @@ __device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
     return r;
 }
+__device__ __forceinline__ void times2(uint32_t &x, uint32_t &y, float a, float b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(__uint_as_float(x), __uint_as_float(y))), "l"(pack2(a, b)));
+    float lo, hi;
+    unpack2(r, lo, hi);
+    x = __float_as_uint(lo);
+    y = __float_as_uint(hi);
+}
 __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
@@ -672,6 +681,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         whole_to[s] = before + row0 + 1 - kTile;
                     }
                     const int step = mode == kTurns ? 2 : 1;
+                    const bool paired = mode == kBoth && tiles >= kPairTiles;
                     int y = 0, good = 0, from = kLookups * kBlocks;
 #pragma unroll 1
                     for (int j = 0; ok && j < tiles; ++j) {
@@ -690,7 +700,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (for_keys) {
                             const int mask = (good >> from) & kAllBlocks;
                             const int k = walk.k + j, t0 = (k < walk.span.head ? k : k + walk.span.skip) * kTile;
-                            const int common = mask | (mode == kBoth ? kPair : 0) | (j < step ? kFresh : 0) |
+                            const int common = mask | (paired ? kPair : 0) | (j < step ? kFresh : 0) |
                                                (j >= tiles - step ? kLast : 0) | note << kPartShift |
                                                static_cast<int>(tile % kSlots) << kSlotShift |
                                                static_cast<int>(tile % kScaleStages) << kStageShift;
@@ -807,6 +817,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (s == 1 && mode == kBoth) x.set(1, &sh.q_full[1], both++ & 1);
                         go = x.wait(a.wait_limit);
                     }
+                    const bool paired = mode == kBoth && tiles >= kPairTiles;
                     bool fresh = true;
                     if (go && (of == 0 || (of == 2 && tiles == 1)) && lane == 0) mbar_arrive(smem_addr(&sh.q_empty));
 #pragma unroll 1
@@ -818,7 +829,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             x.none(1);
                             if (work && uses) x.set(1, &sh.s_empty[s], (uses - 1) & 1);
                             go = x.spin(a.wait_limit);
-                            if (go && s == 1 && mode == kBoth) {
+                            if (go && s == 1 && paired) {
                                 // half 1 stays half a step behind (its exponentials while half
                                 // 0 waits and loads, not at the same time)
                                 go = quick_wait(&sh.behind[keys.slot], behind >> keys.slot & 1, a.wait_limit);
@@ -1090,10 +1101,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 #pragma unroll
                     for (int i = 0; i < kTile; i += 4) {
                         const float4 k = *reinterpret_cast<const float4 *>(scales + i / 16 * 32 + i % 16);
-                        x[i] = __float_as_uint(__uint_as_float(x[i]) * k.x);
-                        x[i + 1] = __float_as_uint(__uint_as_float(x[i + 1]) * k.y);
-                        x[i + 2] = __float_as_uint(__uint_as_float(x[i + 2]) * k.z);
-                        x[i + 3] = __float_as_uint(__uint_as_float(x[i + 3]) * k.w);
+                        times2(x[i], x[i + 1], k.x, k.y);
+                        times2(x[i + 2], x[i + 3], k.z, k.w);
                     }
                 }
                 if (flags & kMasked) {
@@ -1147,11 +1156,27 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     e1 = hw_ex2(e1);
                     sum[i % 2] = add2(sum[i % 2], pack2(e0, e1));
                     if constexpr (kFp8) {
-                        // (a token without weight may have any scale)
-                        const float2 v = *reinterpret_cast<const float2 *>(scales + i / 8 * 32 + 16 + i % 8 * 2);
-                        weights[i] = pack_f16(e0 == 0.0f ? 0.0f : e0 * (v.x * kFp8Fix), e1 == 0.0f ? 0.0f : e1 * (v.y * kFp8Fix));
+                        x[2 * i] = __float_as_uint(e0);
+                        x[2 * i + 1] = __float_as_uint(e1);
                     } else {
                         weights[i] = pack_bf16(e0, e1);
+                    }
+                }
+                if constexpr (kFp8) {
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 4) {
+                        float4 v = *reinterpret_cast<const float4 *>(scales + i / 16 * 32 + 16 + i % 16);
+                        uint32_t *e = x + i;
+                        if (flags & kMasked) {  // a token without weight may have any scale
+                            v.x = e[0] ? v.x : 0.0f;
+                            v.y = e[1] ? v.y : 0.0f;
+                            v.z = e[2] ? v.z : 0.0f;
+                            v.w = e[3] ? v.w : 0.0f;
+                        }
+                        times2(e[0], e[1], v.x, v.y);
+                        times2(e[2], e[3], v.z, v.w);
+                        weights[i / 2] = pack_f16(__uint_as_float(e[0]) * kFp8Fix, __uint_as_float(e[1]) * kFp8Fix);
+                        weights[i / 2 + 1] = pack_f16(__uint_as_float(e[2]) * kFp8Fix, __uint_as_float(e[3]) * kFp8Fix);
                     }
                 }
                 if (!__all_sync(kFull, free) && !warp_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
