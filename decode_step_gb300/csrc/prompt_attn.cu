@@ -52,8 +52,10 @@ constexpr int kBlockBytes = 4096;           // a block's values of a head
 __host__ __device__ constexpr int prompt_slots(bool fp8) { return fp8 ? 2 : 4; }  // tiles of keys, and of values, in the ring
 constexpr int kRawSlots = 3, kRawBytes = kBlocks * 2048;       // FP8: tiles of codes on their way, of keys and of values
 constexpr int kRecordBytes = 4224, kScaleStages = 8, kScaleBytes = kBlocks * 128;
-// FP8: weights times the value's scale times 2^8 in f16, as tts_decode_attn has them
-constexpr float kFp8Fix = 0x1p8f;
+// FP8: the weights are 2^8 times what they are else, so that times their values'
+// scales they stay clear of f16's subnormals, as tts_decode_attn has them; so is
+// their sum
+constexpr float kFp8Log2 = 8.0f;
 // Tensor memory: a half's S, its P (two weights a column), and both halves' O
 constexpr int kS = 0, kP = kTile, kHalf = 128, kO = 256;
 static_assert(kP + kTile / 2 <= kHalf);
@@ -942,23 +944,22 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         const uint32_t codes = q_base + Smem::raw + ((for_keys ? 0 : kRawSlots) + from.slot) * kRawBytes;
                         const uint32_t out = (for_keys ? k_base : v_base) + to.slot * kSlotBytes;
                         if (for_keys) {
-                            // 16 codes of a token: 16-byte piece p of row r, which holds dimensions 16 (p ^ r % 8) on
-#pragma unroll 2
-                            for (int e = me * 32 + lane; e < kRawBytes / 16; e += 64) {
-                                const int r = e / 8, c = e % 8 ^ (r & 7);
-                                const uint4 x = lds128(codes + e * 16);
+                            // 16 codes of a token, 16-byte piece p of row r: dimensions 16 (p ^ r % 8) on.
+                            // A lane's rows are eight apart.
+                            const int r = me * 4 + lane / 8, c = lane % 8 ^ r;
+                            const uint32_t in = codes + (me * 32 + lane) * 16;
+                            const uint32_t at = out + c / 4 * kChunkBytes + r * 128, q = c % 4 * 2;
+                            const uint32_t lo_at = at + ((q ^ r) << 4), hi_at = at + (((q + 1) ^ r) << 4);
+#pragma unroll
+                            for (int e = 0; e < kRawBytes; e += 1024) {
+                                const uint4 x = lds128(in + e);
                                 uint32_t h[8];
                                 codes_to_f16(x.x, h[0], h[1]);
                                 codes_to_f16(x.y, h[2], h[3]);
                                 codes_to_f16(x.z, h[4], h[5]);
                                 codes_to_f16(x.w, h[6], h[7]);
-                                const uint32_t at = out + c / 4 * kChunkBytes + r * 128, q = c % 4 * 2;
-                                // (the two halves' stores on different banks)
-                                const bool second = c >= 4;
-                                sts128(at + (((q + second) ^ (r & 7)) << 4), second ? h[4] : h[0], second ? h[5] : h[1],
-                                       second ? h[6] : h[2], second ? h[7] : h[3]);
-                                sts128(at + (((q + !second) ^ (r & 7)) << 4), second ? h[0] : h[4], second ? h[1] : h[5],
-                                       second ? h[2] : h[6], second ? h[3] : h[7]);
+                                sts128(lo_at + e, h[0], h[1], h[2], h[3]);
+                                sts128(hi_at + e, h[4], h[5], h[6], h[7]);
                             }
                         } else {
                             const int k = k0 + j, t0 = (k < head ? k : k + skip) * kTile;
@@ -966,32 +967,39 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             const bool clean = valid != kAllBlocks || tile_edge(a, t0, first, high);
                             bool odd = false;
                             // a dimension's 16 codes of a block: word i has slots 2i, 2i + 1, 2i + 8, 2i + 9
-#pragma unroll 2
-                            for (int e = me * 32 + lane; e < kBlocks * kDim; e += 64) {
-                                uint4 x = lds128(codes + e * 16);
-                                if (clean) {
-                                    const uint4 was = x;
+                            const uint32_t in = codes + (me * 32 + lane) * 16, at = out + (me * 32 + lane) * 16;
+                            if (clean) {
+#pragma unroll 1
+                                for (int e = 0; e < kRawBytes; e += 1024) {
+                                    const uint4 was = lds128(in + e);
+                                    uint4 x = was;
                                     drop_odd(x.x);
                                     drop_odd(x.y);
                                     drop_odd(x.z);
                                     drop_odd(x.w);
+                                    if (!((was.x ^ x.x) | (was.y ^ x.y) | (was.z ^ x.z) | (was.w ^ x.w))) continue;
+                                    sts128(in + e, x.x, x.y, x.z, x.w);
                                     // (stale codes of a block that is not in the pool count for nothing)
-                                    if (((was.x ^ x.x) | (was.y ^ x.y) | (was.z ^ x.z) | (was.w ^ x.w)) && ((valid >> (e / kDim)) & 1))
+                                    if (!((valid >> (e / 2048)) & 1)) continue;
 #pragma unroll 1
-                                        for (int i = 0; i < 16; ++i) {
-                                            const uint32_t w = i / 4 == 0 ? was.x ^ x.x : i / 4 == 1 ? was.y ^ x.y : i / 4 == 2 ? was.z ^ x.z : was.w ^ x.w;
-                                            const int b = i % 4, t = t0 + e / kDim * TTS_BLOCK_TOKENS + i / 4 * 2 + b % 2 + b / 2 * 8;
-                                            odd = odd || ((w >> (8 * b)) & 0xFF && t < high && (!a.window || t < a.sinks || t >= first - a.window));
-                                        }
+                                    for (int i = 0; i < 16; ++i) {
+                                        const uint32_t w = i / 4 == 0 ? was.x ^ x.x : i / 4 == 1 ? was.y ^ x.y : i / 4 == 2 ? was.z ^ x.z : was.w ^ x.w;
+                                        const int b = i % 4, t = t0 + e / 2048 * TTS_BLOCK_TOKENS + i / 4 * 2 + b % 2 + b / 2 * 8;
+                                        odd = odd || ((w >> (8 * b)) & 0xFF && t < high && (!a.window || t < a.sinks || t >= first - a.window));
+                                    }
                                 }
+                            }
+#pragma unroll
+                            for (int e = 0; e < kRawBytes; e += 1024) {
+                                const uint4 x = lds128(in + e);
                                 uint32_t h[8];
                                 codes_to_f16(x.x, h[0], h[4]);
                                 codes_to_f16(x.y, h[1], h[5]);
                                 codes_to_f16(x.z, h[2], h[6]);
                                 codes_to_f16(x.w, h[3], h[7]);
-                                const uint32_t at = out + e / kDim * kBlockBytes + e % kDim * 16;
-                                sts128(at, h[0], h[1], h[2], h[3]);
-                                sts128(at + kBlockBytes / 2, h[4], h[5], h[6], h[7]);
+                                const uint32_t to_at = at + e / 2048 * kBlockBytes + e % 2048;
+                                sts128(to_at, h[0], h[1], h[2], h[3]);
+                                sts128(to_at + kBlockBytes / 2, h[4], h[5], h[6], h[7]);
                             }
                             if (odd) sh.odd[(part + 1) % 8] = part + 1;
                         }
@@ -1146,7 +1154,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         }
                 }
                 uint64_t sum[2] = {0, 0};
-                const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), minus2 = pack2(-m, -m);
+                const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), minus2 = kFp8 ? pack2(kFp8Log2 - m, kFp8Log2 - m) : pack2(-m, -m);
                 uint32_t weights[kTile / 2];
 #pragma unroll
                 for (int i = 0; i < kTile / 2; ++i) {
@@ -1175,8 +1183,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         }
                         times2(e[0], e[1], v.x, v.y);
                         times2(e[2], e[3], v.z, v.w);
-                        weights[i / 2] = pack_f16(__uint_as_float(e[0]) * kFp8Fix, __uint_as_float(e[1]) * kFp8Fix);
-                        weights[i / 2 + 1] = pack_f16(__uint_as_float(e[2]) * kFp8Fix, __uint_as_float(e[3]) * kFp8Fix);
+                        weights[i / 2] = pack_f16(__uint_as_float(e[0]), __uint_as_float(e[1]));
+                        weights[i / 2 + 1] = pack_f16(__uint_as_float(e[2]), __uint_as_float(e[3]));
                     }
                 }
                 if (!__all_sync(kFull, free) && !warp_wait(&sh.o_done[s], (use - 1) & 1, a.wait_limit)) {
@@ -1202,7 +1210,6 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 ok = warp_wait(&sh.o_done[s], use & 1, a.wait_limit);
                 if (!ok) break;
                 tc_fence_after();
-                if constexpr (kFp8) l *= kFp8Fix;
                 mbar_arrive_by(first_thread, smem_addr(&sh.v_empty[held]));
                 held = -1;
                 const PartInfo &p = sh.parts[(flags >> kPartShift) % kInfos];
