@@ -10,6 +10,10 @@ equal the head's hidden width.
 tts_latent_decode_attn, tts_codebook_head_select), and appends and attends over
 whole prompts.
 
+`WindowStep` does it over the paged KV cache (tts_kv_append_packed,
+tts_prompt_attn, tts_window_decode_attn, tts_codebook_head_select), whole
+prompts as well, with a sliding window and sinks, and forks and compacts.
+
 `GraphedStep` wraps tts_step_graph: a whole serving step captured once by the
 library for fixed buffers (the copy of the step's inputs from pinned host
 memory, the decode step, the chosen ids and a boundary-token count back to
@@ -69,7 +73,24 @@ def _capturing(stream: torch.cuda.Stream) -> bool:
         return torch.cuda.is_current_stream_capturing()
 
 
-class LatentStep:
+class _CallsInOrder:
+    """Calls of one kind share workspaces and buffers: on whatever CUDA streams
+    they are made, each is ordered behind the latest one of its kind.  Not while
+    a graph is being captured, and not for replays."""
+
+    def __init__(self, device):
+        self._device = device
+        self._streams: dict[str, torch.cuda.Stream] = {}  # of the latest call of each kind
+
+    def _follow(self, kind: str, stream) -> None:
+        now = torch.cuda.current_stream(self._device) if stream is None else stream
+        last = self._streams.get(kind, now)
+        if last != now and not (_capturing(last) or _capturing(now)):
+            now.wait_stream(last)
+        self._streams[kind] = now
+
+
+class LatentStep(_CallsInOrder):
     """A batch's steps over a latent cache, for fixed shapes: `prompt` appends
     whole prompts and attends over them, calling the object appends q_len
     tokens a stream, attends (absorbed form) and picks codec tokens.
@@ -115,19 +136,11 @@ class LatentStep:
         self.step_q = torch.empty((self.R, Hq, cache.ROPE_DIM), dtype=torch.bfloat16, device=dev)
         self.prompt_q = torch.empty((prompt_rows, Hq, cache.ROPE_DIM), dtype=torch.bfloat16, device=dev)
         self.q = self.step_q
-        self._streams: dict[str, torch.cuda.Stream] = {}  # of the latest call of each kind
+        super().__init__(dev)
         self.out = torch.empty((B, q_len, Hq, v), dtype=torch.bfloat16, device=dev)
         self.ids = torch.empty(self.R, dtype=torch.int32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.prompt_rows, self.prompt_ctx = prompt_rows, prompt_ctx
-
-    def _follow(self, kind: str, stream) -> None:
-        """Orders a call behind the latest one of its kind."""
-        now = torch.cuda.current_stream(self.out.device) if stream is None else stream
-        last = self._streams.get(kind, now)
-        if last != now and not (_capturing(last) or _capturing(now)):
-            now.wait_stream(last)
-        self._streams[kind] = now
 
     def prompt(self, block_table, ctx_before, ctx_lens, row_start, q_nope, q_rope, c_new, kr_new, out=None,
                stream=None) -> torch.Tensor:
@@ -170,6 +183,125 @@ class LatentStep:
         finally:
             bd.tts_set_launch_flags(flags)
         return self.ids
+
+
+class WindowStep(_CallsInOrder):
+    """A batch's prompts and steps over a paged KV cache (bfloat16 or FP8), for
+    fixed shapes, with a context that stays bounded: rows see the last `window`
+    tokens up to their own and the first `sinks` (window 0: all of them).
+
+    `prompt` appends the packed rows of up to B prompts, or pieces of them, and
+    attends over them; calling the object appends q_len tokens a stream, attends
+    and picks codec tokens (W [V][Hq * head_dim]).  q and k_new are passed
+    unrotated where rope_base is not 0; the rotated queries go to buffers of the
+    object (`q` is the latest call's).  `fork` makes streams continuations of
+    others, `compact` moves blocks as BlockPool.compact says, and `gone` tells which of a
+    stream's blocks can go back to the pool.  The object owns the workspaces and
+    outputs (`out` [B][q_len][Hq][head_dim], `ids` [B * q_len]).
+
+    Prompts may run on one CUDA stream while steps of other streams' blocks run
+    on another, as with LatentStep; forks and compactions change tables and
+    contexts, and the caller orders them with the calls that read those.
+    """
+
+    def __init__(self, cache: bd.KVCache, W: torch.Tensor, num_q_heads: int, B: int, max_ctx_len: int, window: int = 0,
+                 sinks: int = 0, q_len: int = 1, causal: bool = False, mode: int = bd.TTS_ARGMAX,
+                 temperature: float = 0.0, scale: float | None = None, rope_base: float = 10000.0, prompt_rows: int = 0):
+        dev, D = cache.k_pool.device, cache.head_dim
+        if W.shape[1] != num_q_heads * D:
+            raise ValueError(f"head width {W.shape[1]} != num_q_heads * head_dim = {num_q_heads * D}")
+        if window < 0 or sinks < 0:
+            raise ValueError("window and sinks must not be negative")
+        self.cache, self.W = cache, W
+        self.B, self.q_len, self.Hq, self.max_ctx_len, self.causal = B, q_len, num_q_heads, max_ctx_len, causal
+        self.window, self.sinks = window, sinks
+        self.mode, self.temperature, self.rope_base = mode, temperature, rope_base
+        self.scale = 1.0 / math.sqrt(D) if scale is None else scale
+        self.R, self.V, self.prompt_rows = B * q_len, W.shape[0], prompt_rows
+        ws = bd.tts_decode_attn_workspace_size(B, q_len, num_q_heads, cache.num_kv_heads, D, max_ctx_len)
+        head_ws = bd.tts_head_workspace_size(self.R, self.V)
+        prompt_ws = bd.tts_prompt_attn_workspace_size(B, prompt_rows, num_q_heads, cache.num_kv_heads, D)
+        if ws == 0 or head_ws == 0 or (prompt_rows and prompt_ws == 0):
+            raise ValueError("unsupported window-step shape")
+        super().__init__(dev)
+        self.ws = torch.zeros(ws, dtype=torch.uint8, device=dev)
+        self.prompt_ws = torch.zeros(prompt_ws if prompt_rows else 0, dtype=torch.uint8, device=dev)
+        self.head_ws = torch.zeros(head_ws, dtype=torch.uint8, device=dev)
+        self.step_q = torch.empty((self.R, num_q_heads, D), dtype=cache.dtype, device=dev)
+        self.prompt_q = torch.empty((prompt_rows, num_q_heads, D), dtype=cache.dtype, device=dev)
+        self.q = self.step_q
+        self._rows = torch.arange(0, self.R + 1, q_len, dtype=torch.int32, device=dev)  # a step's rows, packed
+        self.out = torch.empty((B, q_len, num_q_heads, D), dtype=cache.dtype, device=dev)
+        self.ids = torch.empty(self.R, dtype=torch.int32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def _append(self, block_table, ctx_before, row_start, q, k_new, v_new, buffer, stream):
+        if self.rope_base == 0.0:
+            bd.tts_kv_append_packed(self.cache, block_table, ctx_before, row_start, k_new, v_new, err=self.err, stream=stream)
+            return q
+        bd.tts_kv_append_packed(self.cache, block_table, ctx_before, row_start, k_new, v_new, q, buffer, self.rope_base,
+                                err=self.err, stream=stream)
+        return buffer
+
+    def prompt(self, block_table, ctx_before, ctx_lens, row_start, q, k_new, v_new, out=None, stream=None) -> torch.Tensor:
+        """Appends the packed rows q [rows][Hq][D], k_new, v_new [rows][Hkv][D]
+        (stream b: rows row_start[b]..row_start[b + 1] - 1 at positions
+        ctx_before[b]..) and attends causally; returns the attention output,
+        shaped like q (a new tensor of `stream`, unless `out` is given)."""
+        T = q.shape[0]
+        if T > self.prompt_rows:
+            raise ValueError(f"{T} prompt rows exceed prompt_rows = {self.prompt_rows}")
+        if out is None:
+            # allocated on the stream that writes it: memory freed on the current one may still be in use there
+            with torch.cuda.stream(stream):
+                out = torch.empty((T, self.Hq, self.cache.head_dim), dtype=self.cache.dtype, device=self.out.device)
+        self._follow("prompt", stream)
+        q = self.q = self._append(block_table, ctx_before, row_start, q, k_new, v_new, self.prompt_q[:T], stream)
+        bd.tts_prompt_attn(self.cache, block_table, ctx_lens, row_start, q, out, self.prompt_ws, self.scale, self.window,
+                           self.sinks, err=self.err, stream=stream)
+        return out
+
+    def __call__(self, block_table, ctx_before, ctx_lens, q, k_new, v_new, seed=None, step=None, eos_allowed=None,
+                 logits_out=None, best=None, stream=None) -> torch.Tensor:
+        """One step: q [B][q_len][Hq][D], k_new, v_new [B][q_len][Hkv][D]; returns
+        the device tensor of chosen ids [B * q_len]."""
+        D, Hkv = self.cache.head_dim, self.cache.num_kv_heads
+        shape = (self.B, self.q_len, self.Hq, D)
+        if q.shape != shape:
+            raise ValueError(f"q must have shape {shape}, got {tuple(q.shape)}")
+        self._follow("step", stream)
+        rows = self.q = self._append(block_table, ctx_before, self._rows, q.view(self.R, self.Hq, D),
+                                     k_new.view(self.R, Hkv, D), v_new.view(self.R, Hkv, D), self.step_q, stream)
+        # the later kernels start while the ones before them finish
+        flags = bd.tts_set_launch_flags(_lib.LAUNCH_PROGRAMMATIC)
+        try:
+            args = (self.cache, block_table, ctx_lens, self.max_ctx_len, rows.view(shape), self.out, self.ws, self.scale)
+            if self.window:
+                bd.tts_window_decode_attn(*args, self.window, self.sinks, causal=self.causal, err=self.err, stream=stream)
+            else:
+                bd.tts_decode_attn(*args, causal=self.causal, err=self.err, stream=stream)
+            bd.tts_codebook_head_select(self.out.view(self.R, -1), self.W, self.ids, self.head_ws, self.mode,
+                                        self.temperature, seed, step, eos_allowed, best, logits_out, stream)
+        finally:
+            bd.tts_set_launch_flags(flags)
+        return self.ids
+
+    def fork(self, block_table, ctx_lens, parent, child, new_block, stream=None) -> None:
+        """tts_kv_fork on the object's cache (the pool's owners are the caller's:
+        BlockPool.share for the full blocks, alloc for new_block)."""
+        bd.tts_kv_fork(self.cache, block_table, ctx_lens, parent, child, new_block, err=self.err, stream=stream)
+
+    def compact(self, block_map, block_table, stream=None) -> None:
+        """tts_kv_compact on the object's cache."""
+        bd.tts_kv_compact(self.cache, block_map, block_table, err=self.err, stream=stream)
+
+    def gone(self, ctx_len: int) -> range:
+        """Table entries of a stream with ctx_len cached tokens whose blocks no
+        row of a later call sees: they can be freed, and the entries set to -1."""
+        if not self.window:
+            return range(0)
+        # the next row is token ctx_len and sees the tokens from ctx_len + 1 - window on
+        return range(-(-self.sinks // 16), max(-(-self.sinks // 16), (ctx_len + 1 - self.window) // 16))
 
 
 class GraphedStep:
