@@ -88,8 +88,8 @@ struct PromptArgs {
     float scale_log2;
     const uint8_t *k_pool, *v_pool;           // FP8: the records, and none
     __nv_bfloat16 *out;
-    float *part;          // [CTA][first, later part][half] partial results
-    int32_t *tickets;     // [CTA][half]
+    float *part;          // [CTA][kind][half] partial results
+    int32_t *tickets;     // [CTA][kKinds]: of a segment that begins in it, either half; of one that it has whole
     int4 *jobs;           // [CTA][half] segments that the second kernel joins: rows (0: none), first row, KV head, parts
     int ctas, max_tiles;  // query tiles at most
     int zero_row;         // a row behind the pool: reads as zeros
@@ -541,16 +541,21 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *out, const float *f, fl
 }
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }  // no token left: zeros
 
-// Slot of a part: CTA, whether the segment begins in it, half.  [32][128 rows][4]
-// floats o, then m and l of the rows.
-__device__ __forceinline__ float *part_slot(float *parts, int cta, bool begins, int half) {
-    return parts + static_cast<size_t>((cta * 2 + (begins ? 0 : 1)) * 2 + half) * kPartFloats;
+// Slot of a part: CTA, kind, half.  [32][128 rows][4] floats o, then m and l of
+// the rows.  A CTA's parts of split segments are its first one (if the segment
+// began in an earlier CTA) and its last one; segments that it has whole, but in
+// turns, have a slot of their own, which the next such one may write once both
+// halves are done with this: it is at least kTakeTurns tiles long, and a half is
+// never more than the ring ahead of the other.
+constexpr int kBegins = 0, kLater = 1, kWhole = 2, kKinds = 3;
+__device__ __forceinline__ float *part_slot(float *parts, int cta, int kind, int half) {
+    return parts + static_cast<size_t>((cta * kKinds + kind) * 2 + half) * kPartFloats;
 }
 // Part i of a segment whose first CTA is `first`: one a CTA (of half s), or with
 // both halves' in turns two.
-__device__ __forceinline__ float *segment_part(float *parts, int first, int i, bool turns, int s) {
+__device__ __forceinline__ float *segment_part(float *parts, int first, int i, bool turns, int s, bool whole = false) {
     const int c = turns ? i / 2 : i;
-    return part_slot(parts, first + c, c == 0, turns ? i % 2 : s);
+    return part_slot(parts, first + c, whole ? kWhole : c == 0 ? kBegins : kLater, turns ? i % 2 : s);
 }
 
 template <bool kFp8>
@@ -1238,7 +1243,8 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
                 const bool begins = static_cast<int>(blockIdx.x) == first || p.more == 0, alone = turns && p.tiles == 1;
                 const int from = p.more == 0 ? static_cast<int>(blockIdx.x) : first;  // the segment's first CTA
-                float *mine = part_slot(a.part, blockIdx.x, begins, s);
+                const bool whole = p.more == 0;
+                float *mine = part_slot(a.part, blockIdx.x, whole ? kWhole : begins ? kBegins : kLater, s);
 #pragma unroll 1
                 for (int c = 0; c < kDim; c += 32) {
                     float f[32];
@@ -1272,7 +1278,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (w == 0) ok = warp_wait(&sh.stored[s], joins & 1, a.wait_limit);
                 if (row == 0 && ok) {
                     int old;
-                    int32_t *ticket = a.tickets + 2 * from + (turns ? 0 : s);
+                    int32_t *ticket = a.tickets + kKinds * from + (whole ? 2 : turns ? 0 : s);
                     const int add = alone ? 2 : 1;
                     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(ticket), "r"(add) : "memory");
                     sh.last[s] = old + add == count;
@@ -1286,10 +1292,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (!*reinterpret_cast<volatile int *>(&sh.last[s]) || !real) continue;
                 float best = kNoScore, total = 0.0f;
 #pragma unroll 1
-                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, from, i, turns, s) + kRows * kDim + row));
+                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, from, i, turns, s, whole) + kRows * kDim + row));
 #pragma unroll 1
                 for (int i = 0; i < count; ++i) {
-                    const float *q = segment_part(a.part, from, i, turns, s) + kRows * kDim + row;
+                    const float *q = segment_part(a.part, from, i, turns, s, whole) + kRows * kDim + row;
                     total = fmaf(hw_ex2(__ldcg(q) - best), __ldcg(q + kRows), total);
                 }
                 const float inv = inverse(total);
@@ -1300,7 +1306,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
 #pragma unroll 1
                     for (int i = 0; i < count; ++i) {
-                        const float *q = segment_part(a.part, from, i, turns, s);
+                        const float *q = segment_part(a.part, from, i, turns, s, whole);
                         const float mq = __ldcg(q + kRows * kDim + row);
                         const float f = hw_ex2(mq - best);
                         if (turns && mq == kNoScore && __ldcg(q + kRows * kDim + kRows + row) == 0.0f) continue;  // (nothing there)
@@ -1447,8 +1453,8 @@ bool prompt_shape_ok(int B, int T, int Hq, int Hkv) {
     return B >= 0 && T >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0;
 }
 
-size_t prompt_part_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 4 * kPartFloats * sizeof(float), 256); }
-size_t prompt_ticket_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 2 * sizeof(int32_t), 256); }
+size_t prompt_part_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * kKinds * 2 * kPartFloats * sizeof(float), 256); }
+size_t prompt_ticket_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * kKinds * sizeof(int32_t), 256); }
 size_t prompt_job_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 2 * sizeof(int4), 256); }
 // parts, jobs, and last the tickets
 size_t prompt_workspace_bytes() { return prompt_part_bytes() + prompt_job_bytes() + prompt_ticket_bytes(); }

@@ -37,7 +37,7 @@ def run(s, err=None, ws=None, q=None):
     bd.tts_prompt_attn(cache, table, lens, start, q, out, ws, s["scale"], s["window"], s["sinks"], err=err)
     torch.cuda.synchronize()
     # the tickets are zero again
-    assert not ws[-8 * 152:].any()
+    assert not ws[-12 * 152:].any()
     return out
 
 
@@ -212,6 +212,20 @@ def test_rows_of_no_stream_are_left_alone():
     out = run(s, q=q)
     pr.check(out[:50], *pr.attend_all(s))
     assert bool((out[50:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seed", range(6))
+def test_segments_of_all_kinds_in_every_cta(dtype, seed):
+    """Several segments a CTA: whole and split, rows for both halves and for one that both work on in turns,
+    after one another in every order."""
+    g = torch.Generator().manual_seed(seed)
+    new = torch.randint(1, 700, (10,), generator=g).tolist()
+    before = torch.randint(0, 1500, (10,), generator=g).tolist()
+    s = pr.make(new, before, 8, 4, dtype, 1000 if seed % 2 else 0, 4, seed=seed)
+    first = run(s)
+    pr.check(first, *pr.attend_all(s))
+    assert torch.equal(run(s), first)
 
 
 def test_many_streams():
