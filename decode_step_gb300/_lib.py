@@ -18,7 +18,7 @@ TTS_VERIFY_BONUS = 1
 ERRBIT_BLOCK_ID, ERRBIT_CTX_LEN, ERRBIT_TOKEN, ERRBIT_TIMEOUT, ERRBIT_STREAM = 1, 2, 4, 8, 16
 LAUNCH_PROGRAMMATIC = 1
 TEST_STALL_NONE, TEST_STALL_ATTN_RING, TEST_STALL_PREDICTOR_GRID = 0, 1, 2
-TEST_STALL_LATENT_DECODE, TEST_STALL_LATENT_PREFILL, TEST_STALL_PROMPT = 4, 5, 6
+TEST_STALL_LATENT_DECODE, TEST_STALL_LATENT_PREFILL, TEST_STALL_PROMPT = 4, 5, 7
 
 HEADER = Path(__file__).resolve().parents[1] / "include" / "tts_decode.h"
 

@@ -166,7 +166,7 @@ extern "C" int32_t tts_set_launch_flags(int32_t flags) {
 }
 
 extern "C" int tts_test_set_stall(int32_t what, int64_t wait_limit_cycles) {
-    if (what < TTS_TEST_STALL_NONE || what > TTS_TEST_STALL_PROMPT || what == 3) return TTS_ERR_INVALID;
+    if (what < TTS_TEST_STALL_NONE || what > TTS_TEST_STALL_PROMPT || what == 3 || what == 6) return TTS_ERR_INVALID;
     if (wait_limit_cycles < 1000 || wait_limit_cycles > 4000000000LL) return TTS_ERR_INVALID;
     tts::ThreadOpts &o = tts::thread_opts();
     o.stall = what;

@@ -852,9 +852,9 @@ enum {
     TTS_TEST_STALL_NONE = 0,
     TTS_TEST_STALL_ATTN_RING = 1,
     TTS_TEST_STALL_PREDICTOR_GRID = 2,
-    TTS_TEST_STALL_LATENT_DECODE = 4, /* (3 is no mode) */
+    TTS_TEST_STALL_LATENT_DECODE = 4, /* (3 and 6 are no modes) */
     TTS_TEST_STALL_LATENT_PREFILL = 5,
-    TTS_TEST_STALL_PROMPT = 6
+    TTS_TEST_STALL_PROMPT = 7
 };
 int tts_test_set_stall(int32_t what, int64_t wait_limit_cycles);
 
