@@ -63,6 +63,7 @@ static_assert(kP + kTile / 2 <= kHalf);
 // converters instead of the checkers
 __host__ __device__ constexpr int prompt_threads(bool fp8) { return fp8 ? 512 : 448; }
 constexpr int kMostThreads = 512;
+constexpr int kFewTiles = 128;              // query tiles that one warp looks at
 constexpr int kMaxStreams = 4096;           // (their lengths are staged in shared memory)
 constexpr int kSnap = 2;                    // tiles
 constexpr int kPartCost = 2;                // what a segment costs beside its tiles, in tiles
@@ -76,6 +77,8 @@ __host__ __device__ constexpr float prompt_slack(bool fp8) { return fp8 ? 0.0f :
 constexpr int kPartFloats = kRows * kDim + 2 * kRows;  // o, m, l of a half
 constexpr int kPairTiles = 10;              // tiles of a part from which on half 1 stays half a step behind
 constexpr int kTakeTurns = 12;              // tiles of a segment from which on its one half's rows use both
+constexpr int kSoloTiles = 10;
+static_assert(kSoloTiles < kTakeTurns && (kSoloTiles - 2 * kSnap) / (kPartCost + 1) + 2 <= 4);
 constexpr int kJoinHere = 4;                // parts that the last CTA joins; more are left to the second kernel
 
 struct PromptArgs {
@@ -92,6 +95,7 @@ struct PromptArgs {
     int32_t *tickets;     // [CTA][kKinds]: of a segment that begins in it, either half; of one that it has whole
     int4 *jobs;           // [CTA][half] segments that the second kernel joins: rows (0: none), first row, KV head, parts
     int ctas, max_tiles;  // query tiles at most
+    int few;              // B <= 32 and few query tiles: one warp finds the ranges
     int zero_row;         // a row behind the pool: reads as zeros
     int32_t *err;
     long long wait_limit; // SM clock cycles per bounded wait
@@ -252,7 +256,7 @@ struct PromptShared {
     int odd[8];            // number of the part whose tiles held values that are not finite, by number % 8
     int last[2];           // whether the half's part was the last one
     long long scan[2][kMostThreads / 32];
-    int b, i, g, k, s0, first, n, ctx, from, to, q, rem;
+    int b, i, g, k, s0, first, n, ctx, from, to, q, rem, refused;
 };
 // Shared memory: the queries, the ring of keys, of values, in FP8 the codes of
 // either and the scales, and PromptShared.
@@ -302,8 +306,104 @@ __device__ __forceinline__ long long scan_before(long long mine, long long *warp
     return before;
 }
 
-// Finds the CTA's range: sh.b, i, g, k, s0 (its first tile) and sh.from, to.
-// `streams`: room for kMaxStreams + 1.  Every thread calls it.
+// What the CTA does, of T in all and of so many segments, into sh.q, rem and, where
+// it has no segment to look up, sh.from and to.  False: the CTA has nothing to do.
+__device__ __forceinline__ bool split_work(const PromptArgs &a, PromptShared &sh, int T, int segments, bool write, int *x0, int *x1) {
+    const int W = min(min(a.ctas, T), max((T + kMinTiles - 1) / kMinTiles, segments)), c = blockIdx.x;
+    const Ranges ranges{W ? T / W : 0, W ? T - T / W * W : 0};
+    if (write) {
+        sh.q = ranges.q;
+        sh.rem = ranges.rem;
+        if (c >= W) sh.from = sh.to = 0;
+        else if (c + 1 == W) sh.to = T - kPartCost * segments;
+    }
+    *x0 = ranges.start(c);
+    *x1 = ranges.start(c + 1);
+    return c < W;
+}
+// Where the range's ends x lie in query tile t (the i-th of stream b), whose
+// segments of n tiles begin at `at` in the list.
+__device__ __forceinline__ void look_up(const PromptArgs &a, PromptShared &sh, int x0, int x1, int at, int b, int t, int i, int n,
+                                        const int4 &stream) {
+    const int each = kPartCost + n;
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+        const int x = which ? x1 : x0;
+        if (x < at || x >= at + each * a.Hkv) continue;
+        const int g = (x - at) / each, s0 = at + g * each;
+        int k = x - s0 - kPartCost;
+        if (k <= kSnap) k = 0;
+        else if (n - k <= kSnap) k = n;
+        const int before = s0 - kPartCost * (t * a.Hkv + g) + k;  // tiles
+        if (which) {
+            sh.to = before;
+        } else {
+            sh.from = before;
+            sh.b = b;
+            sh.i = i;
+            sh.g = g;
+            sh.k = k;
+            sh.s0 = s0;
+            sh.first = stream.x;
+            sh.n = stream.y;
+            sh.ctx = stream.z;
+        }
+    }
+}
+
+// find_range by one warp, without a barrier, for up to 32 streams (a lane each)
+// and few query tiles: what a small call waits for before its first copy.
+__device__ __forceinline__ void find_range_few(const PromptArgs &a, PromptShared &sh) {
+    const int lane = threadIdx.x % 32;
+    int first = 0, n = 0, ctx = 0;
+    const bool good = lane >= a.B || prompt_stream(a, lane, &first, &n, &ctx);
+    const int refused = __any_sync(kFull, !good), mine = query_tiles(a, n);
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += x;
+    }
+    int tiles = __shfl_sync(kFull, upto, 31);
+    const int from = upto - mine;  // the stream's first query tile
+    const bool apart = tiles >= 0 && tiles <= a.max_tiles;  // (else the streams' rows overlap)
+    if (!apart) {
+        if (blockIdx.x == 0 && lane == 0) flag_error(a.err, TTS_ERRBIT_CTX_LEN);
+        tiles = 0;
+    }
+    if (lane == 0) sh.refused = refused;
+    int total = 0, x0 = 0, x1 = 0;
+    bool work = true;
+#pragma unroll 1
+    for (int pass = 0; work && pass < 2; ++pass) {
+        int at = 0;
+#pragma unroll 1
+        for (int t0 = 0; t0 < tiles; t0 += 32) {
+            const int t = t0 + lane;
+            int b = 0;  // the last stream that begins at or before tile t
+#pragma unroll
+            for (int step = 16; step > 0; step /= 2)
+                if (__shfl_sync(kFull, from, b + step) <= t) b += step;
+            const int4 s = make_int4(__shfl_sync(kFull, first, b), __shfl_sync(kFull, n, b), __shfl_sync(kFull, ctx, b),
+                                     __shfl_sync(kFull, from, b));
+            const int here = t < tiles ? span_of(a, s.y, s.z, t - s.w).tiles : -kPartCost;
+            int incl = kPartCost + here;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int x = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += x;
+            }
+            if (pass && t < tiles) look_up(a, sh, x0, x1, (at + incl - kPartCost - here) * a.Hkv, b, t, t - s.w, here, s);
+            at += __shfl_sync(kFull, incl, 31);
+        }
+        total = at;
+        if (!pass) work = split_work(a, sh, total * a.Hkv, tiles * a.Hkv, lane == 0, &x0, &x1);
+    }
+}
+
+// Finds the CTA's range: sh.from, to (tiles before its ends), its first stream,
+// query tile, KV head, tile (sh.b, i, g, k, s0, first, n, ctx), and sh.q, rem.
+// `streams`: room for kMaxStreams.  Every thread calls it; a barrier has to follow.
 template <int kThreads>
 __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh, int4 *streams) {
     const int per = (a.B + kThreads - 1) / kThreads;
@@ -352,47 +452,14 @@ __device__ __forceinline__ void find_range(const PromptArgs &a, PromptShared &sh
     each_tile([&](int, int, int, int n) { sum += kPartCost + n; });
     const long long before = scan_before<kThreads>(sum, sh.scan[1], &total) * a.Hkv;
     const int T = static_cast<int>(total) * a.Hkv;  // (below 2^30, as the host has seen to)
-    const int segments = tiles * a.Hkv;
-    const int W = min(min(a.ctas, T), max((T + kMinTiles - 1) / kMinTiles, segments));
-    const int c = blockIdx.x;
-    Ranges ranges{W ? T / W : 0, W ? T % W : 0};
-    if (threadIdx.x == 0) {
-        sh.q = ranges.q;
-        sh.rem = ranges.rem;
-        if (c >= W) sh.from = sh.to = 0;
-        else if (c + 1 == W) sh.to = T - kPartCost * segments;
-    }
-    if (c < W) {
-        const int x0 = ranges.start(c), x1 = ranges.start(c + 1);
+    int x0, x1;
+    if (split_work(a, sh, T, tiles * a.Hkv, threadIdx.x == 0, &x0, &x1)) {
         int at_tile = static_cast<int>(before);
         each_tile([&](int b, int t, int i, int n) {
-            const int each_g = kPartCost + n, end = at_tile + each_g * a.Hkv;
-            for (int which = 0; which < 2; ++which) {
-                const int x = which ? x1 : x0;
-                if (x < at_tile || x >= end) continue;
-                const int g = (x - at_tile) / each_g, s0 = at_tile + g * each_g;
-                int k = x - s0 - kPartCost;
-                if (k <= kSnap) k = 0;
-                else if (n - k <= kSnap) k = n;
-                const int before_it = s0 - kPartCost * (t * a.Hkv + g) + k;  // tiles
-                if (which) {
-                    sh.to = before_it;
-                } else {
-                    sh.from = before_it;
-                    sh.b = b;
-                    sh.i = i;
-                    sh.g = g;
-                    sh.k = k;
-                    sh.s0 = s0;
-                    sh.first = streams[b].x;
-                    sh.n = streams[b].y;
-                    sh.ctx = streams[b].z;
-                }
-            }
-            at_tile = end;
+            look_up(a, sh, x0, x1, at_tile, b, t, i, n, streams[b]);
+            at_tile += (kPartCost + n) * a.Hkv;
         });
     }
-    __syncthreads();
 }
 
 // CTAs that share a segment: its first part's and how many follow.
@@ -614,12 +681,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    find_range<kThreads>(a, sh, reinterpret_cast<int4 *>(raw + Smem::keys));
-    // (the staged lengths make way for copies)
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (a.few) {
+        if (warp == 13) find_range_few(a, sh);
+    } else {
+        find_range<kThreads>(a, sh, reinterpret_cast<int4 *>(raw + Smem::keys));
+        // (the staged lengths make way for copies)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (a.few && sh.refused) zero_refused(a);
     pdl_allow_dependents();
     const uint32_t tmem = uniform(sh.tmem);
     const Ranges ranges{uniform(sh.q), uniform(sh.rem)};
@@ -1528,6 +1600,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     // the flat list of tiles is 32-bit
     const int64_t query_tiles = static_cast<int64_t>(num_rows) / (2 * a.tokens) + B;
     a.max_tiles = static_cast<int>(query_tiles);
+    a.few = B <= 32 && query_tiles <= kFewTiles;
     if (query_tiles * Hkv * (max_blocks_per_seq / kBlocks + 1 + kPartCost) >= (1LL << 30)) return TTS_ERR_UNSUPPORTED;
     CUtensorMap map_q, map_k{}, map_v{};
     if (!make_tma_queries_bf16(&map_q, d_q, num_rows, Hq, a.group, a.tokens)) return TTS_ERR_CUDA;
@@ -1539,8 +1612,9 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     if (!allow_smem(kernel, smem)) return TTS_ERR_CUDA;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const int rc = launch_kernel(kernel, dim3(a.ctas), dim3(prompt_threads(fp8)), smem, {cs, thread_pdl()}, map_q, map_k, map_v, a);
-    // no segment has more than 2 * kSnap tiles: none is split
-    if (rc != TTS_OK || max_blocks_per_seq <= 2 * kSnap * kBlocks) return rc;
+    // With at most kSoloTiles tiles no segment is worked on in turns, nor has it more
+    // than kJoinHere parts (a range is at least kPartCost + 1 long): none is left over
+    if (rc != TTS_OK || max_blocks_per_seq <= kSoloTiles * kBlocks) return rc;
     return launch_kernel(prompt_join_kernel, dim3(a.ctas), dim3(kJoinThreads), 0, {cs, true}, a.part, a.jobs, a.ctas, a.out,
                          a.Hq, a.group);
 }
