@@ -76,7 +76,12 @@ constexpr float kNoScore = -FLT_MAX;
 __host__ __device__ constexpr float prompt_slack(bool fp8) { return fp8 ? 0.0f : 8.0f; }
 constexpr int kPartFloats = kRows * kDim + 2 * kRows;  // o, m, l of a half
 constexpr int kPairTiles = 10;              // tiles of a part from which on half 1 stays half a step behind
-constexpr int kTakeTurns = 12;              // tiles of a segment from which on its one half's rows use both
+// One half's rows use both halves, tile by tile, in segments of at least so many
+// tiles that are spread over more than two ranges: where a few rows meet a long
+// context the chain of one tile is the bound (4 streams of 17 rows after 4,000: 23
+// us, else 36).  Others gain nothing and would have parts to join (32 streams: 101
+// us, with turns 114; after 1,000 tokens 42 and 58).
+constexpr int kTakeTurns = 24;
 constexpr int kSoloTiles = 10;
 static_assert(kSoloTiles < kTakeTurns && (kSoloTiles - 2 * kSnap) / (kPartCost + 1) + 2 <= 4);
 constexpr int kJoinHere = 4;                // parts that the last CTA joins; more are left to the second kernel
@@ -91,8 +96,8 @@ struct PromptArgs {
     float scale_log2;
     const uint8_t *k_pool, *v_pool;           // FP8: the records, and none
     __nv_bfloat16 *out;
-    float *part;          // [CTA][kind][half] partial results
-    int32_t *tickets;     // [CTA][kKinds]: of a segment that begins in it, either half; of one that it has whole
+    float *part;          // [CTA][first, later part][half] partial results
+    int32_t *tickets;     // [CTA][half] of a segment that begins in it
     int4 *jobs;           // [CTA][half] segments that the second kernel joins: rows (0: none), first row, KV head, parts
     int ctas, max_tiles;  // query tiles at most
     int few;              // B <= 32 and few query tiles: one warp finds the ranges
@@ -167,7 +172,9 @@ struct Walk {
     __device__ __forceinline__ int r0(const PromptArgs &a) const { return i * 2 * a.tokens; }
     __device__ __forceinline__ bool two(const PromptArgs &a) const { return r0(a) + a.tokens < n; }
     __device__ __forceinline__ int tiles() const { return min(left, span.tiles - k); }  // of the part, from its first one on
-    __device__ __forceinline__ int mode(const PromptArgs &a) const { return two(a) ? kBoth : span.tiles >= kTakeTurns ? kTurns : 0; }
+    __device__ __forceinline__ int mode(const PromptArgs &a, int range) const {
+        return two(a) ? kBoth : span.tiles >= kTakeTurns && span.tiles > 2 * range ? kTurns : 0;
+    }
     __device__ __forceinline__ void seek(const PromptArgs &a) {  // b: the next stream that has rows
         for (; b < a.B; ++b) {
             const bool good = prompt_stream(a, b, &first, &n, &ctx);
@@ -608,21 +615,17 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *out, const float *f, fl
 }
 __device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }  // no token left: zeros
 
-// Slot of a part: CTA, kind, half.  [32][128 rows][4] floats o, then m and l of
-// the rows.  A CTA's parts of split segments are its first one (if the segment
-// began in an earlier CTA) and its last one; segments that it has whole, but in
-// turns, have a slot of their own, which the next such one may write once both
-// halves are done with this: it is at least kTakeTurns tiles long, and a half is
-// never more than the ring ahead of the other.
-constexpr int kBegins = 0, kLater = 1, kWhole = 2, kKinds = 3;
-__device__ __forceinline__ float *part_slot(float *parts, int cta, int kind, int half) {
-    return parts + static_cast<size_t>((cta * kKinds + kind) * 2 + half) * kPartFloats;
+// Slot of a part: CTA, whether the segment begins in it, half.  [32][128 rows][4]
+// floats o, then m and l of the rows.  (A CTA's parts of split segments are its
+// first one, of a segment that began in an earlier CTA, and its last one.)
+__device__ __forceinline__ float *part_slot(float *parts, int cta, bool begins, int half) {
+    return parts + static_cast<size_t>((cta * 2 + (begins ? 0 : 1)) * 2 + half) * kPartFloats;
 }
 // Part i of a segment whose first CTA is `first`: one a CTA (of half s), or with
 // both halves' in turns two.
-__device__ __forceinline__ float *segment_part(float *parts, int first, int i, bool turns, int s, bool whole = false) {
+__device__ __forceinline__ float *segment_part(float *parts, int first, int i, bool turns, int s) {
     const int c = turns ? i / 2 : i;
-    return part_slot(parts, first + c, whole ? kWhole : c == 0 ? kBegins : kLater, turns ? i % 2 : s);
+    return part_slot(parts, first + c, c == 0, turns ? i % 2 : s);
 }
 
 template <bool kFp8>
@@ -734,7 +737,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 int uses[2] = {0, 0};
                 int tiles = walk.tiles(), id = lookup(walk, tiles, 0);
                 for (bool begun = false; ok && walk.left > 0;) {
-                    const int mode = walk.mode(a), note = part % kInfos, r0 = walk.r0(a), before = walk.ctx - walk.n;
+                    const int mode = walk.mode(a, ranges.q), note = part % kInfos, r0 = walk.r0(a), before = walk.ctx - walk.n;
                     if (for_keys && lane == 0) {
                         const Shares shares = shares_of(ranges, walk.s0, walk.span.tiles);
                         PartInfo &p = sh.parts[note];
@@ -1313,10 +1316,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     if (lane == 0) mbar_arrive(smem_addr(&sh.o_empty[s]));
                     continue;
                 }
-                const bool begins = static_cast<int>(blockIdx.x) == first || p.more == 0, alone = turns && p.tiles == 1;
-                const int from = p.more == 0 ? static_cast<int>(blockIdx.x) : first;  // the segment's first CTA
-                const bool whole = p.more == 0;
-                float *mine = part_slot(a.part, blockIdx.x, whole ? kWhole : begins ? kBegins : kLater, s);
+                // (a part in turns is of a segment of several CTAs: their rule sees to that)
+                const bool begins = static_cast<int>(blockIdx.x) == first, alone = turns && p.tiles == 1;
+                float *mine = part_slot(a.part, blockIdx.x, begins, s);
 #pragma unroll 1
                 for (int c = 0; c < kDim; c += 32) {
                     float f[32];
@@ -1350,7 +1352,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (w == 0) ok = warp_wait(&sh.stored[s], joins & 1, a.wait_limit);
                 if (row == 0 && ok) {
                     int old;
-                    int32_t *ticket = a.tickets + kKinds * from + (whole ? 2 : turns ? 0 : s);
+                    int32_t *ticket = a.tickets + 2 * first + (turns ? 0 : s);
                     const int add = alone ? 2 : 1;
                     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(ticket), "r"(add) : "memory");
                     sh.last[s] = old + add == count;
@@ -1364,10 +1366,10 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 if (!*reinterpret_cast<volatile int *>(&sh.last[s]) || !real) continue;
                 float best = kNoScore, total = 0.0f;
 #pragma unroll 1
-                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, from, i, turns, s, whole) + kRows * kDim + row));
+                for (int i = 0; i < count; ++i) best = fmaxf(best, __ldcg(segment_part(a.part, first, i, turns, s) + kRows * kDim + row));
 #pragma unroll 1
                 for (int i = 0; i < count; ++i) {
-                    const float *q = segment_part(a.part, from, i, turns, s, whole) + kRows * kDim + row;
+                    const float *q = segment_part(a.part, first, i, turns, s) + kRows * kDim + row;
                     total = fmaf(hw_ex2(__ldcg(q) - best), __ldcg(q + kRows), total);
                 }
                 const float inv = inverse(total);
@@ -1378,7 +1380,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     for (int i = 0; i < 32; ++i) o[i] = 0.0f;
 #pragma unroll 1
                     for (int i = 0; i < count; ++i) {
-                        const float *q = segment_part(a.part, from, i, turns, s, whole);
+                        const float *q = segment_part(a.part, first, i, turns, s);
                         const float mq = __ldcg(q + kRows * kDim + row);
                         const float f = hw_ex2(mq - best);
                         if (turns && mq == kNoScore && __ldcg(q + kRows * kDim + kRows + row) == 0.0f) continue;  // (nothing there)
@@ -1525,8 +1527,8 @@ bool prompt_shape_ok(int B, int T, int Hq, int Hkv) {
     return B >= 0 && T >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0;
 }
 
-size_t prompt_part_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * kKinds * 2 * kPartFloats * sizeof(float), 256); }
-size_t prompt_ticket_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * kKinds * sizeof(int32_t), 256); }
+size_t prompt_part_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 4 * kPartFloats * sizeof(float), 256); }
+size_t prompt_ticket_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 2 * sizeof(int32_t), 256); }
 size_t prompt_job_bytes() { return align_up(static_cast<size_t>(prompt_ctas()) * 2 * sizeof(int4), 256); }
 // parts, jobs, and last the tickets
 size_t prompt_workspace_bytes() { return prompt_part_bytes() + prompt_job_bytes() + prompt_ticket_bytes(); }
