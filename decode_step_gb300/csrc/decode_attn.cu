@@ -795,13 +795,34 @@ template <bool kFp8>
 __device__ __forceinline__ uint32_t clear_hidden(uint8_t *v, uint32_t any, uint32_t every, int lane) {
     uint32_t bad = 0;
     if constexpr (kFp8) {
-        for (int d = lane; d < 128; d += 32) {
-            for (int t = 0; t < TTS_BLOCK_TOKENS; ++t) {
-                uint8_t *p = v + value_at<true>(t, d);
-                if (!((any >> t) & 1)) *p = 0;
-                else if (!((every >> t) & 1) && (*p & 0x7F) == 0x7F) bad |= 1u << t;
+        // a dimension's 16 codes are a row: byte k of word j is slot 2j + k % 2 + 8 (k / 2)
+        uint32_t keep[4], part[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            keep[j] = part[j] = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = 2 * j + (k & 1) + 8 * (k >> 1);
+                if ((any >> t) & 1) keep[j] |= 0xFFu << (8 * k);
+                if (((any & ~every) >> t) & 1) part[j] |= 0x80u << (8 * k);
             }
         }
+        uint32_t odd[4] = {0u, 0u, 0u, 0u};  // 0x80 in a byte: such a code in a token of `part`
+        uint4 *rows = reinterpret_cast<uint4 *>(v);
+#pragma unroll
+        for (int d = lane; d < 128; d += 32) {
+            uint4 x = rows[d];
+            x.x &= keep[0]; x.y &= keep[1]; x.z &= keep[2]; x.w &= keep[3];
+            rows[d] = x;
+            odd[0] |= ((x.x & 0x7F7F7F7Fu) + 0x01010101u) & part[0];
+            odd[1] |= ((x.y & 0x7F7F7F7Fu) + 0x01010101u) & part[1];
+            odd[2] |= ((x.z & 0x7F7F7F7Fu) + 0x01010101u) & part[2];
+            odd[3] |= ((x.w & 0x7F7F7F7Fu) + 0x01010101u) & part[3];
+        }
+        if (odd[0] | odd[1] | odd[2] | odd[3])
+#pragma unroll
+            for (int t = 0; t < TTS_BLOCK_TOKENS; ++t)
+                if ((odd[(t & 7) >> 1] >> (8 * ((t & 1) + 2 * (t >> 3)))) & 0x80u) bad |= 1u << t;
     } else {
         for (int i = lane; i < TTS_BLOCK_TOKENS * 16; i += 32) {
             const int t = i / 16;
