@@ -1087,6 +1087,20 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         }
         if (!timed_out && t_id >= 0 && t_id < a.num_blocks) {
             const int base_tok = block_at(t_blk) * TTS_BLOCK_TOKENS;
+            // kWindow: whether every row sees the whole tile, and where not what the
+            // lane's two rows see (bit t: token base_tok + t)
+            const int first_limit = kWindow && a.causal ? seg_L - a.q_len + 1 : seg_L;
+            const bool whole = kWindow && base_tok + TTS_BLOCK_TOKENS <= first_limit &&
+                               (base_tok + TTS_BLOCK_TOKENS <= a.sinks || base_tok >= seg_L - a.window);
+            uint32_t seen_a = 0xFFFFu, seen_b = 0xFFFFu;
+            if (kWindow && !whole) {
+                seen_a = seen_mask(a, base_tok, limA, limA, true);
+                seen_b = seen_mask(a, base_tok, limB, limB, true);
+            }
+            auto row_sees = [&](int t, int limit, uint32_t seen) {  // t: of the tile
+                if constexpr (kWindow) return ((seen >> t) & 1u) != 0;
+                return base_tok + t < limit;
+            };
             // ---- S = Q K^T: 2 n-tiles of 8 tokens x 8 k-steps of 16 dims
             float s[2][4];
             // FP8: this lane's key and value scales (tokens 2t, 2t+1 | 2t+8, 2t+9)
@@ -1138,11 +1152,11 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tok = base_tok + 8 * nt + 2 * ft + e;
+                    const int tok = 8 * nt + 2 * ft + e;
                     float f = a.qscale;
                     if constexpr (kFp8) f *= (e == 0 ? ksc[nt].x : ksc[nt].y);
-                    xa[2 * nt + e] = sees(tok, limA) ? s[nt][e] * f : -INFINITY;
-                    xb[2 * nt + e] = sees(tok, limB) ? s[nt][2 + e] * f : -INFINITY;
+                    xa[2 * nt + e] = row_sees(tok, limA, seen_a) ? s[nt][e] * f : -INFINITY;
+                    xb[2 * nt + e] = row_sees(tok, limB, seen_b) ? s[nt][2 + e] * f : -INFINITY;
                 }
             }
             float ma = fmaxf(fmaxf(xa[0], xa[1]), fmaxf(xa[2], xa[3]));
@@ -1178,10 +1192,10 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 float qa_[4], qb_[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int tok = base_tok + 8 * (e >> 1) + 2 * ft + (e & 1);
+                    const int tok = 8 * (e >> 1) + 2 * ft + (e & 1);
                     const float vs = ((e & 1) ? vsc[e >> 1].y : vsc[e >> 1].x) * kFp8PFix;
-                    qa_[e] = sees(tok, limA) ? pa[e] * vs : 0.0f;
-                    qb_[e] = sees(tok, limB) ? pb[e] * vs : 0.0f;
+                    qa_[e] = row_sees(tok, limA, seen_a) ? pa[e] * vs : 0.0f;
+                    qb_[e] = row_sees(tok, limB, seen_b) ? pb[e] * vs : 0.0f;
                 }
                 pf[0] = pack_f16x2(qa_[0], qa_[1]);
                 pf[1] = pack_f16x2(qb_[0], qb_[1]);
@@ -1229,14 +1243,13 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                 // the windows, and causal rows' last tokens): where none does
                 // the values are cleared, else those that are not finite go to
                 // the rows that see them here and are cleared for the product.
-                const int first = a.causal ? seg_L - a.q_len + 1 : seg_L;  // the first row's limit
-                const uint32_t any = seen_mask(a, base_tok, first, seg_L, false);
-                const uint32_t every = seen_mask(a, base_tok, first, seg_L, true);
-                if (every != 0xFFFFu) {
+                if (!whole) {
+                    const uint32_t any = seen_mask(a, base_tok, first_limit, seg_L, false);
+                    const uint32_t every = seen_mask(a, base_tok, first_limit, seg_L, true);
                     const uint32_t bad = clear_hidden<kFp8>(smem + (vt - base), any, every, lane);
                     for (uint32_t m = bad; m; m &= m - 1) {
                         const int t = __ffs(m) - 1;
-                        const bool ina = sees(base_tok + t, limA), inb = sees(base_tok + t, limB);
+                        const bool ina = (seen_a >> t) & 1, inb = (seen_b >> t) & 1;
 #pragma unroll
                         for (int nt = 0; nt < 16; ++nt)
 #pragma unroll
