@@ -81,6 +81,15 @@ class KVCache:
             vptr = _dev(v_pool, "v_pool")
         self.k_pool, self.v_pool = k_pool, v_pool
         self.desc = KVCacheDesc(nb, 16, hkv, d, dtype, _dev(k_pool, "k_pool"), vptr)
+        self._ref = ctypes.byref(self.desc)
+        # (num_kv_heads, head_dim, dtype: a field of the descriptor or a property takes longer to read)
+        self._shape = hkv, d, torch.bfloat16 if self.fp8 else k_pool.dtype
+
+    def on(self, device: int):
+        """The descriptor for a call on `device`."""
+        if self.k_pool.get_device() != device or (self.v_pool is not None and self.v_pool.get_device() != device):
+            raise ValueError(f"the cache is on {self.k_pool.device}, the current device is cuda:{device}")
+        return self._ref
 
     @property
     def num_blocks(self) -> int:
@@ -185,16 +194,6 @@ def tts_kv_append_rope(cache: KVCache, block_table, ctx_before, q, k_new, v_new,
     check("tts_kv_append_rope", lib().tts_kv_append_rope(*args))
 
 
-def _cache_on(cache, device: int):
-    """The descriptor of a KV cache for a call on `device`, the current one."""
-    if isinstance(cache, LatentCache):
-        return cache.on(device)
-    for pool in (cache.k_pool, cache.v_pool):
-        if pool is not None and pool.get_device() != device:
-            raise ValueError(f"the cache is on {pool.device}, the current device is cuda:{device}")
-    return ctypes.byref(cache.desc)
-
-
 def tts_kv_append_packed(cache: KVCache, block_table, ctx_before, row_start, k_new, v_new, q=None, q_out=None,
                          rope_base=0.0, err=None, stream=None):
     """Appends the packed rows k_new, v_new [T][Hkv][head_dim] of streams of
@@ -208,13 +207,14 @@ def tts_kv_append_packed(cache: KVCache, block_table, ctx_before, row_start, k_n
         raise ValueError("q_out without q")
     i32, dev = torch.int32, torch.cuda.current_device()
     Hq = 0 if q is None else q.shape[1]
-    shape = (T, cache.num_kv_heads, cache.head_dim)
-    qp = None if q is None else _on(q, "q", cache.dtype, (T, Hq, cache.head_dim), dev)
+    Hkv, D, dtype = cache._shape
+    shape = (T, Hkv, D)
+    qp = None if q is None else _on(q, "q", dtype, (T, Hq, D), dev)
     check("tts_kv_append_packed", lib().tts_kv_append_packed(
-        _cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        cache.on(dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
         _on(ctx_before, "ctx_before", i32, (B,), dev), B, _on(row_start, "row_start", i32, (B + 1,), dev), T, Hq,
-        float(rope_base), qp, qp if q_out is None else _on(q_out, "q_out", cache.dtype, (T, Hq, cache.head_dim), dev),
-        _on(k_new, "k_new", cache.dtype, shape, dev), _on(v_new, "v_new", cache.dtype, shape, dev),
+        rope_base, qp, qp if q_out is None else _on(q_out, "q_out", dtype, (T, Hq, D), dev),
+        _on(k_new, "k_new", dtype, shape, dev), _on(v_new, "v_new", dtype, shape, dev),
         None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
 
 
@@ -228,7 +228,7 @@ def tts_kv_copy_blocks(cache, src, dst, err=None, stream=None):
     """Block dst[i] of a KVCache or LatentCache becomes block src[i] (int32 [n])."""
     n, i32, dev = src.shape[0], torch.int32, torch.cuda.current_device()
     fn, name = _pages(cache, "copy_blocks")
-    check(name, fn(_cache_on(cache, dev), _on(src, "src", i32, (n,), dev), _on(dst, "dst", i32, (n,), dev), n,
+    check(name, fn(cache.on(dev), _on(src, "src", i32, (n,), dev), _on(dst, "dst", i32, (n,), dev), n,
                    None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
 
 
@@ -239,7 +239,7 @@ def tts_kv_fork(cache, block_table, ctx_lens, parent, child, new_block, err=None
     B, max_blocks = block_table.shape
     n, i32, dev = parent.shape[0], torch.int32, torch.cuda.current_device()
     fn, name = _pages(cache, "fork")
-    check(name, fn(_cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+    check(name, fn(cache.on(dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
                    _on(ctx_lens, "ctx_lens", i32, (B,), dev), B, _on(parent, "parent", i32, (n,), dev),
                    _on(child, "child", i32, (n,), dev), _on(new_block, "new_block", i32, (n,), dev), n,
                    None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
@@ -251,7 +251,7 @@ def tts_kv_compact(cache, block_map, block_table, err=None, stream=None):
     B, max_blocks = block_table.shape
     i32, dev = torch.int32, torch.cuda.current_device()
     fn, name = _pages(cache, "compact")
-    check(name, fn(_cache_on(cache, dev), _on(block_map, "block_map", i32, (cache.num_blocks,), dev),
+    check(name, fn(cache.on(dev), _on(block_map, "block_map", i32, (cache.num_blocks,), dev),
                    _on(block_table, "block_table", i32, None, dev), max_blocks, B,
                    None if err is None else _on(err, "err", i32, None, dev), _raw_stream(stream, dev)))
 
@@ -279,13 +279,14 @@ def tts_window_decode_attn(cache: KVCache, block_table, ctx_lens, max_ctx_len, q
     """tts_decode_attn over the last `window` tokens of each row's and the first
     `sinks`; the workspace is tts_decode_attn's."""
     B, max_blocks = block_table.shape
-    _, q_len, Hq, D = q.shape
+    _, q_len, Hq, _ = q.shape
     i32, dev = torch.int32, torch.cuda.current_device()
-    shape = (B, q_len, Hq, cache.head_dim)
+    _, D, dtype = cache._shape
+    shape = (B, q_len, Hq, D)
     check("tts_window_decode_attn", lib().tts_window_decode_attn(
-        _cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
-        _on(ctx_lens, "ctx_lens", i32, (B,), dev), int(max_ctx_len), B, q_len, Hq, float(scale), int(bool(causal)),
-        int(window), int(sinks), _on(q, "q", cache.dtype, shape, dev), _on(out, "out", cache.dtype, shape, dev),
+        cache.on(dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_lens, "ctx_lens", i32, (B,), dev), max_ctx_len, B, q_len, Hq, scale, 1 if causal else 0, window, sinks,
+        _on(q, "q", dtype, shape, dev), _on(out, "out", dtype, shape, dev),
         _on(ws, "ws", None, None, dev), ws.nbytes, None if err is None else _on(err, "err", i32, None, dev),
         _raw_stream(stream, dev)))
 
@@ -300,13 +301,14 @@ def tts_prompt_attn(cache: KVCache, block_table, ctx_lens, row_start, q, out, ws
     streams' cached tokens (ctx_lens, the rows' own among them) -> out, alike;
     row_start int32 [B + 1]; window 0: the whole context."""
     B, max_blocks = block_table.shape
-    T, Hq, D = q.shape
+    T, Hq, _ = q.shape
     i32, dev = torch.int32, torch.cuda.current_device()
-    shape = (T, Hq, cache.head_dim)
+    _, D, dtype = cache._shape
+    shape = (T, Hq, D)
     check("tts_prompt_attn", lib().tts_prompt_attn(
-        _cache_on(cache, dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
-        _on(ctx_lens, "ctx_lens", i32, (B,), dev), B, _on(row_start, "row_start", i32, (B + 1,), dev), T, Hq, float(scale),
-        int(window), int(sinks), _on(q, "q", cache.dtype, shape, dev), _on(out, "out", cache.dtype, shape, dev),
+        cache.on(dev), _on(block_table, "block_table", i32, None, dev), max_blocks,
+        _on(ctx_lens, "ctx_lens", i32, (B,), dev), B, _on(row_start, "row_start", i32, (B + 1,), dev), T, Hq, scale,
+        window, sinks, _on(q, "q", dtype, shape, dev), _on(out, "out", dtype, shape, dev),
         _on(ws, "ws", None, None, dev), ws.nbytes, None if err is None else _on(err, "err", i32, None, dev),
         _raw_stream(stream, dev)))
 
