@@ -1168,7 +1168,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     const volatile PartInfo *p = &sh.parts[(flags >> kPartShift) % kInfos];
                     const int before = p->ctx - p->n, from = p->r0 + (s == 1 && p->mode == kBoth ? a.tokens : 0);
                     limit = before + min(from + token + 1, min(p->n, from + a.tokens));
-                    m = kNoScore;
+                    // (matrix rows that are no query hold whatever is there, and have no say in the
+                    // warp's maximum: the others' roundings would depend on it)
+                    m = token < a.tokens && from + token < p->n ? kNoScore : INFINITY;
                     l = 0.0f;
                 }
                 uint32_t x[kTile];

@@ -228,6 +228,20 @@ def test_segments_of_all_kinds_in_every_cta(dtype, seed):
     assert torch.equal(run(s), first)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_streams_bits_do_not_depend_on_its_neighbours(dtype):
+    """The rows next to a stream's last in a tile are the next stream's, and with three heads a
+    group two are no query at all: neither may move what the stream's own rows are rounded by."""
+    s = pr.make([85, 70, 130], [700, 500, 0], 6, 2, dtype, seed=31)
+    first = run(s)
+    loud = s["q"].clone()
+    loud[85:] *= 64.0
+    mixed = run(s, q=loud.cuda())
+    assert torch.equal(first[:85], mixed[:85])
+    run(s, q=(s["q"] * 64.0).cuda())
+    assert torch.equal(first, run(s))
+
+
 def test_many_streams():
     new = [(7 * i) % 5 for i in range(700)]
     good(pr.make(new, [(13 * i) % 90 for i in range(700)], 2, 1, "bf16", seed=12))
