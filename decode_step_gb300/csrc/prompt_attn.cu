@@ -6,27 +6,49 @@
 // Work.  A query tile is two halves of 128 matrix rows; a half holds 128 /
 // group tokens with all `group` query heads of one KV head (so that a KV tile is
 // read once for the group).  A segment is a query tile and a KV head; its work is
-// the 128-token tiles of the context that some row sees.  The flat list of all
-// segments' tiles is split into equal contiguous ranges, one a CTA: long and
-// short segments, prompts and few rows over a long context all spread over the
-// SMs alike.  A range boundary that falls within kSnap tiles of a segment's end
-// moves there; a segment that is split all the same is published in parts (m, l,
-// o), and the last CTA to finish one (an atomic ticket, never a wait) joins them
-// in the order of the CTAs, so that results do not depend on who is last.  Every
-// CTA finds its range by itself from the streams' lengths.
+// the 80-token tiles of the context that some row sees.  The flat list of all
+// segments, each kPartCost and then its tiles long, is split into equal contiguous
+// ranges, one a CTA: long and short segments, prompts and few rows over a long
+// context all spread over the SMs alike (without the kPartCost the CTAs with many
+// short segments ran 40% longer).  A range boundary that falls within kSnap tiles of
+// a segment's end moves there; a segment that is split all the same is published in
+// parts (m, l, o), and the last CTA to finish one (an atomic ticket, never a wait)
+// joins them in the order of the CTAs, so that results do not depend on who is
+// last; more than kJoinHere parts are left to a second kernel.  Every CTA finds its
+// range by itself from the streams' lengths.
 //
-// A CTA.  Two softmax warpgroups, one a half, that take turns on the tensor core;
-// a producer warp (TMA, one box of 16 tokens x 64 dimensions a block, through the
-// table); an MMA issuer; two warps that look at the values of the tiles that not
-// every row sees whole (below).  S = Q K^T and O += P V run as tcgen05 MMAs of
-// 128 x 128 x 16; S and O are in tensor memory, P (bf16, 2^-9 of a weight at
-// most; the softmax sum is of the weights before the rounding) goes back into
-// S's columns.
+// A CTA: two softmax warpgroups, one a half (or, where one half has no rows and the
+// context is long, both on the one half's, tile by tile in turns); an MMA issuer a
+// half (a commit or a wait takes its warp about 190 cycles: one issuer was the
+// bound); a producer of keys and queries and one of values (TMA through the table, a
+// box of 16 tokens x 64 dimensions of keys, 16 x 128 of values; FP8: bulk copies of
+// codes and scales).  bf16: two warps that look at the values of the tiles that not
+// every row sees whole (below).  FP8: four warps that turn codes into f16, which is
+// exact, where the MMAs want them; the keys' scales go to the scores, the values' to
+// the weights.
+//
+// A tile.  S = Q K^T is a tcgen05 MMA of 128 x 80 x 128 from shared memory, O += P V
+// one of 128 x 128 x 80 with P from tensor memory.  80 tokens, because 80 columns of
+// scores, 40 of weights and 128 of output fit a half's 256 columns side by side: the
+// next scores need only that the last ones were read.  (With 128 tokens P lies in S's
+// columns, and scores, softmax and product are one chain of 3,300 cycles a tile.)  P
+// is bf16 (FP8: f16, times the value's scale); the softmax sum is of the fp32 weights
+// before that rounding (2^-8 of a weight at most; f16 2^-11).  The running maximum
+// moves only when a score passes it by more than prompt_slack.
+//
+// What bounds it.  Long prompts (8,191 rows after 700, 16 query and 8 KV heads): 248
+// us, 1.30 PFLOP/s, 0.68 of a dense product's measured rate; the softmax warps take
+// about 2,000 cycles a tile for both halves, the MMAs 1,435 of them (the first, with
+// both operands in shared memory, 417 a half, bound by their 128 bytes a cycle; the
+// second 320).  61 rows after 65,472: 58 us, 4.6 TB/s.  333 rows: 18 us, latency.
+// FP8: instruction issue of the conversions and scales, twice the bf16 time.  A CTA
+// does not have 16 softmax warps (two threads a row: 386 us, spills and twice the
+// reads of scores).
 //
 // Values that are not finite.  A weight of zero times NaN is NaN, so a token that
 // a row does not see must not meet it in the matrix product.  Tiles that every
-// row sees need no care.  In the others the two spare warps clear such values in
-// shared memory, and the rows that do see them get them at the end.
+// row sees need no care.  In the others the checkers (FP8: the converters) clear such
+// values in shared memory, and the rows that do see them get them at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -75,7 +97,10 @@ constexpr float kNoScore = -FLT_MAX;
 // at 1 at most, so that with a scale below 256 they are in f16's range.
 __host__ __device__ constexpr float prompt_slack(bool fp8) { return fp8 ? 0.0f : 8.0f; }
 constexpr int kPartFloats = kRows * kDim + 2 * kRows;  // o, m, l of a half
-constexpr int kPairTiles = 10;              // tiles of a part from which on half 1 stays half a step behind
+// Tiles of a part from which on half 1 stays half a step behind, its exponentials
+// while half 0 waits and loads; short parts are a chain of latencies, which that would
+// lengthen.
+constexpr int kPairTiles = 10;
 // One half's rows use both halves, tile by tile, in segments of at least so many
 // tiles that are spread over more than two ranges: where a few rows meet a long
 // context the chain of one tile is the bound (4 streams of 17 rows after 4,000: 23
@@ -1417,8 +1442,9 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 // Segments of more than kJoinHere parts: one CTA's threads would read them at a
 // few bytes a cycle (61 rows of 8 KV heads in 19 parts of 62 KB each: 54 us), so
 // a second kernel spreads the work over every SM, 128 rows of 8 dimensions an
-// item, four threads a row.  It always runs, and finds that there is nothing to do by looking at one
-// word a CTA and half.
+// item, four threads a row (that call whole: 95 us, with this kernel 58).  It runs
+// wherever a table may hold more than kSoloTiles tiles, and finds that there is
+// nothing to do by looking at one word a CTA and half.
 constexpr int kJoinThreads = 512, kJoinItems = kDim / 8, kJoinGroups = kJoinThreads / kRows;
 
 __global__ void __launch_bounds__(kJoinThreads)

@@ -322,8 +322,8 @@ size_t tts_prompt_attn_workspace_size(int32_t B, int32_t num_rows, int32_t num_q
  *  window, sinks  >= 0; window 0: the whole context
  * Supported: TTS_BF16 and TTS_FP8_E4M3, head_dim 128, num_q_heads / num_kv_heads
  * <= 128, B <= 4096;
- * query tiles (rows / (2 * (128 / group)) + B) x KV heads x 128-token tiles of
- * max_blocks_per_seq below 2^30.
+ * (rows / (2 * (128 / group)) + B) x KV heads x (max_blocks_per_seq / 5 + 3)
+ * below 2^30 (the work is counted in tiles of 80 tokens).
  * Reads only the blocks that hold a token that some row sees, as
  * tts_window_decode_attn; tokens that a row does not see do not reach it, and a
  * value that is not finite makes that dimension of the rows that see it so.
