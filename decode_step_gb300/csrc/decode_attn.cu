@@ -41,7 +41,7 @@
 // context.  Nothing else of the schedule changes; without a window the kernels
 // are compiled as they were.  Rows' masks are made only in tiles at an edge (made in
 // every tile they cost FP8 with 5 rows a stream 51.8 us, so 45.7).  64 streams, window
-// 1,500: 69.0 us, 5.7 TB/s, as without a window over as many tokens.
+// 1,500: 70.6 us, 5.6 TB/s, as without a window over as many tokens.
 #include <cudaTypedefs.h>
 
 #include <mutex>

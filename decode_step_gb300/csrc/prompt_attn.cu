@@ -22,7 +22,7 @@
 // half (a commit or a wait takes its warp about 190 cycles: one issuer was the
 // bound); a producer of keys and queries and one of values (TMA through the table, a
 // box of 16 tokens x 64 dimensions of keys, 16 x 128 of values; FP8: bulk copies of
-// codes and scales).  bf16: two warps that look at the values of the tiles that not
+// codes and scales).  bf16: two guards, warps that look at the values of the tiles that not
 // every row sees whole (below).  FP8: four warps that turn codes into f16, which is
 // exact, where the MMAs want them; the keys' scales go to the scores, the values' to
 // the weights.
@@ -40,14 +40,14 @@
 // us, 1.30 PFLOP/s, 0.68 of a dense product's measured rate; the softmax warps take
 // about 2,000 cycles a tile for both halves, the MMAs 1,435 of them (the first, with
 // both operands in shared memory, 417 a half, bound by their 128 bytes a cycle; the
-// second 320).  61 rows after 65,472: 58 us, 4.6 TB/s.  333 rows: 18 us, latency.
+// second 320).  61 rows after 65,472: 59 us, 4.6 TB/s.  333 rows: 18 us, latency.
 // FP8: instruction issue of the conversions and scales, twice the bf16 time.  A CTA
 // does not have 16 softmax warps (two threads a row: 386 us, spills and twice the
 // reads of scores).
 //
 // Values that are not finite.  A weight of zero times NaN is NaN, so a token that
 // a row does not see must not meet it in the matrix product.  Tiles that every
-// row sees need no care.  In the others the checkers (FP8: the converters) clear such
+// row sees need no care.  In the others the guards (FP8: the converters) clear such
 // values in shared memory, and the rows that do see them get them at the end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -81,8 +81,8 @@ constexpr float kFp8Log2 = 8.0f;
 // Tensor memory: a half's S, its P (two weights a column), and both halves' O
 constexpr int kS = 0, kP = kTile, kHalf = 128, kO = 256;
 static_assert(kP + kTile / 2 <= kHalf);
-// Two softmax warpgroups; two issuers, two checkers, two producers; FP8: four
-// converters instead of the checkers
+// Two softmax warpgroups; two issuers, two guards, two producers; FP8: four
+// converters instead of the guards
 __host__ __device__ constexpr int prompt_threads(bool fp8) { return fp8 ? 512 : 448; }
 constexpr int kMostThreads = 512;
 constexpr int kFewTiles = 128;              // query tiles that one warp looks at
@@ -595,7 +595,7 @@ __device__ __forceinline__ uint32_t bits_before(int t, int base) {
 }
 
 // Values of this row's tokens that are not finite, of 32 dimensions from d on,
-// added up in o (rare): those of the tiles that the checkers cleared.
+// added up in o (rare): those of the tiles that the guards cleared.
 template <bool kFp8>
 __device__ __noinline__ void find_odd(const PromptArgs &a, const PartInfo &part, int step, int j, int limit, int d, float *o) {
     const int first_limit = part.ctx - part.n + part.r0 + 1;
@@ -1117,7 +1117,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                 }
             } else {
-                // ---- checkers: values that are not finite leave the tiles that some
+                // ---- guards: values that are not finite leave the tiles that some
                 // row does not see whole.  (They keep step with every tile: a barrier's
                 // parity tells one use of a slot from the next, not from the one after.)
                 Place<kSlots> values;
@@ -1442,7 +1442,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 // Segments of more than kJoinHere parts: one CTA's threads would read them at a
 // few bytes a cycle (61 rows of 8 KV heads in 19 parts of 62 KB each: 54 us), so
 // a second kernel spreads the work over every SM, 128 rows of 8 dimensions an
-// item, four threads a row (that call whole: 95 us, with this kernel 58).  It runs
+// item, four threads a row (that call whole: 95 us, with this kernel 59).  It runs
 // wherever a table may hold more than kSoloTiles tiles, and finds that there is
 // nothing to do by looking at one word a CTA and half.
 constexpr int kJoinThreads = 512, kJoinItems = kDim / 8, kJoinGroups = kJoinThreads / kRows;
