@@ -242,6 +242,38 @@ def test_a_streams_bits_do_not_depend_on_its_neighbours(dtype):
     assert torch.equal(first, run(s))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("value", [0.25, float("nan")])
+def test_blocks_past_32_bit_offsets(dtype, value):
+    """The last of 65,600 blocks (33 KB or 32 KB of 8 heads) lie past 2^31 bytes."""
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    s = pr.make([70, 3], [200, 90], 16, 8, dtype, 60, 4, seed=41)
+    if dtype == "bf16":
+        s["pools"][1][:, 3, 5, 17] = value  # (values that are not finite are looked up by address)
+    want = run(s)
+    q = s["q"][:4].cuda().view(2, 2, 16, 128)
+    ws = torch.zeros(bd.tts_decode_attn_workspace_size(2, 2, 16, 8, 128, 400), dtype=torch.uint8, device="cuda")
+    outs = []
+    for far in (False, True):
+        if far:
+            small = s["pools"][0].shape[0]
+            big = []
+            for p in s["pools"]:
+                big.append(p if p is None else torch.zeros(65600, *p.shape[1:], dtype=p.dtype, device="cuda"))
+                if p is not None:
+                    big[-1][65600 - small:] = p.cuda()
+            s["pools"] = tuple(big)
+            s["table"] = torch.where(s["table"] >= 0, s["table"] + 65600 - small, s["table"])
+        cache, table, lens, _ = upload(s)
+        out = torch.empty_like(q)
+        bd.tts_window_decode_attn(cache, table, lens, 400, q, out, ws, s["scale"], 60, 4, causal=True)
+        torch.cuda.synchronize()
+        outs.append(out)
+    same = lambda x, y: torch.equal(x.view(torch.int16), y.view(torch.int16))
+    assert same(run(s), want) and same(*outs)
+
+
 def test_many_streams():
     new = [(7 * i) % 5 for i in range(700)]
     good(pr.make(new, [(13 * i) % 90 for i in range(700)], 2, 1, "bf16", seed=12))
