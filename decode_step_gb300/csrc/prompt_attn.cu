@@ -271,7 +271,9 @@ struct __align__(8) TileInfo {
     int flags, t0;  // bits 0-4: blocks in the pool; then its part's note, its slot and its scales' stage; first token
 };
 constexpr int kAllBlocks = (1 << kBlocks) - 1, kPair = 0x80, kMasked = 0x100, kFresh = 0x200, kLast = 0x400, kEnd = 0x800, kPartShift = 12, kSlotShift = 16, kStageShift = 18;
-constexpr int kInfos = 8;  // (the producers are at most six tiles ahead)
+// (The producers are at most six tiles ahead of a half that works, and of one that
+// has no part in a tile but is still at the end of an earlier part.)
+constexpr int kInfos = 8;
 constexpr int kLookups = 6;  // tiles whose blocks a warp looks up at once
 static_assert(kLookups * kBlocks <= 32);
 
@@ -902,7 +904,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 const int s = warp - 9;
                 const uint32_t leader = elect_leader();
                 Place<kSlots> keys, values;  // of the next scores, and outputs
-                uint32_t uses = 0, outs = 0, parts = 0, both = 0, behind = 0;
+                uint32_t uses = 0, outs = 0, parts = 0, left_parts = 0, both = 0, behind = 0;
                 bool go = true;
                 const uint32_t d_s = tmem + s * kHalf + kS, d_p = tmem + s * kHalf + kP, d_o = tmem + kO + s * kDim;
                 uint64_t queries = 0;
@@ -965,9 +967,13 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             x.none(1);
                             x.none(2);
                             if constexpr (!kFp8) x.set(1, &sh.checked[values.slot], values.phase);
-                            if (work && fresh && outs) x.set(2, &sh.o_empty[s], (parts - 1) & 1);
+                            // (also where the half has no part in this one, before it gives a slot back:
+                            // its softmax warps read the notes on the part that they are at the end of,
+                            // and nothing else holds back the producers, which write over them)
+                            if (fresh && left_parts != parts) x.set(2, &sh.o_empty[s], (parts - 1) & 1);
                             go = x.spin(a.wait_limit);
                             if (!go) break;
+                            if (fresh) left_parts = parts;
                             if (work) {
                                 WarpWaits<1> y;
                                 y.set(0, &sh.p_full[s], outs++ & 1);
@@ -1319,6 +1325,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 tc_fence_after();
                 mbar_arrive_by(first_thread, smem_addr(&sh.v_empty[held]));
                 held = -1;
+                // (the note is read until o_empty says that the rows have left the part, not after)
                 const PartInfo &p = sh.parts[(flags >> kPartShift) % kInfos];
                 const bool turns = p.mode == kTurns;
                 const int r = p.r0 + (s == 1 && !turns ? a.tokens : 0) + token;  // row in the stream
@@ -1346,6 +1353,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 // (a part in turns is of a segment of several CTAs: their rule sees to that)
                 const bool begins = static_cast<int>(blockIdx.x) == first, alone = turns && p.tiles == 1;
                 float *mine = part_slot(a.part, blockIdx.x, begins, s);
+                const int4 job = make_int4(min(p.n - (r - token), a.tokens) * a.group, p.first + r, p.g, turns ? -count : count);
 #pragma unroll 1
                 for (int c = 0; c < kDim; c += 32) {
                     float f[32];
@@ -1370,8 +1378,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.o_empty[s]));
                 if (count > kJoinHere) {
-                    if (begins && row == 0 && (s == 0 || !turns))
-                        sh.jobs[s] = make_int4(min(p.n - (r - token), a.tokens) * a.group, p.first + r, p.g, turns ? -count : count);
+                    if (begins && row == 0 && (s == 0 || !turns)) sh.jobs[s] = job;
                     continue;
                 }
                 if (lane == 0) mbar_arrive(smem_addr(&sh.stored[s]));

@@ -1,0 +1,54 @@
+"""tts_prompt_attn: values that are not finite in the places where the kernel
+looks them up by a part's note, in tiles beside blocks outside the pool, and in
+parts whose rows have no weights."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import paged_ref as pr
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from decode_step_gb300 import binding as bd
+
+NAN = float("nan")
+
+
+def run(s, err=None):
+    pools = tuple(None if p is None else p.cuda() for p in s["pools"])
+    q = s["q"].cuda()
+    out = torch.full_like(q, 7.0)
+    ws = torch.zeros(bd.tts_prompt_attn_workspace_size(len(s["new"]), s["T"], s["Hq"], s["Hkv"], s["D"]), dtype=torch.uint8,
+                     device="cuda")
+    bd.tts_prompt_attn(bd.KVCache(*pools), s["table"].cuda(), s["ctx_lens"].cuda(), s["row_start"].cuda(), q, out, ws,
+                       s["scale"], s["window"], s["sinks"], err=err)
+    torch.cuda.synchronize()
+    return out
+
+
+def put(s, b, t, g, d, value):
+    """Value (token t, KV head g, dimension d) of stream b; NaN in an FP8 cache."""
+    block, slot = int(s["table"][b, t // 16]), t % 16
+    if s["dtype"] == "fp8":
+        assert value != value
+        s["pools"][0][block, g, 2048 + 16 * d + 4 * (slot % 8 // 2) + slot % 2 + 2 * (slot // 8)] = 0x7F
+    else:
+        s["pools"][1][block, g, slot, d] = value
+    s["v_val"][block, g, slot, d] = value
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_a_value_looked_up_while_short_segments_follow(dtype):
+    """A stream with rows for both halves of a query tile, whose last rows see values that are
+    not finite in the last KV head; the CTA goes on with some twenty segments of one tile and one
+    half, whose notes must not take the place of the note that the other half still reads."""
+    s = pr.make([100] + [1 + i % 30 for i in range(600)], [0] + [i % 20 for i in range(600)], 16, 8, dtype, seed=51)
+    for d in (5, 40, 70, 127):
+        put(s, 0, 98, 7, d, NAN)
+    put(s, 0, 66, 7, 33, NAN)
+    ref, tol = pr.attend_all(s)
+    assert int(torch.isnan(ref).sum()) == 2 * (2 * 4 + 34)
+    for _ in range(5):
+        pr.check(run(s), ref, tol)
