@@ -1075,13 +1075,17 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         } else {
                             const int k = k0 + j, t0 = (k < head ? k : k + skip) * kTile;
                             const int valid = *reinterpret_cast<volatile int *>(&sh.v_valid[tile % kInfos]);
-                            const bool clean = valid != kAllBlocks || tile_edge(a, t0, first, high);
+                            // (what the rows see alike meets them in the product: only tiles at an edge are
+                            // cleared, and stale codes of blocks that are not in the pool)
+                            const bool edge = tile_edge(a, t0, first, high);
                             bool odd = false;
                             // a dimension's 16 codes of a block: word i has slots 2i, 2i + 1, 2i + 8, 2i + 9
                             const uint32_t in = codes + (me * 32 + lane) * 16, at = out + (me * 32 + lane) * 16;
-                            if (clean) {
+                            if (edge || valid != kAllBlocks) {
 #pragma unroll 1
                                 for (int e = 0; e < kRawBytes; e += 1024) {
+                                    const bool held = (valid >> (e / 2048)) & 1;
+                                    if (held && !edge) continue;
                                     const uint4 was = lds128(in + e);
                                     uint4 x = was;
                                     drop_odd(x.x);
@@ -1090,8 +1094,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                     drop_odd(x.w);
                                     if (!((was.x ^ x.x) | (was.y ^ x.y) | (was.z ^ x.z) | (was.w ^ x.w))) continue;
                                     sts128(in + e, x.x, x.y, x.z, x.w);
-                                    // (stale codes of a block that is not in the pool count for nothing)
-                                    if (!((valid >> (e / 2048)) & 1)) continue;
+                                    if (!held) continue;
 #pragma unroll 1
                                     for (int i = 0; i < 16; ++i) {
                                         const uint32_t w = i / 4 == 0 ? was.x ^ x.x : i / 4 == 1 ? was.y ^ x.y : i / 4 == 2 ? was.z ^ x.z : was.w ^ x.w;

@@ -11,6 +11,7 @@ import paged_ref as pr
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
+    from decode_step_gb300 import _lib
     from decode_step_gb300 import binding as bd
 
 NAN = float("nan")
@@ -52,3 +53,19 @@ def test_a_value_looked_up_while_short_segments_follow(dtype):
     assert int(torch.isnan(ref).sum()) == 2 * (2 * 4 + 34)
     for _ in range(5):
         pr.check(run(s), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_a_value_beside_a_block_outside_the_pool(dtype):
+    """In a tile that every row sees whole but for one block: the value reaches every row. In the
+    bad block's place nothing does, whatever an earlier tile left there."""
+    s = pr.make([40], [400], 4, 2, dtype, seed=52)
+    s["table"][0, 7] = s["k_pool"].shape[0]        # tokens 112..127, in the tile of 80..159
+    s["table"][0, 20] = -5                         # tokens 320..335, in the tile of 320..399
+    put(s, 0, 100, 1, 5, NAN)
+    put(s, 0, 390, 0, 77, NAN)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ref, tol = pr.attend_all(s)
+    assert int(torch.isnan(ref).sum()) == 2 * 2 * 40
+    pr.check(run(s, err), ref, tol)
+    assert int(err.item()) == _lib.ERRBIT_BLOCK_ID
