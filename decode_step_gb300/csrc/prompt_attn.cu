@@ -93,6 +93,9 @@ constexpr int kMinTiles = 6;                // tiles a CTA at least, where there
 constexpr float kLog2e = 1.4426950408889634f;
 // Running maximum before any token (log2 units): no finite score is below it.
 constexpr float kNoScore = -FLT_MAX;
+// In the place of a part's maximum: there is no such part.  (One without weights, all
+// its scores -inf, has kNoScore, and may have values that are not finite.)
+constexpr float kNoPart = -INFINITY;
 // Scores may pass it by this much before it moves (log2 units); in FP8 weights stay
 // at 1 at most, so that with a scale below 256 they are in f16's range.
 __host__ __device__ constexpr float prompt_slack(bool fp8) { return fp8 ? 0.0f : 8.0f; }
@@ -1373,7 +1376,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     mine[kRows * kDim + row] = m;
                     mine[kRows * kDim + kRows + row] = l;
                     if (alone) {  // no tile was half 1's
-                        mine[kPartFloats + kRows * kDim + row] = kNoScore;
+                        mine[kPartFloats + kRows * kDim + row] = kNoPart;
                         mine[kPartFloats + kRows * kDim + kRows + row] = 0.0f;
                     }
                 }
@@ -1420,7 +1423,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         const float *q = segment_part(a.part, first, i, turns, s);
                         const float mq = __ldcg(q + kRows * kDim + row);
                         const float f = hw_ex2(mq - best);
-                        if (turns && mq == kNoScore && __ldcg(q + kRows * kDim + kRows + row) == 0.0f) continue;  // (nothing there)
+                        if (mq == kNoPart) continue;  // (o was not written)
                         float4 x[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[e] = __ldcg(reinterpret_cast<const float4 *>(q) + (d / 4 + e) * kRows + row);
@@ -1497,7 +1500,7 @@ prompt_join_kernel(float *parts, const int4 *jobs, int ctas, __nv_bfloat16 *out,
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int i = i0 + u * kJoinGroups;
-                    mq[u] = kNoScore;
+                    mq[u] = kNoPart;
                     lq[u] = 0.0f;
                     x[u][0] = x[u][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     if (i >= count) continue;
@@ -1517,9 +1520,9 @@ prompt_join_kernel(float *parts, const int4 *jobs, int ctas, __nv_bfloat16 *out,
                 for (int i = 0; i < 8; ++i) o[i] *= f0;
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
-                    // (a part without a tile of this half has no weights, and nothing in o)
+                    // (where a half had no tile o was not written)
                     const float f = hw_ex2(mq[u] - now);
-                    const bool none = mq[u] == kNoScore && lq[u] == 0.0f;
+                    const bool none = mq[u] == kNoPart;
                     const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
                     l = fmaf(f, lq[u], l);
 #pragma unroll

@@ -69,3 +69,20 @@ def test_a_value_beside_a_block_outside_the_pool(dtype):
     assert int(torch.isnan(ref).sum()) == 2 * 2 * 40
     pr.check(run(s, err), ref, tol)
     assert int(err.item()) == _lib.ERRBIT_BLOCK_ID
+
+
+@pytest.mark.parametrize("new", [5, 100])
+def test_a_value_in_a_part_without_weights(new):
+    """Keys of -inf in the last 1,500 tokens: the last CTAs' parts of a segment have no weights
+    (one half's rows in turns, and both halves'), and a value in them that is no number still
+    reaches the rows that see it."""
+    s = pr.make([new], [9000], 4, 2, "bf16", seed=53)
+    s["q"] = s["q"].abs() + 0.1
+    for t in range(9000 + new - 1500, 9000 + new):
+        s["k_pool"][int(s["table"][0, t // 16]), :, t % 16] = float("-inf")
+    pr.finish(s)
+    put(s, 0, 9000 + new - 2, 1, 5, NAN)
+    put(s, 0, 9000 + new - 1, 0, 99, NAN)
+    ref, tol = pr.attend_all(s)
+    assert int(torch.isnan(ref).sum()) == 2 * 2 + 2 * 1
+    pr.check(run(s), ref, tol)
