@@ -320,6 +320,8 @@ __device__ void finish_split_segment(const AttnArgs &a, int seg, int s0, int s1,
 
 // ---------------------------------------------------------------- fp32 kernel
 
+constexpr float kHidden = -1.0f;  // in the place of a weight
+
 template <int NR>
 struct SimtSmem {
     static constexpr int stage_bytes = 2 * kTileBytes + NR * kRowBytes;  // K, V, query rows
@@ -572,7 +574,8 @@ decode_attn_simt_kernel(const AttnArgs a) {
             float alpha[HALF], other[HALF];
 #pragma unroll
             for (int k = 0; k < HALF; ++k) {
-                const float s = sees(tpos, lim[k]) ? acc[k] : -INFINITY;
+                const bool seen = sees(tpos, lim[k]);
+                const float s = seen ? acc[k] : -INFINITY;
                 float mx = s;
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
                 mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 4));
@@ -583,7 +586,9 @@ decode_attn_simt_kernel(const AttnArgs a) {
                 const float pk = exp2f(s - m_new);
                 l_run[k] = l_run[k] * alpha[k] + pk;
                 m_run[k] = m_new;
-                pbuf[my_tok * NR + (lane & 1) * HALF + k] = pk;
+                // (kWindow: a mark for tokens that the row does not see, whose values have no
+                // part in it, while those of seen ones do, whatever their weight)
+                pbuf[my_tok * NR + (lane & 1) * HALF + k] = kWindow && !seen ? kHidden : pk;
                 other[k] = __shfl_xor_sync(kFull, alpha[k], 1);
             }
             __syncwarp();
@@ -606,9 +611,8 @@ decode_attn_simt_kernel(const AttnArgs a) {
                 for (int r = 0; r < NR; ++r) {
                     const float w = pr[r];
                     if constexpr (kWindow) {
-                        // (a token that the row does not see may hold anything)
 #pragma unroll
-                        for (int e = 0; e < EPC; ++e) o[r][e] = w == 0.0f ? o[r][e] : fmaf(w, vf[e], o[r][e]);
+                        for (int e = 0; e < EPC; ++e) o[r][e] = w == kHidden ? o[r][e] : fmaf(w, vf[e], o[r][e]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < EPC; ++e) o[r][e] = fmaf(w, vf[e], o[r][e]);
