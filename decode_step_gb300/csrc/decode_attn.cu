@@ -44,6 +44,7 @@
 // 1,500: 70.6 us, 5.6 TB/s, as without a window over as many tokens.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <mutex>
 #include <new>
 
@@ -59,7 +60,8 @@ constexpr int kTileBytes = 4096;   // one (block, KV head) tile of K or V: 16 to
 constexpr int kRowBytes = 256;     // one token's key (or value) row
 constexpr int kMaxStreams = 4096;  // streams per call (shared-memory prefix table)
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNegBig = -1e30f;  // finite "minus infinity" for running maxima
+// Running maximum before any token (log2 units): no finite score is below it.
+constexpr float kNoScore = -FLT_MAX;
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 struct AttnArgs {
@@ -237,7 +239,7 @@ __device__ void merge_split_segment(const AttnArgs &a, int b, int g, int n_rows,
             rr[h] = has[h] ? u / UPR : 0;
             cc[h] = has[h] ? u - rr[h] * UPR : 0;
         }
-        float M[2] = {kNegBig, kNegBig}, L[2] = {0.0f, 0.0f};
+        float M[2] = {kNoScore, kNoScore}, L[2] = {0.0f, 0.0f};
         float4 O[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
         for (int c0 = 0; c0 < nc; c0 += CB) {
             float mi[2][CB], li[2][CB];
@@ -253,7 +255,7 @@ __device__ void merge_split_segment(const AttnArgs &a, int b, int g, int n_rows,
                         li[h][k] = __ldcg(pk + ML + NRS + rr[h]);
                         oi[h][k] = __ldcg(reinterpret_cast<const float4 *>(pk + static_cast<size_t>(rr[h]) * D) + cc[h]);
                     } else {
-                        mi[h][k] = kNegBig;
+                        mi[h][k] = kNoScore;
                         li[h][k] = 0.0f;
                         oi[h][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     }
@@ -525,7 +527,7 @@ decode_attn_simt_kernel(const AttnArgs a) {
             for (int k = 0; k < HALF; ++k) {
                 const int r = (lane & 1) * HALF + k;
                 lim[k] = r < n_rows ? (a.causal ? seg_L - a.q_len + r / a.group + 1 : seg_L) : 0;
-                m_run[k] = kNegBig;
+                m_run[k] = kNoScore;
                 l_run[k] = 0.0f;
             }
             const uint32_t qs = ks + 2 * kTileBytes;
@@ -969,7 +971,7 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     int seg_id = -1, seg_b = 0, seg_g = 0, seg_L = 0, seg_skip = 0, s0 = 0, s1 = 0;
     int limA = 0, limB = 0;                 // visible-token limits of rows fg and fg + 8
     uint32_t qa[8][4];                      // Q A-fragments, 8 k-steps of 16 dims
-    float mA = kNegBig, mB = kNegBig, lA = 0.0f, lB = 0.0f;
+    float mA = kNoScore, mB = kNoScore, lA = 0.0f, lB = 0.0f;
     float o[16][4];                         // O accumulators, 16 n-tiles of 8 dims
 
     auto flush = [&]() {
@@ -1065,7 +1067,7 @@ decode_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             const int rA = fg, rB = fg + 8;
             limA = rA < n_rows ? (a.causal ? seg_L - a.q_len + rA / a.group + 1 : seg_L) : 0;
             limB = rB < n_rows ? (a.causal ? seg_L - a.q_len + rB / a.group + 1 : seg_L) : 0;
-            mA = mB = kNegBig;
+            mA = mB = kNoScore;
             lA = lB = 0.0f;
             const uint32_t qs = kt + kQOff;
 #pragma unroll

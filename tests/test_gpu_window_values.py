@@ -66,3 +66,20 @@ def test_values_that_are_not_finite_show_whatever_their_weight(dtype, value, low
         # (bf16: values of tiles at an edge are given to their rows as they are)
         ref, got, tol = (x.masked_fill(bad, 0.0) for x in (ref, got, tol))
         pr.check(got, ref, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "f32"])
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("size", [1e27, 1e30, 1e34])
+def test_scores_far_below_zero_have_weights(dtype, window, size):
+    """Keys that point away from the queries, in steps of which the first takes it all: scores of
+    -1e28 to -2e35, in one part and in parts of several warps.  Without a window the plain decode."""
+    s = pr.make([2, 2], [3, 5000], 4, 2, dtype, window, 4 if window else 0, True, seed=61)
+    s["q"] = torch.ones_like(s["q"])
+    steps = torch.where(torch.rand(s["k_pool"].shape[:3], generator=torch.Generator().manual_seed(62)) < 0.25, 1.0, 2.0)
+    k = (-size * steps)[..., None].expand(s["k_pool"].shape)
+    s["k_pool"] = torch.where(torch.isfinite(s["k_pool"]), k.to(s["k_pool"].dtype), s["k_pool"])
+    pr.finish(s)
+    ref, tol = pr.attend_all(s)
+    assert torch.isfinite(ref).all() and bool((ref.abs().amax(-1) > 0.01).all())
+    pr.check(attend(s, 2, window), ref, tol)
