@@ -93,6 +93,9 @@ constexpr int kMinTiles = 6;                // tiles a CTA at least, where there
 constexpr float kLog2e = 1.4426950408889634f;
 // Running maximum before any token (log2 units): no finite score is below it.
 constexpr float kNoScore = -FLT_MAX;
+// Maxima from which on scores are scaled before the maximum is taken off: half a
+// step of fp32 is 2^-4 here.
+constexpr float kLargeScore = 1 << 20;
 // In the place of a part's maximum: there is no such part.  (One without weights, all
 // its scores -inf, has kNoScore, and may have values that are not finite.)
 constexpr float kNoPart = -INFINITY;
@@ -1272,8 +1275,21 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             tmem_st16(to + c, o);
                         }
                 }
+                // An exponent is scale * score - m by one fused operation, off by what m was
+                // rounded by: one factor for all of the row's weights, which the end divides
+                // out.  Where m is so large that the factor would leave the range the score
+                // is scaled first and rounded as m was (a row at a time: other rows keep
+                // their bits).
+                float scale = a.scale_log2;
+                if (__any_sync(kFull, fabsf(m) > kLargeScore && fabsf(m) < FLT_MAX)) {  // rare
+                    const bool large = fabsf(m) > kLargeScore && fabsf(m) < FLT_MAX;
+                    const float by = large ? scale : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < kTile; i += 2) times2(x[i], x[i + 1], by, by);
+                    if (large) scale = 1.0f;
+                }
                 uint64_t sum[2] = {0, 0};
-                const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), minus2 = kFp8 ? pack2(kFp8Log2 - m, kFp8Log2 - m) : pack2(-m, -m);
+                const uint64_t scale2 = pack2(scale, scale), minus2 = kFp8 ? pack2(kFp8Log2 - m, kFp8Log2 - m) : pack2(-m, -m);
                 uint32_t weights[kTile / 2];
 #pragma unroll
                 for (int i = 0; i < kTile / 2; ++i) {

@@ -86,3 +86,23 @@ def test_a_value_in_a_part_without_weights(new):
     ref, tol = pr.attend_all(s)
     assert int(torch.isnan(ref).sum()) == 2 * 2 + 2 * 1
     pr.check(run(s), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("new", [3, 100])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("size", [1e5, 1e8, 1e11, 1e30, 1e34])
+def test_scores_of_any_size(dtype, new, sign, size):
+    """Keys in steps of which one takes it all, scores from 1e6 to 2e35 on either side of zero; the
+    first tokens see all of one step, so that the maximum moves on the way."""
+    s = pr.make([new, 7], [5000, 0], 4, 2, dtype, seed=61)
+    s["q"] = torch.ones_like(s["q"])
+    far = torch.rand(s["k_pool"].shape[:3], generator=torch.Generator().manual_seed(62)) < 0.25
+    for t in range(700):
+        far[int(s["table"][0, t // 16]), :, t % 16] = sign < 0
+    k = (sign * size * torch.where(far, 2.0, 1.0))[..., None].expand(s["k_pool"].shape)
+    s["k_pool"] = torch.where(torch.isfinite(s["k_pool"]), k.to(s["k_pool"].dtype), s["k_pool"])
+    pr.finish(s)
+    ref, tol = pr.attend_all(s)
+    assert torch.isfinite(ref).all() and bool((ref.abs().amax(-1) > 0.01).all())
+    pr.check(run(s), ref, tol)
