@@ -32,6 +32,9 @@
 namespace tts {
 namespace {
 
+// (Neither kernel reads through the read-only path, nor promises the compiler that it
+// may: with programmatic launches they start while the kernel before still runs, which
+// may write the table, the contexts and the new rows.)
 constexpr int kVecsAhead = 4;  // 16-byte words per thread loaded before the position is known
 
 // The packed rows' streams (kPacked; else NULL and 0).
@@ -58,10 +61,9 @@ __device__ __forceinline__ bool locate(const PackedRows &packed, int q_len, int 
 
 template <bool kPacked>
 __global__ void __launch_bounds__(128)
-kv_append_kernel(const int32_t *__restrict__ table, int max_blocks,
-                 const int32_t *__restrict__ ctx_before, const PackedRows packed, int q_len, int Hkv, int num_blocks,
-                 int row_vecs, const uint4 *__restrict__ k_new, const uint4 *__restrict__ v_new,
-                 uint4 *__restrict__ k_pool, uint4 *__restrict__ v_pool, int32_t *err, int wait_last) {
+kv_append_kernel(const int32_t *table, int max_blocks,
+                 const int32_t *ctx_before, const PackedRows packed, int q_len, int Hkv, int num_blocks,
+                 int row_vecs, const uint4 *k_new, const uint4 *v_new, uint4 *k_pool, uint4 *v_pool, int32_t *err, int wait_last) {
     // wait_last: the inputs are not written by the kernel before (they come
     // from pinned host memory); the append runs at once and waits for that
     // kernel only before it ends, so the kernels after it still find both done
@@ -69,7 +71,7 @@ kv_append_kernel(const int32_t *__restrict__ table, int max_blocks,
     pdl_allow_dependents();
     const int per_tensor = Hkv * row_vecs;
     const size_t src0 = static_cast<size_t>(blockIdx.x) * per_tensor;
-    auto load = [&](int i) { return i < per_tensor ? __ldg(k_new + src0 + i) : __ldg(v_new + src0 + i - per_tensor); };
+    auto load = [&](int i) { return i < per_tensor ? k_new[src0 + i] : v_new[src0 + i - per_tensor]; };
     // the rows do not depend on the position: their first words are in flight
     // while the position and the block are read
     uint4 ahead[kVecsAhead];
@@ -168,11 +170,11 @@ constexpr int kRowsAhead = 4;  // rows per warp loaded before the token's positi
 // through shared memory.
 template <bool kFp8, bool kRope, bool kPacked>
 __global__ void __launch_bounds__(kRowThreads)
-kv_append_rows_kernel(const int32_t *__restrict__ table, int max_blocks, const int32_t *__restrict__ ctx_before,
+kv_append_rows_kernel(const int32_t *table, int max_blocks, const int32_t *ctx_before,
                       const PackedRows packed, int q_len, int Hq, int Hkv, int num_blocks, const RopeFreqs freqs,
                       const __nv_bfloat16 *q, __nv_bfloat16 *q_out,
-                      const __nv_bfloat16 *__restrict__ k_new, const __nv_bfloat16 *__restrict__ v_new,
-                      uint8_t *__restrict__ k_pool, uint8_t *__restrict__ v_pool, int32_t *err) {
+                      const __nv_bfloat16 *k_new, const __nv_bfloat16 *v_new, uint8_t *k_pool, uint8_t *v_pool,
+                      int32_t *err) {
     __shared__ float2 cs[kFp8D / 2];
     __shared__ int where[2];  // block (-1: skip the token), slot
     pdl_wait_prerequisites();
