@@ -90,6 +90,14 @@ class _CallsInOrder:
         self._streams[kind] = now
 
 
+def _zero(buffer: torch.Tensor, stream) -> torch.Tensor:
+    """Zeros on `stream` in a buffer of rotated queries: the append writes no row for a
+    token that it skips, and what such a row is answered with must not be an
+    earlier call's query."""
+    with torch.cuda.stream(stream):
+        return buffer.zero_()
+
+
 class LatentStep(_CallsInOrder):
     """A batch's steps over a latent cache, for fixed shapes: `prompt` appends
     whole prompts and attends over them, calling the object appends q_len
@@ -196,7 +204,8 @@ class WindowStep(_CallsInOrder):
     unrotated where rope_base is not 0; the rotated queries go to buffers of the
     object (`q` is the latest call's).  `fork` makes streams continuations of
     others, `compact` moves blocks as BlockPool.compact says, and `gone` tells which of a
-    stream's blocks can go back to the pool.  The object owns the workspaces and
+    stream's blocks can go back to the pool.  Tokens that the append skips (bits of
+    `err`) have queries of zeros where rope_base is not 0.  The object owns the workspaces and
     outputs (`out` [B][q_len][Hq][head_dim], `ids` [B * q_len]).
 
     Prompts may run on one CUDA stream while steps of other streams' blocks run
@@ -239,8 +248,8 @@ class WindowStep(_CallsInOrder):
         if self.rope_base == 0.0:
             bd.tts_kv_append_packed(self.cache, block_table, ctx_before, row_start, k_new, v_new, err=self.err, stream=stream)
             return q
-        bd.tts_kv_append_packed(self.cache, block_table, ctx_before, row_start, k_new, v_new, q, buffer, self.rope_base,
-                                err=self.err, stream=stream)
+        bd.tts_kv_append_packed(self.cache, block_table, ctx_before, row_start, k_new, v_new, q, _zero(buffer, stream),
+                                self.rope_base, err=self.err, stream=stream)
         return buffer
 
     def prompt(self, block_table, ctx_before, ctx_lens, row_start, q, k_new, v_new, out=None, stream=None) -> torch.Tensor:
@@ -256,9 +265,14 @@ class WindowStep(_CallsInOrder):
             with torch.cuda.stream(stream):
                 out = torch.empty((T, self.Hq, self.cache.head_dim), dtype=self.cache.dtype, device=self.out.device)
         self._follow("prompt", stream)
-        q = self.q = self._append(block_table, ctx_before, row_start, q, k_new, v_new, self.prompt_q[:T], stream)
-        bd.tts_prompt_attn(self.cache, block_table, ctx_lens, row_start, q, out, self.prompt_ws, self.scale, self.window,
-                           self.sinks, err=self.err, stream=stream)
+        # the kernels start while the ones before them finish, and wait for what those write
+        flags = bd.tts_set_launch_flags(_lib.LAUNCH_PROGRAMMATIC)
+        try:
+            q = self.q = self._append(block_table, ctx_before, row_start, q, k_new, v_new, self.prompt_q[:T], stream)
+            bd.tts_prompt_attn(self.cache, block_table, ctx_lens, row_start, q, out, self.prompt_ws, self.scale, self.window,
+                               self.sinks, err=self.err, stream=stream)
+        finally:
+            bd.tts_set_launch_flags(flags)
         return out
 
     def __call__(self, block_table, ctx_before, ctx_lens, q, k_new, v_new, seed=None, step=None, eos_allowed=None,
@@ -270,11 +284,12 @@ class WindowStep(_CallsInOrder):
         if q.shape != shape:
             raise ValueError(f"q must have shape {shape}, got {tuple(q.shape)}")
         self._follow("step", stream)
-        rows = self.q = self._append(block_table, ctx_before, self._rows, q.view(self.R, self.Hq, D),
-                                     k_new.view(self.R, Hkv, D), v_new.view(self.R, Hkv, D), self.step_q, stream)
-        # the later kernels start while the ones before them finish
+        # the kernels start while the ones before them finish (the attention, which reads
+        # contexts and tables before it waits, once the append has waited)
         flags = bd.tts_set_launch_flags(_lib.LAUNCH_PROGRAMMATIC)
         try:
+            rows = self.q = self._append(block_table, ctx_before, self._rows, q.view(self.R, self.Hq, D),
+                                         k_new.view(self.R, Hkv, D), v_new.view(self.R, Hkv, D), self.step_q, stream)
             args = (self.cache, block_table, ctx_lens, self.max_ctx_len, rows.view(shape), self.out, self.ws, self.scale)
             if self.window:
                 bd.tts_window_decode_attn(*args, self.window, self.sinks, causal=self.causal, err=self.err, stream=stream)

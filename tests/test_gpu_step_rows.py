@@ -1,0 +1,62 @@
+"""Steps and prompts with tokens that the append skips, and without any rows."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from decode_step_gb300 import _lib
+    from decode_step_gb300 import binding as bd
+    from decode_step_gb300.step import LatentStep, WindowStep
+
+HQ, HKV, D, V = 4, 2, 128, 300
+
+
+def rand(g, *shape):
+    return torch.randn(*shape, generator=g).to(torch.bfloat16).cuda()
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def window_step(window=40, rope=10000.0, dtype="bf16"):
+    g = torch.Generator().manual_seed(1)
+    pools = [rand(g, 20, HKV, 16, D) for _ in range(2)]
+    W = (torch.randn(V, HQ * D, generator=g) * 0.05).to(torch.bfloat16).cuda()
+    return WindowStep(bd.KVCache(*pools), W, HQ, 2, 160, window, 3, rope_base=rope, prompt_rows=60), g
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_window_step_of_skipped_tokens_knows_no_earlier_call(window):
+    """Stream 1's block is outside the pool in the second call: its rows are answered alike
+    whatever the first call's queries were, and its tokens' queries are zeros."""
+    for prompt in (False, True):
+        outs = []
+        for first in (1.0, -30.0, None):
+            step, g = window_step(window)
+            table = torch.arange(20, dtype=torch.int32).view(2, 10).cuda()
+            n = 25 if prompt else 1
+            T = 2 * n
+            q, k, v = rand(g, T, HQ, D), rand(g, T, HKV, D), rand(g, T, HKV, D)
+
+            def call(q, table):
+                pos, lens = i32(40, 40), i32(40 + n, 40 + n)
+                if prompt:
+                    return step.prompt(table, pos, lens, i32(0, n, T), q, k, v)
+                step(table, pos, lens, q.view(2, 1, HQ, D), k.view(2, 1, HKV, D), v.view(2, 1, HKV, D))
+                return step.out.view(T, HQ, D)
+
+            if first is not None:
+                call(q * first, table)
+            bad = table.clone()
+            bad[1, 3 if prompt else 2:] = 999
+            outs.append((call(q, bad).clone(), step.ids.clone()))
+            assert int(step.err.item()) == _lib.ERRBIT_BLOCK_ID
+            skipped = slice(n + (8 if prompt else 0), T)  # (40 + 8 tokens fill stream 1's good blocks)
+            assert not step.q[skipped].any() and step.q[:n].any()
+        for out, ids in outs[1:]:
+            assert torch.equal(out, outs[0][0])
+            assert prompt or torch.equal(ids, outs[0][1])
