@@ -113,7 +113,8 @@ class LatentStep(_CallsInOrder):
     on another: the two have workspaces and query buffers of their own (`q` is
     the latest call's rotated queries).  Calls of one kind share theirs, and a
     call on another stream than the last one of its kind waits for what that
-    stream holds.  Not while a graph is being captured, and not for replays:
+    stream holds.  Tokens that the append skips (bits of `err`) have rotary query
+    parts of zeros.  Not while a graph is being captured, and not for replays:
     there the caller keeps calls of one kind apart.
     """
 
@@ -164,11 +165,16 @@ class LatentStep(_CallsInOrder):
             with torch.cuda.stream(stream):
                 out = torch.empty((T, self.Hq, self.v), dtype=torch.bfloat16, device=self.out.device)
         self._follow("prompt", stream)
-        q = self.q = self.prompt_q[:T]
-        bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope, q, self.rope_base,
-                             row_start=row_start, err=self.err, stream=stream)
-        bd.tts_latent_prefill_attn(self.cache, block_table, ctx_lens, self.prompt_ctx, row_start, q_nope, q, self.w_uk,
-                                   self.w_uv, out, self.prompt_ws, self.scale, err=self.err, stream=stream)
+        q = self.q = _zero(self.prompt_q[:T], stream)
+        # the kernels start while the ones before them finish, and wait for what those write
+        flags = bd.tts_set_launch_flags(_lib.LAUNCH_PROGRAMMATIC)
+        try:
+            bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope, q, self.rope_base,
+                                 row_start=row_start, err=self.err, stream=stream)
+            bd.tts_latent_prefill_attn(self.cache, block_table, ctx_lens, self.prompt_ctx, row_start, q_nope, q, self.w_uk,
+                                       self.w_uv, out, self.prompt_ws, self.scale, err=self.err, stream=stream)
+        finally:
+            bd.tts_set_launch_flags(flags)
         return out
 
     def __call__(self, block_table, ctx_before, ctx_lens, q_nope, q_rope, c_new, kr_new, seed=None, step=None,
@@ -177,12 +183,12 @@ class LatentStep(_CallsInOrder):
         c_new [B * q_len][latent_dim], kr_new [B * q_len][64]; returns the
         device tensor of chosen ids [B * q_len]."""
         self._follow("step", stream)
-        q = self.q = self.step_q
-        bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope.view(self.R, self.Hq, -1), q,
-                             self.rope_base, err=self.err, stream=stream)
-        # the later kernels start while the ones before them finish
+        q = self.q = _zero(self.step_q, stream)
+        # the kernels start while the ones before them finish
         flags = bd.tts_set_launch_flags(_lib.LAUNCH_PROGRAMMATIC)
         try:
+            bd.tts_latent_append(self.cache, block_table, ctx_before, c_new, kr_new, q_rope.view(self.R, self.Hq, -1), q,
+                                 self.rope_base, err=self.err, stream=stream)
             bd.tts_latent_decode_attn(self.cache, block_table, ctx_lens, self.max_ctx_len, q_nope,
                                       q.view(self.B, self.q_len, self.Hq, -1), self.w_uk, self.w_uv, self.out, self.ws,
                                       self.scale, causal=self.causal, err=self.err, stream=stream)

@@ -60,3 +60,37 @@ def test_window_step_of_skipped_tokens_knows_no_earlier_call(window):
         for out, ids in outs[1:]:
             assert torch.equal(out, outs[0][0])
             assert prompt or torch.equal(ids, outs[0][1])
+
+
+@pytest.mark.parametrize("prompt", [False, True])
+def test_latent_step_of_skipped_tokens_knows_no_earlier_call(prompt):
+    heads, lat, nope, vd = 8, 128, 64, 64
+    n = 25 if prompt else 1
+    T = 2 * n
+    outs = []
+    for first in (1.0, -30.0, None):
+        g = torch.Generator().manual_seed(2)
+        pool = rand(g, 20, 16, lat + 64)
+        W = (torch.randn(V, heads * vd, generator=g) * 0.05).to(torch.bfloat16).cuda()
+        step = LatentStep(bd.LatentCache(pool, lat), rand(g, heads, nope, lat), rand(g, heads, vd, lat), W, 2, 160,
+                          prompt_rows=60, prompt_ctx=200)
+        table = torch.arange(20, dtype=torch.int32).view(2, 10).cuda()
+        qn, qr, c, kr = rand(g, T, heads, nope), rand(g, T, heads, 64), rand(g, T, lat), rand(g, T, 64)
+        pos, lens = i32(40, 40), i32(40 + n, 40 + n)
+
+        def call(qr, table):
+            if prompt:
+                return step.prompt(table, pos, lens, i32(0, n, T), qn, qr, c, kr)
+            step(table, pos, lens, qn.view(2, 1, heads, nope), qr.view(2, 1, heads, 64), c, kr)
+            return step.out.view(T, heads, vd)
+
+        if first is not None:
+            call(qr * first, table)
+        bad = table.clone()
+        bad[1, 3 if prompt else 2:] = 999
+        outs.append((call(qr, bad).clone(), step.ids.clone()))
+        assert int(step.err.item()) == _lib.ERRBIT_BLOCK_ID
+        assert not step.q[n + (8 if prompt else 0):T].any() and step.q[:n].any()
+    for out, ids in outs[1:]:
+        assert torch.equal(out, outs[0][0])
+        assert prompt or torch.equal(ids, outs[0][1])
