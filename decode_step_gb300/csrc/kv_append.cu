@@ -435,6 +435,16 @@ extern "C" int tts_kv_append_packed(const tts_kv_cache *cache, const int32_t *d_
                                     void *stream) {
     if (!d_row_start || B < 0 || B > (1 << 20) || num_rows < 0) return TTS_ERR_INVALID;
     const bool rope = rope_base != 0.0f;
+    if (cache && (B == 0 || num_rows == 0)) {
+        // nothing is read or written: the tensors may be empty (everything else is checked)
+        void *const any = cache->k_pool;
+        if (!d_block_table) d_block_table = static_cast<const int32_t *>(any);
+        if (!d_ctx_before) d_ctx_before = static_cast<const int32_t *>(any);
+        if (!d_q) d_q = any;
+        if (!d_q_out) d_q_out = any;
+        if (!d_k_new) d_k_new = any;
+        if (!d_v_new) d_v_new = any;
+    }
     if (rope && (!d_q_out || !tts::aligned16(d_q_out))) return TTS_ERR_INVALID;
     tts::AppendLaunch L;
     const int st = tts::prepare_append_rope(cache, d_block_table, max_blocks_per_seq, d_ctx_before, num_rows, 1,

@@ -1607,7 +1607,9 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
                                int32_t num_q_heads, float scale, int32_t window, int32_t sinks, const void *d_q,
                                void *d_out, void *d_ws, size_t ws_bytes, int32_t *d_err, void *stream) {
     using namespace tts;
-    if (!cache || !d_block_table || !d_ctx_lens || !d_row_start || !d_q || !d_out) return TTS_ERR_INVALID;
+    const bool none = B == 0 || num_rows == 0;  // nothing is read or written: the tensors may be empty
+    if (!cache || !d_row_start) return TTS_ERR_INVALID;
+    if (!none && (!d_block_table || !d_ctx_lens || !d_q || !d_out)) return TTS_ERR_INVALID;
     if (!cache->k_pool || (!cache->v_pool && cache->dtype != TTS_FP8_E4M3) || cache->num_blocks < 1 ||
         cache->num_kv_heads < 1)
         return TTS_ERR_INVALID;
@@ -1624,7 +1626,7 @@ extern "C" int tts_prompt_attn(const tts_kv_cache *cache, const int32_t *d_block
     if (pool_rows >= (1ULL << 31)) return TTS_ERR_UNSUPPORTED;
     const bool fp8 = cache->dtype == TTS_FP8_E4M3;
     if (!aligned16(cache->k_pool) || (!fp8 && !aligned16(cache->v_pool)) || !aligned16(d_q) || !aligned16(d_out)) return TTS_ERR_INVALID;
-    if (B == 0 || num_rows == 0) return TTS_OK;
+    if (none) return TTS_OK;
     if (!d_ws || ws_bytes < prompt_workspace_bytes() || (reinterpret_cast<uintptr_t>(d_ws) & 255u) != 0)
         return TTS_ERR_WORKSPACE;
 

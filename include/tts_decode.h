@@ -205,7 +205,8 @@ int tts_kv_append_rope(const tts_kv_cache *cache, const int32_t *d_block_table, 
  *                    place) or disjoint ones; only read and written with
  *                    rope_base != 0 (else num_q_heads is not looked at and both
  *                    may be NULL)
- * B <= 2^20. */
+ * B <= 2^20.  With B 0 or num_rows 0 nothing is done, and the pointers to what
+ * then has no elements may be NULL.  A skipped row's d_q_out is not written. */
 int tts_kv_append_packed(const tts_kv_cache *cache, const int32_t *d_block_table, int32_t max_blocks_per_seq,
                          const int32_t *d_ctx_before, int32_t B, const int32_t *d_row_start, int32_t num_rows,
                          int32_t num_q_heads, float rope_base, const void *d_q, void *d_q_out, const void *d_k_new,
@@ -327,6 +328,8 @@ size_t tts_prompt_attn_workspace_size(int32_t B, int32_t num_rows, int32_t num_q
  * Reads only the blocks that hold a token that some row sees, as
  * tts_window_decode_attn; tokens that a row does not see do not reach it, and a
  * value that is not finite makes that dimension of the rows that see it so.
+ * With B 0 or num_rows 0 nothing is done, and the pointers to what then has no
+ * elements may be NULL.
  * Rows of no stream are left alone.  A stream whose rows do not lie in [0,
  * num_rows], or whose context length is outside [its rows,
  * 16 * max_blocks_per_seq], gets zeros in its rows that lie there

@@ -94,3 +94,31 @@ def test_latent_step_of_skipped_tokens_knows_no_earlier_call(prompt):
     for out, ids in outs[1:]:
         assert torch.equal(out, outs[0][0])
         assert prompt or torch.equal(ids, outs[0][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("rope", [0.0, 10000.0])
+@pytest.mark.parametrize("streams", [0, 1, 2])
+def test_no_rows(dtype, rope, streams):
+    """An empty prompt, alone and through the object: nothing is done and nothing refused."""
+    if dtype == "fp8":
+        cache = bd.KVCache(torch.zeros(4, HKV, 4224, dtype=torch.uint8, device="cuda"))
+    else:
+        cache = bd.KVCache(*(torch.zeros(4, HKV, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)))
+    table = torch.zeros(streams, 2, dtype=torch.int32, device="cuda")
+    lens, start = i32(*[0] * streams), i32(*[0] * (streams + 1))
+    q, kv = (torch.zeros(0, h, D, dtype=torch.bfloat16, device="cuda") for h in (HQ, HKV))
+    err = i32(0)
+    if rope:
+        bd.tts_kv_append_packed(cache, table, lens, start, kv, kv, q, torch.empty_like(q), rope, err=err)
+    else:
+        bd.tts_kv_append_packed(cache, table, lens, start, kv, kv, err=err)
+    ws = torch.zeros(bd.tts_prompt_attn_workspace_size(streams, 0, HQ, HKV, D), dtype=torch.uint8, device="cuda")
+    bd.tts_prompt_attn(cache, table, lens, start, q, torch.empty_like(q), ws, 0.1, err=err)
+    if streams:
+        W = torch.zeros(V, HQ * D, dtype=torch.bfloat16, device="cuda")
+        step = WindowStep(cache, W, HQ, streams, 32, 8, 3, rope_base=rope, prompt_rows=4)
+        out = step.prompt(table, lens, lens, start, q, kv, kv)
+        assert out.shape == (0, HQ, D) and int(step.err.item()) == 0
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and not cache.k_pool.any()
