@@ -200,7 +200,7 @@ class LatentStep(_CallsInOrder):
 
 
 class WindowStep(_CallsInOrder):
-    """A batch's prompts and steps over a paged KV cache (bfloat16 or FP8), for
+    """A batch's prompts and steps over a paged KV cache (bfloat16 or FP8; float32: below), for
     fixed shapes, with a context that stays bounded: rows see the last `window`
     tokens up to their own and the first `sinks` (window 0: all of them).
 
@@ -210,7 +210,8 @@ class WindowStep(_CallsInOrder):
     unrotated where rope_base is not 0; the rotated queries go to buffers of the
     object (`q` is the latest call's).  `fork` makes streams continuations of
     others, `compact` moves blocks as BlockPool.compact says, and `gone` tells which of a
-    stream's blocks can go back to the pool.  Tokens that the append skips (bits of
+    stream's blocks can go back to the pool.  A float32 cache has steps alone, without
+    rotation: prompt_rows and rope_base are 0 there.  Tokens that the append skips (bits of
     `err`) have queries of zeros where rope_base is not 0.  The object owns the workspaces and
     outputs (`out` [B][q_len][Hq][head_dim], `ids` [B * q_len]).
 
@@ -227,6 +228,8 @@ class WindowStep(_CallsInOrder):
             raise ValueError(f"head width {W.shape[1]} != num_q_heads * head_dim = {num_q_heads * D}")
         if window < 0 or sinks < 0:
             raise ValueError("window and sinks must not be negative")
+        if cache.dtype == torch.float32 and (prompt_rows or rope_base != 0.0):
+            raise ValueError("a float32 cache has neither prompts nor a rotary append: prompt_rows and rope_base must be 0")
         self.cache, self.W = cache, W
         self.B, self.q_len, self.Hq, self.max_ctx_len, self.causal = B, q_len, num_q_heads, max_ctx_len, causal
         self.window, self.sinks = window, sinks

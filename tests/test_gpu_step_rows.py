@@ -4,6 +4,8 @@ from __future__ import annotations
 import pytest
 import torch
 
+import paged_ref as pr
+
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
@@ -122,3 +124,26 @@ def test_no_rows(dtype, rope, streams):
         assert out.shape == (0, HQ, D) and int(step.err.item()) == 0
     torch.cuda.synchronize()
     assert int(err.item()) == 0 and not cache.k_pool.any()
+
+
+def test_a_float32_cache_has_steps_and_no_prompts():
+    g = torch.Generator().manual_seed(4)
+    pools = [torch.randn(20, HKV, 16, 64, generator=g).cuda() for _ in range(2)]
+    cache = bd.KVCache(*pools)
+    W = torch.randn(V, HQ * 64, generator=g).cuda()
+    for bad in (dict(), dict(rope_base=0.0, prompt_rows=4), dict(rope_base=10000.0)):
+        with pytest.raises(ValueError, match="float32"):
+            WindowStep(cache, W, HQ, 2, 160, 40, 3, **bad)
+    table = torch.arange(20, dtype=torch.int32).view(2, 10)
+    for window in (0, 40):
+        step = WindowStep(cache, W, HQ, 2, 160, window, 3, rope_base=0.0)
+        q, k, v = (torch.randn(2, 1, h, 64, generator=g) for h in (HQ, HKV, HKV))
+        step(table.cuda(), i32(100, 7), i32(101, 8), q.cuda(), k.cuda(), v.cuda())
+        torch.cuda.synchronize()
+        assert int(step.err.item()) == 0
+        for b, p in ((0, 100), (1, 7)):
+            assert all(torch.equal(x[int(table[b, p // 16]), :, p % 16].cpu(), y[b, 0]) for x, y in zip(pools, (k, v)))
+        s = dict(new=[1, 1], before=[100, 7], ctx=[101, 8], Hq=HQ, Hkv=HKV, D=64, dtype="f32", window=window, sinks=3,
+                 causal=False, scale=step.scale, table=table, k_val=pools[0].cpu().double(), v_val=pools[1].cpu().double(),
+                 T=2, q=q.view(2, HQ, 64), row_start=torch.tensor([0, 1, 2]))
+        pr.check(step.out.view(2, HQ, 64), *pr.attend_all(s))
