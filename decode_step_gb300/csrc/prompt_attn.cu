@@ -199,7 +199,6 @@ struct Walk {
     int s0;                    // the segment's place in the flat list
     int first, n, ctx;         // of the stream
     Span span;
-    bool fresh;                // first tile of a part
     __device__ __forceinline__ int r0(const PromptArgs &a) const { return i * 2 * a.tokens; }
     __device__ __forceinline__ bool two(const PromptArgs &a) const { return r0(a) + a.tokens < n; }
     __device__ __forceinline__ int tiles() const { return min(left, span.tiles - k); }  // of the part, from its first one on
@@ -216,7 +215,6 @@ struct Walk {
         }
     }
     __device__ __forceinline__ void settle(const PromptArgs &a) {  // k may be behind the segment's last tile
-        fresh = true;
         if (k < span.tiles) return;
         k = 0;
         s0 += kPartCost + span.tiles;
@@ -230,7 +228,6 @@ struct Walk {
         span = span_of(a, n, ctx, i);
     }
     __device__ __forceinline__ void advance(const PromptArgs &a) {
-        fresh = false;
         ++k;
         if (--left > 0 && k == span.tiles) settle(a);
     }
@@ -266,7 +263,7 @@ struct Place {
 struct PartInfo {
     int first, n, ctx, b;         // of the stream
     int r0, g, number, tiles;     // first row of the query tile, KV head, from 1, tiles of the part
-    int k, head, skip, low;       // first tile of the part; Span
+    int k, head, skip;            // first tile of the part; Span
     int high, shares, more, mode; // first CTA of the segment, CTAs that follow
 };
 // The same of a part's values, by their producer, which may be ahead of the keys'.
@@ -776,7 +773,7 @@ prompt_attn_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         PartInfo &p = sh.parts[note];
                         p.first = walk.first; p.n = walk.n; p.ctx = walk.ctx; p.b = walk.b;
                         p.r0 = r0; p.g = walk.g; p.number = part + 1; p.tiles = tiles;
-                        p.k = walk.k; p.head = walk.span.head; p.skip = walk.span.skip; p.low = walk.span.low;
+                        p.k = walk.k; p.head = walk.span.head; p.skip = walk.span.skip;
                         p.high = walk.span.high; p.shares = shares.first; p.more = shares.more; p.mode = mode;
                     }
                     if (!for_keys && lane == 0)
