@@ -147,3 +147,47 @@ def test_a_float32_cache_has_steps_and_no_prompts():
                  causal=False, scale=step.scale, table=table, k_val=pools[0].cpu().double(), v_val=pools[1].cpu().double(),
                  T=2, q=q.view(2, HQ, 64), row_start=torch.tensor([0, 1, 2]))
         pr.check(step.out.view(2, HQ, 64), *pr.attend_all(s))
+
+
+def test_captured_prompt_and_steps_follow_their_inputs():
+    """A prompt and two steps in one graph, zeros and appends among them, replayed with other tokens,
+    and with a block outside the pool: as the same calls one after another."""
+    step, g = window_step()
+    other, _ = window_step()
+    table = torch.arange(20, dtype=torch.int32).view(2, 10).cuda()
+    q, k, v = (torch.empty(54, h, D, dtype=torch.bfloat16, device="cuda") for h in (HQ, HKV, HKV))
+    at = [i32(0, 30), i32(25, 55), i32(26, 56), i32(27, 57)]
+    start = i32(0, 25, 50)
+
+    def calls(step):
+        out = [step.prompt(table, at[0], at[1], start, q[:50], k[:50], v[:50]).clone()]
+        for i in range(2):
+            rows = slice(50 + 2 * i, 52 + 2 * i)
+            step(table, at[1 + i], at[2 + i], q[rows].view(2, 1, HQ, D), k[rows].view(2, 1, HKV, D),
+                 v[rows].view(2, 1, HKV, D))
+            out += [step.out.clone(), step.ids.clone()]
+        return out
+
+    for x in (q, k, v):
+        x.copy_(rand(g, *x.shape))
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        calls(step)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs = calls(step)
+    for bad in (False, True, False):
+        for x in (q, k, v):
+            x.copy_(rand(g, *x.shape))
+        table[1, 3] = 999 if bad else 13
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = calls(other)
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, want):
+            assert torch.equal(got, ref)
+        assert all(torch.equal(a, b) for a, b in zip((step.cache.k_pool, step.cache.v_pool),
+                                                     (other.cache.k_pool, other.cache.v_pool)))
+    assert int(step.err.item()) == int(other.err.item()) == _lib.ERRBIT_BLOCK_ID
