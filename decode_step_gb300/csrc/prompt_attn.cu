@@ -40,8 +40,11 @@
 // us, 1.30 PFLOP/s, 0.68 of a dense product's measured rate; the softmax warps take
 // about 2,000 cycles a tile for both halves, the MMAs 1,435 of them (the first, with
 // both operands in shared memory, 417 a half, bound by their 128 bytes a cycle; the
-// second 320).  61 rows after 65,472: 59 us, 4.6 TB/s.  333 rows: 18 us, latency.
-// FP8: instruction issue of the conversions and scales, twice the bf16 time.  A CTA
+// second 320).  61 rows after 65,472: 58 us, 4.6 TB/s.  333 rows: 18 us, latency.
+// FP8 takes twice the bf16 time (8,191 rows 520 us) with no unit near its limit (4,095
+// rows: issue slots 45%, matrix unit 24%, shared memory's pipe 30%): chains of waits
+// between converters, MMAs and softmax, and in short contexts O is scaled in nearly
+// every tile, since the maximum moves with any score that passes it.  A CTA
 // does not have 16 softmax warps (two threads a row: 386 us, spills and twice the
 // reads of scores).
 //
